@@ -8,7 +8,8 @@ Low-level functions carry the names of the C ABI in include/gemm_epilog.h:
 gemm_epilog_plan, gemm_epilog_plan_ex, gemm_epilog_plan_info, gemm_epilog_execute,
 gemm_epilog_execute_noalloc, gemm_epilog_autotune, gemm_epilog_lost_waits,
 gemm_epilog_free, gemm_epilog_aux_bytes, gemm_epilog_workspace_bytes,
-gemm_epilog_describe, gemm_epilog_status_string.
+gemm_epilog_describe, gemm_epilog_status_string. The microscaled operators
+(gemm_epilog_mx_*) are wrapped in mx.py, the norm (gemm_epilog_rms_norm*) in norm.py.
 Pointers may be given as torch tensors (device memory), integers or None.
 
 `Matmul` wraps them in the stateful plan / execute / free object with a context
@@ -39,7 +40,14 @@ EXPORTS = ("gemm_epilog_plan", "gemm_epilog_plan_ex", "gemm_epilog_plan_info", "
            "gemm_epilog_execute_noalloc",
            "gemm_epilog_autotune", "gemm_epilog_lost_waits", "gemm_epilog_free",
            "gemm_epilog_aux_bytes", "gemm_epilog_workspace_bytes", "gemm_epilog_describe",
-           "gemm_epilog_status_string")
+           "gemm_epilog_status_string",
+           "gemm_epilog_mx_code_bytes", "gemm_epilog_mx_scale_bytes", "gemm_epilog_mx_quantize",
+           "gemm_epilog_mx_dequantize", "gemm_epilog_mx_pack", "gemm_epilog_mx_plan", "gemm_epilog_mx_plan_info",
+           "gemm_epilog_mx_execute", "gemm_epilog_mx_free",
+           "gemm_epilog_rms_norm", "gemm_epilog_rms_norm_workspace_bytes", "gemm_epilog_rms_norm_backward")
+MXFP4, MXFP8 = 0, 1
+MX_FORMATS = {"mxfp4": MXFP4, "mxfp8": MXFP8}
+MX_OUT = {"f32": 0, "f16": 1, "bf16": 2, "mxfp8": 3}
 OP_N, OP_T = 0, 1
 
 
@@ -52,6 +60,15 @@ class ge_plan_info_t(ctypes.Structure):
                 ("tiles", ctypes.c_int64), ("persistent_workgroups", ctypes.c_int), ("whole_tiles", ctypes.c_int),
                 ("split_workgroups", ctypes.c_int), ("split_run_ktiles", ctypes.c_int), ("group_m", ctypes.c_int),
                 ("workspace_bytes", ctypes.c_size_t), ("stages", ctypes.c_int)]
+
+
+class ge_mx_types_t(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_int), ("d", ctypes.c_int), ("vec", ctypes.c_int)]
+
+
+class ge_mx_plan_info_t(ctypes.Structure):
+    _fields_ = [("tile_m", ctypes.c_int), ("tile_n", ctypes.c_int), ("waves", ctypes.c_int), ("stages", ctypes.c_int),
+                ("splits", ctypes.c_int), ("workgroups", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t)]
 
 
 class GemmEpilogError(RuntimeError):
@@ -99,6 +116,24 @@ def load() -> ctypes.CDLL:
     L.gemm_epilog_describe.restype = ctypes.c_char_p
     L.gemm_epilog_status_string.argtypes = [c_int]
     L.gemm_epilog_status_string.restype = ctypes.c_char_p
+    f32, size = ctypes.c_float, ctypes.c_size_t
+    for name, args, res in (
+            ("mx_code_bytes", [c_int, i64, i64], size),
+            ("mx_scale_bytes", [i64, i64], size),
+            ("mx_quantize", [i64, i64, c_int, vp, i64, i64, c_int, vp, vp, vp], c_int),
+            ("mx_dequantize", [i64, i64, c_int, vp, vp, c_int, vp, i64, vp], c_int),
+            ("mx_pack", [i64, i64, c_int, vp, vp, vp, vp, vp], c_int),
+            ("mx_plan", [i64, i64, i64, ge_mx_types_t, c_int, ctypes.POINTER(vp)], c_int),
+            ("mx_plan_info", [i64, i64, i64, ge_mx_types_t, c_int, i64, c_int, ctypes.POINTER(ge_mx_plan_info_t)],
+             c_int),
+            ("mx_execute", [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp], c_int),
+            ("mx_free", [vp], c_int),
+            ("rms_norm", [i64, i64, c_int, vp, i64, vp, i64, vp, c_int, f32, vp, i64, vp, i64, vp, vp, vp], c_int),
+            ("rms_norm_workspace_bytes", [i64, i64], size),
+            ("rms_norm_backward", [i64, i64, c_int, vp, i64, vp, i64, vp, c_int, f32, vp, i64, vp, i64, vp, vp, size, vp],
+             c_int)):
+        fn = getattr(L, "gemm_epilog_" + name)
+        fn.argtypes, fn.restype = args, res
     _lib = L
     return L
 

@@ -22,7 +22,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.hip", "inst_f32.hip", "inst_f16.hip", "inst_bf16.hip",
            "inst_f16_lay1.hip", "inst_f16_lay2.hip", "inst_f16_lay3.hip",
-           "inst_bf16_lay1.hip", "inst_bf16_lay2.hip", "inst_bf16_lay3.hip"]
+           "inst_bf16_lay1.hip", "inst_bf16_lay2.hip", "inst_bf16_lay3.hip",
+           "mx.hip", "mx_quant.hip", "norm.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -35,7 +36,7 @@ FLAGS = [
 PROBE_SOURCES = ["probe.hip"]
 
 # Host-only C++ (the plan arithmetic): plain g++, no HIP.
-HOST_SOURCES = ["plan_host.cpp"]
+HOST_SOURCES = ["plan_host.cpp", "mx_host.cpp"]
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-I", INCLUDE, "-I", CSRC]
 
 

@@ -1,0 +1,643 @@
+// D = act(X W^T + bias) of microscaled operands (layout: mx_format.hpp): X (m, k) e4m3 or
+// e2m1, W (n, k) e2m1, both along k, products and scales in the scaled matrix instruction
+// with fp32 accumulators. Grouped form: rows of X sorted by expert, each expert with its
+// own W and bias, its row range read on the device.
+//
+// The W fragment is the instruction's row operand and the X fragment its column operand,
+// so a lane holds one row of D (a token) and its registers walk along n.
+#pragma once
+
+#include <type_traits>
+
+#include "kernels.hpp"
+#include "mx_format.hpp"
+#include "mx_tiles.hpp"
+
+namespace gek {
+
+using namespace gemx;
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void mx_lds_void;
+
+enum MxOut { MX_OUT_F32 = 0, MX_OUT_F16 = 1, MX_OUT_BF16 = 2, MX_OUT_FP8 = 3 };
+
+struct MxArgs {
+  const char* xc;
+  const char* xs;
+  const char* wc;
+  const char* ws;
+  const void* bias;        // (n) or (experts, n), type vec; NULL without a bias
+  const int32_t* offsets;  // (experts + 1) or NULL
+  void* D;                 // (m, n), or e4m3 codes
+  char* ds;                // scales of an e4m3 result
+  float* partial;          // split tiles: parts' accumulators
+  uint32_t* counter;       // split tiles: parts arrived
+  int64_t m;
+  int32_t n, k, kt;        // kt: 256-k granules
+  int32_t experts;         // 0: one product
+  int32_t tiles_m, tiles_n;
+  int32_t splits;          // parts of the k loop
+  int32_t ep, out, vec;
+  int32_t group_m;
+};
+
+// Copies of the tile kernels: 16 (4) bytes per lane from srd.base + voff to LDS bytes
+// lds + 16 (4) lane; see copy_to_lds_b128 for the ordering rules.
+__device__ __forceinline__ void copy_to_lds_b32(const i32x4& srd, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :
+               : "v"(voff), "s"(srd), "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "memory", "m0");
+}
+
+__device__ __forceinline__ uint32_t mx_range(int64_t left) {
+  return left <= 0 ? 0u : left > 0x7ffffff0 ? 0x7ffffff0u : (uint32_t)left;
+}
+
+// act(v) by the run-time epilogue code (uniform).
+__device__ __forceinline__ float mx_act(float v, int ep) {
+  return ep == RELU_BIAS ? (v > 0.0f ? v : 0.0f) : ep == GELU_BIAS ? gelu_tanh(v) : v;
+}
+
+// The rows [lo, hi) of expert e; offsets that fall outside 0 .. m or run backwards are
+// held to an empty or valid range, so no row outside X or D is touched.
+__device__ __forceinline__ void expert_rows(const MxArgs& p, int e, int64_t& lo, int64_t& hi) {
+  const int64_t a = p.offsets[e], b = p.offsets[e + 1];
+  lo = a < 0 ? 0 : a > p.m ? p.m : a;
+  hi = b < lo ? lo : b > p.m ? p.m : b;
+}
+
+// ---- finishing outputs ------------------------------------------------------------
+// Eight consecutive finished values of row `row` from column c0 (a multiple of 8).
+__device__ __forceinline__ void mx_store8(const MxArgs& p, int64_t row, int c0, const float (&v)[8], bool vec_ok) {
+  if (c0 >= p.n) return;
+  const int64_t at = row * p.n + c0;
+  if (vec_ok) {
+    if (p.out == MX_OUT_F32) {
+      f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(p.D) + at);
+      d[0] = f32x4{v[0], v[1], v[2], v[3]};
+      d[1] = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+      i32x4 o;
+      if (p.out == MX_OUT_F16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = (int)Tr<F16>::pack2(v[2 * e], v[2 * e + 1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = (int)Tr<BF16>::pack2(v[2 * e], v[2 * e + 1]);
+      }
+      *reinterpret_cast<i32x4*>(static_cast<char*>(p.D) + at * 2) = o;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c0 + e < p.n) store_vec(p.D, p.out, at + e, v[e]);
+  }
+}
+
+// Sixteen finished values of row `row` from column c0 (a multiple of 16) as one chunk of
+// an e4m3 result; `s` is the scale byte of their block.
+__device__ __forceinline__ void mx_store_chunk(const MxArgs& p, int64_t row, int c0, const float (&v)[16], int s) {
+  i32x4 o;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) o[q] = (int)to_fp8x4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3], s);
+  const int64_t chunks = pad_to(p.n, kKPad) / 16;
+  *reinterpret_cast<i32x4*>(static_cast<char*>(p.D) + ((row >> 5) * chunks + c0 / 16) * 512 + (row & 31) * 16) = o;
+}
+__device__ __forceinline__ void mx_store_scale(const MxArgs& p, int64_t row, int c0, int s) {
+  const int64_t granules = pad_to(p.n, kKPad) / kKPad;
+  p.ds[((row >> 5) * granules + c0 / kKPad) * kScaleGranule + ((c0 / 32) & 1) * 128 + (row & 31) * 4 +
+       (c0 / 64) % 4] = (char)s;
+}
+__device__ __forceinline__ bool mx_vec_ok(const MxArgs& p) {
+  return p.n % 8 == 0 && reinterpret_cast<uintptr_t>(p.D) % 16 == 0;
+}
+// Bias of column c of expert e (0 past n, or without a bias).
+__device__ __forceinline__ float mx_bias(const MxArgs& p, int e, int c) {
+  return p.ep != NONE && c < p.n ? load_vec(p.bias, p.vec, (int64_t)e * p.n + c) : 0.0f;
+}
+
+// ---- tile kernel -------------------------------------------------------------------
+// One workgroup computes bm x bn of D over its part of k. Copies go straight to LDS;
+// all waves run the lockstep schedule: at the end of a k-tile every wave waits for its own
+// copies of the next one, one barrier publishes it and releases the stage just read, and
+// the next copies go there.
+template <int XF, int CFG>
+struct MxCfgT {
+  static constexpr MxTile T = kMxTiles[CFG];
+  static constexpr int MB = T.mb, NB = T.nb, STAGES = T.stages;
+  static constexpr int WAVES_M = T.bm / 32 / MB, WAVES_N = T.bn / 32 / NB, NW = WAVES_M * WAVES_N;
+  static constexpr int BK = mx_bk(XF), KS = BK / 64;
+  static constexpr int WRB = BK / 32 * 512;                // bytes of a W row group per stage
+  static constexpr int XRB = BK / chunk_values(XF) * 512;  // and of an X row group (4096)
+  static constexpr int W_BYTES = T.bn / 32 * WRB, X_BYTES = T.bm / 32 * XRB;
+  static constexpr int SW_BYTES = T.bn / 32 * kScaleGranule, SX_BYTES = T.bm / 32 * kScaleGranule;
+  static constexpr int OFF_X = W_BYTES, OFF_SW = OFF_X + X_BYTES, OFF_SX = OFF_SW + SW_BYTES;
+  static constexpr int STAGE = OFF_SX + SX_BYTES;
+  static constexpr int PW = W_BYTES / 1024, PX = X_BYTES / 1024, PS = (T.bn + T.bm) / 32;   // copies per stage
+  static constexpr int IW = (PW + NW - 1) / NW, IX = (PX + NW - 1) / NW, IS = (PS + NW - 1) / NW;   // and per wave
+  static constexpr int INST = IW + IX + IS;
+  static constexpr int EPI_ROW = 68;                       // floats per scratch row: 64 and a pad
+  static constexpr int EPI = 32 * EPI_ROW * 4;             // scratch bytes per wave
+  static constexpr int LDS = STAGES * STAGE > NW * EPI ? STAGES * STAGE : NW * EPI;
+  static constexpr int XR = XF == FP8 ? 2 : 1;             // 16-byte reads per X fragment
+  static_assert(LDS <= 160 * 1024, "LDS");
+  static_assert(NB % 2 == 0, "the epilogue takes two feature blocks at a time");
+};
+
+template <int XF, int MB, int NB>
+struct MxFrags {
+  i32x4 w[NB];
+  i32x4 x[MB][XF == FP8 ? 2 : 1];
+};
+
+// One product of the k-step S of a scale dword (opsel picks its byte).
+template <int XF, int S>
+__device__ __forceinline__ f32x16 mx_mma(i32x4 w, const i32x4 (&x)[XF == FP8 ? 2 : 1], f32x16 c, int sw, int sx) {
+  const i32x8 a = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+  if constexpr (XF == FP8) {
+    const i32x8 b = {x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 0, S, sw, S, sx);
+  } else {
+    const i32x8 b = {x[0][0], x[0][1], x[0][2], x[0][3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, S, sw, S, sx);
+  }
+}
+
+// Tile of this workgroup: expert, first row group (as a row), the rows to keep, column.
+// Grouped: every expert's tiles start at the 32-row group that holds its first row (the
+// rows of its neighbours in that group are computed and dropped), so that the copies stay
+// whole lines; the launch has workgroups for the most tiles there can be, and the ones
+// past the actual count leave at once.
+struct MxPlace {
+  int e, tn;
+  int64_t row0, lo, hi;
+};
+template <int BM>
+__device__ __forceinline__ bool mx_place(const MxArgs& p, int id, MxPlace& o) {
+  int tiles_m = p.tiles_m;
+  if (p.experts) {
+    const int lane = threadIdx.x & 63;
+    int total = 0;
+    for (int e0 = 0; e0 < p.experts; e0 += 64) {
+      int64_t lo = 0, hi = 0;
+      if (e0 + lane < p.experts) expert_rows(p, e0 + lane, lo, hi);
+      int c = hi > lo ? (int)((hi - (lo & ~(int64_t)31) + BM - 1) / BM) : 0;
+#pragma unroll
+      for (int d = 32; d; d >>= 1) c += __shfl_xor(c, d);
+      total += c;
+    }
+    tiles_m = __builtin_amdgcn_readfirstlane(total);
+  }
+  const int G = tiles_m * p.tiles_n;
+  if (id >= G) return false;
+  const int pos = xcd_remap(id, G);
+  const int gsz = p.group_m * p.tiles_n;
+  const int g = pos / gsz, first = g * p.group_m;
+  const int rows = min(tiles_m - first, p.group_m);
+  const int in = pos - g * gsz;
+  const int tm = __builtin_amdgcn_readfirstlane(first + in % rows);
+  o.tn = __builtin_amdgcn_readfirstlane(in / rows);
+  if (!p.experts) {
+    o.e = 0;
+    o.row0 = (int64_t)tm * BM;
+    o.lo = 0;
+    o.hi = p.m;
+    return true;
+  }
+  const int lane = threadIdx.x & 63;
+  int base = 0;
+  for (int e0 = 0; e0 < p.experts; e0 += 64) {
+    int64_t lo = 0, hi = 0;
+    if (e0 + lane < p.experts) expert_rows(p, e0 + lane, lo, hi);
+    const int c = hi > lo ? (int)((hi - (lo & ~(int64_t)31) + BM - 1) / BM) : 0;
+    int incl = c;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(incl, d);
+      if (lane >= d) incl += up;
+    }
+    const uint64_t past = __builtin_amdgcn_ballot_w64(base + incl > tm);
+    if (past) {
+      const int f = __builtin_ctzll(past);
+      o.e = e0 + f;
+      const int t = tm - base - (__builtin_amdgcn_readlane(incl, f) - __builtin_amdgcn_readlane(c, f));
+      o.lo = __builtin_amdgcn_readlane((int)lo, f);
+      o.hi = __builtin_amdgcn_readlane((int)hi, f);
+      o.row0 = (o.lo & ~(int64_t)31) + (int64_t)t * BM;
+      return true;
+    }
+    base += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return false;
+}
+
+template <int XF, int CFG>
+__global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), 1) void mx_tile_kernel(MxArgs p) {
+  using C = MxCfgT<XF, CFG>;
+  constexpr int MB = C::MB, NB = C::NB, KS = C::KS, STAGES = C::STAGES;
+  __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
+  __shared__ int last_part;
+
+  const int part = blockIdx.x % p.splits, id = blockIdx.x / p.splits;
+  MxPlace at;
+  if (!mx_place<C::T.bm>(p, id, at)) return;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = w % C::WAVES_M, wn = w / C::WAVES_M;
+  const uint32_t lds = (uint32_t)(uintptr_t)(mx_lds_void*)smem;
+
+  // ---- copies ----
+  const int64_t gw = group_code_bytes(FP4, p.k), gx = group_code_bytes(XF, p.k), gs = group_scale_bytes(p.k);
+  const int64_t wrg = row_groups(p.n), xrg = row_groups(p.m);
+  const int64_t wg0 = (int64_t)at.tn * (C::T.bn / 32), xg0 = at.row0 / 32;
+  const char* wc = p.wc + at.e * wrg * gw + wg0 * gw;
+  const char* ws = p.ws + at.e * wrg * gs + wg0 * gs;
+  const char* xc = p.xc + xg0 * gx;
+  const char* xs = p.xs + xg0 * gs;
+  const int64_t wleft = (wrg - wg0) * gw, xleft = (xrg - xg0) * gx;
+  const int64_t wsleft = (wrg - wg0) * gs, xsleft = (xrg - xg0) * gs;
+  uint32_t voff_w[C::IW], voff_x[C::IX], voff_s[C::IS];
+#pragma unroll
+  for (int j = 0; j < C::IW; ++j) {
+    const int i = min(w * C::IW + j, C::PW - 1);
+    voff_w[j] = (uint32_t)((i / (C::WRB / 1024)) * gw + (i % (C::WRB / 1024)) * 1024 + lane * 16);
+  }
+#pragma unroll
+  for (int j = 0; j < C::IX; ++j) {
+    const int i = min(w * C::IX + j, C::PX - 1);
+    voff_x[j] = (uint32_t)((i / (C::XRB / 1024)) * gx + (i % (C::XRB / 1024)) * 1024 + lane * 16);
+  }
+#pragma unroll
+  for (int j = 0; j < C::IS; ++j) {
+    const int i = min(w * C::IS + j, C::PS - 1);
+    voff_s[j] = (uint32_t)((i < C::T.bn / 32 ? i : i - C::T.bn / 32) * gs + lane * 4);
+  }
+  auto issue = [&](int kt, int stage) {
+    const uint32_t dst = lds + stage * C::STAGE;
+    const i32x4 rw = make_srd(wc + (int64_t)kt * C::WRB, mx_range(wleft - (int64_t)kt * C::WRB));
+    const i32x4 rx = make_srd(xc + (int64_t)kt * C::XRB, mx_range(xleft - (int64_t)kt * C::XRB));
+    const int64_t so = (int64_t)(kt * C::BK / kKPad) * kScaleGranule;
+    const i32x4 rsw = make_srd(ws + so, mx_range(wsleft - so));
+    const i32x4 rsx = make_srd(xs + so, mx_range(xsleft - so));
+#pragma unroll
+    for (int j = 0; j < C::IW; ++j)
+      copy_to_lds_b128(rw, voff_w[j], dst + min(w * C::IW + j, C::PW - 1) * 1024);
+#pragma unroll
+    for (int j = 0; j < C::IX; ++j)
+      copy_to_lds_b128(rx, voff_x[j], dst + C::OFF_X + min(w * C::IX + j, C::PX - 1) * 1024);
+#pragma unroll
+    for (int j = 0; j < C::IS; ++j) {
+      const int i = min(w * C::IS + j, C::PS - 1);
+      copy_to_lds_b32(i < C::T.bn / 32 ? rsw : rsx, voff_s[j], dst + C::OFF_SW + i * kScaleGranule);
+    }
+  };
+
+  // ---- fragment reads ----
+  using F = MxFrags<XF, MB, NB>;
+  const int rd_w = wn * NB * C::WRB + lane * 16, rd_x = C::OFF_X + wm * MB * C::XRB + lane * 16;
+  const int rd_sw = C::OFF_SW + wn * NB * kScaleGranule + lane * 4;
+  const int rd_sx = C::OFF_SX + wm * MB * kScaleGranule + lane * 4;
+  constexpr int PIECES = NB + MB * C::XR;
+  auto piece = [&](const char* base, int s, int q, F& f) {
+    if (q < C::XR) f.x[0][q] = *reinterpret_cast<const i32x4*>(base + rd_x + (s * C::XR + q) * 1024);
+    else if (q < C::XR + NB) f.w[q - C::XR] = *reinterpret_cast<const i32x4*>(base + rd_w + (q - C::XR) * C::WRB + s * 1024);
+    else {
+      const int b = (q - NB) / C::XR, h = (q - NB) % C::XR;
+      f.x[b][h] = *reinterpret_cast<const i32x4*>(base + rd_x + b * C::XRB + (s * C::XR + h) * 1024);
+    }
+  };
+  int sw[NB], sx[MB];
+  auto read_scales = [&](const char* base, int kt, int (&nw)[NB], int (&nx)[MB]) {
+    const int sh = XF == FP8 ? (kt & 1) * 16 : 0;   // a 128-k stage uses half of the granule's bytes
+#pragma unroll
+    for (int a = 0; a < NB; ++a) nw[a] = *reinterpret_cast<const int*>(base + rd_sw + a * kScaleGranule) >> sh;
+#pragma unroll
+    for (int b = 0; b < MB; ++b) nx[b] = *reinterpret_cast<const int*>(base + rd_sx + b * kScaleGranule) >> sh;
+  };
+
+  const int KTA = (int)(pad_to(p.k, kKPad) / C::BK);
+  const int kb = (int)((int64_t)KTA * part / p.splits), KT = (int)((int64_t)KTA * (part + 1) / p.splits) - kb;
+
+  f32x16 acc[NB][MB];
+#pragma unroll
+  for (int a = 0; a < NB; ++a)
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
+
+  // prologue: the first stages in flight, stage 0 complete
+#pragma unroll
+  for (int t = 0; t < STAGES; ++t)
+    if (t < KT) issue(kb + t, t);
+  if (KT >= STAGES) wait_vmcnt<(STAGES - 1) * C::INST>();
+  else wait_vmcnt<0>();
+  barrier_only();
+  F fr[2];
+#pragma unroll
+  for (int q = 0; q < PIECES; ++q) piece(smem, 0, q, fr[0]);
+  read_scales(smem, kb, sw, sx);
+
+  auto tile = [&](int kt, int u) {
+    const char* cur = smem + u * C::STAGE;
+    const char* nxt = smem + ((u + 1) % STAGES) * C::STAGE;
+    int nsw[NB], nsx[MB];
+    const bool more = kt + 1 < KT;
+    auto step = [&](auto tag) {
+      constexpr int s = decltype(tag)::value;
+      constexpr bool last = s == KS - 1;
+      if constexpr (last) {
+        wait_lgkmcnt<0>();
+        if (kt + STAGES < KT + 1) wait_vmcnt<(STAGES - 2) * C::INST>();
+        else wait_vmcnt<0>();
+        barrier_only();
+        if (kt + STAGES < KT) issue(kb + kt + STAGES, u);
+      }
+      const char* rbase = last ? nxt : cur;
+      constexpr int rs = last ? 0 : s + 1;
+      constexpr int NMMA = MB * NB, PER = (PIECES + NMMA - 1) / NMMA;
+#pragma unroll
+      for (int i = 0; i < NMMA; ++i) {
+        const int a = i % NB, b = i / NB;
+        acc[a][b] = mx_mma<XF, s>(fr[s & 1].w[a], fr[s & 1].x[b], acc[a][b], sw[a], sx[b]);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          const int q = i * PER + e;
+          if (q < PIECES && (!last || more)) piece(rbase, rs, q, fr[(s & 1) ^ 1]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (last) {
+        if (more) {
+          read_scales(nxt, kb + kt + 1, nsw, nsx);
+#pragma unroll
+          for (int a = 0; a < NB; ++a) sw[a] = nsw[a];
+#pragma unroll
+          for (int b = 0; b < MB; ++b) sx[b] = nsx[b];
+        }
+      }
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    if constexpr (KS == 4) {
+      step(std::integral_constant<int, 2>{});
+      step(std::integral_constant<int, 3>{});
+    }
+  };
+  for (int kt = 0; kt < KT; kt += STAGES) {
+#pragma unroll
+    for (int u = 0; u < STAGES; ++u)
+      if (kt + u < KT) tile(kt + u, u);
+  }
+  wait_vmcnt<0>();
+  __syncthreads();   // every wave is done with the stages
+
+  // ---- split k: the part that arrives last adds all parts in order and finishes ----
+  if (p.splits > 1) {
+    constexpr int kDev = 16;   // device scope (sc1): past the XCD's own L2
+    constexpr int PART = C::NW * NB * MB * 16 * 64 * 4;
+    const int tile_id = (int)((at.row0 / C::T.bm) * p.tiles_n + at.tn);
+    char* slots = reinterpret_cast<char*>(p.partial) + (int64_t)tile_id * p.splits * PART;
+    {
+      const __amdgpu_buffer_rsrc_t r = rsrc(slots + (int64_t)part * PART);
+#pragma unroll
+      for (int a = 0; a < NB; ++a)
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const i32x4 v = {__float_as_int(acc[a][b][4 * g]), __float_as_int(acc[a][b][4 * g + 1]),
+                             __float_as_int(acc[a][b][4 * g + 2]), __float_as_int(acc[a][b][4 * g + 3])};
+            __builtin_amdgcn_raw_buffer_store_b128(v, r, (((w * NB + a) * MB + b) * 4 + g) * 1024 + lane * 16, 0, kDev);
+          }
+    }
+    wait_vmcnt<0>();
+    __syncthreads();
+    if (threadIdx.x == 0)
+      last_part = __hip_atomic_fetch_add(p.counter + tile_id, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                  (uint32_t)p.splits - 1u;
+    __syncthreads();
+    if (!last_part) return;
+    if (threadIdx.x == 0) __hip_atomic_store(p.counter + tile_id, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int q = 0; q < p.splits; ++q) {
+      const __amdgpu_buffer_rsrc_t r = rsrc(slots + (int64_t)q * PART);
+#pragma unroll
+      for (int a = 0; a < NB; ++a)
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const i32x4 v = __builtin_amdgcn_raw_buffer_load_b128(
+                r, (((w * NB + a) * MB + b) * 4 + g) * 1024 + lane * 16, 0, kDev);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float f = __int_as_float(v[e]);
+              acc[a][b][4 * g + e] = q == 0 ? f : acc[a][b][4 * g + e] + f;
+            }
+          }
+    }
+  }
+
+  // ---- epilogue: two feature blocks of one token block at a time through scratch ----
+  float* scratch = reinterpret_cast<float*>(smem + w * C::EPI);
+  const int lrow = lane & 31, lhi = lane >> 5;
+  const bool vec_ok = mx_vec_ok(p);
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    const int64_t r0 = at.row0 + (wm * MB + b) * 32;
+#pragma unroll
+    for (int a0 = 0; a0 < NB; a0 += 2) {
+      const int c0 = at.tn * C::T.bn + (wn * NB + a0) * 32;
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<f32x4*>(scratch + lrow * C::EPI_ROW + a * 32 + 8 * g + 4 * lhi) =
+              f32x4{acc[a0 + a][b][4 * g], acc[a0 + a][b][4 * g + 1], acc[a0 + a][b][4 * g + 2],
+                    acc[a0 + a][b][4 * g + 3]};
+      __builtin_amdgcn_wave_barrier();
+      if (p.out == MX_OUT_FP8) {
+        const int64_t row = r0 + lrow;
+        const bool keep = row >= at.lo && row < at.hi;
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const int c = c0 + a * 32 + 16 * lhi;
+          float v[16], m = 0.0f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 t = *reinterpret_cast<const f32x4*>(scratch + lrow * C::EPI_ROW + a * 32 + 16 * lhi + 4 * q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float f = mx_act(t[e] + mx_bias(p, at.e, c + 4 * q + e), p.ep);
+              v[4 * q + e] = c + 4 * q + e < p.n ? f : 0.0f;
+              m = amax2(m, mag(v[4 * q + e]));
+            }
+          }
+          m = amax2(m, __shfl_xor(m, 32));
+          const int s = scale_of(m, FP8);
+          if (keep && c < pad_to(p.n, kKPad)) {
+            mx_store_chunk(p, row, c, v, s);
+            if (lhi == 0) mx_store_scale(p, row, c, s);
+          }
+        }
+      } else {
+        const int c = c0 + (lane & 7) * 8;
+        float bv[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) bv[e] = mx_bias(p, at.e, c + e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 8 + (lane >> 3);
+          const f32x4 t0 = *reinterpret_cast<const f32x4*>(scratch + r * C::EPI_ROW + (lane & 7) * 8);
+          const f32x4 t1 = *reinterpret_cast<const f32x4*>(scratch + r * C::EPI_ROW + (lane & 7) * 8 + 4);
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = mx_act(t0[e] + bv[e], p.ep);
+            v[4 + e] = mx_act(t1[e] + bv[4 + e], p.ep);
+          }
+          const int64_t row = r0 + r;
+          if (row >= at.lo && row < at.hi) mx_store8(p, row, c, v, vec_ok);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+}
+
+// ---- skinny kernel -----------------------------------------------------------------
+// Few rows: bound by reading W once. A workgroup takes 32 rows of W and up to 16 TB rows
+// of X; its eight waves split k, stream W from memory straight into registers (16 bytes a
+// lane, consecutive lines) and add their sums through LDS in wave order. 16x16x128
+// products: lane l holds row l % 16 and the 32 k of quarter l / 16 of a 128-k step.
+// Rows of X are addressed one by one, so an expert's rows may start anywhere.
+template <int XF, int S>
+__device__ __forceinline__ f32x4 mx_mma16(i32x4 w, const i32x4 (&x)[XF == FP8 ? 2 : 1], f32x4 c, int sw, int sx) {
+  const i32x8 a = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+  if constexpr (XF == FP8) {
+    const i32x8 b = {x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 0, S, sw, S, sx);
+  } else {
+    const i32x8 b = {x[0][0], x[0][1], x[0][2], x[0][3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, S, sw, S, sx);
+  }
+}
+
+template <int XF, int TB>
+__global__ __launch_bounds__(512, 1) void mx_skinny_kernel(MxArgs p) {
+  constexpr int FB = 2, NW = 8, XR = XF == FP8 ? 2 : 1;
+  constexpr int ROW = FB * 16 + 4;   // floats per finished row
+  __shared__ __attribute__((aligned(16))) f32x4 red[NW][FB * TB][64];
+  __shared__ __attribute__((aligned(16))) float fin[TB * 16][ROW];
+  const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e = p.experts ? blockIdx.y : 0;
+  int64_t lo = 0, hi = p.m;
+  if (p.experts) expert_rows(p, e, lo, hi);
+  const int fg = blockIdx.x;   // W row group
+  const int64_t gw = group_code_bytes(FP4, p.k), gx = group_code_bytes(XF, p.k), gs = group_scale_bytes(p.k);
+  const int64_t wrg = row_groups(p.n);
+  const bool has_w = fg < wrg;   // columns past the last group only pad an e4m3 result
+  const char* wc = p.wc + (e * wrg + (has_w ? fg : 0)) * gw + g * 512 + li * 16;
+  const char* ws = p.ws + (e * wrg + (has_w ? fg : 0)) * gs + (g & 1) * 128 + li * 4;
+  const int steps = has_w ? p.kt * 2 : 0;
+  const int s0 = steps * w / NW, s1 = steps * (w + 1) / NW;
+
+  for (int64_t r0 = lo; r0 < hi; r0 += TB * 16) {
+    const char* xc[TB];
+    const char* xs[TB];
+    bool xin[TB];
+#pragma unroll
+    for (int b = 0; b < TB; ++b) {
+      const int64_t row = r0 + b * 16 + li;
+      xin[b] = row < hi;
+      const int64_t rr = xin[b] ? row : lo;
+      xc[b] = p.xc + (rr >> 5) * gx + (rr & 31) * 16 + g * 512;
+      xs[b] = p.xs + (rr >> 5) * gs + (rr & 31) * 4 + (g & 1) * 128;
+    }
+    f32x4 acc[FB][TB];
+#pragma unroll
+    for (int f = 0; f < FB; ++f)
+#pragma unroll
+      for (int b = 0; b < TB; ++b) acc[f][b] = f32x4{0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = s0; s < s1; ++s) {
+      // byte of the scale dword: block 4 (s % 2) + g of the granule
+      const int sh = 16 * (s & 1) + 8 * (g >> 1);
+      i32x4 wf[FB];
+      int sw[FB];
+#pragma unroll
+      for (int f = 0; f < FB; ++f) {
+        wf[f] = *reinterpret_cast<const i32x4*>(wc + (int64_t)s * 2048 + f * 256);
+        sw[f] = *reinterpret_cast<const int*>(ws + (int64_t)(s >> 1) * kScaleGranule + f * 64) >> sh;
+      }
+#pragma unroll
+      for (int b = 0; b < TB; ++b) {
+        i32x4 xf[XR];
+        int sx = 0;
+#pragma unroll
+        for (int h = 0; h < XR; ++h) xf[h] = i32x4{0, 0, 0, 0};
+        if (xin[b]) {
+#pragma unroll
+          for (int h = 0; h < XR; ++h)
+            xf[h] = *reinterpret_cast<const i32x4*>(xc[b] + (int64_t)s * (2048 * XR) + h * 2048);
+          sx = *reinterpret_cast<const int*>(xs[b] + (int64_t)(s >> 1) * kScaleGranule) >> sh;
+        }
+#pragma unroll
+        for (int f = 0; f < FB; ++f) acc[f][b] = mx_mma16<XF, 0>(wf[f], xf, acc[f][b], sw[f], sx);
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < FB; ++f)
+#pragma unroll
+      for (int b = 0; b < TB; ++b) red[w][f * TB + b][lane] = acc[f][b];
+    __syncthreads();
+    for (int q = threadIdx.x; q < FB * TB * 64; q += NW * 64) {
+      const int fb = q >> 6, l = q & 63, f = fb / TB, b = fb % TB;
+      f32x4 v = red[0][fb][l];
+#pragma unroll
+      for (int i = 1; i < NW; ++i) {
+        const f32x4 u = red[i][fb][l];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += u[j];
+      }
+      const int c = f * 16 + 4 * (l >> 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = fg * 32 + c + j;
+        const float y = mx_act(v[j] + mx_bias(p, e, col), p.ep);
+        fin[b * 16 + (l & 15)][c + j] = col < p.n ? y : 0.0f;
+      }
+    }
+    __syncthreads();
+    if (p.out == MX_OUT_FP8) {
+      if (threadIdx.x < TB * 16 && r0 + threadIdx.x < hi) {
+        const int t = threadIdx.x;
+        float m = 0.0f;
+        for (int c = 0; c < 32; ++c) m = amax2(m, mag(fin[t][c]));
+        const int s = scale_of(m, FP8);
+        for (int h = 0; h < 2; ++h) {
+          float v[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) v[c] = fin[t][16 * h + c];
+          mx_store_chunk(p, r0 + t, fg * 32 + 16 * h, v, s);
+        }
+        mx_store_scale(p, r0 + t, fg * 32, s);
+      }
+    } else {
+      const bool vec_ok = mx_vec_ok(p);
+      const int t = threadIdx.x >> 2, c = (threadIdx.x & 3) * 8;
+      if (t < TB * 16 && r0 + t < hi) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = fin[t][c + j];
+        mx_store8(p, r0 + t, fg * 32 + c, v, vec_ok);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace gek

@@ -1,0 +1,189 @@
+#include "mx_host.hpp"
+
+#include <algorithm>
+#include <cmath>
+
+#include "mx_tiles.hpp"
+
+namespace gemxh {
+
+namespace {
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxK = int64_t(1) << 20;
+// a launch of 256 lanes per tile keeps its lane count below 2^32
+constexpr int64_t kMaxTiles = (int64_t(1) << 24) - 1;
+bool has_bias(ge_epilog_t ep) { return ep != GE_EPILOG_NONE; }
+}  // namespace
+
+bool format_ok(ge_mx_format_t f) { return f == GE_MXFP4 || f == GE_MXFP8; }
+bool dtype_ok(ge_dtype_t d) { return d == GE_F32 || d == GE_F16 || d == GE_BF16; }
+size_t esize(ge_dtype_t d) { return d == GE_F32 ? 4 : 2; }
+bool shape_ok(int64_t rows, int64_t k) {
+  return rows >= 0 && rows <= kMaxRows && k >= 1 && k <= kMaxK &&
+         gemx::row_groups(rows) * (gemx::pad_to(k, gemx::kKPad) / gemx::kKPad) <= kMaxTiles;
+}
+
+ge_status_t check_quantize(int64_t rows, int64_t k, ge_dtype_t dt, const void* src, int64_t row_stride,
+                           int64_t col_stride, ge_mx_format_t fmt, const void* codes, const void* scales) {
+  if (!format_ok(fmt) || !dtype_ok(dt) || !shape_ok(rows, k) || row_stride < 0 || col_stride < 0)
+    return GE_ERR_INVALID_VALUE;
+  if (rows == 0) return GE_OK;
+  if (!src || !codes || !scales) return GE_ERR_NULL_POINTER;
+  if (!aligned(src, esize(dt)) || !aligned(codes, 16) || !aligned(scales, 16)) return GE_ERR_MISALIGNED;
+  return GE_OK;
+}
+
+ge_status_t check_dequantize(int64_t rows, int64_t k, ge_mx_format_t fmt, const void* codes, const void* scales,
+                             ge_dtype_t dt, const void* dst, int64_t row_stride) {
+  if (!format_ok(fmt) || !dtype_ok(dt) || !shape_ok(rows, k) || row_stride < (rows > 1 ? k : 0))
+    return GE_ERR_INVALID_VALUE;
+  if (rows == 0) return GE_OK;
+  if (!dst || !codes || !scales) return GE_ERR_NULL_POINTER;
+  if (!aligned(dst, esize(dt)) || !aligned(codes, 16) || !aligned(scales, 16)) return GE_ERR_MISALIGNED;
+  return GE_OK;
+}
+
+ge_status_t check_pack(int64_t rows, int64_t k, ge_mx_format_t fmt, const void* src_codes, const void* src_scales,
+                       const void* codes, const void* scales) {
+  if (!format_ok(fmt) || !shape_ok(rows, k)) return GE_ERR_INVALID_VALUE;
+  if (rows == 0) return GE_OK;
+  if (!src_codes || !src_scales || !codes || !scales) return GE_ERR_NULL_POINTER;
+  if (!aligned(codes, 16) || !aligned(scales, 16)) return GE_ERR_MISALIGNED;
+  return GE_OK;
+}
+
+ge_status_t check_plan(int64_t n, int64_t k, int64_t experts, ge_mx_types_t t, ge_epilog_t ep) {
+  if (n < 1 || n > kMaxK || k < 1 || k > kMaxK || experts < 0 || experts > 4096) return GE_ERR_INVALID_VALUE;
+  if (!format_ok(t.x) || !dtype_ok(t.vec)) return GE_ERR_INVALID_VALUE;
+  if (t.d != GE_MX_D_F32 && t.d != GE_MX_D_F16 && t.d != GE_MX_D_BF16 && t.d != GE_MX_D_MXFP8)
+    return GE_ERR_INVALID_VALUE;
+  switch (ep) {
+    case GE_EPILOG_NONE:
+    case GE_EPILOG_BIAS:
+    case GE_EPILOG_RELU_BIAS:
+    case GE_EPILOG_GELU_BIAS: break;
+    case GE_EPILOG_RELU_AUX_BIAS:
+    case GE_EPILOG_DRELU_BGRAD:
+    case GE_EPILOG_RELU_BIAS_UNFUSED:
+    case GE_EPILOG_DRELU_BGRAD_UNFUSED: return GE_ERR_NOT_SUPPORTED;
+    default: return GE_ERR_INVALID_VALUE;
+  }
+  // the bias has D's type or fp32 (any type beside an 8-bit D)
+  if (t.d != GE_MX_D_MXFP8 && t.vec != GE_F32 && (int)t.vec != (int)t.d) return GE_ERR_NOT_SUPPORTED;
+  if (!shape_ok(n, k)) return GE_ERR_NOT_SUPPORTED;
+  return GE_OK;
+}
+
+ge_status_t check_execute(int64_t m, int64_t experts, ge_mx_types_t t, ge_epilog_t ep, const void* xc, const void* xs,
+                          const void* wc, const void* ws, const void* bias, const void* offsets, const void* D,
+                          const void* ds) {
+  if (m < 0 || m > kMaxRows) return GE_ERR_INVALID_VALUE;
+  if (m == 0) return GE_OK;
+  if (!xc || !xs || !wc || !ws || !D || (has_bias(ep) && !bias) || (experts && !offsets) ||
+      (t.d == GE_MX_D_MXFP8 && !ds))
+    return GE_ERR_NULL_POINTER;
+  if (!aligned(xc, 16) || !aligned(xs, 16) || !aligned(wc, 16) || !aligned(ws, 16) ||
+      (has_bias(ep) && !aligned(bias, esize(t.vec))) || (experts && !aligned(offsets, 4)) ||
+      !aligned(D, t.d == GE_MX_D_MXFP8 ? 16 : t.d == GE_MX_D_F32 ? 4 : 2))
+    return GE_ERR_MISALIGNED;
+  return GE_OK;
+}
+
+MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t t, int cus) {
+  using namespace gemx;
+  MxLaunch L;
+  const int64_t cols = t.d == GE_MX_D_MXFP8 ? pad_to(n, kKPad) : n;   // an 8-bit D is written with its padding
+  const int64_t groups = experts ? experts : 1;
+  const int64_t rows = (m + groups - 1) / groups;   // of an even share
+  if (rows <= 64) {
+    L.cfg = rows <= 16 ? MX_S16 : rows <= 32 ? MX_S32 : MX_S64;
+    L.tiles_n = (int)((cols + 31) / 32);
+    L.tiles_m = 1;
+    L.grid_x = L.tiles_n;
+    L.grid_y = groups;
+    return L;
+  }
+  auto count = [&](int cfg, int64_t& tm, int64_t& tn) {
+    const MxTile& T = kMxTiles[cfg];
+    tm = experts ? (m + 31 * experts) / T.bm + experts : (m + T.bm - 1) / T.bm;
+    tn = (cols + T.bn - 1) / T.bn;
+    return tm * tn;
+  };
+  int64_t tm, tn;
+  L.cfg = MX_L;
+  if (count(MX_L, tm, tn) < cus) {
+    L.cfg = MX_M;
+    count(MX_M, tm, tn);
+  }
+  L.tiles_m = (int)tm;
+  L.tiles_n = (int)tn;
+  const int64_t kt = pad_to(k, kKPad) / mx_bk((int)t.x);
+  if (!experts && L.cfg == MX_M && tm * tn < cus && tm * tn <= kMxCounters)
+    L.splits = (int)std::max<int64_t>(1, std::min<int64_t>({cus / (tm * tn), kt / 4, kMxMaxSplit}));
+  L.grid_x = tm * tn * L.splits;
+  return L;
+}
+
+size_t workspace_bytes(int64_t n, int64_t k, int64_t experts, ge_mx_types_t t, int cus) {
+  using namespace gemx;
+  (void)n, (void)k, (void)t;
+  if (experts) return 0;
+  // split tiles times parts stay within one workgroup per compute unit
+  return kMxCounterBytes + (size_t)cus * kMxTiles[MX_M].bm * kMxTiles[MX_M].bn * 4;
+}
+
+
+// ---- norm ---------------------------------------------------------------------------
+namespace {
+ge_status_t norm_common(int64_t rows, int64_t d, ge_dtype_t dt, ge_dtype_t wdt, float eps) {
+  if (rows < 0 || rows > kMaxRows || d < 1 || !dtype_ok(dt) || !dtype_ok(wdt) || !(eps >= 0.0f) || std::isinf(eps))
+    return GE_ERR_INVALID_VALUE;
+  if (d > kNormMaxD || (wdt != GE_F32 && wdt != dt)) return GE_ERR_NOT_SUPPORTED;
+  return GE_OK;
+}
+bool ld_ok(int64_t ld, int64_t rows, int64_t d) { return rows <= 1 || ld >= d; }
+}  // namespace
+
+ge_status_t check_norm(int64_t rows, int64_t d, ge_dtype_t dt, const void* x, int64_t ldx, const void* residual,
+                       int64_t ldr, const void* weight, ge_dtype_t wdt, float eps, const void* sum, int64_t lds,
+                       const void* y, int64_t ldy, const void* codes, const void* scales) {
+  if (ge_status_t st = norm_common(rows, d, dt, wdt, eps); st != GE_OK) return st;
+  // inputs may repeat a row (stride 0), outputs may not overlap
+  if (ldx < 0 || (residual && ldr < 0) || (sum && !ld_ok(lds, rows, d)) || (y && !ld_ok(ldy, rows, d)))
+    return GE_ERR_INVALID_VALUE;
+  if (codes && !shape_ok(rows, d)) return GE_ERR_NOT_SUPPORTED;
+  if (rows == 0) return GE_OK;
+  if (!x || !weight || (!y && !codes) || (residual && !sum) || !codes != !scales) return GE_ERR_NULL_POINTER;
+  const size_t e = esize(dt);
+  if (!aligned(x, e) || !aligned(residual, e) || !aligned(weight, esize(wdt)) || !aligned(sum, e) || !aligned(y, e) ||
+      !aligned(codes, 16) || !aligned(scales, 16))
+    return GE_ERR_MISALIGNED;
+  return GE_OK;
+}
+
+ge_status_t check_norm_backward(int64_t rows, int64_t d, ge_dtype_t dt, const void* dy, int64_t lddy, const void* s,
+                                int64_t lds, const void* weight, ge_dtype_t wdt, float eps, const void* dres,
+                                int64_t lddr, const void* dx, int64_t lddx, const void* dw, const void* ws,
+                                size_t ws_bytes) {
+  if (ge_status_t st = norm_common(rows, d, dt, wdt, eps); st != GE_OK) return st;
+  if (lddy < 0 || lds < 0 || (dres && lddr < 0) || !ld_ok(lddx, rows, d)) return GE_ERR_INVALID_VALUE;
+  if (!dw || !weight || (rows && (!dy || !s || !dx || !ws))) return GE_ERR_NULL_POINTER;
+  const size_t e = esize(dt);
+  if (!aligned(dy, e) || !aligned(s, e) || !aligned(weight, esize(wdt)) || !aligned(dres, e) || !aligned(dx, e) ||
+      !aligned(dw, esize(wdt)) || !aligned(ws, 16))
+    return GE_ERR_MISALIGNED;
+  if (ws_bytes < norm_workspace_bytes(rows, d)) return GE_ERR_SCRATCH;
+  return GE_OK;
+}
+
+int64_t norm_backward_groups(int64_t rows, int64_t d) {
+  (void)d;
+  return std::min<int64_t>(rows, 512);
+}
+size_t norm_workspace_bytes(int64_t rows, int64_t d) {
+  if (rows <= 0 || d < 1) return 0;
+  return (size_t)norm_backward_groups(rows, d) * (size_t)d * 4;
+}
+
+}  // namespace gemxh

@@ -1,0 +1,334 @@
+// Conversion to and from microscaled operands (layout and arithmetic: mx_format.hpp), and
+// packing of row-major codes into that layout.
+//
+// All four kernels work in tiles of 32 rows x 256 k, one workgroup of 256 lanes each: a
+// tile's codes are 4 KB (e2m1) or 8 KB (e4m3) and its scales 256 bytes of consecutive
+// memory, so they pass through LDS and move in whole lines, while the plain side moves in
+// row pieces of 256 values. Bound by memory: one read and one write per value.
+#include <hip/hip_runtime.h>
+
+#include "gemm_epilog.h"
+#include "kernels.hpp"
+#include "mx_format.hpp"
+#include "mx_host.hpp"
+
+namespace gek {
+namespace {
+
+using namespace gemx;
+
+// Element i of a row-major array of type DT, widened.
+template <int DT>
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+  return load_vec(p, DT, i);
+}
+// Eight consecutive elements from 16-byte aligned memory, widened.
+template <int DT>
+__device__ __forceinline__ void load8(const char* p, float (&v)[8]) {
+  if constexpr (DT == F32) {
+    const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = a[e];
+      v[4 + e] = b[e];
+    }
+  } else {
+    const i32x4 a = *reinterpret_cast<const i32x4*>(p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = Tr<DT>::widen((uint16_t)((uint32_t)a[e / 2] >> (16 * (e & 1))));
+  }
+}
+
+struct QuantArgs {
+  const void* src;
+  char* codes;
+  char* scales;
+  int64_t rows, k, row_stride, col_stride;   // strides in elements
+  int64_t kt;                                // 256-k granules
+};
+
+// The tile's codes and scales from LDS to their place, 16 bytes a lane.
+template <int FMT>
+__device__ __forceinline__ void store_tile(const QuantArgs& a, int64_t rb, int64_t kt, const char* lc, const char* ls) {
+  constexpr int CB = FMT == FP4 ? 4096 : 8192;
+  char* dc = a.codes + (rb * a.kt + kt) * CB;
+  char* ds = a.scales + (rb * a.kt + kt) * kScaleGranule;
+#pragma unroll
+  for (int i = 0; i < CB / 4096; ++i)
+    reinterpret_cast<i32x4*>(dc)[i * 256 + threadIdx.x] = reinterpret_cast<const i32x4*>(lc)[i * 256 + threadIdx.x];
+  if (threadIdx.x < 16) reinterpret_cast<i32x4*>(ds)[threadIdx.x] = reinterpret_cast<const i32x4*>(ls)[threadIdx.x];
+}
+
+// Rows contiguous along k (col_stride 1) or any strides (VEC false: element loads).
+// A lane takes 8 consecutive k of a row; the four lanes of a quad share a block.
+template <int DT, int FMT, bool VEC>
+__global__ __launch_bounds__(256) void mx_quantize_rows_kernel(QuantArgs a) {
+  __shared__ __attribute__((aligned(16))) char lc[FMT == FP4 ? 4096 : 8192];
+  __shared__ __attribute__((aligned(16))) char ls[kScaleGranule];
+  const int64_t rb = blockIdx.x / a.kt, kt = blockIdx.x % a.kt;
+  const int t = threadIdx.x, kk = (t & 31) * 8;
+  const int64_t k0 = kt * kKPad + kk;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (t >> 5);
+    const int64_t row = rb * kRowGroup + r;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (row < a.rows) {
+      if constexpr (VEC) {
+        if (k0 < a.k) load8<DT>(static_cast<const char*>(a.src) + (row * a.row_stride + k0) * (DT == F32 ? 4 : 2), v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (k0 + e < a.k) v[e] = load1<DT>(a.src, row * a.row_stride + (k0 + e) * a.col_stride);
+      }
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = amax2(m, mag(v[e]));
+    const int s = scale_of(amax_quad(m), FMT);
+    if constexpr (FMT == FP4) {
+      *reinterpret_cast<uint32_t*>(lc + (kk / 32) * 512 + r * 16 + (kk % 32) / 2) = to_fp4x8(v, s);
+    } else {
+      const i32x2 c = {(int)to_fp8x4(v[0], v[1], v[2], v[3], s), (int)to_fp8x4(v[4], v[5], v[6], v[7], s)};
+      *reinterpret_cast<i32x2*>(lc + (kk / 16) * 512 + r * 16 + kk % 16) = c;
+    }
+    const int b = kk / 32;
+    if ((t & 3) == 0) ls[(b & 1) * 128 + r * 4 + b / 2] = (char)s;
+  }
+  __syncthreads();
+  store_tile<FMT>(a, rb, kt, lc, ls);
+}
+
+// Rows that lie next to each other in memory (row_stride 1): a lane takes one block of
+// one row, so the 32 lanes of a half-wave read 32 neighbouring rows at one k.
+template <int DT, int FMT>
+__global__ __launch_bounds__(256) void mx_quantize_cols_kernel(QuantArgs a) {
+  __shared__ __attribute__((aligned(16))) char lc[FMT == FP4 ? 4096 : 8192];
+  __shared__ __attribute__((aligned(16))) char ls[kScaleGranule];
+  const int64_t groups = row_groups(a.rows);
+  const int64_t kt = blockIdx.x / groups, rb = blockIdx.x % groups;
+  const int r = threadIdx.x & 31, b = threadIdx.x >> 5;
+  const int64_t row = rb * kRowGroup + r, k0 = kt * kKPad + b * 32;
+  float v[32];
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    v[e] = row < a.rows && k0 + e < a.k ? load1<DT>(a.src, row * a.row_stride + (k0 + e) * a.col_stride) : 0.0f;
+    m = amax2(m, mag(v[e]));
+  }
+  const int s = scale_of(m, FMT);
+  if constexpr (FMT == FP4) {
+    i32x4 c;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float w[8] = {v[8 * q],     v[8 * q + 1], v[8 * q + 2], v[8 * q + 3],
+                          v[8 * q + 4], v[8 * q + 5], v[8 * q + 6], v[8 * q + 7]};
+      c[q] = (int)to_fp4x8(w, s);
+    }
+    *reinterpret_cast<i32x4*>(lc + b * 512 + r * 16) = c;
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      i32x4 c;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        c[q] = (int)to_fp8x4(v[16 * h + 4 * q], v[16 * h + 4 * q + 1], v[16 * h + 4 * q + 2], v[16 * h + 4 * q + 3], s);
+      *reinterpret_cast<i32x4*>(lc + (2 * b + h) * 512 + r * 16) = c;
+    }
+  }
+  ls[(b & 1) * 128 + r * 4 + b / 2] = (char)s;
+  __syncthreads();
+  store_tile<FMT>(a, rb, kt, lc, ls);
+}
+
+struct DequantArgs {
+  const char* codes;
+  const char* scales;
+  void* dst;
+  int64_t rows, k, row_stride, kt;
+};
+
+// One lane writes 8 consecutive k of a row. VEC: 16-byte stores (k a multiple of 8, rows
+// 16-byte aligned).
+template <int DT, int FMT, bool VEC>
+__global__ __launch_bounds__(256) void mx_dequantize_kernel(DequantArgs a) {
+  constexpr int CB = FMT == FP4 ? 4096 : 8192;
+  __shared__ __attribute__((aligned(16))) char lc[CB];
+  __shared__ __attribute__((aligned(16))) char ls[kScaleGranule];
+  const int64_t rb = blockIdx.x / a.kt, kt = blockIdx.x % a.kt;
+  const int t = threadIdx.x;
+  const char* sc = a.codes + (rb * a.kt + kt) * CB;
+  const char* ss = a.scales + (rb * a.kt + kt) * kScaleGranule;
+#pragma unroll
+  for (int i = 0; i < CB / 4096; ++i)
+    reinterpret_cast<i32x4*>(lc)[i * 256 + t] = reinterpret_cast<const i32x4*>(sc)[i * 256 + t];
+  if (t < 16) reinterpret_cast<i32x4*>(ls)[t] = reinterpret_cast<const i32x4*>(ss)[t];
+  __syncthreads();
+  const int kk = (t & 31) * 8, b = kk / 32;
+  const int64_t k0 = kt * kKPad + kk;
+  if (k0 >= a.k) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (t >> 5);
+    const int64_t row = rb * kRowGroup + r;
+    if (row >= a.rows) break;
+    const float f = scale_value((uint8_t)ls[(b & 1) * 128 + r * 4 + b / 2]);
+    float v[8];
+    if constexpr (FMT == FP4) {
+      const uint32_t c = *reinterpret_cast<const uint32_t*>(lc + (kk / 32) * 512 + r * 16 + (kk % 32) / 2);
+      const auto p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
+      const auto p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
+      v[0] = p0[0], v[1] = p0[1], v[2] = p1[0], v[3] = p1[1], v[4] = p2[0], v[5] = p2[1], v[6] = p3[0], v[7] = p3[1];
+    } else {
+      const i32x2 c = *reinterpret_cast<const i32x2*>(lc + (kk / 16) * 512 + r * 16 + kk % 16);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const auto p0 = __builtin_amdgcn_cvt_pk_f32_fp8(c[h], 0), p1 = __builtin_amdgcn_cvt_pk_f32_fp8(c[h], 1);
+        v[4 * h] = p0[0], v[4 * h + 1] = p0[1], v[4 * h + 2] = p1[0], v[4 * h + 3] = p1[1];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= f;
+    const int64_t at = row * a.row_stride + k0;
+    if constexpr (VEC) {
+      if constexpr (DT == F32) {
+        f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(a.dst) + at);
+        d[0] = f32x4{v[0], v[1], v[2], v[3]};
+        d[1] = f32x4{v[4], v[5], v[6], v[7]};
+      } else {
+        i32x4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = (int)Tr<DT>::pack2(v[2 * e], v[2 * e + 1]);
+        *reinterpret_cast<i32x4*>(static_cast<char*>(a.dst) + at * 2) = o;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (k0 + e < a.k) store_vec(a.dst, DT, at + e, v[e]);
+    }
+  }
+}
+
+struct PackArgs {
+  const uint8_t* src_codes;    // (rows, code_row) row-major
+  const uint8_t* src_scales;   // (rows, ceil(k / 32)) row-major
+  char* codes;
+  char* scales;
+  int64_t rows, k, kt, code_row;
+  int fp4;
+};
+
+// Row-major codes and scales into the packed layout: one lane per block of 32 values.
+// Runs once per weight, so it is kept simple: byte loads, no staging.
+__global__ __launch_bounds__(256) void mx_pack_kernel(PackArgs a) {
+  const int64_t rb = blockIdx.x / a.kt, kt = blockIdx.x % a.kt;
+  const int r = threadIdx.x & 31, b = threadIdx.x >> 5;
+  const int64_t row = rb * kRowGroup + r, k0 = kt * kKPad + b * 32, blk = k0 / 32;
+  const bool in = row < a.rows && k0 < a.k;
+  const int left = in ? (int)min((int64_t)32, a.k - k0) : 0;   // values of this block
+  a.scales[(rb * a.kt + kt) * kScaleGranule + (b & 1) * 128 + r * 4 + b / 2] =
+      in ? (char)a.src_scales[row * ((a.k + 31) / 32) + blk] : (char)0;
+  if (a.fp4) {
+    char* d = a.codes + (rb * a.kt + kt) * 4096 + b * 512 + r * 16;
+    for (int e = 0; e < 16; ++e) {
+      uint8_t c = 2 * e < left ? a.src_codes[row * a.code_row + k0 / 2 + e] : 0;
+      if (2 * e + 1 >= left) c &= 15;   // an odd k's last byte holds one value
+      d[e] = (char)c;
+    }
+  } else {
+    char* d = a.codes + (rb * a.kt + kt) * 8192 + 2 * b * 512 + r * 16;
+    for (int e = 0; e < 32; ++e) d[(e / 16) * 512 + e % 16] = e < left ? (char)a.src_codes[row * a.code_row + k0 + e] : 0;
+  }
+}
+
+template <int DT, int FMT>
+const void* quantize_fn(bool cols, bool vec) {
+  if (cols) return reinterpret_cast<const void*>(&mx_quantize_cols_kernel<DT, FMT>);
+  return vec ? reinterpret_cast<const void*>(&mx_quantize_rows_kernel<DT, FMT, true>)
+             : reinterpret_cast<const void*>(&mx_quantize_rows_kernel<DT, FMT, false>);
+}
+template <int DT>
+const void* quantize_fn(int fmt, bool cols, bool vec) {
+  return fmt == FP4 ? quantize_fn<DT, FP4>(cols, vec) : quantize_fn<DT, FP8>(cols, vec);
+}
+template <int DT, int FMT>
+const void* dequantize_fn(bool vec) {
+  return vec ? reinterpret_cast<const void*>(&mx_dequantize_kernel<DT, FMT, true>)
+             : reinterpret_cast<const void*>(&mx_dequantize_kernel<DT, FMT, false>);
+}
+template <int DT>
+const void* dequantize_fn(int fmt, bool vec) {
+  return fmt == FP4 ? dequantize_fn<DT, FP4>(vec) : dequantize_fn<DT, FP8>(vec);
+}
+
+}  // namespace
+}  // namespace gek
+
+extern "C" {
+
+size_t gemm_epilog_mx_code_bytes(ge_mx_format_t fmt, int64_t rows, int64_t k) {
+  return gemxh::shape_ok(rows, k) && gemxh::format_ok(fmt) ? (size_t)gemx::code_bytes(fmt, rows, k) : 0;
+}
+
+size_t gemm_epilog_mx_scale_bytes(int64_t rows, int64_t k) {
+  return gemxh::shape_ok(rows, k) ? (size_t)gemx::scale_bytes(rows, k) : 0;
+}
+
+ge_status_t gemm_epilog_mx_quantize(int64_t rows, int64_t k, ge_dtype_t dt, const void* src, int64_t row_stride,
+                                    int64_t col_stride, ge_mx_format_t fmt, void* codes, void* scales, void* stream) {
+  if (ge_status_t st = gemxh::check_quantize(rows, k, dt, src, row_stride, col_stride, fmt, codes, scales); st != GE_OK)
+    return st;
+  if (rows == 0) return GE_OK;
+  const size_t es = dt == GE_F32 ? 4 : 2;
+  gek::QuantArgs a{src, static_cast<char*>(codes), static_cast<char*>(scales), rows, k, row_stride, col_stride,
+                   gemx::pad_to(k, gemx::kKPad) / gemx::kKPad};
+  // Rows next to each other (k strided) go to the kernel whose lanes run along the rows:
+  // reading them along k would touch a line per value.
+  const bool cols = col_stride != 1 && row_stride == 1;
+  const bool vec = col_stride == 1 && k % 8 == 0 && row_stride * (int64_t)es % 16 == 0 &&
+                   reinterpret_cast<uintptr_t>(src) % 16 == 0;
+  const void* fn = dt == GE_F32   ? gek::quantize_fn<gek::F32>(fmt, cols, vec)
+                   : dt == GE_F16 ? gek::quantize_fn<gek::F16>(fmt, cols, vec)
+                                  : gek::quantize_fn<gek::BF16>(fmt, cols, vec);
+  void* params[] = {&a};
+  return hipLaunchKernel(fn, dim3((unsigned)(gemx::row_groups(rows) * a.kt)), dim3(256), params, 0,
+                         static_cast<hipStream_t>(stream)) == hipSuccess
+             ? GE_OK
+             : GE_ERR_HIP;
+}
+
+ge_status_t gemm_epilog_mx_dequantize(int64_t rows, int64_t k, ge_mx_format_t fmt, const void* codes,
+                                      const void* scales, ge_dtype_t dt, void* dst, int64_t row_stride, void* stream) {
+  if (ge_status_t st = gemxh::check_dequantize(rows, k, fmt, codes, scales, dt, dst, row_stride); st != GE_OK) return st;
+  if (rows == 0) return GE_OK;
+  const size_t es = dt == GE_F32 ? 4 : 2;
+  gek::DequantArgs a{static_cast<const char*>(codes), static_cast<const char*>(scales), dst, rows, k, row_stride,
+                     gemx::pad_to(k, gemx::kKPad) / gemx::kKPad};
+  const bool vec =
+      k % 8 == 0 && row_stride * (int64_t)es % 16 == 0 && reinterpret_cast<uintptr_t>(dst) % 16 == 0;
+  const void* fn = dt == GE_F32   ? gek::dequantize_fn<gek::F32>(fmt, vec)
+                   : dt == GE_F16 ? gek::dequantize_fn<gek::F16>(fmt, vec)
+                                  : gek::dequantize_fn<gek::BF16>(fmt, vec);
+  void* params[] = {&a};
+  return hipLaunchKernel(fn, dim3((unsigned)(gemx::row_groups(rows) * a.kt)), dim3(256), params, 0,
+                         static_cast<hipStream_t>(stream)) == hipSuccess
+             ? GE_OK
+             : GE_ERR_HIP;
+}
+
+ge_status_t gemm_epilog_mx_pack(int64_t rows, int64_t k, ge_mx_format_t fmt, const void* src_codes,
+                                const void* src_scales, void* codes, void* scales, void* stream) {
+  if (ge_status_t st = gemxh::check_pack(rows, k, fmt, src_codes, src_scales, codes, scales); st != GE_OK) return st;
+  if (rows == 0) return GE_OK;
+  gek::PackArgs a{static_cast<const uint8_t*>(src_codes), static_cast<const uint8_t*>(src_scales),
+                  static_cast<char*>(codes), static_cast<char*>(scales), rows, k,
+                  gemx::pad_to(k, gemx::kKPad) / gemx::kKPad, fmt == GE_MXFP4 ? (k + 1) / 2 : k, fmt == GE_MXFP4};
+  void* params[] = {&a};
+  return hipLaunchKernel(reinterpret_cast<const void*>(&gek::mx_pack_kernel),
+                         dim3((unsigned)(gemx::row_groups(rows) * a.kt)), dim3(256), params, 0,
+                         static_cast<hipStream_t>(stream)) == hipSuccess
+             ? GE_OK
+             : GE_ERR_HIP;
+}
+
+}  // extern "C"

@@ -306,6 +306,166 @@ const char* gemm_epilog_describe(ge_handle_t h);
 /* Static string for a status code. */
 const char* gemm_epilog_status_string(ge_status_t s);
 
+/* ---- Microscaled feed-forward operators ---------------------------------------------
+ * The serving form of a feed-forward block: the residual addition and root-mean-square
+ * norm in front of it, its operands in 8 and 4 bits with a shared scale per 32 values,
+ * and its products, dense or by expert, with the epilogues above. The tokens lie along
+ * the rows here (X (m, k), W (n, k), D = act(X . W^T + bias) of (m, n), one bias per
+ * column), as a serving stack holds them.
+ *
+ * Microscaled values. Each 32 consecutive k values of a row share the scale 2^(s - 127)
+ * of one byte s; s = 255 stands for NaN. With a the block's largest magnitude,
+ * s = floor(log2 a) - emax + 127 held to 0 .. 254 (emax 2 for MXFP4, 8 for MXFP8; 0 for
+ * a = 0), and 255 if the block holds an infinity or a NaN. The elements are the values over
+ * the scale rounded to nearest even, saturating at the largest element.
+ * Layout (the order the matrix instructions read; k is padded to a multiple of 256 with
+ * zeros, rows to a multiple of 32, C = padded k / V, KT = padded k / 256):
+ *   code byte of (r, k):  ((r/32) C + k/V) 512 + (r%32) 16 + b, with V = 32 and
+ *     b = (k%32)/2, even k in the low nibble (MXFP4), or V = 16 and b = k%16 (MXFP8);
+ *   scale byte of (r, k): ((r/32) KT + k/256) 256 + (k/32%2) 128 + (r%32) 4 + k/64%4.
+ * gemm_epilog_mx_code_bytes / _scale_bytes give the buffers' sizes; both buffers are
+ * 16-byte aligned. The contents of padding rows do not matter to any reader.
+ *
+ * Threading and errors as above: checks on the host first, work enqueued on `stream`,
+ * kernel launches only (an execute may be captured into a HIP graph).
+ */
+typedef enum {
+  GE_MXFP4 = 0, /* 4-bit elements e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives */
+  GE_MXFP8 = 1  /* 8-bit elements e4m3: up to 448, no infinity */
+} ge_mx_format_t;
+
+/* Bytes of the codes / scales of a (rows, k) operand; 0 for sizes outside the supported
+ * set (0 <= rows <= 2^31 - 1, 1 <= k <= 2^20, at most 2^24 - 1 tiles of 32 x 256). */
+size_t gemm_epilog_mx_code_bytes(ge_mx_format_t fmt, int64_t rows, int64_t k);
+size_t gemm_epilog_mx_scale_bytes(int64_t rows, int64_t k);
+
+/*
+ * gemm_epilog_mx_quantize - (rows, k) values of type dt to microscaled form.
+ *   src  : device; element (r, k) at src[r row_stride + k col_stride] (strides in
+ *          elements, not negative). Rows contiguous along k (col_stride 1), the columns of
+ *          a features-by-batch matrix (row_stride 1), or any other strides.
+ *   codes, scales : device, written whole, padding included.
+ * rows = 0 does nothing. The blocks run along k in both orders.
+ */
+ge_status_t gemm_epilog_mx_quantize(int64_t rows, int64_t k, ge_dtype_t dt, const void* src, int64_t row_stride,
+                                    int64_t col_stride, ge_mx_format_t fmt, void* codes, void* scales, void* stream);
+
+/* gemm_epilog_mx_dequantize - the values (element times scale, rounded to dt) of a
+ * microscaled operand, to dst[r row_stride + k], row_stride >= k. */
+ge_status_t gemm_epilog_mx_dequantize(int64_t rows, int64_t k, ge_mx_format_t fmt, const void* codes,
+                                      const void* scales, ge_dtype_t dt, void* dst, int64_t row_stride, void* stream);
+
+/* gemm_epilog_mx_pack - row-major codes ((rows, ceil(k/2)) bytes for MXFP4, (rows, k) for
+ * MXFP8) and row-major scales ((rows, ceil(k/32)) bytes), as checkpoints hold them, into
+ * the layout above. Once per weight. */
+ge_status_t gemm_epilog_mx_pack(int64_t rows, int64_t k, ge_mx_format_t fmt, const void* src_codes,
+                                const void* src_scales, void* codes, void* scales, void* stream);
+
+/* Type of a product's D: 32 or 16 bits, row-major (m, n), or MXFP8 in the layout above
+ * (rows m, k = n), ready to be the next product's X. */
+typedef enum { GE_MX_D_F32 = 0, GE_MX_D_F16 = 1, GE_MX_D_BF16 = 2, GE_MX_D_MXFP8 = 3 } ge_mx_out_t;
+
+/* x: format of X (W is MXFP4); d: type of D; vec: type of bias (fp32, or D's type; any
+ * type with an MXFP8 D). Accumulation is always fp32. */
+typedef struct {
+  ge_mx_format_t x;
+  ge_mx_out_t d;
+  ge_dtype_t vec;
+} ge_mx_types_t;
+
+typedef struct ge_mx_plan* ge_mx_handle_t; /* opaque; owned by the library */
+
+/*
+ * gemm_epilog_mx_plan - plan D = act(X . W^T + bias) for one (n, k) and any m.
+ *   n, k    : 1 .. 2^20.
+ *   experts : 0 for one product; 1 .. 4096 for products by expert, where the rows of X
+ *             are sorted by expert and each expert has its own W and bias.
+ *   ep      : NONE, BIAS, RELU_BIAS or GELU_BIAS (other epilogues: GE_ERR_NOT_SUPPORTED).
+ * Allocates the workspace (sums of a product whose k loop is split over workgroups). A
+ * plan may be used from one stream at a time; any number of weights may share it.
+ */
+ge_status_t gemm_epilog_mx_plan(int64_t n, int64_t k, int64_t experts, ge_mx_types_t types, ge_epilog_t ep,
+                                ge_mx_handle_t* out);
+
+/* What an execute of m rows would launch. */
+typedef struct {
+  int tile_m, tile_n;      /* rows of X and of W per workgroup */
+  int waves;               /* waves per workgroup */
+  int stages;              /* LDS stages of the operand ring (0: W goes straight to registers) */
+  int splits;              /* workgroups that share a tile's k loop */
+  int64_t workgroups;
+  size_t workspace_bytes;  /* device workspace of the plan (independent of m) */
+} ge_mx_plan_info_t;
+
+/* gemm_epilog_mx_plan_info - computed on the host with no HIP call, for a gfx950 device
+ * with `compute_units` compute units (1 .. 4096). */
+ge_status_t gemm_epilog_mx_plan_info(int64_t n, int64_t k, int64_t experts, ge_mx_types_t types, ge_epilog_t ep,
+                                     int64_t m, int compute_units, ge_mx_plan_info_t* info);
+
+/*
+ * gemm_epilog_mx_execute - enqueue the product for m rows (0 <= m <= 2^31 - 1; 0 does
+ * nothing).
+ *   x_codes, x_scales : X (m, k).
+ *   w_codes, w_scales : W (n, k), MXFP4; by expert: the experts' buffers one after the
+ *             other, each of the size of an (n, k) operand.
+ *   bias    : n values of type vec, (experts, n) by expert; ignored (may be NULL) for NONE.
+ *   offsets : by expert: device, experts + 1 int32; expert e has rows offsets[e] ..
+ *             offsets[e+1] - 1 of X and D. Read when the kernel runs, so they may come from
+ *             a kernel before it. Values outside 0 .. m or that run backwards are held to
+ *             valid or empty ranges; rows that no expert has are not written. NULL otherwise.
+ *   D       : (m, n) of type d, aligned to its element; or MXFP8 codes, 16-byte aligned
+ *             (written with the padding along n, without padding rows).
+ *   d_scales: MXFP8 D: its scales; ignored otherwise.
+ */
+ge_status_t gemm_epilog_mx_execute(ge_mx_handle_t h, int64_t m, const void* x_codes, const void* x_scales,
+                                   const void* w_codes, const void* w_scales, const void* bias, const void* offsets,
+                                   void* D, void* d_scales, void* stream);
+
+/* gemm_epilog_mx_free - release a plan and its workspace. NULL is accepted (GE_OK). */
+ge_status_t gemm_epilog_mx_free(ge_mx_handle_t h);
+
+/*
+ * gemm_epilog_rms_norm - s = x + residual rounded to dt (s = x without a residual) and
+ * y = s / sqrt(mean(s^2) + eps) * weight, over rows of d values; sums in fp32.
+ *   rows, d  : 0 <= rows <= 2^31 - 1 (0 does nothing), 1 <= d <= 32768 (above:
+ *              GE_ERR_NOT_SUPPORTED).
+ *   x, residual : (rows, d) of type dt, row strides ldx, ldr in elements (0 repeats a
+ *              row). residual may be NULL.
+ *   weight   : d values of type wdt (dt or fp32).
+ *   eps      : >= 0 and finite.
+ *   sum      : receives s, row stride lds; needed with a residual, optional without. May be
+ *              x or residual itself.
+ *   y        : receives y as dt, row stride ldy; NULL if not wanted.
+ *   codes, scales : receive y as MXFP8, with zeros in the padding along d (padding rows are
+ *              not written); both NULL if not wanted. At least one form of y is needed.
+ * Pointers are aligned to their elements (codes and scales to 16 bytes); 16-byte aligned
+ * rows with d a multiple of 8 run fastest.
+ */
+ge_status_t gemm_epilog_rms_norm(int64_t rows, int64_t d, ge_dtype_t dt, const void* x, int64_t ldx,
+                                 const void* residual, int64_t ldr, const void* weight, ge_dtype_t wdt, float eps,
+                                 void* sum, int64_t lds, void* y, int64_t ldy, void* codes, void* scales,
+                                 void* stream);
+
+/* Bytes of the workspace of gemm_epilog_rms_norm_backward (0 for rows = 0). */
+size_t gemm_epilog_rms_norm_workspace_bytes(int64_t rows, int64_t d);
+
+/*
+ * gemm_epilog_rms_norm_backward - gradients of the norm from the stored s:
+ * dx = r (g - h mean(g h)) + dresidual with r = 1 / sqrt(mean(s^2) + eps), g = dy weight,
+ * h = s r; dweight = sum over rows of dy h, in fp32 and in a fixed order. dx is the gradient
+ * of x and of residual alike.
+ *   dy, s, dresidual : (rows, d) of type dt with their row strides; dresidual (the gradient
+ *              that reaches s past the norm) may be NULL.
+ *   dx       : (rows, d) of type dt; may be dy or dresidual itself.
+ *   dweight  : d values of type wdt (zeros for rows = 0).
+ *   workspace: device, workspace_bytes >= gemm_epilog_rms_norm_workspace_bytes(rows, d)
+ *              (else GE_ERR_SCRATCH), 16-byte aligned, used until the work is done.
+ */
+ge_status_t gemm_epilog_rms_norm_backward(int64_t rows, int64_t d, ge_dtype_t dt, const void* dy, int64_t lddy,
+                                          const void* s, int64_t lds, const void* weight, ge_dtype_t wdt, float eps,
+                                          const void* dresidual, int64_t lddr, void* dx, int64_t lddx, void* dweight,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

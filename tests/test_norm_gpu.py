@@ -1,0 +1,187 @@
+"""The norm and its gradient on the GPU against the 64-bit reference.
+
+Bounds. The sum of squares of d values in fp32: relative error at most (log2 d + 8) 2^-24 of
+a sum of positive terms added in a tree of short runs (64 lanes, at most 32 terms each);
+through the square root half of that, then four more roundings. So |y - want| is at most
+40 2^-24 |want|, and the store's half ulp. The gradient's inner sum has terms of both signs:
+its error is 40 2^-24 of the sum of their magnitudes. dweight adds `rows` terms in fp32."""
+import numpy as np
+import pytest
+import torch
+
+from gemm_epilogues_epilog_amd import mx, norm
+from tests import mx_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+T = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+TINY = {"f32": 2.0 ** -149, "bf16": 2.0 ** -133, "f16": 2.0 ** -25}
+U = 40 * 2.0 ** -24
+SHAPES = [(1, 1), (1, 7), (3, 64), (5, 511), (4, 512), (9, 1024), (333, 1100), (33, 1101), (40, 4096), (2, 8200),
+          (3, 16384), (1, 32768), (2, 32767)]
+
+
+def data(rows, d, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    make = lambda *s: torch.randn(*s, generator=g).to(T[dtype])   # noqa: E731
+    return make(rows, d) * 2, make(rows, d), (1 + 0.3 * torch.randn(d, generator=g)), make(rows, d)
+
+
+def close(got, want, err, dtype, where=""):
+    e = np.abs(got.double().cpu().numpy() - want)
+    b = err * (1 + HALF[dtype]) + HALF[dtype] * np.abs(want) + TINY[dtype]
+    assert (e <= b).all(), (where, float((e / b).max()))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,d", SHAPES)
+def test_forward(gpu, rows, d, dtype):
+    x, res, w, _ = data(rows, d, dtype, rows + d)
+    for wt in {dtype, "f32"}:
+        wd = w.to(T[wt])
+        s = (x.float() + res.float()).to(T[dtype])
+        want = ref.rms_norm(s.double().numpy(), wd.double().numpy(), 1e-5)
+        y, got_s = norm.rms_norm(x.cuda(), wd.cuda(), res.cuda(), eps=1e-5)
+        assert torch.equal(got_s.cpu(), s)
+        close(y, want, U * np.abs(want), dtype, wt)
+        xc = x.cuda()
+        y2, same = norm.rms_norm(xc, wd.cuda(), eps=1e-5)
+        assert same is xc
+        close(y2, ref.rms_norm(x.double().numpy(), wd.double().numpy(), 1e-5),
+              U * np.abs(ref.rms_norm(x.double().numpy(), wd.double().numpy(), 1e-5)), dtype, wt)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,d", SHAPES)
+def test_forward_in_8_bits(gpu, rows, d, dtype):
+    """q is y in 32 bits, quantised. From fp32 rows the same kernel gives that y itself, so
+    the codes have to be equal; from 16-bit rows y comes back rounded, and the values are held
+    to an element's spacing around the 64-bit result."""
+    x, res, w, _ = data(rows, d, dtype, rows + d)
+    q = mx.MXTensor.empty(rows, d, "mxfp8")
+    q.codes.fill_(0xA5)
+    q.scales.fill_(0xA5)
+    y, q, s = norm.rms_norm(x.cuda(), w.cuda(), res.cuda(), out="both", mx_out=q)
+    c, sc = ref.unpack(q.codes.cpu().numpy(), q.scales.cpu().numpy(), rows, ref.pad(d, 256), "mxfp8")
+    assert (c[:, d:] == 0).all() and (sc[:, -(-d // 32):] == 0).all()
+    c, sc = c[:, :d], sc[:, : -(-d // 32)]
+    if dtype == "f32":
+        wc, ws = ref.quantize(y.cpu().double().numpy(), "mxfp8")
+        assert np.array_equal(c, wc) and np.array_equal(sc, ws)
+    want = ref.rms_norm(s.cpu().double().numpy(), w.double().numpy(), 1e-6)
+    top = np.repeat(np.exp2(sc.astype(float) - 127), 32, axis=1)[:, :d]
+    # half a step of an element (1/16 of it, or half the smallest), and 448 of up to 512 at the top
+    assert (np.abs(ref.values(c, sc, "mxfp8") - want) <= np.maximum(np.abs(want) / 8, top * 2.0 ** -10) * (1 + U)).all()
+    q2, s2 = norm.rms_norm(x.cuda(), w.cuda(), res.cuda(), out="mxfp8")
+    c2, sc2 = ref.unpack(q2.codes.cpu().numpy(), q2.scales.cpu().numpy(), rows, d, "mxfp8")
+    assert np.array_equal(c2, c) and np.array_equal(sc2, sc) and torch.equal(s2, s)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,d", SHAPES + [(1500, 520), (600, 4096)])
+def test_backward(gpu, rows, d, dtype):
+    s, dres, w, dy = data(rows, d, dtype, rows * 3 + d)
+    for wt, dr in ((dtype, None), ("f32", dres)):
+        wd = w.to(T[wt])
+        S, W, DY = s.double().numpy(), wd.double().numpy(), dy.double().numpy()
+        dx, dw = norm.rms_norm_backward(dy.cuda(), s.cuda(), wd.cuda(), None if dr is None else dr.cuda(), eps=1e-5)
+        want_dx, want_dw = ref.rms_norm_backward(DY, S, W, 1e-5, None if dr is None else dr.double().numpy())
+        r = 1 / np.sqrt(np.mean(S * S, axis=1, keepdims=True) + 1e-5)
+        g, h = np.abs(DY * W), np.abs(S * r)
+        err = 2 * U * r * (g + h * np.mean(g * h, axis=1, keepdims=True)) + (
+            0 if dr is None else 2.0 ** -24 * np.abs(dr.double().numpy()))
+        close(dx, want_dx, err, dtype, (wt, "dx"))
+        mags = np.sum(np.abs(DY) * h, axis=0)
+        close(dw, want_dw, (U + rows * 2.0 ** -24) * mags, wt, (wt, "dw"))
+        again = norm.rms_norm_backward(dy.cuda(), s.cuda(), wd.cuda(), None if dr is None else dr.cuda(), eps=1e-5)
+        assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
+def test_strides_and_in_place(gpu):
+    for d in (64, 1101):
+        x, res, w, dy = data(37, d, "bf16", d)
+        wide = torch.full((37, d + 5), 3.0, dtype=torch.bfloat16, device="cuda")
+        wide[:, 2:d + 2] = x.cuda()
+        y0, s0 = norm.rms_norm(x.cuda(), w.cuda(), res.cuda())
+        r = res.cuda()
+        y1, s1 = norm.rms_norm(wide[:, 2:d + 2], w.cuda(), r, sum_out=r)
+        assert s1 is r and torch.equal(y0, y1) and torch.equal(s0, r)
+        v = wide[:, 2:d + 2]
+        y2, s2 = norm.rms_norm(v, w.cuda(), res.cuda(), sum_out=v)
+        assert torch.equal(y2, y0) and torch.equal(v, s0) and (wide[:, :2] == 3).all() and (wide[:, d + 2:] == 3).all()
+        row = x.cuda()[:1].expand(37, d)   # one row for all
+        y3, _ = norm.rms_norm(row, w.cuda(), res.cuda())
+        y4, _ = norm.rms_norm(row.contiguous(), w.cuda(), res.cuda())
+        assert torch.equal(y3, y4)
+        dx0, dw0 = norm.rms_norm_backward(dy.cuda(), s0, w.cuda(), res.cuda())
+        g = dy.cuda()
+        dx1, dw1 = norm.rms_norm_backward(g, v, w.cuda(), res.cuda(), dx_out=g)
+        assert dx1 is g and torch.equal(dx0, g) and torch.equal(dw0, dw1)
+
+
+def test_no_rows(gpu):
+    x, w = torch.empty(0, 64, device="cuda"), torch.ones(64, device="cuda")
+    y, s = norm.rms_norm(x, w)
+    q, _ = norm.rms_norm(x, w, out="mxfp8")
+    assert y.shape == (0, 64) and q.shape == (0, 64)
+    dx, dw = norm.rms_norm_backward(x, x, w)
+    assert dx.shape == (0, 64) and (dw == 0).all()
+
+
+def test_special_rows(gpu):
+    x = torch.ones(5, 96)
+    x[1] = 0
+    x[2, 3] = float("nan")
+    x[3, 4] = float("inf")
+    w = torch.ones(96, device="cuda")
+    y, q, _ = norm.rms_norm(x.cuda(), w, out="both", eps=0.0)
+    y, v = y.cpu(), mx.mx_dequantize(q, "f32").cpu()
+    assert (y[0] == 1).all() and (y[4] == 1).all() and (v[0] == 1).all() and (v[4] == 1).all()
+    # a zero row without eps is 0 / 0; a row with a NaN is NaN; inf / inf is NaN and 1 / inf 0
+    assert torch.isnan(y[1]).all() and torch.isnan(y[2]).all()
+    assert torch.isnan(y[3, 4]) and (torch.cat((y[3, :4], y[3, 5:])) == 0).all()
+    assert torch.isnan(v[1]).all() and torch.isnan(v[2]).all() and torch.isnan(v[3, :32]).all() and (v[3, 32:] == 0).all()
+    y, _ = norm.rms_norm(x.cuda(), w, eps=1e-6)
+    assert (y[1] == 0).all()
+
+
+def test_streams_and_graph(gpu):
+    x, res, w, dy = (t.cuda() for t in data(50, 4096, "bf16", 3))
+    y, q, s = norm.rms_norm(x, w, res, out="both")
+    dx, dw = norm.rms_norm_backward(dy, s, w, res)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    y2, q2, s2 = norm.rms_norm(x, w, res, out="both", stream=st)
+    dx2, dw2 = norm.rms_norm_backward(dy, s2, w, res, stream=st)
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in ((y, y2), (s, s2), (dx, dx2), (dw, dw2)))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y3, q3, s3 = norm.rms_norm(x, w, res, out="both")
+        dx3, dw3 = norm.rms_norm_backward(dy, s3, w, res)
+    for _ in range(4):
+        for t in (y3, s3, dx3, dw3):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in ((y, y3), (s, s3), (dx, dx3), (dw, dw3)))
+        assert torch.equal(mx.mx_dequantize(q3), mx.mx_dequantize(q))
+
+
+def test_binding_refusals(gpu):
+    x, w = torch.ones(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    h = x.half()
+    for kw in (dict(residual=h), dict(residual=x[:2]), dict(residual=x.cpu()), dict(out="f16"), dict(sum_out=x),
+               dict(mx_out=mx.MXTensor.empty(4, 64, "mxfp8")), dict(out="mxfp8", y_out=x),
+               dict(residual=x, sum_out=x[:1].expand(4, 64)),
+               dict(out="mxfp8", mx_out=mx.MXTensor.empty(4, 64, "mxfp4"))):
+        with pytest.raises(ValueError):
+            norm.rms_norm(x, w, **kw)
+    for args in ((x.t(), w), (x, w[:8]), (x, w.half()), (x[0], w), (x.double(), w)):
+        with pytest.raises(ValueError):
+            norm.rms_norm(*args)
+    for args in ((h, x, w), (x[:2], x, w), (x, x, w.double()), (x, x, w, h)):
+        with pytest.raises(ValueError):
+            norm.rms_norm_backward(*args)
