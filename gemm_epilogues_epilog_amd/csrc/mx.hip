@@ -2,6 +2,7 @@
 // mx_host.cpp).
 #include <hip/hip_runtime.h>
 
+#include <cstdlib>
 #include <cstring>
 #include <new>
 
@@ -20,12 +21,12 @@ struct ge_mx_plan {
 
 namespace {
 
-template <int XF>
+template <int XF, bool EXACT>
 const void* kernel_of(int cfg) {
   using namespace gek;
   switch (cfg) {
-    case MX_L: return reinterpret_cast<const void*>(&mx_tile_kernel<XF, MX_L>);
-    case MX_M: return reinterpret_cast<const void*>(&mx_tile_kernel<XF, MX_M>);
+    case MX_L: return reinterpret_cast<const void*>(&mx_tile_kernel<XF, MX_L, EXACT>);
+    case MX_M: return reinterpret_cast<const void*>(&mx_tile_kernel<XF, MX_M, EXACT>);
     case MX_S64: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 4>);
     case MX_S32: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 2>);
     case MX_S16: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 1>);
@@ -132,7 +133,10 @@ ge_status_t gemm_epilog_mx_execute(ge_mx_handle_t h, int64_t m, const void* x_co
   a.vec = (int32_t)h->t.vec;
   a.group_m = L.group_m;
   if (L.grid_x > 0x7fffffff || L.grid_y > 65535) return GE_ERR_NOT_SUPPORTED;
-  const void* fn = h->t.x == GE_MXFP4 ? kernel_of<gemx::FP4>(L.cfg) : kernel_of<gemx::FP8>(L.cfg);
+  const bool exact = h->t.d == GE_MX_D_F32 || (h->t.d == GE_MX_D_MXFP8 && !getenv("GE_MX_FAST"));
+  const void* fn = h->t.x == GE_MXFP4 ? kernel_of<gemx::FP4, false>(L.cfg)
+                   : exact            ? kernel_of<gemx::FP8, true>(L.cfg)
+                                      : kernel_of<gemx::FP8, false>(L.cfg);
   void* params[] = {&a};
   return hipLaunchKernel(fn, dim3((unsigned)L.grid_x, (unsigned)L.grid_y),
                          dim3((unsigned)gemx::mx_waves(gemx::kMxTiles[L.cfg]) * 64), params, 0,
