@@ -68,7 +68,7 @@ class ge_mx_types_t(ctypes.Structure):
 
 class ge_mx_plan_info_t(ctypes.Structure):
     _fields_ = [("tile_m", ctypes.c_int), ("tile_n", ctypes.c_int), ("waves", ctypes.c_int), ("stages", ctypes.c_int),
-                ("splits", ctypes.c_int), ("workgroups", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t)]
+                ("splits", ctypes.c_int), ("tiles", ctypes.c_int64), ("workgroups", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t)]
 
 
 class GemmEpilogError(RuntimeError):

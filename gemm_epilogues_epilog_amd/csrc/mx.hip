@@ -94,6 +94,7 @@ ge_status_t gemm_epilog_mx_plan_info(int64_t n, int64_t k, int64_t experts, ge_m
   info->waves = gemx::mx_waves(T);
   info->stages = T.stages;
   info->splits = L.splits;
+  info->tiles = m ? (int64_t)L.tiles_m * L.tiles_n : 0;
   info->workgroups = m ? L.grid_x * L.grid_y : 0;
   info->workspace_bytes = gemxh::workspace_bytes(n, k, experts, types, compute_units);
   return GE_OK;

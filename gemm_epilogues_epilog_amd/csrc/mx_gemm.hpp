@@ -45,21 +45,29 @@ struct MxArgs {
 // A value that is the same in every lane, in a scalar register.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// Copies of the tile kernels: 16 (4) bytes per lane from srd.base + voff + soff (uniform)
-// to LDS bytes lds + 16 (4) lane; see copy_to_lds_b128 for the ordering rules.
-__device__ __forceinline__ void copy_to_lds_b128_at(const i32x4& srd, uint32_t voff, int soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+// Copies of the tile kernels: KB number PC of a row group's stage (lane l moves 16 bytes at
+// 16 l of it), or its 256 bytes of scales, from srd.base + soff (uniform) on to LDS bytes
+// `lds` on. An instruction's offset moves both its source and its LDS address. See
+// copy_to_lds_b128 for the ordering rules.
+template <int PC>
+__device__ __forceinline__ void copy_kb_to_lds(const i32x4& srd, uint32_t lane16, int soff, uint32_t lds) {
+  static_assert(PC >= 0 && PC < 4, "12-bit offsets");
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen offset:%4 lds"
                :
-               : "v"(voff), "s"(srd), "s"(__builtin_amdgcn_readfirstlane(soff)),
-                 "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "v"(lane16), "s"(srd), "s"(soff), "s"(uniform(lds)), "n"(PC * 1024)
                : "memory", "m0");
 }
-__device__ __forceinline__ void copy_to_lds_b32_at(const i32x4& srd, uint32_t voff, int soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
-               :
-               : "v"(voff), "s"(srd), "s"(__builtin_amdgcn_readfirstlane(soff)),
-                 "s"(__builtin_amdgcn_readfirstlane(lds))
-               : "memory", "m0");
+// The scales of four row groups (256 bytes each, 16 lanes each) in one copy, by the waves with
+// `on` set: the branch is inside the assembly, where the compiler cannot move products
+// around it. Copies cost by the instruction here, whatever their size: one copy per row group
+// took 6% of the whole product.
+__device__ __forceinline__ void copy_scales_to_lds(const i32x4& srd, uint32_t voff, uint32_t lds, int on) {
+  asm volatile(
+      "s_cmp_eq_u32 %3, 0\n\ts_cbranch_scc1 .Lno_scales_%=\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\t"
+      "buffer_load_dwordx4 %0, %1, 0 offen lds\n.Lno_scales_%=:"
+      :
+      : "v"(voff), "s"(srd), "s"(uniform(lds)), "s"(uniform(on))
+      : "memory", "m0", "scc");
 }
 
 // act(v) by the run-time epilogue code (uniform).
@@ -77,7 +85,6 @@ __device__ __forceinline__ void mx_act_n(float (&v)[N], int ep) {
     for (int i = 0; i < N; ++i) v[i] = gelu_tanh(v[i]);
   }
 }
-__device__ __forceinline__ void mx_act16(float (&v)[16], int ep) { mx_act_n(v, ep); }
 
 // The rows [lo, hi) of expert e; offsets that fall outside 0 .. m or run backwards are
 // held to an empty or valid range, so no row outside X or D is touched.
@@ -133,29 +140,6 @@ __device__ __forceinline__ float mx_bias(const MxArgs& p, int e, int c) {
   return p.ep != NONE && c < p.n ? load_vec(p.bias, p.vec, (int64_t)e * p.n + c) : 0.0f;
 }
 
-// 32 rows x 64 columns of sums from a wave's scratch (rows of ROW floats) to D: lane l takes
-// columns 8 (l % 8) .. + 7 of every eighth row. `bias`, `c`: of the lane's first column.
-template <int ROW>
-__device__ __forceinline__ void mx_store_rows(const MxArgs& p, const float* scratch, const float* bias, int64_t r0,
-                                              int64_t lo, int64_t hi, int c, int lane, bool vec_ok) {
-  const f32x4 b0 = *reinterpret_cast<const f32x4*>(bias), b1 = *reinterpret_cast<const f32x4*>(bias + 4);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = i * 8 + (lane >> 3);
-    const float* q = scratch + r * ROW + (lane & 7) * 8;
-    const f32x4 t0 = *reinterpret_cast<const f32x4*>(q), t1 = *reinterpret_cast<const f32x4*>(q + 4);
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = t0[e] + b0[e];
-      v[4 + e] = t1[e] + b1[e];
-    }
-    mx_act_n(v, p.ep);
-    const int64_t row = r0 + r;
-    if (row >= lo && row < hi) mx_store8(p, row, c, v, vec_ok);
-  }
-}
-
 // ---- tile kernel -------------------------------------------------------------------
 // One workgroup computes bm x bn of D over its part of k. Copies go straight to LDS;
 // all waves run the lockstep schedule: at the end of a k-tile every wave waits for its own
@@ -168,6 +152,7 @@ struct MxCfgT {
   static_assert(STAGES == 2, "the main loop runs on two stages");
   static constexpr int WAVES_M = T.bm / 32 / MB, WAVES_N = T.bn / 32 / NB, NW = WAVES_M * WAVES_N;
   static constexpr bool SPLIT = CFG == MX_M;               // may share a tile's k loop
+  static constexpr bool ACC_AGPR = MB * NB * 16 > 128;     // one wave per SIMD, sums in the accumulation registers
   static constexpr int BK = mx_bk(XF), KS = BK / 64;
   static constexpr int WRB = BK / 32 * 512;                // bytes of a W row group per stage
   static constexpr int XRB = BK / chunk_values(XF) * 512;  // and of an X row group (4096)
@@ -175,15 +160,21 @@ struct MxCfgT {
   static constexpr int SW_BYTES = T.bn / 32 * kScaleGranule, SX_BYTES = T.bm / 32 * kScaleGranule;
   static constexpr int OFF_X = W_BYTES, OFF_SW = OFF_X + X_BYTES, OFF_SX = OFF_SW + SW_BYTES;
   static constexpr int STAGE = OFF_SX + SX_BYTES;
-  static constexpr int PW = W_BYTES / 1024, PX = X_BYTES / 1024, PS = (T.bn + T.bm) / 32;   // copies per stage
-  static constexpr int IW = (PW + NW - 1) / NW, IX = (PX + NW - 1) / NW, IS = (PS + NW - 1) / NW;   // and per wave
-  static constexpr int INST = IW + IX + IS;
-  static constexpr int EPI_ROW = 68;                       // floats per scratch row: 64 and a pad
-  static constexpr int EPI = (32 * EPI_ROW + NB * 32) * 4;   // scratch bytes per wave: rows and bias
-  static constexpr int LDS = STAGES * STAGE > NW * EPI ? STAGES * STAGE : NW * EPI;
+  static constexpr int CW = NW;                            // waves that copy
+  static constexpr int GW = T.bn / 32 / CW, GX = T.bm / 32 / CW;   // row groups of W and X per copying wave
+  static constexpr int SWW = T.bn / 128, SWV = SWW + T.bm / 128;   // waves that copy W's scales, any scales
+  static constexpr int INST = GW * (WRB / 1024) + GX * (XRB / 1024) + 1;   // a wave's copies per stage
+  // A copy after every STRIDE-th product from a k-tile's last step on: apart, so that the
+  // waves do not queue for the memory pipe, but early enough to land before the next
+  // barrier (8192^3: e2m1 X 170 -> 161 us at 2 on zeros, e4m3 X 272 -> 310).
+  static constexpr int STRIDE = XF == FP4 && MB * NB >= 8 ? 2 : 1;
+  static constexpr int EPI = 32 * 32 * 2 + NB * 32 * 4;    // epilogue LDS per wave: 32 rows of 64 bytes, and bias
+  static constexpr int OFF_EPI = STAGES * STAGE;
+  static constexpr int LDS = OFF_EPI + NW * EPI;
   static constexpr int XR = XF == FP8 ? 2 : 1;             // 16-byte reads per X fragment
   static_assert(LDS <= 160 * 1024, "LDS");
-  static_assert(NB % 2 == 0, "the epilogue takes two feature blocks at a time");
+  static_assert(T.bn / 32 % CW == 0 && T.bm / 32 % CW == 0, "row groups per copying wave");
+  static_assert(NB % 2 == 0, "bias values per lane");
 };
 
 template <int XF, int MB, int NB>
@@ -290,77 +281,276 @@ __device__ __forceinline__ i32x4 large_part(i32x4 x) {
   return r;
 }
 
+// f(0), f(1), .. f(N - 1) with constant arguments.
+template <int N, int I = 0, class Fn>
+__device__ __forceinline__ void static_for(Fn&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<N, I + 1>(f);
+  }
+}
+
+// ---- split k: the part that arrives last adds all parts in order and finishes --------
+// Sums cross XCDs, whose L2 caches are not coherent: device-scope (sc1) accesses go to the
+// memory side. A part's stores have completed before it counts itself; nobody waits, so
+// no order of the workgroups can hang. Returns whether this workgroup finishes the tile.
+template <class C>
+__device__ __forceinline__ bool mx_join_parts(const MxArgs& p, const MxPlace& at, int part, int w, int lane,
+                                              f32x16 (&acc)[C::NB][C::MB], int* flag) {
+  constexpr int NB = C::NB, MB = C::MB;
+  constexpr int kDev = 16;
+  constexpr int PART = C::NW * NB * MB * 16 * 64 * 4;
+  const int tile_id = (int)(at.row0 / C::T.bm) * p.tiles_n + at.tn;
+  char* slots = reinterpret_cast<char*>(p.partial) + (int64_t)tile_id * p.splits * PART;
+  {
+    const __amdgpu_buffer_rsrc_t r = rsrc(slots + (int64_t)part * PART);
+#pragma unroll
+    for (int a = 0; a < NB; ++a)
+#pragma unroll
+      for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const i32x4 v = {__float_as_int(acc[a][b][4 * g]), __float_as_int(acc[a][b][4 * g + 1]),
+                           __float_as_int(acc[a][b][4 * g + 2]), __float_as_int(acc[a][b][4 * g + 3])};
+          __builtin_amdgcn_raw_buffer_store_b128(v, r, (((w * NB + a) * MB + b) * 4 + g) * 1024 + lane * 16, 0, kDev);
+        }
+  }
+  wait_vmcnt<0>();
+  __syncthreads();
+  int* shared = flag - w * (C::EPI / 4);   // wave 0's scratch
+  if (threadIdx.x == 0)
+    *shared = __hip_atomic_fetch_add(p.counter + tile_id, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+              (uint32_t)p.splits - 1u;
+  __syncthreads();
+  if (!uniform(*shared)) return false;
+  __syncthreads();
+  if (threadIdx.x == 0) __hip_atomic_store(p.counter + tile_id, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int q = 0; q < p.splits; ++q) {
+    const __amdgpu_buffer_rsrc_t r = rsrc(slots + (int64_t)q * PART);
+#pragma unroll
+    for (int a = 0; a < NB; ++a)
+#pragma unroll
+      for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const i32x4 v = __builtin_amdgcn_raw_buffer_load_b128(
+              r, (((w * NB + a) * MB + b) * 4 + g) * 1024 + lane * 16, 0, kDev);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float f = __int_as_float(v[e]);
+            acc[a][b][4 * g + e] = q == 0 ? f : acc[a][b][4 * g + e] + f;
+          }
+        }
+  }
+  return true;
+}
+
+// ---- epilogue of a wave: 32 MB rows x 32 NB columns of sums to D -----------------------
+// A lane holds, of one row, columns 8 g + 4 (l / 32) + 0 .. 3 of each 32-column block.
+template <class C>
+__device__ __forceinline__ void mx_epilogue(const MxArgs& p, const MxPlace& at, int wm, int c0w, int lane,
+                                            const f32x16 (&acc)[C::NB][C::MB], const float* bias, char* scratch) {
+  constexpr int NB = C::NB, MB = C::MB;
+  const int lrow = lane & 31, lhi = lane >> 5;
+  const int out = p.out;
+  const bool vec_ok = mx_vec_ok(p);
+  const int cpad = out == MX_OUT_FP8 ? (int)pad_to(p.n, kKPad) : p.n;
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    const int64_t r0 = at.row0 + (wm * MB + b) * 32;
+    const int64_t row = r0 + lrow;
+    const bool keep = row >= at.lo && row < at.hi;
+#pragma unroll
+    for (int a = 0; a < NB; ++a) {
+      const int c = c0w + a * 32;
+      if (c >= cpad) break;
+      float v[16];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 bv = *reinterpret_cast<const f32x4*>(bias + a * 32 + 8 * g + 4 * lhi);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * g + e] = acc[a][b][4 * g + e] + bv[e];
+      }
+      mx_act_n(v, p.ep);
+      if (out == MX_OUT_FP8) {
+        // the other half-wave holds the rest of the block; two swaps of half-waves give
+        // each lane 16 consecutive codes, a chunk
+        if (c + 32 > p.n) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (c + 8 * (i / 4) + 4 * lhi + i % 4 >= p.n) v[i] = 0.0f;
+        }
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = amax2(m, mag(v[i]));
+        const uint32_t mu = __float_as_uint(m);
+        const auto sm = __builtin_amdgcn_permlane32_swap(mu, mu, false, false);
+        m = amax2(__uint_as_float(sm[0]), __uint_as_float(sm[1]));
+        const int s = scale_of(m, FP8);
+        uint32_t q[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) q[g] = to_fp8x4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3], s);
+        const auto s0 = __builtin_amdgcn_permlane32_swap(q[0], q[2], false, false);
+        const auto s1 = __builtin_amdgcn_permlane32_swap(q[1], q[3], false, false);
+        if (keep) {
+          mx_store_chunk(p, row, c + 16 * lhi, i32x4{(int)s0[0], (int)s0[1], (int)s1[0], (int)s1[1]});
+          if (lhi == 0) mx_store_scale(p, row, c, s);
+        }
+      } else if (out == MX_OUT_F32) {
+        // 16 bytes a lane; the line of a row's 32 columns fills over four stores
+        if (keep) {
+          float* d = static_cast<float*>(p.D) + row * p.n + c + 4 * lhi;
+          if (vec_ok && c + 32 <= p.n) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              *reinterpret_cast<f32x4*>(d + 8 * g) = f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c + 8 * (i / 4) + 4 * lhi + i % 4 < p.n) d[8 * (i / 4) + i % 4] = v[i];
+          }
+        }
+      } else {
+        // 16-bit: the block's 32 rows of 64 bytes through scratch, so that a store
+        // instruction writes 64-byte row pieces. 8-byte unit u of row r sits at unit
+        // u ^ (r & 7): the 32 lanes of a write, and the 16-byte reads, spread over all banks.
+        i32x2* t = reinterpret_cast<i32x2*>(scratch) + lrow * 8;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const i32x2 u = out == MX_OUT_F16
+                              ? i32x2{(int)Tr<F16>::pack2(v[4 * g], v[4 * g + 1]), (int)Tr<F16>::pack2(v[4 * g + 2], v[4 * g + 3])}
+                              : i32x2{(int)Tr<BF16>::pack2(v[4 * g], v[4 * g + 1]), (int)Tr<BF16>::pack2(v[4 * g + 2], v[4 * g + 3])};
+          t[(2 * g + lhi) ^ (lrow & 7)] = u;
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = i * 16 + (lane >> 2), cc = c + (lane & 3) * 8;
+          const i32x2* q = reinterpret_cast<const i32x2*>(scratch) + r * 8;
+          const i32x2 lo = q[(2 * (lane & 3)) ^ (r & 7)], hi = q[(2 * (lane & 3) + 1) ^ (r & 7)];
+          const int64_t rw = r0 + r;
+          if (rw >= at.lo && rw < at.hi && cc < p.n) {
+            uint16_t* d = static_cast<uint16_t*>(p.D) + rw * p.n + cc;
+            if (vec_ok) {
+              *reinterpret_cast<i32x4*>(d) = i32x4{lo[0], lo[1], hi[0], hi[1]};
+            } else {
+              const int w4[4] = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (cc + e < p.n) d[e] = (uint16_t)((uint32_t)w4[e / 2] >> (16 * (e & 1)));
+            }
+          }
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+  }
+}
+
+// The copies of one wave into one stage, issued one at a time.
+template <class C>
+struct MxCopies {
+  i32x4 rw, rx, rs;
+  int off_w[C::GW], off_x[C::GX];
+  uint32_t lds_w, lds_x, lds_s;
+  uint32_t voff_s;
+
+  template <int J>
+  __device__ __forceinline__ void issue(uint32_t lane16, int scales) const {
+    constexpr int PW = C::WRB / 1024, PX = C::XRB / 1024;
+    constexpr int JX = J - C::GW * PW, JS = JX - C::GX * PX;
+    if constexpr (JX < 0) copy_kb_to_lds<J % PW>(rw, lane16, off_w[J / PW], lds_w + J / PW * C::WRB);
+    else if constexpr (JS < 0) copy_kb_to_lds<JX % PX>(rx, lane16, off_x[JX / PX], lds_x + JX / PX * C::XRB);
+    else copy_scales_to_lds(rs, voff_s, lds_s, scales);
+  }
+  template <int J0, int J1>
+  __device__ __forceinline__ void issue_range(uint32_t lane16, int scales) const {
+    if constexpr (J0 < J1) {
+      issue<J0>(lane16, scales);
+      issue_range<J0 + 1, J1>(lane16, scales);
+    }
+  }
+};
+
+// Sources of a tile's copies: base addresses of its first row groups at its first k-tile, and
+// this wave's row groups. Row groups past the operand's last one are read from the last
+// one instead (their results are dropped), so every address is in range.
+template <class C>
+struct MxSrc {
+  const char *wc, *xc, *sc;   // sc: scales of W (the first SWW waves) or X
+  int off_w[C::GW], off_x[C::GX];
+  uint32_t voff_s;            // of the lane's scales
+  int KT;                     // k-tiles to copy; 0 for no tile
+
+  __device__ __forceinline__ void set(const MxArgs& p, const MxPlace& at, int XF, int w, int lane, int kb, int nt) {
+    const int64_t gw = group_code_bytes(FP4, p.k), gx = group_code_bytes(XF, p.k), gs = group_scale_bytes(p.k);
+    const int64_t wrg = row_groups(p.n), xrg = row_groups(p.m);
+    // a tile that only pads an 8-bit result reads W's last row group
+    const int wg0 = (int)min((int64_t)at.tn * (C::T.bn / 32), wrg - 1);
+    const int64_t xg0 = at.row0 / 32;
+    const int wg_last = (int)(wrg - 1 - wg0);
+    const int xg_last = (int)min((int64_t)C::T.bm / 32, xrg - 1 - xg0);
+    wc = p.wc + (at.e * wrg + wg0) * gw + (int64_t)kb * C::WRB;
+    xc = p.xc + xg0 * gx + (int64_t)kb * C::XRB;
+#pragma unroll
+    for (int j = 0; j < C::GW; ++j) off_w[j] = uniform((int)(min(w * C::GW + j, wg_last) * gw));
+#pragma unroll
+    for (int j = 0; j < C::GX; ++j) off_x[j] = uniform((int)(min(w * C::GX + j, xg_last) * gx));
+    // wave w copies the scales of row groups 4 w .. 4 w + 3 of [W's, X's]
+    const bool of_w = w < C::SWW;
+    sc = of_w ? p.ws + (at.e * wrg + wg0) * gs : p.xs + xg0 * gs;
+    const int g = (of_w ? 4 * w : 4 * (w - C::SWW)) + (lane >> 4);
+    voff_s = (uint32_t)(min(g, of_w ? wg_last : xg_last) * gs) + (lane & 15) * 16;
+    KT = nt;
+  }
+  // The copies of k-tile kt into the stage at LDS byte `dst`. K-tiles past the last one fill
+  // it with zeros (an empty range: no memory traffic, and zero codes with zero scales add
+  // nothing), so the loop has no branches and always runs over pairs of k-tiles.
+  __device__ __forceinline__ MxCopies<C> at(int kt, int kb, int w, uint32_t dst) const {
+    MxCopies<C> c;
+    const uint32_t range = kt < KT ? 0x7fffffffu : 0u;
+    c.rw = make_srd(wc + (int64_t)kt * C::WRB, range);
+    c.rx = make_srd(xc + (int64_t)kt * C::XRB, range);
+    c.rs = make_srd(sc + (int64_t)((kb + kt) * C::BK / kKPad) * kScaleGranule, range);
+#pragma unroll
+    for (int j = 0; j < C::GW; ++j) c.off_w[j] = off_w[j];
+#pragma unroll
+    for (int j = 0; j < C::GX; ++j) c.off_x[j] = off_x[j];
+    c.lds_w = uniform(dst + w * C::GW * C::WRB);
+    c.lds_x = uniform(dst + C::OFF_X + w * C::GX * C::XRB);
+    c.voff_s = voff_s;
+    c.lds_s = uniform(dst + C::OFF_SW + w * 1024);
+    return c;
+  }
+};
+
+// Persistent: gridDim.x workgroups walk the tile order with that stride, and the k loop runs
+// on from one tile into the next: during a tile's last two k-tiles the copies fetch the
+// next tile's first two, so its latency hides behind this tile's end and its epilogue, and
+// the stores of D drain while the next tile computes. The epilogue has LDS of its own.
 template <int XF, int CFG, bool EXACT>
-__global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), 1) void mx_tile_kernel(MxArgs p) {
+__global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), (MxCfgT<XF, CFG>::ACC_AGPR ? 1 : 2)) void mx_tile_kernel(MxArgs p) {
   using C = MxCfgT<XF, CFG>;
   constexpr int MB = C::MB, NB = C::NB, KS = C::KS;
   constexpr int BM = C::T.bm, BN = C::T.bn;
   __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
-  __shared__ int last_part;
 
-  const int part = blockIdx.x % p.splits, id = blockIdx.x / p.splits;
+  const int part = C::SPLIT ? (int)blockIdx.x % p.splits : 0;
+  int id = C::SPLIT ? (int)blockIdx.x / p.splits : (int)blockIdx.x;
   MxPlace at;
   if (!mx_place<BM>(p, id, at)) return;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w % C::WAVES_M, wn = w / C::WAVES_M;
   const uint32_t lds = (uint32_t)(uintptr_t)(mx_lds_void*)smem;
-
-  // ---- copies ----
-  // Row groups past the operand's last one are read from the last one instead (their
-  // results are dropped), so every address is in range.
-  const int64_t gw = group_code_bytes(FP4, p.k), gx = group_code_bytes(XF, p.k), gs = group_scale_bytes(p.k);
-  const int64_t wrg = row_groups(p.n), xrg = row_groups(p.m);
-  const int wg0 = at.tn * (BN / 32);
-  const int64_t xg0 = at.row0 / 32;
-  const int wg_last = (int)(wrg - 1 - wg0);   // negative when the tile only pads an 8-bit result
-  const int xg_last = (int)min((int64_t)BM / 32, xrg - 1 - xg0);
+  const uint32_t lane16 = lane * 16;
   const int KTA = (int)(pad_to(p.k, kKPad) / C::BK);
-  const int kb = (int)((int64_t)KTA * part / p.splits), KT = (int)((int64_t)KTA * (part + 1) / p.splits) - kb;
-  const char* wc = p.wc + (at.e * wrg + wg0) * gw + (int64_t)kb * C::WRB;
-  const char* xc = p.xc + xg0 * gx + (int64_t)kb * C::XRB;
-  const char* ws = p.ws + (at.e * wrg + wg0) * gs;
-  const char* xs = p.xs + xg0 * gs;
-  int off_w[C::IW], off_x[C::IX], off_s[C::IS];
-#pragma unroll
-  for (int j = 0; j < C::IW; ++j) {
-    const int i = min(w * C::IW + j, C::PW - 1);
-    off_w[j] = uniform((int)(min(i / (C::WRB / 1024), wg_last) * gw) + (i % (C::WRB / 1024)) * 1024);
-  }
-#pragma unroll
-  for (int j = 0; j < C::IX; ++j) {
-    const int i = min(w * C::IX + j, C::PX - 1);
-    off_x[j] = uniform((int)(min(i / (C::XRB / 1024), xg_last) * gx) + (i % (C::XRB / 1024)) * 1024);
-  }
-#pragma unroll
-  for (int j = 0; j < C::IS; ++j) {
-    const int i = min(w * C::IS + j, C::PS - 1);
-    off_s[j] = uniform((int)((i < BN / 32 ? min(i, wg_last) : min(i - BN / 32, xg_last)) * gs));
-  }
-  const uint32_t lane16 = lane * 16, lane4 = lane * 4;
-  // k-tiles past the last one fill the stage with zeros (an empty range: no memory traffic,
-  // and zero codes with zero scales add nothing), so the loop has no branches and always
-  // runs over pairs of k-tiles.
-  auto issue = [&](int kt, int stage) {
-    const uint32_t dst = lds + stage * C::STAGE;
-    const uint32_t range = kt < KT ? 0x7fffffffu : 0u;
-    const i32x4 rw = make_srd(wc + (int64_t)kt * C::WRB, range);
-    const i32x4 rx = make_srd(xc + (int64_t)kt * C::XRB, range);
-    const int64_t so = (int64_t)((kb + kt) * C::BK / kKPad) * kScaleGranule;
-    const i32x4 rsw = make_srd(ws + so, range), rsx = make_srd(xs + so, range);
-#pragma unroll
-    for (int j = 0; j < C::IW; ++j)
-      copy_to_lds_b128_at(rw, lane16, off_w[j], dst + min(w * C::IW + j, C::PW - 1) * 1024);
-#pragma unroll
-    for (int j = 0; j < C::IX; ++j)
-      copy_to_lds_b128_at(rx, lane16, off_x[j], dst + C::OFF_X + min(w * C::IX + j, C::PX - 1) * 1024);
-#pragma unroll
-    for (int j = 0; j < C::IS; ++j) {
-      const int i = min(w * C::IS + j, C::PS - 1);
-      const i32x4 rs = i < BN / 32 ? rsw : rsx;
-      copy_to_lds_b32_at(rs, lane4, off_s[j], dst + C::OFF_SW + i * kScaleGranule);
-    }
-  };
+  const int kb = C::SPLIT ? (int)((int64_t)KTA * part / p.splits) : 0;
+  const int KT = C::SPLIT ? (int)((int64_t)KTA * (part + 1) / p.splits) - kb : KTA;
+  const int KT2 = (KT + 1) & ~1;
+  MxSrc<C> src;
+  src.set(p, at, XF, w, lane, kb, KT);
+  const int scales = w < C::SWV;
 
   // ---- fragment reads ----
   using F = MxFrags<XF, MB, NB>;
@@ -380,7 +570,7 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), 1) void mx_tile_kernel(
   };
   int sw[NB], sx[MB];
   auto read_scales = [&](int u, int kt) {
-    const int sh = XF == FP8 ? (kt & 1) * 16 : 0;   // a 128-k stage uses half of the granule's bytes
+    const int sh = XF == FP8 ? ((kb + kt) & 1) * 16 : 0;   // a 128-k stage uses half of the granule's bytes
 #pragma unroll
     for (int a = 0; a < NB; ++a) sw[a] = *reinterpret_cast<const int*>(rd_sw + u * C::STAGE + a * kScaleGranule) >> sh;
 #pragma unroll
@@ -388,198 +578,118 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), 1) void mx_tile_kernel(
   };
 
   f32x16 acc[NB][MB];
+  F fr[2];
+  constexpr int NMMA = MB * NB;
+  static_assert(C::INST * C::STRIDE <= NMMA * KS, "copies of a stage between two barriers");
+  MxCopies<C> cp;   // the stage being filled
+  // k-tile kt (in stage u); then the copies go to k-tile `ckt` of `from`, one after each
+  // product, so that no wave waits for the memory pipe while its SIMD's matrix unit idles;
+  // the ones that do not fit into the last k-step follow in the next k-tile. Every k-tile
+  // reads one k-step ahead, the tile's last one too: a branch around those reads costs more.
+  auto tile = [&](auto u_tag, int kt, const MxSrc<C>& from, int ckt) {
+    constexpr int u = decltype(u_tag)::value;
+    auto step = [&](auto tag) {
+      constexpr int s = decltype(tag)::value;
+      constexpr bool last = s == KS - 1;
+      constexpr int PER = (PIECES + NMMA - 1) / NMMA;
+      constexpr int ru = last ? u ^ 1 : u, rs = last ? 0 : s + 1;
+      F& f = fr[s & 1];
+      i32x4 xl[MB][C::XR];
+      if constexpr (last) {
+        wait_lgkmcnt<0>();   // this wave's reads of stage u are done
+        wait_vmcnt<0>();     // and its copies of the next k-tile have landed
+        barrier_only();
+        cp = from.at(ckt, kb, w, lds + u * C::STAGE);
+      }
+      auto slot = [&](auto itag) {
+        constexpr int i = decltype(itag)::value;
+        constexpr int a = i % NB, b = i / NB;
+        if constexpr (EXACT) {
+          if constexpr (a == 0) {
 #pragma unroll
-  for (int a = 0; a < NB; ++a)
+            for (int h = 0; h < C::XR; ++h) {
+              xl[b][h] = large_part(f.x[b][h]);
 #pragma unroll
-    for (int b = 0; b < MB; ++b) acc[a][b] = f32x16{};
+              for (int e = 0; e < 4; ++e) f.x[b][h][e] ^= xl[b][h][e];
+            }
+          }
+          acc[a][b] = mx_mma<XF, s>(f.w[a], xl[b], acc[a][b], sw[a], sx[b]);
+        }
+        acc[a][b] = mx_mma<XF, s>(f.w[a], f.x[b], acc[a][b], sw[a], sx[b]);
+#pragma unroll
+        for (int e = 0; e < PER; ++e)
+          if (i * PER + e < PIECES) piece(ru, rs, i * PER + e, fr[(s & 1) ^ 1]);
+        constexpr int j = (last ? 0 : (s + 1) * NMMA) + i;
+        if constexpr (j % C::STRIDE == 0 && j / C::STRIDE < C::INST)
+          cp.template issue<j / C::STRIDE>(lane16, scales);
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      static_for<NMMA>(slot);
+      if constexpr (last) read_scales(ru, kt + 1);
+    };
+    static_for<KS>(step);
+  };
+  constexpr std::integral_constant<int, 0> u0{};
+  constexpr std::integral_constant<int, 1> u1{};
 
-  if (wg_last >= 0) {
-    // prologue: both stages in flight, stage 0 complete
-    issue(0, 0);
-    issue(1, 1);
-    wait_vmcnt<C::INST>();
-    barrier_only();
-    F fr[2];
+  // prologue: the first tile's first two k-tiles in flight, the first complete
+  // (of the second, the copies that a k-tile's last step issues)
+  constexpr int EARLY = (NMMA + C::STRIDE - 1) / C::STRIDE < C::INST ? (NMMA + C::STRIDE - 1) / C::STRIDE : C::INST;
+  cp = src.at(0, kb, w, lds);
+  cp.template issue_range<0, C::INST>(lane16, scales);
+  cp = src.at(1, kb, w, lds + C::STAGE);
+  cp.template issue_range<0, EARLY>(lane16, scales);
+  wait_vmcnt<EARLY - 1>();   // (a wave that copies no scales has one copy less in flight)
+  barrier_only();
+
+  float* bias = reinterpret_cast<float*>(smem + C::OFF_EPI + w * C::EPI);   // NB * 32 values
+  char* scratch = reinterpret_cast<char*>(bias + NB * 32);
+  for (;;) {
+    // this tile's bias, in the epilogue's LDS (its last reads are behind the barriers of
+    // the tile before)
+    const int c0w = at.tn * BN + wn * NB * 32;
+    float bv[NB / 2];
+#pragma unroll
+    for (int i = 0; i < NB / 2; ++i) bv[i] = mx_bias(p, at.e, c0w + i * 64 + lane);
+#pragma unroll
+    for (int a = 0; a < NB; ++a)
+#pragma unroll
+      for (int b = 0; b < MB; ++b) acc[a][b] = f32x16{};
 #pragma unroll
     for (int q = 0; q < PIECES; ++q) piece(0, 0, q, fr[0]);
-    read_scales(0, kb);
+    read_scales(0, 0);
 
-    // k-tile kt in stage u. The last one reads ahead too, from a stage that holds old values
-    // which nothing uses: one code path is worth more than the reads.
-    auto tile = [&](auto u_tag, int kt) {
-      constexpr int u = decltype(u_tag)::value;
-      auto step = [&](auto tag) {
-        constexpr int s = decltype(tag)::value;
-        constexpr bool last = s == KS - 1;
-        constexpr int NMMA = MB * NB, PER = (PIECES + NMMA - 1) / NMMA;
-        if constexpr (last) {
-          wait_lgkmcnt<0>();   // this wave's reads of stage u are done
-          wait_vmcnt<0>();     // and its copies of the next k-tile have landed
-          barrier_only();
-          issue(kt + 2, u);
-        }
-        constexpr int ru = last ? u ^ 1 : u, rs = last ? 0 : s + 1;
-        i32x4 xl[MB][C::XR];
+    for (int kt = 0; kt < KT2 - 2; kt += 2) {
+      tile(u0, kt, src, kt + 2);
+      tile(u1, kt + 1, src, kt + 3);
+    }
+    MxPlace next = at;
+    id += C::SPLIT ? (int)gridDim.x / p.splits : (int)gridDim.x;
+    const bool more = mx_place<BM>(p, id, next);
+    src.set(p, next, XF, w, lane, kb, more ? KT : 0);
+    tile(u0, KT2 - 2, src, 0);
+    tile(u1, KT2 - 1, src, 1);
+    // the sums exist here: without this the compiler moves the last products into the
+    // branches of the epilogue, next to their uses, and spills the fragments meanwhile
 #pragma unroll
-        for (int i = 0; i < NMMA; ++i) {
-          const int a = i % NB, b = i / NB;
-          F& f = fr[s & 1];
-          if constexpr (EXACT) {
-            if (a == 0) {
+    for (int a = 0; a < NB; ++a)
 #pragma unroll
-              for (int h = 0; h < C::XR; ++h) {
-                xl[b][h] = large_part(f.x[b][h]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) f.x[b][h][e] ^= xl[b][h][e];
-              }
-            }
-            acc[a][b] = mx_mma<XF, s>(f.w[a], xl[b], acc[a][b], sw[a], sx[b]);
-          }
-          acc[a][b] = mx_mma<XF, s>(f.w[a], f.x[b], acc[a][b], sw[a], sx[b]);
-#pragma unroll
-          for (int e = 0; e < PER; ++e)
-            if (i * PER + e < PIECES) piece(ru, rs, i * PER + e, fr[(s & 1) ^ 1]);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        if constexpr (last) read_scales(ru, kb + kt + 1);
-      };
-      step(std::integral_constant<int, 0>{});
-      step(std::integral_constant<int, 1>{});
-      if constexpr (KS == 4) {
-        step(std::integral_constant<int, 2>{});
-        step(std::integral_constant<int, 3>{});
+      for (int b = 0; b < MB; ++b) {
+        if constexpr (C::ACC_AGPR) asm volatile("" : "+a"(acc[a][b]));
+        else asm volatile("" : "+v"(acc[a][b]));
       }
-    };
-    constexpr std::integral_constant<int, 0> u0{};
-    constexpr std::integral_constant<int, 1> u1{};
-    for (int kt = 0; kt < KT; kt += 2) {
-      tile(u0, kt);
-      tile(u1, kt + 1);
-    }
-    wait_vmcnt<0>();
-  }
-  __syncthreads();   // every wave is done with the stages
 
-  // ---- split k: the part that arrives last adds all parts in order and finishes ----
-  if (C::SPLIT && p.splits > 1) {
-    constexpr int kDev = 16;   // device scope (sc1): past the XCD's own L2
-    constexpr int PART = C::NW * NB * MB * 16 * 64 * 4;
-    const int tile_id = (int)(at.row0 / BM) * p.tiles_n + at.tn;
-    char* slots = reinterpret_cast<char*>(p.partial) + (int64_t)tile_id * p.splits * PART;
-    {
-      const __amdgpu_buffer_rsrc_t r = rsrc(slots + (int64_t)part * PART);
-#pragma unroll
-      for (int a = 0; a < NB; ++a)
-#pragma unroll
-        for (int b = 0; b < MB; ++b)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const i32x4 v = {__float_as_int(acc[a][b][4 * g]), __float_as_int(acc[a][b][4 * g + 1]),
-                             __float_as_int(acc[a][b][4 * g + 2]), __float_as_int(acc[a][b][4 * g + 3])};
-            __builtin_amdgcn_raw_buffer_store_b128(v, r, (((w * NB + a) * MB + b) * 4 + g) * 1024 + lane * 16, 0, kDev);
-          }
+    if constexpr (C::SPLIT) {
+      if (p.splits > 1 && !mx_join_parts<C>(p, at, part, w, lane, acc, reinterpret_cast<int*>(scratch))) return;
     }
-    wait_vmcnt<0>();
-    __syncthreads();
-    if (threadIdx.x == 0)
-      last_part = __hip_atomic_fetch_add(p.counter + tile_id, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                  (uint32_t)p.splits - 1u;
-    __syncthreads();
-    if (!last_part) return;
-    if (threadIdx.x == 0) __hip_atomic_store(p.counter + tile_id, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    for (int q = 0; q < p.splits; ++q) {
-      const __amdgpu_buffer_rsrc_t r = rsrc(slots + (int64_t)q * PART);
 #pragma unroll
-      for (int a = 0; a < NB; ++a)
-#pragma unroll
-        for (int b = 0; b < MB; ++b)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const i32x4 v = __builtin_amdgcn_raw_buffer_load_b128(
-                r, (((w * NB + a) * MB + b) * 4 + g) * 1024 + lane * 16, 0, kDev);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float f = __int_as_float(v[e]);
-              acc[a][b][4 * g + e] = q == 0 ? f : acc[a][b][4 * g + e] + f;
-            }
-          }
-    }
+    for (int i = 0; i < NB / 2; ++i) bias[i * 64 + lane] = bv[i];
+    __builtin_amdgcn_wave_barrier();
+    mx_epilogue<C>(p, at, wm, c0w, lane, acc, bias, scratch);
+    if (!more) break;
+    at = next;
   }
-
-  // ---- epilogue ----
-  // The wave's bias in fp32, zeros past n.
-  float* bias = reinterpret_cast<float*>(smem + w * C::EPI);
-  const int c0w = at.tn * BN + wn * NB * 32;
-  for (int i = lane; i < NB * 32; i += 64) bias[i] = mx_bias(p, at.e, c0w + i);
-  __builtin_amdgcn_wave_barrier();
-  const int lrow = lane & 31, lhi = lane >> 5;
-
-  if (p.out == MX_OUT_FP8) {
-    // a lane holds 16 of a block's 32 values of its row, 8 g + 4 (l / 32) + 0 .. 3; the
-    // other half-wave holds the rest. Two swaps of half-waves give each lane 16
-    // consecutive ones, a chunk.
-    const int cpad = (int)pad_to(p.n, kKPad);
-#pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      const int64_t row = at.row0 + (wm * MB + b) * 32 + lrow;
-      const bool keep = row >= at.lo && row < at.hi;
-#pragma unroll
-      for (int a = 0; a < NB; ++a) {
-        const int c = c0w + a * 32;
-        float v[16], m = 0.0f;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const f32x4 bv = *reinterpret_cast<const f32x4*>(bias + a * 32 + 8 * g + 4 * lhi);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[4 * g + e] = acc[a][b][4 * g + e] + bv[e];
-        }
-        mx_act16(v, p.ep);
-        if (c + 32 > p.n) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c + 8 * (i / 4) + 4 * lhi + i % 4 >= p.n) v[i] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) m = amax2(m, mag(v[i]));
-        m = amax2(m, __shfl_xor(m, 32));
-        const int s = scale_of(m, FP8);
-        uint32_t q[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) q[g] = to_fp8x4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3], s);
-        const auto s0 = __builtin_amdgcn_permlane32_swap(q[0], q[2], false, false);
-        const auto s1 = __builtin_amdgcn_permlane32_swap(q[1], q[3], false, false);
-        const i32x4 o = {(int)s0[0], (int)s0[1], (int)s1[0], (int)s1[1]};
-        if (keep && c < cpad) {
-          mx_store_chunk(p, row, c + 16 * lhi, o);
-          if (lhi == 0) mx_store_scale(p, row, c, s);
-        }
-      }
-    }
-    return;
-  }
-
-  // Row-major: 64 columns of 32 rows at a time through scratch, so that the stores write
-  // whole lines.
-  float* scratch = bias + NB * 32;
-  const bool vec_ok = mx_vec_ok(p);
-#pragma unroll
-  for (int b = 0; b < MB; ++b) {
-    const int64_t r0 = at.row0 + (wm * MB + b) * 32;
-#pragma unroll
-    for (int a0 = 0; a0 < NB; a0 += 2) {
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<f32x4*>(scratch + lrow * C::EPI_ROW + a * 32 + 8 * g + 4 * lhi) =
-              f32x4{acc[a0 + a][b][4 * g], acc[a0 + a][b][4 * g + 1], acc[a0 + a][b][4 * g + 2],
-                    acc[a0 + a][b][4 * g + 3]};
-      __builtin_amdgcn_wave_barrier();
-      const int cl = (lane & 7) * 8;
-      mx_store_rows<C::EPI_ROW>(p, scratch, bias + a0 * 32 + cl, r0, at.lo, at.hi, c0w + a0 * 32 + cl, lane, vec_ok);
-      __builtin_amdgcn_wave_barrier();
-    }
-  }
+  wait_vmcnt<0>();   // no copy may land in LDS that the next workgroup owns
 }
 
 // ---- skinny kernel -----------------------------------------------------------------

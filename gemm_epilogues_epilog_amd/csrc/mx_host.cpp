@@ -99,7 +99,7 @@ MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t 
   if (rows <= 64) {
     L.cfg = rows <= 16 ? MX_S16 : rows <= 32 ? MX_S32 : MX_S64;
     L.tiles_n = (int)((cols + 31) / 32);
-    L.tiles_m = 1;
+    L.tiles_m = (int)groups;
     L.grid_x = L.tiles_n;
     L.grid_y = groups;
     return L;
@@ -121,7 +121,8 @@ MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t 
   const int64_t kt = pad_to(k, kKPad) / mx_bk((int)t.x);
   if (!experts && L.cfg == MX_M && tm * tn < cus && tm * tn <= kMxCounters)
     L.splits = (int)std::max<int64_t>(1, std::min<int64_t>({cus / (tm * tn), kt / 4, kMxMaxSplit}));
-  L.grid_x = tm * tn * L.splits;
+  // persistent workgroups: as many as fit the device (the 128 x 128 tile fits twice)
+  L.grid_x = L.splits > 1 ? tm * tn * L.splits : std::min<int64_t>(tm * tn, (int64_t)cus * (L.cfg == MX_L ? 1 : 2));
   return L;
 }
 

@@ -169,19 +169,21 @@ def test_plan_info_covers_the_output(m, n, k, experts):
             assert i["workgroups"] == 0
             continue
         assert 1 <= i["splits"] <= max(1, ref.pad(k, 256) // 128)
+        assert 1 <= i["workgroups"] <= i["tiles"] * i["splits"]
         if experts is None:
             rows = -(-m // i["tile_m"]) if i["stages"] else 1
-            assert i["workgroups"] == rows * cover * i["splits"]
+            assert i["tiles"] == rows * cover
             assert i["stages"] or m <= 64
-            # every part of every split tile has its slot of the workspace
+            # every part of every split tile has its workgroup and its slot of the workspace
             if i["splits"] > 1:
+                assert i["workgroups"] == i["tiles"] * i["splits"]
                 assert 4096 + i["workgroups"] * i["tile_m"] * i["tile_n"] * 4 <= i["workspace_bytes"]
                 assert rows * cover <= 1024
         elif i["stages"]:
             # any split of m rows over the experts fits: the worst spreads a row group each
-            assert i["workgroups"] >= cover * max(-(-m // i["tile_m"]), min(m, experts))
+            assert i["tiles"] >= cover * max(-(-m // i["tile_m"]), min(m, experts))
         else:
-            assert i["workgroups"] == cover * experts
+            assert i["tiles"] == i["workgroups"] == cover * experts
 
 
 @pytest.mark.parametrize("args,status", [
