@@ -21,6 +21,11 @@ import torch
 
 from . import (DTYPES, EPILOG, MX_FORMATS, MX_OUT, GemmEpilogError, ge_mx_plan_info_t, ge_mx_types_t, load)
 
+# torch.cuda.current_stream(device).cuda_stream without the Stream object in between, which
+# costs more than a small launch
+_current_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda index: torch.cuda.current_stream(index).cuda_stream
+
 _NAME = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
 _TORCH = {v: k for k, v in _NAME.items()}
 
@@ -47,7 +52,7 @@ def _stream(stream, device) -> int:
     """The hipStream_t to launch on: the given one, or torch's current stream of the
     tensors' device."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _current_stream(device.index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -73,17 +78,25 @@ def on_device(t, name: str, device=None):
     current, so that has to be the tensor's."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if device is None and t.device.index != torch.cuda.current_device():
+    if device is not None:
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+    elif t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}, which is not the current device")
+
+
+def _empty(shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _allocating_on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 class MXTensor:
     """A (rows, k) microscaled operand, or `experts` of them one after the other: uint8
     codes and scales in the library's layout."""
 
-    __slots__ = ("codes", "scales", "rows", "k", "format", "experts")
+    __slots__ = ("rows", "k", "format", "experts", "device", "code_ptr", "scale_ptr", "_codes", "_scales", "_buffer")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, k: int, format: str,
                  experts: Optional[int] = None):
@@ -97,18 +110,40 @@ class MXTensor:
                 raise ValueError(f"{name} must be {size} contiguous uint8 values")
         if codes.device != scales.device:
             raise ValueError("codes and scales must be on the same device")
-        self.codes, self.scales, self.rows, self.k, self.format, self.experts = codes, scales, rows, k, format, experts
+        self.rows, self.k, self.format, self.experts = rows, k, format, experts
+        self._codes, self._scales, self._buffer, self.device = codes, scales, None, codes.device
+        self.code_ptr, self.scale_ptr = codes.data_ptr(), scales.data_ptr()
 
     @classmethod
-    def empty(cls, rows: int, k: int, format: str, experts: Optional[int] = None, device="cuda"):
-        lead = () if experts is None else (experts,)
-        return cls(torch.empty(*lead, mx_code_bytes(format, rows, k), dtype=torch.uint8, device=device),
-                   torch.empty(*lead, mx_scale_bytes(rows, k), dtype=torch.uint8, device=device), rows, k, format,
-                   experts)
+    def empty(cls, rows: int, k: int, format: str, experts: Optional[int] = None, device="cuda", stream=None):
+        """An operand to be written, codes and scales in one allocation."""
+        _format(format)
+        q = cls.__new__(cls)
+        e = 1 if experts is None else experts
+        cb = e * mx_code_bytes(format, rows, k)
+        q.rows, q.k, q.format, q.experts = rows, k, format, experts
+        q._buffer = b = _empty(cb + e * mx_scale_bytes(rows, k), torch.uint8, device, stream)
+        q._codes = q._scales = None
+        q.device = b.device
+        q.code_ptr = b.data_ptr()
+        q.scale_ptr = q.code_ptr + cb
+        return q
+
+    def _view(self, lo: int, hi: int):
+        v = self._buffer[lo:hi]
+        return v if self.experts is None else v.view(self.experts, -1)
 
     @property
-    def device(self):
-        return self.codes.device
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            self._codes = self._view(0, self.scale_ptr - self.code_ptr)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            self._scales = self._view(self.scale_ptr - self.code_ptr, self._buffer.numel())
+        return self._scales
 
     @property
     def shape(self):
@@ -117,9 +152,11 @@ class MXTensor:
 
 def _parts(q: MXTensor):
     """(codes pointer, scales pointer) of each expert."""
+    c, s = q.code_ptr, q.scale_ptr
+    if q.experts is None:
+        return ((c, s),)
     cb, sb = mx_code_bytes(q.format, q.rows, q.k), mx_scale_bytes(q.rows, q.k)
-    c, s = q.codes.data_ptr(), q.scales.data_ptr()
-    return [(c + e * cb, s + e * sb) for e in range(q.experts or 1)]
+    return [(c + e * cb, s + e * sb) for e in range(q.experts)]
 
 
 def mx_quantize(x: torch.Tensor, format: str, out: Optional[MXTensor] = None, stream=None) -> MXTensor:
@@ -134,8 +171,7 @@ def mx_quantize(x: torch.Tensor, format: str, out: Optional[MXTensor] = None, st
     if k < 1 or experts == 0:
         raise ValueError("k and experts must be positive")
     if out is None:
-        with _allocating_on(stream):
-            out = MXTensor.empty(rows, k, format, experts, x.device)
+        out = MXTensor.empty(rows, k, format, experts, x.device, stream)
     elif out.shape != tuple(x.shape) or out.format != format or out.device != x.device:
         raise ValueError("out does not match x")
     L, s, dt = load(), _stream(stream, x.device), DTYPES[_NAME[x.dtype]]
@@ -151,12 +187,12 @@ def mx_quantize(x: torch.Tensor, format: str, out: Optional[MXTensor] = None, st
 
 def mx_dequantize(q: MXTensor, dtype: str = "bf16", out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values q stands for, (rows, k) or (experts, rows, k)."""
-    on_device(q.codes, "q")
+    if not isinstance(q, MXTensor) or q.device.type != "cuda" or q.device.index != torch._C._cuda_getDevice():
+        raise ValueError("q must be an MXTensor on the current device")
     if dtype not in _TORCH:
         raise ValueError(f"unknown type {dtype!r}")
     if out is None:
-        with _allocating_on(stream):
-            out = torch.empty(q.shape, dtype=_TORCH[dtype], device=q.device)
+        out = _empty(q.shape, _TORCH[dtype], q.device, stream)
     else:
         on_device(out, "out", q.device)
         if tuple(out.shape) != q.shape or out.dtype != _TORCH[dtype] or (q.k > 1 and out.stride(-1) != 1) or \
@@ -164,7 +200,11 @@ def mx_dequantize(q: MXTensor, dtype: str = "bf16", out: Optional[torch.Tensor] 
                 (q.experts is not None and q.experts > 1 and out.stride(0) < (q.rows - 1) * out.stride(-2) + q.k):
             raise ValueError(f"out must be a {q.shape} {dtype} tensor whose rows are contiguous and apart")
     L, s, fmt = load(), _stream(stream, q.device), MX_FORMATS[q.format]
-    step = out.stride(0) * out.element_size() if q.experts else 0
+    if q.experts is None:
+        _check(L.gemm_epilog_mx_dequantize(q.rows, q.k, fmt, q.code_ptr, q.scale_ptr, DTYPES[dtype], out.data_ptr(),
+                                           out.stride(0) if q.rows > 1 else q.k, s), "gemm_epilog_mx_dequantize")
+        return out
+    step = out.stride(0) * out.element_size()
     ld = out.stride(-2) if q.rows > 1 else q.k
     for e, (c, sc) in enumerate(_parts(q)):
         _check(L.gemm_epilog_mx_dequantize(q.rows, q.k, fmt, c, sc, DTYPES[dtype], out.data_ptr() + e * step, ld, s),
@@ -188,8 +228,7 @@ def mx_pack(codes: torch.Tensor, scales: torch.Tensor, format: str, k: Optional[
     if k < 1 or width != ((k + 1) // 2 if format == "mxfp4" else k) or \
             tuple(scales.shape) != (*codes.shape[:-1], (k + 31) // 32):
         raise ValueError("codes and scales do not fit k")
-    with _allocating_on(stream):
-        q = MXTensor.empty(rows, k, format, codes.shape[0] if codes.dim() == 3 else None, codes.device)
+    q = MXTensor.empty(rows, k, format, codes.shape[0] if codes.dim() == 3 else None, codes.device, stream)
     L, s = load(), _stream(stream, codes.device)
     for e, (c, sc) in enumerate(_parts(q)):
         _check(L.gemm_epilog_mx_pack(rows, k, fmt, codes.data_ptr() + e * rows * width,
@@ -246,15 +285,16 @@ class MXMatmul:
 
     def execute(self, X: MXTensor, W: MXTensor, bias: Optional[torch.Tensor] = None,
                 offsets: Optional[torch.Tensor] = None, out=None, stream=None):
-        self.plan()
+        if self.handle is None:
+            self.plan()
         n, k, experts, dev = self.n, self.k, self.experts, self.device
         if not isinstance(X, MXTensor) or X.format != self.x_format or X.k != k or X.experts is not None:
             raise ValueError(f"X must be a (rows, {k}) {self.x_format} MXTensor")
         if not isinstance(W, MXTensor) or W.format != "mxfp4" or W.k != k or W.rows != n or W.experts != experts:
             raise ValueError(f"W must be a {(n, k) if experts is None else (experts, n, k)} mxfp4 MXTensor")
-        if X.codes.device != dev or W.codes.device != dev:
+        if X.device != dev or W.device != dev:
             raise ValueError(f"X and W must be on the plan's device {dev}")
-        bp = op = None
+        bp = op = sp = None
         if self.epilog != "NONE":
             if bias is None:
                 raise ValueError(f"{self.epilog} needs a bias")
@@ -270,22 +310,21 @@ class MXMatmul:
         elif offsets is not None:
             raise ValueError("offsets belong to a plan with experts")
         m = X.rows
-        if out is None:
-            with _allocating_on(stream):
-                out = MXTensor.empty(m, n, "mxfp8", device=dev) if self.out == "mxfp8" else \
-                    torch.empty((m, n), dtype=_TORCH[self.out], device=dev)
         if self.out == "mxfp8":
-            if not isinstance(out, MXTensor) or out.shape != (m, n) or out.format != "mxfp8" or out.device != dev:
+            if out is None:
+                out = MXTensor.empty(m, n, "mxfp8", None, dev, stream)
+            elif not isinstance(out, MXTensor) or out.shape != (m, n) or out.format != "mxfp8" or out.device != dev:
                 raise ValueError(f"out must be a ({m}, {n}) mxfp8 MXTensor on {dev}")
-            dp, sp = out.codes.data_ptr(), out.scales.data_ptr()
+            dp, sp = out.code_ptr, out.scale_ptr
         else:
             t = _TORCH[self.out]
-            if out.dtype != t or out.device != dev or not out.is_contiguous() or tuple(out.shape) != (m, n):
+            if out is None:
+                out = _empty((m, n), t, dev, stream)
+            elif out.dtype != t or out.device != dev or not out.is_contiguous() or tuple(out.shape) != (m, n):
                 raise ValueError(f"out must be a contiguous ({m}, {n}) {self.out} tensor on {dev}")
-            dp, sp = out.data_ptr(), None
-        _check(load().gemm_epilog_mx_execute(self.handle, m, X.codes.data_ptr(), X.scales.data_ptr(),
-                                             W.codes.data_ptr(), W.scales.data_ptr(), bp, op, dp, sp,
-                                             _stream(stream, dev)), "gemm_epilog_mx_execute")
+            dp = out.data_ptr()
+        _check(load().gemm_epilog_mx_execute(self.handle, m, X.code_ptr, X.scale_ptr, W.code_ptr, W.scale_ptr, bp, op,
+                                             dp, sp, _stream(stream, dev)), "gemm_epilog_mx_execute")
         return out
 
     def free(self):

@@ -11,34 +11,39 @@ from typing import Optional
 import torch
 
 from . import DTYPES, load
-from .mx import _NAME, MXTensor, _allocating_on, _check, _stream, on_device
+from .mx import _NAME, MXTensor, _check, _empty, _stream, on_device
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype, device):
+def _rows(t: torch.Tensor, name: str, rows: int, d: int, dtype, device) -> int:
     """Row stride of a (rows, d) operand whose rows are contiguous."""
-    on_device(t, name, device)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor")
-    if shape[1] > 1 and t.stride(1) != 1:
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or t.shape != (rows, d):
+        raise ValueError(f"{name} must be a ({rows}, {d}) {dtype} tensor on {device}")
+    if t.is_contiguous():
+        return d
+    if d > 1 and t.stride(1) != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.stride(0) if shape[0] > 1 else shape[1]
+    return t.stride(0) if rows > 1 else d
+
+
+def _like(x: torch.Tensor, stream) -> torch.Tensor:
+    """A contiguous tensor of x's shape and type."""
+    if stream is None and x.is_contiguous():
+        return torch.empty_like(x)
+    return _empty(x.shape, x.dtype, x.device, stream)
+
+
+def _out_rows(t: torch.Tensor, name: str, rows: int, d: int, dtype, device) -> int:
+    ld = _rows(t, name, rows, d, dtype, device)
+    if ld < d:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return ld
 
 
 def _weight(w: torch.Tensor, d: int, dtype, device) -> int:
-    on_device(w, "weight", device)
-    if w.dtype not in (dtype, torch.float32) or w.numel() != d or not w.is_contiguous():
-        raise ValueError(f"weight must be {d} contiguous values of x's type or f32")
+    if not isinstance(w, torch.Tensor) or w.device != device or (w.dtype != dtype and w.dtype != torch.float32) or \
+            w.numel() != d or not w.is_contiguous():
+        raise ValueError(f"weight must be {d} contiguous values of x's type or f32 on {device}")
     return DTYPES[_NAME[w.dtype]]
-
-
-def _empty(rows: int, d: int, dtype, device, stream):
-    with _allocating_on(stream):
-        return torch.empty((rows, d), dtype=dtype, device=device)
-
-
-def _apart(t: torch.Tensor, name: str, rows: int, d: int):
-    if rows > 1 and t.stride(0) < d:
-        raise ValueError(f"the rows of {name} must not overlap")
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -56,36 +61,40 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
         raise ValueError(f"out must be {name!r}, 'mxfp8' or 'both'")
     if d < 1:
         raise ValueError("d must be positive")
-    ldx = _rows(x, "x", x.shape, x.dtype, dev)
-    wdt = _weight(weight, d, x.dtype, dev)
+    t = x.dtype
+    ldx = _rows(x, "x", rows, d, t, dev)
+    wdt = _weight(weight, d, t, dev)
     rp = sp = yp = cp = scp = None
     ldr = lds = ldy = d
     s = x
     if residual is not None:
-        ldr = _rows(residual, "residual", x.shape, x.dtype, dev)
+        ldr = _rows(residual, "residual", rows, d, t, dev)
         rp = residual.data_ptr()
-        s = sum_out if sum_out is not None else _empty(rows, d, x.dtype, dev, stream)
-        lds = _rows(s, "sum_out", x.shape, x.dtype, dev)
-        _apart(s, "sum_out", rows, d)
+        if sum_out is None:
+            s = _like(x, stream)
+        else:
+            s = sum_out
+            lds = _out_rows(s, "sum_out", rows, d, t, dev)
         sp = s.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out belongs to a residual")
     y = q = None
     if out != "mxfp8":
-        y = y_out if y_out is not None else _empty(rows, d, x.dtype, dev, stream)
-        ldy = _rows(y, "y_out", x.shape, x.dtype, dev)
-        _apart(y, "y_out", rows, d)
+        if y_out is None:
+            y = _like(x, stream)
+        else:
+            y = y_out
+            ldy = _out_rows(y, "y_out", rows, d, t, dev)
         yp = y.data_ptr()
     elif y_out is not None:
         raise ValueError("y_out needs out to be x's type or 'both'")
-    if out in ("mxfp8", "both"):
+    if out == "mxfp8" or out == "both":
         q = mx_out
         if q is None:
-            with _allocating_on(stream):
-                q = MXTensor.empty(rows, d, "mxfp8", device=dev)
-        if q.shape != (rows, d) or q.format != "mxfp8" or q.device != dev:
+            q = MXTensor.empty(rows, d, "mxfp8", None, dev, stream)
+        elif q.shape != (rows, d) or q.format != "mxfp8" or q.device != dev:
             raise ValueError(f"mx_out must be a ({rows}, {d}) mxfp8 MXTensor on {dev}")
-        cp, scp = q.codes.data_ptr(), q.scales.data_ptr()
+        cp, scp = q.code_ptr, q.scale_ptr
     elif mx_out is not None:
         raise ValueError("mx_out needs out to be 'mxfp8' or 'both'")
     _check(load().gemm_epilog_rms_norm(rows, d, DTYPES[name], x.data_ptr(), ldx, rp, ldr, weight.data_ptr(), wdt, eps,
@@ -102,23 +111,24 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor,
     if s.dtype not in _NAME or s.dim() != 2 or s.shape[1] < 1:
         raise ValueError("s must be a (rows, d) f32, f16 or bf16 tensor")
     rows, d = s.shape
-    dev = s.device
-    lds = _rows(s, "s", s.shape, s.dtype, dev)
-    lddy = _rows(dy, "dy", s.shape, s.dtype, dev)
-    wdt = _weight(weight, d, s.dtype, dev)
-    drp, lddr = None, d
+    dev, t = s.device, s.dtype
+    lds = _rows(s, "s", rows, d, t, dev)
+    lddy = _rows(dy, "dy", rows, d, t, dev)
+    wdt = _weight(weight, d, t, dev)
+    drp, lddr, lddx = None, d, d
     if dresidual is not None:
-        lddr = _rows(dresidual, "dresidual", s.shape, s.dtype, dev)
+        lddr = _rows(dresidual, "dresidual", rows, d, t, dev)
         drp = dresidual.data_ptr()
-    dx = dx_out if dx_out is not None else _empty(rows, d, s.dtype, dev, stream)
-    lddx = _rows(dx, "dx_out", s.shape, s.dtype, dev)
-    _apart(dx, "dx_out", rows, d)
+    if dx_out is None:
+        dx = _like(s, stream)
+    else:
+        dx = dx_out
+        lddx = _out_rows(dx, "dx_out", rows, d, t, dev)
     L = load()
     size = L.gemm_epilog_rms_norm_workspace_bytes(rows, d)
-    with _allocating_on(stream):
-        dw = torch.empty(d, dtype=weight.dtype, device=dev)
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
-    _check(L.gemm_epilog_rms_norm_backward(rows, d, DTYPES[_NAME[s.dtype]], dy.data_ptr(), lddy, s.data_ptr(), lds,
+    dw = _empty(d, weight.dtype, dev, stream)
+    ws = _empty(size, torch.uint8, dev, stream)
+    _check(L.gemm_epilog_rms_norm_backward(rows, d, DTYPES[_NAME[t]], dy.data_ptr(), lddy, s.data_ptr(), lds,
                                            weight.data_ptr(), wdt, eps, drp, lddr, dx.data_ptr(), lddx, dw.data_ptr(),
                                            ws.data_ptr(), size, _stream(stream, dev)), "gemm_epilog_rms_norm_backward")
     return dx, dw
