@@ -26,9 +26,8 @@ const void* kernel_of(int cfg) {
   using namespace gek;
   switch (cfg) {
     case MX_L: return reinterpret_cast<const void*>(&mx_tile_kernel<XF, MX_L, EXACT>);
-    case MX_M: return reinterpret_cast<const void*>(&mx_tile_kernel<XF, MX_M, EXACT>);
-    case MX_S64: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 4>);
-    case MX_S32: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 2>);
+    case MX_R128: return reinterpret_cast<const void*>(&mx_ring_kernel<XF, MX_R128, EXACT>);
+    case MX_R64: return reinterpret_cast<const void*>(&mx_ring_kernel<XF, MX_R64, EXACT>);
     case MX_S16: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 1>);
   }
   return nullptr;
@@ -133,7 +132,9 @@ ge_status_t gemm_epilog_mx_execute(ge_mx_handle_t h, int64_t m, const void* x_co
   a.out = (int32_t)h->t.d;
   a.vec = (int32_t)h->t.vec;
   a.group_m = L.group_m;
-  if (L.grid_x > 0x7fffffff || L.grid_y > 65535) return GE_ERR_NOT_SUPPORTED;
+  // a launch keeps its lane count below 2^32
+  if (L.grid_x * L.grid_y * gemx::mx_waves(gemx::kMxTiles[L.cfg]) * 64 >= (int64_t(1) << 32) || L.grid_y > 65535)
+    return GE_ERR_NOT_SUPPORTED;
   const bool exact = h->t.d == GE_MX_D_F32 || (h->t.d == GE_MX_D_MXFP8 && !getenv("GE_MX_FAST"));
   const void* fn = h->t.x == GE_MXFP4 ? kernel_of<gemx::FP4, false>(L.cfg)
                    : exact            ? kernel_of<gemx::FP8, true>(L.cfg)

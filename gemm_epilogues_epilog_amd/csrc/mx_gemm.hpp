@@ -148,33 +148,35 @@ __device__ __forceinline__ float mx_bias(const MxArgs& p, int e, int c) {
 template <int XF, int CFG>
 struct MxCfgT {
   static constexpr MxTile T = kMxTiles[CFG];
-  static constexpr int MB = T.mb, NB = T.nb, STAGES = T.stages;
-  static_assert(STAGES == 2, "the main loop runs on two stages");
-  static constexpr int WAVES_M = T.bm / 32 / MB, WAVES_N = T.bn / 32 / NB, NW = WAVES_M * WAVES_N;
-  static constexpr bool SPLIT = CFG == MX_M;               // may share a tile's k loop
-  static constexpr bool ACC_AGPR = MB * NB * 16 > 128;     // one wave per SIMD, sums in the accumulation registers
+  static constexpr bool RING = mx_is_ring(CFG);
+  static constexpr int MB = T.mb, NB = T.nb, STAGES = T.stages, KG = T.kg;
+  static constexpr int WAVES_M = T.bm / 32 / MB, WAVES_N = T.bn / 32 / NB, NW = WAVES_M * WAVES_N;   // of a group
   static constexpr int BK = mx_bk(XF), KS = BK / 64;
   static constexpr int WRB = BK / 32 * 512;                // bytes of a W row group per stage
   static constexpr int XRB = BK / chunk_values(XF) * 512;  // and of an X row group (4096)
   static constexpr int W_BYTES = T.bn / 32 * WRB, X_BYTES = T.bm / 32 * XRB;
-  static constexpr int SW_BYTES = T.bn / 32 * kScaleGranule, SX_BYTES = T.bm / 32 * kScaleGranule;
-  static constexpr int OFF_X = W_BYTES, OFF_SW = OFF_X + X_BYTES, OFF_SX = OFF_SW + SW_BYTES;
-  static constexpr int STAGE = OFF_SX + SX_BYTES;
-  static constexpr int CW = NW;                            // waves that copy
-  static constexpr int GW = T.bn / 32 / CW, GX = T.bm / 32 / CW;   // row groups of W and X per copying wave
-  static constexpr int SWW = T.bn / 128, SWV = SWW + T.bm / 128;   // waves that copy W's scales, any scales
-  static constexpr int INST = GW * (WRB / 1024) + GX * (XRB / 1024) + 1;   // a wave's copies per stage
+  // scales are copied four row groups at a time, by the first SWV waves
+  static constexpr int SWW = (T.bn + 127) / 128, SWV = SWW + (T.bm + 127) / 128;
+  static constexpr int OFF_X = W_BYTES, OFF_SW = OFF_X + X_BYTES, OFF_SX = OFF_SW + SWW * 1024;
+  static constexpr int STAGE = OFF_SW + SWV * 1024;
+  // copies per wave and stage: IW (IX) KB of W (X), PPW (PPX) of each of its GW (GX) row groups
+  static constexpr int IW = W_BYTES / 1024 / NW, IX = X_BYTES / 1024 / NW;
+  static constexpr int PW = WRB / 1024, PX = XRB / 1024;
+  static constexpr int PPW = IW < PW ? IW : PW, PPX = IX < PX ? IX : PX, GW = IW / PPW, GX = IX / PPX;
+  static constexpr int INST = IW + IX + 1;                 // with the copy of the scales
   // A copy after every STRIDE-th product from a k-tile's last step on: apart, so that the
   // waves do not queue for the memory pipe, but early enough to land before the next
   // barrier (8192^3: e2m1 X 170 -> 161 us at 2 on zeros, e4m3 X 272 -> 310).
-  static constexpr int STRIDE = XF == FP4 && MB * NB >= 8 ? 2 : 1;
+  static constexpr int STRIDE = XF == FP4 ? 2 : 1;
   static constexpr int EPI = 32 * 32 * 2 + NB * 32 * 4;    // epilogue LDS per wave: 32 rows of 64 bytes, and bias
-  static constexpr int OFF_EPI = STAGES * STAGE;
-  static constexpr int LDS = OFF_EPI + NW * EPI;
+  // the persistent kernel's stages hold the next tile during the epilogue
+  static constexpr int OFF_EPI = RING ? 0 : STAGES * STAGE;
+  static constexpr int LDS = RING ? STAGES * KG * STAGE : OFF_EPI + NW * EPI;
   static constexpr int XR = XF == FP8 ? 2 : 1;             // 16-byte reads per X fragment
-  static_assert(LDS <= 160 * 1024, "LDS");
-  static_assert(T.bn / 32 % CW == 0 && T.bm / 32 % CW == 0, "row groups per copying wave");
-  static_assert(NB % 2 == 0, "bias values per lane");
+  static_assert(LDS <= 160 * 1024 && NW * EPI <= LDS && NW * (KG - 1) * MB * NB * 4096 <= LDS, "LDS");
+  static_assert(IW >= 1 && IX >= 1 && IW * NW * 1024 == W_BYTES && IX * NW * 1024 == X_BYTES, "whole copies");
+  static_assert(PW % PPW == 0 && PX % PPX == 0, "a wave's copies of a row group are consecutive");
+  static_assert(SWV <= NW, "scale copies");
 };
 
 template <int XF, int MB, int NB>
@@ -295,14 +297,16 @@ __device__ __forceinline__ void static_for(Fn&& f) {
 // memory side. A part's stores have completed before it counts itself; nobody waits, so
 // no order of the workgroups can hang. Returns whether this workgroup finishes the tile.
 template <class C>
-__device__ __forceinline__ bool mx_join_parts(const MxArgs& p, const MxPlace& at, int part, int w, int lane,
+__device__ __forceinline__ bool mx_join_parts(const MxArgs& p, const MxPlace& at, int part, int w, bool mine, int lane,
                                               f32x16 (&acc)[C::NB][C::MB], int* flag) {
+  static_assert(C::MB == 1, "a wave's rows are one row group");
+  const bool has_rows = mine && at.row0 + w % C::WAVES_M * 32 < p.m;   // others only take part in the barriers
   constexpr int NB = C::NB, MB = C::MB;
   constexpr int kDev = 16;
   constexpr int PART = C::NW * NB * MB * 16 * 64 * 4;
   const int tile_id = (int)(at.row0 / C::T.bm) * p.tiles_n + at.tn;
   char* slots = reinterpret_cast<char*>(p.partial) + (int64_t)tile_id * p.splits * PART;
-  {
+  if (has_rows) {
     const __amdgpu_buffer_rsrc_t r = rsrc(slots + (int64_t)part * PART);
 #pragma unroll
     for (int a = 0; a < NB; ++a)
@@ -317,15 +321,14 @@ __device__ __forceinline__ bool mx_join_parts(const MxArgs& p, const MxPlace& at
   }
   wait_vmcnt<0>();
   __syncthreads();
-  int* shared = flag - w * (C::EPI / 4);   // wave 0's scratch
   if (threadIdx.x == 0)
-    *shared = __hip_atomic_fetch_add(p.counter + tile_id, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+    *flag = __hip_atomic_fetch_add(p.counter + tile_id, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
               (uint32_t)p.splits - 1u;
   __syncthreads();
-  if (!uniform(*shared)) return false;
-  __syncthreads();
+  if (!uniform(*flag)) return false;
+  __syncthreads();   // the flag's LDS is the epilogue's
   if (threadIdx.x == 0) __hip_atomic_store(p.counter + tile_id, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  for (int q = 0; q < p.splits; ++q) {
+  for (int q = 0; q < p.splits && has_rows; ++q) {
     const __amdgpu_buffer_rsrc_t r = rsrc(slots + (int64_t)q * PART);
 #pragma unroll
     for (int a = 0; a < NB; ++a)
@@ -457,10 +460,9 @@ struct MxCopies {
 
   template <int J>
   __device__ __forceinline__ void issue(uint32_t lane16, int scales) const {
-    constexpr int PW = C::WRB / 1024, PX = C::XRB / 1024;
-    constexpr int JX = J - C::GW * PW, JS = JX - C::GX * PX;
-    if constexpr (JX < 0) copy_kb_to_lds<J % PW>(rw, lane16, off_w[J / PW], lds_w + J / PW * C::WRB);
-    else if constexpr (JS < 0) copy_kb_to_lds<JX % PX>(rx, lane16, off_x[JX / PX], lds_x + JX / PX * C::XRB);
+    constexpr int JX = J - C::IW, JS = JX - C::IX;
+    if constexpr (JX < 0) copy_kb_to_lds<J % C::PPW>(rw, lane16, off_w[J / C::PPW], lds_w + J / C::PPW * C::WRB);
+    else if constexpr (JS < 0) copy_kb_to_lds<JX % C::PPX>(rx, lane16, off_x[JX / C::PPX], lds_x + JX / C::PPX * C::XRB);
     else copy_scales_to_lds(rs, voff_s, lds_s, scales);
   }
   template <int J0, int J1>
@@ -493,9 +495,11 @@ struct MxSrc {
     wc = p.wc + (at.e * wrg + wg0) * gw + (int64_t)kb * C::WRB;
     xc = p.xc + xg0 * gx + (int64_t)kb * C::XRB;
 #pragma unroll
-    for (int j = 0; j < C::GW; ++j) off_w[j] = uniform((int)(min(w * C::GW + j, wg_last) * gw));
+    for (int j = 0; j < C::GW; ++j)
+      off_w[j] = uniform((int)(min(w * C::IW / C::PW + j, wg_last) * gw) + w * C::IW % C::PW * 1024);
 #pragma unroll
-    for (int j = 0; j < C::GX; ++j) off_x[j] = uniform((int)(min(w * C::GX + j, xg_last) * gx));
+    for (int j = 0; j < C::GX; ++j)
+      off_x[j] = uniform((int)(min(w * C::IX / C::PX + j, xg_last) * gx) + w * C::IX % C::PX * 1024);
     // wave w copies the scales of row groups 4 w .. 4 w + 3 of [W's, X's]
     const bool of_w = w < C::SWW;
     sc = of_w ? p.ws + (at.e * wrg + wg0) * gs : p.xs + xg0 * gs;
@@ -516,8 +520,8 @@ struct MxSrc {
     for (int j = 0; j < C::GW; ++j) c.off_w[j] = off_w[j];
 #pragma unroll
     for (int j = 0; j < C::GX; ++j) c.off_x[j] = off_x[j];
-    c.lds_w = uniform(dst + w * C::GW * C::WRB);
-    c.lds_x = uniform(dst + C::OFF_X + w * C::GX * C::XRB);
+    c.lds_w = uniform(dst + w * C::IW * 1024);
+    c.lds_x = uniform(dst + C::OFF_X + w * C::IX * 1024);
     c.voff_s = voff_s;
     c.lds_s = uniform(dst + C::OFF_SW + w * 1024);
     return c;
@@ -529,14 +533,13 @@ struct MxSrc {
 // next tile's first two, so its latency hides behind this tile's end and its epilogue, and
 // the stores of D drain while the next tile computes. The epilogue has LDS of its own.
 template <int XF, int CFG, bool EXACT>
-__global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), (MxCfgT<XF, CFG>::ACC_AGPR ? 1 : 2)) void mx_tile_kernel(MxArgs p) {
+__global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), 2) void mx_tile_kernel(MxArgs p) {
   using C = MxCfgT<XF, CFG>;
   constexpr int MB = C::MB, NB = C::NB, KS = C::KS;
   constexpr int BM = C::T.bm, BN = C::T.bn;
   __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
 
-  const int part = C::SPLIT ? (int)blockIdx.x % p.splits : 0;
-  int id = C::SPLIT ? (int)blockIdx.x / p.splits : (int)blockIdx.x;
+  int id = (int)blockIdx.x;
   MxPlace at;
   if (!mx_place<BM>(p, id, at)) return;
   const int lane = threadIdx.x & 63;
@@ -544,9 +547,8 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), (MxCfgT<XF, CFG>::ACC_A
   const int wm = w % C::WAVES_M, wn = w / C::WAVES_M;
   const uint32_t lds = (uint32_t)(uintptr_t)(mx_lds_void*)smem;
   const uint32_t lane16 = lane * 16;
-  const int KTA = (int)(pad_to(p.k, kKPad) / C::BK);
-  const int kb = C::SPLIT ? (int)((int64_t)KTA * part / p.splits) : 0;
-  const int KT = C::SPLIT ? (int)((int64_t)KTA * (part + 1) / p.splits) - kb : KTA;
+  constexpr int kb = 0;
+  const int KT = (int)(pad_to(p.k, kKPad) / C::BK);
   const int KT2 = (KT + 1) & ~1;
   MxSrc<C> src;
   src.set(p, at, XF, w, lane, kb, KT);
@@ -664,7 +666,7 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), (MxCfgT<XF, CFG>::ACC_A
       tile(u1, kt + 1, src, kt + 3);
     }
     MxPlace next = at;
-    id += C::SPLIT ? (int)gridDim.x / p.splits : (int)gridDim.x;
+    id += (int)gridDim.x;
     const bool more = mx_place<BM>(p, id, next);
     src.set(p, next, XF, w, lane, kb, more ? KT : 0);
     tile(u0, KT2 - 2, src, 0);
@@ -674,14 +676,8 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), (MxCfgT<XF, CFG>::ACC_A
 #pragma unroll
     for (int a = 0; a < NB; ++a)
 #pragma unroll
-      for (int b = 0; b < MB; ++b) {
-        if constexpr (C::ACC_AGPR) asm volatile("" : "+a"(acc[a][b]));
-        else asm volatile("" : "+v"(acc[a][b]));
-      }
+      for (int b = 0; b < MB; ++b) asm volatile("" : "+v"(acc[a][b]));
 
-    if constexpr (C::SPLIT) {
-      if (p.splits > 1 && !mx_join_parts<C>(p, at, part, w, lane, acc, reinterpret_cast<int*>(scratch))) return;
-    }
 #pragma unroll
     for (int i = 0; i < NB / 2; ++i) bias[i * 64 + lane] = bv[i];
     __builtin_amdgcn_wave_barrier();
@@ -690,6 +686,131 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), (MxCfgT<XF, CFG>::ACC_A
     at = next;
   }
   wait_vmcnt<0>();   // no copy may land in LDS that the next workgroup owns
+}
+
+// ---- ring kernel ---------------------------------------------------------------------
+// Small tiles: bound by the latency and rate of the copies, not by the products. One
+// workgroup per tile and part of k. KG groups of waves take the k-tiles in turn, each with a
+// ring of STAGES stages of its own, so that the copies, LDS reads and products of one
+// group fill the waits of the other; their sums are added through LDS at the end.
+// Per k-tile: wait for this wave's copies of it, one barrier (which also says that every
+// wave is done with the stage read before), the reads, the copies of the k-tile STAGES - 1
+// rounds ahead into that stage, then the products.
+template <int XF, int CFG, bool EXACT>
+__global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * MxCfgT<XF, CFG>::KG * 64), 1) void mx_ring_kernel(MxArgs p) {
+  using C = MxCfgT<XF, CFG>;
+  constexpr int MB = C::MB, NB = C::NB, KS = C::KS, ST = C::STAGES, KG = C::KG;
+  __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
+  const int part = (int)blockIdx.x % p.splits;
+  MxPlace at;
+  if (!mx_place<C::T.bm>(p, (int)blockIdx.x / p.splits, at)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = wave % C::NW, kg = wave / C::NW;
+  const int wm = w % C::WAVES_M, wn = w / C::WAVES_M;
+  const uint32_t lds = (uint32_t)(uintptr_t)(mx_lds_void*)smem + kg * C::STAGE;
+  const uint32_t lane16 = lane * 16;
+  const int KTA = (int)(pad_to(p.k, kKPad) / C::BK);
+  const int kb = (int)((int64_t)KTA * part / p.splits), KT = (int)((int64_t)KTA * (part + 1) / p.splits) - kb;
+  MxSrc<C> src;
+  src.set(p, at, XF, w, lane, kb, KT);
+  const int scales = w < C::SWV;
+
+  f32x16 acc[NB][MB];
+#pragma unroll
+  for (int a = 0; a < NB; ++a)
+#pragma unroll
+    for (int b = 0; b < MB; ++b) acc[a][b] = f32x16{};
+#pragma unroll
+  for (int t = 0; t < ST - 1; ++t)
+    src.at(t * KG + kg, kb, w, lds + t * KG * C::STAGE).template issue_range<0, C::INST>(lane16, scales);
+
+  int u = 0;   // stage of k-tile kt; k-tiles past the last one are zeros
+  for (int kt = kg; kt < KT + kg; kt += KG) {
+    if (scales) wait_vmcnt<(ST - 2) * C::INST>();
+    else wait_vmcnt<(ST - 2) * (C::INST - 1)>();
+    wait_lgkmcnt<0>();
+    barrier_only();
+    const char* st = smem + (u * KG + kg) * C::STAGE;
+    const int sh = XF == FP8 ? ((kb + kt) & 1) * 16 : 0;   // a 128-k stage uses half of the granule's bytes
+    int sw[NB], sx[MB];
+#pragma unroll
+    for (int a = 0; a < NB; ++a)
+      sw[a] = *reinterpret_cast<const int*>(st + C::OFF_SW + (wn * NB + a) * kScaleGranule + lane * 4) >> sh;
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+      sx[b] = *reinterpret_cast<const int*>(st + C::OFF_SX + (wm * MB + b) * kScaleGranule + lane * 4) >> sh;
+    MxFrags<XF, MB, NB> f[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+#pragma unroll
+      for (int a = 0; a < NB; ++a)
+        f[s].w[a] = *reinterpret_cast<const i32x4*>(st + (wn * NB + a) * C::WRB + s * 1024 + lane * 16);
+#pragma unroll
+      for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int h = 0; h < C::XR; ++h)
+          f[s].x[b][h] = *reinterpret_cast<const i32x4*>(st + C::OFF_X + (wm * MB + b) * C::XRB +
+                                                         (s * C::XR + h) * 1024 + lane * 16);
+    }
+    const int free = u == 0 ? ST - 1 : u - 1;
+    src.at(kt + (ST - 1) * KG, kb, w, lds + free * KG * C::STAGE).template issue_range<0, C::INST>(lane16, scales);
+    static_for<KS>([&](auto tag) {
+      constexpr int s = decltype(tag)::value;
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+        if constexpr (EXACT) {
+          i32x4 xl[C::XR];
+#pragma unroll
+          for (int h = 0; h < C::XR; ++h) {
+            xl[h] = large_part(f[s].x[b][h]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[s].x[b][h][e] ^= xl[h][e];
+          }
+#pragma unroll
+          for (int a = 0; a < NB; ++a) acc[a][b] = mx_mma<XF, s>(f[s].w[a], xl, acc[a][b], sw[a], sx[b]);
+        }
+#pragma unroll
+        for (int a = 0; a < NB; ++a) acc[a][b] = mx_mma<XF, s>(f[s].w[a], f[s].x[b], acc[a][b], sw[a], sx[b]);
+      }
+    });
+    u = u + 1 == ST ? 0 : u + 1;
+  }
+  wait_vmcnt<0>();
+  __syncthreads();   // every wave is done with the stages, whose LDS serves the rest
+
+  if constexpr (KG > 1) {
+    f32x4* red = reinterpret_cast<f32x4*>(smem);
+    constexpr int Q = NB * MB * 4;
+    if (kg > 0) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const f32x16& v = acc[q / 4 % NB][q / 4 / NB];
+        red[(((kg - 1) * C::NW + w) * Q + q) * 64 + lane] =
+            f32x4{v[q % 4 * 4], v[q % 4 * 4 + 1], v[q % 4 * 4 + 2], v[q % 4 * 4 + 3]};
+      }
+    }
+    __syncthreads();
+    if (kg == 0) {
+#pragma unroll
+      for (int o = 0; o < KG - 1; ++o)
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const f32x4 v = red[((o * C::NW + w) * Q + q) * 64 + lane];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[q / 4 % NB][q / 4 / NB][q % 4 * 4 + e] += v[e];
+        }
+    }
+    __syncthreads();
+  }
+  if (p.splits > 1 && !mx_join_parts<C>(p, at, part, w, kg == 0, lane, acc, reinterpret_cast<int*>(smem))) return;
+  if (kg != 0) return;
+  float* bias = reinterpret_cast<float*>(smem + C::OFF_EPI + w * C::EPI);
+  char* scratch = reinterpret_cast<char*>(bias + NB * 32);
+  const int c0w = at.tn * C::T.bn + wn * NB * 32;
+  if (lane < NB * 32) bias[lane] = mx_bias(p, at.e, c0w + lane);
+  __builtin_amdgcn_wave_barrier();
+  mx_epilogue<C>(p, at, wm, c0w, lane, acc, bias, scratch);
 }
 
 // ---- skinny kernel -----------------------------------------------------------------

@@ -2,6 +2,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 
 #include "mx_tiles.hpp"
 
@@ -96,33 +97,46 @@ MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t 
   const int64_t cols = t.d == GE_MX_D_MXFP8 ? pad_to(n, kKPad) : n;   // an 8-bit D is written with its padding
   const int64_t groups = experts ? experts : 1;
   const int64_t rows = (m + groups - 1) / groups;   // of an even share
-  if (rows <= 64) {
-    L.cfg = rows <= 16 ? MX_S16 : rows <= 32 ? MX_S32 : MX_S64;
-    L.tiles_n = (int)((cols + 31) / 32);
+  int force = -1;
+  if (const char* e = std::getenv("GE_MX_CFG")) force = std::atoi(e);
+  if (force >= 0 ? force == MX_S16 : rows <= 16) {
+    L.cfg = MX_S16;
+    L.tiles_n = (int)((cols + kMxTiles[MX_S16].bn - 1) / kMxTiles[MX_S16].bn);
     L.tiles_m = (int)groups;
     L.grid_x = L.tiles_n;
     L.grid_y = groups;
     return L;
   }
-  auto count = [&](int cfg, int64_t& tm, int64_t& tn) {
-    const MxTile& T = kMxTiles[cfg];
-    tm = experts ? (m + 31 * experts) / T.bm + experts : (m + T.bm - 1) / T.bm;
-    tn = (cols + T.bn - 1) / T.bn;
-    return tm * tn;
-  };
-  int64_t tm, tn;
-  L.cfg = MX_L;
-  if (count(MX_L, tm, tn) < cus) {
-    L.cfg = MX_M;
-    count(MX_M, tm, tn);
-  }
-  L.tiles_m = (int)tm;
-  L.tiles_n = (int)tn;
+  // Estimated microseconds of each configuration: rounds of workgroups over the compute
+  // units, each so many k-tiles and a fixed part (start, epilogue, joining parts of k).
   const int64_t kt = pad_to(k, kKPad) / mx_bk((int)t.x);
-  if (!experts && L.cfg == MX_M && tm * tn < cus && tm * tn <= kMxCounters)
-    L.splits = (int)std::max<int64_t>(1, std::min<int64_t>({cus / (tm * tn), kt / 4, kMxMaxSplit}));
-  // persistent workgroups: as many as fit the device (the 128 x 128 tile fits twice)
-  L.grid_x = L.splits > 1 ? tm * tn * L.splits : std::min<int64_t>(tm * tn, (int64_t)cus * (L.cfg == MX_L ? 1 : 2));
+  double best = 0;
+  for (int cfg = MX_L; cfg <= MX_R64; ++cfg) {
+    if (force >= 0 && cfg != force) continue;
+    const MxTile& T = kMxTiles[cfg];
+    const int64_t tm = experts ? (m + 31 * experts) / T.bm + experts : (m + T.bm - 1) / T.bm;
+    const int64_t tn = (cols + T.bn - 1) / T.bn, tiles = tm * tn;
+    const double per_kt = cfg == MX_L ? 1.4 : cfg == MX_R128 ? 0.2 : 0.13;
+    const double fixed = cfg == MX_L ? 10 : 4;
+    const int most = cfg == MX_L || experts || tiles > kMxCounters
+                         ? 1
+                         : (int)std::max<int64_t>(1, std::min<int64_t>({cus / tiles, kt / 2, kMxMaxSplit}));
+    for (int s = 1; s <= most; ++s) {
+      const double rounds = (double)((tiles * s + cus - 1) / cus);
+      const double us = rounds * ((double)((kt + s - 1) / s) * per_kt + fixed + (s > 1 ? 1.5 + 0.5 * s : 0));
+      if (best == 0 || us < best) {
+        best = us;
+        L.cfg = cfg;
+        L.tiles_m = (int)tm;
+        L.tiles_n = (int)tn;
+        L.splits = s;
+      }
+    }
+  }
+  if (const char* e = std::getenv("GE_MX_SPLIT"); e && L.cfg != MX_L && !experts) L.splits = std::atoi(e);
+  const int64_t tiles = (int64_t)L.tiles_m * L.tiles_n;
+  // the persistent kernel: one workgroup per compute unit
+  L.grid_x = L.cfg == MX_L ? std::min<int64_t>(tiles, cus) : tiles * L.splits;
   return L;
 }
 
@@ -131,9 +145,8 @@ size_t workspace_bytes(int64_t n, int64_t k, int64_t experts, ge_mx_types_t t, i
   (void)n, (void)k, (void)t;
   if (experts) return 0;
   // split tiles times parts stay within one workgroup per compute unit
-  return kMxCounterBytes + (size_t)cus * kMxTiles[MX_M].bm * kMxTiles[MX_M].bn * 4;
+  return kMxCounterBytes + (size_t)cus * kMxTiles[MX_R128].bm * kMxTiles[MX_R128].bn * 4;
 }
-
 
 // ---- norm ---------------------------------------------------------------------------
 namespace {
