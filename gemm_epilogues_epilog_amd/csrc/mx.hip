@@ -2,7 +2,6 @@
 // mx_host.cpp).
 #include <hip/hip_runtime.h>
 
-#include <cstdlib>
 #include <cstring>
 #include <new>
 
@@ -28,7 +27,7 @@ const void* kernel_of(int cfg) {
     case MX_L: return reinterpret_cast<const void*>(&mx_tile_kernel<XF, MX_L, EXACT>);
     case MX_R128: return reinterpret_cast<const void*>(&mx_ring_kernel<XF, MX_R128, EXACT>);
     case MX_R64: return reinterpret_cast<const void*>(&mx_ring_kernel<XF, MX_R64, EXACT>);
-    case MX_S16: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 1>);
+    case MX_S16: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 1, EXACT>);
   }
   return nullptr;
 }
@@ -135,7 +134,7 @@ ge_status_t gemm_epilog_mx_execute(ge_mx_handle_t h, int64_t m, const void* x_co
   // a launch keeps its lane count below 2^32
   if (L.grid_x * L.grid_y * gemx::mx_waves(gemx::kMxTiles[L.cfg]) * 64 >= (int64_t(1) << 32) || L.grid_y > 65535)
     return GE_ERR_NOT_SUPPORTED;
-  const bool exact = h->t.d == GE_MX_D_F32 || (h->t.d == GE_MX_D_MXFP8 && !getenv("GE_MX_FAST"));
+  const bool exact = h->t.d == GE_MX_D_F32 || h->t.d == GE_MX_D_MXFP8;   // see large_part
   const void* fn = h->t.x == GE_MXFP4 ? kernel_of<gemx::FP4, false>(L.cfg)
                    : exact            ? kernel_of<gemx::FP8, true>(L.cfg)
                                       : kernel_of<gemx::FP8, false>(L.cfg);

@@ -208,7 +208,7 @@ struct MxPlace {
   int64_t row0, lo, hi;
 };
 template <int BM>
-__device__ __forceinline__ bool mx_place(const MxArgs& p, int id, MxPlace& o) {
+__device__ __forceinline__ bool mx_place(const MxArgs& p, int id, bool remap, MxPlace& o) {
   int tiles_m = p.tiles_m;
   if (p.experts) {
     const int lane = threadIdx.x & 63;
@@ -225,7 +225,7 @@ __device__ __forceinline__ bool mx_place(const MxArgs& p, int id, MxPlace& o) {
   }
   const int G = tiles_m * p.tiles_n;
   if (id >= G) return false;
-  const int pos = xcd_remap(id, G);
+  const int pos = remap ? xcd_remap(id, G) : id;   // each XCD takes a run of the order
   const int gsz = p.group_m * p.tiles_n;
   const int g = pos / gsz, first = g * p.group_m;
   const int rows = min(tiles_m - first, p.group_m);
@@ -266,19 +266,22 @@ __device__ __forceinline__ bool mx_place(const MxArgs& p, int id, MxPlace& o) {
   return false;
 }
 
-// X's e4m3 values in two parts whose sum they are: the ones of at least 4 in magnitude, and
+// X's e4m3 values in two parts whose sum they are: the ones of at least 2 in magnitude, and
 // the rest. The matrix unit adds the products of eight neighbouring elements aligned to the
-// largest of them and drops what lies more than 13 bits below it. A block's largest value
-// is in [256, 448]; products with the large part (4 .. 448 by 0.5 .. 6) span 13 bits and
-// those with the rest lose only bits 2^-21 below the block's largest product, so two
-// instructions keep the 24 bits that an fp32 sum has, where one keeps about 16.
+// largest of them and drops what lies more than 13 bits below it (4 x 6 products span
+// 21 bits). A block's largest value is in [256, 448]; products with the large part (2 ..
+// 448 by 0.5 .. 6) span 13 bits, 14 where one of them reaches 2048, and those with the rest
+// lose nothing, so two instructions keep what an fp32 sum keeps, where one leaves 1.3e-5
+// of the result's norm (k = 4096, normal values with outlier channels). Results in 32 or 8
+// bits take two; 16-bit results, whose own rounding is 15 times as coarse in fp16 and 120
+// times in bf16, take one.
 __device__ __forceinline__ i32x4 large_part(i32x4 x) {
   i32x4 r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t v = (uint32_t)x[i];
-    const uint32_t m = ((v & 0x7f7f7f7fu) + 0x38383838u) & 0x80808080u;   // byte >= 0x48 (4.0)
-    r[i] = (int)(v & (m | (m - (m >> 7))));
+    // bit 6 of a byte is the exponent's top bit: selector 13 gives 0xff, 12 gives 0
+    const uint32_t sel = (((uint32_t)x[i] >> 6) & 0x01010101u) | 0x0c0c0c0cu;
+    r[i] = (int)((uint32_t)x[i] & __builtin_amdgcn_perm(0u, 0u, sel));
   }
   return r;
 }
@@ -322,28 +325,40 @@ __device__ __forceinline__ bool mx_join_parts(const MxArgs& p, const MxPlace& at
   wait_vmcnt<0>();
   __syncthreads();
   if (threadIdx.x == 0)
-    *flag = __hip_atomic_fetch_add(p.counter + tile_id, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+    *flag = __hip_atomic_fetch_add(p.counter + tile_id * kMxCounterStride, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
               (uint32_t)p.splits - 1u;
   __syncthreads();
   if (!uniform(*flag)) return false;
   __syncthreads();   // the flag's LDS is the epilogue's
-  if (threadIdx.x == 0) __hip_atomic_store(p.counter + tile_id, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  for (int q = 0; q < p.splits && has_rows; ++q) {
-    const __amdgpu_buffer_rsrc_t r = rsrc(slots + (int64_t)q * PART);
+  if (threadIdx.x == 0) __hip_atomic_store(p.counter + tile_id * kMxCounterStride, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (!has_rows) return true;
+  // four parts' loads in flight together: a trip to the memory side takes longer than the adds
+  constexpr int Q = NB * MB * 4, G = 4;
 #pragma unroll
-    for (int a = 0; a < NB; ++a)
+  for (int q = 0; q < Q; ++q)
 #pragma unroll
-      for (int b = 0; b < MB; ++b)
+    for (int e = 0; e < 4; ++e) acc[q / 4 % NB][q / 4 / NB][q % 4 * 4 + e] = 0.0f;
+  for (int s0 = 0; s0 < p.splits; s0 += G) {
+    i32x4 v[G][Q];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const i32x4 v = __builtin_amdgcn_raw_buffer_load_b128(
-              r, (((w * NB + a) * MB + b) * 4 + g) * 1024 + lane * 16, 0, kDev);
+    for (int s = 0; s < G; ++s) {
+      if (s0 + s < p.splits) {
+        const __amdgpu_buffer_rsrc_t r = rsrc(slots + (int64_t)(s0 + s) * PART);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float f = __int_as_float(v[e]);
-            acc[a][b][4 * g + e] = q == 0 ? f : acc[a][b][4 * g + e] + f;
-          }
-        }
+        for (int q = 0; q < Q; ++q)
+          v[s][q] = __builtin_amdgcn_raw_buffer_load_b128(
+              r, (((w * NB + q / 4 % NB) * MB + q / 4 / NB) * 4 + q % 4) * 1024 + lane * 16, 0, kDev);
+      } else {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) v[s][q] = i32x4{0, 0, 0, 0};
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < G; ++s)
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[q / 4 % NB][q / 4 / NB][q % 4 * 4 + e] += __int_as_float(v[s][q][e]);
   }
   return true;
 }
@@ -541,7 +556,7 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), 2) void mx_tile_kernel(
 
   int id = (int)blockIdx.x;
   MxPlace at;
-  if (!mx_place<BM>(p, id, at)) return;
+  if (!mx_place<BM>(p, id, true, at)) return;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w % C::WAVES_M, wn = w / C::WAVES_M;
@@ -667,7 +682,7 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), 2) void mx_tile_kernel(
     }
     MxPlace next = at;
     id += (int)gridDim.x;
-    const bool more = mx_place<BM>(p, id, next);
+    const bool more = mx_place<BM>(p, id, true, next);
     src.set(p, next, XF, w, lane, kb, more ? KT : 0);
     tile(u0, KT2 - 2, src, 0);
     tile(u1, KT2 - 1, src, 1);
@@ -693,17 +708,19 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), 2) void mx_tile_kernel(
 // workgroup per tile and part of k. KG groups of waves take the k-tiles in turn, each with a
 // ring of STAGES stages of its own, so that the copies, LDS reads and products of one
 // group fill the waits of the other; their sums are added through LDS at the end.
-// Per k-tile: wait for this wave's copies of it, one barrier (which also says that every
-// wave is done with the stage read before), the reads, the copies of the k-tile STAGES - 1
-// rounds ahead into that stage, then the products.
+// Per round one barrier; the LDS reads of the next k-tile and the copies of a later one run
+// beside the products of this one.
 template <int XF, int CFG, bool EXACT>
 __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * MxCfgT<XF, CFG>::KG * 64), 1) void mx_ring_kernel(MxArgs p) {
   using C = MxCfgT<XF, CFG>;
   constexpr int MB = C::MB, NB = C::NB, KS = C::KS, ST = C::STAGES, KG = C::KG;
   __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
-  const int part = (int)blockIdx.x % p.splits;
+  // The parts of a tile run on one XCD (the XCDs start a launch's workgroups some
+  // microseconds apart, and the last part to arrive finishes the tile).
+  const int q = p.splits > 1 ? xcd_remap(blockIdx.x, gridDim.x) : (int)blockIdx.x;
+  const int part = q % p.splits;
   MxPlace at;
-  if (!mx_place<C::T.bm>(p, (int)blockIdx.x / p.splits, at)) return;
+  if (!mx_place<C::T.bm>(p, q / p.splits, p.splits == 1, at)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int w = wave % C::NW, kg = wave / C::NW;
@@ -721,60 +738,94 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * MxCfgT<XF, CFG>::KG * 64), 1
   for (int a = 0; a < NB; ++a)
 #pragma unroll
     for (int b = 0; b < MB; ++b) acc[a][b] = f32x16{};
-#pragma unroll
-  for (int t = 0; t < ST - 1; ++t)
-    src.at(t * KG + kg, kb, w, lds + t * KG * C::STAGE).template issue_range<0, C::INST>(lane16, scales);
-
-  int u = 0;   // stage of k-tile kt; k-tiles past the last one are zeros
-  for (int kt = kg; kt < KT + kg; kt += KG) {
-    if (scales) wait_vmcnt<(ST - 2) * C::INST>();
-    else wait_vmcnt<(ST - 2) * (C::INST - 1)>();
-    wait_lgkmcnt<0>();
-    barrier_only();
-    const char* st = smem + (u * KG + kg) * C::STAGE;
-    const int sh = XF == FP8 ? ((kb + kt) & 1) * 16 : 0;   // a 128-k stage uses half of the granule's bytes
+  // the fragments and scales of one k-tile
+  struct Tile {
+    MxFrags<XF, MB, NB> f[KS];
     int sw[NB], sx[MB];
+  };
+  auto read = [&](int u, int kt, Tile& t) {   // k-tile kt from stage u
+    const char* st = smem + (u * KG + kg) * C::STAGE;
 #pragma unroll
     for (int a = 0; a < NB; ++a)
-      sw[a] = *reinterpret_cast<const int*>(st + C::OFF_SW + (wn * NB + a) * kScaleGranule + lane * 4) >> sh;
+      t.sw[a] = *reinterpret_cast<const int*>(st + C::OFF_SW + (wn * NB + a) * kScaleGranule + lane * 4);
 #pragma unroll
     for (int b = 0; b < MB; ++b)
-      sx[b] = *reinterpret_cast<const int*>(st + C::OFF_SX + (wm * MB + b) * kScaleGranule + lane * 4) >> sh;
-    MxFrags<XF, MB, NB> f[KS];
+      t.sx[b] = *reinterpret_cast<const int*>(st + C::OFF_SX + (wm * MB + b) * kScaleGranule + lane * 4);
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
 #pragma unroll
       for (int a = 0; a < NB; ++a)
-        f[s].w[a] = *reinterpret_cast<const i32x4*>(st + (wn * NB + a) * C::WRB + s * 1024 + lane * 16);
+        t.f[s].w[a] = *reinterpret_cast<const i32x4*>(st + (wn * NB + a) * C::WRB + s * 1024 + lane * 16);
 #pragma unroll
       for (int b = 0; b < MB; ++b)
 #pragma unroll
         for (int h = 0; h < C::XR; ++h)
-          f[s].x[b][h] = *reinterpret_cast<const i32x4*>(st + C::OFF_X + (wm * MB + b) * C::XRB +
-                                                         (s * C::XR + h) * 1024 + lane * 16);
+          t.f[s].x[b][h] = *reinterpret_cast<const i32x4*>(st + C::OFF_X + (wm * MB + b) * C::XRB +
+                                                           (s * C::XR + h) * 1024 + lane * 16);
     }
-    const int free = u == 0 ? ST - 1 : u - 1;
-    src.at(kt + (ST - 1) * KG, kb, w, lds + free * KG * C::STAGE).template issue_range<0, C::INST>(lane16, scales);
-    static_for<KS>([&](auto tag) {
-      constexpr int s = decltype(tag)::value;
+  };
+  auto wait_copies = [&]() {   // all but the copies of the last ST - 2 k-tiles have landed
+    if (scales) wait_vmcnt<(ST - 2) * C::INST>();
+    else wait_vmcnt<(ST - 2) * (C::INST - 1)>();
+  };
 #pragma unroll
-      for (int b = 0; b < MB; ++b) {
+  for (int t = 0; t < ST - 1; ++t)
+    src.at(t * KG + kg, kb, w, lds + t * KG * C::STAGE).template issue_range<0, C::INST>(lane16, scales);
+  wait_copies();
+  barrier_only();
+  Tile tiles[2];
+  read(0, kg, tiles[0]);
+  src.at((ST - 1) * KG + kg, kb, w, lds + (ST - 1) * KG * C::STAGE).template issue_range<0, C::INST>(lane16, scales);
+
+  // Round r: k-tile r KG + kg is in registers; the next one is read and the one ST rounds
+  // ahead copied while its products run. K-tiles past the last one are zeros.
+  const int R = (KT + KG - 1) / KG;
+  int u = 0;   // stage of the round's k-tile
+  auto round = [&](int r, Tile& now, Tile& next) {
+    wait_copies();
+    wait_lgkmcnt<0>();   // this wave's reads of stage u are done
+    barrier_only();
+    const int kt = r * KG + kg, un = u + 1 == ST ? 0 : u + 1;
+    read(un, kt + KG, next);
+    const int sh = XF == FP8 ? ((kb + kt) & 1) * 16 : 0;   // a 128-k stage uses half of the granule's bytes
+#pragma unroll
+    for (int a = 0; a < NB; ++a) now.sw[a] >>= sh;
+#pragma unroll
+    for (int b = 0; b < MB; ++b) now.sx[b] >>= sh;
+    const MxCopies<C> cp = src.at(kt + ST * KG, kb, w, lds + u * KG * C::STAGE);
+    static_for<KS>([&](auto stag) {
+      constexpr int s = decltype(stag)::value;
+      static_for<MB * NB>([&](auto itag) {
+        constexpr int i = decltype(itag)::value, a = i % NB, b = i / NB, N = MB * NB * KS;
         if constexpr (EXACT) {
           i32x4 xl[C::XR];
 #pragma unroll
           for (int h = 0; h < C::XR; ++h) {
-            xl[h] = large_part(f[s].x[b][h]);
+            xl[h] = large_part(now.f[s].x[b][h]);
+            if constexpr (a == NB - 1) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[s].x[b][h][e] ^= xl[h][e];
+              for (int e = 0; e < 4; ++e) now.f[s].x[b][h][e] ^= xl[h][e];
+            }
           }
+          acc[a][b] = mx_mma<XF, s>(now.f[s].w[a], xl, acc[a][b], now.sw[a], now.sx[b]);
+          if constexpr (a == NB - 1) {
 #pragma unroll
-          for (int a = 0; a < NB; ++a) acc[a][b] = mx_mma<XF, s>(f[s].w[a], xl, acc[a][b], sw[a], sx[b]);
+            for (int c = 0; c < NB; ++c)
+              acc[c][b] = mx_mma<XF, s>(now.f[s].w[c], now.f[s].x[b], acc[c][b], now.sw[c], now.sx[b]);
+          }
+        } else {
+          acc[a][b] = mx_mma<XF, s>(now.f[s].w[a], now.f[s].x[b], acc[a][b], now.sw[a], now.sx[b]);
         }
-#pragma unroll
-        for (int a = 0; a < NB; ++a) acc[a][b] = mx_mma<XF, s>(f[s].w[a], f[s].x[b], acc[a][b], sw[a], sx[b]);
-      }
+        constexpr int j = s * MB * NB + i;   // the copies spread over the products
+        cp.template issue_range<j * C::INST / N, (j + 1) * C::INST / N>(lane16, scales);
+        __builtin_amdgcn_sched_barrier(0);
+      });
     });
-    u = u + 1 == ST ? 0 : u + 1;
+    u = un;
+  };
+  for (int r = 0; r < R; r += 2) {
+    round(r, tiles[0], tiles[1]);
+    round(r + 1, tiles[1], tiles[0]);
   }
   wait_vmcnt<0>();
   __syncthreads();   // every wave is done with the stages, whose LDS serves the rest
@@ -831,7 +882,7 @@ __device__ __forceinline__ f32x4 mx_mma16(i32x4 w, const i32x4 (&x)[XF == FP8 ? 
   }
 }
 
-template <int XF, int TB>
+template <int XF, int TB, bool EXACT>
 __global__ __launch_bounds__(512, 1) void mx_skinny_kernel(MxArgs p) {
   constexpr int FB = 2, NW = 8, XR = XF == FP8 ? 2 : 1;
   constexpr int ROW = FB * 16 + 4;   // floats per finished row
@@ -890,6 +941,16 @@ __global__ __launch_bounds__(512, 1) void mx_skinny_kernel(MxArgs p) {
           for (int h = 0; h < XR; ++h)
             xf[h] = *reinterpret_cast<const i32x4*>(xc[b] + (int64_t)s * (2048 * XR) + h * 2048);
           sx = *reinterpret_cast<const int*>(xs[b] + (int64_t)(s >> 1) * kScaleGranule) >> sh;
+        }
+        if constexpr (EXACT) {
+          i32x4 xl[XR];
+#pragma unroll
+          for (int h = 0; h < XR; ++h) {
+            xl[h] = large_part(xf[h]);
+            xf[h] ^= xl[h];
+          }
+#pragma unroll
+          for (int f = 0; f < FB; ++f) acc[f][b] = mx_mma16<XF, 0>(wf[f], xl, acc[f][b], sw[f], sx);
         }
 #pragma unroll
         for (int f = 0; f < FB; ++f) acc[f][b] = mx_mma16<XF, 0>(wf[f], xf, acc[f][b], sw[f], sx);

@@ -108,7 +108,11 @@ MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t 
     return L;
   }
   // Estimated microseconds of each configuration: rounds of workgroups over the compute
-  // units, each so many k-tiles and a fixed part (start, epilogue, joining parts of k).
+  // units, each so many k-tiles and a fixed part (start, epilogue, joining parts of k),
+  // from measurements at one full round (X e2m1; e4m3; e4m3 in two parts).
+  static constexpr double kPerTile[3][3] = {{1.55, 1.2, 2.1}, {0.34, 0.26, 0.42}, {0.19, 0.17, 0.33}};
+  static constexpr double kFixed[3] = {3.0, 5.5, 4.6};
+  const int kind = t.x == GE_MXFP4 ? 0 : (t.d == GE_MX_D_F32 || t.d == GE_MX_D_MXFP8) ? 2 : 1;
   const int64_t kt = pad_to(k, kKPad) / mx_bk((int)t.x);
   double best = 0;
   for (int cfg = MX_L; cfg <= MX_R64; ++cfg) {
@@ -116,14 +120,13 @@ MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t 
     const MxTile& T = kMxTiles[cfg];
     const int64_t tm = experts ? (m + 31 * experts) / T.bm + experts : (m + T.bm - 1) / T.bm;
     const int64_t tn = (cols + T.bn - 1) / T.bn, tiles = tm * tn;
-    const double per_kt = cfg == MX_L ? 1.4 : cfg == MX_R128 ? 0.2 : 0.13;
-    const double fixed = cfg == MX_L ? 10 : 4;
     const int most = cfg == MX_L || experts || tiles > kMxCounters
                          ? 1
                          : (int)std::max<int64_t>(1, std::min<int64_t>({cus / tiles, kt / 2, kMxMaxSplit}));
     for (int s = 1; s <= most; ++s) {
       const double rounds = (double)((tiles * s + cus - 1) / cus);
-      const double us = rounds * ((double)((kt + s - 1) / s) * per_kt + fixed + (s > 1 ? 1.5 + 0.5 * s : 0));
+      const double us = rounds * ((double)((kt + s - 1) / s) * kPerTile[cfg][kind] + kFixed[cfg]) +
+                        (cfg == MX_L ? 7.0 : s > 1 ? 1.0 * s : 0.0);
       if (best == 0 || us < best) {
         best = us;
         L.cfg = cfg;

@@ -28,9 +28,11 @@ constexpr int mx_waves(const MxTile& t) { return t.stages ? (t.bm / 32 / t.mb) *
 // k values of one LDS stage: 128 bytes of a row of X.
 constexpr int mx_bk(int xfmt) { return xfmt == FP4 ? 256 : 128; }
 
-// Split tiles: fp32 partial accumulators of one part, and the counters of arrived parts.
+// Split tiles: the counters of arrived parts, each in a cache line of its own (neighbours in
+// one line queue for it), then the parts' fp32 accumulators.
 constexpr int kMxMaxSplit = 16;
-constexpr int kMxCounters = 1024;   // one per split tile
-constexpr size_t kMxCounterBytes = kMxCounters * 4;
+constexpr int kMxCounters = 512;
+constexpr int kMxCounterStride = 64;   // words
+constexpr size_t kMxCounterBytes = (size_t)kMxCounters * kMxCounterStride * 4;
 
 }  // namespace gemx

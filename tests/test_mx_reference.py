@@ -177,8 +177,7 @@ def test_plan_info_covers_the_output(m, n, k, experts):
             # every part of every split tile has its workgroup and its slot of the workspace
             if i["splits"] > 1:
                 assert i["workgroups"] == i["tiles"] * i["splits"]
-                assert 4096 + i["workgroups"] * i["tile_m"] * i["tile_n"] * 4 <= i["workspace_bytes"]
-                assert rows * cover <= 1024
+                assert i["workgroups"] * i["tile_m"] * i["tile_n"] * 4 <= i["workspace_bytes"]
         elif i["stages"]:
             # any split of m rows over the experts fits: the worst spreads a row group each
             assert i["tiles"] >= cover * max(-(-m // i["tile_m"]), min(m, experts))
