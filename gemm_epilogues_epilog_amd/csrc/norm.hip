@@ -14,7 +14,6 @@
 
 #include "gemm_epilog.h"
 #include "kernels.hpp"
-#include "launch.hpp"
 #include "mx_format.hpp"
 #include "mx_host.hpp"
 
@@ -34,30 +33,41 @@ struct NormArgs {
   int64_t rows, ldx, ldr, lds, ldy;
   int d, wdt;
   float eps;
+  int walk;   // rows per slot
 };
 
-// Eight values from element i on; the ones from `n` on (of this chunk) read as zero.
+// Eight values from element i on as they lie in memory, and widened; the ones from `n` on
+// (of this chunk) read as zero. VEC: 16-byte loads, n at least 8.
 template <int DT, bool VEC>
-__device__ __forceinline__ void load_chunk(const void* p, int64_t i, int n, float (&v)[8]) {
-  if constexpr (VEC) {
-    if constexpr (DT == F32) {
-      const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
-      const f32x4 a = q[0], b = q[1];
+struct Chunk {
+  static constexpr int W = DT == F32 ? 2 : 1;
+  i32x4 raw[W];
+  __device__ __forceinline__ void load(const void* p, int64_t i, int n) {
+    const char* q = static_cast<const char*>(p) + i * (DT == F32 ? 4 : 2);
+    if constexpr (VEC) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = a[e];
-        v[4 + e] = b[e];
-      }
+      for (int j = 0; j < W; ++j) raw[j] = reinterpret_cast<const i32x4*>(q)[j];
     } else {
-      const i32x4 a = *reinterpret_cast<const i32x4*>(static_cast<const uint16_t*>(p) + i);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = Tr<DT>::widen((uint16_t)((uint32_t)a[e / 2] >> (16 * (e & 1))));
+      for (int j = 0; j < W; ++j) raw[j] = i32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (e < n) {
+          if constexpr (DT == F32) raw[e / 4][e % 4] = reinterpret_cast<const int*>(q)[e];
+          else raw[0][e / 2] |= (int)((uint32_t)reinterpret_cast<const uint16_t*>(q)[e] << (16 * (e & 1)));
+        }
+      }
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < n ? load_vec(p, DT, i + e) : 0.0f;
   }
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < W; ++j) raw[j] = i32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (DT == F32) return __int_as_float(raw[e / 4][e % 4]);
+    else return Tr<DT>::widen((uint16_t)((uint32_t)raw[0][e / 2] >> (16 * (e & 1))));
+  }
+};
 template <int DT, bool VEC>
 __device__ __forceinline__ void store_chunk(void* p, int64_t i, int n, const float (&v)[8]) {
   if constexpr (VEC) {
@@ -80,8 +90,17 @@ __device__ __forceinline__ void store_chunk(void* p, int64_t i, int n, const flo
 // Weight values: of the row type or fp32.
 template <int DT, bool VEC>
 __device__ __forceinline__ void load_weight(const void* p, int wdt, int i, int n, float (&v)[8]) {
-  if (DT == F32 || wdt != F32) load_chunk<DT, VEC>(p, i, n, v);
-  else load_chunk<F32, VEC>(p, i, n, v);
+  if (DT == F32 || wdt != F32) {
+    Chunk<DT, VEC> c;
+    c.load(p, i, n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c.get(e);
+  } else {
+    Chunk<F32, VEC> c;
+    c.load(p, i, n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c.get(e);
+  }
 }
 template <int DT>
 __device__ __forceinline__ float round_to(float v) {
@@ -95,84 +114,126 @@ __device__ __forceinline__ float wave_sum(float v) {
   for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
   return v;
 }
-// Sum over the NT lanes of a row (waves added in order, the same in each of them).
-template <int NT>
-__device__ __forceinline__ float row_sum(float v, float* red, int t) {
-  v = wave_sum(v);
-  if constexpr (NT > 64) {
-    if ((t & 63) == 0) red[t >> 6] = v;
-    __syncthreads();
-    v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NT / 64; ++i) v += red[i];
-  }
-  return v;
-}
-
-// NT lanes per row, C chunks of eight values per lane, WG / NT rows per workgroup.
-constexpr int wg_of(int nt) { return nt > 256 ? nt : 256; }
+// NT lanes per row, C chunks of eight values per lane, WG / NT rows side by side in a
+// workgroup and a.walk rows one after the other per row slot: the weight is read once per
+// slot, and the next row's loads are in flight while this one is summed and written.
+// LDS of one slot's 8-bit rows.
+constexpr int norm_stage_bytes(int granules, int walk) { return granules * (16 * (walk + 1) * 16 + 2 * walk * 4); }
+constexpr int wg_of(int nt) { return nt > 64 ? nt : 256; }
 
 template <int DT, int NT, int C, bool VEC>
 __global__ __launch_bounds__(wg_of(NT)) void rms_norm_kernel(NormArgs a) {
-  constexpr int RPW = wg_of(NT) / NT;
-  __shared__ float red[16];
+  constexpr int RPW = wg_of(NT) / NT, NWV = NT / 64;
+  static_assert(NT == 64 || RPW == 1, "rows that share a workgroup share no barrier");
+  constexpr bool HOLD = NT * C <= 1024;   // registers for the next row and the weight (up to 8192 values)
+  __shared__ float red[2][16];
   const int t = threadIdx.x % NT, slot = threadIdx.x / NT;
-  // With an 8-bit result the workgroups of 32 consecutive rows run on one XCD: their
-  // 16-byte chunks share cache lines, which its L2 then joins.
-  int64_t row;
-  if (a.codes) {
-    constexpr int Q = 32 / RPW;
-    const int64_t x = blockIdx.x & 7, l = blockIdx.x >> 3;
-    row = ((l / Q) * 8 + x) * 32 + (l % Q) * RPW + slot;
-  } else {
-    row = (int64_t)blockIdx.x * RPW + slot;
-  }
-  const bool in = row < a.rows;
-  if (NT > 64 && RPW == 1 && !in) return;   // the whole workgroup
-  const int64_t rr = in ? row : 0;
-  float s[C][8], w[C][8];
-  float sq = 0.0f;
+  int64_t row = ((int64_t)blockIdx.x * RPW + slot) * a.walk;
+  const int64_t end = min(row + a.walk, a.rows);
+  if (row >= end) return;   // the whole workgroup, or a wave that meets no barrier
+  // An 8-bit result's rows are gathered in LDS: their 16-byte chunks lie 512 bytes apart in
+  // memory, but those of neighbouring rows are neighbours, so a slot's rows leave together in
+  // runs of 16 walk bytes (stored row by row the lines left the L2 half filled:
+  // 16384 x 8192 took 206 to 320 us). Chunk c of the slot's row j is at (c (walk + 1) + j) 16
+  // (the odd stride spreads the banks), scales of granule half g at (g walk + j) 4 after them.
+  const int granules = (a.d + kKPad - 1) / kKPad, chunks = granules * 16;
+  const int64_t row0 = row;
+  extern __shared__ __attribute__((aligned(16))) char stage_all[];
+  char* stage = stage_all + slot * norm_stage_bytes(granules, a.walk);
+  char* stage_s = stage + chunks * (a.walk + 1) * 16;
+  Chunk<DT, VEC> x[C], res[C];
+  auto load = [&](int64_t r) {
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int i = (c * NT + t) * 8, n = a.d - i;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[c][e] = w[c][e] = 0.0f;
-    if (n > 0) {
-      load_chunk<DT, VEC>(a.x, rr * a.ldx + i, n, s[c]);
-      if (a.res) {
-        float q[8];
-        load_chunk<DT, VEC>(a.res, rr * a.ldr + i, n, q);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[c][e] = round_to<DT>(s[c][e] + q[e]);
+    for (int c = 0; c < C; ++c) {
+      const int i = (c * NT + t) * 8, n = a.d - i;
+      x[c].zero();
+      res[c].zero();
+      if (n > 0) {
+        x[c].load(a.x, r * a.ldx + i, n);
+        if (a.res) res[c].load(a.res, r * a.ldr + i, n);
       }
-      load_weight<DT, VEC>(a.w, a.wdt, i, n, w[c]);
-      if (a.sum && in) store_chunk<DT, VEC>(a.sum, rr * a.lds + i, n, s[c]);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sq = __builtin_fmaf(s[c][e], s[c][e], sq);
-  }
-  static_assert(NT == 64 || RPW == 1 || NT * RPW == 256, "");
-  const float r = rsqrtf(row_sum<NT>(sq, red + slot * (NT / 64), t) / (float)a.d + a.eps);
-  const int64_t granules = (a.d + kKPad - 1) / kKPad;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
+  };
+  float w[HOLD ? C : 1][8];
+  auto weight = [&](int c, float (&v)[8]) {
     const int i = (c * NT + t) * 8, n = a.d - i;
-    float y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = s[c][e] * r * w[c][e];
-    if (a.y && in && n > 0) store_chunk<DT, VEC>(a.y, rr * a.ldy + i, n, y);
-    if (a.codes) {
-      float m = 0.0f;
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    if (n > 0) load_weight<DT, VEC>(a.w, a.wdt, i, n, v);
+  };
+  if constexpr (HOLD) {
+    load(row);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = amax2(m, mag(y[e]));
-      const int sc = scale_of(amax_quad(m), FP8);
-      if (in && i < granules * kKPad) {
-        const i32x2 q = {(int)to_fp8x4(y[0], y[1], y[2], y[3], sc), (int)to_fp8x4(y[4], y[5], y[6], y[7], sc)};
-        *reinterpret_cast<i32x2*>(a.codes + ((row >> 5) * granules * 16 + i / 16) * 512 + (row & 31) * 16 + i % 16) = q;
-        if ((t & 3) == 0)
-          a.scales[((row >> 5) * granules + i / kKPad) * kScaleGranule + ((i / 32) & 1) * 128 + (row & 31) * 4 +
-                   (i / 64) % 4] = (char)sc;
+    for (int c = 0; c < C; ++c) weight(c, w[c]);
+  }
+  for (int par = 0; row < end; ++row, par ^= 1) {
+    if constexpr (!HOLD) load(row);
+    float s[C][8];
+    float sq = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s[c][e] = a.res ? round_to<DT>(x[c].get(e) + res[c].get(e)) : x[c].get(e);
+        sq = __builtin_fmaf(s[c][e], s[c][e], sq);
       }
+    if constexpr (HOLD) {
+      if (row + 1 < end) load(row + 1);
+    }
+    if (a.sum) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int i = (c * NT + t) * 8, n = a.d - i;
+        if (n > 0) store_chunk<DT, VEC>(a.sum, row * a.lds + i, n, s[c]);
+      }
+    }
+    sq = wave_sum(sq);
+    if constexpr (NT > 64) {
+      // two sets of words in turn, so that one barrier a row is enough
+      if ((t & 63) == 0) red[par][t >> 6] = sq;
+      __syncthreads();
+      sq = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NWV; ++i) sq += red[par][i];
+    }
+    const float r = rsqrtf(sq / (float)a.d + a.eps);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int i = (c * NT + t) * 8, n = a.d - i;
+      float y[8];
+      if constexpr (!HOLD) weight(c, w[0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = s[c][e] * r * w[HOLD ? c : 0][e];
+      if (a.y && n > 0) store_chunk<DT, VEC>(a.y, row * a.ldy + i, n, y);
+      if (a.codes) {
+        float m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = amax2(m, mag(y[e]));
+        const int sc = scale_of(amax_quad(m), FP8);
+        if (i < granules * kKPad) {
+          const int j = (int)(row - row0);
+          const i32x2 q = {(int)to_fp8x4(y[0], y[1], y[2], y[3], sc), (int)to_fp8x4(y[4], y[5], y[6], y[7], sc)};
+          *reinterpret_cast<i32x2*>(stage + (i / 16 * (a.walk + 1) + j) * 16 + i % 16) = q;
+          if ((t & 3) == 0) stage_s[((i / kKPad * 2 + ((i / 32) & 1)) * a.walk + j) * 4 + (i / 64) % 4] = (char)sc;
+        }
+      }
+    }
+  }
+  if (a.codes) {
+    if constexpr (NT > 64) __syncthreads();
+    else __builtin_amdgcn_wave_barrier();
+    const int rows = (int)(end - row0);
+    char* dc = a.codes + (row0 >> 5) * chunks * 512 + (row0 & 31) * 16;
+    for (int k = t; k < chunks * a.walk; k += NT) {
+      const int c = k / a.walk, j = k % a.walk;
+      if (j < rows)
+        *reinterpret_cast<i32x4*>(dc + c * 512 + j * 16) =
+            *reinterpret_cast<const i32x4*>(stage + (c * (a.walk + 1) + j) * 16);
+    }
+    char* ds = a.scales + (row0 >> 5) * granules * kScaleGranule + (row0 & 31) * 4;
+    for (int k = t; k < granules * 2 * a.walk; k += NT) {
+      const int g = k / a.walk, j = k % a.walk;
+      if (j < rows) *reinterpret_cast<int*>(ds + g * 128 + j * 4) = *reinterpret_cast<const int*>(stage_s + k * 4);
     }
   }
 }
@@ -189,44 +250,67 @@ struct NormBwdArgs {
   float eps;
 };
 
-// Each row slot walks the rows with the stride of all slots and keeps its share of dw in
-// registers; launch_bgrad_reduce then adds the slots in order (no atomics).
+// Each row slot walks the rows with the stride of all slots, the next row's loads in flight
+// while this one is summed, and keeps its share of dw in registers; norm_dweight_kernel then
+// adds the slots in order (no atomics).
 template <int DT, int NT, int C, bool VEC>
 __global__ __launch_bounds__(wg_of(NT)) void rms_norm_backward_kernel(NormBwdArgs a) {
   constexpr int RPW = wg_of(NT) / NT, NWV = NT / 64;
+  static_assert(NT == 64 || RPW == 1, "rows that share a workgroup share no barrier");
+  constexpr bool HOLD = NT * C <= 1024;   // registers for the next row and the weight (up to 8192 values)
   __shared__ float red[2][2][16];
   const int t = threadIdx.x % NT, slot = threadIdx.x / NT;
   const int64_t first = (int64_t)blockIdx.x * RPW + slot;
-  float w[C][8], dw[C][8];
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int i = (c * NT + t) * 8, n = a.d - i;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[c][e] = dw[c][e] = 0.0f;
-    if (n > 0) load_weight<DT, VEC>(a.w, a.wdt, i, n, w[c]);
-  }
-  // every slot of a workgroup takes the same number of steps (they share barriers)
-  int par = 0;
-  for (int64_t base = (int64_t)blockIdx.x * RPW; base < a.rows; base += a.slots, par ^= 1) {
-    const int64_t row = base + slot;
-    const bool in = row < a.rows;
-    const int64_t rr = in ? row : 0;
-    float s[C][8], g[C][8];
-    float sq = 0.0f, dot = 0.0f;
+  if (first >= a.slots) return;   // a wave that meets no barrier
+  Chunk<DT, VEC> sc[C], gc[C], rc[C];
+  auto load = [&](int64_t r) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = (c * NT + t) * 8, n = a.d - i;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[c][e] = g[c][e] = 0.0f;
+      sc[c].zero();
+      gc[c].zero();
+      rc[c].zero();
       if (n > 0) {
-        load_chunk<DT, VEC>(a.s, rr * a.lds + i, n, s[c]);
-        load_chunk<DT, VEC>(a.dy, rr * a.lddy + i, n, g[c]);
+        sc[c].load(a.s, r * a.lds + i, n);
+        gc[c].load(a.dy, r * a.lddy + i, n);
+        if (a.dres) rc[c].load(a.dres, r * a.lddr + i, n);
       }
+    }
+  };
+  float w[HOLD ? C : 1][8], dw[C][8];
+  auto weight = [&](int c, float (&v)[8]) {
+    const int i = (c * NT + t) * 8, n = a.d - i;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    if (n > 0) load_weight<DT, VEC>(a.w, a.wdt, i, n, v);
+  };
+  if constexpr (HOLD) load(first);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if constexpr (HOLD) weight(c, w[c]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[c][e] = 0.0f;
+  }
+  int par = 0;
+  for (int64_t row = first; row < a.rows; row += a.slots, par ^= 1) {
+    if constexpr (!HOLD) load(row);
+    // this row's values move out of the way of the next row's
+    Chunk<DT, VEC> s[C], g[C], o[C];
+    float sq = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      s[c] = sc[c];
+      g[c] = gc[c];
+      o[c] = rc[c];
+      if constexpr (!HOLD) weight(c, w[0]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        sq = __builtin_fmaf(s[c][e], s[c][e], sq);
-        dot = __builtin_fmaf(g[c][e] * w[c][e], s[c][e], dot);
+        sq = __builtin_fmaf(s[c].get(e), s[c].get(e), sq);
+        dot = __builtin_fmaf(g[c].get(e) * w[HOLD ? c : 0][e], s[c].get(e), dot);
       }
+    }
+    if constexpr (HOLD) {
+      if (row + a.slots < a.rows) load(row + a.slots);
     }
     sq = wave_sum(sq);
     dot = wave_sum(dot);
@@ -249,28 +333,58 @@ __global__ __launch_bounds__(wg_of(NT)) void rms_norm_backward_kernel(NormBwdArg
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = (c * NT + t) * 8, n = a.d - i;
-      if (n > 0 && in) {
-        float o[8], q[8];
-        if (a.dres) load_chunk<DT, VEC>(a.dres, rr * a.lddr + i, n, q);
+      if (n > 0) {
+        if constexpr (!HOLD) weight(c, w[0]);
+        float dx[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          o[e] = r * (g[c][e] * w[c][e] - s[c][e] * k);
-          if (a.dres) o[e] += q[e];
-          dw[c][e] = __builtin_fmaf(g[c][e], s[c][e] * r, dw[c][e]);
+          dx[e] = o[c].get(e) + r * (g[c].get(e) * w[HOLD ? c : 0][e] - s[c].get(e) * k);
+          dw[c][e] = __builtin_fmaf(g[c].get(e), s[c].get(e) * r, dw[c][e]);
         }
-        store_chunk<DT, VEC>(a.dx, rr * a.lddx + i, n, o);
+        store_chunk<DT, VEC>(a.dx, row * a.lddx + i, n, dx);
       }
     }
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int i = (c * NT + t) * 8, n = a.d - i;
-    if (n > 0 && first < a.slots) {
+    if (n > 0) {
       float* p = a.partial + first * a.d + i;
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (e < n) p[e] = dw[c][e];
     }
+  }
+}
+
+// dw[i] = sum over t of partial[t][i]: 16 waves take 64 columns, each a run of the slots with
+// 16 loads in flight, and their sums are added in wave order. (The bias gradient's second
+// pass has four waves for this; here the columns are few and the slots many: 512 x 8192
+// took 9.3 us with it.)
+constexpr int kDwWaves = 16, kDwBatch = 16;
+__global__ __launch_bounds__(64 * kDwWaves) void norm_dweight_kernel(const float* __restrict__ partial, int T, int d,
+                                                                     void* dw, int wdt) {
+  __shared__ float sums[kDwWaves][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int i = blockIdx.x * 64 + lane;
+  const int t0 = (int)((int64_t)T * w / kDwWaves), t1 = (int)((int64_t)T * (w + 1) / kDwWaves);
+  float s = 0.0f;
+  if (i < d) {
+    for (int t = t0; t < t1; t += kDwBatch) {
+      float v[kDwBatch];
+#pragma unroll
+      for (int j = 0; j < kDwBatch; ++j) v[j] = t + j < t1 ? partial[(int64_t)(t + j) * d + i] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < kDwBatch; ++j) s += v[j];
+    }
+  }
+  sums[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && i < d) {
+    float r = sums[0][lane];
+#pragma unroll
+    for (int q = 1; q < kDwWaves; ++q) r += sums[q][lane];
+    store_vec(dw, wdt, i, r);
   }
 }
 
@@ -297,9 +411,10 @@ const void* norm_bwd_fn(int d, int* nt) {
   };
 #define GE_NORM(N, C) return pick(N, reinterpret_cast<const void*>(&rms_norm_backward_kernel<DT, N, C, VEC>))
   if (d <= 512) GE_NORM(64, 1);
-  if (d <= 1024) GE_NORM(64, 2);
-  if (d <= 4096) GE_NORM(256, 2);
-  if (d <= 8192) GE_NORM(512, 2);
+  if (d <= 1024) GE_NORM(128, 1);
+  if (d <= 2048) GE_NORM(256, 1);
+  if (d <= 4096) GE_NORM(512, 1);
+  if (d <= 8192) GE_NORM(1024, 1);
   if (d <= 16384) GE_NORM(1024, 2);
   GE_NORM(1024, 4);
 #undef GE_NORM
@@ -324,7 +439,7 @@ ge_status_t gemm_epilog_rms_norm(int64_t rows, int64_t d, ge_dtype_t dt, const v
     return st;
   if (rows == 0) return GE_OK;
   gek::NormArgs a{x,   residual, weight, sum, y,   static_cast<char*>(codes), static_cast<char*>(scales), rows, ldx,
-                  ldr, lds,      ldy,    (int)d, (int)wdt, eps};
+                  ldr, lds,      ldy,    (int)d, (int)wdt, eps, 1};
   const size_t e = gemxh::esize(dt);
   const bool vec = d % 8 == 0 && gek::lines(x, ldx, e) && gek::lines(residual, residual ? ldr : 0, e) &&
                    gek::lines(sum, sum ? lds : 0, e) && gek::lines(y, y ? ldy : 0, e) && gek::lines(weight, 0, e);
@@ -334,11 +449,18 @@ ge_status_t gemm_epilog_rms_norm(int64_t rows, int64_t d, ge_dtype_t dt, const v
                                   : (vec ? gek::norm_fn<gek::BF16, true>(a.d, &nt)
                                          : gek::norm_fn<gek::BF16, false>(a.d, &nt));
   const int wg = gek::wg_of(nt), rpw = wg / nt;
-  int64_t grid = (rows + rpw - 1) / rpw;
-  if (codes) grid = (gemx::row_groups(rows) + 7) / 8 * 8 * (32 / rpw);
+  // rows one after the other: as many (up to 8) as leave the device 1024 workgroups and,
+  // with an 8-bit result, as fit 72 KB of LDS (two workgroups per compute unit)
+  const int granules = (int)((d + gemx::kKPad - 1) / gemx::kKPad);
+  while (a.walk < 8 && rows >= (int64_t)1024 * rpw * a.walk * 2 &&
+         (!codes || rpw * gek::norm_stage_bytes(granules, a.walk * 2) <= 76 * 1024))
+    a.walk *= 2;
+  const size_t stage = codes ? (size_t)rpw * gek::norm_stage_bytes(granules, a.walk) : 0;
+  const int per = rpw * a.walk;
+  const int64_t grid = (rows + per - 1) / per;
   if (grid * wg >= (int64_t(1) << 32)) return GE_ERR_NOT_SUPPORTED;
   void* params[] = {&a};
-  return hipLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)wg), params, 0, static_cast<hipStream_t>(stream)) ==
+  return hipLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)wg), params, stage, static_cast<hipStream_t>(stream)) ==
                  hipSuccess
              ? GE_OK
              : GE_ERR_HIP;
@@ -375,7 +497,11 @@ ge_status_t gemm_epilog_rms_norm_backward(int64_t rows, int64_t d, ge_dtype_t dt
     if (hipLaunchKernel(fn, dim3((unsigned)((slots + rpw - 1) / rpw)), dim3((unsigned)wg), params, 0, q) != hipSuccess)
       return GE_ERR_HIP;
   }
-  return gek::launch_bgrad_reduce(static_cast<float*>(workspace), (int)slots, d, dw, (int)wdt, q) == hipSuccess
+  const float* partial = static_cast<const float*>(workspace);
+  int T = (int)slots, width = (int)d, wt = (int)wdt;
+  void* params[] = {&partial, &T, &width, &dw, &wt};
+  return hipLaunchKernel(reinterpret_cast<const void*>(&gek::norm_dweight_kernel), dim3((unsigned)((d + 63) / 64)),
+                         dim3(64 * gek::kDwWaves), params, 0, q) == hipSuccess
              ? GE_OK
              : GE_ERR_HIP;
 }
