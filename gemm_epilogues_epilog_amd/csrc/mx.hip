@@ -27,7 +27,8 @@ const void* kernel_of(int cfg) {
     case MX_L: return reinterpret_cast<const void*>(&mx_tile_kernel<XF, MX_L, EXACT>);
     case MX_R128: return reinterpret_cast<const void*>(&mx_ring_kernel<XF, MX_R128, EXACT>);
     case MX_R64: return reinterpret_cast<const void*>(&mx_ring_kernel<XF, MX_R64, EXACT>);
-    case MX_S16: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 1, EXACT>);
+    case MX_S16: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 2, EXACT>);
+    case MX_S16N: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 1, EXACT>);
   }
   return nullptr;
 }
@@ -89,11 +90,11 @@ ge_status_t gemm_epilog_mx_plan_info(int64_t n, int64_t k, int64_t experts, ge_m
   const gemx::MxTile& T = gemx::kMxTiles[L.cfg];
   info->tile_m = T.bm;
   info->tile_n = T.bn;
-  info->waves = gemx::mx_waves(T);
+  info->waves = L.waves;
   info->stages = T.stages;
   info->splits = L.splits;
   info->tiles = m ? (int64_t)L.tiles_m * L.tiles_n : 0;
-  info->workgroups = m ? L.grid_x * L.grid_y : 0;
+  info->workgroups = m ? L.grid_x * L.grid_y * L.grid_z : 0;
   info->workspace_bytes = gemxh::workspace_bytes(n, k, experts, types, compute_units);
   return GE_OK;
 }
@@ -132,15 +133,15 @@ ge_status_t gemm_epilog_mx_execute(ge_mx_handle_t h, int64_t m, const void* x_co
   a.vec = (int32_t)h->t.vec;
   a.group_m = L.group_m;
   // a launch keeps its lane count below 2^32
-  if (L.grid_x * L.grid_y * gemx::mx_waves(gemx::kMxTiles[L.cfg]) * 64 >= (int64_t(1) << 32) || L.grid_y > 65535)
+  if (L.grid_x * L.grid_y * L.grid_z * L.waves * 64 >= (int64_t(1) << 32) || L.grid_y > 65535)
     return GE_ERR_NOT_SUPPORTED;
   const bool exact = h->t.d == GE_MX_D_F32 || h->t.d == GE_MX_D_MXFP8;   // see large_part
   const void* fn = h->t.x == GE_MXFP4 ? kernel_of<gemx::FP4, false>(L.cfg)
                    : exact            ? kernel_of<gemx::FP8, true>(L.cfg)
                                       : kernel_of<gemx::FP8, false>(L.cfg);
   void* params[] = {&a};
-  return hipLaunchKernel(fn, dim3((unsigned)L.grid_x, (unsigned)L.grid_y),
-                         dim3((unsigned)gemx::mx_waves(gemx::kMxTiles[L.cfg]) * 64), params, 0,
+  return hipLaunchKernel(fn, dim3((unsigned)L.grid_x, (unsigned)L.grid_y, (unsigned)L.grid_z),
+                         dim3((unsigned)L.waves * 64), params, 0,
                          static_cast<hipStream_t>(stream)) == hipSuccess
              ? GE_OK
              : GE_ERR_HIP;

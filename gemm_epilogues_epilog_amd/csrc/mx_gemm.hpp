@@ -415,17 +415,36 @@ __device__ __forceinline__ void mx_epilogue(const MxArgs& p, const MxPlace& at, 
           if (lhi == 0) mx_store_scale(p, row, c, s);
         }
       } else if (out == MX_OUT_F32) {
-        // 16 bytes a lane; the line of a row's 32 columns fills over four stores
-        if (keep) {
-          float* d = static_cast<float*>(p.D) + row * p.n + c + 4 * lhi;
-          if (vec_ok && c + 32 <= p.n) {
+        if (vec_ok && c + 32 <= p.n) {
+          // 16 bytes a lane; the line of a row's 32 columns fills over four stores
+          if (keep) {
+            float* d = static_cast<float*>(p.D) + row * p.n + c + 4 * lhi;
 #pragma unroll
             for (int g = 0; g < 4; ++g)
               *reinterpret_cast<f32x4*>(d + 8 * g) = f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
-          } else {
+          }
+        } else {
+          // unaligned rows: 16 rows at a time through scratch, so that 32 lanes store 32
+          // neighbouring values. 16-byte unit u of row r sits at unit u ^ (r & 7).
+          int l = lane;   // kept from being computed ahead: the accumulators need the registers
+          asm volatile("" : "+v"(l));
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            f32x4* t = reinterpret_cast<f32x4*>(scratch) + (l & 15) * 8;
+            if ((l >> 4 & 1) == half) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c + 8 * (i / 4) + 4 * lhi + i % 4 < p.n) d[8 * (i / 4) + i % 4] = v[i];
+              for (int g = 0; g < 4; ++g)
+                t[(2 * g + (l >> 5)) ^ (l & 7)] = f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+            }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll 2
+            for (int i = 0; i < 8; ++i) {
+              const int r = 2 * i + (l >> 5), u = l & 31, cc = c + u;
+              const float y = reinterpret_cast<const float*>(scratch)[r * 32 + (((u >> 2) ^ (r & 7)) << 2) + (u & 3)];
+              const int64_t rw = r0 + half * 16 + r;
+              if (rw >= at.lo && rw < at.hi && cc < p.n) static_cast<float*>(p.D)[rw * p.n + cc] = y;
+            }
+            __builtin_amdgcn_wave_barrier();
           }
         }
       } else {
@@ -441,22 +460,27 @@ __device__ __forceinline__ void mx_epilogue(const MxArgs& p, const MxPlace& at, 
           t[(2 * g + lhi) ^ (lrow & 7)] = u;
         }
         __builtin_amdgcn_wave_barrier();
+        if (vec_ok) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = i * 16 + (lane >> 2), cc = c + (lane & 3) * 8;
-          const i32x2* q = reinterpret_cast<const i32x2*>(scratch) + r * 8;
-          const i32x2 lo = q[(2 * (lane & 3)) ^ (r & 7)], hi = q[(2 * (lane & 3) + 1) ^ (r & 7)];
-          const int64_t rw = r0 + r;
-          if (rw >= at.lo && rw < at.hi && cc < p.n) {
-            uint16_t* d = static_cast<uint16_t*>(p.D) + rw * p.n + cc;
-            if (vec_ok) {
-              *reinterpret_cast<i32x4*>(d) = i32x4{lo[0], lo[1], hi[0], hi[1]};
-            } else {
-              const int w4[4] = {lo[0], lo[1], hi[0], hi[1]};
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (cc + e < p.n) d[e] = (uint16_t)((uint32_t)w4[e / 2] >> (16 * (e & 1)));
-            }
+          for (int i = 0; i < 2; ++i) {
+            const int r = i * 16 + (lane >> 2), cc = c + (lane & 3) * 8;
+            const i32x2* q = reinterpret_cast<const i32x2*>(scratch) + r * 8;
+            const i32x2 lo = q[(2 * (lane & 3)) ^ (r & 7)], hi = q[(2 * (lane & 3) + 1) ^ (r & 7)];
+            const int64_t rw = r0 + r;
+            if (rw >= at.lo && rw < at.hi && cc < p.n)
+              *reinterpret_cast<i32x4*>(static_cast<uint16_t*>(p.D) + rw * p.n + cc) = i32x4{lo[0], lo[1], hi[0], hi[1]};
+          }
+        } else {
+          // unaligned rows: 32 lanes store 32 neighbouring values
+          int l = lane;   // as above
+          asm volatile("" : "+v"(l));
+#pragma unroll 2
+          for (int i = 0; i < 16; ++i) {
+            const int r = 2 * i + (l >> 5), u = l & 31, cc = c + u;
+            const uint16_t y =
+                reinterpret_cast<const uint16_t*>(scratch)[r * 32 + (((u >> 2) ^ (r & 7)) << 2) + (u & 3)];
+            const int64_t rw = r0 + r;
+            if (rw >= at.lo && rw < at.hi && cc < p.n) static_cast<uint16_t*>(p.D)[rw * p.n + cc] = y;
           }
         }
         __builtin_amdgcn_wave_barrier();
@@ -865,8 +889,8 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * MxCfgT<XF, CFG>::KG * 64), 1
 }
 
 // ---- skinny kernel -----------------------------------------------------------------
-// Few rows: bound by reading W once. A workgroup takes 32 rows of W and up to 16 TB rows
-// of X; its eight waves split k, stream W from memory straight into registers (16 bytes a
+// Few rows: bound by reading W once. A workgroup takes 16 FB rows of W and up to 16 rows
+// of X at a time; its eight waves split k, stream W from memory straight into registers (16 bytes a
 // lane, consecutive lines) and add their sums through LDS in wave order. 16x16x128
 // products: lane l holds row l % 16 and the 32 k of quarter l / 16 of a 128-k step.
 // Rows of X are addressed one by one, so an expert's rows may start anywhere.
@@ -882,66 +906,90 @@ __device__ __forceinline__ f32x4 mx_mma16(i32x4 w, const i32x4 (&x)[XF == FP8 ? 
   }
 }
 
-template <int XF, int TB, bool EXACT>
-__global__ __launch_bounds__(512, 1) void mx_skinny_kernel(MxArgs p) {
-  constexpr int FB = 2, NW = 8, XR = XF == FP8 ? 2 : 1;
+// A batch of U steps of 128 k is loaded whole before its products; the next batch's loads
+// are on their way meanwhile.
+template <int XF, int FB>
+struct MxSteps {
+  static constexpr int U = 1, XR = XF == FP8 ? 2 : 1;
+  i32x4 w[U][FB], x[U][XR];
+  int sw[U][FB], sx[U];
+};
+
+constexpr int kPastRange = 0x7fffffff;   // rsrc()'s range
+
+template <int XF, int FB, bool EXACT>
+__global__ __launch_bounds__(512, 4) void mx_skinny_kernel(MxArgs p) {
+  constexpr int XR = XF == FP8 ? 2 : 1;
+  const int nw = blockDim.x >> 6;
   constexpr int ROW = FB * 16 + 4;   // floats per finished row
-  __shared__ __attribute__((aligned(16))) f32x4 red[NW][FB * TB][64];
-  __shared__ __attribute__((aligned(16))) float fin[TB * 16][ROW];
+  __shared__ __attribute__((aligned(16))) f32x4 red[kMxSkinnyWaves][FB][64];
+  __shared__ __attribute__((aligned(16))) float fin[16][ROW];
   const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = p.experts ? blockIdx.y : 0;
   int64_t lo = 0, hi = p.m;
   if (p.experts) expert_rows(p, e, lo, hi);
-  const int fg = blockIdx.x;   // W row group
+  const int c0 = blockIdx.x * (FB * 16), fg = c0 >> 5;   // first row of W, its row group
   const int64_t gw = group_code_bytes(FP4, p.k), gx = group_code_bytes(XF, p.k), gs = group_scale_bytes(p.k);
   const int64_t wrg = row_groups(p.n);
   const bool has_w = fg < wrg;   // columns past the last group only pad an e4m3 result
-  const char* wc = p.wc + (e * wrg + (has_w ? fg : 0)) * gw + g * 512 + li * 16;
-  const char* ws = p.ws + (e * wrg + (has_w ? fg : 0)) * gs + (g & 1) * 128 + li * 4;
   const int steps = has_w ? p.kt * 2 : 0;
-  const int s0 = steps * w / NW, s1 = steps * (w + 1) / NW;
-
-  for (int64_t r0 = lo; r0 < hi; r0 += TB * 16) {
-    const char* xc[TB];
-    const char* xs[TB];
-    bool xin[TB];
+  const int s0 = steps * w / nw, s1 = steps * (w + 1) / nw;
+  const __amdgpu_buffer_rsrc_t rw = rsrc(p.wc + (e * wrg + (has_w ? fg : 0)) * gw), rws = rsrc(p.ws + (e * wrg + (has_w ? fg : 0)) * gs);
+  const int lw = g * 512 + (c0 % 32 + li) * 16, lws = (g & 1) * 128 + (c0 % 32 + li) * 4;
+  using Steps = MxSteps<XF, FB>;
+  constexpr int U = Steps::U;
+  // The first FB waves finish the sums, four columns a lane. Their bias is read here as it
+  // lies (an fp32 value in two halves), so that nothing waits for it before the end; past n
+  // and without a bias the range gives zeros.
+  const bool finish = w < FB;
+  const int vs = p.vec == F32 ? 4 : 2;
+  uint16_t b_lo[4] = {}, b_hi[4] = {};
+  if (finish) {
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(static_cast<const char*>(p.bias)) + (int64_t)e * p.n * vs, 0, p.ep != NONE ? p.n * vs : 0, kBufDword3);
 #pragma unroll
-    for (int b = 0; b < TB; ++b) {
-      const int64_t row = r0 + b * 16 + li;
-      xin[b] = row < hi;
-      const int64_t rr = xin[b] ? row : lo;
-      xc[b] = p.xc + (rr >> 5) * gx + (rr & 31) * 16 + g * 512;
-      xs[b] = p.xs + (rr >> 5) * gs + (rr & 31) * 4 + (g & 1) * 128;
+    for (int j = 0; j < 4; ++j) {
+      const int at = (c0 + w * 16 + 4 * g + j) * vs;
+      b_lo[j] = __builtin_amdgcn_raw_buffer_load_b16(rb, at, 0, 0);
+      b_hi[j] = __builtin_amdgcn_raw_buffer_load_b16(rb, at + 2, 0, 0);
     }
-    f32x4 acc[FB][TB];
+  }
+
+  for (int64_t r0 = lo + (int64_t)blockIdx.z * 16; r0 < hi; r0 += (int64_t)gridDim.z * 16) {
+    // Lanes past the last row read the first one again: a row of X is a column of the
+    // products, and theirs is not stored.
+    const int64_t rr = r0 + li < hi ? r0 + li : r0;
+    const __amdgpu_buffer_rsrc_t rx = rsrc(p.xc + (r0 >> 5) * gx), rxs = rsrc(p.xs + (r0 >> 5) * gs);
+    const int rg = (int)((rr >> 5) - (r0 >> 5));   // the rows lie in one row group or two
+    const int lx = rg * (int)gx + (int)(rr & 31) * 16 + g * 512, lxs = rg * (int)gs + (int)(rr & 31) * 4 + (g & 1) * 128;
+    f32x4 acc[FB];
 #pragma unroll
-    for (int f = 0; f < FB; ++f)
+    for (int f = 0; f < FB; ++f) acc[f] = f32x4{0, 0, 0, 0};
+    const auto load = [&](Steps& b, int s) {
 #pragma unroll
-      for (int b = 0; b < TB; ++b) acc[f][b] = f32x4{0, 0, 0, 0};
-#pragma unroll 4
-    for (int s = s0; s < s1; ++s) {
-      // byte of the scale dword: block 4 (s % 2) + g of the granule
-      const int sh = 16 * (s & 1) + 8 * (g >> 1);
-      i32x4 wf[FB];
-      int sw[FB];
+      for (int u = 0; u < U; ++u) {
+        // steps past the wave's last one lie past the buffers' range: zeros, and no reads
+        const int t = s + u, past = t < s1 ? 0 : kPastRange, ts = past | (t >> 1) * kScaleGranule;
 #pragma unroll
-      for (int f = 0; f < FB; ++f) {
-        wf[f] = *reinterpret_cast<const i32x4*>(wc + (int64_t)s * 2048 + f * 256);
-        sw[f] = *reinterpret_cast<const int*>(ws + (int64_t)(s >> 1) * kScaleGranule + f * 64) >> sh;
-      }
-#pragma unroll
-      for (int b = 0; b < TB; ++b) {
-        i32x4 xf[XR];
-        int sx = 0;
-#pragma unroll
-        for (int h = 0; h < XR; ++h) xf[h] = i32x4{0, 0, 0, 0};
-        if (xin[b]) {
-#pragma unroll
-          for (int h = 0; h < XR; ++h)
-            xf[h] = *reinterpret_cast<const i32x4*>(xc[b] + (int64_t)s * (2048 * XR) + h * 2048);
-          sx = *reinterpret_cast<const int*>(xs[b] + (int64_t)(s >> 1) * kScaleGranule) >> sh;
+        for (int f = 0; f < FB; ++f) {
+          b.w[u][f] = __builtin_amdgcn_raw_buffer_load_b128(rw, lw + f * 256 + (past | t * 2048), 0, 0);
+          b.sw[u][f] = __builtin_amdgcn_raw_buffer_load_b32(rws, lws + f * 64 + ts, 0, 0);
         }
+#pragma unroll
+        for (int h = 0; h < XR; ++h)
+          b.x[u][h] = __builtin_amdgcn_raw_buffer_load_b128(rx, lx + h * 2048 + (past | t * (2048 * XR)), 0, 0);
+        b.sx[u] = __builtin_amdgcn_raw_buffer_load_b32(rxs, lxs + ts, 0, 0);
+      }
+    };
+    const auto multiply = [&](const Steps& b, int s) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        // byte of the scale dword: block 4 (s % 2) + g of the granule
+        const int sh = 16 * ((s + u) & 1) + 8 * (g >> 1);
+        i32x4 xf[XR];
+#pragma unroll
+        for (int h = 0; h < XR; ++h) xf[h] = b.x[u][h];
         if constexpr (EXACT) {
           i32x4 xl[XR];
 #pragma unroll
@@ -950,37 +998,48 @@ __global__ __launch_bounds__(512, 1) void mx_skinny_kernel(MxArgs p) {
             xf[h] ^= xl[h];
           }
 #pragma unroll
-          for (int f = 0; f < FB; ++f) acc[f][b] = mx_mma16<XF, 0>(wf[f], xl, acc[f][b], sw[f], sx);
+          for (int f = 0; f < FB; ++f) acc[f] = mx_mma16<XF, 0>(b.w[u][f], xl, acc[f], b.sw[u][f] >> sh, b.sx[u] >> sh);
         }
 #pragma unroll
-        for (int f = 0; f < FB; ++f) acc[f][b] = mx_mma16<XF, 0>(wf[f], xf, acc[f][b], sw[f], sx);
+        for (int f = 0; f < FB; ++f) acc[f] = mx_mma16<XF, 0>(b.w[u][f], xf, acc[f], b.sw[u][f] >> sh, b.sx[u] >> sh);
       }
+    };
+    Steps b0, b1;
+    load(b0, s0);
+    for (int s = s0; s < s1; s += 2 * U) {
+      load(b1, s + U);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(b0, s);
+      load(b0, s + 2 * U);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(b1, s + U);
     }
 #pragma unroll
-    for (int f = 0; f < FB; ++f)
-#pragma unroll
-      for (int b = 0; b < TB; ++b) red[w][f * TB + b][lane] = acc[f][b];
+    for (int f = 0; f < FB; ++f) red[w][f][lane] = acc[f];
     __syncthreads();
-    for (int q = threadIdx.x; q < FB * TB * 64; q += NW * 64) {
-      const int fb = q >> 6, l = q & 63, f = fb / TB, b = fb % TB;
-      f32x4 v = red[0][fb][l];
-#pragma unroll
-      for (int i = 1; i < NW; ++i) {
-        const f32x4 u = red[i][fb][l];
+    if (finish) {
+      const int f = w, l = lane;
+      f32x4 v = red[0][f][l];
+#pragma unroll 4
+      for (int i = 1; i < nw; ++i) {
+        const f32x4 u = red[i][f][l];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] += u[j];
       }
       const int c = f * 16 + 4 * (l >> 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int col = fg * 32 + c + j;
-        const float y = mx_act(v[j] + mx_bias(p, e, col), p.ep);
-        fin[b * 16 + (l & 15)][c + j] = col < p.n ? y : 0.0f;
+        const float bias = p.vec == F32   ? __uint_as_float(b_lo[j] | (uint32_t)b_hi[j] << 16)
+                           : p.vec == F16 ? Tr<F16>::widen(b_lo[j])
+                                          : Tr<BF16>::widen(b_lo[j]);
+        const int col = c0 + c + j;
+        const float y = mx_act(v[j] + bias, p.ep);
+        fin[l & 15][c + j] = col < p.n ? y : 0.0f;
       }
     }
     __syncthreads();
-    if (p.out == MX_OUT_FP8) {
-      if (threadIdx.x < TB * 16 && r0 + threadIdx.x < hi) {
+    if (FB == 2 && p.out == MX_OUT_FP8) {
+      if (threadIdx.x < 16 && r0 + threadIdx.x < hi) {
         const int t = threadIdx.x;
         float m = 0.0f;
         for (int c = 0; c < 32; ++c) m = amax2(m, mag(fin[t][c]));
@@ -990,18 +1049,18 @@ __global__ __launch_bounds__(512, 1) void mx_skinny_kernel(MxArgs p) {
           i32x4 o;
 #pragma unroll
           for (int q = 0; q < 4; ++q) o[q] = (int)to_fp8x4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3], s);
-          mx_store_chunk(p, r0 + t, fg * 32 + 16 * h, o);
+          mx_store_chunk(p, r0 + t, c0 + 16 * h, o);
         }
-        mx_store_scale(p, r0 + t, fg * 32, s);
+        mx_store_scale(p, r0 + t, c0, s);
       }
     } else {
       const bool vec_ok = mx_vec_ok(p);
-      const int t = threadIdx.x >> 2, c = (threadIdx.x & 3) * 8;
-      if (t < TB * 16 && r0 + t < hi) {
+      const int t = threadIdx.x / (FB * 2), c = threadIdx.x % (FB * 2) * 8;
+      if (t < 16 && r0 + t < hi) {
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = fin[t][c + j];
-        mx_store8(p, r0 + t, fg * 32 + c, v, vec_ok);
+        mx_store8(p, r0 + t, c0 + c, v, vec_ok);
       }
     }
     __syncthreads();

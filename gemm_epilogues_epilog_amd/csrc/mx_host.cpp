@@ -100,11 +100,23 @@ MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t 
   int force = -1;
   if (const char* e = std::getenv("GE_MX_CFG")) force = std::atoi(e);
   if (force >= 0 ? force == MX_S16 : rows <= 16) {
-    L.cfg = MX_S16;
-    L.tiles_n = (int)((cols + kMxTiles[MX_S16].bn - 1) / kMxTiles[MX_S16].bn);
+    L.cfg = t.d != GE_MX_D_MXFP8 && (cols + 31) / 32 * groups < cus ? MX_S16N : MX_S16;
+    L.tiles_n = (int)((cols + kMxTiles[L.cfg].bn - 1) / kMxTiles[L.cfg].bn);
     L.tiles_m = (int)groups;
     L.grid_x = L.tiles_n;
     L.grid_y = groups;
+    // two workgroups share an expert's rows, sixteen each at a time: a skewed router gives
+    // some experts several times the even share (m 320, n 1148, k 192, 16 experts: 8.4 us,
+    // one workgroup 10.7, eight 9.7; 512 x 2048 x 1024 over 64: 23.2, 21.0 and 26.5)
+    L.grid_z = experts && m > 16 ? 2 : 1;
+    // Waves by the 128-k steps there are: with workgroups to spare eight steps or more to
+    // each, as a wave's start costs as much as some steps (32 experts of 1376 x 4096, 48 rows:
+    // two waves 12.1 us, four 11.8, eight 12.8; 64 of 2048 x 1024, 512 rows: 15, 19, 36);
+    // otherwise two, to have the reads of k on their way together (4096 x 11008, one row:
+    // 15, 10.6, 9.0).
+    const int64_t steps = pad_to(k, kKPad) / 128;
+    L.waves = (int)std::max<int64_t>(
+        2, std::min<int64_t>(kMxSkinnyWaves, steps / (L.grid_x * L.grid_y * L.grid_z > cus ? 8 : 2)));
     return L;
   }
   // Estimated microseconds of each configuration: rounds of workgroups over the compute
@@ -137,6 +149,7 @@ MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t 
     }
   }
   if (const char* e = std::getenv("GE_MX_SPLIT"); e && L.cfg != MX_L && !experts) L.splits = std::atoi(e);
+  L.waves = mx_waves(kMxTiles[L.cfg]);
   const int64_t tiles = (int64_t)L.tiles_m * L.tiles_n;
   // the persistent kernel: one workgroup per compute unit
   L.grid_x = L.cfg == MX_L ? std::min<int64_t>(tiles, cus) : tiles * L.splits;

@@ -34,8 +34,9 @@ struct MxLaunch {
   int cfg = 0;               // gemx::MxCfg
   int tiles_m = 0, tiles_n = 0;   // grouped: the most tiles of rows there can be
   int splits = 1;
+  int waves = 0;             // of a workgroup
   int group_m = 8;
-  int64_t grid_x = 0, grid_y = 1;
+  int64_t grid_x = 0, grid_y = 1, grid_z = 1;
 };
 MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t t, int cus);
 // Workspace that covers every m: the split tiles' counters and partial sums.

@@ -101,8 +101,10 @@ __global__ __launch_bounds__(256) void mx_quantize_rows_kernel(QuantArgs a) {
 
 // Rows that lie next to each other in memory (row_stride 1): a workgroup takes 128 rows by
 // 256 k, each of its eight waves one block of 32 k; a lane takes two neighbouring rows, so
-// a wave reads 128 rows of one k at a time (256 or 512 consecutive bytes, 32 reads in
-// flight). One row per lane of a half-wave took 13.5 us for 1000 x 2048 f16, this 4.
+// a wave reads 128 rows of one k at a time (256 or 512 consecutive bytes). Bound by the
+// memory: with the 32 reads of a lane in flight together 16384 x 8192 bf16 takes 81 us
+// (5.0 TB/s read and written; with a branch between the reads 83, and 1000 x 2048 f16
+// went from 13 us to 6).
 constexpr int kColRows = 128;
 template <int DT, int FMT>
 __global__ __launch_bounds__(512) void mx_quantize_cols_kernel(QuantArgs a) {
@@ -113,34 +115,36 @@ __global__ __launch_bounds__(512) void mx_quantize_cols_kernel(QuantArgs a) {
   const int64_t kt = blockIdx.x / tiles, row0 = blockIdx.x % tiles * kColRows;
   const int lane = threadIdx.x & 63, b = threadIdx.x >> 6, r = 2 * lane;
   const int64_t k0 = kt * kKPad + b * 32;
-  const int left = (int)min((int64_t)32, a.k - k0);          // values of this block
-  const int have = (int)min((int64_t)2, a.rows - row0 - r);   // of this lane's rows
+  const int left = (int)min((int64_t)32, a.k - k0);   // values of this block (none past k)
+  // Lanes past the last row read the last two, and the k past the last one read it again, so
+  // that no branch parts the loads; what they read is replaced by zeros. Row r + h is value
+  // h + skip of the pair.
+  const int64_t at = min(row0 + r, a.rows - 2);
+  const int skip = (int)min((int64_t)2, row0 + r - at);
   struct Pair {   // two rows' values at one k, in whatever alignment
     char bytes[2 * ES];
   };
   Pair raw[32];
-  const char* p = static_cast<const char*>(a.src) + (row0 + r + k0 * a.col_stride) * ES;
+  const char* p = static_cast<const char*>(a.src) + (at + min(k0, a.k - 1) * a.col_stride) * ES;
 #pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    __builtin_memset(&raw[e], 0, sizeof(Pair));
-    if (e < left) {
-      if (have == 2) __builtin_memcpy(&raw[e], p + e * a.col_stride * ES, 2 * ES);
-      else if (have == 1) __builtin_memcpy(&raw[e], p + e * a.col_stride * ES, ES);
-    }
-  }
+  for (int e = 0; e < 32; ++e)
+    __builtin_memcpy(&raw[e], p + min(e, max(left - 1, 0)) * a.col_stride * ES, 2 * ES);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float v[32];
     float m = 0.0f;
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
+      float x[2];
       if constexpr (DT == F32) {
-        __builtin_memcpy(&v[e], raw[e].bytes + h * 4, 4);
+        __builtin_memcpy(x, raw[e].bytes, 8);
       } else {
-        uint16_t x;
-        __builtin_memcpy(&x, raw[e].bytes + h * 2, 2);
-        v[e] = Tr<DT>::widen(x);
+        uint16_t u[2];
+        __builtin_memcpy(u, raw[e].bytes, 4);
+        x[0] = Tr<DT>::widen(u[0]);
+        x[1] = Tr<DT>::widen(u[1]);
       }
+      v[e] = e < left && h + skip < 2 ? (h + skip ? x[1] : x[0]) : 0.0f;
       m = amax2(m, mag(v[e]));
     }
     const int s = scale_of(m, FMT);
@@ -323,7 +327,7 @@ ge_status_t gemm_epilog_mx_quantize(int64_t rows, int64_t k, ge_dtype_t dt, cons
                    gemx::pad_to(k, gemx::kKPad) / gemx::kKPad};
   // Rows next to each other (k strided) go to the kernel whose lanes run along the rows:
   // reading them along k would touch a line per value.
-  const bool cols = col_stride != 1 && row_stride == 1;
+  const bool cols = col_stride != 1 && row_stride == 1 && rows > 1;
   const bool vec = col_stride == 1 && k % 8 == 0 && row_stride * (int64_t)es % 16 == 0 &&
                    reinterpret_cast<uintptr_t>(src) % 16 == 0;
   const void* fn = dt == GE_F32   ? gek::quantize_fn<gek::F32>(fmt, cols, vec)

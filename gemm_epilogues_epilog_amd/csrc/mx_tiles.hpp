@@ -13,18 +13,20 @@ namespace gemx {
 //   MX_L: persistent tile kernel, waves of 32 mb x 32 nb, two large stages: large products.
 //   MX_R: ring kernel, many small stages, k shared by several workgroups where the tiles are
 //     fewer than the compute units: a few dozen to a few thousand rows.
-//   MX_S16: skinny kernel (stages 0), eight waves that split k and read W straight into
-//     registers: up to 16 rows.
+//   MX_S16, MX_S16N: skinny kernel (stages 0), eight waves that split k and read W straight
+//     into registers: up to 16 rows.
 // kg: groups of waves, each with every kg-th k-tile (their sums are added through LDS).
 struct MxTile {
   int bm, bn, mb, nb, stages, kg;
 };
-enum MxCfg { MX_L = 0, MX_R128, MX_R64, MX_S16, MX_COUNT };
+enum MxCfg { MX_L = 0, MX_R128, MX_R64, MX_S16, MX_S16N, MX_COUNT };
 constexpr MxTile kMxTiles[MX_COUNT] = {
-    {256, 256, 2, 4, 2, 1}, {128, 64, 1, 2, 3, 2}, {64, 64, 1, 1, 4, 2}, {16, 32, 0, 0, 0, 1}};
-constexpr bool mx_is_skinny(int c) { return c == MX_S16; }
+    {256, 256, 2, 4, 2, 1}, {128, 64, 1, 2, 3, 2}, {64, 64, 1, 1, 4, 2}, {16, 32, 0, 0, 0, 1},
+    {16, 16, 0, 0, 0, 1}};
+constexpr bool mx_is_skinny(int c) { return c >= MX_S16; }
 constexpr bool mx_is_ring(int c) { return c == MX_R128 || c == MX_R64; }
-constexpr int mx_waves(const MxTile& t) { return t.stages ? (t.bm / 32 / t.mb) * (t.bn / 32 / t.nb) * t.kg : 8; }
+constexpr int mx_waves(const MxTile& t) { return (t.bm / 32 / t.mb) * (t.bn / 32 / t.nb) * t.kg; }
+constexpr int kMxSkinnyWaves = 8;   // at most
 // k values of one LDS stage: 128 bytes of a row of X.
 constexpr int mx_bk(int xfmt) { return xfmt == FP4 ? 256 : 128; }
 
