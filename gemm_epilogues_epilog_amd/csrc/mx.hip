@@ -65,7 +65,7 @@ ge_status_t gemm_epilog_mx_plan(int64_t n, int64_t k, int64_t experts, ge_mx_typ
   h->t = types;
   h->ep = ep;
   h->cus = prop.multiProcessorCount > 0 ? prop.multiProcessorCount : 256;
-  h->ws_bytes = gemxh::workspace_bytes(n, k, experts, types, h->cus);
+  h->ws_bytes = gemxh::workspace_bytes(experts, h->cus);
   if (h->ws_bytes) {
     if (hipMalloc(&h->ws, h->ws_bytes) != hipSuccess) {
       delete h;
@@ -95,7 +95,7 @@ ge_status_t gemm_epilog_mx_plan_info(int64_t n, int64_t k, int64_t experts, ge_m
   info->splits = L.splits;
   info->tiles = m ? (int64_t)L.tiles_m * L.tiles_n : 0;
   info->workgroups = m ? L.grid_x * L.grid_y * L.grid_z : 0;
-  info->workspace_bytes = gemxh::workspace_bytes(n, k, experts, types, compute_units);
+  info->workspace_bytes = gemxh::workspace_bytes(experts, compute_units);
   return GE_OK;
 }
 

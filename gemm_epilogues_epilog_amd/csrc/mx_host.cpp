@@ -2,7 +2,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 
 #include "mx_tiles.hpp"
 
@@ -91,74 +90,84 @@ ge_status_t check_execute(int64_t m, int64_t experts, ge_mx_types_t t, ge_epilog
   return GE_OK;
 }
 
+// Estimated microseconds of each configuration; the least wins. The constants come from
+// measurements (X e2m1; e4m3; e4m3 in two parts); `experts` products are estimated with three
+// experts in four used, and half a tile of each left empty.
 MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t t, int cus) {
   using namespace gemx;
   MxLaunch L;
   const int64_t cols = t.d == GE_MX_D_MXFP8 ? pad_to(n, kKPad) : n;   // an 8-bit D is written with its padding
   const int64_t groups = experts ? experts : 1;
-  const int64_t rows = (m + groups - 1) / groups;   // of an even share
-  int force = -1;
-  if (const char* e = std::getenv("GE_MX_CFG")) force = std::atoi(e);
-  if (force >= 0 ? force == MX_S16 : rows <= 16) {
-    L.cfg = t.d != GE_MX_D_MXFP8 && (cols + 31) / 32 * groups < cus ? MX_S16N : MX_S16;
-    L.tiles_n = (int)((cols + kMxTiles[L.cfg].bn - 1) / kMxTiles[L.cfg].bn);
+  const auto over = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+
+  // Skinny kernel: the workgroups' work over the device, or one workgroup's way through its
+  // rows, sixteen at a time, whichever is longer.
+  double best;
+  {
+    const int64_t steps = pad_to(k, kKPad) / 128, sixteens = std::max<int64_t>(1, over(m, 16));
+    // 16 columns each where 32 leave compute units idle (4096 x 11008, one row: 11.2 us, 9.0)
+    L.cfg = t.d != GE_MX_D_MXFP8 && over(cols, 32) * groups < cus ? MX_S16N : MX_S16;
+    L.tiles_n = (int)over(cols, kMxTiles[L.cfg].bn);
     L.tiles_m = (int)groups;
     L.grid_x = L.tiles_n;
     L.grid_y = groups;
-    // two workgroups share an expert's rows, sixteen each at a time: a skewed router gives
-    // some experts several times the even share (m 320, n 1148, k 192, 16 experts: 8.4 us,
-    // one workgroup 10.7, eight 9.7; 512 x 2048 x 1024 over 64: 23.2, 21.0 and 26.5)
-    L.grid_z = experts && m > 16 ? 2 : 1;
-    // Waves by the 128-k steps there are: with workgroups to spare eight steps or more to
-    // each, as a wave's start costs as much as some steps (32 experts of 1376 x 4096, 48 rows:
-    // two waves 12.1 us, four 11.8, eight 12.8; 64 of 2048 x 1024, 512 rows: 15, 19, 36);
-    // otherwise two, to have the reads of k on their way together (4096 x 11008, one row:
-    // 15, 10.6, 9.0).
-    const int64_t steps = pad_to(k, kKPad) / 128;
+    // Workgroups that share an expert's rows: two, as a skewed router gives some experts
+    // several times the even share (m 320, n 1148, k 192, 16 experts: 8.4 us, one workgroup
+    // 10.7, eight 9.7; 512 x 2048 x 1024 over 64: 23.2, 21.0 and 26.5), more where the
+    // device has room.
+    L.grid_z = std::min<int64_t>({sixteens, 64, std::max<int64_t>(experts ? 2 : 1, 2 * cus / (L.grid_x * groups))});
+    // Waves by the 128-k steps there are: with workgroups to spare six or eight steps to each,
+    // as a wave's start costs as much as some steps (32 experts of 1376 x 4096, 48 rows: two
+    // waves 12.1 us, four 11.8, eight 12.8; 64 of 2048 x 1024, 512 rows: 15, 19, 36; 6144 x
+    // 4096, one row: 7.6, 6.0, 6.4); otherwise two, to have the reads of k on their way
+    // together (4096 x 11008, one row: 15, 10.6, 9.0).
+    const int64_t wgs = L.grid_x * groups * L.grid_z;
     L.waves = (int)std::max<int64_t>(
-        2, std::min<int64_t>(kMxSkinnyWaves, steps / (L.grid_x * L.grid_y * L.grid_z > cus ? 8 : 2)));
-    return L;
+        2, std::min<int64_t>(kMxSkinnyWaves, steps / (wgs > 4 * cus ? 8 : wgs > cus ? 6 : 2)));
+    const double work = 1.0 + 0.36e-3 * (double)over(cols, 32) * ((double)m / 16 + 0.5 * (double)groups) * (double)steps;
+    // (an expert may have four times the even share)
+    const int64_t most = experts ? std::min(sixteens, over(4 * sixteens, groups)) : sixteens;
+    const double way = (double)over(most, L.grid_z) * (1.0 + 0.5 * (double)over(steps, L.waves));
+    best = 2.0 + std::max(work, way);
   }
-  // Estimated microseconds of each configuration: rounds of workgroups over the compute
-  // units, each so many k-tiles and a fixed part (start, epilogue, joining parts of k),
-  // from measurements at one full round (X e2m1; e4m3; e4m3 in two parts).
+
+  // Tile kernels: rounds of workgroups over the compute units, each so many k-tiles and a
+  // fixed part (start, epilogue, joining parts of k).
   static constexpr double kPerTile[3][3] = {{1.55, 1.2, 2.1}, {0.34, 0.26, 0.42}, {0.19, 0.17, 0.33}};
   static constexpr double kFixed[3] = {3.0, 5.5, 4.6};
   const int kind = t.x == GE_MXFP4 ? 0 : (t.d == GE_MX_D_F32 || t.d == GE_MX_D_MXFP8) ? 2 : 1;
   const int64_t kt = pad_to(k, kKPad) / mx_bk((int)t.x);
-  double best = 0;
   for (int cfg = MX_L; cfg <= MX_R64; ++cfg) {
-    if (force >= 0 && cfg != force) continue;
     const MxTile& T = kMxTiles[cfg];
-    const int64_t tm = experts ? (m + 31 * experts) / T.bm + experts : (m + T.bm - 1) / T.bm;
-    const int64_t tn = (cols + T.bn - 1) / T.bn, tiles = tm * tn;
+    const int64_t tm = experts ? (m + 31 * experts) / T.bm + experts : over(m, T.bm);   // at most
+    const int64_t tn = over(cols, T.bn), tiles = tm * tn;
+    const double used = std::max((double)m / T.bm + 0.5 * (double)experts, 0.75 * (double)experts) * (double)tn;
     const int most = cfg == MX_L || experts || tiles > kMxCounters
                          ? 1
-                         : (int)std::max<int64_t>(1, std::min<int64_t>({cus / tiles, kt / 2, kMxMaxSplit}));
+                         : (int)std::max<int64_t>(1, std::min<int64_t>({cus / std::max<int64_t>(1, tiles), kt / 2, kMxMaxSplit}));
     for (int s = 1; s <= most; ++s) {
-      const double rounds = (double)((tiles * s + cus - 1) / cus);
-      const double us = rounds * ((double)((kt + s - 1) / s) * kPerTile[cfg][kind] + kFixed[cfg]) +
+      const double rounds = experts ? std::max(1.0, used / cus + 0.5) : (double)over(tiles * s, cus);
+      // (tiles that the experts leave part empty multiply fewer rows)
+      const double us = rounds * ((double)over(kt, s) * kPerTile[cfg][kind] * (experts && cfg == MX_L ? 0.85 : 1.0) + kFixed[cfg]) +
                         (cfg == MX_L ? 7.0 : s > 1 ? 1.0 * s : 0.0);
-      if (best == 0 || us < best) {
+      if (us < best) {
         best = us;
+        L = MxLaunch();
         L.cfg = cfg;
         L.tiles_m = (int)tm;
         L.tiles_n = (int)tn;
         L.splits = s;
+        L.waves = mx_waves(T);
+        // the persistent kernel: one workgroup per compute unit
+        L.grid_x = cfg == MX_L ? std::min<int64_t>(tiles, cus) : tiles * s;
       }
     }
   }
-  if (const char* e = std::getenv("GE_MX_SPLIT"); e && L.cfg != MX_L && !experts) L.splits = std::atoi(e);
-  L.waves = mx_waves(kMxTiles[L.cfg]);
-  const int64_t tiles = (int64_t)L.tiles_m * L.tiles_n;
-  // the persistent kernel: one workgroup per compute unit
-  L.grid_x = L.cfg == MX_L ? std::min<int64_t>(tiles, cus) : tiles * L.splits;
   return L;
 }
 
-size_t workspace_bytes(int64_t n, int64_t k, int64_t experts, ge_mx_types_t t, int cus) {
+size_t workspace_bytes(int64_t experts, int cus) {
   using namespace gemx;
-  (void)n, (void)k, (void)t;
   if (experts) return 0;
   // split tiles times parts stay within one workgroup per compute unit
   return kMxCounterBytes + (size_t)cus * kMxTiles[MX_R128].bm * kMxTiles[MX_R128].bn * 4;

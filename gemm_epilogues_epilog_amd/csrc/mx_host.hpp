@@ -40,7 +40,7 @@ struct MxLaunch {
 };
 MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t t, int cus);
 // Workspace that covers every m: the split tiles' counters and partial sums.
-size_t workspace_bytes(int64_t n, int64_t k, int64_t experts, ge_mx_types_t t, int cus);
+size_t workspace_bytes(int64_t experts, int cus);
 
 ge_status_t check_norm(int64_t rows, int64_t d, ge_dtype_t dt, const void* x, int64_t ldx, const void* residual,
                        int64_t ldr, const void* weight, ge_dtype_t wdt, float eps, const void* sum, int64_t lds,

@@ -171,10 +171,11 @@ def test_plan_info_covers_the_output(m, n, k, experts):
         assert 1 <= i["splits"] <= max(1, ref.pad(k, 256) // 128)
         if i["stages"]:
             assert 1 <= i["workgroups"] <= i["tiles"] * i["splits"]
+        else:   # workgroups per expert and columns: one, or several that share its rows
+            assert i["workgroups"] % i["tiles"] == 0
         if experts is None:
             rows = -(-m // i["tile_m"]) if i["stages"] else 1
             assert i["tiles"] == rows * cover
-            assert i["stages"] or m <= 64
             # every part of every split tile has its workgroup and its slot of the workspace
             if i["splits"] > 1:
                 assert i["workgroups"] == i["tiles"] * i["splits"]
@@ -183,8 +184,28 @@ def test_plan_info_covers_the_output(m, n, k, experts):
             # any split of m rows over the experts fits: the worst spreads a row group each
             assert i["tiles"] >= cover * max(-(-m // i["tile_m"]), min(m, experts))
         else:
-            # workgroups per expert and columns: one, or several that share its rows
-            assert i["tiles"] == cover * experts and i["workgroups"] % i["tiles"] == 0
+            assert i["tiles"] == cover * experts
+
+
+def test_tested_products_reach_every_kernel():
+    """The shapes that the device tests multiply, and their result types, take every
+    configuration with every kind of operand on 256 compute units."""
+    from tests import test_mx_gpu as gpu
+    single = {(256, 256, False), (128, 64, False), (64, 64, False), (64, 64, True), (16, 32, False), (16, 16, False)}
+    grouped = {(t, n, False) for t, n, _ in single}
+    for fmt in ("mxfp8", "mxfp4"):
+        for out in ("f32", "bf16"):
+            seen = set()
+            for m, n, k in gpu.MNK + gpu.MNK_TILES:
+                i = mx.MXMatmul(n, k, fmt, "NONE", out).plan_info(m, compute_units=256)
+                seen.add((i["tile_m"], i["tile_n"], i["splits"] > 1))
+            assert single <= seen, (fmt, out, sorted(single - seen))
+            cases = [(c, n, k) for c in gpu.COUNTS for n, k in ((96, 300), (300, 512))] + gpu.COUNTS_TILES
+            seen = set()
+            for counts, n, k in cases:
+                i = mx.MXMatmul(n, k, fmt, "NONE", out, experts=len(counts)).plan_info(sum(counts), compute_units=256)
+                seen.add((i["tile_m"], i["tile_n"], i["splits"] > 1))
+            assert grouped <= seen, (fmt, out, sorted(grouped - seen))
 
 
 @pytest.mark.parametrize("args,status", [
