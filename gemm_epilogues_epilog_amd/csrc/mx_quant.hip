@@ -7,6 +7,8 @@
 // row pieces of 256 values. Bound by memory: one read and one write per value.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "gemm_epilog.h"
 #include "kernels.hpp"
 #include "mx_format.hpp"
@@ -17,28 +19,28 @@ namespace {
 
 using namespace gemx;
 
-// Element i of a row-major array of type DT, widened.
+// Eight values of type DT as they lie in memory.
 template <int DT>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  return load_vec(p, DT, i);
-}
-// Eight consecutive elements from 16-byte aligned memory, widened.
-template <int DT>
-__device__ __forceinline__ void load8(const char* p, float (&v)[8]) {
-  if constexpr (DT == F32) {
-    const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = a[e];
-      v[4 + e] = b[e];
-    }
-  } else {
-    const i32x4 a = *reinterpret_cast<const i32x4*>(p);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = Tr<DT>::widen((uint16_t)((uint32_t)a[e / 2] >> (16 * (e & 1))));
+struct Raw8 {
+  i32x4 v[DT == F32 ? 2 : 1];
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (DT == F32) return __int_as_float(v[e / 4][e % 4]);
+    else return Tr<DT>::widen((uint16_t)((uint32_t)v[0][e / 2] >> (16 * (e & 1))));
   }
-}
-
+  // one by one, `step` elements apart, those from `n` on (n at least 1) repeating the last
+  __device__ __forceinline__ void gather(const char* p, int64_t step, int n) {
+    using U = std::conditional_t<DT == F32, uint32_t, uint16_t>;
+    uint32_t x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = *reinterpret_cast<const U*>(p + min(e, n - 1) * step * (int64_t)sizeof(U));
+    if constexpr (DT == F32) {
+      __builtin_memcpy(v, x, 32);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[0][e] = (int)(x[2 * e] | x[2 * e + 1] << 16);
+    }
+  }
+};
 struct QuantArgs {
   const void* src;
   char* codes;
@@ -59,29 +61,41 @@ __device__ __forceinline__ void store_tile(const QuantArgs& a, int64_t rb, int64
   if (threadIdx.x < 16) reinterpret_cast<i32x4*>(ds)[threadIdx.x] = reinterpret_cast<const i32x4*>(ls)[threadIdx.x];
 }
 
-// Rows contiguous along k (col_stride 1) or any strides (VEC false: element loads).
-// A lane takes 8 consecutive k of a row; the four lanes of a quad share a block.
-template <int DT, int FMT, bool VEC>
+// Rows contiguous along k (WIDE: 16-byte loads at the elements' alignment, which the memory
+// pipe takes) or any strides. A lane takes 8 consecutive k of four rows; the four lanes of a
+// quad share a block. Lanes past the operand read its last values again and put zeros in
+// their place, so that no branch parts the loads of the rows.
+// Bound by the memory: 16384 x 8192 bf16 to MXFP4 59 us (340 MB, 5.8 TB/s; with a branch
+// around each row's load 66), 8192 x 8191 to MXFP8 36 (element by element 69).
+template <int DT, int FMT, bool WIDE>
 __global__ __launch_bounds__(256) void mx_quantize_rows_kernel(QuantArgs a) {
   __shared__ __attribute__((aligned(16))) char lc[FMT == FP4 ? 4096 : 8192];
   __shared__ __attribute__((aligned(16))) char ls[kScaleGranule];
+  constexpr int ES = DT == F32 ? 4 : 2;
   const int64_t rb = blockIdx.x / a.kt, kt = blockIdx.x % a.kt;
   const int t = threadIdx.x, kk = (t & 31) * 8;
   const int64_t k0 = kt * kKPad + kk;
+  const int left = (int)min((int64_t)8, a.k - k0);   // values of this lane (none past k)
+  const int64_t from = min(k0, a.k - 1);
+  Raw8<DT> raw[4];
+  const auto at = [&](int i) {
+    const int64_t row = min(rb * kRowGroup + i * 8 + (t >> 5), a.rows - 1);
+    return static_cast<const char*>(a.src) + (row * a.row_stride + from * a.col_stride) * ES;
+  };
+  if (WIDE && left == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) __builtin_memcpy(raw[i].v, at(i), sizeof(raw[i].v));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw[i].gather(at(i), a.col_stride, max(left, 1));
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = i * 8 + (t >> 5);
-    const int64_t row = rb * kRowGroup + r;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (row < a.rows) {
-      if constexpr (VEC) {
-        if (k0 < a.k) load8<DT>(static_cast<const char*>(a.src) + (row * a.row_stride + k0) * (DT == F32 ? 4 : 2), v);
-      } else {
+    const bool in = rb * kRowGroup + r < a.rows;
+    float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (k0 + e < a.k) v[e] = load1<DT>(a.src, row * a.row_stride + (k0 + e) * a.col_stride);
-      }
-    }
+    for (int e = 0; e < 8; ++e) v[e] = in && e < left ? raw[i].get(e) : 0.0f;
     float m = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) m = amax2(m, mag(v[e]));
@@ -191,9 +205,10 @@ struct DequantArgs {
   int64_t rows, k, row_stride, kt;
 };
 
-// One lane writes 8 consecutive k of a row. VEC: 16-byte stores (k a multiple of 8, rows
-// 16-byte aligned).
-template <int DT, int FMT, bool VEC>
+// One lane writes 8 consecutive k of a row, in 16-byte stores at the elements' alignment, a
+// row's last values one by one. Bound by the memory: MXFP8 16384 x 8192 to bf16 73 us
+// (407 MB, 5.6 TB/s), 8192 x 8191 35 (element by element 95).
+template <int DT, int FMT>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(DequantArgs a) {
   constexpr int CB = FMT == FP4 ? 4096 : 8192;
   __shared__ __attribute__((aligned(16))) char lc[CB];
@@ -233,16 +248,15 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(DequantArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= f;
     const int64_t at = row * a.row_stride + k0;
-    if constexpr (VEC) {
+    char* d = static_cast<char*>(a.dst) + at * (DT == F32 ? 4 : 2);
+    if (k0 + 8 <= a.k) {
       if constexpr (DT == F32) {
-        f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(a.dst) + at);
-        d[0] = f32x4{v[0], v[1], v[2], v[3]};
-        d[1] = f32x4{v[4], v[5], v[6], v[7]};
+        __builtin_memcpy(d, v, 32);
       } else {
         i32x4 o;
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = (int)Tr<DT>::pack2(v[2 * e], v[2 * e + 1]);
-        *reinterpret_cast<i32x4*>(static_cast<char*>(a.dst) + at * 2) = o;
+        __builtin_memcpy(d, &o, 16);
       }
     } else {
 #pragma unroll
@@ -285,23 +299,19 @@ __global__ __launch_bounds__(256) void mx_pack_kernel(PackArgs a) {
 }
 
 template <int DT, int FMT>
-const void* quantize_fn(bool cols, bool vec) {
+const void* quantize_fn(bool cols, bool wide) {
   if (cols) return reinterpret_cast<const void*>(&mx_quantize_cols_kernel<DT, FMT>);
-  return vec ? reinterpret_cast<const void*>(&mx_quantize_rows_kernel<DT, FMT, true>)
-             : reinterpret_cast<const void*>(&mx_quantize_rows_kernel<DT, FMT, false>);
+  return wide ? reinterpret_cast<const void*>(&mx_quantize_rows_kernel<DT, FMT, true>)
+              : reinterpret_cast<const void*>(&mx_quantize_rows_kernel<DT, FMT, false>);
 }
 template <int DT>
-const void* quantize_fn(int fmt, bool cols, bool vec) {
-  return fmt == FP4 ? quantize_fn<DT, FP4>(cols, vec) : quantize_fn<DT, FP8>(cols, vec);
-}
-template <int DT, int FMT>
-const void* dequantize_fn(bool vec) {
-  return vec ? reinterpret_cast<const void*>(&mx_dequantize_kernel<DT, FMT, true>)
-             : reinterpret_cast<const void*>(&mx_dequantize_kernel<DT, FMT, false>);
+const void* quantize_fn(int fmt, bool cols, bool wide) {
+  return fmt == FP4 ? quantize_fn<DT, FP4>(cols, wide) : quantize_fn<DT, FP8>(cols, wide);
 }
 template <int DT>
-const void* dequantize_fn(int fmt, bool vec) {
-  return fmt == FP4 ? dequantize_fn<DT, FP4>(vec) : dequantize_fn<DT, FP8>(vec);
+const void* dequantize_fn(int fmt) {
+  return fmt == FP4 ? reinterpret_cast<const void*>(&mx_dequantize_kernel<DT, FP4>)
+                    : reinterpret_cast<const void*>(&mx_dequantize_kernel<DT, FP8>);
 }
 
 }  // namespace
@@ -322,17 +332,14 @@ ge_status_t gemm_epilog_mx_quantize(int64_t rows, int64_t k, ge_dtype_t dt, cons
   if (ge_status_t st = gemxh::check_quantize(rows, k, dt, src, row_stride, col_stride, fmt, codes, scales); st != GE_OK)
     return st;
   if (rows == 0) return GE_OK;
-  const size_t es = dt == GE_F32 ? 4 : 2;
   gek::QuantArgs a{src, static_cast<char*>(codes), static_cast<char*>(scales), rows, k, row_stride, col_stride,
                    gemx::pad_to(k, gemx::kKPad) / gemx::kKPad};
   // Rows next to each other (k strided) go to the kernel whose lanes run along the rows:
   // reading them along k would touch a line per value.
   const bool cols = col_stride != 1 && row_stride == 1 && rows > 1;
-  const bool vec = col_stride == 1 && k % 8 == 0 && row_stride * (int64_t)es % 16 == 0 &&
-                   reinterpret_cast<uintptr_t>(src) % 16 == 0;
-  const void* fn = dt == GE_F32   ? gek::quantize_fn<gek::F32>(fmt, cols, vec)
-                   : dt == GE_F16 ? gek::quantize_fn<gek::F16>(fmt, cols, vec)
-                                  : gek::quantize_fn<gek::BF16>(fmt, cols, vec);
+  const void* fn = dt == GE_F32   ? gek::quantize_fn<gek::F32>(fmt, cols, col_stride == 1)
+                   : dt == GE_F16 ? gek::quantize_fn<gek::F16>(fmt, cols, col_stride == 1)
+                                  : gek::quantize_fn<gek::BF16>(fmt, cols, col_stride == 1);
   void* params[] = {&a};
   const int64_t tiles = cols ? (rows + gek::kColRows - 1) / gek::kColRows : gemx::row_groups(rows);
   return hipLaunchKernel(fn, dim3((unsigned)(tiles * a.kt)), dim3(cols ? 512 : 256), params, 0,
@@ -345,14 +352,11 @@ ge_status_t gemm_epilog_mx_dequantize(int64_t rows, int64_t k, ge_mx_format_t fm
                                       const void* scales, ge_dtype_t dt, void* dst, int64_t row_stride, void* stream) {
   if (ge_status_t st = gemxh::check_dequantize(rows, k, fmt, codes, scales, dt, dst, row_stride); st != GE_OK) return st;
   if (rows == 0) return GE_OK;
-  const size_t es = dt == GE_F32 ? 4 : 2;
   gek::DequantArgs a{static_cast<const char*>(codes), static_cast<const char*>(scales), dst, rows, k, row_stride,
                      gemx::pad_to(k, gemx::kKPad) / gemx::kKPad};
-  const bool vec =
-      k % 8 == 0 && row_stride * (int64_t)es % 16 == 0 && reinterpret_cast<uintptr_t>(dst) % 16 == 0;
-  const void* fn = dt == GE_F32   ? gek::dequantize_fn<gek::F32>(fmt, vec)
-                   : dt == GE_F16 ? gek::dequantize_fn<gek::F16>(fmt, vec)
-                                  : gek::dequantize_fn<gek::BF16>(fmt, vec);
+  const void* fn = dt == GE_F32   ? gek::dequantize_fn<gek::F32>(fmt)
+                   : dt == GE_F16 ? gek::dequantize_fn<gek::F16>(fmt)
+                                  : gek::dequantize_fn<gek::BF16>(fmt);
   void* params[] = {&a};
   return hipLaunchKernel(fn, dim3((unsigned)(gemx::row_groups(rows) * a.kt)), dim3(256), params, 0,
                          static_cast<hipStream_t>(stream)) == hipSuccess
