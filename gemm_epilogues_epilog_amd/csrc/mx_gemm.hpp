@@ -96,14 +96,12 @@ __device__ __forceinline__ void expert_rows(const MxArgs& p, int e, int64_t& lo,
 
 // ---- finishing outputs ------------------------------------------------------------
 // Eight consecutive finished values of row `row` from column c0 (a multiple of 8).
-__device__ __forceinline__ void mx_store8(const MxArgs& p, int64_t row, int c0, const float (&v)[8], bool vec_ok) {
+__device__ __forceinline__ void mx_store8(const MxArgs& p, int64_t row, int c0, const float (&v)[8]) {
   if (c0 >= p.n) return;
   const int64_t at = row * p.n + c0;
-  if (vec_ok) {
+  if (c0 + 8 <= p.n) {   // 16 bytes at a time, at the elements' alignment
     if (p.out == MX_OUT_F32) {
-      f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(p.D) + at);
-      d[0] = f32x4{v[0], v[1], v[2], v[3]};
-      d[1] = f32x4{v[4], v[5], v[6], v[7]};
+      __builtin_memcpy(static_cast<float*>(p.D) + at, v, 32);
     } else {
       i32x4 o;
       if (p.out == MX_OUT_F16) {
@@ -113,7 +111,7 @@ __device__ __forceinline__ void mx_store8(const MxArgs& p, int64_t row, int c0, 
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = (int)Tr<BF16>::pack2(v[2 * e], v[2 * e + 1]);
       }
-      *reinterpret_cast<i32x4*>(static_cast<char*>(p.D) + at * 2) = o;
+      __builtin_memcpy(static_cast<char*>(p.D) + at * 2, &o, 16);
     }
   } else {
 #pragma unroll
@@ -131,9 +129,6 @@ __device__ __forceinline__ void mx_store_scale(const MxArgs& p, int64_t row, int
   const int64_t granules = pad_to(p.n, kKPad) / kKPad;
   p.ds[((row >> 5) * granules + c0 / kKPad) * kScaleGranule + ((c0 / 32) & 1) * 128 + (row & 31) * 4 +
        (c0 / 64) % 4] = (char)s;
-}
-__device__ __forceinline__ bool mx_vec_ok(const MxArgs& p) {
-  return p.n % 8 == 0 && reinterpret_cast<uintptr_t>(p.D) % 16 == 0;
 }
 // Bias of column c of expert e (0 past n, or without a bias).
 __device__ __forceinline__ float mx_bias(const MxArgs& p, int e, int c) {
@@ -371,7 +366,6 @@ __device__ __forceinline__ void mx_epilogue(const MxArgs& p, const MxPlace& at, 
   constexpr int NB = C::NB, MB = C::MB;
   const int lrow = lane & 31, lhi = lane >> 5;
   const int out = p.out;
-  const bool vec_ok = mx_vec_ok(p);
   const int cpad = out == MX_OUT_FP8 ? (int)pad_to(p.n, kKPad) : p.n;
 #pragma unroll
   for (int b = 0; b < MB; ++b) {
@@ -415,36 +409,17 @@ __device__ __forceinline__ void mx_epilogue(const MxArgs& p, const MxPlace& at, 
           if (lhi == 0) mx_store_scale(p, row, c, s);
         }
       } else if (out == MX_OUT_F32) {
-        if (vec_ok && c + 32 <= p.n) {
-          // 16 bytes a lane; the line of a row's 32 columns fills over four stores
-          if (keep) {
-            float* d = static_cast<float*>(p.D) + row * p.n + c + 4 * lhi;
+        // 16 bytes a lane, at the elements' alignment; the line of a row's 32 columns fills
+        // over four stores
+        if (keep) {
+          float* d = static_cast<float*>(p.D) + row * p.n + c + 4 * lhi;
+          if (c + 32 <= p.n) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-              *reinterpret_cast<f32x4*>(d + 8 * g) = f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
-          }
-        } else {
-          // unaligned rows: 16 rows at a time through scratch, so that 32 lanes store 32
-          // neighbouring values. 16-byte unit u of row r sits at unit u ^ (r & 7).
-          int l = lane;   // kept from being computed ahead: the accumulators need the registers
-          asm volatile("" : "+v"(l));
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            f32x4* t = reinterpret_cast<f32x4*>(scratch) + (l & 15) * 8;
-            if ((l >> 4 & 1) == half) {
+            for (int g = 0; g < 4; ++g) __builtin_memcpy(d + 8 * g, v + 4 * g, 16);
+          } else {
 #pragma unroll
-              for (int g = 0; g < 4; ++g)
-                t[(2 * g + (l >> 5)) ^ (l & 7)] = f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
-            }
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll 2
-            for (int i = 0; i < 8; ++i) {
-              const int r = 2 * i + (l >> 5), u = l & 31, cc = c + u;
-              const float y = reinterpret_cast<const float*>(scratch)[r * 32 + (((u >> 2) ^ (r & 7)) << 2) + (u & 3)];
-              const int64_t rw = r0 + half * 16 + r;
-              if (rw >= at.lo && rw < at.hi && cc < p.n) static_cast<float*>(p.D)[rw * p.n + cc] = y;
-            }
-            __builtin_amdgcn_wave_barrier();
+            for (int i = 0; i < 16; ++i)
+              if (c + 8 * (i / 4) + 4 * lhi + i % 4 < p.n) d[8 * (i / 4) + i % 4] = v[i];
           }
         }
       } else {
@@ -460,27 +435,22 @@ __device__ __forceinline__ void mx_epilogue(const MxArgs& p, const MxPlace& at, 
           t[(2 * g + lhi) ^ (lrow & 7)] = u;
         }
         __builtin_amdgcn_wave_barrier();
-        if (vec_ok) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = i * 16 + (lane >> 2), cc = c + (lane & 3) * 8;
-            const i32x2* q = reinterpret_cast<const i32x2*>(scratch) + r * 8;
-            const i32x2 lo = q[(2 * (lane & 3)) ^ (r & 7)], hi = q[(2 * (lane & 3) + 1) ^ (r & 7)];
-            const int64_t rw = r0 + r;
-            if (rw >= at.lo && rw < at.hi && cc < p.n)
-              *reinterpret_cast<i32x4*>(static_cast<uint16_t*>(p.D) + rw * p.n + cc) = i32x4{lo[0], lo[1], hi[0], hi[1]};
-          }
-        } else {
-          // unaligned rows: 32 lanes store 32 neighbouring values
-          int l = lane;   // as above
-          asm volatile("" : "+v"(l));
-#pragma unroll 2
-          for (int i = 0; i < 16; ++i) {
-            const int r = 2 * i + (l >> 5), u = l & 31, cc = c + u;
-            const uint16_t y =
-                reinterpret_cast<const uint16_t*>(scratch)[r * 32 + (((u >> 2) ^ (r & 7)) << 2) + (u & 3)];
-            const int64_t rw = r0 + r;
-            if (rw >= at.lo && rw < at.hi && cc < p.n) static_cast<uint16_t*>(p.D)[rw * p.n + cc] = y;
+        for (int i = 0; i < 2; ++i) {
+          const int r = i * 16 + (lane >> 2), cc = c + (lane & 3) * 8;
+          const i32x2* q = reinterpret_cast<const i32x2*>(scratch) + r * 8;
+          const i32x2 lo = q[(2 * (lane & 3)) ^ (r & 7)], hi = q[(2 * (lane & 3) + 1) ^ (r & 7)];
+          const int64_t rw = r0 + r;
+          if (rw >= at.lo && rw < at.hi && cc < p.n) {
+            uint16_t* d = static_cast<uint16_t*>(p.D) + rw * p.n + cc;   // element-aligned
+            const i32x4 o = {lo[0], lo[1], hi[0], hi[1]};
+            if (cc + 8 <= p.n) {
+              __builtin_memcpy(d, &o, 16);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 7; ++e)
+                if (cc + e < p.n) d[e] = (uint16_t)((uint32_t)o[e / 2] >> (16 * (e & 1)));
+            }
           }
         }
         __builtin_amdgcn_wave_barrier();
@@ -1054,13 +1024,12 @@ __global__ __launch_bounds__(512, 4) void mx_skinny_kernel(MxArgs p) {
         mx_store_scale(p, r0 + t, c0, s);
       }
     } else {
-      const bool vec_ok = mx_vec_ok(p);
       const int t = threadIdx.x / (FB * 2), c = threadIdx.x % (FB * 2) * 8;
       if (t < 16 && r0 + t < hi) {
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = fin[t][c + j];
-        mx_store8(p, r0 + t, c0 + c, v, vec_ok);
+        mx_store8(p, r0 + t, c0 + c, v);
       }
     }
     __syncthreads();
