@@ -25,6 +25,8 @@ const void* kernel_of(int cfg) {
   using namespace gek;
   switch (cfg) {
     case MX_L: return reinterpret_cast<const void*>(&mx_tile_kernel<XF, MX_L, EXACT>);
+    case MX_R256: return reinterpret_cast<const void*>(&mx_ring_kernel<XF, MX_R256, EXACT>);
+    case MX_R128W: return reinterpret_cast<const void*>(&mx_ring_kernel<XF, MX_R128W, EXACT>);
     case MX_R128: return reinterpret_cast<const void*>(&mx_ring_kernel<XF, MX_R128, EXACT>);
     case MX_R64: return reinterpret_cast<const void*>(&mx_ring_kernel<XF, MX_R64, EXACT>);
     case MX_S16: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 2, EXACT>);

@@ -848,7 +848,9 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * MxCfgT<XF, CFG>::KG * 64), 1
     }
     __syncthreads();
   }
-  if (p.splits > 1 && !mx_join_parts<C>(p, at, part, w, kg == 0, lane, acc, reinterpret_cast<int*>(smem))) return;
+  if constexpr (MB == 1) {   // (the configurations that split k)
+    if (p.splits > 1 && !mx_join_parts<C>(p, at, part, w, kg == 0, lane, acc, reinterpret_cast<int*>(smem))) return;
+  }
   if (kg != 0) return;
   float* bias = reinterpret_cast<float*>(smem + C::OFF_EPI + w * C::EPI);
   char* scratch = reinterpret_cast<char*>(bias + NB * 32);

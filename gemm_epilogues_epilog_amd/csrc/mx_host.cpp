@@ -133,8 +133,9 @@ MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t 
 
   // Tile kernels: rounds of workgroups over the compute units, each so many k-tiles and a
   // fixed part (start, epilogue, joining parts of k).
-  static constexpr double kPerTile[3][3] = {{1.55, 1.2, 2.1}, {0.34, 0.26, 0.42}, {0.19, 0.17, 0.33}};
-  static constexpr double kFixed[3] = {3.0, 5.5, 4.6};
+  static constexpr double kPerTile[5][3] = {
+      {1.55, 1.2, 2.1}, {1.2, 0.88, 1.6}, {0.58, 0.48, 0.87}, {0.34, 0.26, 0.42}, {0.19, 0.17, 0.33}};
+  static constexpr double kFixed[5] = {3.0, 5.6, 5.8, 5.5, 4.6};
   const int kind = t.x == GE_MXFP4 ? 0 : (t.d == GE_MX_D_F32 || t.d == GE_MX_D_MXFP8) ? 2 : 1;
   const int64_t kt = pad_to(k, kKPad) / mx_bk((int)t.x);
   for (int cfg = MX_L; cfg <= MX_R64; ++cfg) {
@@ -142,7 +143,7 @@ MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t 
     const int64_t tm = experts ? (m + 31 * experts) / T.bm + experts : over(m, T.bm);   // at most
     const int64_t tn = over(cols, T.bn), tiles = tm * tn;
     const double used = std::max((double)m / T.bm + 0.5 * (double)experts, 0.75 * (double)experts) * (double)tn;
-    const int most = cfg == MX_L || experts || tiles > kMxCounters
+    const int most = T.mb > 1 || experts || tiles > kMxCounters
                          ? 1
                          : (int)std::max<int64_t>(1, std::min<int64_t>({cus / std::max<int64_t>(1, tiles), kt / 2, kMxMaxSplit}));
     for (int s = 1; s <= most; ++s) {
@@ -170,7 +171,7 @@ size_t workspace_bytes(int64_t experts, int cus) {
   using namespace gemx;
   if (experts) return 0;
   // split tiles times parts stay within one workgroup per compute unit
-  return kMxCounterBytes + (size_t)cus * kMxTiles[MX_R128].bm * kMxTiles[MX_R128].bn * 4;
+  return kMxCounterBytes + (size_t)cus * kMxTiles[MX_R128W].bm * kMxTiles[MX_R128W].bn * 4;   // the largest tile that splits
 }
 
 // ---- norm ---------------------------------------------------------------------------

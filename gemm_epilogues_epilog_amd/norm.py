@@ -126,7 +126,7 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor,
         lddx = _out_rows(dx, "dx_out", rows, d, t, dev)
     L = load()
     size = L.gemm_epilog_rms_norm_workspace_bytes(rows, d)
-    dw = _empty(d, weight.dtype, dev, stream)
+    dw = torch.empty_like(weight) if stream is None else _empty(weight.shape, weight.dtype, dev, stream)
     ws = _empty(size, torch.uint8, dev, stream)
     _check(L.gemm_epilog_rms_norm_backward(rows, d, DTYPES[_NAME[t]], dy.data_ptr(), lddy, s.data_ptr(), lds,
                                            weight.data_ptr(), wdt, eps, drp, lddr, dx.data_ptr(), lddx, dw.data_ptr(),

@@ -159,7 +159,8 @@ MNK = [(1, 1, 1), (1, 33, 300), (2, 64, 64), (15, 100, 512), (16, 257, 256), (17
        (64, 130, 2048), (65, 130, 2048), (100, 257, 700), (129, 128, 257), (256, 512, 1024), (300, 777, 640),
        (1, 1024, 11008), (70, 96, 11008), (520, 260, 96)]
 # ... and what takes the kernels that those leave out (see the reference's test)
-MNK_TILES = [(5, 8200, 300), (40, 4100, 96), (130, 1000, 3300), (777, 130, 11008), (70, 8200, 96), (1000, 4100, 96)]
+MNK_TILES = [(5, 8200, 300), (40, 4100, 96), (130, 1000, 3300), (777, 130, 11008), (70, 8200, 96), (70, 16400, 96),
+             (200, 16400, 96), (1000, 8200, 96), (200, 2050, 3300)]
 
 
 @pytest.mark.parametrize("x_format", ["mxfp8", "mxfp4"])
@@ -258,7 +259,7 @@ def run_experts(counts, n, k, x_format, ep, out, offsets=None, seed=0):
 
 
 COUNTS_TILES = [([40, 0, 1, 9], 4100, 96), ([100, 17, 0, 0], 520, 96), ([30, 131, 0, 139], 2050, 96),
-                ([0, 129, 91, 80], 8200, 96)]
+                ([0, 129, 20, 51], 4100, 96), ([140, 0, 11, 49], 8200, 96), ([300, 0, 133, 87], 16400, 96)]
 COUNTS = [[1], [0, 1], [3, 0, 5, 1], [16, 17, 0, 31, 33], [0, 0, 200, 0], [1] * 40, [70, 1, 300, 0, 129],
           [257, 500, 31, 33, 64, 0, 900], [5] * 70 + [0, 900, 0]]
 
@@ -276,7 +277,7 @@ def test_experts(gpu, counts, n, k, x_format):
 
 
 @pytest.mark.parametrize("x_format", ["mxfp8", "mxfp4"])
-@pytest.mark.parametrize("counts,n,k", COUNTS_TILES, ids=[str(c[1]) for c in COUNTS_TILES])
+@pytest.mark.parametrize("counts,n,k", COUNTS_TILES, ids=lambda v: str(max(v)) if isinstance(v, list) else None)
 def test_experts_in_every_tile(gpu, counts, n, k, x_format):
     for ep, out in (("RELU_BIAS", "f32"), ("NONE", "bf16")):
         D, xv, wv, b, off = run_experts(counts, n, k, x_format, ep, out)

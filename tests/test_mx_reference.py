@@ -191,7 +191,8 @@ def test_tested_products_reach_every_kernel():
     """The shapes that the device tests multiply, and their result types, take every
     configuration with every kind of operand on 256 compute units."""
     from tests import test_mx_gpu as gpu
-    single = {(256, 256, False), (128, 64, False), (64, 64, False), (64, 64, True), (16, 32, False), (16, 16, False)}
+    single = {(256, 256, False), (128, 256, False), (128, 128, False), (128, 64, False), (64, 64, False),
+              (64, 64, True), (16, 32, False), (16, 16, False)}
     grouped = {(t, n, False) for t, n, _ in single}
     for fmt in ("mxfp8", "mxfp4"):
         for out in ("f32", "bf16"):
