@@ -218,10 +218,11 @@ ge_status_t check_norm_backward(int64_t rows, int64_t d, ge_dtype_t dt, const vo
 }
 
 int64_t norm_backward_groups(int64_t rows, int64_t d) {
-  // enough to fill the device, few enough to keep the second pass short (16384 x 1024:
-  // 29 us at 1024, 37 at 512; 4096 x 4096: 30 at 512, 36 at 1024; 16384 x 8192: 203 at 256,
-  // 210 at 512)
-  return std::min<int64_t>(rows, d <= 1024 ? 1024 : d <= 4096 ? 512 : 256);
+  // Row slots: enough to fill the device, few enough to keep the second pass short (16384 x
+  // 512, where four slots share a workgroup and its row of sums: 16.4 us at 2048, 18.7 at
+  // 1024, 17.8 at 4096; 16384 x 1024: 30 at 1024, 34 at 2048, 37 at 512; 4096 x 4096: 26 at 512,
+  // 32 at 1024; 16384 x 8192: 196 at 256, 203 at 512)
+  return std::min<int64_t>(rows, d <= 512 ? 2048 : d <= 1024 ? 1024 : d <= 4096 ? 512 : 256);
 }
 size_t norm_workspace_bytes(int64_t rows, int64_t d) {
   if (rows <= 0 || d < 1) return 0;
