@@ -541,6 +541,11 @@ struct MxSrc {
 // on from one tile into the next: during a tile's last two k-tiles the copies fetch the
 // next tile's first two, so its latency hides behind this tile's end and its epilogue, and
 // the stores of D drain while the next tile computes. The epilogue has LDS of its own.
+// Bound by the matrix unit: it sustains 6650 TFLOP/s (e2m1) and 3880 (e4m3 X) on random
+// values in registers under the power limit, and 8192^3 runs at 4520 (243 us) and 3000
+// (366 us; in two parts 669 us, twice the products at 3290). What e2m1 lacks is the LDS: a
+// 256 x 256 tile of eight 64 x 128 waves reads 1.5 KB of fragments per product there, four
+// waves of 128 x 128 a third less, but one wave per SIMD hides no wait (387 us).
 template <int XF, int CFG, bool EXACT>
 __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), 2) void mx_tile_kernel(MxArgs p) {
   using C = MxCfgT<XF, CFG>;
@@ -703,7 +708,10 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), 2) void mx_tile_kernel(
 // ring of STAGES stages of its own, so that the copies, LDS reads and products of one
 // group fill the waits of the other; their sums are added through LDS at the end.
 // Per round one barrier; the LDS reads of the next k-tile and the copies of a later one run
-// beside the products of this one.
+// beside the products of this one. A k-tile's time is its copies' and reads', 0.17 us
+// (64 x 64) to 0.88 us (128 x 256) with e4m3 X, against 0.04 to 0.28 us of products. Measured
+// with W from memory: 100 x 4096 x 11008 16.7 us (W alone is 3.8 us of reading), 1000 x 4096 x
+// 4096 19.7 us (1700 TFLOP/s).
 template <int XF, int CFG, bool EXACT>
 __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * MxCfgT<XF, CFG>::KG * 64), 1) void mx_ring_kernel(MxArgs p) {
   using C = MxCfgT<XF, CFG>;
@@ -862,10 +870,13 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * MxCfgT<XF, CFG>::KG * 64), 1
 
 // ---- skinny kernel -----------------------------------------------------------------
 // Few rows: bound by reading W once. A workgroup takes 16 FB rows of W and up to 16 rows
-// of X at a time; its eight waves split k, stream W from memory straight into registers (16 bytes a
+// of X at a time; its waves split k, stream W from memory straight into registers (16 bytes a
 // lane, consecutive lines) and add their sums through LDS in wave order. 16x16x128
 // products: lane l holds row l % 16 and the 32 k of quarter l / 16 of a 128-k step.
 // Rows of X are addressed one by one, so an expert's rows may start anywhere.
+// One row by W from memory: 32768 x 8192 26 us (5.5 TB/s of W), 11008 x 4096 8.8 us and
+// 4096 x 11008 8.9 us (2.7 TB/s: the launch, the first reads and the joining of the waves take
+// about 4 us); 48 rows over 32 experts of 1376 x 4096 11.7 us.
 template <int XF, int S>
 __device__ __forceinline__ f32x4 mx_mma16(i32x4 w, const i32x4 (&x)[XF == FP8 ? 2 : 1], f32x4 c, int sw, int sx) {
   const i32x8 a = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
@@ -878,16 +889,17 @@ __device__ __forceinline__ f32x4 mx_mma16(i32x4 w, const i32x4 (&x)[XF == FP8 ? 
   }
 }
 
-// A batch of U steps of 128 k is loaded whole before its products; the next batch's loads
-// are on their way meanwhile.
+// A step of 128 k; the next one's loads are on their way during its products. (Two or more steps
+// at a time read sooner but take registers, and with them resident waves: 11008 x 4096 8.7 us
+// at one, 10.4 at two, 13.6 at four; without the step ahead 8.9, and 32768 x 8192 28.3
+// instead of 25.8.)
 template <int XF, int FB>
-struct MxSteps {
-  static constexpr int U = 1, XR = XF == FP8 ? 2 : 1;
-  i32x4 w[U][FB], x[U][XR];
-  int sw[U][FB], sx[U];
+struct MxStep {
+  i32x4 w[FB], x[XF == FP8 ? 2 : 1];
+  int sw[FB], sx;
 };
 
-constexpr int kPastRange = 0x7fffffff;   // rsrc()'s range
+constexpr uint32_t kPastRange = 0x7fffffffu;   // rsrc()'s range
 
 template <int XF, int FB, bool EXACT>
 __global__ __launch_bounds__(512, 4) void mx_skinny_kernel(MxArgs p) {
@@ -908,9 +920,7 @@ __global__ __launch_bounds__(512, 4) void mx_skinny_kernel(MxArgs p) {
   const int steps = has_w ? p.kt * 2 : 0;
   const int s0 = steps * w / nw, s1 = steps * (w + 1) / nw;
   const __amdgpu_buffer_rsrc_t rw = rsrc(p.wc + (e * wrg + (has_w ? fg : 0)) * gw), rws = rsrc(p.ws + (e * wrg + (has_w ? fg : 0)) * gs);
-  const int lw = g * 512 + (c0 % 32 + li) * 16, lws = (g & 1) * 128 + (c0 % 32 + li) * 4;
-  using Steps = MxSteps<XF, FB>;
-  constexpr int U = Steps::U;
+  const uint32_t lw = g * 512 + (c0 % 32 + li) * 16, lws = (g & 1) * 128 + (c0 % 32 + li) * 4;
   // The first FB waves finish the sums, four columns a lane. Their bias is read here as it
   // lies (an fp32 value in two halves), so that nothing waits for it before the end; past n
   // and without a bias the range gives zeros.
@@ -934,57 +944,50 @@ __global__ __launch_bounds__(512, 4) void mx_skinny_kernel(MxArgs p) {
     const int64_t rr = r0 + li < hi ? r0 + li : r0;
     const __amdgpu_buffer_rsrc_t rx = rsrc(p.xc + (r0 >> 5) * gx), rxs = rsrc(p.xs + (r0 >> 5) * gs);
     const int rg = (int)((rr >> 5) - (r0 >> 5));   // the rows lie in one row group or two
-    const int lx = rg * (int)gx + (int)(rr & 31) * 16 + g * 512, lxs = rg * (int)gs + (int)(rr & 31) * 4 + (g & 1) * 128;
+    const uint32_t lx = rg * (int)gx + (int)(rr & 31) * 16 + g * 512, lxs = rg * (int)gs + (int)(rr & 31) * 4 + (g & 1) * 128;
     f32x4 acc[FB];
 #pragma unroll
     for (int f = 0; f < FB; ++f) acc[f] = f32x4{0, 0, 0, 0};
-    const auto load = [&](Steps& b, int s) {
+    const auto load = [&](MxStep<XF, FB>& b, int t) {
+      // steps past the wave's last one lie past the buffers' range: zeros, and no reads
+      const uint32_t past = t < s1 ? 0u : kPastRange, ts = past | (uint32_t)((t >> 1) * kScaleGranule);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        // steps past the wave's last one lie past the buffers' range: zeros, and no reads
-        const int t = s + u, past = t < s1 ? 0 : kPastRange, ts = past | (t >> 1) * kScaleGranule;
+      for (int f = 0; f < FB; ++f) {
+        b.w[f] = __builtin_amdgcn_raw_buffer_load_b128(rw, lw + f * 256 + (past | (uint32_t)(t * 2048)), 0, 0);
+        b.sw[f] = __builtin_amdgcn_raw_buffer_load_b32(rws, lws + f * 64 + ts, 0, 0);
+      }
 #pragma unroll
-        for (int f = 0; f < FB; ++f) {
-          b.w[u][f] = __builtin_amdgcn_raw_buffer_load_b128(rw, lw + f * 256 + (past | t * 2048), 0, 0);
-          b.sw[u][f] = __builtin_amdgcn_raw_buffer_load_b32(rws, lws + f * 64 + ts, 0, 0);
+      for (int h = 0; h < XR; ++h)
+        b.x[h] = __builtin_amdgcn_raw_buffer_load_b128(rx, lx + h * 2048 + (past | (uint32_t)(t * (2048 * XR))), 0, 0);
+      b.sx = __builtin_amdgcn_raw_buffer_load_b32(rxs, lxs + ts, 0, 0);
+    };
+    const auto multiply = [&](const MxStep<XF, FB>& b, int t) {
+      const int sh = 16 * (t & 1) + 8 * (g >> 1);   // byte of the scale dword: block 4 (t % 2) + g of the granule
+      i32x4 xf[XR];
+#pragma unroll
+      for (int h = 0; h < XR; ++h) xf[h] = b.x[h];
+      if constexpr (EXACT) {
+        i32x4 xl[XR];
+#pragma unroll
+        for (int h = 0; h < XR; ++h) {
+          xl[h] = large_part(xf[h]);
+          xf[h] ^= xl[h];
         }
 #pragma unroll
-        for (int h = 0; h < XR; ++h)
-          b.x[u][h] = __builtin_amdgcn_raw_buffer_load_b128(rx, lx + h * 2048 + (past | t * (2048 * XR)), 0, 0);
-        b.sx[u] = __builtin_amdgcn_raw_buffer_load_b32(rxs, lxs + ts, 0, 0);
+        for (int f = 0; f < FB; ++f) acc[f] = mx_mma16<XF, 0>(b.w[f], xl, acc[f], b.sw[f] >> sh, b.sx >> sh);
       }
+#pragma unroll
+      for (int f = 0; f < FB; ++f) acc[f] = mx_mma16<XF, 0>(b.w[f], xf, acc[f], b.sw[f] >> sh, b.sx >> sh);
     };
-    const auto multiply = [&](const Steps& b, int s) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        // byte of the scale dword: block 4 (s % 2) + g of the granule
-        const int sh = 16 * ((s + u) & 1) + 8 * (g >> 1);
-        i32x4 xf[XR];
-#pragma unroll
-        for (int h = 0; h < XR; ++h) xf[h] = b.x[u][h];
-        if constexpr (EXACT) {
-          i32x4 xl[XR];
-#pragma unroll
-          for (int h = 0; h < XR; ++h) {
-            xl[h] = large_part(xf[h]);
-            xf[h] ^= xl[h];
-          }
-#pragma unroll
-          for (int f = 0; f < FB; ++f) acc[f] = mx_mma16<XF, 0>(b.w[u][f], xl, acc[f], b.sw[u][f] >> sh, b.sx[u] >> sh);
-        }
-#pragma unroll
-        for (int f = 0; f < FB; ++f) acc[f] = mx_mma16<XF, 0>(b.w[u][f], xf, acc[f], b.sw[u][f] >> sh, b.sx[u] >> sh);
-      }
-    };
-    Steps b0, b1;
+    MxStep<XF, FB> b0, b1;
     load(b0, s0);
-    for (int s = s0; s < s1; s += 2 * U) {
-      load(b1, s + U);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int s = s0; s < s1; s += 2) {
+      load(b1, s + 1);
+      __builtin_amdgcn_sched_barrier(0);   // the loads first
       multiply(b0, s);
-      load(b0, s + 2 * U);
+      load(b0, s + 2);
       __builtin_amdgcn_sched_barrier(0);
-      multiply(b1, s + U);
+      multiply(b1, s + 1);
     }
 #pragma unroll
     for (int f = 0; f < FB; ++f) red[w][f][lane] = acc[f];

@@ -131,7 +131,9 @@ __device__ __forceinline__ float wave_sum(float v) {
 // NT lanes per row, C chunks of eight values per lane, WG / NT rows side by side in a
 // workgroup and a.walk rows one after the other per row slot: the weight is read once per
 // slot, and the next row's loads are in flight while this one is summed and written.
-// LDS of one slot's 8-bit rows.
+// 16384 x 8192 bf16 with a residual: 189 us to MXFP8 (943 MB, 5.0 TB/s), 210 to bf16 (5.1),
+// without a residual 104; 4096 x 4096 21 us (6.3 TB/s, the 256 MB cache helps).
+// LDS of one slot's 8-bit rows:
 constexpr int norm_stage_bytes(int granules, int walk) { return granules * (16 * (walk + 1) * 16 + 2 * walk * 4); }
 constexpr int wg_of(int nt) { return nt > 64 ? nt : 256; }
 
@@ -266,7 +268,9 @@ struct NormBwdArgs {
 
 // Each row slot walks the rows with the stride of all slots, the next row's loads in flight
 // while this one is summed, and keeps its share of dw in registers; norm_dweight_kernel then
-// adds the workgroups' sums in order (no atomics).
+// adds the workgroups' sums in order (no atomics). 8192 x 8192 bf16 100 us and the second
+// pass 4.6 (403 MB read and written, 4.0 TB/s); 16384 x 8192 with the gradient past the norm
+// 197 us (1.07 GB, 5.4 TB/s). More registers per lane (two chunks of the next row) spilled.
 template <int DT, int NT, int C, bool VEC>
 __global__ __launch_bounds__(wg_of(NT)) void rms_norm_backward_kernel(NormBwdArgs a) {
   constexpr int RPW = wg_of(NT) / NT, NWV = NT / 64;
