@@ -138,13 +138,20 @@ ge_status_t gemm_epilog_mx_execute(ge_mx_handle_t h, int64_t m, const void* x_co
   if (L.grid_x * L.grid_y * L.grid_z * L.waves * 64 >= (int64_t(1) << 32) || L.grid_y > 65535)
     return GE_ERR_NOT_SUPPORTED;
   const bool exact = h->t.d == GE_MX_D_F32 || h->t.d == GE_MX_D_MXFP8;   // see large_part
-  const void* fn = h->t.x == GE_MXFP4 ? kernel_of<gemx::FP4, false>(L.cfg)
-                   : exact            ? kernel_of<gemx::FP8, true>(L.cfg)
-                                      : kernel_of<gemx::FP8, false>(L.cfg);
-  void* params[] = {&a};
-  return hipLaunchKernel(fn, dim3((unsigned)L.grid_x, (unsigned)L.grid_y, (unsigned)L.grid_z),
-                         dim3((unsigned)L.waves * 64), params, 0,
-                         static_cast<hipStream_t>(stream)) == hipSuccess
+  const auto launch = [&](int cfg, dim3 grid, int waves) {
+    const void* fn = h->t.x == GE_MXFP4 ? kernel_of<gemx::FP4, false>(cfg)
+                     : exact            ? kernel_of<gemx::FP8, true>(cfg)
+                                        : kernel_of<gemx::FP8, false>(cfg);
+    void* params[] = {&a};
+    return hipLaunchKernel(fn, grid, dim3((unsigned)waves * 64), params, 0, static_cast<hipStream_t>(stream)) ==
+           hipSuccess;
+  };
+  a.round = L.tail ? (int32_t)L.grid_x : 0;
+  a.tail = 0;
+  if (!launch(L.cfg, dim3((unsigned)L.grid_x, (unsigned)L.grid_y, (unsigned)L.grid_z), L.waves)) return GE_ERR_HIP;
+  if (!L.tail) return GE_OK;
+  a.tail = 1;
+  return launch(gemx::kMxTailCfg, dim3((unsigned)(a.round / 4 * 4)), gemx::mx_waves(gemx::kMxTiles[gemx::kMxTailCfg]))
              ? GE_OK
              : GE_ERR_HIP;
 }

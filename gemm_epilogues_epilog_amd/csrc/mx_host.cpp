@@ -146,11 +146,20 @@ MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t 
     const int most = T.mb > 1 || experts || tiles > kMxCounters
                          ? 1
                          : (int)std::max<int64_t>(1, std::min<int64_t>({cus / std::max<int64_t>(1, tiles), kt / 2, kMxMaxSplit}));
+    const auto round_us = [&](int c, int s) { return (double)over(kt, s) * kPerTile[c][kind] + kFixed[c]; };
+    // a short last round of large tiles goes to smaller ones (by expert it may)
+    const int64_t rest = tiles % cus;
+    const bool tail = cfg == MX_L && tiles > cus && (experts || (rest > 0 && rest <= cus / 4));
     for (int s = 1; s <= most; ++s) {
-      const double rounds = experts ? std::max(1.0, used / cus + 0.5) : (double)over(tiles * s, cus);
-      // (tiles that the experts leave part empty multiply fewer rows)
-      const double us = rounds * ((double)over(kt, s) * kPerTile[cfg][kind] * (experts && cfg == MX_L ? 0.85 : 1.0) + kFixed[cfg]) +
-                        (cfg == MX_L ? 7.0 : s > 1 ? 1.0 * s : 0.0);
+      double us;
+      if (experts) {
+        // (tiles that the experts leave part empty multiply fewer rows)
+        us = std::max(1.0, used / cus + 0.5) * (cfg == MX_L ? 0.85 : 1.0) * round_us(cfg, 1);
+      } else {
+        us = tail ? (double)(tiles / cus) * round_us(cfg, 1) + round_us(kMxTailCfg, 1) + 3.0
+                  : (double)over(tiles * s, cus) * round_us(cfg, s);
+      }
+      us += cfg == MX_L ? 7.0 : s > 1 ? 1.0 * s : 0.0;
       if (us < best) {
         best = us;
         L = MxLaunch();
@@ -159,6 +168,7 @@ MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t 
         L.tiles_n = (int)tn;
         L.splits = s;
         L.waves = mx_waves(T);
+        L.tail = tail;
         // the persistent kernel: one workgroup per compute unit
         L.grid_x = cfg == MX_L ? std::min<int64_t>(tiles, cus) : tiles * s;
       }

@@ -36,6 +36,7 @@ struct MxLaunch {
   int splits = 1;
   int waves = 0;             // of a workgroup
   int group_m = 8;
+  bool tail = false;         // a second launch takes (or may take, by expert) a short last round
   int64_t grid_x = 0, grid_y = 1, grid_z = 1;
 };
 MxLaunch choose(int64_t m, int64_t n, int64_t k, int64_t experts, ge_mx_types_t t, int cus);

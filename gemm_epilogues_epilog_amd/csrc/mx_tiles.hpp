@@ -31,6 +31,8 @@ constexpr MxTile kMxTiles[MX_COUNT] = {
 constexpr bool mx_is_ring(int c) { return c >= MX_R256 && c <= MX_R64; }
 constexpr int mx_waves(const MxTile& t) { return (t.bm / 32 / t.mb) * (t.bn / 32 / t.nb) * t.kg; }
 constexpr int kMxSkinnyWaves = 8;   // at most
+constexpr int kMxTailCfg = MX_R128W;   // quarters of the tile kernel's tiles, for its short last rounds
+static_assert(kMxTiles[MX_L].bm == 2 * kMxTiles[kMxTailCfg].bm && kMxTiles[MX_L].bn == 2 * kMxTiles[kMxTailCfg].bn, "quarters");
 // k values of one LDS stage: 128 bytes of a row of X.
 constexpr int mx_bk(int xfmt) { return xfmt == FP4 ? 256 : 128; }
 

@@ -160,7 +160,7 @@ MNK = [(1, 1, 1), (1, 33, 300), (2, 64, 64), (15, 100, 512), (16, 257, 256), (17
        (1, 1024, 11008), (70, 96, 11008), (520, 260, 96)]
 # ... and what takes the kernels that those leave out (see the reference's test)
 MNK_TILES = [(5, 8200, 300), (40, 4100, 96), (130, 1000, 3300), (777, 130, 11008), (70, 8200, 96), (70, 16400, 96),
-             (200, 16400, 96), (1000, 8200, 96), (200, 2050, 3300)]
+             (200, 16400, 96), (1000, 8200, 96), (200, 2050, 3300), (2200, 7300, 96)]
 
 
 @pytest.mark.parametrize("x_format", ["mxfp8", "mxfp4"])
@@ -285,6 +285,33 @@ def test_experts_in_every_tile(gpu, counts, n, k, x_format):
             if counts[e]:
                 r = slice(off[e], off[e + 1])
                 check(D[r], xv[r], wv[e], b[e], k, ep, out, (ep, out, e))
+
+
+# a last round of at most a quarter of the device's large tiles, which smaller ones take: 264
+# and 290 tiles of 256 x 256 on 256 compute units, an empty expert and ragged ends among them
+@pytest.mark.parametrize("x_format", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("counts", [[300, 700, 0, 500], [1, 255, 1000, 244]], ids=str)
+def test_experts_with_a_short_last_round(gpu, counts, x_format):
+    n, k = 8200, 96
+    m = sum(counts)
+    i = mx.MXMatmul(n, k, x_format, "NONE", "f32", experts=4).plan_info(m)
+    assert (i["tile_m"], i["tile_n"]) == (256, 256) and i["tiles"] > 256
+    for ep, out in (("NONE", "f32"), ("GELU_BIAS", "bf16")):
+        D, xv, wv, b, off = run_experts(counts, n, k, x_format, ep, out)
+        for e in range(4):
+            if counts[e]:
+                r = slice(off[e], off[e + 1])
+                check(D[r], xv[r], wv[e], b[e], k, ep, out, (ep, out, e))
+    # the 8-bit result is the fp32 one's quantisation, its padding columns included
+    X, W, _, _, _ = operands(m, n, k, x_format, m, experts=4)
+    o = torch.tensor(off, dtype=torch.int32, device="cuda")
+    with mx.MXMatmul(n, k, x_format, "NONE", "f32", experts=4) as mm, \
+            mx.MXMatmul(n, k, x_format, "NONE", "mxfp8", experts=4) as m8:
+        want = mx.mx_quantize(mm.execute(X, W, offsets=o), "mxfp8")
+        got = mx.MXTensor.empty(m, n, "mxfp8")
+        got.codes.zero_(), got.scales.zero_()
+        m8.execute(X, W, offsets=o, out=got)
+        assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
 
 
 @pytest.mark.parametrize("m", [40, 700])
