@@ -268,9 +268,9 @@ struct NormBwdArgs {
 
 // Each row slot walks the rows with the stride of all slots, the next row's loads in flight
 // while this one is summed, and keeps its share of dw in registers; norm_dweight_kernel then
-// adds the workgroups' sums in order (no atomics). 8192 x 8192 bf16 100 us and the second
-// pass 4.6 (403 MB read and written, 4.0 TB/s); 16384 x 8192 with the gradient past the norm
-// 197 us (1.07 GB, 5.4 TB/s). More registers per lane (two chunks of the next row) spilled.
+// adds the workgroups' sums in order (no atomics). With the gradient past
+// the norm 8192 x 8192 bf16 takes 98 us (546 MB, 5.6 TB/s) and the second pass 4.6, 16384 x 8192
+// 196 together (5.5 TB/s). More registers per lane (two chunks of the next row) spilled.
 template <int DT, int NT, int C, bool VEC>
 __global__ __launch_bounds__(wg_of(NT)) void rms_norm_backward_kernel(NormBwdArgs a) {
   constexpr int RPW = wg_of(NT) / NT, NWV = NT / 64;
