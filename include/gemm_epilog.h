@@ -394,7 +394,8 @@ typedef struct {
   int stages;              /* LDS stages of the operand ring (0: W goes straight to registers) */
   int splits;              /* workgroups that share a tile's k loop */
   int64_t tiles;           /* by expert: the most there can be */
-  int64_t workgroups;      /* fewer than tiles times splits where they walk the tiles */
+  int64_t workgroups;      /* fewer than tiles times splits where they walk the tiles (a second
+                              launch, not counted here, may take a short last round of them) */
   size_t workspace_bytes;  /* device workspace of the plan (independent of m) */
 } ge_mx_plan_info_t;
 
