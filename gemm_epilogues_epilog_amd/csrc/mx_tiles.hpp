@@ -18,8 +18,8 @@ namespace gemx {
 //     256 32.7, 128 x 128 41, 256 x 256 47; 500 rows: 128 x 64 13.6, 128 x 128 18.9). Those
 //     with mb 1 can share k between workgroups where the tiles are fewer than the compute
 //     units.
-//   MX_S16, MX_S16N: skinny kernel (stages 0), eight waves that split k and read W straight
-//     into registers: up to 16 rows.
+//   MX_S16, MX_S16N: skinny kernel (stages 0), two to eight waves that split k and read W
+//     straight into registers, sixteen rows at a time: few rows, or few per expert.
 // kg: groups of waves, each with every kg-th k-tile (their sums are added through LDS).
 struct MxTile {
   int bm, bn, mb, nb, stages, kg;

@@ -408,3 +408,58 @@ def test_binding_refusals(gpu):
     with pytest.raises(ValueError):
         mx.mx_pack(torch.zeros(4, 16, dtype=torch.uint8, device="cuda"), torch.zeros(4, 2, dtype=torch.uint8, device="cuda"),
                    "mxfp4", k=40)
+
+
+def test_operands_past_four_gib(gpu):
+    """Offsets that pass 32 bits: quantisation, norm and product of 8.6 GB of rows give the
+    last rows what they give them alone. Whole numbers, so every sum is exact."""
+    from gemm_epilogues_epilog_amd.norm import rms_norm, rms_norm_backward
+    k, n, last = 32768, 40, 96
+    m = (1 << 17) + last
+    row = torch.arange(k, device="cuda") % 5 - 2
+    x = torch.empty(m, k, dtype=torch.bfloat16, device="cuda")
+    x.copy_(row.to(torch.bfloat16))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x[-last:] = torch.randint(-2, 3, (last, k), generator=g, device="cuda").to(torch.bfloat16)
+    tail = x[-last:].clone()
+    X, T_ = mx.mx_quantize(x, "mxfp8"), mx.mx_quantize(tail, "mxfp8")
+    assert torch.equal(X.codes[-last * k:], T_.codes) and torch.equal(X.scales[-last * k // 32:], T_.scales)
+    assert torch.equal(mx.mx_dequantize(X, "bf16")[-last:], tail)
+    W = mx.mx_quantize(torch.randint(-2, 3, (n, k), generator=g, device="cuda").float(), "mxfp4")
+    with mx.MXMatmul(n, k, out="f32") as mm:
+        D = mm.execute(X, W)
+        want = tail.float() @ mx.mx_dequantize(W, "f32").T
+        assert torch.equal(D[-last:], want) and torch.equal(D[0], D[1 << 16])
+    with mx.MXMatmul(n, k, out="f32", experts=2) as mm:
+        W2 = mx.MXTensor(torch.stack([W.codes, W.codes]), torch.stack([W.scales, W.scales]), n, k, "mxfp4", 2)
+        off = torch.tensor([0, m - last, m], dtype=torch.int32, device="cuda")
+        assert torch.equal(mm.execute(X, W2, offsets=off), D)
+    del X, D
+    w = torch.ones(k, dtype=torch.bfloat16, device="cuda")
+    y, _ = rms_norm(x, w, y_out=x)   # in place
+    assert torch.equal(y[-last:], rms_norm(tail, w)[0])
+    s = y[-last:].clone()
+    dx, dw = rms_norm_backward(y, y, w, dx_out=y)
+    assert torch.equal(dx[-last:], rms_norm_backward(s, s, w)[0]) and torch.isfinite(dw.float()).all()
+
+
+@pytest.mark.parametrize("m,n,k,experts", [(2200, 7300, 520, None), (1012, 16400, 520, 3), (130, 1000, 3300, None)])
+def test_graph_of_short_last_rounds_and_split_tiles(gpu, m, n, k, experts):
+    """Products of two launches, and one whose parts of k meet through counters, replayed with
+    eager work in between: every replay as the eager result."""
+    X, W, _, _, b = operands(m, n, k, "mxfp8", 5, experts=experts)
+    off = None if experts is None else torch.tensor([0, 512, 512, m], dtype=torch.int32, device="cuda")
+    with mx.MXMatmul(n, k, "mxfp8", "GELU_BIAS", "bf16", vec_dtype="f32", experts=experts) as mm:
+        i = mm.plan_info(m)
+        assert i["splits"] > 1 or (i["tile_m"] == 256 and i["tiles"] > 256)
+        want = mm.execute(X, W, b.cuda(), offsets=off).clone()
+        out, bias = torch.empty_like(want), b.cuda()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            mm.execute(X, W, bias, offsets=off, out=out)
+        for _ in range(4):
+            out.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+            assert torch.equal(mm.execute(X, W, bias, offsets=off), want)
