@@ -296,6 +296,8 @@ class MXMatmul:
             raise ValueError(f"W must be a {(n, k) if experts is None else (experts, n, k)} mxfp4 MXTensor")
         if X.device != dev or W.device != dev:
             raise ValueError(f"X and W must be on the plan's device {dev}")
+        if dev.index != torch._C._cuda_getDevice():   # (where the library launches)
+            raise ValueError(f"the plan's device {dev} is not the current device")
         bp = op = sp = None
         if self.epilog != "NONE":
             if bias is None:
