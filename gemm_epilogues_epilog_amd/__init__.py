@@ -291,6 +291,11 @@ _TORCH_NAME = {"torch.float32": "f32", "torch.float16": "f16", "torch.bfloat16":
 _BIAS_EPILOGS = ("RELU_BIAS", "GELU_BIAS", "RELU_AUX_BIAS", "BIAS", "RELU_BIAS_UNFUSED")
 
 
+def _current_device() -> int:
+    import torch
+    return torch._C._cuda_getDevice()
+
+
 def _require(t, name: str, dtype_name: str, numel: int, device) -> None:
     """A caller-supplied tensor that the kernels will read or write through its data
     pointer: a contiguous device tensor on `device`, of element type `dtype_name`
@@ -325,6 +330,7 @@ class Matmul:
         self.vec_dtype = vec_dtype or dtype
         self.trans_a, self.trans_b = bool(trans_a), bool(trans_b)
         self.handle = None
+        self.device_index = None
 
     def plan(self):
         if self.handle is None:
@@ -334,6 +340,7 @@ class Matmul:
                                                   OP_T if self.trans_a else OP_N, OP_T if self.trans_b else OP_N)
             else:
                 self.handle = gemm_epilog_plan(self.m, self.n, self.k, dts, self.epilog)
+            self.device_index = _current_device()
         return self
 
     def describe(self) -> str:
@@ -370,8 +377,13 @@ class Matmul:
             if act is None:
                 raise ValueError("DRELU_BGRAD_UNFUSED needs the forward activation as act")
             _require(act, "act", self.dtype, self.m * self.n, dev)
+        # the library plans and launches on the current device
+        if dev.index != _current_device():
+            raise ValueError(f"the operands are on {dev}, which is not the current device")
         if self.handle is None:
             self.plan()
+        elif self.device_index != dev.index:
+            raise ValueError(f"planned on device {self.device_index}, the operands are on {dev}")
         if out is None:
             out = torch.empty((self.m, self.n), dtype=A.dtype, device=dev)
         if self.epilog == "RELU_AUX_BIAS" and relu_aux is None:

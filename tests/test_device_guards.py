@@ -5,7 +5,9 @@ index is patched and operands are stood in for."""
 import pytest
 import torch
 
+import gemm_epilogues_epilog_amd as ge
 from gemm_epilogues_epilog_amd import mx
+from tests.test_binding_checks import FakeDev
 
 
 @pytest.fixture
@@ -14,6 +16,7 @@ def current(monkeypatch):
     def used(*a, **k):
         raise AssertionError("the library was reached")
     monkeypatch.setattr(mx, "load", used)
+    monkeypatch.setattr(ge, "load", used)
     def to(index):
         monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: index, raising=False)
         monkeypatch.setattr(torch.cuda, "current_device", lambda: index)
@@ -41,3 +44,28 @@ def test_microscaled_product(current):
         with pytest.raises(ValueError, match="current device"):
             m8.execute(X, W, out=out)
         mm.handle = m8.handle = None
+
+
+def test_fused_product(current):
+    def operands(index):
+        return [FakeDev(s, torch.float16, device=f"cuda:{index}") for s in ((64, 32), (32, 48), (64,), (64, 48))]
+    for plan_on, now in ((1, 0), (0, 1)):
+        A, B, bias, out = operands(plan_on)
+        current(now)
+        for planned in (True, False):   # planning also goes to the current device
+            m = ge.Matmul(64, 48, 32, "f16", "BIAS")
+            if planned:
+                m.handle, m.device_index = 1 << 20, plan_on   # as plan() leaves it
+            for call in (m.execute, m.autotune):
+                with pytest.raises(ValueError, match="current device"):
+                    call(A, B, bias, out=out)
+            assert planned or m.handle is None
+            m.handle = None
+    # a plan of another device than the operands'
+    A, B, bias, out = operands(0)
+    current(0)
+    m = ge.Matmul(64, 48, 32, "f16", "BIAS")
+    m.handle, m.device_index = 1 << 20, 1
+    with pytest.raises(ValueError, match="planned on"):
+        m.execute(A, B, bias, out=out)
+    m.handle = None
