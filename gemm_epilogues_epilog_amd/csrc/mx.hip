@@ -29,8 +29,8 @@ const void* kernel_of(int cfg) {
     case MX_R128W: return reinterpret_cast<const void*>(&mx_ring_kernel<XF, MX_R128W, EXACT>);
     case MX_R128: return reinterpret_cast<const void*>(&mx_ring_kernel<XF, MX_R128, EXACT>);
     case MX_R64: return reinterpret_cast<const void*>(&mx_ring_kernel<XF, MX_R64, EXACT>);
-    case MX_S16: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 2, EXACT>);
-    case MX_S16N: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 1, EXACT>);
+    case MX_S16: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 2>);
+    case MX_S16N: return reinterpret_cast<const void*>(&mx_skinny_kernel<XF, 1>);
   }
   return nullptr;
 }
@@ -137,7 +137,7 @@ ge_status_t gemm_epilog_mx_execute(ge_mx_handle_t h, int64_t m, const void* x_co
   // a launch keeps its lane count below 2^32
   if (L.grid_x * L.grid_y * L.grid_z * L.waves * 64 >= (int64_t(1) << 32) || L.grid_y > 65535)
     return GE_ERR_NOT_SUPPORTED;
-  const bool exact = h->t.d == GE_MX_D_F32 || h->t.d == GE_MX_D_MXFP8;   // see large_part
+  const bool exact = h->t.d == GE_MX_D_F32 || h->t.d == GE_MX_D_MXFP8;   // see large_part (the skinny kernel always is)
   const auto launch = [&](int cfg, dim3 grid, int waves) {
     const void* fn = h->t.x == GE_MXFP4 ? kernel_of<gemx::FP4, false>(cfg)
                      : exact            ? kernel_of<gemx::FP8, true>(cfg)

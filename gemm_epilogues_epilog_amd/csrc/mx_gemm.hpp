@@ -280,8 +280,11 @@ __device__ __forceinline__ bool mx_place(const MxArgs& p, int id, bool remap, Mx
 // 448 by 0.5 .. 6) span 13 bits, 14 where one of them reaches 2048, and those with the rest
 // lose nothing, so two instructions keep what an fp32 sum keeps, where one leaves 1.3e-5
 // of the result's norm (k = 4096, normal values with outlier channels). Results in 32 or 8
-// bits take two; 16-bit results, whose own rounding is 15 times as coarse in fp16 and 120
-// times in bf16, take one.
+// bits take two. So does the skinny kernel, which waits for W (with one part and with two: one
+// row by 11008 x 4096 9.5 and 9.9 us, 16 by 4096 x 4096 4.9 and 5.0, 512 rows over 64 experts
+// of 2048 x 1024 15.8 and 16.9). 16-bit results of the tile and ring kernels, whose own
+// rounding is 15 times as coarse in fp16 and 120 times in bf16, take one: two cost them 100 x
+// 4096 x 11008 16.7 -> 23.2 us, 1000 x 4096 x 4096 22.6 -> 34, 8192^3 380 -> 645.
 __device__ __forceinline__ i32x4 large_part(i32x4 x) {
   i32x4 r;
 #pragma unroll
@@ -922,9 +925,10 @@ struct MxStep {
 
 constexpr uint32_t kPastRange = 0x7fffffffu;   // rsrc()'s range
 
-template <int XF, int FB, bool EXACT>
+template <int XF, int FB>
 __global__ __launch_bounds__(512, 4) void mx_skinny_kernel(MxArgs p) {
   constexpr int XR = XF == FP8 ? 2 : 1;
+  constexpr bool EXACT = XF == FP8;   // see large_part
   const int nw = blockDim.x >> 6;
   constexpr int ROW = FB * 16 + 4;   // floats per finished row
   __shared__ __attribute__((aligned(16))) f32x4 red[kMxSkinnyWaves][FB][64];
