@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "gemm_epilog.h"
+#include "mx_format.hpp"
 
 namespace gemxh {
 
@@ -51,6 +52,12 @@ ge_status_t check_norm_backward(int64_t rows, int64_t d, ge_dtype_t dt, const vo
                                 int64_t lddr, const void* dx, int64_t lddx, const void* dw, const void* ws,
                                 size_t ws_bytes);
 constexpr int64_t kNormMaxD = 32768;
+// LDS of a row slot's 8-bit rows in the norm's kernel, `walk` rows of `granules` 256-value
+// granules: the rows' 16-byte chunks with an odd stride, then their scales. A workgroup's slots
+// lie one after the other, each on 16 bytes.
+constexpr int norm_stage_bytes(int granules, int walk) {
+  return (int)gemx::pad_to(granules * (16 * (walk + 1) * 16 + 2 * walk * 4), 16);
+}
 // Workgroups of the backward (each adds up the weight gradient of its rows) and the
 // workspace for their sums.
 int64_t norm_backward_groups(int64_t rows, int64_t d);

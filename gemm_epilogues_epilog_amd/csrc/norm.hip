@@ -133,8 +133,6 @@ __device__ __forceinline__ float wave_sum(float v) {
 // slot, and the next row's loads are in flight while this one is summed and written.
 // 16384 x 8192 bf16 with a residual: 189 us to MXFP8 (943 MB, 5.0 TB/s), 210 to bf16 (5.1),
 // without a residual 104; 4096 x 4096 21 us (6.3 TB/s, the 256 MB cache helps).
-// LDS of one slot's 8-bit rows:
-constexpr int norm_stage_bytes(int granules, int walk) { return granules * (16 * (walk + 1) * 16 + 2 * walk * 4); }
 constexpr int wg_of(int nt) { return nt > 64 ? nt : 256; }
 
 template <int DT, int NT, int C, bool VEC>
@@ -155,7 +153,7 @@ __global__ __launch_bounds__(wg_of(NT)) void rms_norm_kernel(NormArgs a) {
   const int granules = (a.d + kKPad - 1) / kKPad, chunks = granules * 16;
   const int64_t row0 = row;
   extern __shared__ __attribute__((aligned(16))) char stage_all[];
-  char* stage = stage_all + slot * norm_stage_bytes(granules, a.walk);
+  char* stage = stage_all + slot * gemxh::norm_stage_bytes(granules, a.walk);
   char* stage_s = stage + chunks * (a.walk + 1) * 16;
   Chunk<DT, VEC> x[C], res[C];
   auto load = [&](int64_t r) {
@@ -479,12 +477,12 @@ ge_status_t gemm_epilog_rms_norm(int64_t rows, int64_t d, ge_dtype_t dt, const v
                                          : gek::norm_fn<gek::BF16, false>(a.d, &nt));
   const int wg = gek::wg_of(nt), rpw = wg / nt;
   // rows one after the other: as many (up to 8) as leave the device 1024 workgroups and,
-  // with an 8-bit result, as fit 72 KB of LDS (two workgroups per compute unit)
+  // with an 8-bit result, as fit 76 KB of LDS (two workgroups per compute unit)
   const int granules = (int)((d + gemx::kKPad - 1) / gemx::kKPad);
   while (a.walk < 8 && rows >= (int64_t)1024 * rpw * a.walk * 2 &&
-         (!codes || rpw * gek::norm_stage_bytes(granules, a.walk * 2) <= 76 * 1024))
+         (!codes || rpw * gemxh::norm_stage_bytes(granules, a.walk * 2) <= 76 * 1024))
     a.walk *= 2;
-  const size_t stage = codes ? (size_t)rpw * gek::norm_stage_bytes(granules, a.walk) : 0;
+  const size_t stage = codes ? (size_t)rpw * gemxh::norm_stage_bytes(granules, a.walk) : 0;
   const int per = rpw * a.walk;
   const int64_t grid = (rows + per - 1) / per;
   if (grid * wg >= (int64_t(1) << 32)) return GE_ERR_NOT_SUPPORTED;

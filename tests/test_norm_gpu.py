@@ -185,3 +185,15 @@ def test_binding_refusals(gpu):
     for args in ((h, x, w), (x[:2], x, w), (x, x, w.double()), (x, x, w, h)):
         with pytest.raises(ValueError):
             norm.rms_norm_backward(*args)
+
+
+@pytest.mark.parametrize("rows", [4, 5, 33])
+@pytest.mark.parametrize("d", [64, 256, 700])
+def test_rows_that_share_a_workgroup_in_8_bits(gpu, d, rows):
+    """Narrow rows to MXFP8, four to a workgroup, with an odd number of 256-value granules: each
+    row's part of the LDS begins on 16 bytes. From fp32 rows the codes are y's, quantised."""
+    x, res, w, _ = data(rows, d, "f32", rows + d)
+    y, q, _ = norm.rms_norm(x.cuda(), w.cuda(), res.cuda(), out="both")
+    c, s = ref.unpack(q.codes.cpu().numpy(), q.scales.cpu().numpy(), rows, d, "mxfp8")
+    wc, ws = ref.quantize(y.cpu().double().numpy(), "mxfp8")
+    assert np.array_equal(c, wc) and np.array_equal(s, ws)
