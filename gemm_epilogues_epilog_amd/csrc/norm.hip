@@ -12,6 +12,7 @@
 // value is read once and written once.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "gemm_epilog.h"
@@ -483,14 +484,26 @@ ge_status_t gemm_epilog_rms_norm(int64_t rows, int64_t d, ge_dtype_t dt, const v
          (!codes || rpw * gemxh::norm_stage_bytes(granules, a.walk * 2) <= 76 * 1024))
     a.walk *= 2;
   const size_t stage = codes ? (size_t)rpw * gemxh::norm_stage_bytes(granules, a.walk) : 0;
-  const int per = rpw * a.walk;
-  const int64_t grid = (rows + per - 1) / per;
-  if (grid * wg >= (int64_t(1) << 32)) return GE_ERR_NOT_SUPPORTED;
-  void* params[] = {&a};
-  return hipLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)wg), params, stage, static_cast<hipStream_t>(stream)) ==
-                 hipSuccess
-             ? GE_OK
-             : GE_ERR_HIP;
+  // a launch keeps its lane count below 2^32: more rows (5.4e8 narrow ones) take several, each
+  // beginning on a row group of the 8-bit result
+  const int64_t per = rpw * a.walk, most = ((int64_t(1) << 32) / wg - 1) * per / 32 * 32;
+  const auto from = [](const void* p, int64_t bytes) {
+    return p ? const_cast<char*>(static_cast<const char*>(p)) + bytes : nullptr;
+  };
+  for (int64_t r = 0; r < rows; r += most) {
+    a.rows = std::min(rows - r, most);
+    a.x = from(x, r * ldx * (int64_t)e);
+    a.res = from(residual, r * ldr * (int64_t)e);
+    a.sum = from(sum, r * lds * (int64_t)e);
+    a.y = from(y, r * ldy * (int64_t)e);
+    a.codes = from(codes, r / 32 * granules * 16 * 512);
+    a.scales = from(scales, r / 32 * granules * gemx::kScaleGranule);
+    void* params[] = {&a};
+    if (hipLaunchKernel(fn, dim3((unsigned)((a.rows + per - 1) / per)), dim3((unsigned)wg), params, stage,
+                        static_cast<hipStream_t>(stream)) != hipSuccess)
+      return GE_ERR_HIP;
+  }
+  return GE_OK;
 }
 
 size_t gemm_epilog_rms_norm_workspace_bytes(int64_t rows, int64_t d) { return gemxh::norm_workspace_bytes(rows, d); }

@@ -197,3 +197,21 @@ def test_rows_that_share_a_workgroup_in_8_bits(gpu, d, rows):
     c, s = ref.unpack(q.codes.cpu().numpy(), q.scales.cpu().numpy(), rows, d, "mxfp8")
     wc, ws = ref.quantize(y.cpu().double().numpy(), "mxfp8")
     assert np.array_equal(c, wc) and np.array_equal(s, ws)
+
+
+def test_more_rows_than_a_launch_of_waves_takes(gpu):
+    """537 million rows of one value: more lanes than one launch has."""
+    rows = 537_000_001
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(rows, 1, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    res = torch.empty_like(x).normal_(generator=g)
+    w = torch.full((1,), 1.5, device="cuda")
+    y, s = norm.rms_norm(x, w, res, eps=0.25)
+    for r in range(0, rows, 1 << 26):
+        part = slice(r, min(rows, r + (1 << 26)))
+        f = x[part].float() + res[part].float()
+        assert torch.equal(s[part], f.to(torch.bfloat16))
+        f = s[part].double()
+        want = f / torch.sqrt(f * f + 0.25) * 1.5
+        b = want.abs() * (U * (1 + HALF["bf16"]) + HALF["bf16"]) + TINY["bf16"]
+        assert ((y[part].double() - want).abs() <= b).all()
