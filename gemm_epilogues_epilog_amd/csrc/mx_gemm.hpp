@@ -88,12 +88,55 @@ __device__ __forceinline__ void mx_act_n(float (&v)[N], int ep) {
   }
 }
 
-// The rows [lo, hi) of expert e; offsets that fall outside 0 .. m or run backwards are
-// held to an empty or valid range, so no row outside X or D is touched.
-__device__ __forceinline__ void expert_rows(const MxArgs& p, int e, int64_t& lo, int64_t& hi) {
-  const int64_t a = p.offsets[e], b = p.offsets[e + 1];
-  lo = a < 0 ? 0 : a > p.m ? p.m : a;
-  hi = b < lo ? lo : b > p.m ? p.m : b;
+// The rows [lo, hi) of 64 experts from e0 on, one to a lane (lanes past the last expert get
+// none). Offsets outside 0 .. m or that run backwards are held to an empty or valid range, and
+// of that the rows up to `end`, the furthest end of the experts before, are taken off: a row
+// has one expert, so no two workgroups write it, and there are at most as many tiles as the
+// launch allows for. `end` moves on for the next 64. Ascending offsets need no look at the other lanes.
+__device__ __forceinline__ void expert_rows(const MxArgs& p, int e0, int& end, int& lo, int& hi) {
+  const int lane = threadIdx.x & 63, m = (int)p.m;
+  int a = 0, b = 0;
+  const bool in = e0 + lane < p.experts;
+  if (in) {
+    a = p.offsets[e0 + lane];
+    b = p.offsets[e0 + lane + 1];
+  }
+  lo = min(max(a, 0), m);
+  hi = max(min(b, m), lo);
+  const int first = __builtin_amdgcn_readlane(lo, 0);
+  if (__builtin_amdgcn_ballot_w64(b < a) == 0 && first >= end) {
+    const int last = __builtin_amdgcn_readlane(hi, 63);
+    if (last > first) end = last;
+    return;
+  }
+  int top = hi > lo ? hi : 0;   // the furthest end up to this lane
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(top, d);
+    if (lane >= d) top = max(top, up);
+  }
+  const int before = __shfl_up(top, 1);
+  lo = max(lo, max(end, lane ? before : 0));
+  hi = max(hi, lo);
+  end = max(end, __builtin_amdgcn_readlane(top, 63));
+}
+// Expert e's alone, without a look at the ones before it.
+__device__ __forceinline__ void offset_rows(const MxArgs& p, int e, int64_t& lo, int64_t& hi) {
+  const int a = p.offsets[e], b = p.offsets[e + 1], m = (int)p.m;
+  lo = min(max(a, 0), m);
+  hi = max(min(b, m), (int)lo);
+}
+// The furthest end of the experts before e.
+__device__ __forceinline__ int end_before(const MxArgs& p, int e) {
+  int end = 0;
+  for (int i = threadIdx.x & 63; i < e; i += 64) {
+    int64_t lo, hi;
+    offset_rows(p, i, lo, hi);
+    if (hi > lo) end = max(end, (int)hi);
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) end = max(end, __shfl_xor(end, d));
+  return end;
 }
 
 // ---- finishing outputs ------------------------------------------------------------
@@ -204,6 +247,11 @@ struct MxPlace {
   int e, tn;
   int64_t row0, lo, hi;
 };
+// Tiles of BM rows over rows [lo, hi).
+template <int BM>
+__device__ __forceinline__ int expert_tiles(int lo, int hi) {
+  return hi > lo ? (int)(((int64_t)hi - (lo & ~31) + BM - 1) / BM) : 0;
+}
 // TAIL 1: without the tiles of a short last round; 2: those only. A last round that fills at
 // most a quarter of the device is left to smaller tiles in a launch of its own, which take
 // under half its time (2200 x 7300 x 4096, 261 tiles on 256 units: e4m3 X to bf16 85 us, now
@@ -213,12 +261,11 @@ template <int BM, int TAIL = 0>
 __device__ __forceinline__ bool mx_place(const MxArgs& p, int id, bool remap, MxPlace& o) {
   int tiles_m = p.tiles_m;
   if (p.experts) {
-    const int lane = threadIdx.x & 63;
-    int total = 0;
+    int total = 0, end = 0;
     for (int e0 = 0; e0 < p.experts; e0 += 64) {
-      int64_t lo = 0, hi = 0;
-      if (e0 + lane < p.experts) expert_rows(p, e0 + lane, lo, hi);
-      int c = hi > lo ? (int)((hi - (lo & ~(int64_t)31) + BM - 1) / BM) : 0;
+      int lo, hi;
+      expert_rows(p, e0, end, lo, hi);
+      int c = expert_tiles<BM>(lo, hi);
 #pragma unroll
       for (int d = 32; d; d >>= 1) c += __shfl_xor(c, d);
       total += c;
@@ -247,11 +294,11 @@ __device__ __forceinline__ bool mx_place(const MxArgs& p, int id, bool remap, Mx
     return true;
   }
   const int lane = threadIdx.x & 63;
-  int base = 0;
+  int base = 0, end = 0;
   for (int e0 = 0; e0 < p.experts; e0 += 64) {
-    int64_t lo = 0, hi = 0;
-    if (e0 + lane < p.experts) expert_rows(p, e0 + lane, lo, hi);
-    const int c = hi > lo ? (int)((hi - (lo & ~(int64_t)31) + BM - 1) / BM) : 0;
+    int lo, hi;
+    expert_rows(p, e0, end, lo, hi);
+    const int c = expert_tiles<BM>(lo, hi);
     int incl = c;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -263,8 +310,8 @@ __device__ __forceinline__ bool mx_place(const MxArgs& p, int id, bool remap, Mx
       const int f = __builtin_ctzll(past);
       o.e = e0 + f;
       const int t = tm - base - (__builtin_amdgcn_readlane(incl, f) - __builtin_amdgcn_readlane(c, f));
-      o.lo = __builtin_amdgcn_readlane((int)lo, f);
-      o.hi = __builtin_amdgcn_readlane((int)hi, f);
+      o.lo = __builtin_amdgcn_readlane(lo, f);
+      o.hi = __builtin_amdgcn_readlane(hi, f);
       o.row0 = (o.lo & ~(int64_t)31) + (int64_t)t * BM;
       return true;
     }
@@ -937,7 +984,7 @@ __global__ __launch_bounds__(512, 4) void mx_skinny_kernel(MxArgs p) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = p.experts ? blockIdx.y : 0;
   int64_t lo = 0, hi = p.m;
-  if (p.experts) expert_rows(p, e, lo, hi);
+  if (p.experts) offset_rows(p, e, lo, hi);
   const int c0 = blockIdx.x * (FB * 16), fg = c0 >> 5;   // first row of W, its row group
   const int64_t gw = group_code_bytes(FP4, p.k), gx = group_code_bytes(XF, p.k), gs = group_scale_bytes(p.k);
   const int64_t wrg = row_groups(p.n);
@@ -1014,6 +1061,15 @@ __global__ __launch_bounds__(512, 4) void mx_skinny_kernel(MxArgs p) {
       __builtin_amdgcn_sched_barrier(0);
       multiply(b1, s + 1);
     }
+    // Rows that are an earlier expert's, by offsets that run backwards, were computed and are
+    // dropped here; the first wave stores. (Looking here at the offsets before e takes 0.4 of
+    // 18.9 us with 512 rows over 64 experts of 2048 x 1024; waiting for them before the products
+    // took 0.8.)
+    int off_a = 0, off_b = 0;
+    if (w == 0 && lane < e) {
+      off_a = p.offsets[lane];
+      off_b = p.offsets[lane + 1];
+    }
 #pragma unroll
     for (int f = 0; f < FB; ++f) red[w][f][lane] = acc[f];
     __syncthreads();
@@ -1038,8 +1094,14 @@ __global__ __launch_bounds__(512, 4) void mx_skinny_kernel(MxArgs p) {
       }
     }
     __syncthreads();
+    int own = 0;   // the first row to keep
+    if (w == 0) {
+      bool back = off_b < off_a;
+      for (int i = lane + 64; i < e; i += 64) back |= p.offsets[i + 1] < p.offsets[i];
+      if (__builtin_amdgcn_ballot_w64(back)) own = end_before(p, e);
+    }
     if (FB == 2 && p.out == MX_OUT_FP8) {
-      if (threadIdx.x < 16 && r0 + threadIdx.x < hi) {
+      if (threadIdx.x < 16 && r0 + threadIdx.x < hi && r0 + threadIdx.x >= own) {
         const int t = threadIdx.x;
         float m = 0.0f;
         for (int c = 0; c < 32; ++c) m = amax2(m, mag(fin[t][c]));
@@ -1055,7 +1117,7 @@ __global__ __launch_bounds__(512, 4) void mx_skinny_kernel(MxArgs p) {
       }
     } else {
       const int t = threadIdx.x / (FB * 2), c = threadIdx.x % (FB * 2) * 8;
-      if (t < 16 && r0 + t < hi) {
+      if (t < 16 && r0 + t < hi && r0 + t >= own) {
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = fin[t][c + j];

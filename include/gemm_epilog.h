@@ -421,7 +421,9 @@ ge_status_t gemm_epilog_mx_plan_info(int64_t n, int64_t k, int64_t experts, ge_m
  *   offsets : by expert: device, experts + 1 int32; expert e has rows offsets[e] ..
  *             offsets[e+1] - 1 of X and D. Read when the kernel runs, so they may come from
  *             a kernel before it. Values outside 0 .. m or that run backwards are held to
- *             valid or empty ranges; rows that no expert has are not written. NULL otherwise.
+ *             valid or empty ranges, and each range to the rows past the furthest end of
+ *             those before it, so that a row has one expert at most; rows that no expert has
+ *             are not written. NULL otherwise.
  *   D       : (m, n) of type d, aligned to its element; or MXFP8 codes, 16-byte aligned
  *             (written with the padding along n, without padding rows).
  *   d_scales: MXFP8 D: its scales; ignored otherwise.
