@@ -215,3 +215,95 @@ def test_more_rows_than_a_launch_of_waves_takes(gpu):
         want = f / torch.sqrt(f * f + 0.25) * 1.5
         b = want.abs() * (U * (1 + HALF["bf16"]) + HALF["bf16"]) + TINY["bf16"]
         assert ((y[part].double() - want).abs() <= b).all()
+
+
+def codes_of(y, fmt="mxfp8"):
+    """(codes, scales) of y (rows, d) in 64 bits on the device, as the reference's quantize."""
+    t = torch.tensor(ref.ELEMENTS[fmt], device=y.device)
+    d = y.shape[1]
+    p = torch.nn.functional.pad(y.double(), (0, -d % 32)).view(y.shape[0], -1, 32)
+    top = p.abs().amax(-1)
+    s = torch.where(top == 0, 0, (torch.frexp(top)[1] - 1 - ref.EMAX[fmt] + 127).clamp(0, 254))
+    a = (p.abs() * torch.exp2(127.0 - s.double())[..., None]).clamp(max=float(t[-1]))
+    hi = torch.searchsorted(t, a).clamp(max=len(t) - 1)
+    lo = (hi - 1).clamp(min=0)
+    up, down = t[hi] - a, a - t[lo]
+    c = torch.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo) + 128 * torch.signbit(p)
+    return c.view(y.shape[0], -1)[:, :d].to(torch.uint8), s.to(torch.uint8)
+
+
+def unpacked(q):
+    """Row-major codes and scales of an MXFP8 operand, on the device."""
+    r, kp = -(-q.rows // 32) * 32, -(-q.k // 256) * 256
+    c = q.codes.view(r // 32, kp // 16, 32, 16).transpose(1, 2).reshape(r, kp)
+    s = q.scales.view(r // 32, kp // 256, 2, 32, 4).permute(0, 3, 1, 4, 2).reshape(r, kp // 32)
+    return c[: q.rows, : q.k], s[: q.rows, : -(-q.k // 32)]
+
+
+def test_device_forms_of_the_reference(gpu):
+    x = torch.randn(70, 300, generator=torch.Generator().manual_seed(2)) * 3
+    x[3, 32:64] = 0
+    c, s = ref.quantize(x.double().numpy(), "mxfp8")
+    c2, s2 = codes_of(x.cuda())
+    assert np.array_equal(c2.cpu().numpy(), c) and np.array_equal(s2.cpu().numpy(), s)
+    c3, s3 = unpacked(mx.mx_quantize(x.cuda(), "mxfp8"))
+    assert torch.equal(c3, c2) and torch.equal(s3, s2)
+
+
+# enough rows for a row slot to take two, four or eight one after the other, the last slot fewer
+@pytest.mark.parametrize("rows,d,unaligned", [(2051, 1101, True), (4099, 2048, False), (8195, 4096, False),
+                                              (8200, 520, False), (8201, 519, True), (33001, 300, True),
+                                              (16389, 8192, False), (9001, 6000, False), (2049, 12000, False),
+                                              (4100, 16001, True), (2050, 32768, False)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_rows(gpu, rows, d, unaligned, dtype):
+    """Row slots that take several rows: the next row's loads in flight, an 8-bit result
+    gathered in LDS, a last slot with fewer rows. In place, and with rows at any alignment."""
+    g = torch.Generator(device="cuda").manual_seed(rows + d)
+    wide = d + (3 if unaligned else 0)
+    make = lambda: torch.randn(rows, wide, generator=g, device="cuda").to(T[dtype])[:, :d]   # noqa: E731
+    x, res = make(), make()
+    w = 1 + 0.3 * torch.randn(d, generator=g, device="cuda")
+    want_s = (x.float() + res.float()).to(T[dtype])
+    q = mx.MXTensor.empty(rows, d, "mxfp8")
+    q.codes.fill_(0xA5)
+    q.scales.fill_(0xA5)
+    y, q, s = norm.rms_norm(x, w, res, eps=1e-5, out="both", sum_out=res, mx_out=q)
+    assert s is res and torch.equal(s, want_s)
+    c, sc = unpacked(q)
+    for r in range(0, rows, 1024):
+        part = slice(r, min(rows, r + 1024))
+        f = want_s[part].double()
+        want = f / torch.sqrt((f * f).mean(1, keepdim=True) + 1e-5) * w.double()
+        b = want.abs() * (U * (1 + HALF[dtype]) + HALF[dtype]) + TINY[dtype]
+        assert ((y[part].double() - want).abs() <= b).all(), r
+        if dtype == "f32":   # y is what was quantised
+            wc, ws = codes_of(y[part])
+            assert torch.equal(c[part], wc) and torch.equal(sc[part], ws), r
+        else:   # a value near the middle of two elements may fall to either
+            top = torch.exp2(sc[part].double() - 127).repeat_interleave(32, 1)[:, :d]
+            v = mx.mx_dequantize(q, "f32")[part].double()
+            assert ((v - want).abs() <= torch.maximum(want.abs() / 8, top * 2.0 ** -10) * (1 + U)).all(), r
+    q2, _ = norm.rms_norm(want_s, w, eps=1e-5, out="mxfp8")
+    c2, s2 = unpacked(q2)
+    assert torch.equal(c2, c) and torch.equal(s2, sc)
+
+
+@pytest.mark.parametrize("rows,d", [(2500, 300), (5000, 512), (2051, 64), (3001, 1100), (1100, 2050), (300, 8191),
+                                    (600, 16384), (300, 32767)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_backward_of_many_rows(gpu, rows, d, dtype):
+    """Row slots that take several rows, several slots to a workgroup."""
+    g = torch.Generator(device="cuda").manual_seed(rows + d)
+    make = lambda: torch.randn(rows, d, generator=g, device="cuda").to(T[dtype])   # noqa: E731
+    s, dy, dres = make() * 2, make(), make()
+    w = 1 + 0.3 * torch.randn(d, generator=g, device="cuda")
+    dx, dw = norm.rms_norm_backward(dy, s, w, dres, eps=1e-5)
+    S, G, R, W = s.double(), dy.double(), dres.double(), w.double()
+    r = 1 / torch.sqrt((S * S).mean(1, keepdim=True) + 1e-5)
+    gw, h = G * W, S * r
+    want = r * (gw - h * (gw * h).mean(1, keepdim=True)) + R
+    err = 2 * U * r * (gw.abs() + h.abs() * (gw * h).abs().mean(1, keepdim=True)) + 2.0 ** -24 * R.abs()
+    assert ((dx.double() - want).abs() <= err * (1 + HALF[dtype]) + HALF[dtype] * want.abs() + TINY[dtype]).all()
+    mags = (G * h).abs().sum(0)
+    assert ((dw.double() - (G * h).sum(0)).abs() <= (U + rows * 2.0 ** -24) * mags * (1 + HALF["f32"]) + TINY["f32"]).all()
