@@ -149,3 +149,78 @@ def test_few_rows_in_16_bits_are_the_fp32_result_rounded(gpu, m, n, k, experts, 
                 assert mm.plan_info(m)["stages"] == 0
                 got.append(mm.execute(X, W, bias, offsets=offsets))
         assert torch.equal(got[0], got[1].to(T[out]))
+
+
+# every configuration that 256 compute units choose, by format of X and result; (128, 64) tiles
+# share k with an MXFP8 X only
+EVERY = [(5, 96, 2048), (5, 8200, 520), (33, 4100, 1101), (40, 4100, 2048), (17, 4100, 3300), (17, 4100, 6144),
+         (70, 8200, 520), (70, 4100, 6144), (60, 16400, 300), (33, 16400, 300), (70, 8200, 6144), (130, 16400, 300), (400, 16400, 300)]
+EVERY_8 = [(5, 96, 2048), (2100, 96, 300), (1100, 96, 300), (1100, 96, 2048), (700, 96, 6144), (2100, 257, 300),
+           (2100, 96, 3300), (60, 16400, 300), (33, 16400, 300), (2100, 257, 6144), (130, 16400, 300), (400, 16400, 300)]
+
+
+def dropped(x, w):
+    """The most that one part drops: 2^-13 of the largest of eight products, for the other seven,
+    with the largest held to the largest x by the largest w of the eight."""
+    def tops(v):
+        return torch.nn.functional.pad(v.abs(), (0, -v.shape[1] % 8)).view(v.shape[0], -1, 8).amax(-1)
+    return 7 * 2.0 ** -13 * (tops(x) @ tops(w).t().contiguous())
+
+
+@pytest.mark.parametrize("x_format,out", [("mxfp8", "f32"), ("mxfp8", "bf16"), ("mxfp8", "f16"), ("mxfp4", "f32"),
+                                          ("mxfp4", "bf16"), ("mxfp4", "f16")])
+@pytest.mark.parametrize("m,n,k", EVERY)
+def test_every_configuration(gpu, m, n, k, x_format, out):
+    """Every value within (k + 2) 2^-23 of the sum of its terms' magnitudes and the result's own
+    rounding, and where a 16-bit result takes one part what that drops; an fp32 result within
+    the bound above in norm."""
+    X, W = operands(m, n, k, x_format)
+    x, w = values(X), values(W)
+    bias = torch.randn(n, generator=torch.Generator().manual_seed(n)).cuda()
+    want = torch.relu(x @ w.t().contiguous() + bias.double())
+    err = (k + 2) * 2.0 ** -23 * (x.abs() @ w.abs().t().contiguous() + bias.double().abs())
+    with mx.MXMatmul(n, k, x_format, "RELU_BIAS", out, vec_dtype="f32") as mm:
+        got = mm.execute(X, W, bias)
+        again = mm.execute(X, W, bias)
+        if x_format == "mxfp8" and out != "f32" and mm.plan_info(m)["stages"]:
+            err = err + dropped(x, w)
+    assert torch.equal(got, again)
+    half = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[out]
+    assert ((got.double() - want).abs() <= err * (1 + half) + half * want + 2.0 ** -25).all()
+    if out == "f32":
+        assert off(got.double(), want) < math.sqrt(k / 8) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("x_format", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("m,n,k", EVERY_8)
+def test_every_configuration_in_8_bits(gpu, m, n, k, x_format):
+    X, W = operands(m, n, k, x_format)
+    bias = torch.randn(n, generator=torch.Generator().manual_seed(n)).cuda()
+    want = values(X) @ values(W).t().contiguous() + bias.double()
+    # (1 + tanh cancels to 0 where the result is small)
+    want = want / (1 + torch.exp(-2 * math.sqrt(2 / math.pi) * (want + 0.044715 * want ** 3)))
+    want_c, want_s = ref.quantize(want.cpu().numpy(), "mxfp8")
+    with mx.MXMatmul(n, k, x_format, "GELU_BIAS", "mxfp8") as mm:
+        got = values(mm.execute(X, W, bias))
+    w8 = torch.from_numpy(ref.values(want_c, want_s, "mxfp8")).cuda()
+    top = torch.from_numpy(np.repeat(np.exp2(want_s.astype(float) - 127), 32, axis=1)[:, :n]).cuda()
+    # a value near the middle of two elements may fall to either
+    assert ((got - w8).abs() <= torch.maximum(w8.abs() / 8, top * 2.0 ** -8)).all()
+    assert off(got, w8) < 2 * math.sqrt(1.13 * math.sqrt(k / 8) * 2.0 ** -23 / 8)
+
+
+@pytest.mark.parametrize("counts,n,k", [([3, 0, 5, 1], 300, 2048), ([1] * 130, 96, 520), ([40, 0, 1, 9], 4100, 300),
+                                        ([140, 0, 11, 49], 4100, 300), ([140, 0, 11, 49], 8200, 300),
+                                        ([300, 0, 300, 0], 8200, 300), ([512, 0, 500], 16400, 520)],
+                         ids=lambda v: f"{len(v)}x{max(v)}" if isinstance(v, list) else None)
+@pytest.mark.parametrize("x_format", ["mxfp8", "mxfp4"])
+def test_8_bit_results_by_expert(gpu, counts, n, k, x_format):
+    E, m = len(counts), sum(counts)
+    X, W = operands(m, n, k, x_format, experts=E)
+    offsets = [0] + np.cumsum(counts).tolist()
+    want = by_expert(values(X), values(W), offsets)
+    want_c, want_s = ref.quantize(want.cpu().numpy(), "mxfp8")
+    with mx.MXMatmul(n, k, x_format, "NONE", "mxfp8", experts=E) as mm:
+        got = values(mm.execute(X, W, offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda")))
+    w8 = torch.from_numpy(ref.values(want_c, want_s, "mxfp8")).cuda()
+    assert off(got, w8) < 2 * math.sqrt(math.sqrt(k / 8) * 2.0 ** -23 / 8)

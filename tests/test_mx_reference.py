@@ -265,3 +265,18 @@ def test_binding_refuses_host_tensors():
     for kw in (dict(x_format="f16"), dict(epilog="SWISH"), dict(out="u8"), dict(vec_dtype="f64"), dict(experts=0)):
         with pytest.raises(ValueError):
             mx.MXMatmul(64, 64, **kw)
+
+
+def test_accuracy_shapes_reach_every_configuration_and_split():
+    """The shapes of the accuracy tests take every tile, whole and with k shared between
+    workgroups, on 256 compute units, by format of X and type of result."""
+    from tests import test_mx_accuracy_gpu as gpu
+    whole = {(16, 16, False), (16, 32, False), (64, 64, False), (128, 64, False), (128, 128, False), (128, 256, False),
+             (256, 256, False)}
+    for fmt in ("mxfp8", "mxfp4"):
+        split = {(64, 64, True), (128, 128, True)} | ({(128, 64, True)} if fmt == "mxfp8" else set())
+        for out in ("f32", "bf16", "f16", "mxfp8"):
+            seen = {gpu.takes(mx.MXMatmul(n, k, fmt, "NONE", out), m)
+                    for m, n, k in (gpu.EVERY_8 if out == "mxfp8" else gpu.EVERY)}
+            need = (whole | split) - ({(16, 16, False)} if out == "mxfp8" else set())   # 8 bits take whole blocks of 32
+            assert need <= seen, (fmt, out, sorted(need - seen))
