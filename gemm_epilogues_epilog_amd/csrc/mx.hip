@@ -133,7 +133,6 @@ ge_status_t gemm_epilog_mx_execute(ge_mx_handle_t h, int64_t m, const void* x_co
   a.ep = (int32_t)h->ep;
   a.out = (int32_t)h->t.d;
   a.vec = (int32_t)h->t.vec;
-  a.group_m = L.group_m;
   // a launch keeps its lane count below 2^32
   if (L.grid_x * L.grid_y * L.grid_z * L.waves * 64 >= (int64_t(1) << 32) || L.grid_y > 65535)
     return GE_ERR_NOT_SUPPORTED;

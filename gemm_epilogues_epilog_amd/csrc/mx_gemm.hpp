@@ -39,7 +39,6 @@ struct MxArgs {
   int32_t tiles_m, tiles_n;
   int32_t splits;          // parts of the k loop
   int32_t ep, out, vec;
-  int32_t group_m;
   int32_t round;           // tile kernel: its workgroups, if a short last round is left over
   int32_t tail;            // ring kernel: takes what the tile kernel left over
 };
@@ -280,9 +279,9 @@ __device__ __forceinline__ bool mx_place(const MxArgs& p, int id, bool remap, Mx
   if (TAIL == 2) id += G;
   if (id >= (TAIL == 2 ? all : G)) return false;
   const int pos = remap ? xcd_remap(id, G) : id;   // each XCD takes a run of the order
-  const int gsz = p.group_m * p.tiles_n;
-  const int g = pos / gsz, first = g * p.group_m;
-  const int rows = min(tiles_m - first, p.group_m);
+  const int gsz = kMxGroupM * p.tiles_n;
+  const int g = pos / gsz, first = g * kMxGroupM;
+  const int rows = min(tiles_m - first, kMxGroupM);
   const int in = pos - g * gsz;
   const int tm = __builtin_amdgcn_readfirstlane(first + in % rows);
   o.tn = __builtin_amdgcn_readfirstlane(in / rows);

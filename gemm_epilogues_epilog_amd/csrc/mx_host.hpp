@@ -36,7 +36,6 @@ struct MxLaunch {
   int tiles_m = 0, tiles_n = 0;   // grouped: the most tiles of rows there can be
   int splits = 1;
   int waves = 0;             // of a workgroup
-  int group_m = 8;
   bool tail = false;         // a second launch takes (or may take, by expert) a short last round
   int64_t grid_x = 0, grid_y = 1, grid_z = 1;
 };

@@ -33,6 +33,9 @@ constexpr int mx_waves(const MxTile& t) { return (t.bm / 32 / t.mb) * (t.bn / 32
 constexpr int kMxSkinnyWaves = 8;   // at most
 constexpr int kMxTailCfg = MX_R128W;   // quarters of the tile kernel's tiles, for its short last rounds
 static_assert(kMxTiles[MX_L].bm == 2 * kMxTiles[kMxTailCfg].bm && kMxTiles[MX_L].bn == 2 * kMxTiles[kMxTailCfg].bn, "quarters");
+// Tiles go down this many rows of tiles before the next column, so that neighbours share W and X
+// in the L2.
+constexpr int kMxGroupM = 8;
 // k values of one LDS stage: 128 bytes of a row of X.
 constexpr int mx_bk(int xfmt) { return xfmt == FP4 ? 256 : 128; }
 

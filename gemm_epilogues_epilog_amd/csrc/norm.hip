@@ -55,7 +55,7 @@ struct Chunk {
 #pragma unroll
       for (int j = 0; j < W; ++j) raw[j] = reinterpret_cast<const i32x4*>(q)[j];
     } else {
-if (n >= 8) {
+      if (n >= 8) {
         __builtin_memcpy(raw, q, sizeof(raw));
       } else {
         using U = std::conditional_t<DT == F32, uint32_t, uint16_t>;
