@@ -770,9 +770,9 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * 64), 2) void mx_tile_kernel(
 // group fill the waits of the other; their sums are added through LDS at the end.
 // Per round one barrier; the LDS reads of the next k-tile and the copies of a later one run
 // beside the products of this one. A k-tile's time is its copies' and reads', 0.17 us
-// (64 x 64) to 0.88 us (128 x 256) with e4m3 X, against 0.04 to 0.28 us of products. Measured
-// with W from memory: 100 x 4096 x 11008 16.7 us (W alone is 3.8 us of reading), 1000 x 4096 x
-// 4096 19.7 us (1700 TFLOP/s).
+// (64 x 64) to 0.88 us (128 x 256) with e4m3 X, against 0.04 to 0.28 us of products. 100 x 4096 x
+// 11008 takes 16.5 us with W from memory (W alone is 3.8 us of reading) and 15.2 with three W in
+// turn, which the 256 MB cache holds; 1000 x 4096 x 4096 21 us (1600 TFLOP/s).
 template <int XF, int CFG, bool EXACT>
 __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * MxCfgT<XF, CFG>::KG * 64), 1) void mx_ring_kernel(MxArgs p) {
   using C = MxCfgT<XF, CFG>;
@@ -944,9 +944,9 @@ __global__ __launch_bounds__((MxCfgT<XF, CFG>::NW * MxCfgT<XF, CFG>::KG * 64), 1
 // lane, consecutive lines) and add their sums through LDS in wave order. 16x16x128
 // products: lane l holds row l % 16 and the 32 k of quarter l / 16 of a 128-k step.
 // Rows of X are addressed one by one, so an expert's rows may start anywhere.
-// One row by W from memory: 32768 x 8192 26 us (5.5 TB/s of W), 11008 x 4096 8.8 us and
-// 4096 x 11008 8.9 us (2.7 TB/s: the launch, the first reads and the joining of the waves take
-// about 4 us); 48 rows over 32 experts of 1376 x 4096 11.7 us.
+// One row by W from memory: 32768 x 8192 29 us (4.9 TB/s of W), 11008 x 4096 10.1 us and
+// 4096 x 11008 10.0 us (2.4 TB/s: the launch, the first reads and the joining of the waves take
+// about 4 us); 48 rows over 32 experts of 1376 x 4096 16.4 us.
 template <int XF, int S>
 __device__ __forceinline__ f32x4 mx_mma16(i32x4 w, const i32x4 (&x)[XF == FP8 ? 2 : 1], f32x4 c, int sw, int sx) {
   const i32x8 a = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};

@@ -8,8 +8,14 @@
 //   dx = r (g - h mean(g h)) + dresidual, g = dy w, h = s r;   dw = sum over rows of dy h
 // The 8-bit result passes the gradient straight through.
 //
-// Bound by memory: a row stays in registers between its sums and its result, so each
-// value is read once and written once.
+// Bound by memory: a row stays in registers between its sums and its result, so each value is
+// read once and written once. That holds up to 8192 values (the gradient of fp32 rows at any
+// alignment spills 56 bytes a lane from 4096 on). Longer rows take 1024 lanes of 128 registers:
+// with 16-byte aligned rows the forward still spills nothing, the gradient 148 to 244 bytes a lane
+// from 16384 values on; at any other alignment the forward spills 36 to 156 bytes up to 16384 values
+// and 276 to 708 above, the gradient 296 to 416 and 1040 to 1160. 4096 rows of bf16 with a residual, to
+// bf16 and the gradient: 16384 values 109 and 116 us (4.9 and 4.7 TB/s), 16383 174 and 418, 32768
+// 213 and 400, 32767 756 and 1789.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

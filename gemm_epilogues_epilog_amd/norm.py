@@ -3,7 +3,7 @@ gemm_epilog_rms_norm, gemm_epilog_rms_norm_backward in include/gemm_epilog.h).
 
 y, s = rms_norm(x, weight, residual)                    # s = x + residual, y = norm(s) weight
 q, s = rms_norm(x, weight, residual, out="mxfp8")       # y in 8 bits, the X of MXMatmul
-y, q, s = rms_norm(x, weight, residual, out="both")     # y as x's type for a router, q for the experts
+y, q, s = rms_norm(x, weight, residual, out="both")     # y in x's type as well, for what is not quantised
 dx, dweight = rms_norm_backward(dy, s, weight, dresidual)
 """
 from typing import Optional

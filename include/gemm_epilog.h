@@ -372,8 +372,9 @@ typedef enum { GE_MX_D_F32 = 0, GE_MX_D_F16 = 1, GE_MX_D_BF16 = 2, GE_MX_D_MXFP8
  * MXFP4 fits in that whole. An MXFP8 X does not: for an fp32 or MXFP8 D, and for any D where
  * the rows are few (plan_info gives stages 0), X is multiplied in two parts that do, and the
  * sums are fp32's (2.5e-8 of the result's norm at k = 4096). A 16-bit D of more rows takes one
- * part, 1.3e-5 of the norm of the sums: below the result's own rounding, unless a bias cancels
- * most of a sum. */
+ * part, 1.3e-5 of the norm of the sums (its own rounding is 2e-4 of it in fp16, 1.7e-3 in bf16):
+ * a value far below the others, its terms or its sum and bias having cancelled, can be off by
+ * more than its own rounding. */
 typedef struct {
   ge_mx_format_t x;
   ge_mx_out_t d;
@@ -388,6 +389,7 @@ typedef struct ge_mx_plan* ge_mx_handle_t; /* opaque; owned by the library */
  *   experts : 0 for one product; 1 .. 4096 for products by expert, where the rows of X
  *             are sorted by expert and each expert has its own W and bias.
  *   ep      : NONE, BIAS, RELU_BIAS or GELU_BIAS (other epilogues: GE_ERR_NOT_SUPPORTED).
+ *             As above, the ReLU keeps a value only where it is > 0: of NaN it gives 0.
  * Allocates the workspace (sums of a product whose k loop is split over workgroups). A
  * plan may be used from one stream at a time; any number of weights may share it.
  */
@@ -447,10 +449,12 @@ ge_status_t gemm_epilog_mx_free(ge_mx_handle_t h);
  *   sum      : receives s, row stride lds; needed with a residual, optional without. May be
  *              x or residual itself.
  *   y        : receives y as dt, row stride ldy; NULL if not wanted.
- *   codes, scales : receive y as MXFP8, with zeros in the padding along d (padding rows are
- *              not written); both NULL if not wanted. At least one form of y is needed.
+ *   codes, scales : receive y as MXFP8, with zeros in the padding along d (NaN in a row that
+ *              is NaN; padding rows are not written); both NULL if not wanted. At least one
+ *              form of y is needed. Their size limits rows and d as for an operand (above:
+ *              GE_ERR_NOT_SUPPORTED).
  * Pointers are aligned to their elements (codes and scales to 16 bytes); 16-byte aligned
- * rows with d a multiple of 8 run fastest.
+ * rows with d a multiple of 8 run fastest, by far so where d is over 8192.
  */
 ge_status_t gemm_epilog_rms_norm(int64_t rows, int64_t d, ge_dtype_t dt, const void* x, int64_t ldx,
                                  const void* residual, int64_t ldr, const void* weight, ge_dtype_t wdt, float eps,
