@@ -391,7 +391,9 @@ typedef struct ge_mx_plan* ge_mx_handle_t; /* opaque; owned by the library */
  *   ep      : NONE, BIAS, RELU_BIAS or GELU_BIAS (other epilogues: GE_ERR_NOT_SUPPORTED).
  *             As above, the ReLU keeps a value only where it is > 0: of NaN it gives 0.
  * Allocates the workspace (sums of a product whose k loop is split over workgroups). A
- * plan may be used from one stream at a time; any number of weights may share it.
+ * plan may be used from one stream at a time; any number of weights may share it. Its
+ * executes run on the device that was current when it was made, which has to be current
+ * again, with that device's pointers.
  */
 ge_status_t gemm_epilog_mx_plan(int64_t n, int64_t k, int64_t experts, ge_mx_types_t types, ge_epilog_t ep,
                                 ge_mx_handle_t* out);
