@@ -9,7 +9,8 @@ gemm_epilog_plan, gemm_epilog_plan_ex, gemm_epilog_plan_info, gemm_epilog_execut
 gemm_epilog_execute_noalloc, gemm_epilog_autotune, gemm_epilog_lost_waits,
 gemm_epilog_free, gemm_epilog_aux_bytes, gemm_epilog_workspace_bytes,
 gemm_epilog_describe, gemm_epilog_status_string. The microscaled operators
-(gemm_epilog_mx_*) are wrapped in mx.py, the norm (gemm_epilog_rms_norm*) in norm.py.
+(gemm_epilog_mx_*) are wrapped in mx.py, the norm (gemm_epilog_rms_norm*) in norm.py, the
+gated feed-forward block (gemm_epilog_gated_*) in gated.py.
 Pointers may be given as torch tensors (device memory), integers or None.
 
 `Matmul` wraps them in the stateful plan / execute / free object with a context
@@ -44,10 +45,13 @@ EXPORTS = ("gemm_epilog_plan", "gemm_epilog_plan_ex", "gemm_epilog_plan_info", "
            "gemm_epilog_mx_code_bytes", "gemm_epilog_mx_scale_bytes", "gemm_epilog_mx_quantize",
            "gemm_epilog_mx_dequantize", "gemm_epilog_mx_pack", "gemm_epilog_mx_plan", "gemm_epilog_mx_plan_info",
            "gemm_epilog_mx_execute", "gemm_epilog_mx_free",
-           "gemm_epilog_rms_norm", "gemm_epilog_rms_norm_workspace_bytes", "gemm_epilog_rms_norm_backward")
+           "gemm_epilog_rms_norm", "gemm_epilog_rms_norm_workspace_bytes", "gemm_epilog_rms_norm_backward",
+           "gemm_epilog_gated_forward", "gemm_epilog_gated_down", "gemm_epilog_gated_workspace_bytes",
+           "gemm_epilog_gated_backward")
 MXFP4, MXFP8 = 0, 1
 MX_FORMATS = {"mxfp4": MXFP4, "mxfp8": MXFP8}
 MX_OUT = {"f32": 0, "f16": 1, "bf16": 2, "mxfp8": 3}
+GATES = {"SILU": 0, "GELU": 1, "RELU": 2}
 OP_N, OP_T = 0, 1
 
 
@@ -131,7 +135,11 @@ def load() -> ctypes.CDLL:
             ("rms_norm", [i64, i64, c_int, vp, i64, vp, i64, vp, c_int, f32, vp, i64, vp, i64, vp, vp, vp], c_int),
             ("rms_norm_workspace_bytes", [i64, i64], size),
             ("rms_norm_backward", [i64, i64, c_int, vp, i64, vp, i64, vp, c_int, f32, vp, i64, vp, i64, vp, vp, size, vp],
-             c_int)):
+             c_int),
+            ("gated_forward", [i64, i64, i64, c_int, c_int, vp, vp, vp, c_int, vp, vp, vp], c_int),
+            ("gated_down", [i64, i64, i64, c_int, vp, vp, vp, vp], c_int),
+            ("gated_workspace_bytes", [i64, i64, i64, i64, c_int], size),
+            ("gated_backward", [i64, i64, i64, i64, c_int, c_int, *[vp] * 10, c_int, vp, size, vp], c_int)):
         fn = getattr(L, "gemm_epilog_" + name)
         fn.argtypes, fn.restype = args, res
     _lib = L

@@ -11,6 +11,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 #include <cstdio>
 #include <cstdlib>
@@ -23,6 +24,7 @@
 #include "gemm_epilog.h"
 #include "launch.hpp"
 #include "plan_host.hpp"
+#include "product.hpp"
 
 struct ge_plan {
   int64_t m;
@@ -215,6 +217,52 @@ __global__ void clear_words_kernel(uint32_t* p, int n) {
   if (i < n) p[i] = 0u;
 }
 }  // namespace gek
+
+namespace gei {
+
+ge_status_t current_device(int* cus) {
+  static std::atomic<int> known[kMaxDevices] = {};   // compute units + 1 of a gfx950, -1 of another device
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return GE_ERR_HIP;
+  if (dev < 0 || dev >= kMaxDevices) return GE_ERR_NOT_SUPPORTED;
+  int c = known[dev].load(std::memory_order_relaxed);
+  if (c == 0) {
+    int n = 0;
+    const ge_status_t st = query_device(&dev, &n);
+    if (st == GE_ERR_HIP) return st;
+    c = st == GE_OK ? n + 1 : -1;
+    known[dev].store(c, std::memory_order_relaxed);
+  }
+  if (c < 0) return GE_ERR_NOT_SUPPORTED;
+  *cus = c - 1;
+  return GE_OK;
+}
+
+ge_status_t run_product(int64_t m, int n, int k, ge_dtype_t dt, const geh::Layout& L, const void* A, const void* B,
+                        void* D, char* ws, hipStream_t s) {
+  ge_plan h;
+  h.m = m;
+  h.n = n;
+  h.k = k;
+  h.dt = {dt, dt, dt};
+  h.ep = GE_EPILOG_NONE;
+  h.L = L;
+  h.gemm = lookup(dt, GE_EPILOG_NONE, L.cfg, L.lay);
+  if (!h.gemm) return GE_ERR_NOT_SUPPORTED;
+  h.ws = ws;
+  h.spin_limit = kSkSpinDefault;
+  if (L.sk_wgs) {
+    uint32_t* words = reinterpret_cast<uint32_t*>(ws + L.off_sk_flag);
+    int nw = gek::kSkFlagWords;
+    void* params[] = {&words, &nw};
+    if (hipLaunchKernel(reinterpret_cast<const void*>(&gek::clear_words_kernel), dim3(gek::kSkFlagWords / 256), dim3(256),
+                        params, 0, s) != hipSuccess)
+      return GE_ERR_HIP;
+  }
+  return enqueue(h, ws, 1u, A, B, nullptr, D, nullptr, nullptr, s);
+}
+
+}  // namespace gei
 
 extern "C" {
 

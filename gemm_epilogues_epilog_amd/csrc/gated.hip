@@ -1,0 +1,260 @@
+// The gated feed-forward block: entry points and small kernels.
+//   H = act(G) * U, [G | U] = X W^T + bias;  Y = H Wd^T
+//   dH = dY Wd;  dG = dH U a'(G), dU = dH a(G);  dX = dZ W, dW = dZ^T X, dWd = dY^T H
+// with dZ = [dG | dU], so that both projections' products are one.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+#include <type_traits>
+
+#include "gated_general.hpp"
+#include "gated_host.hpp"
+#include "product.hpp"
+
+namespace gek {
+namespace {
+
+// Eight values of a row of len from pos on (zeros past its end), widened.
+template <int DT>
+__device__ __forceinline__ void load8(const void* row, int64_t pos, int64_t len, float (&v)[8]) {
+  constexpr int ES = Tr<DT>::es, E = 16 / ES;
+  const char* p = static_cast<const char*>(row);
+  i32x4 raw[8 / E];
+#pragma unroll
+  for (int j = 0; j < 8 / E; ++j)
+    raw[j] = pos + 8 <= len ? load16(p + (pos + j * E) * ES) : load_end<ES>(p, pos + j * E, len);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (DT == F32) v[e] = __int_as_float(raw[e / 4][e % 4]);
+    else v[e] = Tr<DT>::widen((uint16_t)((uint32_t)raw[0][e / 2] >> (16 * (e & 1))));
+  }
+}
+template <int DT>
+__device__ __forceinline__ void store8(void* row, int64_t pos, int64_t len, const float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float q[4] = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+    store4<DT>(row, pos + 4 * h, len - pos - 4 * h, q);
+  }
+}
+
+// dZ from dH and Z, eight columns a thread. Bound by memory: reads dH and Z, writes dZ.
+template <int DT, int DH>
+__global__ __launch_bounds__(256) void dz_kernel(const void* dh, const void* z, void* dz, int64_t m, int64_t n, int act) {
+  constexpr int64_t es = Tr<DT>::es;
+  const int cpr = (int)((n + 7) / 8);   // chunks of a row
+  const int64_t first = (int64_t)blockIdx.x * 256, row0 = first / cpr;
+  const int at = (int)(first - row0 * cpr) + threadIdx.x;
+  const int64_t row = row0 + at / cpr, pos = (int64_t)(at % cpr) * 8;
+  if (row >= m) return;
+  float d[8], g[8], u[8], dg[8], du[8];
+  load8<DH>(static_cast<const char*>(dh) + row * n * Tr<DH>::es, pos, n, d);
+  const char* zr = static_cast<const char*>(z) + row * 2 * n * es;
+  load8<DT>(zr, pos, n, g);
+  load8<DT>(zr + n * es, pos, n, u);
+  with_gate(act, [&](auto a) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float v, s;
+      gate_slope<decltype(a)::value, DT == F32>(g[e], v, s);
+      dg[e] = d[e] * u[e] * s;
+      du[e] = d[e] * v;
+    }
+  });
+  char* o = static_cast<char*>(dz) + row * 2 * n * es;
+  store8<DT>(o, pos, n, dg);
+  store8<DT>(o + n * es, pos, n, du);
+}
+
+// partial[part][col]: sums of the columns of a dense (m, cols) matrix over the part's rows, in a
+// fixed order: four rows side by side, each in ascending order, then those four in order.
+template <int DT>
+__global__ __launch_bounds__(256) void colsum_kernel(const void* x, int64_t m, int64_t cols, float* partial) {
+  constexpr int U = 4;
+  __shared__ float sums[4][64][9];
+  const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int64_t pos = ((int64_t)blockIdx.x * 64 + c) * 8;
+  const int64_t r0 = m * blockIdx.y / gridDim.y, r1 = m * (blockIdx.y + 1) / gridDim.y;
+  const char* p = static_cast<const char*>(x);
+  float s[8] = {};
+  if (pos < cols) {
+    for (int64_t r = r0 + q; r < r1; r += 4 * U) {
+      float v[U][8];
+#pragma unroll
+      for (int i = 0; i < U; ++i) load8<DT>(p + (r + 4 * i < r1 ? r + 4 * i : r) * cols * Tr<DT>::es, pos, cols, v[i]);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += r + 4 * i < r1 ? v[i][e] : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[q][c][e] = s[e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 512; i += 256) {
+    const int64_t col = (int64_t)blockIdx.x * 512 + i;
+    if (col < cols)
+      partial[(int64_t)blockIdx.y * cols + col] =
+          ((sums[0][i / 8][i % 8] + sums[1][i / 8][i % 8]) + sums[2][i / 8][i % 8]) + sums[3][i / 8][i % 8];
+  }
+}
+
+template <int DT, int OUT, int LAY>
+const void* gen_of(bool large) {
+  return large ? reinterpret_cast<const void*>(&gen_kernel<DT, OUT, LAY, 128, 128, 64>)
+               : reinterpret_cast<const void*>(&gen_kernel<DT, OUT, LAY, 64, 64, 32>);
+}
+template <int DT>
+const void* gen_kernel_of(int lay, bool f32_out, bool large) {
+  switch (lay) {
+    case 0: return f32_out ? gen_of<DT, F32, 0>(large) : gen_of<DT, DT, 0>(large);
+    case 1: return gen_of<DT, DT, 1>(large);
+    case 2: return gen_of<DT, DT, 2>(large);
+    default: return gen_of<DT, DT, 6>(large);
+  }
+}
+
+hipError_t launch(const void* fn, dim3 grid, int threads, void** params, hipStream_t s) {
+  return hipLaunchKernel(fn, grid, dim3(threads), params, 0, s);
+}
+
+// The general kernel. lay 6: gated, N columns of D from 2 N rows of B.
+hipError_t general(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, const void* A, const void* B, void* D,
+                   bool f32_out, const void* bias, int vec, int act, void* Z, int cus, hipStream_t s) {
+  GenArgs a;
+  a.A = A;
+  a.B = B;
+  a.bias = bias;
+  a.D = D;
+  a.Z = Z;
+  a.m = M;
+  a.n = N;
+  a.k = K;
+  a.lda = lay & 1 ? M : K;
+  a.ldb = lay & 2 ? K : N;
+  a.ldd = N;
+  a.vec = vec;
+  a.act = act;
+  // the large tile where it gives every compute unit one
+  const auto tiles = [&](int t) { return (M + t - 1) / t * ((N + (lay == 6 ? t / 2 : t) - 1) / (lay == 6 ? t / 2 : t)); };
+  const bool large = tiles(128) >= cus;
+  const int t = large ? 128 : 64;
+  a.tiles_m = (int)((M + t - 1) / t);
+  a.tiles_n = (int)(tiles(t) / a.tiles_m);
+  const void* fn = dt == GE_F32   ? gen_kernel_of<F32>(lay, f32_out, large)
+                   : dt == GE_F16 ? gen_kernel_of<F16>(lay, f32_out, large)
+                                  : gen_kernel_of<BF16>(lay, f32_out, large);
+  void* params[] = {&a};
+  return launch(fn, dim3((unsigned)tiles(t)), large ? 256 : 128, params, s);
+}
+
+// D (M, N) of type dt = A . B; `ws` for the k loop's split.
+ge_status_t product(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, const void* A, const void* B, void* D,
+                    char* ws, size_t ws_bytes, int cus, hipStream_t s) {
+  if (K > 0 && gegh::fast_shape(M, N, K, dt, lay) && gegh::aligned(A, 16) && gegh::aligned(B, 16) &&
+      gegh::aligned(D, 16)) {
+    geh::Layout L;
+    if (ge_status_t st = gegh::fast_layout(M, N, K, dt, lay, cus, ws_bytes, &L); st != GE_OK) return st;
+    return gei::run_product(M, (int)N, (int)K, dt, L, A, B, D, ws, s);
+  }
+  return general(M, N, K, dt, lay, A, B, D, false, nullptr, F32, 0, nullptr, cus, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
+}
+
+ge_status_t column_sums(const void* x, int64_t m, int64_t cols, ge_dtype_t dt, void* out, ge_dtype_t vec, float* partial,
+                        hipStream_t s) {
+  int parts = m ? (int)gegh::colsum_parts(m, cols) : 0;
+  if (parts) {
+    const void* fn = dt == GE_F32   ? reinterpret_cast<const void*>(&colsum_kernel<F32>)
+                     : dt == GE_F16 ? reinterpret_cast<const void*>(&colsum_kernel<F16>)
+                                    : reinterpret_cast<const void*>(&colsum_kernel<BF16>);
+    void* params[] = {&x, &m, &cols, &partial};
+    if (launch(fn, dim3((unsigned)((cols + 511) / 512), parts), 256, params, s) != hipSuccess) return GE_ERR_HIP;
+  }
+  return launch_bgrad_reduce(partial, parts, cols, out, (int)vec, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
+}
+
+template <int DT>
+const void* dz_of(bool f32_dh) {
+  return f32_dh ? reinterpret_cast<const void*>(&dz_kernel<DT, F32>) : reinterpret_cast<const void*>(&dz_kernel<DT, DT>);
+}
+
+}  // namespace
+}  // namespace gek
+
+extern "C" {
+
+ge_status_t gemm_epilog_gated_forward(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, ge_gate_t act, const void* x,
+                                      const void* w, const void* bias, ge_dtype_t vec, void* h, void* z, void* stream) {
+  if (ge_status_t st = gegh::check_forward(m, n, k, dt, act, x, w, bias, vec, h, z); st != GE_OK) return st;
+  if (m == 0) return GE_OK;
+  int cus = 0;
+  if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return gek::general(m, n, k, dt, 6, x, w, h, false, bias, (int)vec, (int)act, z, cus, s) == hipSuccess ? GE_OK
+                                                                                                      : GE_ERR_HIP;
+}
+
+ge_status_t gemm_epilog_gated_down(int64_t m, int64_t d, int64_t n, ge_dtype_t dt, const void* h, const void* w_down,
+                                   void* y, void* stream) {
+  if (ge_status_t st = gegh::check_down(m, d, n, dt, h, w_down, y); st != GE_OK) return st;
+  if (m == 0) return GE_OK;
+  int cus = 0;
+  if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
+  return gek::product(m, d, n, dt, 2, h, w_down, y, nullptr, 0, cus, static_cast<hipStream_t>(stream));
+}
+
+size_t gemm_epilog_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t d, ge_dtype_t dt) {
+  return gegh::backward_space(m, n, k, d, dt).total;
+}
+
+ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t d, ge_dtype_t dt, ge_gate_t act,
+                                       const void* dy, const void* x, const void* w, const void* z, const void* h,
+                                       const void* w_down, void* dx, void* dw, void* dw_down, void* dbias,
+                                       ge_dtype_t vec, void* workspace, size_t workspace_bytes, void* stream) {
+  const gegh::Backward b = {dy, x, w, z, h, w_down, dx, dw, dw_down, dbias};
+  if (ge_status_t st = gegh::check_backward(m, n, k, d, dt, act, b, vec, workspace, workspace_bytes); st != GE_OK)
+    return st;
+  int cus = 0;
+  if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const gegh::BackwardSpace at = gegh::backward_space(m, n, k, d, dt);
+  char* ws = static_cast<char*>(workspace);
+  char* dz = ws;
+  char* scratch = ws + at.scratch;
+  const size_t scratch_bytes = workspace_bytes - at.scratch;   // (m = 0: nothing, and nothing is needed)
+
+  if (m > 0) {
+    const void* dh = dy;
+    bool f32 = false;
+    if (w_down) {
+      dh = ws + at.dh;
+      f32 = true;
+      if (gek::general(m, n, d, dt, 0, dy, w_down, ws + at.dh, true, nullptr, 0, 0, nullptr, cus, s) != hipSuccess)
+        return GE_ERR_HIP;
+    }
+    const void* fn = dt == GE_F32   ? gek::dz_of<gek::F32>(f32)
+                     : dt == GE_F16 ? gek::dz_of<gek::F16>(f32)
+                                    : gek::dz_of<gek::BF16>(f32);
+    int a = (int)act;
+    void* params[] = {&dh, &z, &dz, &m, &n, &a};
+    const int64_t chunks = m * ((n + 7) / 8);
+    if (gek::launch(fn, dim3((unsigned)((chunks + 255) / 256)), 256, params, s) != hipSuccess) return GE_ERR_HIP;
+    if (dx)
+      if (ge_status_t st = gek::product(m, k, 2 * n, dt, 0, dz, w, dx, scratch, scratch_bytes, cus, s); st != GE_OK)
+        return st;
+  }
+  if (dw)
+    if (ge_status_t st = gek::product(2 * n, k, m, dt, 1, dz, x, dw, nullptr, 0, cus, s); st != GE_OK) return st;
+  if (dw_down)
+    if (ge_status_t st = gek::product(d, n, m, dt, 1, dy, h, dw_down, nullptr, 0, cus, s); st != GE_OK) return st;
+  if (dbias)
+    if (ge_status_t st =
+            gek::column_sums(dz, m, 2 * n, dt, dbias, vec, reinterpret_cast<float*>(scratch), s);
+        st != GE_OK)
+      return st;
+  return GE_OK;
+}
+
+}  // extern "C"

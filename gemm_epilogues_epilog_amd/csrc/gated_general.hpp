@@ -1,0 +1,278 @@
+// General product kernel of the gated feed-forward operators: fp32, and 16-bit operands whose
+// rows are not whole 16-byte chunks (odd sizes, any alignment).
+//
+// D = A . B over 128 x 128 or 64 x 64 tiles, operands in any of the storage orders below, copied
+// through registers into two LDS buffers of "row = m or n, 128 bytes of k" whatever the order
+// (mn-major operands are transposed in registers on the way). Every load is 16 bytes at the
+// elements' alignment. At the end of a row the load is moved back to the row's last 16 bytes
+// and its value shifted, so that nothing past a row is read and nothing branches per element;
+// rows of fewer than 16 bytes are read one element at a time.
+// fp32 runs v_mfma_f32_32x32x2 and is bound by it (157 TFLOP/s).
+#pragma once
+
+#include <type_traits>
+
+#include "gated_math.hpp"
+
+namespace gek {
+
+struct GenArgs {
+  const void* A;
+  const void* B;
+  const void* bias;
+  void* D;
+  void* Z;            // gated: receives [G | U] (m, 2 n), or null
+  int64_t m, n, k;    // gated: n columns of D, 2 n rows of B
+  int64_t lda, ldb, ldd;   // elements between stored rows
+  int32_t vec;        // type of bias
+  int32_t act;
+  int32_t tiles_m, tiles_n;
+};
+
+// 16 bytes at any alignment.
+__device__ __forceinline__ i32x4 load16(const void* p) {
+  i32x4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+// v moved down by s elements (0 .. E), zeros from above.
+template <int ES>
+__device__ __forceinline__ i32x4 shift_down(i32x4 v, int s) {
+  const int d = ES == 4 ? s : s >> 1;   // whole dwords
+  if (d & 4) v = i32x4{0, 0, 0, 0};
+  if (d & 2) v = i32x4{v[2], v[3], 0, 0};
+  if (d & 1) v = i32x4{v[1], v[2], v[3], 0};
+  if constexpr (ES == 2) {
+    if (s & 1) {
+      const uint32_t a = v[0], b = v[1], c = v[2], e = v[3];
+      v = i32x4{(int)(a >> 16 | b << 16), (int)(b >> 16 | c << 16), (int)(c >> 16 | e << 16), (int)(e >> 16)};
+    }
+  }
+  return v;
+}
+// Elements pos .. pos + E - 1 of a row of len elements (len >= 1), zeros past its end.
+template <int ES>
+__device__ __forceinline__ i32x4 load_end(const char* row, int64_t pos, int64_t len) {
+  constexpr int E = 16 / ES;
+  if (len >= E) {
+    const int64_t a = pos < len - E ? pos : len - E, s = pos - a;
+    return shift_down<ES>(load16(row + a * ES), (int)(s < E ? s : E));
+  }
+  i32x4 v = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int64_t i = pos + e;
+    if (i < len) {
+      if constexpr (ES == 4) v[e] = reinterpret_cast<const int*>(row)[i];
+      else v[e / 2] |= (int)((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << (16 * (e & 1)));
+    }
+  }
+  return v;
+}
+
+// One operand's tile: MN rows (or columns, mn-major) by BK k values, NT threads.
+// HALVES (k-major): tile rows come from two halves of the stored rows, alternating by HW:
+// HW rows of the first half, the same HW of the second, and so on.
+template <int ES, int MN, bool KMAJ, int NT, int HW = 0>
+struct GenOperand {
+  static constexpr int E = 16 / ES, BK = kRowBytes / ES;
+  static constexpr int LD = MN * 8 / NT;   // k-major: 16-byte chunks per thread
+  static constexpr int R = 4, NB = MN / E;   // mn-major: one block of R k-rows by E columns per thread
+  static_assert(KMAJ ? MN * 8 % NT == 0 : NB * (BK / R) == NT, "tile split");
+  static constexpr int REGS = KMAJ ? LD : R;
+  i32x4 reg[REGS];
+
+  __device__ static __forceinline__ int swz(int row) { return (row ^ (row >> 3)) & 7; }
+
+  // k0: first k of the tile; mn0: first row / column; mndim, kdim the extents.
+  __device__ __forceinline__ void load(const char* X, int64_t ld, int64_t mn0, int64_t mndim, int64_t k0, int64_t kdim,
+                                       int t) {
+    const bool tail = k0 + BK > kdim;
+    if constexpr (KMAJ) {
+#pragma unroll
+      for (int i = 0; i < LD; ++i) {
+        const int row = (t + i * NT) >> 3;
+        int64_t at;
+        if constexpr (HW > 0) {
+          const int64_t c = mn0 + row / (2 * HW) * HW + row % HW;
+          at = (c < mndim ? c : mndim - 1) + (row / HW % 2 ? mndim : 0);
+        } else {
+          at = mn0 + row < mndim ? mn0 + row : mndim - 1;   // (rows past the last one are not stored)
+        }
+        const char* p = X + at * ld * ES;
+        const int64_t pos = k0 + (t & 7) * E;
+        reg[i] = tail ? load_end<ES>(p, pos, kdim) : load16(p + pos * ES);
+      }
+    } else {
+      const int64_t pos = mn0 + t % NB * E, kr = k0 + t / NB * R;
+      const bool edge = tail || mn0 + MN > mndim;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (!edge) {
+          reg[r] = load16(X + ((kr + r) * ld + pos) * ES);
+        } else {
+          const int64_t kk = kr + r < kdim ? kr + r : kdim - 1;
+          const i32x4 v = load_end<ES>(X + kk * ld * ES, pos, mndim);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) reg[r][e] = kr + r < kdim ? v[e] : 0;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(char* lds, int t) const {
+    if constexpr (KMAJ) {
+#pragma unroll
+      for (int i = 0; i < LD; ++i) {
+        const int row = (t + i * NT) >> 3;
+        *reinterpret_cast<i32x4*>(lds + row * kRowBytes + (((t & 7) ^ swz(row)) << 4)) = reg[i];
+      }
+    } else {
+      const int kb = t / NB * R * ES, chunk = kb >> 4, within = kb & 15;
+#pragma unroll
+      for (int c = 0; c < E; ++c) {
+        const int row = t % NB * E + c;
+        char* dst = lds + row * kRowBytes + ((chunk ^ swz(row)) << 4) + within;
+        if constexpr (ES == 4) {
+          *reinterpret_cast<i32x4*>(dst) = i32x4{reg[0][c], reg[1][c], reg[2][c], reg[3][c]};
+        } else {
+          const uint32_t sel = (c & 1) ? 0x07060302u : 0x05040100u;
+          const i32x2 v = {(int)__builtin_amdgcn_perm((uint32_t)reg[1][c >> 1], (uint32_t)reg[0][c >> 1], sel),
+                           (int)__builtin_amdgcn_perm((uint32_t)reg[3][c >> 1], (uint32_t)reg[2][c >> 1], sel)};
+          *reinterpret_cast<i32x2*>(dst) = v;
+        }
+      }
+    }
+  }
+};
+
+// v to elements i .. i + 3 of p, the first n of them.
+template <int OUT>
+__device__ __forceinline__ void store4(void* p, int64_t i, int64_t n, const float (&v)[4]) {
+  if (n >= 4) {
+    if constexpr (OUT == F32) {
+      __builtin_memcpy(static_cast<float*>(p) + i, v, 16);
+    } else {
+      const i32x2 o = {(int)Tr<OUT>::pack2(v[0], v[1]), (int)Tr<OUT>::pack2(v[2], v[3])};
+      __builtin_memcpy(static_cast<uint16_t*>(p) + i, &o, 8);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) store_vec(p, OUT, i + e, v[e]);
+  }
+}
+
+// LAY bit 0: A stored (k, m); bit 1: B stored (n, k); bit 2 (with bit 1): gated, B (2 n, k).
+// OUT: type of D. Waves of WM x 64.
+template <int DT, int OUT, int LAY, int BM, int BN, int WM>
+__global__ __launch_bounds__((BM / WM) * (BN / 64) * 64, 1) void gen_kernel(GenArgs p) {
+  using T = Tr<DT>;
+  constexpr bool TA = (LAY & 1) != 0, TB = (LAY & 2) != 0, GATED = (LAY & 4) != 0;
+  constexpr int WN = 64, WAVES_M = BM / WM, NT = WAVES_M * (BN / WN) * 64, MB = WM / 32, NB = 2;
+  constexpr int ES = T::es, BK = kRowBytes / ES, STAGE = (BM + BN) * kRowBytes;
+  constexpr bool FINE = DT == F32;
+  __shared__ __attribute__((aligned(16))) char lds[2 * STAGE];
+  using OA = GenOperand<ES, BM, !TA, NT>;
+  using OB = GenOperand<ES, BN, TB, NT, GATED ? 32 : 0>;
+  OA oa;
+  OB ob;
+
+  const int pos = xcd_remap(blockIdx.x, p.tiles_m * p.tiles_n);
+  const int tm = __builtin_amdgcn_readfirstlane(pos % p.tiles_m), tn = __builtin_amdgcn_readfirstlane(pos / p.tiles_m);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * (GATED ? BN / 2 : BN);
+  const int t = threadIdx.x, lane = t & 63;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = w % WAVES_M, wn = w / WAVES_M, lrow = lane & 31, lhi = lane >> 5;
+  const char* A = static_cast<const char*>(p.A);
+  const char* B = static_cast<const char*>(p.B);
+  const int64_t KT = (p.k + BK - 1) / BK;
+
+  f32x16 acc[NB][MB];
+#pragma unroll
+  for (int a = 0; a < NB; ++a)
+#pragma unroll
+    for (int b = 0; b < MB; ++b) acc[a][b] = f32x16{};
+
+  if (KT > 0) {   // (a product over no tokens is zero)
+    oa.load(A, p.lda, m0, p.m, 0, p.k, t);
+    ob.load(B, p.ldb, n0, p.n, 0, p.k, t);
+    oa.store(lds, t);
+    ob.store(lds + BM * kRowBytes, t);
+  }
+  __syncthreads();
+  for (int64_t kt = 0; kt < KT; ++kt) {
+    const int cur = (int)(kt & 1);
+    if (kt + 1 < KT) {
+      oa.load(A, p.lda, m0, p.m, (kt + 1) * BK, p.k, t);
+      ob.load(B, p.ldb, n0, p.n, (kt + 1) * BK, p.k, t);
+    }
+    const char* sA = lds + cur * STAGE + (wm * WM + lrow) * kRowBytes;
+    const char* sB = lds + cur * STAGE + (BM + wn * WN + lrow) * kRowBytes;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      i32x4 af[MB], bf[NB];
+      // (the swizzle depends on the row's place in the tile: blocks of 32 rows, waves of 32 or 64)
+#pragma unroll
+      for (int b = 0; b < MB; ++b)
+        af[b] = *reinterpret_cast<const i32x4*>(sA + b * 32 * kRowBytes + (((2 * s + lhi) ^ OA::swz(wm * WM + b * 32 + lrow)) << 4));
+#pragma unroll
+      for (int a = 0; a < NB; ++a)
+        bf[a] = *reinterpret_cast<const i32x4*>(sB + a * 32 * kRowBytes + (((2 * s + lhi) ^ OB::swz(wn * WN + a * 32 + lrow)) << 4));
+#pragma unroll
+      for (int a = 0; a < NB; ++a)
+#pragma unroll
+        for (int b = 0; b < MB; ++b) acc[a][b] = T::mma(bf[a], af[b], acc[a][b]);
+    }
+    if (kt + 1 < KT) {
+      oa.store(lds + (cur ^ 1) * STAGE, t);
+      ob.store(lds + (cur ^ 1) * STAGE + BM * kRowBytes, t);
+    }
+    __syncthreads();
+  }
+
+  // lane: row m0 + wm WM + 32 b + l % 32; register r: column 8 (r / 4) + 4 (l / 32) + r % 4 of a block
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    const int64_t row = m0 + wm * WM + 32 * b + lrow;
+    if (row >= p.m) continue;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int in = 8 * g + 4 * lhi;
+      if constexpr (GATED) {
+        const int64_t col = n0 + wn * 32 + in, left = p.n - col;
+        if (left <= 0) continue;
+        float gv[4], uv[4], hv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          gv[e] = acc[0][b][4 * g + e];
+          uv[e] = acc[1][b][4 * g + e];
+          if (p.bias && e < left) {
+            gv[e] += load_vec(p.bias, p.vec, col + e);
+            uv[e] += load_vec(p.bias, p.vec, p.n + col + e);
+          }
+        }
+        with_gate(p.act, [&](auto act) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) hv[e] = gate_act<decltype(act)::value, FINE>(gv[e]) * uv[e];
+        });
+        store4<OUT>(p.D, row * p.ldd + col, left, hv);
+        if (p.Z) {
+          store4<OUT>(p.Z, row * 2 * p.n + col, left, gv);
+          store4<OUT>(p.Z, row * 2 * p.n + p.n + col, left, uv);
+        }
+      } else {
+#pragma unroll
+        for (int a = 0; a < NB; ++a) {
+          const int64_t col = n0 + wn * WN + 32 * a + in, left = p.n - col;
+          if (left <= 0) continue;
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc[a][b][4 * g + e];
+          store4<OUT>(p.D, row * p.ldd + col, left, v);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace gek

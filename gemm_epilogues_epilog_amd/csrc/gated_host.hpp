@@ -1,0 +1,47 @@
+// Host-side rules of the gated feed-forward block: argument checks, workspaces, the choice of
+// kernels. Plain C++17 with no HIP call or header, like plan_host.hpp.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "gemm_epilog.h"
+#include "plan_host.hpp"
+
+namespace gegh {
+
+constexpr int64_t kMaxDim = 1 << 20;
+constexpr int64_t kMaxTokens = 0x7fffffff;
+constexpr int64_t kMaxBackwardTokens = 1 << 24;   // k of the weights' gradients
+constexpr int kCompute = 256;                     // compute units that workspaces are sized for
+
+bool gate_ok(ge_gate_t a);
+bool aligned(const void* p, size_t a);
+
+ge_status_t check_forward(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, ge_gate_t act, const void* x, const void* w,
+                          const void* bias, ge_dtype_t vec, const void* h, const void* z);
+ge_status_t check_down(int64_t m, int64_t d, int64_t n, ge_dtype_t dt, const void* h, const void* w, const void* y);
+struct Backward {   // what a call of the backward wants, by its pointers
+  const void *dy, *x, *w, *z, *h, *w_down, *dx, *dw, *dw_down, *dbias;
+};
+ge_status_t check_backward(int64_t m, int64_t n, int64_t k, int64_t d, ge_dtype_t dt, ge_gate_t act, const Backward& b,
+                           ge_dtype_t vec, const void* ws, size_t ws_bytes);
+
+// One product D (M, N) = A . B over K, dense operands in the storage orders of `lay` (bit 0: A
+// stored (K, M), bit 1: B stored (N, K)): whether the 16-bit tile kernels take it (rows of whole
+// 16-byte chunks).
+bool fast_shape(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay);
+// Its configuration there, with the k loop split where that pays and `ws` bytes hold it.
+ge_status_t fast_layout(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, int cus, size_t ws, geh::Layout* L);
+
+// Column sums of (m, 2 n) values: row ranges summed side by side.
+int64_t colsum_parts(int64_t m, int64_t cols);
+
+// The backward's workspace: dZ (m, 2 n), then dH in fp32 (only where the product and the
+// activations' gradient are separate kernels), then what one product or the column sums need.
+struct BackwardSpace {
+  size_t dh, scratch, total;   // offsets; dZ is at 0
+};
+BackwardSpace backward_space(int64_t m, int64_t n, int64_t k, int64_t d, ge_dtype_t dt);
+
+}  // namespace gegh

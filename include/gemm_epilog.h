@@ -483,6 +483,63 @@ ge_status_t gemm_epilog_rms_norm_backward(int64_t rows, int64_t d, ge_dtype_t dt
                                           const void* dresidual, int64_t lddr, void* dx, int64_t lddx, void* dweight,
                                           void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Gated feed-forward block ---------------------------------------------------------
+ * H = act(G) * U with [G | U] = X . W^T + bias, and Y = H . Wd^T: the gate and the up
+ * projection are one product, whose epilogue applies the activation and multiplies. Tokens
+ * along the rows: X (m, k), W (2 n, k) the gate's n rows and then the up projection's, bias 2 n
+ * values, H (m, n), Wd (d, n), Y (m, d). Every matrix is dense row-major, of one type dt (fp32,
+ * fp16 or bf16), aligned to its elements; sums are fp32. 16-bit matrices with 16-byte aligned
+ * rows (n, k, d multiples of 8) run on the direct-to-LDS kernels, any others on a slower one.
+ * No plan: a call chooses its kernels by its sizes. Work is enqueued on `stream`, kernel
+ * launches only (a call may be captured into a HIP graph), on the current device, whose
+ * pointers they are.
+ */
+typedef enum {
+  GE_GATE_SILU = 0, /* g / (1 + e^-g) */
+  GE_GATE_GELU = 1, /* the tanh form, as GE_EPILOG_GELU_BIAS */
+  GE_GATE_RELU = 2  /* g where g > 0, else 0 (of NaN too) */
+} ge_gate_t;
+
+/*
+ * gemm_epilog_gated_forward - H, and Z = [G | U] if wanted.
+ *   m : 0 .. 2^31 - 1 (0 does nothing); n, k : 1 .. 2^20.
+ *   bias : 2 n values of type vec (dt or fp32), or NULL.
+ *   h    : receives H (m, n).
+ *   z    : receives Z (m, 2 n), rounded to dt, for the backward pass; NULL if not wanted. H
+ *          comes from the fp32 sums in either case.
+ */
+ge_status_t gemm_epilog_gated_forward(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, ge_gate_t act, const void* x,
+                                      const void* w, const void* bias, ge_dtype_t vec, void* h, void* z, void* stream);
+
+/* gemm_epilog_gated_down - Y (m, d) = H (m, n) . Wd^T, Wd (d, n). Sizes as above. */
+ge_status_t gemm_epilog_gated_down(int64_t m, int64_t d, int64_t n, ge_dtype_t dt, const void* h, const void* w_down,
+                                   void* y, void* stream);
+
+/* Bytes of the workspace of gemm_epilog_gated_backward (0 for m = 0 and for sizes outside the
+ * supported set). */
+size_t gemm_epilog_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t d, ge_dtype_t dt);
+
+/*
+ * gemm_epilog_gated_backward - the block's gradients.
+ *   dH = dY . Wd;  dG = dH U a'(G), dU = dH a(G), dZ = [dG | dU], rounded to dt;
+ *   dX = dZ . W, dW = dZ^T . X, dWd = dY^T . H, dbias = column sums of dZ (in a fixed order).
+ *   m      : 0 .. 2^24 (above: GE_ERR_NOT_SUPPORTED); with m = 0 the gradients of the weights
+ *            and of the bias are zero.
+ *   dy     : (m, d), and w_down (d, n); with w_down NULL dy is dH itself, (m, n) with d = n.
+ *   z      : Z (m, 2 n) as the forward pass left it.
+ *   x, w, h: X (m, k), W (2 n, k), H (m, n): needed for dw, dx and dw_down.
+ *   dx (m, k), dw (2 n, k), dw_down (d, n), dbias (2 n values of type vec): each may be NULL if
+ *            not wanted. None may overlap an input.
+ *   workspace : device, 256-byte aligned, workspace_bytes >= gemm_epilog_gated_workspace_bytes
+ *            (else GE_ERR_SCRATCH), used until the work is done.
+ * dX may share its k loop between workgroups that wait for each other's sums, bounded, as a split
+ * plan does (see gemm_epilog_lost_waits): a wait that runs out gives that tile NaN.
+ */
+ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t d, ge_dtype_t dt, ge_gate_t act,
+                                       const void* dy, const void* x, const void* w, const void* z, const void* h,
+                                       const void* w_down, void* dx, void* dw, void* dw_down, void* dbias,
+                                       ge_dtype_t vec, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
