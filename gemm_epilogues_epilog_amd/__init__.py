@@ -10,7 +10,8 @@ gemm_epilog_execute_noalloc, gemm_epilog_autotune, gemm_epilog_lost_waits,
 gemm_epilog_free, gemm_epilog_aux_bytes, gemm_epilog_workspace_bytes,
 gemm_epilog_describe, gemm_epilog_status_string. The microscaled operators
 (gemm_epilog_mx_*) are wrapped in mx.py, the norm (gemm_epilog_rms_norm*) in norm.py, the
-gated feed-forward block (gemm_epilog_gated_*) in gated.py.
+gated feed-forward block (gemm_epilog_gated_*) in gated.py, 4-bit weights with group scales
+(gemm_epilog_w4_*) in w4.py.
 Pointers may be given as torch tensors (device memory), integers or None.
 
 `Matmul` wraps them in the stateful plan / execute / free object with a context
@@ -47,7 +48,9 @@ EXPORTS = ("gemm_epilog_plan", "gemm_epilog_plan_ex", "gemm_epilog_plan_info", "
            "gemm_epilog_mx_execute", "gemm_epilog_mx_free",
            "gemm_epilog_rms_norm", "gemm_epilog_rms_norm_workspace_bytes", "gemm_epilog_rms_norm_backward",
            "gemm_epilog_gated_forward", "gemm_epilog_gated_down", "gemm_epilog_gated_workspace_bytes",
-           "gemm_epilog_gated_backward")
+           "gemm_epilog_gated_backward",
+           "gemm_epilog_w4_code_bytes", "gemm_epilog_w4_scale_count", "gemm_epilog_w4_quantize", "gemm_epilog_w4_pack",
+           "gemm_epilog_w4_dequantize", "gemm_epilog_w4_matmul", "gemm_epilog_w4_gated")
 MXFP4, MXFP8 = 0, 1
 MX_FORMATS = {"mxfp4": MXFP4, "mxfp8": MXFP8}
 MX_OUT = {"f32": 0, "f16": 1, "bf16": 2, "mxfp8": 3}
@@ -139,7 +142,14 @@ def load() -> ctypes.CDLL:
             ("gated_forward", [i64, i64, i64, c_int, c_int, vp, vp, vp, c_int, vp, vp, vp], c_int),
             ("gated_down", [i64, i64, i64, c_int, vp, vp, vp, vp], c_int),
             ("gated_workspace_bytes", [i64, i64, i64, i64, c_int], size),
-            ("gated_backward", [i64, i64, i64, i64, c_int, c_int, *[vp] * 10, c_int, vp, size, vp], c_int)):
+            ("gated_backward", [i64, i64, i64, i64, c_int, c_int, *[vp] * 10, c_int, vp, size, vp], c_int),
+            ("w4_code_bytes", [i64, i64, c_int], size),
+            ("w4_scale_count", [i64, i64, i64, c_int], size),
+            ("w4_quantize", [i64, i64, c_int, vp, i64, i64, c_int, c_int, c_int, vp, vp, vp, vp], c_int),
+            ("w4_pack", [i64, i64, i64, c_int, *[vp] * 7], c_int),
+            ("w4_dequantize", [i64, i64, i64, c_int, c_int, vp, vp, vp, c_int, vp, i64, vp], c_int),
+            ("w4_matmul", [i64, i64, i64, i64, c_int, c_int, c_int, vp, vp, vp, vp, vp, c_int, vp, vp], c_int),
+            ("w4_gated", [i64, i64, i64, i64, c_int, c_int, vp, vp, vp, vp, vp, c_int, vp, vp], c_int)):
         fn = getattr(L, "gemm_epilog_" + name)
         fn.argtypes, fn.restype = args, res
     _lib = L

@@ -23,7 +23,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["api.hip", "inst_f32.hip", "inst_f16.hip", "inst_bf16.hip",
            "inst_f16_lay1.hip", "inst_f16_lay2.hip", "inst_f16_lay3.hip",
            "inst_bf16_lay1.hip", "inst_bf16_lay2.hip", "inst_bf16_lay3.hip",
-           "mx.hip", "mx_quant.hip", "norm.hip", "gated.hip"]
+           "mx.hip", "mx_quant.hip", "norm.hip", "gated.hip", "w4.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -36,7 +36,7 @@ FLAGS = [
 PROBE_SOURCES = ["probe.hip"]
 
 # Host-only C++ (the plan arithmetic): plain g++, no HIP.
-HOST_SOURCES = ["plan_host.cpp", "mx_host.cpp", "gated_host.cpp"]
+HOST_SOURCES = ["plan_host.cpp", "mx_host.cpp", "gated_host.cpp", "w4_host.cpp"]
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-I", INCLUDE, "-I", CSRC]
 
 

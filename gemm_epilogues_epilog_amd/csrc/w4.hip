@@ -1,0 +1,380 @@
+// 4-bit weights with group scales: entry points, and the kernels that make and undo them.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "product.hpp"
+#include "w4.hpp"
+#include "w4_host.hpp"
+
+namespace gek {
+namespace {
+
+struct W4Weight {
+  char* codes;
+  uint16_t* scales;
+  uint8_t* zeros;
+  int64_t rows, k, kt, groups, group, rgs;   // rows and rgs: of a half
+};
+
+__device__ __forceinline__ uint16_t to_bits16(float v, int dt) {
+  return dt == F16 ? (uint16_t)(Tr<F16>::pack2(v, v) & 0xffff) : (uint16_t)(Tr<BF16>::pack2(v, v) & 0xffff);
+}
+__device__ __forceinline__ float from_bits16(uint16_t v, int dt) {
+  return dt == F16 ? Tr<F16>::widen(v) : Tr<BF16>::widen(v);
+}
+
+// Rounds to a group's codes. A wave takes the tiles of one group (at most one tile holds several
+// groups): row l % 16, and in each tile the k values 32 j + 8 (l / 16) .. + 7. Groups past one
+// tile are read twice, for the range and for the codes. Bound by memory.
+template <int SRC>
+__global__ __launch_bounds__(256) void w4_quantize_kernel(const void* src, int64_t ld, W4Weight o, int dt, int symmetric,
+                                                          int64_t units) {
+  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (unit >= units) return;
+  const int lane = threadIdx.x & 63, li = lane & 15, q = lane >> 4;
+  const int64_t per = o.group > kTileK ? o.groups : o.kt;   // units of a row group
+  const int64_t rg = unit / per, u = unit - rg * per;        // row group, counted over both halves
+  const int64_t span = o.group > kTileK ? o.group / kTileK : 1;
+  const int64_t ta = u * span, tb = ta + span < o.kt ? ta + span : o.kt;
+  const int ng = o.group >= kTileK ? 1 : (int)(kTileK / o.group);
+  const int64_t half = rg / o.rgs, in = (rg - half * o.rgs) * kRows + li;
+  const bool on = in < o.rows;
+  const char* row = static_cast<const char*>(src) + (half * o.rows + (on ? in : 0)) * ld * Tr<SRC>::es;
+
+  const auto read = [&](int64_t t, int j, float (&v)[8]) {
+    constexpr int ES = Tr<SRC>::es, E = 16 / ES;
+    const int64_t kp = t * kTileK + 32 * j + 8 * q;
+    i32x4 raw[8 / E];
+#pragma unroll
+    for (int h = 0; h < 8 / E; ++h)
+      raw[h] = kp + 8 <= o.k ? load16(row + (kp + h * E) * ES) : load_end<ES>(row, kp + h * E, o.k);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (SRC == F32) v[e] = __int_as_float(raw[e / 4][e % 4]);
+      else v[e] = Tr<SRC>::widen((uint16_t)((uint32_t)raw[0][e / 2] >> (16 * (e & 1))));
+    }
+  };
+  // Scale and zero of a group from its range (of this lane's part; joined over the four quarters).
+  const auto finish = [&](float lo, float hi, bool bad, float& s, float& z, uint16_t& bits) {
+#pragma unroll
+    for (int d = 16; d < 64; d <<= 1) {
+      lo = fminf(lo, __shfl_xor(lo, d));
+      hi = fmaxf(hi, __shfl_xor(hi, d));
+      bad |= (bool)__shfl_xor((int)bad, d);
+    }
+    const double width = symmetric ? (double)fmaxf(-lo, hi) / 7.0 : ((double)hi - (double)lo) / 15.0;
+    bits = bad ? (uint16_t)(dt == F16 ? 0x7e00 : 0x7fc0) : to_bits16((float)width, dt);
+    s = from_bits16(bits, dt);
+    z = symmetric ? 8.0f : s > 0.0f ? (float)fmin(rint(-(double)lo / (double)s), 15.0) : 0.0f;
+  };
+  const auto encode = [&](const float (&v)[8], int64_t t, int j, float s, float z) {
+    const int64_t left = o.k - (t * kTileK + 32 * j + 8 * q);   // padding is zero
+    uint32_t d = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float c = s > 0.0f ? fminf(fmaxf(rintf(v[e] / s) + z, 0.0f), 15.0f) : z;
+      d |= (on && e < left ? (uint32_t)c : 0u) << (8 * (e % 4) + 4 * (e / 4));
+    }
+    return d;
+  };
+  const auto put = [&](int64_t g, float z, uint16_t bits) {
+    if (q == 0) {
+      o.scales[(rg * o.groups + g) * kRows + li] = on ? bits : (uint16_t)0;
+      o.zeros[(rg * o.groups + g) * kRows + li] = on ? (uint8_t)z : (uint8_t)0;
+    }
+  };
+  const auto range = [&](const float (&v)[8], float& lo, float& hi, bool& bad) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      lo = fminf(lo, v[e]);
+      hi = fmaxf(hi, v[e]);
+      bad |= !(fabsf(v[e]) <= 3.402823466e38f);
+    }
+  };
+
+  if (o.group <= kTileK) {
+    float v[4][8], s[4], z[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) read(ta, j, v[j]);
+    float lo[4], hi[4];
+    bool bad[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      lo[j] = hi[j] = 0.0f;
+      bad[j] = false;
+      range(v[j], lo[j], hi[j], bad[j]);
+    }
+    // two or four runs of 32 to a group
+    if (ng <= 2) {
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        lo[j] = lo[j + 1] = fminf(lo[j], lo[j + 1]);
+        hi[j] = hi[j + 1] = fmaxf(hi[j], hi[j + 1]);
+        bad[j] = bad[j + 1] = bad[j] || bad[j + 1];
+      }
+    }
+    if (ng == 1) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        lo[j] = lo[j + 2] = fminf(lo[j], lo[j + 2]);
+        hi[j] = hi[j + 2] = fmaxf(hi[j], hi[j + 2]);
+        bad[j] = bad[j + 2] = bad[j] || bad[j + 2];
+      }
+    }
+    i32x4 out;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint16_t bits;
+      finish(lo[j], hi[j], bad[j], s[j], z[j], bits);
+      out[j] = (int)encode(v[j], ta, j, s[j], z[j]);
+      const int64_t g = ta * ng + j * ng / 4;
+      if (j * ng % 4 == 0 && g < o.groups) put(g, z[j], bits);
+    }
+    *reinterpret_cast<i32x4*>(o.codes + (rg * o.kt + ta) * kTileBytes + lane * 16) = out;
+  } else {
+    float lo = 0.0f, hi = 0.0f, s, z, v[8];
+    bool bad = false;
+    uint16_t bits;
+    for (int64_t t = ta; t < tb; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        read(t, j, v);
+        range(v, lo, hi, bad);
+      }
+    finish(lo, hi, bad, s, z, bits);
+    put(u, z, bits);
+    for (int64_t t = ta; t < tb; ++t) {
+      i32x4 out;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        read(t, j, v);
+        out[j] = (int)encode(v, t, j, s, z);
+      }
+      *reinterpret_cast<i32x4*>(o.codes + (rg * o.kt + t) * kTileBytes + lane * 16) = out;
+    }
+  }
+}
+
+// Row-major codes, scales and zeros (null: all 8) into the layout; a wave per tile, and per 16
+// rows' scales beside it.
+__global__ __launch_bounds__(256) void w4_pack_kernel(const uint8_t* src, const uint16_t* scales, const uint8_t* zeros,
+                                                      W4Weight o, int64_t units) {
+  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (unit >= units) return;
+  const int lane = threadIdx.x & 63, li = lane & 15, q = lane >> 4;
+  const int64_t rg = unit / o.kt, t = unit - rg * o.kt;
+  const int64_t half = rg / o.rgs, in = (rg - half * o.rgs) * kRows + li, row = half * o.rows + in;
+  const bool on = in < o.rows;
+  const int64_t width = (o.k + 1) / 2;
+  i32x4 out = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t kp = t * kTileK + 32 * j + 8 * q;
+    uint32_t d = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int64_t at = kp / 2 + b;   // holds k 2 at (low) and 2 at + 1 (high)
+      uint32_t v = on && at < width ? src[row * width + at] : 0u;
+      if (2 * at + 1 >= o.k) v &= 15u;
+      const int e = 2 * b;   // element e and e + 1 of the dword
+      d |= (v & 15u) << (8 * (e % 4) + 4 * (e / 4)) | (v >> 4) << (8 * ((e + 1) % 4) + 4 * ((e + 1) / 4));
+    }
+    out[j] = (int)d;
+  }
+  *reinterpret_cast<i32x4*>(o.codes + unit * kTileBytes + lane * 16) = out;
+  // the groups that begin in this tile
+  const int64_t ga = gew4::ceil_div(t * kTileK, o.group), gb = gew4::ceil_div((t + 1) * kTileK, o.group);
+  const int64_t g = ga + q;
+  if (g < gb && g < o.groups) {
+    o.scales[(rg * o.groups + g) * kRows + li] = on ? scales[row * o.groups + g] : (uint16_t)0;
+    o.zeros[(rg * o.groups + g) * kRows + li] = !on ? 0 : zeros ? zeros[row * o.groups + g] & 15 : 8;
+  }
+}
+
+// (q - z) s, rounded to DT. A wave per tile, eight values at a time.
+template <int DT>
+__global__ __launch_bounds__(256) void w4_dequantize_kernel(W4Weight o, int sdt, void* dst, int64_t ld, int64_t units) {
+  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (unit >= units) return;
+  const int lane = threadIdx.x & 63, li = lane & 15, q = lane >> 4;
+  const int64_t rg = unit / o.kt, t = unit - rg * o.kt;
+  const int64_t half = rg / o.rgs, in = (rg - half * o.rgs) * kRows + li, row = half * o.rows + in;
+  const i32x4 c = *reinterpret_cast<const i32x4*>(o.codes + unit * kTileBytes + lane * 16);
+  if (in >= o.rows) return;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t kp = t * kTileK + 32 * j + 8 * q;
+    if (kp >= o.k) continue;
+    const int64_t at = (rg * o.groups + kp / o.group) * kRows + li;
+    const float s = from_bits16(o.scales[at], sdt), z = (float)o.zeros[at];
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = ((float)(((uint32_t)c[j] >> (8 * (e % 4) + 4 * (e / 4))) & 15u) - z) * s;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float u[4] = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+      store4<DT>(dst, row * ld + kp + 4 * h, o.k - kp - 4 * h, u);
+    }
+  }
+}
+
+W4Weight weight(int64_t rows, int64_t k, int64_t group, int halves, const void* codes, const void* scales,
+                const void* zeros) {
+  W4Weight w;
+  w.codes = static_cast<char*>(const_cast<void*>(codes));
+  w.scales = static_cast<uint16_t*>(const_cast<void*>(scales));
+  w.zeros = static_cast<uint8_t*>(const_cast<void*>(zeros));
+  w.rows = rows / halves;
+  w.k = k;
+  w.kt = gew4::k_tiles(k);
+  w.group = group;
+  w.groups = gew4::k_groups(k, group);
+  w.rgs = gew4::row_groups(rows, halves);
+  return w;
+}
+
+ge_status_t run(const void* fn, dim3 grid, int threads, size_t lds, void** params, void* stream) {
+  return hipLaunchKernel(fn, grid, dim3(threads), params, lds, static_cast<hipStream_t>(stream)) == hipSuccess ? GE_OK
+                                                                                                           : GE_ERR_HIP;
+}
+
+template <int DT, bool GATED>
+ge_status_t skinny(W4Args& a, void* stream) {
+  constexpr int NB = GATED ? 2 : 1;
+  void* params[] = {&a};
+  const int mt = a.m <= 16 ? 1 : a.m <= 32 ? 2 : 4;
+  const int nw = mt == 4 ? 4 : 8;
+  const void* fn = mt == 1   ? reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, 1>)
+                   : mt == 2 ? reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, 2>)
+                             : reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, 4>);
+  // (a launch has at most 65535 rows of workgroups)
+  const int64_t step = (int64_t)65535 * 16 * mt, all = a.m;
+  const char* x = static_cast<const char*>(a.x);
+  char* d = static_cast<char*>(a.D);
+  for (int64_t at = 0; at < all; at += step) {
+    a.m = std::min(step, all - at);
+    a.x = x + at * a.k * 2;
+    a.D = d + at * a.n * (a.out == F32 ? 4 : 2);
+    const dim3 grid((unsigned)a.rgs, (unsigned)gew4::ceil_div(a.m, 16 * mt));
+    if (ge_status_t st = run(fn, grid, nw * 64, (size_t)nw * NB * mt * 1024, params, stream); st != GE_OK) return st;
+  }
+  return GE_OK;
+}
+
+ge_status_t multiply(int64_t m, int64_t n, int64_t k, int64_t group, ge_dtype_t dt, ge_dtype_t out, bool gated, int ep,
+                     const void* x, const void* codes, const void* scales, const void* zeros, const void* bias,
+                     ge_dtype_t vec, void* D, void* stream) {
+  const W4Weight w = weight(gated ? 2 * n : n, k, group, gated ? 2 : 1, codes, scales, zeros);
+  W4Args a;
+  a.x = x;
+  a.codes = w.codes;
+  a.scales = w.scales;
+  a.zeros = w.zeros;
+  a.bias = bias;
+  a.D = D;
+  a.m = m;
+  a.n = (int32_t)n;
+  a.k = (int32_t)k;
+  a.kt = (int32_t)w.kt;
+  a.groups = (int32_t)w.groups;
+  a.group = (int32_t)group;
+  a.rgs = (int32_t)w.rgs;
+  a.vec = (int32_t)vec;
+  a.out = (int32_t)out;
+  a.ep = ep;
+  a.vecx = k % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+  if (dt == GE_F16) return gated ? skinny<F16, true>(a, stream) : skinny<F16, false>(a, stream);
+  return gated ? skinny<BF16, true>(a, stream) : skinny<BF16, false>(a, stream);
+}
+
+dim3 waves(int64_t units) { return dim3((unsigned)((units + 3) / 4)); }
+
+}  // namespace
+}  // namespace gek
+
+extern "C" {
+
+size_t gemm_epilog_w4_code_bytes(int64_t rows, int64_t k, int halves) { return gew4h::code_bytes(rows, k, halves); }
+size_t gemm_epilog_w4_scale_count(int64_t rows, int64_t k, int64_t group, int halves) {
+  return gew4h::scale_count(rows, k, group, halves);
+}
+
+ge_status_t gemm_epilog_w4_quantize(int64_t rows, int64_t k, ge_dtype_t src_dt, const void* src, int64_t ld,
+                                    int64_t group, int halves, int symmetric, ge_dtype_t dt, void* codes, void* scales,
+                                    void* zeros, void* stream) {
+  if (ge_status_t st = gew4h::check_weight(rows, k, group, halves, codes, scales, zeros); st != GE_OK) return st;
+  if (ge_status_t st = gew4h::check_quantize(rows, k, src_dt, src, ld, dt); st != GE_OK) return st;
+  int cus = 0;
+  if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
+  gek::W4Weight w = gek::weight(rows, k, group, halves, codes, scales, zeros);
+  int64_t units = w.rgs * halves * (group > gew4::kTileK ? w.groups : w.kt);
+  int d = (int)dt, sym = symmetric != 0;
+  void* params[] = {&src, &ld, &w, &d, &sym, &units};
+  const void* fn = src_dt == GE_F32   ? reinterpret_cast<const void*>(&gek::w4_quantize_kernel<gek::F32>)
+                   : src_dt == GE_F16 ? reinterpret_cast<const void*>(&gek::w4_quantize_kernel<gek::F16>)
+                                      : reinterpret_cast<const void*>(&gek::w4_quantize_kernel<gek::BF16>);
+  return gek::run(fn, gek::waves(units), 256, 0, params, stream);
+}
+
+ge_status_t gemm_epilog_w4_pack(int64_t rows, int64_t k, int64_t group, int halves, const void* src_codes,
+                                const void* src_scales, const void* src_zeros, void* codes, void* scales, void* zeros,
+                                void* stream) {
+  if (ge_status_t st = gew4h::check_weight(rows, k, group, halves, codes, scales, zeros); st != GE_OK) return st;
+  if (!src_codes || !src_scales) return GE_ERR_NULL_POINTER;
+  if (reinterpret_cast<uintptr_t>(src_scales) % 2) return GE_ERR_MISALIGNED;
+  int cus = 0;
+  if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
+  gek::W4Weight w = gek::weight(rows, k, group, halves, codes, scales, zeros);
+  int64_t units = w.rgs * halves * w.kt;
+  void* params[] = {&src_codes, &src_scales, &src_zeros, &w, &units};
+  return gek::run(reinterpret_cast<const void*>(&gek::w4_pack_kernel), gek::waves(units), 256, 0, params, stream);
+}
+
+ge_status_t gemm_epilog_w4_dequantize(int64_t rows, int64_t k, int64_t group, int halves, ge_dtype_t dt,
+                                      const void* codes, const void* scales, const void* zeros, ge_dtype_t dst_dt,
+                                      void* dst, int64_t ld, void* stream) {
+  if (ge_status_t st = gew4h::check_weight(rows, k, group, halves, codes, scales, zeros); st != GE_OK) return st;
+  if (ge_status_t st = gew4h::check_dequantize(rows, k, dt, dst_dt, dst, ld); st != GE_OK) return st;
+  int cus = 0;
+  if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
+  gek::W4Weight w = gek::weight(rows, k, group, halves, codes, scales, zeros);
+  int64_t units = w.rgs * halves * w.kt;
+  int d = (int)dt;
+  void* params[] = {&w, &d, &dst, &ld, &units};
+  const void* fn = dst_dt == GE_F32   ? reinterpret_cast<const void*>(&gek::w4_dequantize_kernel<gek::F32>)
+                   : dst_dt == GE_F16 ? reinterpret_cast<const void*>(&gek::w4_dequantize_kernel<gek::F16>)
+                                      : reinterpret_cast<const void*>(&gek::w4_dequantize_kernel<gek::BF16>);
+  return gek::run(fn, gek::waves(units), 256, 0, params, stream);
+}
+
+ge_status_t gemm_epilog_w4_matmul(int64_t m, int64_t n, int64_t k, int64_t group, ge_dtype_t dt, ge_dtype_t out,
+                                  ge_epilog_t ep, const void* x, const void* codes, const void* scales,
+                                  const void* zeros, const void* bias, ge_dtype_t vec, void* D, void* stream) {
+  if (ge_status_t st = gew4h::check_weight(n, k, group, 1, codes, scales, zeros); st != GE_OK) return st;
+  if (ep != GE_EPILOG_NONE && ep != GE_EPILOG_BIAS && ep != GE_EPILOG_RELU_BIAS && ep != GE_EPILOG_GELU_BIAS)
+    return GE_ERR_NOT_SUPPORTED;
+  if (ge_status_t st = gew4h::check_product(m, n, dt, out, x, bias, vec, D); st != GE_OK) return st;
+  if (ep != GE_EPILOG_NONE && !bias) return GE_ERR_NULL_POINTER;
+  if (m == 0) return GE_OK;
+  int cus = 0;
+  if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
+  return gek::multiply(m, n, k, group, dt, out, false, (int)ep, x, codes, scales, zeros,
+                       ep == GE_EPILOG_NONE ? nullptr : bias, vec, D, stream);
+}
+
+ge_status_t gemm_epilog_w4_gated(int64_t m, int64_t n, int64_t k, int64_t group, ge_dtype_t dt, ge_gate_t act,
+                                 const void* x, const void* codes, const void* scales, const void* zeros,
+                                 const void* bias, ge_dtype_t vec, void* h, void* stream) {
+  if (n < 1 || n > gew4h::kMaxDim) return GE_ERR_INVALID_VALUE;
+  if (ge_status_t st = gew4h::check_weight(2 * n, k, group, 2, codes, scales, zeros); st != GE_OK) return st;
+  if (act != GE_GATE_SILU && act != GE_GATE_GELU && act != GE_GATE_RELU) return GE_ERR_INVALID_VALUE;
+  if (ge_status_t st = gew4h::check_product(m, n, dt, dt, x, bias, vec, h); st != GE_OK) return st;
+  if (m == 0) return GE_OK;
+  int cus = 0;
+  if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
+  return gek::multiply(m, n, k, group, dt, dt, true, (int)act, x, codes, scales, zeros, bias, vec, h, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,65 @@
+// Rules declared in w4_host.hpp.
+#include "w4_host.hpp"
+
+namespace gew4h {
+
+namespace {
+bool known(ge_dtype_t d) { return d == GE_F32 || d == GE_F16 || d == GE_BF16; }
+bool half_type(ge_dtype_t d) { return d == GE_F16 || d == GE_BF16; }
+size_t esize(ge_dtype_t d) { return d == GE_F32 ? 4 : 2; }
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+}  // namespace
+
+bool shape_ok(int64_t rows, int64_t k, int64_t group, int halves) {
+  if (halves != 1 && halves != 2) return false;
+  if (rows < 1 || rows > kMaxDim * halves || rows % halves || k < 1 || k > kMaxDim) return false;
+  return group == 32 || group == 64 || (group >= 128 && group <= kMaxDim && group % 128 == 0);
+}
+
+size_t code_bytes(int64_t rows, int64_t k, int halves) {
+  if (!shape_ok(rows, k, 128, halves)) return 0;
+  return (size_t)(gew4::row_groups(rows, halves) * halves * gew4::k_tiles(k)) * gew4::kTileBytes;
+}
+
+size_t scale_count(int64_t rows, int64_t k, int64_t group, int halves) {
+  if (!shape_ok(rows, k, group, halves)) return 0;
+  return (size_t)(gew4::row_groups(rows, halves) * halves * gew4::k_groups(k, group)) * gew4::kRows;
+}
+
+ge_status_t check_weight(int64_t rows, int64_t k, int64_t group, int halves, const void* codes, const void* scales,
+                         const void* zeros) {
+  if (!shape_ok(rows, k, group, halves)) return GE_ERR_INVALID_VALUE;
+  if (!codes || !scales || !zeros) return GE_ERR_NULL_POINTER;
+  if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(zeros, 16)) return GE_ERR_MISALIGNED;
+  return GE_OK;
+}
+
+ge_status_t check_quantize(int64_t rows, int64_t k, ge_dtype_t src_dt, const void* src, int64_t ld, ge_dtype_t dt) {
+  if (!known(src_dt) || !known(dt)) return GE_ERR_INVALID_VALUE;
+  if (!half_type(dt)) return GE_ERR_NOT_SUPPORTED;
+  if (rows > 1 && (ld < 0 || ld > (int64_t(1) << 40))) return GE_ERR_INVALID_VALUE;
+  (void)k;
+  if (!src) return GE_ERR_NULL_POINTER;
+  return aligned(src, esize(src_dt)) ? GE_OK : GE_ERR_MISALIGNED;
+}
+
+ge_status_t check_dequantize(int64_t rows, int64_t k, ge_dtype_t dt, ge_dtype_t dst_dt, const void* dst, int64_t ld) {
+  if (!known(dt) || !known(dst_dt)) return GE_ERR_INVALID_VALUE;
+  if (!half_type(dt)) return GE_ERR_NOT_SUPPORTED;
+  if (rows > 1 && (ld < k || ld > (int64_t(1) << 40))) return GE_ERR_INVALID_VALUE;
+  if (!dst) return GE_ERR_NULL_POINTER;
+  return aligned(dst, esize(dst_dt)) ? GE_OK : GE_ERR_MISALIGNED;
+}
+
+ge_status_t check_product(int64_t m, int64_t n, ge_dtype_t dt, ge_dtype_t out, const void* x, const void* bias,
+                          ge_dtype_t vec, const void* D) {
+  if (m < 0 || m > 0x7fffffff || !known(dt) || !known(out) || !known(vec)) return GE_ERR_INVALID_VALUE;
+  if (!half_type(dt) || (out != dt && out != GE_F32) || (vec != dt && vec != GE_F32)) return GE_ERR_NOT_SUPPORTED;
+  // every launch has at most 2^31 - 1 workgroups of 64 x 16 values
+  if (gew4::ceil_div(m, 16) * gew4::ceil_div(n, 16) > 0x7fffffff) return GE_ERR_NOT_SUPPORTED;
+  if (m && (!x || !D)) return GE_ERR_NULL_POINTER;
+  if (!aligned(x, 2) || !aligned(D, esize(out)) || !aligned(bias, esize(vec))) return GE_ERR_MISALIGNED;
+  return GE_OK;
+}
+
+}  // namespace gew4h

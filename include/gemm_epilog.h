@@ -540,6 +540,69 @@ ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t 
                                        const void* w_down, void* dx, void* dw, void* dw_down, void* dbias,
                                        ge_dtype_t vec, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- 4-bit weights with group scales ----------------------------------------------------
+ * W (rows, k) = (q - z) s: codes q of 0 .. 15, and for each `group` consecutive k values of a row
+ * a 16-bit scale s and a zero z of 0 .. 15. group is 32, 64 or a multiple of 128 (k padded to a
+ * multiple of it or more gives one scale a row); the last group of a row may be short. Sums are
+ * fp32 over the exact codes, scaled once per group: no weight is rounded on the way.
+ * rows and k are 1 .. 2^20. halves is 1, or 2 for a gated weight, whose `rows` (2 n) are the
+ * gate's n rows and then the up projection's.
+ * Held in memory (16-byte aligned each): rows in groups of 16, each half padded to whole groups
+ * (RG of them), k in tiles of 128 (KT), G = ceil(k / group):
+ *   code of (r, k): four bits of the byte ((r/16) KT + k/128) 1024 + (k%32/8) 256 + (r%16) 16 +
+ *     (k%128/32) 4 + k%4, the low ones for k%8 < 4, the high ones otherwise;
+ *   scale and zero of (r, g): element ((r/16) G + g) 16 + r%16 of 16-bit and of 8-bit values,
+ * with r counted inside a half and the second half's groups of 16 after the first's.
+ * Padding is zero. Calls are as for the gated block: no plan, kernel launches only.
+ */
+size_t gemm_epilog_w4_code_bytes(int64_t rows, int64_t k, int halves);
+/* 16-bit scales, and bytes of zeros; 0 for sizes outside the supported set, as above. */
+size_t gemm_epilog_w4_scale_count(int64_t rows, int64_t k, int64_t group, int halves);
+
+/*
+ * gemm_epilog_w4_quantize - a (rows, k) weight of type src_dt, row stride ld (elements), to codes,
+ * scales of type dt (fp16 or bf16) and zeros. With lo and hi the smallest and the largest of a
+ * group's values and zero: s = (hi - lo) / 15 rounded to dt, z = -lo / s and q = x / s + z, each
+ * quotient rounded to nearest even, held to 0 .. 15. symmetric: s = max(-lo, hi) / 7 and z = 8. A
+ * group with s = 0 stands for zeros; one that holds an infinity or a NaN gets s = NaN.
+ */
+ge_status_t gemm_epilog_w4_quantize(int64_t rows, int64_t k, ge_dtype_t src_dt, const void* src, int64_t ld,
+                                    int64_t group, int halves, int symmetric, ge_dtype_t dt, void* codes, void* scales,
+                                    void* zeros, void* stream);
+
+/* gemm_epilog_w4_pack - row-major codes ((rows, ceil(k/2)) bytes, even k in the low four bits),
+ * scales and zeros ((rows, G) 16-bit values and bytes, of which the low four bits count; zeros
+ * NULL: all 8), as checkpoints hold them, into the layout above. Once per weight. */
+ge_status_t gemm_epilog_w4_pack(int64_t rows, int64_t k, int64_t group, int halves, const void* src_codes,
+                                const void* src_scales, const void* src_zeros, void* codes, void* scales, void* zeros,
+                                void* stream);
+
+/* gemm_epilog_w4_dequantize - (q - z) s in fp32, rounded to dst_dt, to dst[r ld + k], ld >= k. dt:
+ * the scales' type. */
+ge_status_t gemm_epilog_w4_dequantize(int64_t rows, int64_t k, int64_t group, int halves, ge_dtype_t dt,
+                                      const void* codes, const void* scales, const void* zeros, ge_dtype_t dst_dt,
+                                      void* dst, int64_t ld, void* stream);
+
+/*
+ * gemm_epilog_w4_matmul - D = act(X . W^T + bias), X (m, k) dense of type dt (fp16 or bf16, as W's
+ * scales), W (n, k).
+ *   m    : 0 .. 2^31 - 1 (0 does nothing).
+ *   out  : type of D (m, n), dense: dt or fp32.
+ *   ep   : NONE, BIAS, RELU_BIAS or GELU_BIAS (other epilogues: GE_ERR_NOT_SUPPORTED).
+ *   bias : n values of type vec (dt or fp32); ignored (may be NULL) for NONE.
+ * x, D and bias are aligned to their elements; X with k a multiple of 8 and 16-byte aligned runs
+ * faster.
+ */
+ge_status_t gemm_epilog_w4_matmul(int64_t m, int64_t n, int64_t k, int64_t group, ge_dtype_t dt, ge_dtype_t out,
+                                  ge_epilog_t ep, const void* x, const void* codes, const void* scales,
+                                  const void* zeros, const void* bias, ge_dtype_t vec, void* D, void* stream);
+
+/* gemm_epilog_w4_gated - H (m, n) = act(G) * U, [G | U] = X . W^T + bias, of a gated weight (2 n, k)
+ * (halves 2), in one launch. bias: 2 n values of type vec, or NULL. */
+ge_status_t gemm_epilog_w4_gated(int64_t m, int64_t n, int64_t k, int64_t group, ge_dtype_t dt, ge_gate_t act,
+                                 const void* x, const void* codes, const void* scales, const void* zeros,
+                                 const void* bias, ge_dtype_t vec, void* h, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
