@@ -240,15 +240,22 @@ ge_status_t run(const void* fn, dim3 grid, int threads, size_t lds, void** param
                                                                                                            : GE_ERR_HIP;
 }
 
+template <int DT, bool GATED, int MT>
+const void* skinny_of(int64_t group) {
+  return group == 32   ? reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, MT, 4>)
+         : group == 64 ? reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, MT, 2>)
+                       : reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, MT, 1>);
+}
+
 template <int DT, bool GATED>
 ge_status_t skinny(W4Args& a, void* stream) {
   constexpr int NB = GATED ? 2 : 1;
   void* params[] = {&a};
   const int mt = a.m <= 16 ? 1 : a.m <= 32 ? 2 : 4;
   const int nw = mt == 4 ? 4 : 8;
-  const void* fn = mt == 1   ? reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, 1>)
-                   : mt == 2 ? reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, 2>)
-                             : reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, 4>);
+  const void* fn = mt == 1   ? skinny_of<DT, GATED, 1>(a.group)
+                   : mt == 2 ? skinny_of<DT, GATED, 2>(a.group)
+                             : skinny_of<DT, GATED, 4>(a.group);
   // (a launch has at most 65535 rows of workgroups)
   const int64_t step = (int64_t)65535 * 16 * mt, all = a.m;
   const char* x = static_cast<const char*>(a.x);

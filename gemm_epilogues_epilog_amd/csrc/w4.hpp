@@ -70,20 +70,21 @@ __device__ __forceinline__ float act_ep(float v, int ep) {
 }
 
 // A step of 128 k of the skinny kernel: codes, group scales and zeros of NB row groups, X of 16 MT
-// tokens.
-template <int NB, int MT>
+// tokens. NG groups to a step.
+template <int NB, int MT, int NG>
 struct W4Step {
   i32x4 w[NB], x[MT][4];
-  i32x2 s[NB][4];
-  uint32_t z[NB][4];
+  i32x2 s[NB][NG];
+  uint32_t z[NB][NG];
 };
 
 // Skinny kernel: a few tokens; bound by reading W once. A workgroup takes NB row groups (gated:
 // the gate's and the up projection's) and 16 MT tokens; its waves take the steps of 128 k in
 // turn and add their sums through LDS in wave order.
-template <int DT, bool GATED, int FB, int MT>
-__global__ __launch_bounds__(512, 2) void w4_skinny_kernel(W4Args p) {
+template <int DT, bool GATED, int FB, int MT, int NG>
+__global__ __launch_bounds__(512, MT == 4 ? 2 : MT == 2 ? 3 : 4) void w4_skinny_kernel(W4Args p) {
   constexpr int NB = GATED ? 2 * FB : FB;
+  using Step = W4Step<NB, MT, NG>;
   extern __shared__ __attribute__((aligned(16))) f32x4 red[];   // [wave][NB MT][64]
   const int nw = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, li = lane & 15, q = lane >> 4;
@@ -91,34 +92,31 @@ __global__ __launch_bounds__(512, 2) void w4_skinny_kernel(W4Args p) {
   const int rg0 = blockIdx.x * FB;
   const int64_t t0 = (int64_t)blockIdx.y * (16 * MT);
 
+  // (row groups past the last one have an empty range: zeros, and no reads)
   __amdgpu_buffer_rsrc_t rc[NB], rs[NB], rz[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const int in = rg0 + b % FB;
-    const int64_t rg = (in < p.rgs ? in : 0) + (b < FB ? 0 : (int64_t)p.rgs);
-    const int on = in < p.rgs;   // (a row group past the last one reads nothing)
+    const bool on = in < p.rgs;
+    const int64_t rg = (on ? in : 0) + (b < FB ? 0 : (int64_t)p.rgs);
     rc[b] = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p.codes) + rg * p.kt * kTileBytes, 0, on ? p.kt * kTileBytes : 0, kBufDword3);
     rs[b] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.scales) + rg * p.groups * kRows, 0, on ? p.groups * kRows * 2 : 0, kBufDword3);
     rz[b] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.zeros) + rg * p.groups * kRows, 0, on ? p.groups * kRows : 0, kBufDword3);
   }
   const char* xb = static_cast<const char*>(p.x) + t0 * p.k * 2;
   const __amdgpu_buffer_rsrc_t rx = rsrc(xb);
-  const int ng = p.group >= kTileK ? 1 : kTileK / p.group;   // groups of a step
 
-  const auto load = [&](W4Step<NB, MT>& st, int t) {
+  const auto load = [&](Step& st, int t) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b) st.w[b] = __builtin_amdgcn_raw_buffer_load_b128(rc[b], t * kTileBytes + lane * 16, 0, 0);
-    const int g0 = t * kTileK / p.group;
+    for (int b = 0; b < NB; ++b) st.w[b] = __builtin_amdgcn_raw_buffer_load_b128(rc[b], lane * 16, t * kTileBytes, 0);
+    const int g0 = NG > 1 ? t * NG : (int)((uint32_t)(t * kTileK) / (uint32_t)p.group);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j < ng) {
+    for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          st.s[b][j] = __builtin_amdgcn_raw_buffer_load_b64(rs[b], (g0 + j) * 32 + q * 8, 0, 0);
-          st.z[b][j] = __builtin_amdgcn_raw_buffer_load_b32(rz[b], (g0 + j) * 16 + q * 4, 0, 0);
-        }
+      for (int b = 0; b < NB; ++b) {
+        st.s[b][g] = __builtin_amdgcn_raw_buffer_load_b64(rs[b], q * 8 + g * 32, g0 * 32, 0);
+        st.z[b][g] = __builtin_amdgcn_raw_buffer_load_b32(rz[b], q * 4 + g * 16, g0 * 16, 0);
       }
-    }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const bool in = t0 + mt * 16 + li < p.m;
@@ -142,48 +140,38 @@ __global__ __launch_bounds__(512, 2) void w4_skinny_kernel(W4Args p) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[b][mt] = f32x4{0, 0, 0, 0};
 
-  const auto multiply = [&](const W4Step<NB, MT>& st) {
-    f32x4 part[NB][MT], sx[MT];
+  const auto multiply = [&](const Step& st) {
     const i32x4 ones = {kOnes<DT>, kOnes<DT>, kOnes<DT>, kOnes<DT>};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool first = j == 0 || (ng == 4) || (ng == 2 && j == 2);
+    for (int g = 0; g < NG; ++g) {
+      f32x4 part[NB][MT], sx[MT];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (first) sx[mt] = f32x4{0, 0, 0, 0};
-        sx[mt] = mma16<DT>(ones, st.x[mt][j], sx[mt]);
-      }
+      for (int j = 4 / NG * g; j < 4 / NG * (g + 1); ++j) {
+        const bool first = j == 4 / NG * g;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const i32x4 wq = w4_unpack<DT>((uint32_t)st.w[b][j]);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          if (first) part[b][mt] = f32x4{0, 0, 0, 0};
-          part[b][mt] = mma16<DT>(wq, st.x[mt][j], part[b][mt]);
-        }
-      }
-      const bool last = j == 3 || ng == 4 || (ng == 2 && j == 1);
-      if (last) {
-        const int g = ng == 4 ? j : ng == 2 ? j / 2 : 0;
+        for (int mt = 0; mt < MT; ++mt) sx[mt] = mma16<DT>(ones, st.x[mt][j], first ? f32x4{0, 0, 0, 0} : sx[mt]);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          // (g is a constant in each case: selects, no indexed registers)
-          const i32x2 s2 = g == 0 ? st.s[b][0] : g == 1 ? st.s[b][1] : g == 2 ? st.s[b][2] : st.s[b][3];
-          const uint32_t z4 = g == 0 ? st.z[b][0] : g == 1 ? st.z[b][1] : g == 2 ? st.z[b][2] : st.z[b][3];
+          const i32x4 wq = w4_unpack<DT>((uint32_t)st.w[b][j]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float s = Tr<DT>::widen((uint16_t)((uint32_t)s2[r / 2] >> (16 * (r & 1))));
-            const float z = (float)((z4 >> (8 * r)) & 255u);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              acc[b][mt][r] = __builtin_fmaf(s, __builtin_fmaf(-z, sx[mt][r], part[b][mt][r]), acc[b][mt][r]);
-          }
+          for (int mt = 0; mt < MT; ++mt)
+            part[b][mt] = mma16<DT>(wq, st.x[mt][j], first ? f32x4{0, 0, 0, 0} : part[b][mt]);
         }
       }
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float s = Tr<DT>::widen((uint16_t)((uint32_t)st.s[b][g][r / 2] >> (16 * (r & 1))));
+          const float z = (float)((st.z[b][g] >> (8 * r)) & 255u);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            acc[b][mt][r] = __builtin_fmaf(s, __builtin_fmaf(-z, sx[mt][r], part[b][mt][r]), acc[b][mt][r]);
+        }
     }
   };
 
-  W4Step<NB, MT> s0, s1;
+  Step s0, s1;
   if (w < p.kt) load(s0, w);
   for (int t = w; t < p.kt; t += 2 * nw) {
     if (t + nw < p.kt) load(s1, t + nw);
