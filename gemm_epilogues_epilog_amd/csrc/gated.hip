@@ -11,6 +11,7 @@
 
 #include "gated_general.hpp"
 #include "gated_host.hpp"
+#include "gated_tiles.hpp"
 #include "product.hpp"
 
 namespace gek {
@@ -162,6 +163,32 @@ ge_status_t product(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, con
   return general(M, N, K, dt, lay, A, B, D, false, nullptr, F32, 0, nullptr, cus, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
 }
 
+// The tile kernels with the gated epilogues: H (and Z) of X and W, or dZ of dY, Wd and Z.
+ge_status_t gated_tiles(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool backward, int act, const void* A,
+                        const void* B, const void* bias, int vec, const void* z, void* D, void* z_out, int cus,
+                        hipStream_t s) {
+  geh::Layout L;
+  if (ge_status_t st = gegh::gated_layout(m, n, k, dt, backward, cus, &L); st != GE_OK) return st;
+  Args a = {};
+  a.A = A;
+  a.B = B;
+  a.bias = bias;
+  a.D = D;
+  a.m = m;
+  a.n = (int32_t)n;
+  a.k = (int32_t)k;
+  a.vec_dt = vec;
+  a.tiles_m = L.tiles_m;
+  a.tiles_n = L.tiles_n;
+  a.group_m = L.group_m;
+  a.dp_tiles = L.dp_tiles;
+  a.persist_grid = L.persist_grid;
+  a.act = act;
+  a.z = z;
+  a.z_out = z_out;
+  return get_launch_gated((int)dt, backward, L.cfg)(a, L.tiles_m * L.tiles_n, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
+}
+
 ge_status_t column_sums(const void* x, int64_t m, int64_t cols, ge_dtype_t dt, void* out, ge_dtype_t vec, float* partial,
                         hipStream_t s) {
   int parts = m ? (int)gegh::colsum_parts(m, cols) : 0;
@@ -192,6 +219,9 @@ ge_status_t gemm_epilog_gated_forward(int64_t m, int64_t n, int64_t k, ge_dtype_
   int cus = 0;
   if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  if (gegh::fast_shape(m, n, k, dt, 2) && gegh::aligned(x, 16) && gegh::aligned(w, 16) && gegh::aligned(h, 16) &&
+      gegh::aligned(z, 16))
+    return gek::gated_tiles(m, n, k, dt, false, (int)act, x, w, bias, (int)vec, nullptr, h, z, cus, s);
   return gek::general(m, n, k, dt, 6, x, w, h, false, bias, (int)vec, (int)act, z, cus, s) == hipSuccess ? GE_OK
                                                                                                       : GE_ERR_HIP;
 }
@@ -228,7 +258,13 @@ ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t 
   if (m > 0) {
     const void* dh = dy;
     bool f32 = false;
-    if (w_down) {
+    if (w_down && gegh::fast_shape(m, n, d, dt, 2) && gegh::aligned(dy, 16) && gegh::aligned(w_down, 16) &&
+        gegh::aligned(z, 16)) {
+      if (ge_status_t st = gek::gated_tiles(m, n, d, dt, true, (int)act, dy, w_down, nullptr, 0, z, dz, nullptr, cus, s);
+          st != GE_OK)
+        return st;
+      dh = nullptr;
+    } else if (w_down) {
       dh = ws + at.dh;
       f32 = true;
       if (gek::general(m, n, d, dt, 0, dy, w_down, ws + at.dh, true, nullptr, 0, 0, nullptr, cus, s) != hipSuccess)
@@ -240,7 +276,7 @@ ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t 
     int a = (int)act;
     void* params[] = {&dh, &z, &dz, &m, &n, &a};
     const int64_t chunks = m * ((n + 7) / 8);
-    if (gek::launch(fn, dim3((unsigned)((chunks + 255) / 256)), 256, params, s) != hipSuccess) return GE_ERR_HIP;
+    if (dh && gek::launch(fn, dim3((unsigned)((chunks + 255) / 256)), 256, params, s) != hipSuccess) return GE_ERR_HIP;
     if (dx)
       if (ge_status_t st = gek::product(m, k, 2 * n, dt, 0, dz, w, dx, scratch, scratch_bytes, cus, s); st != GE_OK)
         return st;

@@ -3,6 +3,8 @@
 
 #include <algorithm>
 
+#include "tiles.hpp"
+
 namespace gegh {
 
 namespace {
@@ -73,6 +75,13 @@ ge_status_t fast_layout(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay,
   ge_status_t st = geh::make_layout(M, N, K, t, GE_EPILOG_NONE, lay, cus, cfg, true, true, L);
   if (st == GE_OK && L->ws_bytes > ws) st = geh::make_layout(M, N, K, t, GE_EPILOG_NONE, lay, cus, cfg, false, true, L);
   return st;
+}
+
+ge_status_t gated_layout(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool backward, int cus, geh::Layout* L) {
+  const ge_dtypes_t t = {dt, dt, dt};
+  const int64_t cols = backward ? n : 2 * n;
+  int cfg = geh::choose_cfg(m, cols, k, dt, cus, 2);   // (2: only configurations that take transposed operands)
+  return geh::make_layout(m, cols, k, t, GE_EPILOG_NONE, 2, cus, cfg, false, cfg == gek::CFG_L, L);
 }
 
 int64_t colsum_parts(int64_t m, int64_t cols) {

@@ -30,6 +30,7 @@
 
 #include <type_traits>
 
+#include "gated_epilogue.hpp"
 #include "kernels.hpp"
 #include "tiles.hpp"
 
@@ -441,7 +442,7 @@ __device__ __forceinline__ void read_piece(const O& op, const char* base, int s,
 
 // ---- operands in either storage order ----------------------------------------------
 // LAY bit 0: A is stored as A^T, a row-major (k, m) matrix; bit 1: B is stored as
-// B^T, a row-major (n, k) matrix. An operand tile then sits in LDS in the order it
+// B^T, a row-major (n, k) matrix; bit 2 (with bit 1): that of a gated block (HalvesCopy). An operand tile then sits in LDS in the order it
 // has in memory:
 //   k-major (A as stored normally, B given as B^T): MN rows of 2 BK bytes, 16-byte
 //     chunks swizzled by swz_a, one ds_read_b128 per 32-row fragment (8 k values);
@@ -507,6 +508,44 @@ struct OperandCopy {
   }
 };
 
+// Copies of a gated B^T (2 n stored rows: the gate's n, then the up projection's), k-major: the
+// tile's MN rows are, for each wave column of 2 HW, HW rows of the gate and the same HW of the up
+// projection. mn0 is the first of the n columns. As OperandCopy otherwise.
+template <int MN, int BK, int HW, int INST>
+struct HalvesCopy {
+  using G = TileGeom<MN, BK, true>;
+  static_assert(HW % G::RPI == 0, "a copy instruction stays in one half");
+  const char* base;
+  int64_t up;             // bytes from a gate row to the up projection's
+  uint32_t src[INST];
+  int kpos[INST];
+
+  __device__ static __forceinline__ bool second(int w, int j) { return (w * INST + j) * G::RPI % (2 * HW) >= HW; }
+  __device__ __forceinline__ void init(const void* X, int64_t mn0, int64_t mndim, int K, int w, int lane) {
+    const int64_t ldb = (int64_t)K * 2;
+    base = static_cast<const char*>(X) + mn0 * ldb;
+    up = mndim * ldb;
+#pragma unroll
+    for (int j = 0; j < INST; ++j) {
+      const int row = (w * INST + j) * G::RPI + lane / G::CHUNKS;   // of the tile
+      const int col = row / (2 * HW) * HW + row % HW;               // of the n columns
+      const int c = (lane % G::CHUNKS) ^ G::swz(row);
+      kpos[j] = 8 * c;
+      src[j] = (mn0 + col < mndim) ? (uint32_t)(col * ldb + c * 16) : kOOB;
+    }
+  }
+  __device__ __forceinline__ void issue(int k0, int K, int w, uint32_t dst) const {
+    const char* at = base + (int64_t)k0 * 2;
+    const bool tail = k0 + BK > K;
+#pragma unroll
+    for (int j = 0; j < INST; ++j) {
+      const i32x4 srd = make_srd(second(w, j) ? at + up : at);
+      const uint32_t off = (tail && k0 + kpos[j] >= K) ? kOOB : src[j];
+      copy_to_lds_b128(srd, off, dst + (w * INST + j) * 1024);
+    }
+  }
+};
+
 // Fragment reads of one operand for a wave whose fragments start at index wpos * W
 // of the tile (NBLK fragments of 32, KS k-steps per k-tile), from the LDS region at
 // byte `region` of a stage.
@@ -556,7 +595,7 @@ struct OperandsT {
   static constexpr bool TA = (LAY & 1) != 0, TB = (LAY & 2) != 0;
   static constexpr int MB = C::MB, NB = C::NB;
   OperandCopy<BM, BK, !TA, C::A_INST> ca;
-  OperandCopy<BN, BK, TB, C::B_INST> cb;
+  std::conditional_t<(LAY & 4) != 0, HalvesCopy<BN, BK, WN / 2, C::B_INST>, OperandCopy<BN, BK, TB, C::B_INST>> cb;
   FragRead<BM, BK, !TA, WM, MB, C::KSTEPS> fa;
   FragRead<BN, BK, TB, WN, NB, C::KSTEPS> fb;
   int K, w;
@@ -761,7 +800,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 1) void gemm_dtl_kernel
   int tm, tn;
   tile_coords(p, tm, tn);
   const int64_t m0 = (int64_t)tm * BM;
-  const int n0 = tn * BN;
+  const int n0 = tn * (EP == GATED ? BN / 2 : BN);
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w % C::WAVES_M, wn = w / C::WAVES_M;
@@ -772,6 +811,14 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 1) void gemm_dtl_kernel
   // every wave is done with the stages: reuse them as per-wave epilogue scratch
   wait_lgkmcnt<0>();
   barrier_only();
+  if constexpr (EP == GATED) {
+    if (p.bias) gated_bias<C::MB, C::NB>(p, acc, n0 + wn * (WN / 2), lane, smem + w * C::SCRATCH);
+#pragma unroll
+    for (int b = 0; b < C::MB; ++b)
+      gated_block<DT, C::MB, C::NB>(p, acc, b, m0 + wm * WM, n0 + wn * (WN / 2), lane, smem + w * C::SCRATCH);
+  } else if constexpr (EP == DGATED) {
+    dgated_tile<DT, C::MB, C::NB>(p, acc, m0 + wm * WM, n0 + wn * WN, lane, smem + w * C::SCRATCH);
+  } else
   epilogue_lds<DT, EP, C::MB, C::NB, WN>(p, acc, m0 + wm * WM, n0 + wn * WN, lane, smem + w * C::SCRATCH);
 }
 
@@ -918,12 +965,26 @@ struct MNMajorCopy {
   }
 };
 
+// A gated B^T (HalvesCopy): each copy wave copies the HW rows of one half.
+template <int MN, int BK, int HW, int INST>
+struct HalvesMajorCopy : KMajorCopy<MN, BK, INST> {
+  using B = KMajorCopy<MN, BK, INST>;
+  static_assert(INST * B::G::RPI == HW, "one half of a wave column per copy wave");
+  __device__ __forceinline__ void retarget(const void* X, int64_t mn0, int64_t mndim, int w, int) {
+    const int64_t c0 = mn0 + (w >> 1) * HW;
+    B::rows = static_cast<const char*>(X) + ((w & 1 ? mndim : 0) + c0) * B::ldb;
+    const int64_t left = mndim - c0;
+    B::valid = __builtin_amdgcn_readfirstlane((int)((left <= 0 ? 0 : left >= HW ? HW : left) * B::ldb));
+  }
+};
+
 template <int BM, int BN, int WM, int WN, int BK, int STAGES, int CW, int LAY>
 struct CopyPlanT {
   using C = DtlCfg<BM, BN, WM, WN, BK, STAGES, CW>;
   static constexpr bool TA = (LAY & 1) != 0, TB = (LAY & 2) != 0;
   std::conditional_t<TA, MNMajorCopy<BM, BK, C::A_INST>, KMajorCopy<BM, BK, C::A_INST>> ca;
-  std::conditional_t<TB, KMajorCopy<BN, BK, C::B_INST>, MNMajorCopy<BN, BK, C::B_INST>> cb;
+  std::conditional_t<(LAY & 4) != 0, HalvesMajorCopy<BN, BK, WN / 2, C::B_INST>,
+                     std::conditional_t<TB, KMajorCopy<BN, BK, C::B_INST>, MNMajorCopy<BN, BK, C::B_INST>>> cb;
   int w;
   uint32_t lds_base;
   __device__ __forceinline__ CopyPlanT(const Args& p, int w_, int lane, uint32_t lds) {
@@ -973,7 +1034,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 1) void gemm_persist_ke
     if constexpr (LAY == 0) return F::PIECES;
     else return O::PIECES;
   }();
-  constexpr int EPI_BYTES = 32 * WN * 2;   // epilogue rows of one wave
+  constexpr int TN = EP == GATED ? BN / 2 : BN;           // columns of D per tile
+  constexpr int EPI_BYTES = 32 * (EP == GATED ? WN / 2 : WN) * 2;   // epilogue rows of one wave
+  static_assert(EP != DGATED || EPI_BYTES >= 4096, "a 32 x 32 block of fp32");
   static_assert(DT == F16 || DT == BF16, "16-bit types only");
   static_assert(C::LDS + C::NW * EPI_BYTES <= 160 * 1024, "LDS");
   static_assert(KS % 2 == 0, "every k-tile starts on fragment buffer 0");
@@ -992,7 +1055,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 1) void gemm_persist_ke
   int tm, tn;
   raster(p, xcd_remap(v, T), tm, tn);
   int64_t m0 = (int64_t)tm * BM;
-  int n0 = tn * BN;
+  int n0 = tn * TN;
   const uint32_t lds = (uint32_t)(uintptr_t)(lds_void*)smem;
   const O op(p, m0, n0, w, wm, wn, lane, lds);   // fragment reads only
   CP cp(p, w, lane, lds);
@@ -1014,7 +1077,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 1) void gemm_persist_ke
     for (int b = 0; b < MB; ++b) {
       const int64_t row = m0 + wm * WM + 32 * b + (l & 31);
       bbits[b] = 0;
-      if constexpr (EP != NONE && EP != DRELU_BGRAD) {
+      if constexpr (EP != NONE && EP != DRELU_BGRAD && EP != GATED && EP != DGATED) {
         if (row < p.m) bbits[b] = load_vec_bits(p.bias, p.vec_dt, row);
       }
       if constexpr (EP == DRELU_BGRAD) {
@@ -1112,11 +1175,19 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 1) void gemm_persist_ke
 #pragma unroll
       for (int u = 0; u < STAGES; ++u) ktile(std::false_type{}, std::false_type{}, kt + u, u, more);
     }
-    if (more) cp.retarget(p, (int64_t)tmn * BM, tnn * BN, opaque(lane));
+    if (more) cp.retarget(p, (int64_t)tmn * BM, tnn * TN, opaque(lane));
 #pragma unroll
     for (int u = 0; u < STAGES; ++u) ktile(std::true_type{}, std::false_type{}, KT - STAGES + u, u, more);
 
     const int elane = opaque(lane);   // the epilogue's lane arithmetic stays out of the k loop
+    if constexpr (EP == GATED) {
+      if (p.bias) gated_bias<MB, NB>(p, acc, n0 + wn * (WN / 2), elane, scratch);
+#pragma unroll
+      for (int b = 0; b < MB; ++b)
+        gated_block<DT, MB, NB>(p, acc, b, m0 + wm * WM, n0 + wn * (WN / 2), elane, scratch);
+    } else if constexpr (EP == DGATED) {
+      dgated_tile<DT, MB, NB>(p, acc, m0 + wm * WM, n0 + wn * WN, elane, scratch);
+    } else
 #pragma unroll
     for (int b = 0; b < MB; ++b)
       epilogue_block<DT, EP, MB, NB, WN>(p, acc, b, vec_value(bbits[b], p.vec_dt), mwords[b], m0 + wm * WM,
@@ -1124,7 +1195,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 1) void gemm_persist_ke
     if (!more) break;
     v = vn;
     m0 = (int64_t)tmn * BM;
-    n0 = tnn * BN;
+    n0 = tnn * TN;
     load_bias();
     read_all(smem, 0, fr[0]);   // k-tile 0 of the new tile, published by the last barrier
   }

@@ -35,7 +35,9 @@
 namespace gek {
 
 enum Dt { F32 = 0, F16 = 1, BF16 = 2 };
-enum Ep { NONE = 0, RELU_BIAS = 1, GELU_BIAS = 2, RELU_AUX_BIAS = 3, DRELU_BGRAD = 4, BIAS = 5 };
+enum Ep { NONE = 0, RELU_BIAS = 1, GELU_BIAS = 2, RELU_AUX_BIAS = 3, DRELU_BGRAD = 4, BIAS = 5,
+          // of the gated feed-forward block only (gated_epilogue.hpp)
+          GATED = 6, DGATED = 7 };
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
@@ -77,6 +79,11 @@ struct Args {
   // Persistent kernels: workgroups launched (one per compute unit), each walking the
   // tile order with that stride; 0 when the plan launches one workgroup per tile.
   int32_t persist_grid;
+  // Gated feed-forward block: the activation, Z = [G | U] (m, 2 n) that DGATED reads, and where
+  // GATED writes it (null: nowhere). GATED: n columns of D, B^T has 2 n rows; DGATED: D is dZ (m, 2 n).
+  int32_t act;
+  const void* z;
+  void* z_out;
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base) {

@@ -85,6 +85,38 @@ def test_forward(gpu, m, n, k, dtype):
         check_forward(x, w, b, act, dtype, h, z, "f32 bias")
 
 
+# the 256 x 256 tiles: persistent (k a multiple of 128, from 256 on) and one workgroup a tile; a
+# three-stage ring (k of 24 tiles or more); ragged rows and columns; more tiles than compute units
+LARGE = [(2048, 2176, 256), (1999, 2168, 384), (2048, 2176, 320), (1801, 2200, 200), (130, 264, 1600), (2300, 4100, 264)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k", LARGE)
+def test_forward_tiles(gpu, m, n, k, dtype):
+    for act, bias in (("SILU", False), ("GELU", True), ("RELU", True)):
+        x, w, b = make(m, n, k, dtype, m + n + k, bias=bias)
+        h, z = gated.gated_forward(x, w, b, act=act, save=True)
+        check_forward(x, w, b, act, dtype, h, z, act)
+        if b is not None:
+            b = b.float()
+            h, z = gated.gated_forward(x, w, b, act=act, save=True)
+            check_forward(x, w, b, act, dtype, h, z, act)
+        assert torch.equal(gated.gated_forward(x, w, b, act=act)[0], h)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,d", [(2048, 4352, 256), (1999, 4344, 384), (2048, 4352, 320), (1801, 4400, 200), (130, 264, 1600)])
+def test_backward_tiles(gpu, m, n, d, dtype):
+    for act in ACTS:
+        x, w, _ = make(m, n, 64, dtype, m + n + d, bias=False)
+        g = torch.Generator().manual_seed(d)
+        h, z = gated.gated_forward(x, w, act=act, save=True)
+        wd = (torch.randn(d, n, generator=g) * n ** -0.5).to(T[dtype]).cuda()
+        dy = (torch.randn(m, d, generator=g) * 0.3).to(T[dtype]).cuda()
+        out = gated.gated_backward(dy, x, w, z, w_down=wd, h=h, act=act, bias_grad="f32")
+        check_backward(dy, x, w, z, wd, h, act, dtype, out, act)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("m,d,n", [(1, 1, 1), (1, 512, 1376), (3, 33, 129), (40, 264, 1000), (130, 500, 96), (257, 128, 3000)])
 def test_down(gpu, m, d, n, dtype):
