@@ -8,6 +8,10 @@
 #include "w4_host.hpp"
 
 namespace gek {
+
+const void* w4_tile_f16(int cfg, bool gated, bool g32, bool xd);    // w4_tile_f16.hip
+const void* w4_tile_bf16(int cfg, bool gated, bool g32, bool xd);   // w4_tile_bf16.hip
+
 namespace {
 
 struct W4Weight {
@@ -270,6 +274,18 @@ ge_status_t skinny(W4Args& a, void* stream) {
   return GE_OK;
 }
 
+ge_status_t tiled(W4Args& a, int cfg, ge_dtype_t dt, bool gated, void* stream) {
+  const gew4::W4TileCfg& T = gew4::kTiles[cfg];
+  W4Launch L;
+  L.tiles_m = (int32_t)gew4::ceil_div(a.m, T.bm);
+  L.tiles_n = (int32_t)gew4::ceil_div(gated ? 2 * (int64_t)a.n : a.n, T.bn);
+  L.group_m = 8;
+  const bool g32 = a.group == 32, xd = a.vecx != 0;
+  const void* fn = dt == GE_F16 ? w4_tile_f16(cfg, gated, g32, xd) : w4_tile_bf16(cfg, gated, g32, xd);
+  void* params[] = {&a, &L};
+  return run(fn, dim3((unsigned)((int64_t)L.tiles_m * L.tiles_n)), T.waves * 64, 0, params, stream);
+}
+
 ge_status_t multiply(int64_t m, int64_t n, int64_t k, int64_t group, ge_dtype_t dt, ge_dtype_t out, bool gated, int ep,
                      const void* x, const void* codes, const void* scales, const void* zeros, const void* bias,
                      ge_dtype_t vec, void* D, void* stream) {
@@ -292,6 +308,9 @@ ge_status_t multiply(int64_t m, int64_t n, int64_t k, int64_t group, ge_dtype_t 
   a.out = (int32_t)out;
   a.ep = ep;
   a.vecx = k % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+  int cus = 0;
+  if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
+  if (const int cfg = gew4h::choose(m, n, k, group, gated, cus); cfg >= 0) return tiled(a, cfg, dt, gated, stream);
   if (dt == GE_F16) return gated ? skinny<F16, true>(a, stream) : skinny<F16, false>(a, stream);
   return gated ? skinny<BF16, true>(a, stream) : skinny<BF16, false>(a, stream);
 }
@@ -365,8 +384,6 @@ ge_status_t gemm_epilog_w4_matmul(int64_t m, int64_t n, int64_t k, int64_t group
   if (ge_status_t st = gew4h::check_product(m, n, dt, out, x, bias, vec, D); st != GE_OK) return st;
   if (ep != GE_EPILOG_NONE && !bias) return GE_ERR_NULL_POINTER;
   if (m == 0) return GE_OK;
-  int cus = 0;
-  if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
   return gek::multiply(m, n, k, group, dt, out, false, (int)ep, x, codes, scales, zeros,
                        ep == GE_EPILOG_NONE ? nullptr : bias, vec, D, stream);
 }
@@ -379,8 +396,6 @@ ge_status_t gemm_epilog_w4_gated(int64_t m, int64_t n, int64_t k, int64_t group,
   if (act != GE_GATE_SILU && act != GE_GATE_GELU && act != GE_GATE_RELU) return GE_ERR_INVALID_VALUE;
   if (ge_status_t st = gew4h::check_product(m, n, dt, dt, x, bias, vec, h); st != GE_OK) return st;
   if (m == 0) return GE_OK;
-  int cus = 0;
-  if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
   return gek::multiply(m, n, k, group, dt, dt, true, (int)act, x, codes, scales, zeros, bias, vec, h, stream);
 }
 

@@ -35,6 +35,11 @@ struct W4Args {
   int32_t vecx;          // X's rows are 16-byte aligned and whole 16-byte chunks
 };
 
+// Grid of the tile kernel.
+struct W4Launch {
+  int32_t tiles_m, tiles_n, group_m;
+};
+
 // The eight codes of a dword, in the order of k, as 16-bit numbers.
 template <int DT>
 __device__ __forceinline__ i32x4 w4_unpack(uint32_t w) {

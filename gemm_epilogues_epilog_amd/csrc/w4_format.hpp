@@ -24,7 +24,11 @@ constexpr int64_t row_groups(int64_t rows, int halves) { return ceil_div(rows / 
 constexpr int64_t k_tiles(int64_t k) { return ceil_div(k, kTileK); }
 constexpr int64_t k_groups(int64_t k, int64_t group) { return ceil_div(k, group); }
 
-// Tokens that one workgroup of the skinny kernel takes, and its waves.
-constexpr int kMaxWaves = 8;
+// Tiles of the products: tokens by rows of W, and waves.
+struct W4TileCfg {
+  int bm, bn, waves;
+};
+enum W4Tiles { W4_L = 0, W4_M, W4_S, W4_COUNT };
+constexpr W4TileCfg kTiles[W4_COUNT] = {{256, 256, 8}, {128, 128, 4}, {64, 128, 4}};
 
 }  // namespace gew4

@@ -23,4 +23,7 @@ ge_status_t check_dequantize(int64_t rows, int64_t k, ge_dtype_t dt, ge_dtype_t 
 ge_status_t check_product(int64_t m, int64_t n, ge_dtype_t dt, ge_dtype_t out, const void* x, const void* bias,
                           ge_dtype_t vec, const void* D);
 
+// The kernel of a product: a tile (gew4::W4Tiles), or -1 for the skinny kernel.
+int choose(int64_t m, int64_t n, int64_t k, int64_t group, bool gated, int cus);
+
 }  // namespace gew4h

@@ -1,0 +1,409 @@
+// Tile kernel of the products with 4-bit weights (layout: w4_format.hpp): dozens to thousands of
+// tokens.
+//
+// A BM x BN tile of D, k in tiles of 64. X goes straight into LDS; W's codes go through registers,
+// each once per workgroup, and lie in LDS as 16-bit numbers in the same k-major order. The two
+// operands then meet in v_mfma_f32_32x32x16 as in the 16-bit kernels (gemm_dtl.hpp).
+//
+// No weight is rounded: a scale s is split into a power of two p and f = s / p, and W in LDS is
+// (q - z) p, exact in 16 bits. The sums are held in units of f: where a group of a row begins they
+// are multiplied by the last group's f over the new one's (one fp32 multiplication per sum and
+// group, no second set of sums), and by the last f at the end. p takes the whole exponent of s
+// where (q - z) p stays a normal number, so f lies in [1, 2) but for scales out there, and the
+// quotients stay far from fp32's limits.
+//
+// At the end of k-tile t every wave waits until its copies of X's tile t + 1 have landed and its
+// reads of tile t and its writes of W's tile t + 1 are done; one barrier publishes tile t + 1 and
+// releases tile t's stage, which X's tile t + 2 is copied into and, during the products of t + 1,
+// W's tile t + 2 is converted into. Codes and scales are loaded two k-tiles at a time, one such
+// pair ahead.
+#pragma once
+
+#include "gemm_dtl.hpp"
+#include "w4.hpp"
+
+namespace gek {
+
+template <int BM_, int BN_, int WM_, int WN_>
+struct W4Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN, NW = WAVES_M * WAVES_N, NT = NW * 64;
+  static constexpr int MB = WM / 32, NB = WN / 32;
+  static constexpr int X_BYTES = BM * 128, W_BYTES = BN * 128, STAGE = X_BYTES + W_BYTES;
+  static constexpr int XI = X_BYTES / 1024 / NW;      // copies of X per wave and k-tile
+  static constexpr int RG = BN / 16 / NW;             // row groups that a wave converts
+  static constexpr int OFF_R = 2 * STAGE;             // factors of the sums: [stage][group of the k-tile][BN]
+  static constexpr int EPI = 8192;                    // epilogue bytes per wave (in the stages)
+  static constexpr int LDS = OFF_R + 2 * 2 * BN * 4;
+  static_assert(X_BYTES % (1024 * NW) == 0 && BN % (16 * NW) == 0, "shares of a wave");
+  static_assert(NW * EPI <= OFF_R && LDS <= 160 * 1024, "LDS");
+};
+
+template <int N, class F, int I = 0>
+__device__ __forceinline__ void w4_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    w4_for<N, F, I + 1>(static_cast<F&&>(f));
+  }
+}
+
+// Waits whose place among the loads and copies the compiler keeps.
+template <int N>
+__device__ __forceinline__ void w4_wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"i"(N) : "memory");
+}
+
+// A scale in two: its power of two p (0 for 0, the scale itself if it is not finite), and f.
+template <int DT>
+__device__ __forceinline__ void w4_split(uint16_t bits, float& p, float& f) {
+  const float s = Tr<DT>::widen(bits);
+  const uint32_t e = __float_as_uint(s) & 0x7f800000u;
+  constexpr uint32_t lo = (uint32_t)(127 - (DT == BF16 ? 100 : 14)) << 23, hi = (uint32_t)(127 + (DT == BF16 ? 100 : 11)) << 23;
+  const uint32_t c = min(max(e, lo), hi);
+  p = __uint_as_float(c);
+  f = s * __uint_as_float((254u << 23) - c);
+  if (s == 0.0f) {
+    p = 0.0f;
+    f = 1.0f;
+  } else if (e == 0x7f800000u) {
+    p = s;
+    f = 1.0f;
+  }
+}
+
+// The eight codes of a dword as (q - z) p, nz = -z p.
+template <int DT>
+__device__ __forceinline__ i32x4 w4_expand(uint32_t w, float p, float nz) {
+  const uint32_t h[2] = {w & 0x0f0f0f0fu, (w >> 4) & 0x0f0f0f0fu};
+  i32x4 o;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(h[i], 512.0f, false);
+    const auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(h[i], 512.0f, true);
+    o[2 * i] = (int)Tr<DT>::pack2(__builtin_fmaf(a[0], p, nz), __builtin_fmaf(a[1], p, nz));
+    o[2 * i + 1] = (int)Tr<DT>::pack2(__builtin_fmaf(b[0], p, nz), __builtin_fmaf(b[1], p, nz));
+  }
+  return o;
+}
+
+// Codes, scales and zeros of a pair of k-tiles; GPT groups to a k-tile.
+template <int RG, int GPT>
+struct W4Codes {
+  i32x4 c[RG];
+  uint16_t s[RG][2 * GPT];
+  uint8_t z[RG][2 * GPT];
+  // The loads are done (the caller has waited): later uses wait for nothing.
+  __device__ __forceinline__ void landed() {
+#pragma unroll
+    for (int r = 0; r < RG; ++r) {
+      asm volatile("" : "+v"(c[r]));
+#pragma unroll
+      for (int g = 0; g < 2 * GPT; ++g) {
+        int a = s[r][g], b = z[r][g];
+        asm volatile("" : "+v"(a), "+v"(b));
+        s[r][g] = (uint16_t)a;
+        z[r][g] = (uint8_t)b;
+      }
+    }
+  }
+};
+
+// Epilogue: 32 x 32 blocks of sums through fp32 scratch (gated: one of the gate and one of the up
+// projection), so that a lane gets eight neighbouring columns of a token and memory sees whole
+// pieces of rows at any alignment.
+template <int DT, bool GATED, class C>
+__device__ __forceinline__ void w4_tile_epilogue(const W4Args& p, const f32x16 (&acc)[C::NB][C::MB], int64_t m0, int n0,
+                                                 int lane, char* scratch) {
+  constexpr int NH = GATED ? C::NB / 2 : C::NB;
+  const int lrow = lane & 31, lhi = lane >> 5, r16 = lane >> 2, c = lane & 3;
+  const auto swz = [](int row) { return (row ^ (row >> 3)) & 7; };   // 16-byte units of 128-byte rows
+  const auto put = [&](const f32x16& v, char* to) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      *reinterpret_cast<f32x4*>(to + lrow * 128 + (((2 * g + lhi) ^ swz(lrow)) << 4)) =
+          f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+  };
+  const auto get = [&](const char* from, int h, float (&v)[8]) {
+    const int row = 16 * h + r16;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const f32x4 d = *reinterpret_cast<const f32x4*>(from + row * 128 + (((2 * c + u) ^ swz(row)) << 4));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * u + e] = d[e];
+    }
+  };
+#pragma unroll
+  for (int a = 0; a < NH; ++a) {
+    const int64_t col = n0 + 32 * a + 8 * c, left = p.n - col;
+    float bg[8], bu[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      bg[e] = p.bias && e < left ? load_vec(p.bias, p.vec, col + e) : 0.0f;
+      bu[e] = GATED && p.bias && e < left ? load_vec(p.bias, p.vec, p.n + col + e) : 0.0f;
+    }
+#pragma unroll
+    for (int b = 0; b < C::MB; ++b) {
+      put(acc[a][b], scratch);
+      if constexpr (GATED) put(acc[a + NH][b], scratch + 4096);
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t token = m0 + 32 * b + 16 * h + r16;
+        float y[8];
+        get(scratch, h, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] += bg[e];
+        if constexpr (GATED) {
+          float u[8];
+          get(scratch + 4096, h, u);
+          with_gate(p.ep, [&](auto act) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = gate_act<decltype(act)::value, false>(y[e]) * (u[e] + bu[e]);
+          });
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = act_ep(y[e], p.ep);
+        }
+        if (token < p.m && left > 0) {
+          const int64_t at = token * p.n + col;
+          const float y0[4] = {y[0], y[1], y[2], y[3]}, y1[4] = {y[4], y[5], y[6], y[7]};
+          if (p.out == F32) {
+            store4<F32>(p.D, at, left, y0);
+            store4<F32>(p.D, at + 4, left - 4, y1);
+          } else if (left >= 8) {
+            const i32x4 o = {(int)Tr<DT>::pack2(y[0], y[1]), (int)Tr<DT>::pack2(y[2], y[3]), (int)Tr<DT>::pack2(y[4], y[5]),
+                             (int)Tr<DT>::pack2(y[6], y[7])};
+            __builtin_memcpy(static_cast<uint16_t*>(p.D) + at, &o, 16);
+          } else {
+            store4<DT>(p.D, at, left, y0);
+            store4<DT>(p.D, at + 4, left - 4, y1);
+          }
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+}
+
+// G32: groups of 32 (two to a k-tile). XD: X's rows are whole 16-byte chunks, copied straight into
+// LDS; otherwise they go through registers.
+template <int DT, bool GATED, class C, bool G32, bool XD>
+__global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W4Launch L) {
+  constexpr int BM = C::BM, BN = C::BN, WM = C::WM, WN = C::WN, MB = C::MB, NB = C::NB, RG = C::RG, XI = C::XI;
+  constexpr int GPT = G32 ? 2 : 1, NCODE = RG * (1 + 4 * GPT), NMMA = MB * NB;
+  __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = w % C::WAVES_M, wn = w / C::WAVES_M;
+  const int li = lane & 15, q = lane >> 4, lrow = lane & 31, lhi = lane >> 5;
+  int tm, tn;
+  {
+    Args r;
+    r.tiles_m = L.tiles_m;
+    r.tiles_n = L.tiles_n;
+    r.group_m = L.group_m;
+    raster(r, xcd_remap(blockIdx.x, L.tiles_m * L.tiles_n), tm, tn);
+  }
+  const int64_t m0 = (int64_t)tm * BM;
+  const int n0 = tn * (GATED ? BN / 2 : BN);
+  const int KT = (p.k + 63) / 64, KT2 = (KT + 1) & ~1;
+  const uint32_t lds = (uint32_t)(uintptr_t)(lds_void*)smem;
+
+  // ---- X ----
+  uint32_t x_src[XI];
+  int x_chunk[XI];
+  const char* xb = static_cast<const char*>(p.x) + m0 * p.k * 2;
+#pragma unroll
+  for (int j = 0; j < XI; ++j) {
+    const int row = (w * XI + j) * 8 + lane / 8;
+    x_chunk[j] = (lane % 8) ^ swz_a<128>(row);
+    x_src[j] = m0 + row < p.m ? (uint32_t)(row * p.k * 2 + x_chunk[j] * 16) : kOOB;
+  }
+  i32x4 xr[XD ? 1 : XI];
+  auto issue_x = [&](int t) {
+    const int k0 = t * 64;
+    if constexpr (XD) {
+      // (a k-tile past the last one reads nothing: zeros)
+      const i32x4 srd = make_srd(xb + (int64_t)k0 * 2, t < KT ? 0x7fffffffu : 0u);
+      const bool tail = k0 + 64 > p.k;
+#pragma unroll
+      for (int j = 0; j < XI; ++j) {
+        const uint32_t off = tail && k0 + x_chunk[j] * 8 >= p.k ? kOOB : x_src[j];
+        copy_to_lds_b128(srd, off, lds + (t & 1) * C::STAGE + (w * XI + j) * 1024);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < XI; ++j) {
+        const int64_t row = (w * XI + j) * 8 + lane / 8;
+        const int64_t at = m0 + row < p.m ? row : 0;   // (tokens past the last one are not stored)
+        xr[j] = load_end<2>(xb + at * p.k * 2, k0 + x_chunk[j] * 8, p.k);
+      }
+    }
+  };
+  auto store_x = [&](int t) {
+    if constexpr (!XD) {
+#pragma unroll
+      for (int j = 0; j < XI; ++j)
+        *reinterpret_cast<i32x4*>(smem + (t & 1) * C::STAGE + (w * XI + j) * 1024 + lane * 16) = xr[j];
+    }
+  };
+
+  // ---- W ----
+  // Tile row groups of this wave: w RG .. + RG - 1; of a gated tile, pairs of groups alternate
+  // between the halves, so that each wave column has 32 rows of both.
+  __amdgpu_buffer_rsrc_t rc[RG], rs[RG], rz[RG];
+#pragma unroll
+  for (int r = 0; r < RG; ++r) {
+    const int i = w * RG + r;
+    const int in = n0 / 16 + (GATED ? i / 4 * 2 + i % 2 : i);
+    const bool on = in < p.rgs;
+    const int64_t rg = (on ? in : 0) + (GATED && i / 2 % 2 ? (int64_t)p.rgs : 0);
+    rc[r] = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p.codes) + rg * p.kt * kTileBytes, 0, on ? p.kt * kTileBytes : 0, kBufDword3);
+    rs[r] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.scales) + rg * p.groups * kRows, 0, on ? p.groups * kRows * 2 : 0, kBufDword3);
+    rz[r] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.zeros) + rg * p.groups * kRows, 0, on ? p.groups * kRows : 0, kBufDword3);
+  }
+  using Codes = W4Codes<RG, GPT>;
+  auto load_w = [&](Codes& d, int t) {   // k-tiles t and t + 1, t even
+#pragma unroll
+    for (int r = 0; r < RG; ++r) {
+      d.c[r] = __builtin_amdgcn_raw_buffer_load_b128(rc[r], lane * 16, t / 2 * kTileBytes, 0);
+#pragma unroll
+      for (int g = 0; g < 2 * GPT; ++g) {
+        const int at = G32 ? t * 2 + g : (int)((uint32_t)((t + g) * 64) / (uint32_t)p.group);
+        d.s[r][g] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[r], li * 2, at * 32, 0);
+        d.z[r][g] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rz[r], li, at * 16, 0);
+      }
+    }
+  };
+  float f[RG];   // of the group converted last
+#pragma unroll
+  for (int r = 0; r < RG; ++r) f[r] = 1.0f;
+  // Whether k-tile t begins a group (of 64 or more).
+  auto begins = [&](int t) { return G32 || (uint32_t)(t * 64) % (uint32_t)p.group == 0; };
+  // Converts the eight codes i of this wave's 2 RG per k-tile into k-tile t's stage: row group
+  // i / 2, dword 2 (t % 2) + i % 2.
+  auto convert = [&](Codes& d, int t, auto itag) {
+    constexpr int i = decltype(itag)::value, r = i / 2, h = i % 2;
+    const int g = (t & 1) * GPT + (G32 ? h : 0);
+    float pw, fn;
+    w4_split<DT>(g == 0 ? d.s[r][0] : g == 1 ? d.s[r][1] : g == 2 ? d.s[r][2 % (2 * GPT)] : d.s[r][3 % (2 * GPT)], pw, fn);
+    const uint8_t zb = g == 0 ? d.z[r][0] : g == 1 ? d.z[r][1] : g == 2 ? d.z[r][2 % (2 * GPT)] : d.z[r][3 % (2 * GPT)];
+    const int row = (w * RG + r) * 16 + li;   // of the tile
+    char* st = smem + (t & 1) * C::STAGE + C::X_BYTES + row * 128;
+    const uint32_t code = (uint32_t)(t & 1 ? d.c[r][2 + h] : d.c[r][h]);
+    *reinterpret_cast<i32x4*>(st + (((4 * h + q) ^ swz_a<128>(row)) << 4)) = w4_expand<DT>(code, pw, -(float)zb * pw);
+    if ((G32 || h == 0) && begins(t)) {
+      if (q == 0) reinterpret_cast<float*>(smem + C::OFF_R)[((t & 1) * 2 + (G32 ? h : 0)) * BN + row] = f[r] / fn;
+      f[r] = fn;
+    }
+  };
+
+  // ---- fragments ----
+  FragRead<BM, 64, true, WM, MB, 4> fx;
+  FragRead<BN, 64, true, WN, NB, 4> fw;
+  fx.init(wm, lane, 0);
+  fw.init(wn, lane, C::X_BYTES);
+  f32x16 acc[NB][MB];
+#pragma unroll
+  for (int a = 0; a < NB; ++a)
+#pragma unroll
+    for (int b = 0; b < MB; ++b) acc[a][b] = f32x16{};
+  // Multiplies the sums by the factors of group g of k-tile t.
+  auto rescale = [&](int t, int g) {
+    const float* R = reinterpret_cast<const float*>(smem + C::OFF_R) + ((t & 1) * 2 + g) * BN + wn * WN + 4 * lhi;
+#pragma unroll
+    for (int a = 0; a < NB; ++a)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(R + 32 * a + 8 * c);
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[a][b][4 * c + e] *= v[e];
+      }
+  };
+  struct Frag {
+    i32x4 x[MB], w[NB];
+  };
+  auto read = [&](Frag& fr, int t, int s) {
+    const char* st = smem + (t & 1) * C::STAGE;
+#pragma unroll
+    for (int a = 0; a < NB; ++a) fr.w[a] = fw.read(st, s, a);
+#pragma unroll
+    for (int b = 0; b < MB; ++b) fr.x[b] = fx.read(st, s, b);
+  };
+
+  Codes now, next;   // codes of the k-tiles being converted, and of the pair after them
+  load_w(now, 0);
+  issue_x(0);
+  store_x(0);
+  issue_x(1);
+  now.landed();
+  w4_for<2 * RG>([&](auto i) { convert(now, 0, i); });
+  w4_for<2 * RG>([&](auto i) { convert(now, 1, i); });
+  load_w(next, 2);
+  w4_wait_vm<XD ? NCODE : 0>();
+  wait_lgkmcnt<0>();
+  barrier_only();
+  Frag fr[2];
+  read(fr[0], 0, 0);
+
+  // k-tile t, t % 2 == u; `now` holds the codes of k-tiles t + 2 - u .. once landed
+  auto ktile = [&](auto utag, int t) {
+    constexpr int u = decltype(utag)::value;
+    if (!G32 && t > 0 && begins(t)) rescale(t, 0);
+    w4_for<4>([&](auto stag) {
+      constexpr int s = decltype(stag)::value;
+      constexpr bool last = s == 3;
+      if (G32 && s % 2 == 0 && (t > 0 || s > 0)) rescale(t, s / 2);
+      if constexpr (last) {
+        wait_lgkmcnt<0>();   // reads of k-tile t, writes of W's t + 1
+        if constexpr (!XD) {
+          store_x(t + 1);
+          wait_lgkmcnt<0>();
+        }
+        // copies of X's t + 1 have landed; codes loaded after them may still be on their way
+        if constexpr (u == 0) w4_wait_vm<0>();
+        else if constexpr (XD) w4_wait_vm<NCODE>();
+        barrier_only();
+        if constexpr (u == 0) {   // W's t + 2 begins a pair
+          next.landed();
+          now = next;
+        }
+        issue_x(t + 2);
+        if constexpr (u == 0) {
+          load_w(next, t + 4);
+          asm volatile("" ::: "memory");   // (the loads are issued here: the next waits count them)
+        }
+        read(fr[0], t + 1, 0);
+        if (t + 2 < KT2) convert(now, t + 2, std::integral_constant<int, 0>{});
+      } else {
+        read(fr[(s + 1) & 1], t, s + 1);
+        // the rest of W's t + 1, whose first part came with the last step of k-tile t - 1
+        if (t > 0 && t + 1 < KT2) {
+          constexpr int per = (2 * RG - 1 + 2) / 3, i0 = 1 + s * per, i1 = i0 + per < 2 * RG ? i0 + per : 2 * RG;
+          w4_for<(i1 > i0 ? i1 - i0 : 0)>([&](auto i) { convert(now, t + 1, std::integral_constant<int, i0 + decltype(i)::value>{}); });
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NMMA; ++i) acc[i / MB][i % MB] = Tr<DT>::mma(fr[s & 1].w[i / MB], fr[s & 1].x[i % MB], acc[i / MB][i % MB]);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  for (int t = 0; t < KT2; t += 2) {
+    ktile(std::integral_constant<int, 0>{}, t);
+    ktile(std::integral_constant<int, 1>{}, t + 1);
+  }
+  wait_vmcnt<0>();
+  wait_lgkmcnt<0>();
+  // the last groups' f of every row, and the stages to the epilogue
+#pragma unroll
+  for (int r = 0; r < RG; ++r)
+    if (q == 0) reinterpret_cast<float*>(smem + C::OFF_R)[(w * RG + r) * 16 + li] = f[r];
+  __syncthreads();
+  rescale(0, 0);
+  w4_tile_epilogue<DT, GATED, C>(p, acc, m0 + wm * WM, n0 + wn * (GATED ? WN / 2 : WN), lane, smem + w * C::EPI);
+}
+
+}  // namespace gek

@@ -1,0 +1,6 @@
+// The 4-bit tile kernel for f16 activations.
+#include "w4_tile_inst.hpp"
+
+namespace gek {
+const void* w4_tile_f16(int cfg, bool gated, bool g32, bool xd) { return w4_tile_pick<F16>(cfg, gated, g32, xd); }
+}  // namespace gek

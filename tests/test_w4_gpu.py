@@ -207,11 +207,52 @@ def test_gated(gpu, m, n, k, group, dtype):
     check_gated(*a, dtype, [("SILU", True), ("GELU", False), ("RELU", True)])
 
 
+# 256 x 256, 128 x 128 and 64 x 128 tiles: more than one of each, ragged rows, columns and k, an odd
+# number of k-tiles, one k-tile, groups longer than k
+TILES = [(1030, 8208, 392, 64), (1030, 8208, 520, 128), (2100, 4100, 64, 64), (1000, 4130, 456, 32), (1290, 8300, 131, 128),
+         (900, 5000, 130, 32), (700, 1500, 1100, 256), (130, 260, 2000, 64), (66, 1000, 24, 1024), (257, 4099, 333, 64)]
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("m", [1, 5, 40, 200])
+@pytest.mark.parametrize("m,n,k,group", TILES)
+def test_tiles(gpu, m, n, k, group, dtype):
+    check(*make(m, n, k, group, dtype, m + n + k), dtype, [("GELU_BIAS", None), ("BIAS", "f32")])
+    check_gated(*make(m, n // 2, k, group, dtype, m + n, gated=True), dtype, [("SILU", True), ("RELU", False)])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m", [1, 20, 100, 600, 2100])
+@pytest.mark.parametrize("group", [32, 128])
+def test_scales_far_apart(gpu, m, group, dtype):
+    """Zero scales, scales from the type's smallest to large ones, negative ones, beside each other in
+    a row; a NaN and an infinite scale reach their own column alone."""
+    n, k = 4200, 512
+    g = torch.Generator().manual_seed(m)
+    G = k // group
+    q = torch.randint(0, 16, (n, k), generator=g).to(torch.uint8)
+    z = torch.randint(0, 16, (n, G), generator=g).to(torch.uint8)
+    lo, hi = (-24, 12) if dtype == "f16" else (-60, 40)
+    s = torch.exp2(torch.randint(lo, hi, (n, G), generator=g).double()) * (1 + torch.randint(0, 8, (n, G), generator=g) / 8)
+    s = s * torch.where(torch.rand(n, G, generator=g) < 0.3, -1.0, 1.0) * (torch.rand(n, G, generator=g) > 0.2)
+    s = s.to(T[dtype])
+    s[7], s[9, 0], s[11, 1] = 0, float("nan"), float("inf")
+    x = torch.randn(m, k, generator=g).to(T[dtype])
+    W = w4.w4_pack(nibbles(q).cuda(), s.cuda(), z.cuda(), group)
+    got = w4.w4_matmul(x.cuda(), W, out_dtype="f32")
+    assert got[:, 9].isnan().all() and not torch.isfinite(got[:, 11]).any() and (got[:, 7] == 0).all()
+    keep = [i for i in range(n) if i not in (9, 11)]
+    s2 = s.double()[keep]
+    full = values64(q[keep], s2, z[keep], group).cuda()
+    mags = ((q[keep].double() + z[keep].double().repeat_interleave(group, 1)) * s2.abs().repeat_interleave(group, 1)).cuda()
+    X = x.double().cuda()
+    close(got[:, keep], X @ full.t(), (8 * math.sqrt(k) + 8) * U * (X.abs() @ mags.t()), "f32")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m", [1, 5, 40, 200, 2100])
 def test_exact_sums(gpu, m, dtype):
     """Whole numbers small enough for exact fp32 sums: equal, whatever the order."""
-    n, k, group = 70, 500, 64
+    n, k, group = (70 if m < 1000 else 4200), 500, 64
     g = torch.Generator().manual_seed(m)
     q = torch.randint(0, 16, (n, k), generator=g).to(torch.uint8)
     s = torch.exp2(torch.randint(0, 3, (n, -(-k // group)), generator=g).float()).to(T[dtype])
