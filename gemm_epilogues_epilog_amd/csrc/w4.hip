@@ -310,7 +310,7 @@ ge_status_t multiply(int64_t m, int64_t n, int64_t k, int64_t group, ge_dtype_t 
   a.vecx = k % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
   int cus = 0;
   if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
-  if (const int cfg = gew4h::choose(m, n, k, group, gated, cus); cfg >= 0) return tiled(a, cfg, dt, gated, stream);
+  if (const int cfg = gew4h::choose(m, n, k, group, gated, a.vecx != 0, cus); cfg >= 0) return tiled(a, cfg, dt, gated, stream);
   if (dt == GE_F16) return gated ? skinny<F16, true>(a, stream) : skinny<F16, false>(a, stream);
   return gated ? skinny<BF16, true>(a, stream) : skinny<BF16, false>(a, stream);
 }

@@ -64,13 +64,13 @@ ge_status_t check_product(int64_t m, int64_t n, ge_dtype_t dt, ge_dtype_t out, c
   return GE_OK;
 }
 
-int choose(int64_t m, int64_t n, int64_t k, int64_t group, bool gated, int cus) {
+int choose(int64_t m, int64_t n, int64_t k, int64_t group, bool gated, bool aligned, int cus) {
   if (const char* e = std::getenv("W4_TILE")) return std::atoi(e);
   (void)k;
   const int64_t rows = gated ? 2 * n : n;
   if (m <= 64) return -1;
   const auto tiles = [&](int c) { return gew4::ceil_div(m, gew4::kTiles[c].bm) * gew4::ceil_div(rows, gew4::kTiles[c].bn); };
-  if (2 * tiles(gew4::W4_L) > cus && group != 32) return gew4::W4_L;
+  if (2 * tiles(gew4::W4_L) > cus && group != 32 && aligned) return gew4::W4_L;
   if (tiles(gew4::W4_M) >= cus) return gew4::W4_M;
   return gew4::W4_S;
 }

@@ -24,6 +24,7 @@ ge_status_t check_product(int64_t m, int64_t n, ge_dtype_t dt, ge_dtype_t out, c
                           ge_dtype_t vec, const void* D);
 
 // The kernel of a product: a tile (gew4::W4Tiles), or -1 for the skinny kernel.
-int choose(int64_t m, int64_t n, int64_t k, int64_t group, bool gated, int cus);
+// aligned: X's rows are whole 16-byte chunks.
+int choose(int64_t m, int64_t n, int64_t k, int64_t group, bool gated, bool aligned, int cus);
 
 }  // namespace gew4h

@@ -14,9 +14,11 @@
 //
 // At the end of k-tile t every wave waits until its copies of X's tile t + 1 have landed and its
 // reads of tile t and its writes of W's tile t + 1 are done; one barrier publishes tile t + 1 and
-// releases tile t's stage, which X's tile t + 2 is copied into and, during the products of t + 1,
-// W's tile t + 2 is converted into. Codes and scales are loaded two k-tiles at a time, one such
-// pair ahead.
+// releases tile t's stages, which X's tile t + XS is copied into and, during the products of t + 1,
+// W's tile t + 2 is converted into. Codes, scales and zeros come two k-tiles at a time, XS / 2 such
+// pairs ahead, through LDS as well (each wave its own), so that every wait in the loop is for
+// copies whose number the kernel knows: registers loaded that early would be waited for by the
+// compiler, which does not see the copies of X between them.
 #pragma once
 
 #include "gemm_dtl.hpp"
@@ -24,17 +26,20 @@
 
 namespace gek {
 
-template <int BM_, int BN_, int WM_, int WN_>
+// XS: stages of X's ring (of W's there are two).
+template <int BM_, int BN_, int WM_, int WN_, int XS_>
 struct W4Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, XS = XS_;
   static constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN, NW = WAVES_M * WAVES_N, NT = NW * 64;
   static constexpr int MB = WM / 32, NB = WN / 32;
-  static constexpr int X_BYTES = BM * 128, W_BYTES = BN * 128, STAGE = X_BYTES + W_BYTES;
+  static constexpr int X_BYTES = BM * 128, W_BYTES = BN * 128, OFF_W = XS * X_BYTES;
   static constexpr int XI = X_BYTES / 1024 / NW;      // copies of X per wave and k-tile
   static constexpr int RG = BN / 16 / NW;             // row groups that a wave converts
-  static constexpr int OFF_R = 2 * STAGE;             // factors of the sums: [stage][group of the k-tile][BN]
+  static constexpr int CODES = RG * 1024 + 512;       // a pair's codes, scales and zeros of one wave
+  static constexpr int OFF_R = OFF_W + 2 * W_BYTES;   // factors of the sums: [stage][group of the k-tile][BN]
+  static constexpr int OFF_C = OFF_R + 2 * 2 * BN * 4;
   static constexpr int EPI = 8192;                    // epilogue bytes per wave (in the stages)
-  static constexpr int LDS = OFF_R + 2 * 2 * BN * 4;
+  static constexpr int LDS = OFF_C + XS / 2 * NW * CODES;
   static_assert(X_BYTES % (1024 * NW) == 0 && BN % (16 * NW) == 0, "shares of a wave");
   static_assert(NW * EPI <= OFF_R && LDS <= 160 * 1024, "LDS");
 };
@@ -87,27 +92,20 @@ __device__ __forceinline__ i32x4 w4_expand(uint32_t w, float p, float nz) {
   return o;
 }
 
-// Codes, scales and zeros of a pair of k-tiles; GPT groups to a k-tile.
+// Codes, scales (low halves) and zeros (above) of a pair of k-tiles; GPT groups to a k-tile.
 template <int RG, int GPT>
 struct W4Codes {
   i32x4 c[RG];
-  uint16_t s[RG][2 * GPT];
-  uint8_t z[RG][2 * GPT];
-  // The loads are done (the caller has waited): later uses wait for nothing.
-  __device__ __forceinline__ void landed() {
-#pragma unroll
-    for (int r = 0; r < RG; ++r) {
-      asm volatile("" : "+v"(c[r]));
-#pragma unroll
-      for (int g = 0; g < 2 * GPT; ++g) {
-        int a = s[r][g], b = z[r][g];
-        asm volatile("" : "+v"(a), "+v"(b));
-        s[r][g] = (uint16_t)a;
-        z[r][g] = (uint8_t)b;
-      }
-    }
-  }
+  uint32_t sz[RG][2 * GPT];
 };
+
+// 4 bytes per lane, as copy_to_lds_b128.
+__device__ __forceinline__ void copy_to_lds_b32(const i32x4& srd, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :
+               : "v"(voff), "s"(srd), "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "memory", "m0");
+}
 
 // Epilogue: 32 x 32 blocks of sums through fp32 scratch (gated: one of the gate and one of the up
 // projection), so that a lane gets eight neighbouring columns of a token and memory sees whole
@@ -191,7 +189,12 @@ __device__ __forceinline__ void w4_tile_epilogue(const W4Args& p, const f32x16 (
 template <int DT, bool GATED, class C, bool G32, bool XD>
 __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W4Launch L) {
   constexpr int BM = C::BM, BN = C::BN, WM = C::WM, WN = C::WN, MB = C::MB, NB = C::NB, RG = C::RG, XI = C::XI;
-  constexpr int GPT = G32 ? 2 : 1, NCODE = RG * (1 + 4 * GPT), NMMA = MB * NB;
+  constexpr int GPT = G32 ? 2 : 1, NCODE = RG + 2, NMMA = MB * NB;
+  constexpr int XS = XD ? C::XS : 2, D = XS / 2;   // (through registers X is one k-tile ahead)
+  static_assert(XS == 2 || XS == 4, "stages of X");
+  // Copies younger than X's tile t + 1 at the end of k-tile t: those of the XS - 2 k-tiles after it,
+  // of which every other one brings codes, and for an odd t the codes that came with it.
+  constexpr int AHEAD = (XS - 2) * XI + (XS - 2) / 2 * NCODE;
   __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -230,7 +233,7 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
 #pragma unroll
       for (int j = 0; j < XI; ++j) {
         const uint32_t off = tail && k0 + x_chunk[j] * 8 >= p.k ? kOOB : x_src[j];
-        copy_to_lds_b128(srd, off, lds + (t & 1) * C::STAGE + (w * XI + j) * 1024);
+        copy_to_lds_b128(srd, off, lds + (t & (XS - 1)) * C::X_BYTES + (w * XI + j) * 1024);
       }
     } else {
 #pragma unroll
@@ -245,35 +248,51 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
     if constexpr (!XD) {
 #pragma unroll
       for (int j = 0; j < XI; ++j)
-        *reinterpret_cast<i32x4*>(smem + (t & 1) * C::STAGE + (w * XI + j) * 1024 + lane * 16) = xr[j];
+        *reinterpret_cast<i32x4*>(smem + (t & 1) * C::X_BYTES + (w * XI + j) * 1024 + lane * 16) = xr[j];
     }
   };
 
   // ---- W ----
   // Tile row groups of this wave: w RG .. + RG - 1; of a gated tile, pairs of groups alternate
   // between the halves, so that each wave column has 32 rows of both.
-  __amdgpu_buffer_rsrc_t rc[RG], rs[RG], rz[RG];
+  constexpr int E = 2 * GPT;   // scales of a row in a pair
+  const int first = w * RG;
+  const int in0 = n0 / 16 + (GATED ? first / 4 * 2 + first % 2 : first);   // (RG of them follow each other)
+  const int on = max(0, min(RG, p.rgs - in0));
+  const int64_t rg0 = (on > 0 ? in0 : 0) + (GATED && first / 2 % 2 ? (int64_t)p.rgs : 0);
+  const char* cb = p.codes + rg0 * p.kt * kTileBytes;
+  const i32x4 srd_s = make_srd(p.scales + rg0 * p.groups * kRows), srd_z = make_srd(p.zeros + rg0 * p.groups * kRows);
+  // this lane's dword of the scales and of the zeros: row group, entry, place
+  const int s_r = lane / (8 * E), s_e = lane / 8 % E, z_r = lane / (4 * E), z_e = lane / 4 % E;
+  const uint32_t s_off = s_r < on ? (uint32_t)(s_r * p.groups * 32 + lane % 8 * 4) : kOOB;
+  const uint32_t z_off = z_r < on ? (uint32_t)(z_r * p.groups * 16 + lane % 4 * 4) : kOOB;
+  const uint32_t lds_c = lds + C::OFF_C + w * C::CODES;
+  constexpr int SLOT = C::NW * C::CODES;
+  auto copy_w = [&](int pair) {   // k-tiles 2 pair and 2 pair + 1
+    const uint32_t to = lds_c + (D == 1 ? 0 : (pair & (D - 1)) * SLOT);
+    const bool in = pair < p.kt;
 #pragma unroll
-  for (int r = 0; r < RG; ++r) {
-    const int i = w * RG + r;
-    const int in = n0 / 16 + (GATED ? i / 4 * 2 + i % 2 : i);
-    const bool on = in < p.rgs;
-    const int64_t rg = (on ? in : 0) + (GATED && i / 2 % 2 ? (int64_t)p.rgs : 0);
-    rc[r] = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p.codes) + rg * p.kt * kTileBytes, 0, on ? p.kt * kTileBytes : 0, kBufDword3);
-    rs[r] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.scales) + rg * p.groups * kRows, 0, on ? p.groups * kRows * 2 : 0, kBufDword3);
-    rz[r] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.zeros) + rg * p.groups * kRows, 0, on ? p.groups * kRows : 0, kBufDword3);
-  }
+    for (int r = 0; r < RG; ++r)
+      copy_to_lds_b128(make_srd(cb + ((int64_t)r * p.kt + pair) * kTileBytes, in && r < on ? kTileBytes : 0u), lane * 16, to + r * 1024);
+    const auto group = [&](int e) {   // of entry e
+      if (G32) return pair * 4 + e;
+      const int a = (int)((uint32_t)(pair * 128) / (uint32_t)p.group), b = (int)((uint32_t)(pair * 128 + 64) / (uint32_t)p.group);
+      return e ? b : a;
+    };
+    const int gs = group(s_e), gz = group(z_e);
+    copy_to_lds_b32(srd_s, gs < p.groups ? s_off + (s_off == kOOB ? 0u : gs * 32) : kOOB, to + RG * 1024);
+    copy_to_lds_b32(srd_z, gz < p.groups ? z_off + (z_off == kOOB ? 0u : gz * 16) : kOOB, to + RG * 1024 + 256);
+  };
   using Codes = W4Codes<RG, GPT>;
-  auto load_w = [&](Codes& d, int t) {   // k-tiles t and t + 1, t even
+  auto read_w = [&](Codes& d, int pair) {
+    const char* at = smem + C::OFF_C + w * C::CODES + (D == 1 ? 0 : (pair & (D - 1)) * SLOT);
 #pragma unroll
     for (int r = 0; r < RG; ++r) {
-      d.c[r] = __builtin_amdgcn_raw_buffer_load_b128(rc[r], lane * 16, t / 2 * kTileBytes, 0);
+      d.c[r] = *reinterpret_cast<const i32x4*>(at + r * 1024 + lane * 16);
 #pragma unroll
-      for (int g = 0; g < 2 * GPT; ++g) {
-        const int at = G32 ? t * 2 + g : (int)((uint32_t)((t + g) * 64) / (uint32_t)p.group);
-        d.s[r][g] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[r], li * 2, at * 32, 0);
-        d.z[r][g] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rz[r], li, at * 16, 0);
-      }
+      for (int e = 0; e < E; ++e)
+        d.sz[r][e] = *reinterpret_cast<const uint16_t*>(at + RG * 1024 + ((r * E + e) * 16 + li) * 2) |
+                     (uint32_t)*reinterpret_cast<const uint8_t*>(at + RG * 1024 + 256 + (r * E + e) * 16 + li) << 16;
     }
   };
   float f[RG];   // of the group converted last
@@ -281,20 +300,19 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
   for (int r = 0; r < RG; ++r) f[r] = 1.0f;
   // Whether k-tile t begins a group (of 64 or more).
   auto begins = [&](int t) { return G32 || (uint32_t)(t * 64) % (uint32_t)p.group == 0; };
-  // Converts the eight codes i of this wave's 2 RG per k-tile into k-tile t's stage: row group
-  // i / 2, dword 2 (t % 2) + i % 2.
-  auto convert = [&](Codes& d, int t, auto itag) {
-    constexpr int i = decltype(itag)::value, r = i / 2, h = i % 2;
-    const int g = (t & 1) * GPT + (G32 ? h : 0);
+  // Converts dword i of this wave's 2 RG per k-tile into k-tile t's stage (t % 2 == par): row group
+  // i / 2, dword 2 par + i % 2.
+  auto convert = [&](Codes& d, int t, auto ptag, auto itag) {
+    constexpr int par = decltype(ptag)::value, i = decltype(itag)::value, r = i / 2, h = i % 2;
+    constexpr int g = par * GPT + (G32 ? h : 0);
     float pw, fn;
-    w4_split<DT>(g == 0 ? d.s[r][0] : g == 1 ? d.s[r][1] : g == 2 ? d.s[r][2 % (2 * GPT)] : d.s[r][3 % (2 * GPT)], pw, fn);
-    const uint8_t zb = g == 0 ? d.z[r][0] : g == 1 ? d.z[r][1] : g == 2 ? d.z[r][2 % (2 * GPT)] : d.z[r][3 % (2 * GPT)];
+    w4_split<DT>((uint16_t)d.sz[r][g], pw, fn);
     const int row = (w * RG + r) * 16 + li;   // of the tile
-    char* st = smem + (t & 1) * C::STAGE + C::X_BYTES + row * 128;
-    const uint32_t code = (uint32_t)(t & 1 ? d.c[r][2 + h] : d.c[r][h]);
-    *reinterpret_cast<i32x4*>(st + (((4 * h + q) ^ swz_a<128>(row)) << 4)) = w4_expand<DT>(code, pw, -(float)zb * pw);
+    char* st = smem + C::OFF_W + par * C::W_BYTES + row * 128;
+    *reinterpret_cast<i32x4*>(st + (((4 * h + q) ^ swz_a<128>(row)) << 4)) =
+        w4_expand<DT>((uint32_t)d.c[r][2 * par + h], pw, -(float)(d.sz[r][g] >> 16) * pw);
     if ((G32 || h == 0) && begins(t)) {
-      if (q == 0) reinterpret_cast<float*>(smem + C::OFF_R)[((t & 1) * 2 + (G32 ? h : 0)) * BN + row] = f[r] / fn;
+      if (q == 0) reinterpret_cast<float*>(smem + C::OFF_R)[(par * 2 + (G32 ? h : 0)) * BN + row] = f[r] / fn;
       f[r] = fn;
     }
   };
@@ -303,15 +321,15 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
   FragRead<BM, 64, true, WM, MB, 4> fx;
   FragRead<BN, 64, true, WN, NB, 4> fw;
   fx.init(wm, lane, 0);
-  fw.init(wn, lane, C::X_BYTES);
+  fw.init(wn, lane, C::OFF_W);
   f32x16 acc[NB][MB];
 #pragma unroll
   for (int a = 0; a < NB; ++a)
 #pragma unroll
     for (int b = 0; b < MB; ++b) acc[a][b] = f32x16{};
-  // Multiplies the sums by the factors of group g of k-tile t.
-  auto rescale = [&](int t, int g) {
-    const float* R = reinterpret_cast<const float*>(smem + C::OFF_R) + ((t & 1) * 2 + g) * BN + wn * WN + 4 * lhi;
+  // Multiplies the sums by the factors of group g of a k-tile of this parity.
+  auto rescale = [&](int par, int g) {
+    const float* R = reinterpret_cast<const float*>(smem + C::OFF_R) + (par * 2 + g) * BN + wn * WN + 4 * lhi;
 #pragma unroll
     for (int a = 0; a < NB; ++a)
 #pragma unroll
@@ -326,64 +344,72 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
   struct Frag {
     i32x4 x[MB], w[NB];
   };
-  auto read = [&](Frag& fr, int t, int s) {
-    const char* st = smem + (t & 1) * C::STAGE;
+  auto read = [&](Frag& fr, int t, auto ptag, int s) {
+    constexpr int par = decltype(ptag)::value;
 #pragma unroll
-    for (int a = 0; a < NB; ++a) fr.w[a] = fw.read(st, s, a);
+    for (int a = 0; a < NB; ++a) fr.w[a] = fw.read(smem + par * C::W_BYTES, s, a);
 #pragma unroll
-    for (int b = 0; b < MB; ++b) fr.x[b] = fx.read(st, s, b);
+    for (int b = 0; b < MB; ++b) fr.x[b] = fx.read(smem + (XS == 2 ? par : t & (XS - 1)) * C::X_BYTES, s, b);
   };
 
-  Codes now, next;   // codes of the k-tiles being converted, and of the pair after them
-  load_w(now, 0);
-  issue_x(0);
-  store_x(0);
-  issue_x(1);
-  now.landed();
-  w4_for<2 * RG>([&](auto i) { convert(now, 0, i); });
-  w4_for<2 * RG>([&](auto i) { convert(now, 1, i); });
-  load_w(next, 2);
-  w4_wait_vm<XD ? NCODE : 0>();
+  constexpr std::integral_constant<int, 0> p0{};
+  constexpr std::integral_constant<int, 1> p1{};
+  Codes now;   // of the pair being converted
+  copy_w(0);
+#pragma unroll
+  for (int t = 0; t < XS; ++t) {
+    issue_x(t);
+    if (t == 0) store_x(0);
+  }
+  w4_wait_vm<0>();
+  read_w(now, 0);
+  w4_for<2 * RG>([&](auto i) { convert(now, 0, p0, i); });
+  w4_for<2 * RG>([&](auto i) { convert(now, 1, p1, i); });
   wait_lgkmcnt<0>();
   barrier_only();
+#pragma unroll
+  for (int d = 1; d <= D; ++d) copy_w(d);
   Frag fr[2];
-  read(fr[0], 0, 0);
+  read(fr[0], 0, p0, 0);
 
-  // k-tile t, t % 2 == u; `now` holds the codes of k-tiles t + 2 - u .. once landed
+  // k-tile t, t % 2 == u. The first W conversion of the next but one comes with its last step, the
+  // rest with the three steps after.
   auto ktile = [&](auto utag, int t) {
     constexpr int u = decltype(utag)::value;
-    if (!G32 && t > 0 && begins(t)) rescale(t, 0);
+    constexpr std::integral_constant<int, u ^ 1> other{};
+    if (!G32 && t > 0 && begins(t)) rescale(u, 0);
     w4_for<4>([&](auto stag) {
       constexpr int s = decltype(stag)::value;
       constexpr bool last = s == 3;
-      if (G32 && s % 2 == 0 && (t > 0 || s > 0)) rescale(t, s / 2);
+      if (G32 && s % 2 == 0 && (t > 0 || s > 0)) rescale(u, s / 2);
+      if constexpr (u == 1 && s == 0) {   // the pair read at the end of the last k-tile makes room
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        copy_w(t / 2 + 1 + D);
+      }
       if constexpr (last) {
         wait_lgkmcnt<0>();   // reads of k-tile t, writes of W's t + 1
         if constexpr (!XD) {
           store_x(t + 1);
           wait_lgkmcnt<0>();
         }
-        // copies of X's t + 1 have landed; codes loaded after them may still be on their way
-        if constexpr (u == 0) w4_wait_vm<0>();
-        else if constexpr (XD) w4_wait_vm<NCODE>();
+        // X's t + 1 has landed, and for an even t the codes of the next pair
+        if constexpr (XD) w4_wait_vm<AHEAD + u * NCODE>();
+        else w4_wait_vm<u * NCODE>();
+        if constexpr (u == 0 && D > 1) {
+          // (the first copies have no X between them: all but the last D - 1 pairs)
+          if (t == 0) w4_wait_vm<(D - 1) * NCODE>();
+        }
         barrier_only();
-        if constexpr (u == 0) {   // W's t + 2 begins a pair
-          next.landed();
-          now = next;
-        }
-        issue_x(t + 2);
-        if constexpr (u == 0) {
-          load_w(next, t + 4);
-          asm volatile("" ::: "memory");   // (the loads are issued here: the next waits count them)
-        }
-        read(fr[0], t + 1, 0);
-        if (t + 2 < KT2) convert(now, t + 2, std::integral_constant<int, 0>{});
+        issue_x(t + XS);
+        if constexpr (u == 0) read_w(now, t / 2 + 1);   // W's t + 2 begins a pair
+        read(fr[0], t + 1, other, 0);
+        if (t + 2 < KT2) convert(now, t + 2, utag, std::integral_constant<int, 0>{});
       } else {
-        read(fr[(s + 1) & 1], t, s + 1);
-        // the rest of W's t + 1, whose first part came with the last step of k-tile t - 1
+        read(fr[(s + 1) & 1], t, utag, s + 1);
         if (t > 0 && t + 1 < KT2) {
           constexpr int per = (2 * RG - 1 + 2) / 3, i0 = 1 + s * per, i1 = i0 + per < 2 * RG ? i0 + per : 2 * RG;
-          w4_for<(i1 > i0 ? i1 - i0 : 0)>([&](auto i) { convert(now, t + 1, std::integral_constant<int, i0 + decltype(i)::value>{}); });
+          w4_for<(i1 > i0 ? i1 - i0 : 0)>(
+              [&](auto i) { convert(now, t + 1, other, std::integral_constant<int, i0 + decltype(i)::value>{}); });
         }
       }
 #pragma unroll
@@ -392,8 +418,8 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
     });
   };
   for (int t = 0; t < KT2; t += 2) {
-    ktile(std::integral_constant<int, 0>{}, t);
-    ktile(std::integral_constant<int, 1>{}, t + 1);
+    ktile(p0, t);
+    ktile(p1, t + 1);
   }
   wait_vmcnt<0>();
   wait_lgkmcnt<0>();

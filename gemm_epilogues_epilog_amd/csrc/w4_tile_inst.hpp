@@ -16,11 +16,14 @@ const void* w4_tile_fn(bool g32, bool xd) {
 // Tile `cfg` (gew4::W4Tiles) of one type.
 template <int DT>
 const void* w4_tile_pick(int cfg, bool gated, bool g32, bool xd) {
-  using L = W4Tile<256, 256, 128, 64>;
-  using M = W4Tile<128, 128, 64, 64>;
-  using S = W4Tile<64, 128, 32, 64>;
+  using L = W4Tile<256, 256, 128, 64, 2>;
+  using M = W4Tile<128, 128, 32, 64, 4>;
+  using S = W4Tile<64, 128, 32, 64, 4>;
   switch (cfg) {
-    case gew4::W4_L: return gated ? w4_tile_fn<DT, true, L>(g32, xd) : w4_tile_fn<DT, false, L>(g32, xd);
+    case gew4::W4_L:   // (the other variants do not fit its registers, and choose() does not ask for them)
+      if (g32 || !xd) return nullptr;
+      return gated ? reinterpret_cast<const void*>(&w4_tile_kernel<DT, true, L, false, true>)
+                   : reinterpret_cast<const void*>(&w4_tile_kernel<DT, false, L, false, true>);
     case gew4::W4_M: return gated ? w4_tile_fn<DT, true, M>(g32, xd) : w4_tile_fn<DT, false, M>(g32, xd);
     default: return gated ? w4_tile_fn<DT, true, S>(g32, xd) : w4_tile_fn<DT, false, S>(g32, xd);
   }
