@@ -9,8 +9,8 @@
 
 namespace gek {
 
-const void* w4_tile_f16(int cfg, bool gated, bool g32, bool xd);    // w4_tile_f16.hip
-const void* w4_tile_bf16(int cfg, bool gated, bool g32, bool xd);   // w4_tile_bf16.hip
+const void* w4_tile_f16(int cfg, bool gated, int64_t group, bool xd);    // w4_tile_f16.hip
+const void* w4_tile_bf16(int cfg, bool gated, int64_t group, bool xd);   // w4_tile_bf16.hip
 
 namespace {
 
@@ -280,8 +280,8 @@ ge_status_t tiled(W4Args& a, int cfg, ge_dtype_t dt, bool gated, void* stream) {
   L.tiles_m = (int32_t)gew4::ceil_div(a.m, T.bm);
   L.tiles_n = (int32_t)gew4::ceil_div(gated ? 2 * (int64_t)a.n : a.n, T.bn);
   L.group_m = 8;
-  const bool g32 = a.group == 32, xd = a.vecx != 0;
-  const void* fn = dt == GE_F16 ? w4_tile_f16(cfg, gated, g32, xd) : w4_tile_bf16(cfg, gated, g32, xd);
+  const bool xd = a.vecx != 0;
+  const void* fn = dt == GE_F16 ? w4_tile_f16(cfg, gated, a.group, xd) : w4_tile_bf16(cfg, gated, a.group, xd);
   void* params[] = {&a, &L};
   return run(fn, dim3((unsigned)((int64_t)L.tiles_m * L.tiles_n)), T.waves * 64, 0, params, stream);
 }

@@ -29,6 +29,6 @@ struct W4TileCfg {
   int bm, bn, waves;
 };
 enum W4Tiles { W4_L = 0, W4_M, W4_S, W4_COUNT };
-constexpr W4TileCfg kTiles[W4_COUNT] = {{256, 256, 8}, {128, 128, 8}, {64, 128, 4}};
+constexpr W4TileCfg kTiles[W4_COUNT] = {{256, 256, 8}, {128, 128, 8}, {64, 128, 8}};
 
 }  // namespace gew4

@@ -26,11 +26,12 @@
 
 namespace gek {
 
-// XS: stages of X's ring (of W's there are two).
-template <int BM_, int BN_, int WM_, int WN_, int XS_>
+// XS: stages of X's ring (of W's there are two). KG: groups of waves that share the k-steps of every
+// k-tile (their sums are added at the end).
+template <int BM_, int BN_, int WM_, int WN_, int XS_, int KG_>
 struct W4Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, XS = XS_;
-  static constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN, NW = WAVES_M * WAVES_N, NT = NW * 64;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, XS = XS_, KG = KG_;
+  static constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN, NW = WAVES_M * WAVES_N * KG, NT = NW * 64;
   static constexpr int MB = WM / 32, NB = WN / 32;
   static constexpr int X_BYTES = BM * 128, W_BYTES = BN * 128, OFF_W = XS * X_BYTES;
   static constexpr int XI = X_BYTES / 1024 / NW;      // copies of X per wave and k-tile
@@ -41,7 +42,8 @@ struct W4Tile {
   static constexpr int EPI = 8192;                    // epilogue bytes per wave (in the stages)
   static constexpr int LDS = OFF_C + XS / 2 * NW * CODES;
   static_assert(X_BYTES % (1024 * NW) == 0 && BN % (16 * NW) == 0, "shares of a wave");
-  static_assert(NW * EPI <= OFF_R && LDS <= 160 * 1024, "LDS");
+  static_assert(NW / KG * EPI <= OFF_R && LDS <= 160 * 1024, "LDS");
+  static_assert(KG == 1 || (KG == 2 && MB * NB * 4096 <= EPI), "sums of the second group of waves");
 };
 
 template <int N, class F, int I = 0>
@@ -77,26 +79,42 @@ __device__ __forceinline__ void w4_split(uint16_t bits, float& p, float& f) {
   }
 }
 
-// The eight codes of a dword as (q - z) p, nz = -z p.
+// p in a register's high half and z in its low byte. (p is a power of two, 0, or not finite: fp32
+// with a 16-bit pattern.)
+__device__ __forceinline__ uint32_t w4_pz(float p, uint32_t z) { return (__float_as_uint(p) & 0xffff0000u) | z; }
+
+// The eight codes of a dword as (q - z) p, exact in 16 bits.
 template <int DT>
-__device__ __forceinline__ i32x4 w4_expand(uint32_t w, float p, float nz) {
+__device__ __forceinline__ i32x4 w4_expand(uint32_t w, uint32_t pz) {
   const uint32_t h[2] = {w & 0x0f0f0f0fu, (w >> 4) & 0x0f0f0f0fu};
+  const float p = __uint_as_float(pz & 0xffff0000u), nz = -(float)(pz & 0xffu) * p;
   i32x4 o;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(h[i], 512.0f, false);
-    const auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(h[i], 512.0f, true);
-    o[2 * i] = (int)Tr<DT>::pack2(__builtin_fmaf(a[0], p, nz), __builtin_fmaf(a[1], p, nz));
-    o[2 * i + 1] = (int)Tr<DT>::pack2(__builtin_fmaf(b[0], p, nz), __builtin_fmaf(b[1], p, nz));
+    if constexpr (DT == F16) {
+      typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+      const f16x2_t pp = {(_Float16)p, (_Float16)p}, zz = {(_Float16)nz, (_Float16)nz};
+      const f16x2_t a = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(h[i], 512.0f, false));
+      const f16x2_t b = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(h[i], 512.0f, true));
+      o[2 * i] = __builtin_bit_cast(int, __builtin_elementwise_fma(a, pp, zz));
+      o[2 * i + 1] = __builtin_bit_cast(int, __builtin_elementwise_fma(b, pp, zz));
+    } else {
+      const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(h[i], 512.0f, false);
+      const auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(h[i], 512.0f, true);
+      o[2 * i] = (int)Tr<DT>::pack2(__builtin_fmaf(a[0], p, nz), __builtin_fmaf(a[1], p, nz));
+      o[2 * i + 1] = (int)Tr<DT>::pack2(__builtin_fmaf(b[0], p, nz), __builtin_fmaf(b[1], p, nz));
+    }
   }
   return o;
 }
 
-// Codes, scales (low halves) and zeros (above) of a pair of k-tiles; GPT groups to a k-tile.
-template <int RG, int GPT>
+// A pair of k-tiles of RG row groups, E groups of k to a row in it: codes, and of each group p and z
+// and the factor that brings the sums into its units.
+template <int RG, int E>
 struct W4Codes {
   i32x4 c[RG];
-  uint32_t sz[RG][2 * GPT];
+  uint32_t pz[RG][E];
+  float ratio[RG][E];
 };
 
 // 4 bytes per lane, as copy_to_lds_b128.
@@ -184,12 +202,12 @@ __device__ __forceinline__ void w4_tile_epilogue(const W4Args& p, const f32x16 (
   }
 }
 
-// G32: groups of 32 (two to a k-tile). XD: X's rows are whole 16-byte chunks, copied straight into
+// E: groups of a row in a pair of k-tiles: 4 (of 32), 2 (of 64), 1 (of 128 and more). XD: X's rows are whole 16-byte chunks, copied straight into
 // LDS; otherwise they go through registers.
-template <int DT, bool GATED, class C, bool G32, bool XD>
+template <int DT, bool GATED, class C, int E, bool XD>
 __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W4Launch L) {
   constexpr int BM = C::BM, BN = C::BN, WM = C::WM, WN = C::WN, MB = C::MB, NB = C::NB, RG = C::RG, XI = C::XI;
-  constexpr int GPT = G32 ? 2 : 1, NCODE = RG + 2, NMMA = MB * NB;
+  constexpr int NCODE = RG + 2, NMMA = MB * NB, KG = C::KG, NS = 4 / KG;   // (NS: a wave's k-steps of a tile)
   constexpr int XS = XD ? C::XS : 2, D = XS / 2;   // (through registers X is one k-tile ahead)
   static_assert(XS == 2 || XS == 4, "stages of X");
   // Copies younger than X's tile t + 1 at the end of k-tile t: those of the XS - 2 k-tiles after it,
@@ -198,8 +216,9 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
   __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = w % C::WAVES_M, wn = w / C::WAVES_M;
-  const int li = lane & 15, q = lane >> 4, lrow = lane & 31, lhi = lane >> 5;
+  const int kg = KG == 1 ? 0 : w / (C::NW / KG), wt = KG == 1 ? w : w % (C::NW / KG);
+  const int wm = wt % C::WAVES_M, wn = wt / C::WAVES_M;
+  const int li = lane & 15, q = lane >> 4, lhi = lane >> 5;
   int tm, tn;
   {
     Args r;
@@ -255,7 +274,6 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
   // ---- W ----
   // Tile row groups of this wave: w RG .. + RG - 1; of a gated tile, pairs of groups alternate
   // between the halves, so that each wave column has 32 rows of both.
-  constexpr int E = 2 * GPT;   // scales of a row in a pair
   const int first = w * RG;
   const int in0 = n0 / 16 + (GATED ? first / 4 * 2 + first % 2 : first);   // (RG of them follow each other)
   const int on = max(0, min(RG, p.rgs - in0));
@@ -268,60 +286,71 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
   const uint32_t z_off = z_r < on ? (uint32_t)(z_r * p.groups * 16 + lane % 4 * 4) : kOOB;
   const uint32_t lds_c = lds + C::OFF_C + w * C::CODES;
   constexpr int SLOT = C::NW * C::CODES;
-  auto copy_w = [&](int pair) {   // k-tiles 2 pair and 2 pair + 1
+  // pairs to a group (E 1); the group of the pair copied next and its pairs copied; pairs read of theirs
+  const int span = E == 1 ? p.group / 128 : 1;
+  int next_group = 0, copied = 0, begun = 0;
+  auto copy_w = [&](int pair) {   // k-tiles 2 pair and 2 pair + 1, in order
     const uint32_t to = lds_c + (D == 1 ? 0 : (pair & (D - 1)) * SLOT);
     const bool in = pair < p.kt;
 #pragma unroll
     for (int r = 0; r < RG; ++r)
       copy_to_lds_b128(make_srd(cb + ((int64_t)r * p.kt + pair) * kTileBytes, in && r < on ? kTileBytes : 0u), lane * 16, to + r * 1024);
-    const auto group = [&](int e) {   // of entry e
-      if (G32) return pair * 4 + e;
-      const int a = (int)((uint32_t)(pair * 128) / (uint32_t)p.group), b = (int)((uint32_t)(pair * 128 + 64) / (uint32_t)p.group);
-      return e ? b : a;
-    };
-    const int gs = group(s_e), gz = group(z_e);
+    // group of this lane's dwords (E 1: the pairs of a group follow each other)
+    const int gs = E == 1 ? next_group : pair * E + s_e, gz = E == 1 ? next_group : pair * E + z_e;
     copy_to_lds_b32(srd_s, gs < p.groups ? s_off + (s_off == kOOB ? 0u : gs * 32) : kOOB, to + RG * 1024);
     copy_to_lds_b32(srd_z, gz < p.groups ? z_off + (z_off == kOOB ? 0u : gz * 16) : kOOB, to + RG * 1024 + 256);
+    if (E == 1 && ++copied == span) {
+      copied = 0;
+      ++next_group;
+    }
   };
-  using Codes = W4Codes<RG, GPT>;
+  using Codes = W4Codes<RG, E>;
+  float f[RG];   // of the group read last
+#pragma unroll
+  for (int r = 0; r < RG; ++r) f[r] = 1.0f;
   auto read_w = [&](Codes& d, int pair) {
     const char* at = smem + C::OFF_C + w * C::CODES + (D == 1 ? 0 : (pair & (D - 1)) * SLOT);
+    // past the last pair, and inside a group of several, the units stay as they are
+    bool in = 2 * pair < KT2;
+    if (E == 1) {
+      in = in && begun == 0;
+      if (++begun == span) begun = 0;
+    }
 #pragma unroll
     for (int r = 0; r < RG; ++r) {
       d.c[r] = *reinterpret_cast<const i32x4*>(at + r * 1024 + lane * 16);
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        d.sz[r][e] = *reinterpret_cast<const uint16_t*>(at + RG * 1024 + ((r * E + e) * 16 + li) * 2) |
-                     (uint32_t)*reinterpret_cast<const uint8_t*>(at + RG * 1024 + 256 + (r * E + e) * 16 + li) << 16;
+      for (int e = 0; e < E; ++e) {
+        float p, fn;
+        w4_split<DT>(*reinterpret_cast<const uint16_t*>(at + RG * 1024 + ((r * E + e) * 16 + li) * 2), p, fn);
+        d.pz[r][e] = w4_pz(p, *reinterpret_cast<const uint8_t*>(at + RG * 1024 + 256 + (r * E + e) * 16 + li));
+        d.ratio[r][e] = in ? f[r] * __builtin_amdgcn_rcpf(fn) : 1.0f;
+        f[r] = in ? fn : f[r];
+      }
     }
   };
-  float f[RG];   // of the group converted last
-#pragma unroll
-  for (int r = 0; r < RG; ++r) f[r] = 1.0f;
-  // Whether k-tile t begins a group (of 64 or more).
-  auto begins = [&](int t) { return G32 || (uint32_t)(t * 64) % (uint32_t)p.group == 0; };
-  // Converts dword i of this wave's 2 RG per k-tile into k-tile t's stage (t % 2 == par): row group
-  // i / 2, dword 2 par + i % 2.
-  auto convert = [&](Codes& d, int t, auto ptag, auto itag) {
+  // Converts dword i of this wave's 2 RG per k-tile into the stage of a k-tile of parity par: row
+  // group i / 2, dword 2 par + i % 2. No branches, so that it runs among the products. (The four
+  // lanes of a row write the same factor.)
+  auto convert = [&](const Codes& d, auto ptag, auto itag) {
     constexpr int par = decltype(ptag)::value, i = decltype(itag)::value, r = i / 2, h = i % 2;
-    constexpr int g = par * GPT + (G32 ? h : 0);
-    float pw, fn;
-    w4_split<DT>((uint16_t)d.sz[r][g], pw, fn);
+    constexpr int g = E == 4 ? 2 * par + h : E == 2 ? par : 0;
     const int row = (w * RG + r) * 16 + li;   // of the tile
     char* st = smem + C::OFF_W + par * C::W_BYTES + row * 128;
-    *reinterpret_cast<i32x4*>(st + (((4 * h + q) ^ swz_a<128>(row)) << 4)) =
-        w4_expand<DT>((uint32_t)d.c[r][2 * par + h], pw, -(float)(d.sz[r][g] >> 16) * pw);
-    if ((G32 || h == 0) && begins(t)) {
-      if (q == 0) reinterpret_cast<float*>(smem + C::OFF_R)[(par * 2 + (G32 ? h : 0)) * BN + row] = f[r] / fn;
-      f[r] = fn;
-    }
+    *reinterpret_cast<i32x4*>(st + (((4 * h + q) ^ swz_a<128>(row)) << 4)) = w4_expand<DT>((uint32_t)d.c[r][2 * par + h], d.pz[r][g]);
+    if constexpr (E == 4 || (h == 0 && (E == 2 || par == 0)))
+      reinterpret_cast<float*>(smem + C::OFF_R)[(par * 2 + (E == 4 ? h : 0)) * BN + row] = d.ratio[r][g];
   };
 
   // ---- fragments ----
-  FragRead<BM, 64, true, WM, MB, 4> fx;
-  FragRead<BN, 64, true, WN, NB, 4> fw;
-  fx.init(wm, lane, 0);
-  fw.init(wn, lane, C::OFF_W);
+  // (k-step s of a wave is step s of the tile, or with two groups of waves step 2 s + kg)
+  int rd_x[NS], rd_w[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    const int row = lane & 31, chunk = ((KG * s + kg) * 2 + lhi) ^ swz_a<128>(row);
+    rd_x[s] = (wm * WM + row) * 128 + (chunk << 4);
+    rd_w[s] = C::OFF_W + (wn * WN + row) * 128 + (chunk << 4);
+  }
   f32x16 acc[NB][MB];
 #pragma unroll
   for (int a = 0; a < NB; ++a)
@@ -331,7 +360,7 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
   auto rescale = [&](int par, int g) {
     const float* R = reinterpret_cast<const float*>(smem + C::OFF_R) + (par * 2 + g) * BN + wn * WN + 4 * lhi;
 #pragma unroll
-    for (int a = 0; a < NB; ++a)
+    for (int a = 0; a < NB; ++a) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const f32x4 v = *reinterpret_cast<const f32x4*>(R + 32 * a + 8 * c);
@@ -340,6 +369,7 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[a][b][4 * c + e] *= v[e];
       }
+    }
   };
   struct Frag {
     i32x4 x[MB], w[NB];
@@ -347,9 +377,11 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
   auto read = [&](Frag& fr, int t, auto ptag, int s) {
     constexpr int par = decltype(ptag)::value;
 #pragma unroll
-    for (int a = 0; a < NB; ++a) fr.w[a] = fw.read(smem + par * C::W_BYTES, s, a);
+    for (int a = 0; a < NB; ++a)
+      fr.w[a] = *reinterpret_cast<const i32x4*>(smem + par * C::W_BYTES + rd_w[s] + a * 32 * 128);
+    const char* x = smem + (XS == 2 ? par : t & (XS - 1)) * C::X_BYTES;
 #pragma unroll
-    for (int b = 0; b < MB; ++b) fr.x[b] = fx.read(smem + (XS == 2 ? par : t & (XS - 1)) * C::X_BYTES, s, b);
+    for (int b = 0; b < MB; ++b) fr.x[b] = *reinterpret_cast<const i32x4*>(x + rd_x[s] + b * 32 * 128);
   };
 
   constexpr std::integral_constant<int, 0> p0{};
@@ -363,8 +395,8 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
   }
   w4_wait_vm<0>();
   read_w(now, 0);
-  w4_for<2 * RG>([&](auto i) { convert(now, 0, p0, i); });
-  w4_for<2 * RG>([&](auto i) { convert(now, 1, p1, i); });
+  w4_for<2 * RG>([&](auto i) { convert(now, p0, i); });
+  w4_for<2 * RG>([&](auto i) { convert(now, p1, i); });
   wait_lgkmcnt<0>();
   barrier_only();
 #pragma unroll
@@ -372,49 +404,68 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
   Frag fr[2];
   read(fr[0], 0, p0, 0);
 
-  // k-tile t, t % 2 == u. The first W conversion of the next but one comes with its last step, the
-  // rest with the three steps after.
+  // One k-step of k-tile t, t % 2 == u: reads of the next step's fragments, a part of the next
+  // k-tile's (in the last step, of the next but one's) conversion, and with SCALE the factors of
+  // group g, all among the products.
+  auto step = [&](auto utag, auto stag, auto scale_tag, int g, int t) {
+    constexpr int u = decltype(utag)::value, s = decltype(stag)::value;
+    constexpr bool last = s == NS - 1, SCALE = decltype(scale_tag)::value;
+    constexpr std::integral_constant<int, u ^ 1> other{};
+    if constexpr (SCALE) rescale(u, g);
+    if constexpr (u == 1 && s == 0) {   // the pair read at the end of the last k-tile makes room
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      copy_w(t / 2 + 1 + D);
+    }
+    constexpr int per = last ? 1 : (2 * RG - 1 + NS - 2) / (NS - 1);
+    if constexpr (last) {
+      wait_lgkmcnt<0>();   // reads of k-tile t, writes of W's t + 1
+      if constexpr (!XD) {
+        store_x(t + 1);
+        wait_lgkmcnt<0>();
+      }
+      // X's t + 1 has landed, and for an even t the codes of the next pair
+      if constexpr (XD) w4_wait_vm<AHEAD + u * NCODE>();
+      else w4_wait_vm<u * NCODE>();
+      if constexpr (u == 0 && D > 1) {
+        // (the first copies have no X between them: all but the last D - 1 pairs)
+        if (t == 0) w4_wait_vm<(D - 1) * NCODE>();
+      }
+      barrier_only();
+      issue_x(t + XS);
+      read(fr[0], t + 1, other, 0);
+      if constexpr (u == 0) read_w(now, t / 2 + 1);   // W's t + 2 begins a pair
+      convert(now, utag, std::integral_constant<int, 0>{});
+    } else {
+      read(fr[(s + 1) & 1], t, utag, s + 1);
+      constexpr int i0 = 1 + s * per, i1 = i0 + per < 2 * RG ? i0 + per : 2 * RG;
+      w4_for<(i1 > i0 ? i1 - i0 : 0)>([&](auto i) { convert(now, other, std::integral_constant<int, i0 + decltype(i)::value>{}); });
+    }
+#pragma unroll
+    for (int i = 0; i < NMMA; ++i)
+      acc[i / MB][i % MB] = Tr<DT>::mma(fr[s & 1].w[i / MB], fr[s & 1].x[i % MB], acc[i / MB][i % MB]);
+    // one product, then a read and a share of the rest (256 x 256: 120 -> 115 us at 3000 x 4096 x
+    // 4096; with the two products a step of the small tiles it costs 2 to 10%)
+    if constexpr (NMMA >= 8) {
+      w4_for<NMMA>([&](auto) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, (MB + NB + NMMA - 1) / NMMA, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, (per * 24 + NMMA - 1) / NMMA, 0);
+      });
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
   auto ktile = [&](auto utag, int t) {
     constexpr int u = decltype(utag)::value;
-    constexpr std::integral_constant<int, u ^ 1> other{};
-    if (!G32 && t > 0 && begins(t)) rescale(u, 0);
-    w4_for<4>([&](auto stag) {
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    w4_for<NS>([&](auto stag) {
       constexpr int s = decltype(stag)::value;
-      constexpr bool last = s == 3;
-      if (G32 && s % 2 == 0 && (t > 0 || s > 0)) rescale(u, s / 2);
-      if constexpr (u == 1 && s == 0) {   // the pair read at the end of the last k-tile makes room
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        copy_w(t / 2 + 1 + D);
-      }
-      if constexpr (last) {
-        wait_lgkmcnt<0>();   // reads of k-tile t, writes of W's t + 1
-        if constexpr (!XD) {
-          store_x(t + 1);
-          wait_lgkmcnt<0>();
-        }
-        // X's t + 1 has landed, and for an even t the codes of the next pair
-        if constexpr (XD) w4_wait_vm<AHEAD + u * NCODE>();
-        else w4_wait_vm<u * NCODE>();
-        if constexpr (u == 0 && D > 1) {
-          // (the first copies have no X between them: all but the last D - 1 pairs)
-          if (t == 0) w4_wait_vm<(D - 1) * NCODE>();
-        }
-        barrier_only();
-        issue_x(t + XS);
-        if constexpr (u == 0) read_w(now, t / 2 + 1);   // W's t + 2 begins a pair
-        read(fr[0], t + 1, other, 0);
-        if (t + 2 < KT2) convert(now, t + 2, utag, std::integral_constant<int, 0>{});
-      } else {
-        read(fr[(s + 1) & 1], t, utag, s + 1);
-        if (t > 0 && t + 1 < KT2) {
-          constexpr int per = (2 * RG - 1 + 2) / 3, i0 = 1 + s * per, i1 = i0 + per < 2 * RG ? i0 + per : 2 * RG;
-          w4_for<(i1 > i0 ? i1 - i0 : 0)>(
-              [&](auto i) { convert(now, t + 1, other, std::integral_constant<int, i0 + decltype(i)::value>{}); });
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NMMA; ++i) acc[i / MB][i % MB] = Tr<DT>::mma(fr[s & 1].w[i / MB], fr[s & 1].x[i % MB], acc[i / MB][i % MB]);
-      __builtin_amdgcn_sched_barrier(0);
+      // a group's factors, before its first products: with groups of 32, of which each has two steps of
+      // the tile, with 64 every tile, else every other one (1 where no group begins: a branch around
+      // the multiplications would keep them from running among the products)
+      if constexpr (E == 4 && (KG == 2 || s % 2 == 0)) step(utag, stag, yes, KG == 2 ? s : s / 2, t);
+      else if constexpr (s == 0 && (E == 2 || (E == 1 && u == 0))) step(utag, stag, yes, 0, t);
+      else step(utag, stag, no, 0, t);
     });
   };
   for (int t = 0; t < KT2; t += 2) {
@@ -429,7 +480,30 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
     if (q == 0) reinterpret_cast<float*>(smem + C::OFF_R)[(w * RG + r) * 16 + li] = f[r];
   __syncthreads();
   rescale(0, 0);
-  w4_tile_epilogue<DT, GATED, C>(p, acc, m0 + wm * WM, n0 + wn * (GATED ? WN / 2 : WN), lane, smem + w * C::EPI);
+  if constexpr (KG == 2) {
+    f32x4* sums = reinterpret_cast<f32x4*>(smem + wt * C::EPI) + lane;
+    if (kg == 1) {
+#pragma unroll
+      for (int i = 0; i < NMMA; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const f32x16& v = acc[i / MB][i % MB];
+          sums[(i * 4 + c) * 64] = f32x4{v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]};
+        }
+    }
+    __syncthreads();
+    if (kg == 1) return;
+#pragma unroll
+    for (int i = 0; i < NMMA; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const f32x4 v = sums[(i * 4 + c) * 64];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i / MB][i % MB][4 * c + e] += v[e];
+      }
+    __builtin_amdgcn_wave_barrier();
+  }
+  w4_tile_epilogue<DT, GATED, C>(p, acc, m0 + wm * WM, n0 + wn * (GATED ? WN / 2 : WN), lane, smem + wt * C::EPI);
 }
 
 }  // namespace gek

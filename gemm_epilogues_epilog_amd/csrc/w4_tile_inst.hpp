@@ -5,27 +5,34 @@
 
 namespace gek {
 
+template <int DT, bool GATED, class C, int E>
+const void* w4_tile_fn(bool xd) {
+  return xd ? reinterpret_cast<const void*>(&w4_tile_kernel<DT, GATED, C, E, true>)
+            : reinterpret_cast<const void*>(&w4_tile_kernel<DT, GATED, C, E, false>);
+}
 template <int DT, bool GATED, class C>
-const void* w4_tile_fn(bool g32, bool xd) {
-  if (g32) return xd ? reinterpret_cast<const void*>(&w4_tile_kernel<DT, GATED, C, true, true>)
-                     : reinterpret_cast<const void*>(&w4_tile_kernel<DT, GATED, C, true, false>);
-  return xd ? reinterpret_cast<const void*>(&w4_tile_kernel<DT, GATED, C, false, true>)
-            : reinterpret_cast<const void*>(&w4_tile_kernel<DT, GATED, C, false, false>);
+const void* w4_tile_fn(int e, bool xd) {
+  return e == 4 ? w4_tile_fn<DT, GATED, C, 4>(xd) : e == 2 ? w4_tile_fn<DT, GATED, C, 2>(xd) : w4_tile_fn<DT, GATED, C, 1>(xd);
+}
+// The large tile: the other variants do not fit its registers, and choose() does not ask for them.
+template <int DT, bool GATED, class C>
+const void* w4_tile_large(int e, bool xd) {
+  if (e == 4 || !xd) return nullptr;
+  return e == 2 ? reinterpret_cast<const void*>(&w4_tile_kernel<DT, GATED, C, 2, true>)
+                : reinterpret_cast<const void*>(&w4_tile_kernel<DT, GATED, C, 1, true>);
 }
 
 // Tile `cfg` (gew4::W4Tiles) of one type.
 template <int DT>
-const void* w4_tile_pick(int cfg, bool gated, bool g32, bool xd) {
-  using L = W4Tile<256, 256, 128, 64, 2>;
-  using M = W4Tile<128, 128, 32, 64, 4>;
-  using S = W4Tile<64, 128, 32, 64, 4>;
+const void* w4_tile_pick(int cfg, bool gated, int64_t group, bool xd) {
+  using L = W4Tile<256, 256, 128, 64, 2, 1>;
+  using M = W4Tile<128, 128, 32, 64, 4, 1>;
+  using S = W4Tile<64, 128, 32, 64, 4, 2>;
+  const int e = group == 32 ? 4 : group == 64 ? 2 : 1;
   switch (cfg) {
-    case gew4::W4_L:   // (the other variants do not fit its registers, and choose() does not ask for them)
-      if (g32 || !xd) return nullptr;
-      return gated ? reinterpret_cast<const void*>(&w4_tile_kernel<DT, true, L, false, true>)
-                   : reinterpret_cast<const void*>(&w4_tile_kernel<DT, false, L, false, true>);
-    case gew4::W4_M: return gated ? w4_tile_fn<DT, true, M>(g32, xd) : w4_tile_fn<DT, false, M>(g32, xd);
-    default: return gated ? w4_tile_fn<DT, true, S>(g32, xd) : w4_tile_fn<DT, false, S>(g32, xd);
+    case gew4::W4_L: return gated ? w4_tile_large<DT, true, L>(e, xd) : w4_tile_large<DT, false, L>(e, xd);
+    case gew4::W4_M: return gated ? w4_tile_fn<DT, true, M>(e, xd) : w4_tile_fn<DT, false, M>(e, xd);
+    default: return gated ? w4_tile_fn<DT, true, S>(e, xd) : w4_tile_fn<DT, false, S>(e, xd);
   }
 }
 
