@@ -23,7 +23,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["api.hip", "inst_f32.hip", "inst_f16.hip", "inst_bf16.hip",
            "inst_f16_lay1.hip", "inst_f16_lay2.hip", "inst_f16_lay3.hip",
            "inst_bf16_lay1.hip", "inst_bf16_lay2.hip", "inst_bf16_lay3.hip",
-           "mx.hip", "mx_quant.hip", "norm.hip", "gated.hip", "gated_tiles.hip", "w4.hip", "w4_tile_f16.hip", "w4_tile_bf16.hip"]
+           "mx.hip", "mx_quant.hip", "norm.hip", "gated.hip", "gated_tiles.hip", "gated_skinny.hip", "w4.hip", "w4_tile_f16.hip", "w4_tile_bf16.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -104,15 +104,15 @@ __global__ __launch_bounds__(256) void colsum_kernel(const void* x, int64_t m, i
 
 template <int DT, int OUT, int LAY>
 const void* gen_of(bool large) {
-  return large ? reinterpret_cast<const void*>(&gen_kernel<DT, OUT, LAY, 128, 128, 64>)
-               : reinterpret_cast<const void*>(&gen_kernel<DT, OUT, LAY, 64, 64, 32>);
+  return large ? reinterpret_cast<const void*>(&gen_kernel<DT, OUT, LAY, 128, 128, 64, 1>)
+               : reinterpret_cast<const void*>(&gen_kernel<DT, OUT, LAY, 64, 64, 32, 2>);
 }
 template <int DT>
 const void* gen_kernel_of(int lay, bool f32_out, bool large) {
   switch (lay) {
     case 0: return f32_out ? gen_of<DT, F32, 0>(large) : gen_of<DT, DT, 0>(large);
-    case 1: return gen_of<DT, DT, 1>(large);
-    case 2: return gen_of<DT, DT, 2>(large);
+    case 1: return f32_out ? gen_of<DT, F32, 1>(large) : gen_of<DT, DT, 1>(large);
+    case 2: return f32_out ? gen_of<DT, F32, 2>(large) : gen_of<DT, DT, 2>(large);
     default: return gen_of<DT, DT, 6>(large);
   }
 }
@@ -121,9 +121,10 @@ hipError_t launch(const void* fn, dim3 grid, int threads, void** params, hipStre
   return hipLaunchKernel(fn, grid, dim3(threads), params, 0, s);
 }
 
-// The general kernel. lay 6: gated, N columns of D from 2 N rows of B.
+// The general kernel. lay 6: gated, N columns of D from 2 N rows of B. splits: workgroups that share
+// a tile's k loop, D then that many matrices of sums.
 hipError_t general(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, const void* A, const void* B, void* D,
-                   bool f32_out, const void* bias, int vec, int act, void* Z, int cus, hipStream_t s) {
+                   bool f32_out, int splits, const void* bias, int vec, int act, void* Z, int cus, hipStream_t s) {
   GenArgs a;
   a.A = A;
   a.B = B;
@@ -140,7 +141,7 @@ hipError_t general(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, cons
   a.act = act;
   // the large tile where it gives every compute unit one
   const auto tiles = [&](int t) { return (M + t - 1) / t * ((N + (lay == 6 ? t / 2 : t) - 1) / (lay == 6 ? t / 2 : t)); };
-  const bool large = tiles(128) >= cus;
+  const bool large = gegh::general_large(M, lay == 6 ? 2 * N : N, cus);
   const int t = large ? 128 : 64;
   a.tiles_m = (int)((M + t - 1) / t);
   a.tiles_n = (int)(tiles(t) / a.tiles_m);
@@ -148,7 +149,7 @@ hipError_t general(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, cons
                    : dt == GE_F16 ? gen_kernel_of<F16>(lay, f32_out, large)
                                   : gen_kernel_of<BF16>(lay, f32_out, large);
   void* params[] = {&a};
-  return launch(fn, dim3((unsigned)tiles(t)), large ? 256 : 128, params, s);
+  return launch(fn, dim3((unsigned)tiles(t), (unsigned)splits), 256, params, s);
 }
 
 // D (M, N) of type dt = A . B; `ws` for the k loop's split.
@@ -157,10 +158,14 @@ ge_status_t product(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, con
   if (K > 0 && gegh::fast_shape(M, N, K, dt, lay) && gegh::aligned(A, 16) && gegh::aligned(B, 16) &&
       gegh::aligned(D, 16)) {
     geh::Layout L;
-    if (ge_status_t st = gegh::fast_layout(M, N, K, dt, lay, cus, ws_bytes, &L); st != GE_OK) return st;
+    if (ge_status_t st = gegh::fast_layout(M, N, K, dt, lay, cus, lay ? 0 : ws_bytes, &L); st != GE_OK) return st;
     return gei::run_product(M, (int)N, (int)K, dt, L, A, B, D, ws, s);
   }
-  return general(M, N, K, dt, lay, A, B, D, false, nullptr, F32, 0, nullptr, cus, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
+  const int splits = gegh::general_splits(M, N, K, dt, ws_bytes);
+  if (splits == 1)
+    return general(M, N, K, dt, lay, A, B, D, false, 1, nullptr, F32, 0, nullptr, cus, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
+  if (general(M, N, K, dt, lay, A, B, ws, true, splits, nullptr, F32, 0, nullptr, cus, s) != hipSuccess) return GE_ERR_HIP;
+  return launch_bgrad_reduce(reinterpret_cast<float*>(ws), splits, M * N, D, (int)dt, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
 }
 
 // The tile kernels with the gated epilogues: H (and Z) of X and W, or dZ of dY, Wd and Z.
@@ -219,10 +224,14 @@ ge_status_t gemm_epilog_gated_forward(int64_t m, int64_t n, int64_t k, ge_dtype_
   int cus = 0;
   if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  if (gegh::skinny(m, 2 * n, k, dt, true, cus))
+    return gek::launch_skinny(m, n, k, (int)dt, true, (int)act, x, w, bias, (int)vec, h, z, cus, s) == hipSuccess
+               ? GE_OK
+               : GE_ERR_HIP;
   if (gegh::fast_shape(m, n, k, dt, 2) && gegh::aligned(x, 16) && gegh::aligned(w, 16) && gegh::aligned(h, 16) &&
       gegh::aligned(z, 16))
     return gek::gated_tiles(m, n, k, dt, false, (int)act, x, w, bias, (int)vec, nullptr, h, z, cus, s);
-  return gek::general(m, n, k, dt, 6, x, w, h, false, bias, (int)vec, (int)act, z, cus, s) == hipSuccess ? GE_OK
+  return gek::general(m, n, k, dt, 6, x, w, h, false, 1, bias, (int)vec, (int)act, z, cus, s) == hipSuccess ? GE_OK
                                                                                                       : GE_ERR_HIP;
 }
 
@@ -232,6 +241,11 @@ ge_status_t gemm_epilog_gated_down(int64_t m, int64_t d, int64_t n, ge_dtype_t d
   if (m == 0) return GE_OK;
   int cus = 0;
   if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
+  if (gegh::skinny(m, d, n, dt, false, cus))
+    return gek::launch_skinny(m, d, n, (int)dt, false, 0, h, w_down, nullptr, 0, y, nullptr, cus,
+                              static_cast<hipStream_t>(stream)) == hipSuccess
+               ? GE_OK
+               : GE_ERR_HIP;
   return gek::product(m, d, n, dt, 2, h, w_down, y, nullptr, 0, cus, static_cast<hipStream_t>(stream));
 }
 
@@ -267,7 +281,7 @@ ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t 
     } else if (w_down) {
       dh = ws + at.dh;
       f32 = true;
-      if (gek::general(m, n, d, dt, 0, dy, w_down, ws + at.dh, true, nullptr, 0, 0, nullptr, cus, s) != hipSuccess)
+      if (gek::general(m, n, d, dt, 0, dy, w_down, ws + at.dh, true, 1, nullptr, 0, 0, nullptr, cus, s) != hipSuccess)
         return GE_ERR_HIP;
     }
     const void* fn = dt == GE_F32   ? gek::dz_of<gek::F32>(f32)
@@ -282,9 +296,9 @@ ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t 
         return st;
   }
   if (dw)
-    if (ge_status_t st = gek::product(2 * n, k, m, dt, 1, dz, x, dw, nullptr, 0, cus, s); st != GE_OK) return st;
+    if (ge_status_t st = gek::product(2 * n, k, m, dt, 1, dz, x, dw, scratch, scratch_bytes, cus, s); st != GE_OK) return st;
   if (dw_down)
-    if (ge_status_t st = gek::product(d, n, m, dt, 1, dy, h, dw_down, nullptr, 0, cus, s); st != GE_OK) return st;
+    if (ge_status_t st = gek::product(d, n, m, dt, 1, dy, h, dw_down, scratch, scratch_bytes, cus, s); st != GE_OK) return st;
   if (dbias)
     if (ge_status_t st =
             gek::column_sums(dz, m, 2 * n, dt, dbias, vec, reinterpret_cast<float*>(scratch), s);

@@ -77,8 +77,8 @@ template <int ES, int MN, bool KMAJ, int NT, int HW = 0>
 struct GenOperand {
   static constexpr int E = 16 / ES, BK = kRowBytes / ES;
   static constexpr int LD = MN * 8 / NT;   // k-major: 16-byte chunks per thread
-  static constexpr int R = 4, NB = MN / E;   // mn-major: one block of R k-rows by E columns per thread
-  static_assert(KMAJ ? MN * 8 % NT == 0 : NB * (BK / R) == NT, "tile split");
+  static constexpr int NB = MN / E, R = NB * BK / NT;   // mn-major: one block of R k-rows by E columns per thread
+  static_assert(KMAJ ? MN * 8 % NT == 0 : (R == 2 || R == 4) && NB * (BK / R) == NT, "tile split");
   static constexpr int REGS = KMAJ ? LD : R;
   i32x4 reg[REGS];
 
@@ -133,12 +133,16 @@ struct GenOperand {
         const int row = t % NB * E + c;
         char* dst = lds + row * kRowBytes + ((chunk ^ swz(row)) << 4) + within;
         if constexpr (ES == 4) {
-          *reinterpret_cast<i32x4*>(dst) = i32x4{reg[0][c], reg[1][c], reg[2][c], reg[3][c]};
+          if constexpr (R == 4) *reinterpret_cast<i32x4*>(dst) = i32x4{reg[0][c], reg[1][c], reg[2][c], reg[3][c]};
+          else *reinterpret_cast<i32x2*>(dst) = i32x2{reg[0][c], reg[1][c]};
         } else {
           const uint32_t sel = (c & 1) ? 0x07060302u : 0x05040100u;
-          const i32x2 v = {(int)__builtin_amdgcn_perm((uint32_t)reg[1][c >> 1], (uint32_t)reg[0][c >> 1], sel),
-                           (int)__builtin_amdgcn_perm((uint32_t)reg[3][c >> 1], (uint32_t)reg[2][c >> 1], sel)};
-          *reinterpret_cast<i32x2*>(dst) = v;
+          const int lo = (int)__builtin_amdgcn_perm((uint32_t)reg[1][c >> 1], (uint32_t)reg[0][c >> 1], sel);
+          if constexpr (R == 4)
+            *reinterpret_cast<i32x2*>(dst) =
+                i32x2{lo, (int)__builtin_amdgcn_perm((uint32_t)reg[3][c >> 1], (uint32_t)reg[2][c >> 1], sel)};
+          else
+            *reinterpret_cast<int*>(dst) = lo;
         }
       }
     }
@@ -163,29 +167,35 @@ __device__ __forceinline__ void store4(void* p, int64_t i, int64_t n, const floa
 }
 
 // LAY bit 0: A stored (k, m); bit 1: B stored (n, k); bit 2 (with bit 1): gated, B (2 n, k).
-// OUT: type of D. Waves of WM x 64.
-template <int DT, int OUT, int LAY, int BM, int BN, int WM>
-__global__ __launch_bounds__((BM / WM) * (BN / 64) * 64, 1) void gen_kernel(GenArgs p) {
+// OUT: type of D. Waves of WM x 64, in KG groups that share the k-steps of every tile (their sums
+// are added through LDS): the 64 x 64 tile has two, so that the few tiles of a small product still
+// put a wave on every SIMD. gridDim.y workgroups share the k loop (not gated), each with its own D.
+// Two k-tiles are on their way in registers while a third is multiplied.
+template <int DT, int OUT, int LAY, int BM, int BN, int WM, int KG>
+__global__ __launch_bounds__((BM / WM) * (BN / 64) * KG * 64, 2) void gen_kernel(GenArgs p) {
   using T = Tr<DT>;
   constexpr bool TA = (LAY & 1) != 0, TB = (LAY & 2) != 0, GATED = (LAY & 4) != 0;
-  constexpr int WN = 64, WAVES_M = BM / WM, NT = WAVES_M * (BN / WN) * 64, MB = WM / 32, NB = 2;
-  constexpr int ES = T::es, BK = kRowBytes / ES, STAGE = (BM + BN) * kRowBytes;
+  constexpr int WN = 64, WAVES_M = BM / WM, WAVES = WAVES_M * (BN / WN), NT = WAVES * KG * 64, MB = WM / 32, NB = 2;
+  constexpr int ES = T::es, BK = kRowBytes / ES, STAGE = (BM + BN) * kRowBytes, NS = 4 / KG;
   constexpr bool FINE = DT == F32;
   __shared__ __attribute__((aligned(16))) char lds[2 * STAGE];
   using OA = GenOperand<ES, BM, !TA, NT>;
   using OB = GenOperand<ES, BN, TB, NT, GATED ? 32 : 0>;
-  OA oa;
-  OB ob;
+  struct Tile {
+    OA a;
+    OB b;
+  } in[2];
 
   const int pos = xcd_remap(blockIdx.x, p.tiles_m * p.tiles_n);
   const int tm = __builtin_amdgcn_readfirstlane(pos % p.tiles_m), tn = __builtin_amdgcn_readfirstlane(pos / p.tiles_m);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * (GATED ? BN / 2 : BN);
   const int t = threadIdx.x, lane = t & 63;
-  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int wm = w % WAVES_M, wn = w / WAVES_M, lrow = lane & 31, lhi = lane >> 5;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6), kg = w / WAVES, wt = w % WAVES;
+  const int wm = wt % WAVES_M, wn = wt / WAVES_M, lrow = lane & 31, lhi = lane >> 5;
   const char* A = static_cast<const char*>(p.A);
   const char* B = static_cast<const char*>(p.B);
-  const int64_t KT = (p.k + BK - 1) / BK;
+  const int64_t KTA = (p.k + BK - 1) / BK;
+  const int64_t kb = KTA * blockIdx.y / gridDim.y, KT = KTA * (blockIdx.y + 1) / gridDim.y - kb;
 
   f32x16 acc[NB][MB];
 #pragma unroll
@@ -193,42 +203,72 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64, 1) void gen_kernel(GenA
 #pragma unroll
     for (int b = 0; b < MB; ++b) acc[a][b] = f32x16{};
 
-  if (KT > 0) {   // (a product over no tokens is zero)
-    oa.load(A, p.lda, m0, p.m, 0, p.k, t);
-    ob.load(B, p.ldb, n0, p.n, 0, p.k, t);
-    oa.store(lds, t);
-    ob.store(lds + BM * kRowBytes, t);
-  }
-  __syncthreads();
-  for (int64_t kt = 0; kt < KT; ++kt) {
-    const int cur = (int)(kt & 1);
-    if (kt + 1 < KT) {
-      oa.load(A, p.lda, m0, p.m, (kt + 1) * BK, p.k, t);
-      ob.load(B, p.ldb, n0, p.n, (kt + 1) * BK, p.k, t);
-    }
-    const char* sA = lds + cur * STAGE + (wm * WM + lrow) * kRowBytes;
-    const char* sB = lds + cur * STAGE + (BM + wn * WN + lrow) * kRowBytes;
+  const auto load = [&](Tile& v, int64_t kt) {
+    v.a.load(A, p.lda, m0, p.m, (kb + kt) * BK, p.k, t);
+    v.b.load(B, p.ldb, n0, p.n, (kb + kt) * BK, p.k, t);
+  };
+  const auto store = [&](const Tile& v, int stage) {
+    v.a.store(lds + stage * STAGE, t);
+    v.b.store(lds + stage * STAGE + BM * kRowBytes, t);
+  };
+  const auto tile = [&](auto utag, int64_t kt) {   // kt % 2 == u: in stage u; its successor is in in[u ^ 1]
+    constexpr int u = decltype(utag)::value;
+    if (kt + 2 < KT) load(in[u], kt + 2);
+    const char* sA = lds + u * STAGE + (wm * WM + lrow) * kRowBytes;
+    const char* sB = lds + u * STAGE + (BM + wn * WN + lrow) * kRowBytes;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < NS; ++s) {
+      const int chunk = 2 * (KG * s + kg) + lhi;
       i32x4 af[MB], bf[NB];
       // (the swizzle depends on the row's place in the tile: blocks of 32 rows, waves of 32 or 64)
 #pragma unroll
       for (int b = 0; b < MB; ++b)
-        af[b] = *reinterpret_cast<const i32x4*>(sA + b * 32 * kRowBytes + (((2 * s + lhi) ^ OA::swz(wm * WM + b * 32 + lrow)) << 4));
+        af[b] = *reinterpret_cast<const i32x4*>(sA + b * 32 * kRowBytes + ((chunk ^ OA::swz(wm * WM + b * 32 + lrow)) << 4));
 #pragma unroll
       for (int a = 0; a < NB; ++a)
-        bf[a] = *reinterpret_cast<const i32x4*>(sB + a * 32 * kRowBytes + (((2 * s + lhi) ^ OB::swz(wn * WN + a * 32 + lrow)) << 4));
+        bf[a] = *reinterpret_cast<const i32x4*>(sB + a * 32 * kRowBytes + ((chunk ^ OB::swz(wn * WN + a * 32 + lrow)) << 4));
 #pragma unroll
       for (int a = 0; a < NB; ++a)
 #pragma unroll
         for (int b = 0; b < MB; ++b) acc[a][b] = T::mma(bf[a], af[b], acc[a][b]);
     }
-    if (kt + 1 < KT) {
-      oa.store(lds + (cur ^ 1) * STAGE, t);
-      ob.store(lds + (cur ^ 1) * STAGE + BM * kRowBytes, t);
+    if (kt + 1 < KT) store(in[u ^ 1], u ^ 1);
+    __syncthreads();
+  };
+  if (KT > 0) {   // (a product over no tokens is zero)
+    load(in[0], 0);
+    if (KT > 1) load(in[1], 1);
+    store(in[0], 0);
+  }
+  __syncthreads();
+  for (int64_t kt = 0; kt < KT; kt += 2) {
+    tile(std::integral_constant<int, 0>{}, kt);
+    if (kt + 1 < KT) tile(std::integral_constant<int, 1>{}, kt + 1);
+  }
+  if constexpr (KG == 2) {
+    static_assert(WAVES * MB * NB * 4096 <= 2 * STAGE, "sums of the second group of waves");
+    f32x4* sums = reinterpret_cast<f32x4*>(lds) + wt * (MB * NB * 256) + lane;
+    if (kg == 1) {
+#pragma unroll
+      for (int i = 0; i < MB * NB; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const f32x16& v = acc[i / MB][i % MB];
+          sums[(i * 4 + c) * 64] = f32x4{v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]};
+        }
     }
     __syncthreads();
+    if (kg == 1) return;
+#pragma unroll
+    for (int i = 0; i < MB * NB; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const f32x4 v = sums[(i * 4 + c) * 64];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i / MB][i % MB][4 * c + e] += v[e];
+      }
   }
+  char* const D = static_cast<char*>(p.D) + (int64_t)blockIdx.y * p.m * p.ldd * Tr<OUT>::es;
 
   // lane: row m0 + wm WM + 32 b + l % 32; register r: column 8 (r / 4) + 4 (l / 32) + r % 4 of a block
 #pragma unroll
@@ -255,7 +295,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64, 1) void gen_kernel(GenA
 #pragma unroll
           for (int e = 0; e < 4; ++e) hv[e] = gate_act<decltype(act)::value, FINE>(gv[e]) * uv[e];
         });
-        store4<OUT>(p.D, row * p.ldd + col, left, hv);
+        store4<OUT>(D, row * p.ldd + col, left, hv);
         if (p.Z) {
           store4<OUT>(p.Z, row * 2 * p.n + col, left, gv);
           store4<OUT>(p.Z, row * 2 * p.n + p.n + col, left, uv);
@@ -268,7 +308,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64, 1) void gen_kernel(GenA
           float v[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = acc[a][b][4 * g + e];
-          store4<OUT>(p.D, row * p.ldd + col, left, v);
+          store4<OUT>(D, row * p.ldd + col, left, v);
         }
       }
     }

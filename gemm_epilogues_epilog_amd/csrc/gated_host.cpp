@@ -77,11 +77,47 @@ ge_status_t fast_layout(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay,
   return st;
 }
 
+// The large tile where it gives every compute unit one.
+bool general_large(int64_t M, int64_t N, int cus) { return cdiv(M, 128) * cdiv(N, 128) >= cus; }
+
+// Parts of at least eight k-tiles of 128 bytes, so many that the tiles fill the compute units twice.
+// Sized for kCompute of them, so that the result does not depend on the device.
+int general_splits(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, size_t ws) {
+  if (general_large(M, N, kCompute)) return 1;
+  const int64_t kt = cdiv(K * (int64_t)geh::elem_size(dt), 128), tiles = cdiv(M, 64) * cdiv(N, 64);
+  const int64_t s = std::min({kt / 8, cdiv(2 * kCompute, tiles), (int64_t)16});
+  return s > 1 && (size_t)s * M * N * 4 <= ws ? (int)s : 1;
+}
+
 ge_status_t gated_layout(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool backward, int cus, geh::Layout* L) {
   const ge_dtypes_t t = {dt, dt, dt};
   const int64_t cols = backward ? n : 2 * n;
   int cfg = geh::choose_cfg(m, cols, k, dt, cus, 2);   // (2: only configurations that take transposed operands)
   return geh::make_layout(m, cols, k, t, GE_EPILOG_NONE, 2, cus, cfg, false, cfg == gek::CFG_L, L);
+}
+
+// By estimated time in microseconds, from measurements at 1 to 64 tokens by 2 x 11008 x 4096, 4096 x
+// 11008, 2 x 1376 x 1024 and, fp32, 2 x 4096 x 2048. The kernel for few tokens: start and joining
+// 4, then W once per block of tokens and X, which every 16 rows read for themselves, at 6 TB/s
+// together (1 token 35 and 22 us, 32 tokens 63 and 40). The 128 x 128 tiles: 3, then W at 4.2 TB/s
+// or half a microsecond per k-tile and round of workgroups, whichever is longer (43 to 49, 79 to
+// 91, 12); the general kernel 1.4 per 128 bytes of k and round (99).
+bool skinny(int64_t m, int64_t rows, int64_t k, ge_dtype_t dt, bool gated, int cus) {
+  if (m <= 16) return true;
+  if (m > 65535) return false;   // (its grid, by far)
+  const double es = dt == GE_F32 ? 4 : 2, w = (double)rows * k * es;
+  const int64_t step = m <= 32 ? 32 : 64, blocks = cdiv(m, step), groups = cdiv(gated ? rows / 2 : rows, 16);
+  const double share = std::min(1.0, (double)(groups * blocks) / cus);
+  // (rows that are not whole 16-byte chunks read at less than half the rate)
+  const double rate = (int64_t)(k * es) % 16 == 0 ? 6e6 : 2.6e6;
+  const double few = 4.0 + ((double)blocks * w + (double)(groups * blocks * step) * k * es) / rate / share;
+  double tiles;
+  if (fast_shape(m, rows, k, dt, 2)) {
+    tiles = 3.0 + std::max(w / 4.2e6, (double)(cdiv(cdiv(m, 128) * cdiv(rows, 128), cus) * cdiv(k, 64)) * 0.5);
+  } else {
+    tiles = 3.0 + (double)(cdiv(cdiv(m, 64) * cdiv(rows, 64), 2 * cus) * cdiv((int64_t)(k * es), 128)) * 1.4;
+  }
+  return few < tiles;
 }
 
 int64_t colsum_parts(int64_t m, int64_t cols) {
@@ -98,6 +134,12 @@ BackwardSpace backward_space(int64_t m, int64_t n, int64_t k, int64_t d, ge_dtyp
   geh::Layout L;
   if (fast_shape(m, k, 2 * n, dt, 0) && fast_layout(m, k, 2 * n, dt, 0, kCompute, ~(size_t)0, &L) == GE_OK)
     most = std::max(most, L.ws_bytes);
+  // sums of the general kernel's parts (also of 16-bit products whose pointers turn out unaligned)
+  const int64_t prod[3][3] = {{m, k, 2 * n}, {2 * n, k, m}, {d, n, m}};
+  for (const auto& q : prod) {
+    const int parts = general_splits(q[0], q[1], q[2], dt, ~(size_t)0);
+    if (parts > 1) most = std::max(most, (size_t)parts * q[0] * q[1] * 4);
+  }
   s.total = s.scratch + align256(most);
   return s;
 }

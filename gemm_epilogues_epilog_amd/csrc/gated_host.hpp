@@ -34,9 +34,18 @@ bool fast_shape(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay);
 // Its configuration there, with the k loop split where that pays and `ws` bytes hold it.
 ge_status_t fast_layout(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, int cus, size_t ws, geh::Layout* L);
 
+// The general kernel: 128 x 128 tiles, or 64 x 64; and how many workgroups share a tile's k loop, as
+// far as `ws` bytes hold their fp32 sums.
+bool general_large(int64_t M, int64_t N, int cus);
+int general_splits(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, size_t ws);
+
 // The gated product X . W^T of (m, n) from 2 n rows, or (backward) dY . Wd with the activations'
 // gradient, on the tile kernels.
 ge_status_t gated_layout(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool backward, int cus, geh::Layout* L);
+
+// Whether X (m, k) . W^T with `rows` rows of W (gated: of both halves) goes to the kernel for few
+// tokens.
+bool skinny(int64_t m, int64_t rows, int64_t k, ge_dtype_t dt, bool gated, int cus);
 
 // Column sums of (m, 2 n) values: row ranges summed side by side.
 int64_t colsum_parts(int64_t m, int64_t cols);
