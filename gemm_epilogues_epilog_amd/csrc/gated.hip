@@ -69,10 +69,11 @@ __global__ __launch_bounds__(256) void dz_kernel(const void* dh, const void* z, 
   store8<DT>(o + n * es, pos, n, du);
 }
 
-// partial[part][col]: sums of the columns of a dense (m, cols) matrix over the part's rows, in a
+// partial[part][col], or with one part out[col] of type vec: sums of the columns of a dense (m, cols) matrix over the part's rows, in a
 // fixed order: four rows side by side, each in ascending order, then those four in order.
 template <int DT>
-__global__ __launch_bounds__(256) void colsum_kernel(const void* x, int64_t m, int64_t cols, float* partial) {
+__global__ __launch_bounds__(256) void colsum_kernel(const void* x, int64_t m, int64_t cols, float* partial, void* out,
+                                                     int vec) {
   constexpr int U = 4;
   __shared__ float sums[4][64][9];
   const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
@@ -96,9 +97,11 @@ __global__ __launch_bounds__(256) void colsum_kernel(const void* x, int64_t m, i
   __syncthreads();
   for (int i = threadIdx.x; i < 512; i += 256) {
     const int64_t col = (int64_t)blockIdx.x * 512 + i;
-    if (col < cols)
-      partial[(int64_t)blockIdx.y * cols + col] =
-          ((sums[0][i / 8][i % 8] + sums[1][i / 8][i % 8]) + sums[2][i / 8][i % 8]) + sums[3][i / 8][i % 8];
+    if (col < cols) {
+      const float v = ((sums[0][i / 8][i % 8] + sums[1][i / 8][i % 8]) + sums[2][i / 8][i % 8]) + sums[3][i / 8][i % 8];
+      if (gridDim.y == 1) store_vec(out, vec, col, v);
+      else partial[(int64_t)blockIdx.y * cols + col] = v;
+    }
   }
 }
 
@@ -201,8 +204,10 @@ ge_status_t column_sums(const void* x, int64_t m, int64_t cols, ge_dtype_t dt, v
     const void* fn = dt == GE_F32   ? reinterpret_cast<const void*>(&colsum_kernel<F32>)
                      : dt == GE_F16 ? reinterpret_cast<const void*>(&colsum_kernel<F16>)
                                     : reinterpret_cast<const void*>(&colsum_kernel<BF16>);
-    void* params[] = {&x, &m, &cols, &partial};
+    int v = (int)vec;
+    void* params[] = {&x, &m, &cols, &partial, &out, &v};
     if (launch(fn, dim3((unsigned)((cols + 511) / 512), parts), 256, params, s) != hipSuccess) return GE_ERR_HIP;
+    if (parts == 1) return GE_OK;
   }
   return launch_bgrad_reduce(partial, parts, cols, out, (int)vec, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
 }

@@ -92,8 +92,13 @@ int general_splits(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, size_t ws) {
 ge_status_t gated_layout(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool backward, int cus, geh::Layout* L) {
   const ge_dtypes_t t = {dt, dt, dt};
   const int64_t cols = backward ? n : 2 * n;
-  int cfg = geh::choose_cfg(m, cols, k, dt, cus, 2);   // (2: only configurations that take transposed operands)
-  return geh::make_layout(m, cols, k, t, GE_EPILOG_NONE, 2, cus, cfg, false, cfg == gek::CFG_L, L);
+  // (forward: the configurations for transposed operands; backward: those and the 192 and 128 x 256
+  // tiles; the others' places are taken by the nearest)
+  const int lay = backward ? 0 : 2;
+  int cfg = geh::choose_cfg(m, cols, k, dt, cus, lay);
+  if (cfg == gek::CFG_LH) cfg = gek::CFG_L;
+  if (cfg == gek::CFG_LM4) cfg = gek::CFG_LM;
+  return geh::make_layout(m, cols, k, t, GE_EPILOG_NONE, lay, cus, cfg, false, gek::cfg_can_persist(cfg), L);
 }
 
 // By estimated time in microseconds, from measurements at 1 to 64 tokens by 2 x 11008 x 4096, 4096 x
@@ -122,6 +127,7 @@ bool skinny(int64_t m, int64_t rows, int64_t k, ge_dtype_t dt, bool gated, int c
 
 int64_t colsum_parts(int64_t m, int64_t cols) {
   const int64_t across = cdiv(cols, 512);
+  if (m <= 128) return 1;   // (one kernel, 20 to 32 rows after each other in each of its four rows)
   return std::max<int64_t>(1, std::min(cdiv(m, 32), cdiv(1024, across)));
 }
 

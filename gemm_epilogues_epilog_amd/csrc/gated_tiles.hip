@@ -15,7 +15,7 @@ hipError_t tile(const Args& a, int grid, hipStream_t s) {
   Args copy = a;
   void* params[] = {&copy};
   const void* fn = reinterpret_cast<const void*>(&gemm_dtl_kernel<DT, EP, BM, BN, WM, WN, 64, ST, ILV, CW, LAY>);
-  if constexpr (BM == 256) {
+  if constexpr (BN == 256) {
     if (a.persist_grid > 0) {
       fn = reinterpret_cast<const void*>(
           &gemm_persist_kernel<DT, EP, BM, BN, WM, WN, 64, ST, CW, persist_pre((WM / 32) * (WN / 32)), LAY>);
@@ -36,6 +36,8 @@ LaunchFn pick_gated(int cfg) {
 template <int DT>
 LaunchFn pick_dgated(int cfg) {
   switch (cfg) {
+    case CFG_L3: return &tile<DT, DGATED, 0, 192, 256, 96, 64, 2, true, 4>;
+    case CFG_LW: return &tile<DT, DGATED, 0, 128, 256, 64, 64, 2, true, 4>;
     case CFG_LM: return &tile<DT, DGATED, 0, 128, 128, 32, 64, 2, false, 0>;
     case CFG_LMD: return &tile<DT, DGATED, 0, 128, 128, 32, 64, 3, false, 0>;
     default: return &tile<DT, DGATED, 0, 256, 256, 128, 64, 2, true, 4>;

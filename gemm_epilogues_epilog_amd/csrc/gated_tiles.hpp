@@ -7,7 +7,7 @@
 
 namespace gek {
 using LaunchFn = hipError_t (*)(const Args&, int grid, hipStream_t);
-// cfg: one of the configurations with kernels for transposed operands (cfg_has_layouts).
+// cfg: as gegh::gated_layout chooses it.
 LaunchFn get_launch_gated(int dt, bool backward, int cfg);
 
 // X . W^T of few tokens (gated_skinny.hpp), any type and alignment. At most 65535 groups of 64 tokens.

@@ -28,20 +28,40 @@ __device__ __forceinline__ float from_bits16(uint16_t v, int dt) {
   return dt == F16 ? Tr<F16>::widen(v) : Tr<BF16>::widen(v);
 }
 
-// Rounds to a group's codes. A wave takes the tiles of one group (at most one tile holds several
-// groups): row l % 16, and in each tile the k values 32 j + 8 (l / 16) .. + 7. Groups past one
-// tile are read twice, for the range and for the codes. Bound by memory.
+// The quotients of eight values and a scale, rounded to nearest even. 16-bit values: a product with
+// the reciprocal rs, its mantissa rounded to 20 bits. A quotient of two 16-bit numbers lies on a
+// border between two whole numbers or at least 2^-16 of itself away from it, and the product is
+// within 2^-22 of the quotient: so borders come out exactly and nothing else reaches them. (The exact
+// division took twice the instructions, which bound the kernel: 45 us at 11008 x 4096.) The exact
+// division for fp32 values, and where the reciprocal overflows.
 template <int SRC>
+__device__ __forceinline__ void w4_quotients(const float (&v)[8], float s, float rs, float (&o)[8]) {
+#pragma clang fp contract(off)
+  if (SRC == F32 || __builtin_amdgcn_ballot_w64(!(rs <= 3.402823466e38f)) != 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = rintf(v[e] / s);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float y = fminf(fmaxf(v[e] * rs, -64.0f), 64.0f), c = y * 17.0f;   // (held: far outside of the codes either way)
+      o[e] = rintf(c - (c - y));
+    }
+  }
+}
+
+// Rounds to a group's codes. A wave takes the tiles of one group (at most one tile holds several,
+// NG): row l % 16, and in each tile the k values 32 j + 8 (l / 16) .. + 7. Groups past one tile
+// (NG 0) are read twice, for the range and for the codes.
+template <int SRC, int NG>
 __global__ __launch_bounds__(256) void w4_quantize_kernel(const void* src, int64_t ld, W4Weight o, int dt, int symmetric,
                                                           int64_t units) {
   const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (unit >= units) return;
   const int lane = threadIdx.x & 63, li = lane & 15, q = lane >> 4;
-  const int64_t per = o.group > kTileK ? o.groups : o.kt;   // units of a row group
-  const int64_t rg = unit / per, u = unit - rg * per;        // row group, counted over both halves
-  const int64_t span = o.group > kTileK ? o.group / kTileK : 1;
+  const int64_t per = NG == 0 ? o.groups : o.kt;       // units of a row group
+  const int64_t rg = unit / per, u = unit - rg * per;   // row group, counted over both halves
+  const int64_t span = NG == 0 ? o.group / kTileK : 1;
   const int64_t ta = u * span, tb = ta + span < o.kt ? ta + span : o.kt;
-  const int ng = o.group >= kTileK ? 1 : (int)(kTileK / o.group);
   const int64_t half = rg / o.rgs, in = (rg - half * o.rgs) * kRows + li;
   const bool on = in < o.rows;
   const char* row = static_cast<const char*>(src) + (half * o.rows + (on ? in : 0)) * ld * Tr<SRC>::es;
@@ -59,105 +79,99 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(const void* src, int64
       else v[e] = Tr<SRC>::widen((uint16_t)((uint32_t)raw[0][e / 2] >> (16 * (e & 1))));
     }
   };
-  // Scale and zero of a group from its range (of this lane's part; joined over the four quarters).
-  const auto finish = [&](float lo, float hi, bool bad, float& s, float& z, uint16_t& bits) {
-#pragma unroll
-    for (int d = 16; d < 64; d <<= 1) {
-      lo = fminf(lo, __shfl_xor(lo, d));
-      hi = fmaxf(hi, __shfl_xor(hi, d));
-      bad |= (bool)__shfl_xor((int)bad, d);
-    }
-    const double width = symmetric ? (double)fmaxf(-lo, hi) / 7.0 : ((double)hi - (double)lo) / 15.0;
-    bits = bad ? (uint16_t)(dt == F16 ? 0x7e00 : 0x7fc0) : to_bits16((float)width, dt);
-    s = from_bits16(bits, dt);
-    z = symmetric ? 8.0f : s > 0.0f ? (float)fmin(rint(-(double)lo / (double)s), 15.0) : 0.0f;
+  struct Group {
+    float lo = 0.0f, hi = 0.0f, bad = 0.0f;   // bad: 0, or NaN once a value was not finite
+    float s, rs, z;
+    uint16_t bits;
   };
-  const auto encode = [&](const float (&v)[8], int64_t t, int j, float s, float z) {
-    const int64_t left = o.k - (t * kTileK + 32 * j + 8 * q);   // padding is zero
-    uint32_t d = 0;
+  const auto range = [&](Group& g, const float (&v)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float c = s > 0.0f ? fminf(fmaxf(rintf(v[e] / s) + z, 0.0f), 15.0f) : z;
-      d |= (on && e < left ? (uint32_t)c : 0u) << (8 * (e % 4) + 4 * (e / 4));
+      g.lo = fminf(g.lo, v[e]);
+      g.hi = fmaxf(g.hi, v[e]);
+      g.bad = __builtin_fmaf(v[e], 0.0f, g.bad);
+    }
+  };
+  // Scale and zero of a group from its range (of this lane's part; joined over the four quarters).
+  const auto finish = [&](Group& g) {
+#pragma unroll
+    for (int d = 16; d < 64; d <<= 1) {
+      g.lo = fminf(g.lo, __shfl_xor(g.lo, d));
+      g.hi = fmaxf(g.hi, __shfl_xor(g.hi, d));
+      g.bad += __shfl_xor(g.bad, d);
+    }
+    const double width = symmetric ? (double)fmaxf(-g.lo, g.hi) / 7.0 : ((double)g.hi - (double)g.lo) / 15.0;
+    g.bits = g.bad != 0.0f ? (uint16_t)(dt == F16 ? 0x7e00 : 0x7fc0) : to_bits16((float)width, dt);
+    g.s = from_bits16(g.bits, dt);
+    g.rs = 1.0f / (g.s > 0.0f ? g.s : 1.0f);
+    g.z = symmetric ? 8.0f : g.s > 0.0f ? (float)fmin(rint(-(double)g.lo / (double)g.s), 15.0) : 0.0f;
+  };
+  const auto encode = [&](const Group& g, const float (&v)[8], int64_t t, int j) {
+    const int64_t left = on ? o.k - (t * kTileK + 32 * j + 8 * q) : 0;   // padding is zero
+    float c[8];
+    w4_quotients<SRC>(v, g.s, g.rs, c);
+    uint32_t d = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      d |= (uint32_t)(g.s > 0.0f ? fminf(fmaxf(c[e] + g.z, 0.0f), 15.0f) : g.z) << (8 * (e % 4) + 4 * (e / 4));
+    if (left < 8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e >= left) d &= ~(15u << (8 * (e % 4) + 4 * (e / 4)));
     }
     return d;
   };
-  const auto put = [&](int64_t g, float z, uint16_t bits) {
-    if (q == 0) {
-      o.scales[(rg * o.groups + g) * kRows + li] = on ? bits : (uint16_t)0;
-      o.zeros[(rg * o.groups + g) * kRows + li] = on ? (uint8_t)z : (uint8_t)0;
-    }
-  };
-  const auto range = [&](const float (&v)[8], float& lo, float& hi, bool& bad) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo = fminf(lo, v[e]);
-      hi = fmaxf(hi, v[e]);
-      bad |= !(fabsf(v[e]) <= 3.402823466e38f);
+  const auto put = [&](const Group& g, int64_t at) {
+    if (q == 0 && at < o.groups) {
+      o.scales[(rg * o.groups + at) * kRows + li] = on ? g.bits : (uint16_t)0;
+      o.zeros[(rg * o.groups + at) * kRows + li] = on ? (uint8_t)g.z : (uint8_t)0;
     }
   };
 
-  if (o.group <= kTileK) {
-    float v[4][8], s[4], z[4];
+  if constexpr (NG > 0) {
+    float v[4][8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) read(ta, j, v[j]);
-    float lo[4], hi[4];
-    bool bad[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      lo[j] = hi[j] = 0.0f;
-      bad[j] = false;
-      range(v[j], lo[j], hi[j], bad[j]);
-    }
-    // two or four runs of 32 to a group
-    if (ng <= 2) {
-#pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        lo[j] = lo[j + 1] = fminf(lo[j], lo[j + 1]);
-        hi[j] = hi[j + 1] = fmaxf(hi[j], hi[j + 1]);
-        bad[j] = bad[j + 1] = bad[j] || bad[j + 1];
-      }
-    }
-    if (ng == 1) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        lo[j] = lo[j + 2] = fminf(lo[j], lo[j + 2]);
-        hi[j] = hi[j + 2] = fmaxf(hi[j], hi[j + 2]);
-        bad[j] = bad[j + 2] = bad[j] || bad[j + 2];
-      }
-    }
     i32x4 out;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint16_t bits;
-      finish(lo[j], hi[j], bad[j], s[j], z[j], bits);
-      out[j] = (int)encode(v[j], ta, j, s[j], z[j]);
-      const int64_t g = ta * ng + j * ng / 4;
-      if (j * ng % 4 == 0 && g < o.groups) put(g, z[j], bits);
+    for (int i = 0; i < NG; ++i) {
+      Group g;
+#pragma unroll
+      for (int j = 4 / NG * i; j < 4 / NG * (i + 1); ++j) range(g, v[j]);
+      finish(g);
+#pragma unroll
+      for (int j = 4 / NG * i; j < 4 / NG * (i + 1); ++j) out[j] = (int)encode(g, v[j], ta, j);
+      put(g, ta * NG + i);
     }
     *reinterpret_cast<i32x4*>(o.codes + (rg * o.kt + ta) * kTileBytes + lane * 16) = out;
   } else {
-    float lo = 0.0f, hi = 0.0f, s, z, v[8];
-    bool bad = false;
-    uint16_t bits;
+    Group g;
+    float v[8];
     for (int64_t t = ta; t < tb; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         read(t, j, v);
-        range(v, lo, hi, bad);
+        range(g, v);
       }
-    finish(lo, hi, bad, s, z, bits);
-    put(u, z, bits);
+    finish(g);
+    put(g, u);
     for (int64_t t = ta; t < tb; ++t) {
       i32x4 out;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         read(t, j, v);
-        out[j] = (int)encode(v, t, j, s, z);
+        out[j] = (int)encode(g, v, t, j);
       }
       *reinterpret_cast<i32x4*>(o.codes + (rg * o.kt + t) * kTileBytes + lane * 16) = out;
     }
   }
+}
+template <int SRC>
+const void* quantize_of(int64_t group) {
+  return group == 32    ? reinterpret_cast<const void*>(&w4_quantize_kernel<SRC, 4>)
+         : group == 64  ? reinterpret_cast<const void*>(&w4_quantize_kernel<SRC, 2>)
+         : group == 128 ? reinterpret_cast<const void*>(&w4_quantize_kernel<SRC, 1>)
+                        : reinterpret_cast<const void*>(&w4_quantize_kernel<SRC, 0>);
 }
 
 // Row-major codes, scales and zeros (null: all 8) into the layout; a wave per tile, and per 16
@@ -338,9 +352,9 @@ ge_status_t gemm_epilog_w4_quantize(int64_t rows, int64_t k, ge_dtype_t src_dt, 
   int64_t units = w.rgs * halves * (group > gew4::kTileK ? w.groups : w.kt);
   int d = (int)dt, sym = symmetric != 0;
   void* params[] = {&src, &ld, &w, &d, &sym, &units};
-  const void* fn = src_dt == GE_F32   ? reinterpret_cast<const void*>(&gek::w4_quantize_kernel<gek::F32>)
-                   : src_dt == GE_F16 ? reinterpret_cast<const void*>(&gek::w4_quantize_kernel<gek::F16>)
-                                      : reinterpret_cast<const void*>(&gek::w4_quantize_kernel<gek::BF16>);
+  const void* fn = src_dt == GE_F32   ? gek::quantize_of<gek::F32>(group)
+                   : src_dt == GE_F16 ? gek::quantize_of<gek::F16>(group)
+                                      : gek::quantize_of<gek::BF16>(group);
   return gek::run(fn, gek::waves(units), 256, 0, params, stream);
 }
 

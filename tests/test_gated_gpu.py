@@ -105,7 +105,8 @@ def test_forward_tiles(gpu, m, n, k, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("m,n,d", [(2048, 4352, 256), (1999, 4344, 384), (2048, 4352, 320), (1801, 4400, 200), (130, 264, 1600)])
+@pytest.mark.parametrize("m,n,d", [(2048, 4352, 256), (1999, 4344, 384), (2048, 4352, 320), (1801, 4400, 200), (130, 264, 1600),
+                                   (2048, 8192, 256), (1152, 4096, 512), (1150, 4088, 200)])
 def test_backward_tiles(gpu, m, n, d, dtype):
     for act in ACTS:
         x, w, _ = make(m, n, 64, dtype, m + n + d, bias=False)
