@@ -258,22 +258,31 @@ ge_status_t run(const void* fn, dim3 grid, int threads, size_t lds, void** param
                                                                                                            : GE_ERR_HIP;
 }
 
-template <int DT, bool GATED, int MT>
+template <int DT, bool GATED, int MT, bool VEC, bool FEW>
 const void* skinny_of(int64_t group) {
-  return group == 32   ? reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, MT, 4>)
-         : group == 64 ? reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, MT, 2>)
-                       : reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, MT, 1>);
+  return group == 32   ? reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, MT, 4, VEC, FEW>)
+         : group == 64 ? reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, MT, 2, VEC, FEW>)
+                       : reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, MT, 1, VEC, FEW>);
+}
+template <int DT, bool GATED, int MT>
+const void* skinny_of(int64_t group, bool vec) {
+  return vec ? skinny_of<DT, GATED, MT, true, false>(group) : skinny_of<DT, GATED, MT, false, false>(group);
 }
 
 template <int DT, bool GATED>
-ge_status_t skinny(W4Args& a, void* stream) {
+ge_status_t skinny(W4Args& a, bool vec, int cus, void* stream) {
   constexpr int NB = GATED ? 2 : 1;
   void* params[] = {&a};
   const int mt = a.m <= 16 ? 1 : a.m <= 32 ? 2 : 4;
-  const int nw = mt == 4 ? 4 : 8;
-  const void* fn = mt == 1   ? skinny_of<DT, GATED, 1>(a.group)
-                   : mt == 2 ? skinny_of<DT, GATED, 2>(a.group)
-                             : skinny_of<DT, GATED, 4>(a.group);
+  // Waves of a workgroup: as many as the device holds at once (16 to a compute unit, 12 and 8 with
+  // more tokens), four at least: 1 x 4096 x 11008 takes 14.8, 9.9 and 8.1 us with 4, 8 and 16 waves in
+  // 256 workgroups, 1 x 2 x 11008 x 4096 13.2, 15.5 and 16.7 in 688.
+  const int64_t most = (int64_t)cus * (mt == 1 ? 16 : mt == 2 ? 12 : 8) / (a.rgs * gew4::ceil_div(a.m, 16 * mt));
+  const int nw = mt == 1 && most >= 16 ? 16 : mt < 4 && most >= 8 ? 8 : 4;
+  const void* fn = a.m <= 4 && vec ? skinny_of<DT, GATED, 1, true, true>(a.group)
+                   : mt == 1 ? skinny_of<DT, GATED, 1>(a.group, vec)
+                   : mt == 2 ? skinny_of<DT, GATED, 2>(a.group, vec)
+                             : skinny_of<DT, GATED, 4>(a.group, vec);
   // (a launch has at most 65535 rows of workgroups)
   const int64_t step = (int64_t)65535 * 16 * mt, all = a.m;
   const char* x = static_cast<const char*>(a.x);
@@ -288,14 +297,13 @@ ge_status_t skinny(W4Args& a, void* stream) {
   return GE_OK;
 }
 
-ge_status_t tiled(W4Args& a, int cfg, ge_dtype_t dt, bool gated, void* stream) {
+ge_status_t tiled(W4Args& a, int cfg, ge_dtype_t dt, bool gated, bool vec, void* stream) {
   const gew4::W4TileCfg& T = gew4::kTiles[cfg];
   W4Launch L;
   L.tiles_m = (int32_t)gew4::ceil_div(a.m, T.bm);
   L.tiles_n = (int32_t)gew4::ceil_div(gated ? 2 * (int64_t)a.n : a.n, T.bn);
   L.group_m = 8;
-  const bool xd = a.vecx != 0;
-  const void* fn = dt == GE_F16 ? w4_tile_f16(cfg, gated, a.group, xd) : w4_tile_bf16(cfg, gated, a.group, xd);
+  const void* fn = dt == GE_F16 ? w4_tile_f16(cfg, gated, a.group, vec) : w4_tile_bf16(cfg, gated, a.group, vec);
   void* params[] = {&a, &L};
   return run(fn, dim3((unsigned)((int64_t)L.tiles_m * L.tiles_n)), T.waves * 64, 0, params, stream);
 }
@@ -321,12 +329,15 @@ ge_status_t multiply(int64_t m, int64_t n, int64_t k, int64_t group, ge_dtype_t 
   a.vec = (int32_t)vec;
   a.out = (int32_t)out;
   a.ep = ep;
-  a.vecx = k % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+  a.span = (int32_t)(group / gew4::kTileK);
+  a.inv_span = a.span > 1 ? (uint32_t)(((uint64_t(1) << 32) + a.span - 1) / a.span) : 0u;
+  const bool chunks = k % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
   int cus = 0;
   if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
-  if (const int cfg = gew4h::choose(m, n, k, group, gated, a.vecx != 0, cus); cfg >= 0) return tiled(a, cfg, dt, gated, stream);
-  if (dt == GE_F16) return gated ? skinny<F16, true>(a, stream) : skinny<F16, false>(a, stream);
-  return gated ? skinny<BF16, true>(a, stream) : skinny<BF16, false>(a, stream);
+  if (const int cfg = gew4h::choose(m, n, k, group, gated, chunks, cus); cfg >= 0)
+    return tiled(a, cfg, dt, gated, chunks, stream);
+  if (dt == GE_F16) return gated ? skinny<F16, true>(a, chunks, cus, stream) : skinny<F16, false>(a, chunks, cus, stream);
+  return gated ? skinny<BF16, true>(a, chunks, cus, stream) : skinny<BF16, false>(a, chunks, cus, stream);
 }
 
 dim3 waves(int64_t units) { return dim3((unsigned)((units + 3) / 4)); }

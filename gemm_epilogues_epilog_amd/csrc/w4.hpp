@@ -32,8 +32,17 @@ struct W4Args {
   int32_t rgs;           // row groups (gated: of a half)
   int32_t vec, out;      // types of the bias and of D
   int32_t ep;            // Ep, or Gate
-  int32_t vecx;          // X's rows are 16-byte aligned and whole 16-byte chunks
+  int32_t span;          // groups of 128 and more: k-tiles of a group
+  uint32_t inv_span;     // ceil(2^32 / span) (span > 1): t / span is the high half of t times it
 };
+
+template <int N, class F, int I = 0>
+__device__ __forceinline__ void w4_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    w4_for<N, F, I + 1>(static_cast<F&&>(f));
+  }
+}
 
 // Grid of the tile kernel.
 struct W4Launch {
@@ -74,22 +83,34 @@ __device__ __forceinline__ float act_ep(float v, int ep) {
   return ep == RELU_BIAS ? (v > 0.0f ? v : 0.0f) : ep == GELU_BIAS ? gelu_tanh(v) : v;
 }
 
-// A step of 128 k of the skinny kernel: codes, group scales and zeros of NB row groups, X of 16 MT
-// tokens. NG groups to a step.
-template <int NB, int MT, int NG>
+// v of another lane of the row of 16, by a DPP control.
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, true);
+}
+constexpr int kRowShl = 0x100, kRowRor = 0x120, kRowBcast = 0x150;   // lane i takes i + n, i - n, n
+
+// A step of 128 k of the skinny kernel: codes of NB row groups and X of 16 MT tokens (XR loads).
+template <int NB, int XR>
 struct W4Step {
-  i32x4 w[NB], x[MT][4];
-  i32x2 s[NB][NG];
-  uint32_t z[NB][NG];
+  i32x4 w[NB], x[XR];
 };
 
-// Skinny kernel: a few tokens; bound by reading W once. A workgroup takes NB row groups (gated:
-// the gate's and the up projection's) and 16 MT tokens; its waves take the steps of 128 k in
-// turn and add their sums through LDS in wave order.
-template <int DT, bool GATED, int FB, int MT, int NG>
-__global__ __launch_bounds__(512, MT == 4 ? 2 : MT == 2 ? 3 : 4) void w4_skinny_kernel(W4Args p) {
-  constexpr int NB = GATED ? 2 * FB : FB;
-  using Step = W4Step<NB, MT, NG>;
+// Skinny kernel: a few tokens; bound by reading W once, and beside that by the number of memory
+// instructions. A workgroup takes NB row groups (gated: the gate's and the up projection's) and 16
+// MT tokens; its waves take the steps of 128 k in turn and add their sums through LDS in wave
+// order. NG: groups to a step. VEC: X's rows are whole, aligned 16-byte chunks. FEW: up to four
+// tokens.
+// Scales and zeros are loaded for 16 groups at a time, a group to each of the 16 lanes of a row
+// (which need the same four scales, those of the rows 4 (l / 16) .. + 3 of the products), and
+// handed to all of them as their turn comes. Of up to four tokens a lane loads a chunk of its own,
+// and passes it on likewise: three memory instructions to a gated step of 2 KB instead of ten (one
+// token by 2 x 11008 x 4096 from memory: 14.7 -> 13.2 us; 4096 x 11008 8.1).
+template <int DT, bool GATED, int FB, int MT, int NG, bool VEC, bool FEW>
+__global__ __launch_bounds__(MT == 1 ? 1024 : 512, MT == 4 ? 2 : MT == 2 ? 3 : 4) void w4_skinny_kernel(W4Args p) {
+  constexpr int NB = GATED ? 2 * FB : FB, XR = FEW ? 1 : 4 * MT, SPAN = 16 / NG;   // SPAN: steps of a load of scales
+  static_assert(!FEW || (MT == 1 && VEC), "few tokens");
+  using Step = W4Step<NB, XR>;
   extern __shared__ __attribute__((aligned(16))) f32x4 red[];   // [wave][NB MT][64]
   const int nw = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, li = lane & 15, q = lane >> 4;
@@ -110,32 +131,61 @@ __global__ __launch_bounds__(512, MT == 4 ? 2 : MT == 2 ? 3 : 4) void w4_skinny_
   }
   const char* xb = static_cast<const char*>(p.x) + t0 * p.k * 2;
   const __amdgpu_buffer_rsrc_t rx = rsrc(xb);
+  uint32_t xo[MT];   // this lane's place in a step; of a token past the last one, out of range
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int row = FEW ? li & 3 : mt * 16 + li;
+    xo[mt] = t0 + row < p.m ? (uint32_t)(row * p.k * 2 + (FEW ? (li >> 2) * 64 : 0) + q * 16) : kOOB;
+  }
 
-  const auto load = [&](Step& st, int t) {
+  const auto load = [&](Step& st, int tv) {
+    // (the same in all lanes, which the compiler loses in the loop: offsets in vector registers
+    // would cost each load a loop over the lanes)
+    const int t = __builtin_amdgcn_readfirstlane(tv);
 #pragma unroll
     for (int b = 0; b < NB; ++b) st.w[b] = __builtin_amdgcn_raw_buffer_load_b128(rc[b], lane * 16, t * kTileBytes, 0);
-    const int g0 = NG > 1 ? t * NG : (int)((uint32_t)(t * kTileK) / (uint32_t)p.group);
+    const bool whole = (t + 1) * kTileK <= p.k;
+    if constexpr (FEW) {
+      const uint32_t off = whole || t * kTileK + (li >> 2) * 32 + 8 * q < p.k ? xo[0] : kOOB;
+      st.x[0] = __builtin_amdgcn_raw_buffer_load_b128(rx, off, t * (2 * kTileK), 0);
+    } else {
+      if (VEC && whole) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        st.s[b][g] = __builtin_amdgcn_raw_buffer_load_b64(rs[b], q * 8 + g * 32, g0 * 32, 0);
-        st.z[b][g] = __builtin_amdgcn_raw_buffer_load_b32(rz[b], q * 4 + g * 16, g0 * 16, 0);
+          for (int j = 0; j < 4; ++j)
+            st.x[mt * 4 + j] = __builtin_amdgcn_raw_buffer_load_b128(rx, xo[mt] + j * 64, t * (2 * kTileK), 0);
+        return;
       }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const bool in = t0 + mt * 16 + li < p.m;
+      for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int kp = t * kTileK + 32 * j + 8 * q;
-        if (p.vecx) {
-          const uint32_t off = in && kp < p.k ? (uint32_t)(((mt * 16 + li) * p.k + kp) * 2) : kOOB;
-          st.x[mt][j] = __builtin_amdgcn_raw_buffer_load_b128(rx, off, 0, 0);
-        } else {
-          const int row = in ? mt * 16 + li : 0;   // (its column of the products is not stored)
-          st.x[mt][j] = load_end<2>(xb + (int64_t)row * p.k * 2, kp, p.k);
+        for (int j = 0; j < 4; ++j) {
+          const int kp = t * kTileK + 32 * j + 8 * q;
+          if constexpr (VEC) {
+            st.x[mt * 4 + j] = __builtin_amdgcn_raw_buffer_load_b128(rx, kp < p.k ? xo[mt] + j * 64 : kOOB, t * (2 * kTileK), 0);
+          } else {
+            // (tokens past the last one read the first: their columns of the products are not stored)
+            const char* row = xb + (int64_t)(xo[mt] == kOOB ? 0 : mt * 16 + li) * p.k * 2;
+            st.x[mt * 4 + j] = whole ? load16(row + (int64_t)kp * 2) : load_end<2>(row, kp, p.k);
+          }
         }
       }
+    }
+  };
+  // Scales and zeros of this wave's steps i .. i + SPAN - 1: those of group li % NG of step
+  // i + li / NG in lane li.
+  struct Scales {
+    i32x2 s[NB];
+    int z[NB];
+  };
+  const auto load_scales = [&](Scales& sc, int i) {
+    const int t = w + (i + li / NG) * nw;
+    const int g = NG > 1 ? t * NG + li % NG : p.span == 1 ? t : (int)__umulhi((uint32_t)t, p.inv_span);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      sc.s[b] = __builtin_amdgcn_raw_buffer_load_b64(rs[b], t < p.kt ? (uint32_t)(g * 32 + q * 8) : kOOB, 0, 0);
+      sc.z[b] = __builtin_amdgcn_raw_buffer_load_b32(rz[b], t < p.kt ? (uint32_t)(g * 16 + q * 4) : kOOB, 0, 0);
     }
   };
 
@@ -145,47 +195,76 @@ __global__ __launch_bounds__(512, MT == 4 ? 2 : MT == 2 ? 3 : 4) void w4_skinny_
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[b][mt] = f32x4{0, 0, 0, 0};
 
-  const auto multiply = [&](const Step& st) {
+  const auto multiply = [&](const Step& st, Scales& sc) {
     const i32x4 ones = {kOnes<DT>, kOnes<DT>, kOnes<DT>, kOnes<DT>};
+    i32x4 x[4 * MT];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
+    for (int i = 0; i < 4 * MT; ++i) x[i] = st.x[FEW ? 0 : i];
+    if constexpr (FEW) {   // chunk j of token l % 4 is in lane l + 4 j
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[1][e] = dpp<kRowShl + 4>(st.x[0][e]);
+        x[2][e] = dpp<kRowShl + 8>(st.x[0][e]);
+        x[3][e] = dpp<kRowShl + 12>(st.x[0][e]);
+      }
+    }
+    w4_for<NG>([&](auto gtag) {
+      constexpr int g = decltype(gtag)::value;
       f32x4 part[NB][MT], sx[MT];
 #pragma unroll
       for (int j = 4 / NG * g; j < 4 / NG * (g + 1); ++j) {
         const bool first = j == 4 / NG * g;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) sx[mt] = mma16<DT>(ones, st.x[mt][j], first ? f32x4{0, 0, 0, 0} : sx[mt]);
+        for (int mt = 0; mt < MT; ++mt) sx[mt] = mma16<DT>(ones, x[mt * 4 + j], first ? f32x4{0, 0, 0, 0} : sx[mt]);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const i32x4 wq = w4_unpack<DT>((uint32_t)st.w[b][j]);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
-            part[b][mt] = mma16<DT>(wq, st.x[mt][j], first ? f32x4{0, 0, 0, 0} : part[b][mt]);
+            part[b][mt] = mma16<DT>(wq, x[mt * 4 + j], first ? f32x4{0, 0, 0, 0} : part[b][mt]);
         }
       }
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < NB; ++b) {
+        const i32x2 s2 = {dpp<kRowBcast + g>(sc.s[b][0]), dpp<kRowBcast + g>(sc.s[b][1])};
+        const uint32_t z4 = (uint32_t)dpp<kRowBcast + g>(sc.z[b]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float s = Tr<DT>::widen((uint16_t)((uint32_t)st.s[b][g][r / 2] >> (16 * (r & 1))));
-          const float z = (float)((st.z[b][g] >> (8 * r)) & 255u);
+          const float s = Tr<DT>::widen((uint16_t)((uint32_t)s2[r / 2] >> (16 * (r & 1))));
+          const float z = (float)((z4 >> (8 * r)) & 255u);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
             acc[b][mt][r] = __builtin_fmaf(s, __builtin_fmaf(-z, sx[mt][r], part[b][mt][r]), acc[b][mt][r]);
         }
+      }
+    });
+    // the next step's groups to the first lanes
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      sc.s[b] = i32x2{dpp<kRowRor + 16 - NG>(sc.s[b][0]), dpp<kRowRor + 16 - NG>(sc.s[b][1])};
+      sc.z[b] = dpp<kRowRor + 16 - NG>(sc.z[b]);
     }
   };
 
+  const int steps = w < p.kt ? (p.kt - w + nw - 1) / nw : 0;   // of this wave
   Step s0, s1;
-  if (w < p.kt) load(s0, w);
-  for (int t = w; t < p.kt; t += 2 * nw) {
-    if (t + nw < p.kt) load(s1, t + nw);
+  Scales sc, ahead;
+  if (steps > 0) {
+    load_scales(ahead, 0);
+    load(s0, w);
+  }
+  for (int i = 0; i < steps; i += 2) {
+    if (i % SPAN == 0) {
+      sc = ahead;
+      if (i + SPAN < steps) load_scales(ahead, i + SPAN);
+    }
+    if (i + 1 < steps) load(s1, w + (i + 1) * nw);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(s0);
-    if (t + nw >= p.kt) break;
-    if (t + 2 * nw < p.kt) load(s0, t + 2 * nw);
+    multiply(s0, sc);
+    if (i + 1 >= steps) break;
+    if (i + 2 < steps) load(s0, w + (i + 2) * nw);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(s1);
+    multiply(s1, sc);
   }
 #pragma unroll
   for (int b = 0; b < NB; ++b)

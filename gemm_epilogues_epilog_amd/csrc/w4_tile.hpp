@@ -46,14 +46,6 @@ struct W4Tile {
   static_assert(KG == 1 || (KG == 2 && MB * NB * 4096 <= EPI), "sums of the second group of waves");
 };
 
-template <int N, class F, int I = 0>
-__device__ __forceinline__ void w4_for(F&& f) {
-  if constexpr (I < N) {
-    f(std::integral_constant<int, I>{});
-    w4_for<N, F, I + 1>(static_cast<F&&>(f));
-  }
-}
-
 // Waits whose place among the loads and copies the compiler keeps.
 template <int N>
 __device__ __forceinline__ void w4_wait_vm() {
