@@ -9,8 +9,8 @@
 
 namespace gek {
 
-const void* w4_tile_f16(int cfg, bool gated, int64_t group, bool xd);    // w4_tile_f16.hip
-const void* w4_tile_bf16(int cfg, bool gated, int64_t group, bool xd);   // w4_tile_bf16.hip
+const void* w4_tile_f16(int cfg, bool gated, int64_t group);    // w4_tile_f16.hip
+const void* w4_tile_bf16(int cfg, bool gated, int64_t group);   // w4_tile_bf16.hip
 
 namespace {
 
@@ -297,13 +297,13 @@ ge_status_t skinny(W4Args& a, bool vec, int cus, void* stream) {
   return GE_OK;
 }
 
-ge_status_t tiled(W4Args& a, int cfg, ge_dtype_t dt, bool gated, bool vec, void* stream) {
+ge_status_t tiled(W4Args& a, int cfg, ge_dtype_t dt, bool gated, void* stream) {
   const gew4::W4TileCfg& T = gew4::kTiles[cfg];
   W4Launch L;
   L.tiles_m = (int32_t)gew4::ceil_div(a.m, T.bm);
   L.tiles_n = (int32_t)gew4::ceil_div(gated ? 2 * (int64_t)a.n : a.n, T.bn);
   L.group_m = 8;
-  const void* fn = dt == GE_F16 ? w4_tile_f16(cfg, gated, a.group, vec) : w4_tile_bf16(cfg, gated, a.group, vec);
+  const void* fn = dt == GE_F16 ? w4_tile_f16(cfg, gated, a.group) : w4_tile_bf16(cfg, gated, a.group);
   void* params[] = {&a, &L};
   return run(fn, dim3((unsigned)((int64_t)L.tiles_m * L.tiles_n)), T.waves * 64, 0, params, stream);
 }
@@ -335,7 +335,7 @@ ge_status_t multiply(int64_t m, int64_t n, int64_t k, int64_t group, ge_dtype_t 
   int cus = 0;
   if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
   if (const int cfg = gew4h::choose(m, n, k, group, gated, chunks, cus); cfg >= 0)
-    return tiled(a, cfg, dt, gated, chunks, stream);
+    return tiled(a, cfg, dt, gated, stream);
   if (dt == GE_F16) return gated ? skinny<F16, true>(a, chunks, cus, stream) : skinny<F16, false>(a, chunks, cus, stream);
   return gated ? skinny<BF16, true>(a, chunks, cus, stream) : skinny<BF16, false>(a, chunks, cus, stream);
 }

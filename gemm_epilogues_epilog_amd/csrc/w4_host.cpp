@@ -1,7 +1,6 @@
 // Rules declared in w4_host.hpp.
 #include "w4_host.hpp"
 
-
 namespace gew4h {
 
 namespace {
@@ -63,26 +62,29 @@ ge_status_t check_product(int64_t m, int64_t n, ge_dtype_t dt, ge_dtype_t out, c
   return GE_OK;
 }
 
-// By estimated time in microseconds, from measurements at 16 to 3000 tokens by 4096 x 4096 and 2 x
-// 2752 x 2048:
-//   skinny  start and joining 4, W from memory once per 64 tokens, and X, which every row group reads
-//           for itself, at the 7 TB/s that the L2 caches gave (fewer workgroups than compute units get
-//           their share): 7, 19 and 29 us for 16, 64 and 100 tokens;
-//   tiles   start and epilogue 3, then the k-tiles of each round of workgroups: 1.75 us each (256 x 256),
-//           0.8 (128 x 128), 0.6 (64 x 128); groups of 64 and of 32 multiply the sums more often.
+// By estimated time in microseconds, from measurements at 16 to 4000 tokens by 4096 x 4096 and below, 2 x
+// 2752 x 2048 and 2 x 11008 x 4096:
+//   skinny  start and joining 4, then 1.2 a round of workgroups; W from memory once per 64 tokens, and
+//           X, which every row group reads for itself, at the 10 TB/s that the L2 caches gave (fewer
+//           workgroups than compute units get their share): 7, 11, 18, 28 and 60 us for 16, 32, 64, 100
+//           and 256 tokens by 4096 x 4096. X in pieces of less than 16 bytes: 2.5 times that;
+//   tiles   start 2, a round of workgroups 2 and 128 k in 3.45 us (256 x 256), 1.15 (128 x 128) or 0.75
+//           (64 x 128: 28 us for 100 tokens); groups of 64 and of 32 multiply the sums more often.
 int choose(int64_t m, int64_t n, int64_t k, int64_t group, bool gated, bool aligned, int cus) {
+  if (k < 8) return -1;   // (the tiles load eight k at a time)
   const int64_t rows = gated ? 2 * n : n;
-  const double kt = (double)gew4::ceil_div(k, 64);
+  const double kt = (double)gew4::k_tiles(k);
   const int64_t step = m <= 16 ? 16 : m <= 32 ? 32 : 64, blocks = gew4::ceil_div(m, step);
   const double wgs = (double)gew4::ceil_div(n, 16) * (double)blocks, share = wgs < cus ? wgs / cus : 1.0;
-  double best = 4.0 + ((double)blocks * step * ((double)rows / 16) * (double)k * 2 / 7e6 + (double)blocks * rows * k * 0.5 / 5e6) / share;
+  const double x = (double)m * (double)rows / 16 * (double)k * 2 / 10e6, w = (double)blocks * (double)rows * (double)k * 0.5 / 5e6;
+  double best = (4.0 + 1.2 * (wgs / (share * cus) - 1.0) + (x + w) / share) * (aligned ? 1.0 : 2.5);
   int cfg = -1;
-  const double per[gew4::W4_COUNT][3] = {{1.75, 2.0, 0.0}, {0.8, 0.9, 1.2}, {0.6, 0.7, 0.94}};
+  const double per[gew4::W4_COUNT][3] = {{3.45, 4.0, 0.0}, {1.15, 1.55, 2.0}, {0.75, 0.87, 1.3}};
   const int e = group == 32 ? 2 : group == 64 ? 1 : 0;
   for (int c = 0; c < gew4::W4_COUNT; ++c) {
-    if (c == gew4::W4_L && (e == 2 || !aligned)) continue;   // (not instantiated: their registers spill)
+    if (c == gew4::W4_L && (e == 2 || !aligned)) continue;   // (not instantiated)
     const int64_t tiles = gew4::ceil_div(m, gew4::kTiles[c].bm) * gew4::ceil_div(rows, gew4::kTiles[c].bn);
-    const double t = 3.0 + (double)gew4::ceil_div(tiles, cus) * kt * per[c][e];
+    const double t = 2.0 + (double)gew4::ceil_div(tiles, cus) * (2.0 + kt * per[c][e]);
     if (t < best) {
       best = t;
       cfg = c;

@@ -1,57 +1,32 @@
 // Tile kernel of the products with 4-bit weights (layout: w4_format.hpp): dozens to thousands of
 // tokens.
 //
-// A BM x BN tile of D, k in tiles of 64. X goes straight into LDS; W's codes go through registers,
-// each once per workgroup, and lie in LDS as 16-bit numbers in the same k-major order. The two
-// operands then meet in v_mfma_f32_32x32x16 as in the 16-bit kernels (gemm_dtl.hpp).
+// A workgroup computes BM tokens by 128 rows of W, in steps of 128 k ("pairs" of 64). Eight waves:
+// four take 32 rows of W each (gated: 16 of the gate and the same 16 of the up projection), twice, for
+// the even and the odd ones of a pair's eight products along k. A wave turns its own codes into the
+// operand of v_mfma_f32_32x32x16 in registers, each code once in the workgroup, with no LDS between;
+// lane l holds row l % 32 of W throughout: its codes, scales and sums. X is shared: it goes through
+// registers into two LDS stages, with one barrier to a pair; X is loaded three pairs ahead of its use
+// and W two, and no load stands behind a branch, so every wait leaves the younger ones on their way.
 //
-// No weight is rounded: a scale s is split into a power of two p and f = s / p, and W in LDS is
+// What bounds it is instruction issue: turning eight codes into bf16 takes 19 vector instructions
+// (f16: 11), and a group's factor one per sum, beside BM / 32 products. With W converted through LDS
+// for both halves of the waves (w4_large.hpp's way) tiles of 128 x 128 took 156 us at 3000 x 4096 x
+// 4096 bf16 (groups of 128) and 53 at 600 tokens, and tiles of 64 x 128 23 at 200 x 2 x 2752 x 2048 f16; in
+// registers 137, 42 and 15.5.
+//
+// No weight is rounded: a scale s is split into a power of two p and f = s / p, and the operand is
 // (q - z) p, exact in 16 bits. The sums are held in units of f: where a group of a row begins they
 // are multiplied by the last group's f over the new one's (one fp32 multiplication per sum and
 // group, no second set of sums), and by the last f at the end. p takes the whole exponent of s
 // where (q - z) p stays a normal number, so f lies in [1, 2) but for scales out there, and the
 // quotients stay far from fp32's limits.
-//
-// At the end of k-tile t every wave waits until its copies of X's tile t + 1 have landed and its
-// reads of tile t and its writes of W's tile t + 1 are done; one barrier publishes tile t + 1 and
-// releases tile t's stages, which X's tile t + XS is copied into and, during the products of t + 1,
-// W's tile t + 2 is converted into. Codes, scales and zeros come two k-tiles at a time, XS / 2 such
-// pairs ahead, through LDS as well (each wave its own), so that every wait in the loop is for
-// copies whose number the kernel knows: registers loaded that early would be waited for by the
-// compiler, which does not see the copies of X between them.
 #pragma once
 
 #include "gemm_dtl.hpp"
 #include "w4.hpp"
 
 namespace gek {
-
-// XS: stages of X's ring (of W's there are two). KG: groups of waves that share the k-steps of every
-// k-tile (their sums are added at the end).
-template <int BM_, int BN_, int WM_, int WN_, int XS_, int KG_>
-struct W4Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, XS = XS_, KG = KG_;
-  static constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN, NW = WAVES_M * WAVES_N * KG, NT = NW * 64;
-  static constexpr int MB = WM / 32, NB = WN / 32;
-  static constexpr int X_BYTES = BM * 128, W_BYTES = BN * 128, OFF_W = XS * X_BYTES;
-  static constexpr int XI = X_BYTES / 1024 / NW;      // copies of X per wave and k-tile
-  static constexpr int RG = BN / 16 / NW;             // row groups that a wave converts
-  static constexpr int CODES = RG * 1024 + 512;       // a pair's codes, scales and zeros of one wave
-  static constexpr int OFF_R = OFF_W + 2 * W_BYTES;   // factors of the sums: [stage][group of the k-tile][BN]
-  static constexpr int OFF_C = OFF_R + 2 * 2 * BN * 4;
-  static constexpr int EPI = 8192;                    // epilogue bytes per wave (in the stages)
-  static constexpr int LDS = OFF_C + XS / 2 * NW * CODES;
-  static_assert(X_BYTES % (1024 * NW) == 0 && BN % (16 * NW) == 0, "shares of a wave");
-  static_assert(NW / KG * EPI <= OFF_R && LDS <= 160 * 1024, "LDS");
-  static_assert(KG == 1 || (KG == 2 && MB * NB * 4096 <= EPI), "sums of the second group of waves");
-};
-
-// Waits whose place among the loads and copies the compiler keeps.
-template <int N>
-__device__ __forceinline__ void w4_wait_vm() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  asm volatile("s_waitcnt vmcnt(%0)" ::"i"(N) : "memory");
-}
 
 // A scale in two: its power of two p (0 for 0, the scale itself if it is not finite), and f.
 template <int DT>
@@ -100,117 +75,91 @@ __device__ __forceinline__ i32x4 w4_expand(uint32_t w, uint32_t pz) {
   return o;
 }
 
-// A pair of k-tiles of RG row groups, E groups of k to a row in it: codes, and of each group p and z
-// and the factor that brings the sums into its units.
-template <int RG, int E>
-struct W4Codes {
-  i32x4 c[RG];
-  uint32_t pz[RG][E];
-  float ratio[RG][E];
+// Groups of a row in a pair: scales and zeros as loaded, and a pair's codes.
+template <int E>
+struct W4Raw {
+  i32x4 c;
+  uint32_t s[E], z[E];
 };
 
-// 4 bytes per lane, as copy_to_lds_b128.
-__device__ __forceinline__ void copy_to_lds_b32(const i32x4& srd, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
-               :
-               : "v"(voff), "s"(srd), "s"(__builtin_amdgcn_readfirstlane(lds))
-               : "memory", "m0");
-}
-
-// Epilogue: 32 x 32 blocks of sums through fp32 scratch (gated: one of the gate and one of the up
-// projection), so that a lane gets eight neighbouring columns of a token and memory sees whole
-// pieces of rows at any alignment.
-template <int DT, bool GATED, class C>
-__device__ __forceinline__ void w4_tile_epilogue(const W4Args& p, const f32x16 (&acc)[C::NB][C::MB], int64_t m0, int n0,
-                                                 int lane, char* scratch) {
-  constexpr int NH = GATED ? C::NB / 2 : C::NB;
-  const int lrow = lane & 31, lhi = lane >> 5, r16 = lane >> 2, c = lane & 3;
+// Epilogue of one 32 x 32 block (lane l: row l % 32 of W, register r: token 8 (r / 4) + 4 (l / 32) +
+// r % 4) through 4 KB of fp32 scratch, so that a lane gets eight neighbouring columns of a token
+// and memory sees whole pieces of rows at any alignment. Gated: columns 0 .. 15 are the gate's, 16 ..
+// 31 the up projection's.
+template <int DT, bool GATED>
+__device__ __forceinline__ void w4_block(const W4Args& p, const f32x16& acc, int64_t m0, int64_t n0, int lane, char* scratch) {
+  const int col = lane & 31, lhi = lane >> 5;
   const auto swz = [](int row) { return (row ^ (row >> 3)) & 7; };   // 16-byte units of 128-byte rows
-  const auto put = [&](const f32x16& v, char* to) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
-      *reinterpret_cast<f32x4*>(to + lrow * 128 + (((2 * g + lhi) ^ swz(lrow)) << 4)) =
-          f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
-  };
-  const auto get = [&](const char* from, int h, float (&v)[8]) {
-    const int row = 16 * h + r16;
+  for (int r = 0; r < 16; ++r) {
+    const int row = 8 * (r / 4) + 4 * lhi + r % 4;
+    *reinterpret_cast<float*>(scratch + row * 128 + (((col >> 2) ^ swz(row)) << 4) + (col & 3) * 4) = acc[r];
+  }
+  __builtin_amdgcn_wave_barrier();
+  const auto get = [&](int row, int unit, float (&v)[8]) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const f32x4 d = *reinterpret_cast<const f32x4*>(from + row * 128 + (((2 * c + u) ^ swz(row)) << 4));
+      const f32x4 d = *reinterpret_cast<const f32x4*>(scratch + row * 128 + (((unit + u) ^ swz(row)) << 4));
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[4 * u + e] = d[e];
     }
   };
+  constexpr int LPR = GATED ? 2 : 4, PASSES = GATED ? 1 : 2;   // lanes to a token
+  const int c = lane % LPR;
+  const int64_t at0 = n0 + 8 * c, left = p.n - at0;
+  float bg[8], bu[8];
 #pragma unroll
-  for (int a = 0; a < NH; ++a) {
-    const int64_t col = n0 + 32 * a + 8 * c, left = p.n - col;
-    float bg[8], bu[8];
+  for (int e = 0; e < 8; ++e) {
+    bg[e] = p.bias && e < left ? load_vec(p.bias, p.vec, at0 + e) : 0.0f;
+    bu[e] = GATED && p.bias && e < left ? load_vec(p.bias, p.vec, p.n + at0 + e) : 0.0f;
+  }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      bg[e] = p.bias && e < left ? load_vec(p.bias, p.vec, col + e) : 0.0f;
-      bu[e] = GATED && p.bias && e < left ? load_vec(p.bias, p.vec, p.n + col + e) : 0.0f;
+  for (int h = 0; h < PASSES; ++h) {
+    const int row = h * (64 / LPR) + lane / LPR;
+    const int64_t token = m0 + row;
+    float y[8];
+    get(row, 2 * c, y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] += bg[e];
+    if constexpr (GATED) {
+      float u[8];
+      get(row, 4 + 2 * c, u);
+      with_gate(p.ep, [&](auto act) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = gate_act<decltype(act)::value, false>(y[e]) * (u[e] + bu[e]);
+      });
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = act_ep(y[e], p.ep);
     }
-#pragma unroll
-    for (int b = 0; b < C::MB; ++b) {
-      put(acc[a][b], scratch);
-      if constexpr (GATED) put(acc[a + NH][b], scratch + 4096);
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t token = m0 + 32 * b + 16 * h + r16;
-        float y[8];
-        get(scratch, h, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] += bg[e];
-        if constexpr (GATED) {
-          float u[8];
-          get(scratch + 4096, h, u);
-          with_gate(p.ep, [&](auto act) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = gate_act<decltype(act)::value, false>(y[e]) * (u[e] + bu[e]);
-          });
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = act_ep(y[e], p.ep);
-        }
-        if (token < p.m && left > 0) {
-          const int64_t at = token * p.n + col;
-          const float y0[4] = {y[0], y[1], y[2], y[3]}, y1[4] = {y[4], y[5], y[6], y[7]};
-          if (p.out == F32) {
-            store4<F32>(p.D, at, left, y0);
-            store4<F32>(p.D, at + 4, left - 4, y1);
-          } else if (left >= 8) {
-            const i32x4 o = {(int)Tr<DT>::pack2(y[0], y[1]), (int)Tr<DT>::pack2(y[2], y[3]), (int)Tr<DT>::pack2(y[4], y[5]),
-                             (int)Tr<DT>::pack2(y[6], y[7])};
-            __builtin_memcpy(static_cast<uint16_t*>(p.D) + at, &o, 16);
-          } else {
-            store4<DT>(p.D, at, left, y0);
-            store4<DT>(p.D, at + 4, left - 4, y1);
-          }
-        }
+    if (token < p.m && left > 0) {
+      const int64_t at = token * p.n + at0;
+      const float y0[4] = {y[0], y[1], y[2], y[3]}, y1[4] = {y[4], y[5], y[6], y[7]};
+      if (p.out == F32) {
+        store4<F32>(p.D, at, left, y0);
+        store4<F32>(p.D, at + 4, left - 4, y1);
+      } else if (left >= 8) {
+        const i32x4 o = {(int)Tr<DT>::pack2(y[0], y[1]), (int)Tr<DT>::pack2(y[2], y[3]), (int)Tr<DT>::pack2(y[4], y[5]),
+                         (int)Tr<DT>::pack2(y[6], y[7])};
+        __builtin_memcpy(static_cast<uint16_t*>(p.D) + at, &o, 16);
+      } else {
+        store4<DT>(p.D, at, left, y0);
+        store4<DT>(p.D, at + 4, left - 4, y1);
       }
-      __builtin_amdgcn_wave_barrier();
     }
   }
+  __builtin_amdgcn_wave_barrier();
 }
 
-// E: groups of a row in a pair of k-tiles: 4 (of 32), 2 (of 64), 1 (of 128 and more). XD: X's rows are whole 16-byte chunks, copied straight into
-// LDS; otherwise they go through registers.
-template <int DT, bool GATED, class C, int E, bool XD>
-__global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W4Launch L) {
-  constexpr int BM = C::BM, BN = C::BN, WM = C::WM, WN = C::WN, MB = C::MB, NB = C::NB, RG = C::RG, XI = C::XI;
-  constexpr int NCODE = RG + 2, NMMA = MB * NB, KG = C::KG, NS = 4 / KG;   // (NS: a wave's k-steps of a tile)
-  constexpr int XS = XD ? C::XS : 2, D = XS / 2;   // (through registers X is one k-tile ahead)
-  static_assert(XS == 2 || XS == 4, "stages of X");
-  // Copies younger than X's tile t + 1 at the end of k-tile t: those of the XS - 2 k-tiles after it,
-  // of which every other one brings codes, and for an odd t the codes that came with it.
-  constexpr int AHEAD = (XS - 2) * XI + (XS - 2) / 2 * NCODE;
-  __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
-  const int lane = threadIdx.x & 63;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int kg = KG == 1 ? 0 : w / (C::NW / KG), wt = KG == 1 ? w : w % (C::NW / KG);
-  const int wm = wt % C::WAVES_M, wn = wt / C::WAVES_M;
-  const int li = lane & 15, q = lane >> 4, lhi = lane >> 5;
+// E: groups of a row in a pair: 4 (of 32), 2 (of 64), 1 (of 128 and more). X's rows may have any
+// alignment: the memory pipe takes 16-byte loads at it.
+template <int DT, bool GATED, int BM, int E>
+__global__ __launch_bounds__(512, 2) void w4_tile_kernel(W4Args p, W4Launch L) {
+  constexpr int MB = BM / 32, XI = BM * 16 / 512, STAGE = BM * 256;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wn = w & 3, kg = w >> 2;
+  const int lrow = lane & 31, lhi = lane >> 5;
   int tm, tn;
   {
     Args r;
@@ -220,282 +169,163 @@ __global__ __launch_bounds__(C::NT, 512 / C::NT) void w4_tile_kernel(W4Args p, W
     raster(r, xcd_remap(blockIdx.x, L.tiles_m * L.tiles_n), tm, tn);
   }
   const int64_t m0 = (int64_t)tm * BM;
-  const int n0 = tn * (GATED ? BN / 2 : BN);
-  const int KT = (p.k + 63) / 64, KT2 = (KT + 1) & ~1;
-  const uint32_t lds = (uint32_t)(uintptr_t)(lds_void*)smem;
+  const int n0 = tn * (GATED ? 64 : 128) + wn * (GATED ? 16 : 32);   // this wave's first column
+  const int KP = p.kt;
 
-  // ---- X ----
-  uint32_t x_src[XI];
-  int x_chunk[XI];
+  // ---- X: chunk i of a thread is chunk tid % 16 of row tid / 16 + 32 i of the pair ----
+  // Every load happens (one that may not would turn the later waits into waits for all that are on
+  // their way): past the last pair it is the last again, and where k ends in a chunk, or before it,
+  // the row's last eight elements are loaded and moved down (k >= 8).
   const char* xb = static_cast<const char*>(p.x) + m0 * p.k * 2;
+  const int over = max(0, (KP - 1) * 128 + (tid & 15) * 8 + 8 - p.k);   // of the last pair's chunk past k
+  uint32_t x_off[XI];
+  int x_lds[XI];
 #pragma unroll
-  for (int j = 0; j < XI; ++j) {
-    const int row = (w * XI + j) * 8 + lane / 8;
-    x_chunk[j] = (lane % 8) ^ swz_a<128>(row);
-    x_src[j] = m0 + row < p.m ? (uint32_t)(row * p.k * 2 + x_chunk[j] * 16) : kOOB;
+  for (int i = 0; i < XI; ++i) {
+    const int row = tid / 16 + 32 * i, c = tid & 15;
+    const int at = (int)(m0 + row < p.m ? row : p.m - 1 - m0);   // (tokens past the last one are not stored)
+    x_off[i] = (uint32_t)(at * (p.k * 2)) + c * 16;
+    x_lds[i] = (c >> 3) * (BM * 128) + row * 128 + (((c & 7) ^ swz_a<128>(row)) << 4);
   }
-  i32x4 xr[XD ? 1 : XI];
-  auto issue_x = [&](int t) {
-    const int k0 = t * 64;
-    if constexpr (XD) {
-      // (a k-tile past the last one reads nothing: zeros)
-      const i32x4 srd = make_srd(xb + (int64_t)k0 * 2, t < KT ? 0x7fffffffu : 0u);
-      const bool tail = k0 + 64 > p.k;
+  i32x4 xr[2][XI];
+  auto load_x = [&](i32x4 (&r)[XI], int pair) {
+    const char* at = xb + (int64_t)min(pair, KP - 1) * 256 - (pair < KP - 1 ? 0 : 2 * over);
 #pragma unroll
-      for (int j = 0; j < XI; ++j) {
-        const uint32_t off = tail && k0 + x_chunk[j] * 8 >= p.k ? kOOB : x_src[j];
-        copy_to_lds_b128(srd, off, lds + (t & (XS - 1)) * C::X_BYTES + (w * XI + j) * 1024);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < XI; ++j) {
-        const int64_t row = (w * XI + j) * 8 + lane / 8;
-        const int64_t at = m0 + row < p.m ? row : 0;   // (tokens past the last one are not stored)
-        xr[j] = load_end<2>(xb + at * p.k * 2, k0 + x_chunk[j] * 8, p.k);
-      }
-    }
+    for (int i = 0; i < XI; ++i) r[i] = load16(at + x_off[i]);
   };
-  auto store_x = [&](int t) {
-    if constexpr (!XD) {
+  auto store_x = [&](i32x4 (&r)[XI], int stage, int pair) {
+    if (pair == KP - 1 && p.k % 128) {
 #pragma unroll
-      for (int j = 0; j < XI; ++j)
-        *reinterpret_cast<i32x4*>(smem + (t & 1) * C::X_BYTES + (w * XI + j) * 1024 + lane * 16) = xr[j];
+      for (int i = 0; i < XI; ++i) r[i] = shift_down<2>(r[i], min(over, 8));
     }
+#pragma unroll
+    for (int i = 0; i < XI; ++i) *reinterpret_cast<i32x4*>(smem + stage * STAGE + x_lds[i]) = r[i];
   };
 
-  // ---- W ----
-  // Tile row groups of this wave: w RG .. + RG - 1; of a gated tile, pairs of groups alternate
-  // between the halves, so that each wave column has 32 rows of both.
-  const int first = w * RG;
-  const int in0 = n0 / 16 + (GATED ? first / 4 * 2 + first % 2 : first);   // (RG of them follow each other)
-  const int on = max(0, min(RG, p.rgs - in0));
-  const int64_t rg0 = (on > 0 ? in0 : 0) + (GATED && first / 2 % 2 ? (int64_t)p.rgs : 0);
-  const char* cb = p.codes + rg0 * p.kt * kTileBytes;
-  const i32x4 srd_s = make_srd(p.scales + rg0 * p.groups * kRows), srd_z = make_srd(p.zeros + rg0 * p.groups * kRows);
-  // this lane's dword of the scales and of the zeros: row group, entry, place
-  const int s_r = lane / (8 * E), s_e = lane / 8 % E, z_r = lane / (4 * E), z_e = lane / 4 % E;
-  const uint32_t s_off = s_r < on ? (uint32_t)(s_r * p.groups * 32 + lane % 8 * 4) : kOOB;
-  const uint32_t z_off = z_r < on ? (uint32_t)(z_r * p.groups * 16 + lane % 4 * 4) : kOOB;
-  const uint32_t lds_c = lds + C::OFF_C + w * C::CODES;
-  constexpr int SLOT = C::NW * C::CODES;
-  // pairs to a group (E 1); the group of the pair copied next and its pairs copied; pairs read of theirs
-  const int span = E == 1 ? p.group / 128 : 1;
-  int next_group = 0, copied = 0, begun = 0;
-  auto copy_w = [&](int pair) {   // k-tiles 2 pair and 2 pair + 1, in order
-    const uint32_t to = lds_c + (D == 1 ? 0 : (pair & (D - 1)) * SLOT);
-    const bool in = pair < p.kt;
+  // ---- W: this lane's row ----
+  const int in = n0 / 16 + (GATED ? 0 : lrow >> 4);
+  const int64_t rg = (in < p.rgs ? in : p.rgs - 1) + (GATED && lrow >= 16 ? (int64_t)p.rgs : 0);
+  const char* cp = p.codes + rg * p.kt * kTileBytes + ((lane & 15) + 16 * (2 * kg + lhi)) * 16;
+  const uint16_t* sp = p.scales + rg * p.groups * kRows + (lane & 15);
+  const uint8_t* zp = p.zeros + rg * p.groups * kRows + (lane & 15);
+  using Raw = W4Raw<E>;
+  int group = 0, loaded = 0, begun = 0;   // (E 1) of the pair loaded next; pairs loaded, and used, of its group
+  auto load_w = [&](Raw& d, int pair) {   // in order; past the last pair, the last one again
+    d.c = *reinterpret_cast<const i32x4*>(cp + (int64_t)(pair < KP ? pair : KP - 1) * kTileBytes);
 #pragma unroll
-    for (int r = 0; r < RG; ++r)
-      copy_to_lds_b128(make_srd(cb + ((int64_t)r * p.kt + pair) * kTileBytes, in && r < on ? kTileBytes : 0u), lane * 16, to + r * 1024);
-    // group of this lane's dwords (E 1: the pairs of a group follow each other)
-    const int gs = E == 1 ? next_group : pair * E + s_e, gz = E == 1 ? next_group : pair * E + z_e;
-    copy_to_lds_b32(srd_s, gs < p.groups ? s_off + (s_off == kOOB ? 0u : gs * 32) : kOOB, to + RG * 1024);
-    copy_to_lds_b32(srd_z, gz < p.groups ? z_off + (z_off == kOOB ? 0u : gz * 16) : kOOB, to + RG * 1024 + 256);
-    if (E == 1 && ++copied == span) {
-      copied = 0;
-      ++next_group;
+    for (int e = 0; e < E; ++e) {
+      const int g = min(E == 1 ? group : pair * E + e, p.groups - 1);
+      d.s[e] = sp[(int64_t)g * kRows];
+      d.z[e] = zp[(int64_t)g * kRows];
+    }
+    if (E == 1 && ++loaded == p.span) {
+      loaded = 0;
+      ++group;
     }
   };
-  using Codes = W4Codes<RG, E>;
-  float f[RG];   // of the group read last
-#pragma unroll
-  for (int r = 0; r < RG; ++r) f[r] = 1.0f;
-  auto read_w = [&](Codes& d, int pair) {
-    const char* at = smem + C::OFF_C + w * C::CODES + (D == 1 ? 0 : (pair & (D - 1)) * SLOT);
-    // past the last pair, and inside a group of several, the units stay as they are
-    bool in = 2 * pair < KT2;
-    if (E == 1) {
-      in = in && begun == 0;
-      if (++begun == span) begun = 0;
-    }
-#pragma unroll
-    for (int r = 0; r < RG; ++r) {
-      d.c[r] = *reinterpret_cast<const i32x4*>(at + r * 1024 + lane * 16);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float p, fn;
-        w4_split<DT>(*reinterpret_cast<const uint16_t*>(at + RG * 1024 + ((r * E + e) * 16 + li) * 2), p, fn);
-        d.pz[r][e] = w4_pz(p, *reinterpret_cast<const uint8_t*>(at + RG * 1024 + 256 + (r * E + e) * 16 + li));
-        d.ratio[r][e] = in ? f[r] * __builtin_amdgcn_rcpf(fn) : 1.0f;
-        f[r] = in ? fn : f[r];
-      }
-    }
-  };
-  // Converts dword i of this wave's 2 RG per k-tile into the stage of a k-tile of parity par: row
-  // group i / 2, dword 2 par + i % 2. No branches, so that it runs among the products. (The four
-  // lanes of a row write the same factor.)
-  auto convert = [&](const Codes& d, auto ptag, auto itag) {
-    constexpr int par = decltype(ptag)::value, i = decltype(itag)::value, r = i / 2, h = i % 2;
-    constexpr int g = E == 4 ? 2 * par + h : E == 2 ? par : 0;
-    const int row = (w * RG + r) * 16 + li;   // of the tile
-    char* st = smem + C::OFF_W + par * C::W_BYTES + row * 128;
-    *reinterpret_cast<i32x4*>(st + (((4 * h + q) ^ swz_a<128>(row)) << 4)) = w4_expand<DT>((uint32_t)d.c[r][2 * par + h], d.pz[r][g]);
-    if constexpr (E == 4 || (h == 0 && (E == 2 || par == 0)))
-      reinterpret_cast<float*>(smem + C::OFF_R)[(par * 2 + (E == 4 ? h : 0)) * BN + row] = d.ratio[r][g];
-  };
+  float f = 1.0f;   // of the group multiplied last
 
-  // ---- fragments ----
-  // (k-step s of a wave is step s of the tile, or with two groups of waves step 2 s + kg)
-  int rd_x[NS], rd_w[NS];
+  // ---- fragments of X: own k-step i is step 2 i + kg of the pair ----
+  const int rd = lrow * 128;
+  auto read = [&](i32x4 (&fr)[MB], int stage, int i) {
+    const int c = 2 * i + kg;   // 16-k step of the pair: chunks 2 (c % 4) and the next of half c / 4
+    const char* at = smem + stage * STAGE + (c >> 2) * (BM * 128) + rd + (((2 * (c & 3) + lhi) ^ swz_a<128>(lrow)) << 4);
 #pragma unroll
-  for (int s = 0; s < NS; ++s) {
-    const int row = lane & 31, chunk = ((KG * s + kg) * 2 + lhi) ^ swz_a<128>(row);
-    rd_x[s] = (wm * WM + row) * 128 + (chunk << 4);
-    rd_w[s] = C::OFF_W + (wn * WN + row) * 128 + (chunk << 4);
-  }
-  f32x16 acc[NB][MB];
+    for (int b = 0; b < MB; ++b) fr[b] = *reinterpret_cast<const i32x4*>(at + b * 32 * 128);
+  };
+  f32x16 acc[MB];
 #pragma unroll
-  for (int a = 0; a < NB; ++a)
+  for (int b = 0; b < MB; ++b) acc[b] = f32x16{};
+
+  Raw raw[2];
+  load_x(xr[1], 0);   // (in the loop's order, so that its waits hold here too)
+  load_x(xr[0], 1);
+  load_w(raw[0], 0);
+  store_x(xr[1], 0, 0);
+  load_x(xr[1], 2);
+  load_w(raw[1], 1);
+  wait_lgkmcnt<0>();
+  barrier_only();
+
+  auto pair_step = [&](auto utag, int P) {   // pair P, P % 2 == u
+    constexpr int u = decltype(utag)::value;
+    // the next pair to the other stage, later ones on their way
+    const Raw now = raw[u];
+    store_x(xr[u], u ^ 1, P + 1);
+    load_x(xr[u], P + 3);
+    load_w(raw[u], P + 2);
+    // the groups' p, z and factors
+    uint32_t pz[E];
+    float ratio[E];
+    const bool begins = E > 1 || begun == 0;
+    if (E == 1 && ++begun == p.span) begun = 0;
 #pragma unroll
-    for (int b = 0; b < MB; ++b) acc[a][b] = f32x16{};
-  // Multiplies the sums by the factors of group g of a k-tile of this parity.
-  auto rescale = [&](int par, int g) {
-    const float* R = reinterpret_cast<const float*>(smem + C::OFF_R) + (par * 2 + g) * BN + wn * WN + 4 * lhi;
-#pragma unroll
-    for (int a = 0; a < NB; ++a) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(R + 32 * a + 8 * c);
+    for (int e = 0; e < E; ++e) {
+      uint32_t sb = now.s[e], zb = now.z[e];
+      asm volatile("" : "+v"(sb), "+v"(zb));   // (or they are narrowed, and waited for, where they are loaded)
+      float pw, fn;
+      w4_split<DT>((uint16_t)sb, pw, fn);
+      pz[e] = w4_pz(pw, zb);
+      ratio[e] = begins ? f * __builtin_amdgcn_rcpf(fn) : 1.0f;
+      f = begins ? fn : f;
+    }
+    i32x4 fr[2][MB];   // (the next step's beside this one's products)
+    read(fr[0], u, 0);
+    w4_for<4>([&](auto itag) {
+      constexpr int i = decltype(itag)::value;
+      if constexpr (i < 3) read(fr[(i + 1) & 1], u, i + 1);
+      constexpr int e = E == 4 ? i : E == 2 ? i / 2 : 0;
+      const i32x4 wf = w4_expand<DT>((uint32_t)now.c[i], pz[e]);
+      if constexpr (E == 4 || (E == 2 && i % 2 == 0) || i == 0) {
 #pragma unroll
         for (int b = 0; b < MB; ++b)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[a][b][4 * c + e] *= v[e];
+          for (int j = 0; j < 16; ++j) acc[b][j] *= ratio[e];
       }
-    }
-  };
-  struct Frag {
-    i32x4 x[MB], w[NB];
-  };
-  auto read = [&](Frag& fr, int t, auto ptag, int s) {
-    constexpr int par = decltype(ptag)::value;
 #pragma unroll
-    for (int a = 0; a < NB; ++a)
-      fr.w[a] = *reinterpret_cast<const i32x4*>(smem + par * C::W_BYTES + rd_w[s] + a * 32 * 128);
-    const char* x = smem + (XS == 2 ? par : t & (XS - 1)) * C::X_BYTES;
-#pragma unroll
-    for (int b = 0; b < MB; ++b) fr.x[b] = *reinterpret_cast<const i32x4*>(x + rd_x[s] + b * 32 * 128);
-  };
-
-  constexpr std::integral_constant<int, 0> p0{};
-  constexpr std::integral_constant<int, 1> p1{};
-  Codes now;   // of the pair being converted
-  copy_w(0);
-#pragma unroll
-  for (int t = 0; t < XS; ++t) {
-    issue_x(t);
-    if (t == 0) store_x(0);
-  }
-  w4_wait_vm<0>();
-  read_w(now, 0);
-  w4_for<2 * RG>([&](auto i) { convert(now, p0, i); });
-  w4_for<2 * RG>([&](auto i) { convert(now, p1, i); });
-  wait_lgkmcnt<0>();
-  barrier_only();
-#pragma unroll
-  for (int d = 1; d <= D; ++d) copy_w(d);
-  Frag fr[2];
-  read(fr[0], 0, p0, 0);
-
-  // One k-step of k-tile t, t % 2 == u: reads of the next step's fragments, a part of the next
-  // k-tile's (in the last step, of the next but one's) conversion, and with SCALE the factors of
-  // group g, all among the products.
-  auto step = [&](auto utag, auto stag, auto scale_tag, int g, int t) {
-    constexpr int u = decltype(utag)::value, s = decltype(stag)::value;
-    constexpr bool last = s == NS - 1, SCALE = decltype(scale_tag)::value;
-    constexpr std::integral_constant<int, u ^ 1> other{};
-    if constexpr (SCALE) rescale(u, g);
-    if constexpr (u == 1 && s == 0) {   // the pair read at the end of the last k-tile makes room
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      copy_w(t / 2 + 1 + D);
-    }
-    constexpr int per = last ? 1 : (2 * RG - 1 + NS - 2) / (NS - 1);
-    if constexpr (last) {
-      wait_lgkmcnt<0>();   // reads of k-tile t, writes of W's t + 1
-      if constexpr (!XD) {
-        store_x(t + 1);
-        wait_lgkmcnt<0>();
-      }
-      // X's t + 1 has landed, and for an even t the codes of the next pair
-      if constexpr (XD) w4_wait_vm<AHEAD + u * NCODE>();
-      else w4_wait_vm<u * NCODE>();
-      if constexpr (u == 0 && D > 1) {
-        // (the first copies have no X between them: all but the last D - 1 pairs)
-        if (t == 0) w4_wait_vm<(D - 1) * NCODE>();
-      }
-      barrier_only();
-      issue_x(t + XS);
-      read(fr[0], t + 1, other, 0);
-      if constexpr (u == 0) read_w(now, t / 2 + 1);   // W's t + 2 begins a pair
-      convert(now, utag, std::integral_constant<int, 0>{});
-    } else {
-      read(fr[(s + 1) & 1], t, utag, s + 1);
-      constexpr int i0 = 1 + s * per, i1 = i0 + per < 2 * RG ? i0 + per : 2 * RG;
-      w4_for<(i1 > i0 ? i1 - i0 : 0)>([&](auto i) { convert(now, other, std::integral_constant<int, i0 + decltype(i)::value>{}); });
-    }
-#pragma unroll
-    for (int i = 0; i < NMMA; ++i)
-      acc[i / MB][i % MB] = Tr<DT>::mma(fr[s & 1].w[i / MB], fr[s & 1].x[i % MB], acc[i / MB][i % MB]);
-    // one product, then a read and a share of the rest (256 x 256: 120 -> 115 us at 3000 x 4096 x
-    // 4096; with the two products a step of the small tiles it costs 2 to 10%)
-    if constexpr (NMMA >= 8) {
-      w4_for<NMMA>([&](auto) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, (MB + NB + NMMA - 1) / NMMA, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, (per * 24 + NMMA - 1) / NMMA, 0);
-      });
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  auto ktile = [&](auto utag, int t) {
-    constexpr int u = decltype(utag)::value;
-    constexpr std::true_type yes{};
-    constexpr std::false_type no{};
-    w4_for<NS>([&](auto stag) {
-      constexpr int s = decltype(stag)::value;
-      // a group's factors, before its first products: with groups of 32, of which each has two steps of
-      // the tile, with 64 every tile, else every other one (1 where no group begins: a branch around
-      // the multiplications would keep them from running among the products)
-      if constexpr (E == 4 && (KG == 2 || s % 2 == 0)) step(utag, stag, yes, KG == 2 ? s : s / 2, t);
-      else if constexpr (s == 0 && (E == 2 || (E == 1 && u == 0))) step(utag, stag, yes, 0, t);
-      else step(utag, stag, no, 0, t);
+      for (int b = 0; b < MB; ++b) acc[b] = Tr<DT>::mma(fr[i & 1][b], wf, acc[b]);
     });
+    wait_lgkmcnt<0>();   // reads of this stage, writes of the other
+    barrier_only();
   };
-  for (int t = 0; t < KT2; t += 2) {
-    ktile(p0, t);
-    ktile(p1, t + 1);
+  int P = 0;
+  for (; P + 1 < KP; P += 2) {
+    pair_step(std::integral_constant<int, 0>{}, P);
+    pair_step(std::integral_constant<int, 1>{}, P + 1);
   }
-  wait_vmcnt<0>();
-  wait_lgkmcnt<0>();
-  // the last groups' f of every row, and the stages to the epilogue
+  if (P < KP) pair_step(std::integral_constant<int, 0>{}, P);
+
+  // ---- the sums of the two waves of the same rows: each finishes half of the tokens ----
 #pragma unroll
-  for (int r = 0; r < RG; ++r)
-    if (q == 0) reinterpret_cast<float*>(smem + C::OFF_R)[(w * RG + r) * 16 + li] = f[r];
-  __syncthreads();
-  rescale(0, 0);
-  if constexpr (KG == 2) {
-    f32x4* sums = reinterpret_cast<f32x4*>(smem + wt * C::EPI) + lane;
-    if (kg == 1) {
+  for (int b = 0; b < MB; ++b)
 #pragma unroll
-      for (int i = 0; i < NMMA; ++i)
+    for (int j = 0; j < 16; ++j) acc[b][j] *= f;
+  constexpr int HB = MB / 2;
+  f32x4* theirs = reinterpret_cast<f32x4*>(smem + ((kg ^ 1) * 4 + wn) * (HB * 4096)) + lane;
+  char* mine = smem + w * (HB * 4096);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const f32x16& v = acc[i / MB][i % MB];
-          sums[(i * 4 + c) * 64] = f32x4{v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]};
-        }
+  for (int b = 0; b < HB; ++b)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      f32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = kg ? acc[b][4 * c + e] : acc[HB + b][4 * c + e];
+      theirs[(b * 4 + c) * 64] = v;
     }
-    __syncthreads();
-    if (kg == 1) return;
+  __syncthreads();
+  f32x16 sum[HB];
 #pragma unroll
-    for (int i = 0; i < NMMA; ++i)
+  for (int b = 0; b < HB; ++b)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const f32x4 v = sums[(i * 4 + c) * 64];
+    for (int c = 0; c < 4; ++c) {
+      const f32x4 v = reinterpret_cast<const f32x4*>(mine)[(b * 4 + c) * 64 + lane];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i / MB][i % MB][4 * c + e] += v[e];
-      }
-    __builtin_amdgcn_wave_barrier();
-  }
-  w4_tile_epilogue<DT, GATED, C>(p, acc, m0 + wm * WM, n0 + wn * (GATED ? WN / 2 : WN), lane, smem + wt * C::EPI);
+      for (int e = 0; e < 4; ++e) sum[b][4 * c + e] = (kg ? acc[HB + b][4 * c + e] : acc[b][4 * c + e]) + v[e];
+    }
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int b = 0; b < HB; ++b)
+    w4_block<DT, GATED>(p, sum[b], m0 + (kg * HB + b) * 32, n0, lane, mine);
 }
 
 }  // namespace gek

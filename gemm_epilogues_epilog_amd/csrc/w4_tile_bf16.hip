@@ -2,5 +2,5 @@
 #include "w4_tile_inst.hpp"
 
 namespace gek {
-const void* w4_tile_bf16(int cfg, bool gated, int64_t group, bool xd) { return w4_tile_pick<BF16>(cfg, gated, group, xd); }
+const void* w4_tile_bf16(int cfg, bool gated, int64_t group) { return w4_tile_pick<BF16>(cfg, gated, group); }
 }  // namespace gek

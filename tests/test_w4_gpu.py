@@ -220,6 +220,30 @@ def test_tiles(gpu, m, n, k, group, dtype):
     check_gated(*make(m, n // 2, k, group, dtype, m + n, gated=True), dtype, [("SILU", True), ("RELU", False)])
 
 
+# k that ends in its first chunk of eight, at its end, just past it and inside a later one; fewer than
+# eight; the middle and small tiles with every size of group
+ENDS = [(1000, 4130, 9, 64), (1290, 8300, 8, 64), (900, 5000, 135, 64), (257, 4099, 8, 32), (300, 2000, 257, 32), (257, 4099, 15, 128),
+        (700, 1500, 127, 32), (2000, 700, 7, 32), (300, 264, 1, 64)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k,group", ENDS)
+def test_ends_of_k(gpu, m, n, k, group, dtype):
+    check(*make(m, n, k, group, dtype, m + n + k), dtype, [("BIAS", "f32")])
+    check_gated(*make(m, n // 2, k, group, dtype, m + n, gated=True), dtype, [("SILU", True)])
+
+
+@pytest.mark.parametrize("m,n,k", [(300, 1000, 260), (1030, 5000, 133), (7, 100, 260)])
+def test_nothing_past_a_row(gpu, m, n, k):
+    """X inside a tensor of NaN: nothing beside its rows reaches a result."""
+    x, W, b, full, mags = make(m, n, k, 64, "bf16", 9)
+    buf = torch.full((m * k + 64,), float("nan"), device="cuda", dtype=torch.bfloat16)
+    for at in (0, 1, 24):
+        y = buf[at:at + m * k].view(m, k)
+        y.copy_(x)
+        check(y, W, b, full, mags, "bf16", [("BIAS", "f32")], at)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("m", [1, 20, 100, 600, 2100])
 @pytest.mark.parametrize("group", [32, 128])
