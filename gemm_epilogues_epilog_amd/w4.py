@@ -19,6 +19,7 @@ from .gated import _bias, _gate, _out, _rows2
 from .mx import _NAME, _TORCH, _check, _empty, _stream, on_device
 
 _HALF = (torch.float16, torch.bfloat16)
+_MAX_DIM = 1 << 20   # of a half's rows, of k and of a group
 _EPILOGS = ("NONE", "BIAS", "RELU_BIAS", "GELU_BIAS")
 
 
@@ -33,7 +34,7 @@ class W4Tensor:
     """A (rows, k) weight in 4 bits: uint8 codes, 16-bit scales and uint8 zeros in the library's
     layout. gated: rows is 2 n, the gate's rows and then the up projection's."""
 
-    __slots__ = ("rows", "k", "group", "gated", "dtype", "device", "codes", "scales", "zeros")
+    __slots__ = ("rows", "k", "group", "gated", "dtype", "device", "ptrs", "_parts", "_buf")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, rows: int, k: int,
                  group: int = 128, gated: bool = False):
@@ -43,46 +44,61 @@ class W4Tensor:
                                      ("zeros", zeros, (torch.uint8,), sc)):
             if t.dtype not in types or not t.is_contiguous() or t.numel() != size or t.device != codes.device:
                 raise ValueError(f"{name} must be {size} contiguous {types[0]} values on {codes.device}")
-        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self._parts, self._buf = (codes, scales, zeros), codes
+        self.ptrs = codes.data_ptr(), scales.data_ptr(), zeros.data_ptr()
         self.dtype, self.device = scales.dtype, codes.device
 
     @staticmethod
     def sizes(rows: int, k: int, group: int, gated: bool):
         """(code bytes, scales) of a weight, padding included."""
-        L, halves = load(), 2 if gated else 1
-        sc = L.gemm_epilog_w4_scale_count(rows, k, group, halves)
-        if not sc:
+        halves = 2 if gated else 1
+        if not (1 <= rows <= _MAX_DIM * halves and rows % halves == 0 and 1 <= k <= _MAX_DIM and group <= _MAX_DIM):
             raise ValueError(f"a weight of {rows} x {k} with groups of {group} is not supported")
-        return L.gemm_epilog_w4_code_bytes(rows, k, halves), sc
+        rg = halves * -(-(rows // halves) // 16)
+        return rg * -(-k // 128) * 1024, rg * -(-k // group) * 16
 
     @classmethod
     def empty(cls, rows: int, k: int, group: int = 128, gated: bool = False, dtype=torch.bfloat16, device="cuda",
               stream=None):
-        """A weight to be written."""
+        """A weight to be written: codes, scales and zeros in one allocation."""
         group = _group_ok(group)
         if dtype not in _HALF:
             raise ValueError("the scales are f16 or bf16")
         cb, sc = cls.sizes(rows, k, group, gated)
         q = cls.__new__(cls)
         q.rows, q.k, q.group, q.gated, q.dtype = int(rows), int(k), group, bool(gated), dtype
-        q.codes = _empty(cb, torch.uint8, device, stream)
-        q.scales = _empty(sc, dtype, device, stream)
-        q.zeros = _empty(sc, torch.uint8, device, stream)
-        q.device = q.codes.device
+        q._buf, q._parts = _empty(cb + 3 * sc, torch.uint8, device, stream), None
+        at = q._buf.data_ptr()
+        q.device, q.ptrs = q._buf.device, (at, at + cb, at + cb + 2 * sc)
         return q
+
+    def _views(self):
+        if self._parts is None:
+            cb, sc = self.sizes(self.rows, self.k, self.group, self.gated)
+            self._parts = self._buf[:cb], self._buf[cb:cb + 2 * sc].view(self.dtype), self._buf[cb + 2 * sc:]
+        return self._parts
+
+    @property
+    def codes(self) -> torch.Tensor:
+        return self._views()[0]
+
+    @property
+    def scales(self) -> torch.Tensor:
+        return self._views()[1]
+
+    @property
+    def zeros(self) -> torch.Tensor:
+        return self._views()[2]
 
     @property
     def shape(self):
         return (self.rows, self.k)
 
-    def _ptrs(self):
-        return self.codes.data_ptr(), self.scales.data_ptr(), self.zeros.data_ptr()
-
 
 def _weight(q, device=None) -> W4Tensor:
     if not isinstance(q, W4Tensor):
         raise ValueError("the weight must be a W4Tensor")
-    on_device(q.codes, "the weight", device)
+    on_device(q._buf, "the weight", device)
     return q
 
 
@@ -110,7 +126,7 @@ def w4_quantize(w: torch.Tensor, group: int = 128, symmetric: bool = False, gate
     group = _group_ok(group)
     q = _target(out, rows, k, group, bool(gated), t, w.device, stream)
     _check(load().gemm_epilog_w4_quantize(rows, k, DTYPES[_NAME[w.dtype]], w.data_ptr(), w.stride(0) if rows > 1 else k,
-                                          group, 2 if gated else 1, int(bool(symmetric)), DTYPES[_NAME[t]], *q._ptrs(),
+                                          group, 2 if gated else 1, int(bool(symmetric)), DTYPES[_NAME[t]], *q.ptrs,
                                           _stream(stream, w.device)), "gemm_epilog_w4_quantize")
     return q
 
@@ -136,7 +152,7 @@ def w4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Ten
             raise ValueError(f"{name} must be a contiguous ({rows}, {groups}) tensor of {types}")
     q = _target(out, rows, k, group, bool(gated), scales.dtype, codes.device, stream)
     _check(load().gemm_epilog_w4_pack(rows, k, group, 2 if gated else 1, codes.data_ptr(), scales.data_ptr(),
-                                      None if zeros is None else zeros.data_ptr(), *q._ptrs(),
+                                      None if zeros is None else zeros.data_ptr(), *q.ptrs,
                                       _stream(stream, codes.device)), "gemm_epilog_w4_pack")
     return q
 
@@ -148,7 +164,7 @@ def w4_dequantize(q: W4Tensor, dtype: Optional[str] = None, out: Optional[torch.
     if t is None:
         raise ValueError(f"unknown type {dtype!r}")
     v = _out(out, "out", (q.rows, q.k), t, q.device, stream)
-    _check(load().gemm_epilog_w4_dequantize(q.rows, q.k, q.group, 2 if q.gated else 1, DTYPES[_NAME[q.dtype]], *q._ptrs(),
+    _check(load().gemm_epilog_w4_dequantize(q.rows, q.k, q.group, 2 if q.gated else 1, DTYPES[_NAME[q.dtype]], *q.ptrs,
                                             DTYPES[_NAME[t]], v.data_ptr(), q.k, _stream(stream, q.device)),
            "gemm_epilog_w4_dequantize")
     return v
@@ -179,7 +195,7 @@ def w4_matmul(x: torch.Tensor, W: W4Tensor, bias: Optional[torch.Tensor] = None,
     o = out_dtype or name
     D = _out(out, "out", (m, n), _TORCH[o], dev, stream)
     _check(load().gemm_epilog_w4_matmul(m, n, k, W.group, DTYPES[name], DTYPES[o], EPILOG[epilog], x.data_ptr(),
-                                        *W._ptrs(), bp, vec, D.data_ptr(), _stream(stream, dev)), "gemm_epilog_w4_matmul")
+                                        *W.ptrs, bp, vec, D.data_ptr(), _stream(stream, dev)), "gemm_epilog_w4_matmul")
     return D
 
 
@@ -190,6 +206,6 @@ def w4_gated(x: torch.Tensor, W: W4Tensor, bias: Optional[torch.Tensor] = None, 
     a, n, dev = _gate(act), W.rows // 2, x.device
     bp, vec = _bias(bias, 2 * n, x.dtype, dev)
     h = _out(out, "out", (m, n), x.dtype, dev, stream)
-    _check(load().gemm_epilog_w4_gated(m, n, k, W.group, DTYPES[_NAME[x.dtype]], a, x.data_ptr(), *W._ptrs(), bp, vec,
+    _check(load().gemm_epilog_w4_gated(m, n, k, W.group, DTYPES[_NAME[x.dtype]], a, x.data_ptr(), *W.ptrs, bp, vec,
                                        h.data_ptr(), _stream(stream, dev)), "gemm_epilog_w4_gated")
     return h
