@@ -106,17 +106,18 @@ __global__ __launch_bounds__(256) void colsum_kernel(const void* x, int64_t m, i
 }
 
 template <int DT, int OUT, int LAY>
-const void* gen_of(bool large) {
-  return large ? reinterpret_cast<const void*>(&gen_kernel<DT, OUT, LAY, 128, 128, 64, 1>)
-               : reinterpret_cast<const void*>(&gen_kernel<DT, OUT, LAY, 64, 64, 32, 2>);
+const void* gen_of(bool large, bool narrow) {
+  return narrow  ? reinterpret_cast<const void*>(&gen_kernel<DT, OUT, LAY, 64, 64, 32, 2, true>)
+         : large ? reinterpret_cast<const void*>(&gen_kernel<DT, OUT, LAY, 128, 128, 64, 1, false>)
+                 : reinterpret_cast<const void*>(&gen_kernel<DT, OUT, LAY, 64, 64, 32, 2, false>);
 }
 template <int DT>
-const void* gen_kernel_of(int lay, bool f32_out, bool large) {
+const void* gen_kernel_of(int lay, bool f32_out, bool large, bool narrow) {
   switch (lay) {
-    case 0: return f32_out ? gen_of<DT, F32, 0>(large) : gen_of<DT, DT, 0>(large);
-    case 1: return f32_out ? gen_of<DT, F32, 1>(large) : gen_of<DT, DT, 1>(large);
-    case 2: return f32_out ? gen_of<DT, F32, 2>(large) : gen_of<DT, DT, 2>(large);
-    default: return gen_of<DT, DT, 6>(large);
+    case 0: return f32_out ? gen_of<DT, F32, 0>(large, narrow) : gen_of<DT, DT, 0>(large, narrow);
+    case 1: return f32_out ? gen_of<DT, F32, 1>(large, narrow) : gen_of<DT, DT, 1>(large, narrow);
+    case 2: return f32_out ? gen_of<DT, F32, 2>(large, narrow) : gen_of<DT, DT, 2>(large, narrow);
+    default: return gen_of<DT, DT, 6>(large, narrow);
   }
 }
 
@@ -144,13 +145,15 @@ hipError_t general(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, cons
   a.act = act;
   // the large tile where it gives every compute unit one
   const auto tiles = [&](int t) { return (M + t - 1) / t * ((N + (lay == 6 ? t / 2 : t) - 1) / (lay == 6 ? t / 2 : t)); };
-  const bool large = gegh::general_large(M, lay == 6 ? 2 * N : N, cus);
+  const int64_t row_a = lay & 1 ? M : K, row_b = lay & 2 ? K : N;
+  const bool narrow = (row_a < row_b ? row_a : row_b) * (dt == GE_F32 ? 4 : 2) < 16;
+  const bool large = !narrow && gegh::general_large(M, lay == 6 ? 2 * N : N, cus);
   const int t = large ? 128 : 64;
   a.tiles_m = (int)((M + t - 1) / t);
   a.tiles_n = (int)(tiles(t) / a.tiles_m);
-  const void* fn = dt == GE_F32   ? gen_kernel_of<F32>(lay, f32_out, large)
-                   : dt == GE_F16 ? gen_kernel_of<F16>(lay, f32_out, large)
-                                  : gen_kernel_of<BF16>(lay, f32_out, large);
+  const void* fn = dt == GE_F32   ? gen_kernel_of<F32>(lay, f32_out, large, narrow)
+                   : dt == GE_F16 ? gen_kernel_of<F16>(lay, f32_out, large, narrow)
+                                  : gen_kernel_of<BF16>(lay, f32_out, large, narrow);
   void* params[] = {&a};
   return launch(fn, dim3((unsigned)tiles(t), (unsigned)splits), 256, params, s);
 }

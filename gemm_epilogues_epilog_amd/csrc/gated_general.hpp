@@ -73,74 +73,105 @@ __device__ __forceinline__ i32x4 load_end(const char* row, int64_t pos, int64_t 
 // One operand's tile: MN rows (or columns, mn-major) by BK k values, NT threads.
 // HALVES (k-major): tile rows come from two halves of the stored rows, alternating by HW:
 // HW rows of the first half, the same HW of the second, and so on.
-template <int ES, int MN, bool KMAJ, int NT, int HW = 0>
+// Every load happens, at the row's last 16 bytes where a chunk would pass its end, and is moved into
+// place when it is stored: a load that may not happen would turn the waits for the loads before it
+// into waits for all that are on their way. NARROW: rows of fewer than 16 bytes, element by element.
+template <int ES, int MN, bool KMAJ, int NT, bool NARROW, int HW = 0>
 struct GenOperand {
   static constexpr int E = 16 / ES, BK = kRowBytes / ES;
   static constexpr int LD = MN * 8 / NT;   // k-major: 16-byte chunks per thread
   static constexpr int NB = MN / E, R = NB * BK / NT;   // mn-major: one block of R k-rows by E columns per thread
   static_assert(KMAJ ? MN * 8 % NT == 0 : (R == 2 || R == 4) && NB * (BK / R) == NT, "tile split");
   static constexpr int REGS = KMAJ ? LD : R;
-  i32x4 reg[REGS];
+
+  const char* row[KMAJ ? LD : 1];   // k-major: this thread's rows; mn-major: its columns' first k
+  int64_t ld, kdim;                 // (ld: bytes)
+  int64_t col, len;                 // mn-major: first column and the number of columns
+  struct Regs {
+    i32x4 v[REGS];
+  };
 
   __device__ static __forceinline__ int swz(int row) { return (row ^ (row >> 3)) & 7; }
 
-  // k0: first k of the tile; mn0: first row / column; mndim, kdim the extents.
-  __device__ __forceinline__ void load(const char* X, int64_t ld, int64_t mn0, int64_t mndim, int64_t k0, int64_t kdim,
-                                       int t) {
-    const bool tail = k0 + BK > kdim;
+  // mn0: first row / column; mndim, kdim the extents.
+  __device__ __forceinline__ GenOperand(const char* X, int64_t ld_, int64_t mn0, int64_t mndim, int64_t kdim_, int t)
+      : ld(ld_ * ES), kdim(kdim_), col(mn0 + t % NB * E), len(mndim) {
     if constexpr (KMAJ) {
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
-        const int row = (t + i * NT) >> 3;
+        const int r = (t + i * NT) >> 3;
         int64_t at;
         if constexpr (HW > 0) {
-          const int64_t c = mn0 + row / (2 * HW) * HW + row % HW;
-          at = (c < mndim ? c : mndim - 1) + (row / HW % 2 ? mndim : 0);
+          const int64_t c = mn0 + r / (2 * HW) * HW + r % HW;
+          at = (c < mndim ? c : mndim - 1) + (r / HW % 2 ? mndim : 0);
         } else {
-          at = mn0 + row < mndim ? mn0 + row : mndim - 1;   // (rows past the last one are not stored)
+          at = mn0 + r < mndim ? mn0 + r : mndim - 1;   // (rows past the last one are not stored)
         }
-        const char* p = X + at * ld * ES;
-        const int64_t pos = k0 + (t & 7) * E;
-        reg[i] = tail ? load_end<ES>(p, pos, kdim) : load16(p + pos * ES);
+        row[i] = X + at * ld;
       }
     } else {
-      const int64_t pos = mn0 + t % NB * E, kr = k0 + t / NB * R;
-      const bool edge = tail || mn0 + MN > mndim;
+      row[0] = NARROW ? X : X + (col < mndim - E ? col : mndim - E) * ES;
+    }
+  }
+  // Tile kt (of all k).
+  __device__ __forceinline__ void load(Regs& reg, int64_t kt, int t) const {
+    if constexpr (KMAJ) {
+      const int64_t pos = kt * BK + (t & 7) * E;
+#pragma unroll
+      for (int i = 0; i < LD; ++i)
+        reg.v[i] = NARROW ? load_end<ES>(row[i], pos, kdim) : load16(row[i] + (pos < kdim - E ? pos : kdim - E) * ES);
+    } else {
+      const int64_t kr = kt * BK + t / NB * R;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if (!edge) {
-          reg[r] = load16(X + ((kr + r) * ld + pos) * ES);
-        } else {
-          const int64_t kk = kr + r < kdim ? kr + r : kdim - 1;
-          const i32x4 v = load_end<ES>(X + kk * ld * ES, pos, mndim);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) reg[r][e] = kr + r < kdim ? v[e] : 0;
-        }
+        const char* p = row[0] + (kr + r < kdim ? kr + r : kdim - 1) * ld;
+        reg.v[r] = NARROW ? load_end<ES>(p, col, len) : load16(p);
       }
     }
   }
-  __device__ __forceinline__ void store(char* lds, int t) const {
+  __device__ __forceinline__ void store(Regs& reg, char* lds, int64_t kt, int t) const {
     if constexpr (KMAJ) {
+      if constexpr (!NARROW) {
+        if ((kt + 1) * BK > kdim) {
+          const int64_t over = kt * BK + (t & 7) * E + E - kdim;
+#pragma unroll
+          for (int i = 0; i < LD; ++i) reg.v[i] = shift_down<ES>(reg.v[i], (int)(over < 0 ? 0 : over < E ? over : E));
+        }
+      }
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
-        const int row = (t + i * NT) >> 3;
-        *reinterpret_cast<i32x4*>(lds + row * kRowBytes + (((t & 7) ^ swz(row)) << 4)) = reg[i];
+        const int r = (t + i * NT) >> 3;
+        *reinterpret_cast<i32x4*>(lds + r * kRowBytes + (((t & 7) ^ swz(r)) << 4)) = reg.v[i];
       }
     } else {
+      const int64_t k0 = kt * BK + t / NB * R;
+      if constexpr (!NARROW) {
+        if (col - t % NB * E + MN > len) {
+          const int64_t over = col + E - len;
+#pragma unroll
+          for (int r = 0; r < R; ++r) reg.v[r] = shift_down<ES>(reg.v[r], (int)(over < 0 ? 0 : over < E ? over : E));
+        }
+      }
+      if ((kt + 1) * BK > kdim) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) reg.v[r][e] = k0 + r < kdim ? reg.v[r][e] : 0;
+      }
       const int kb = t / NB * R * ES, chunk = kb >> 4, within = kb & 15;
 #pragma unroll
       for (int c = 0; c < E; ++c) {
-        const int row = t % NB * E + c;
-        char* dst = lds + row * kRowBytes + ((chunk ^ swz(row)) << 4) + within;
+        const int r = t % NB * E + c;
+        char* dst = lds + r * kRowBytes + ((chunk ^ swz(r)) << 4) + within;
         if constexpr (ES == 4) {
-          if constexpr (R == 4) *reinterpret_cast<i32x4*>(dst) = i32x4{reg[0][c], reg[1][c], reg[2][c], reg[3][c]};
-          else *reinterpret_cast<i32x2*>(dst) = i32x2{reg[0][c], reg[1][c]};
+          if constexpr (R == 4) *reinterpret_cast<i32x4*>(dst) = i32x4{reg.v[0][c], reg.v[1][c], reg.v[2][c], reg.v[3][c]};
+          else *reinterpret_cast<i32x2*>(dst) = i32x2{reg.v[0][c], reg.v[1][c]};
         } else {
           const uint32_t sel = (c & 1) ? 0x07060302u : 0x05040100u;
-          const int lo = (int)__builtin_amdgcn_perm((uint32_t)reg[1][c >> 1], (uint32_t)reg[0][c >> 1], sel);
+          const int lo = (int)__builtin_amdgcn_perm((uint32_t)reg.v[1][c >> 1], (uint32_t)reg.v[0][c >> 1], sel);
           if constexpr (R == 4)
             *reinterpret_cast<i32x2*>(dst) =
-                i32x2{lo, (int)__builtin_amdgcn_perm((uint32_t)reg[3][c >> 1], (uint32_t)reg[2][c >> 1], sel)};
+                i32x2{lo, (int)__builtin_amdgcn_perm((uint32_t)reg.v[3][c >> 1], (uint32_t)reg.v[2][c >> 1], sel)};
           else
             *reinterpret_cast<int*>(dst) = lo;
         }
@@ -171,7 +202,7 @@ __device__ __forceinline__ void store4(void* p, int64_t i, int64_t n, const floa
 // are added through LDS): the 64 x 64 tile has two, so that the few tiles of a small product still
 // put a wave on every SIMD. gridDim.y workgroups share the k loop (not gated), each with its own D.
 // Two k-tiles are on their way in registers while a third is multiplied.
-template <int DT, int OUT, int LAY, int BM, int BN, int WM, int KG>
+template <int DT, int OUT, int LAY, int BM, int BN, int WM, int KG, bool NARROW>
 __global__ __launch_bounds__((BM / WM) * (BN / 64) * KG * 64, 2) void gen_kernel(GenArgs p) {
   using T = Tr<DT>;
   constexpr bool TA = (LAY & 1) != 0, TB = (LAY & 2) != 0, GATED = (LAY & 4) != 0;
@@ -179,11 +210,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * KG * 64, 2) void gen_kernel
   constexpr int ES = T::es, BK = kRowBytes / ES, STAGE = (BM + BN) * kRowBytes, NS = 4 / KG;
   constexpr bool FINE = DT == F32;
   __shared__ __attribute__((aligned(16))) char lds[2 * STAGE];
-  using OA = GenOperand<ES, BM, !TA, NT>;
-  using OB = GenOperand<ES, BN, TB, NT, GATED ? 32 : 0>;
+  using OA = GenOperand<ES, BM, !TA, NT, NARROW>;
+  using OB = GenOperand<ES, BN, TB, NT, NARROW, GATED ? 32 : 0>;
   struct Tile {
-    OA a;
-    OB b;
+    typename OA::Regs a;
+    typename OB::Regs b;
   } in[2];
 
   const int pos = xcd_remap(blockIdx.x, p.tiles_m * p.tiles_n);
@@ -192,8 +223,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * KG * 64, 2) void gen_kernel
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6), kg = w / WAVES, wt = w % WAVES;
   const int wm = wt % WAVES_M, wn = wt / WAVES_M, lrow = lane & 31, lhi = lane >> 5;
-  const char* A = static_cast<const char*>(p.A);
-  const char* B = static_cast<const char*>(p.B);
+  const OA oa(static_cast<const char*>(p.A), p.lda, m0, p.m, p.k, t);
+  const OB ob(static_cast<const char*>(p.B), p.ldb, n0, p.n, p.k, t);
   const int64_t KTA = (p.k + BK - 1) / BK;
   const int64_t kb = KTA * blockIdx.y / gridDim.y, KT = KTA * (blockIdx.y + 1) / gridDim.y - kb;
 
@@ -203,17 +234,19 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * KG * 64, 2) void gen_kernel
 #pragma unroll
     for (int b = 0; b < MB; ++b) acc[a][b] = f32x16{};
 
-  const auto load = [&](Tile& v, int64_t kt) {
-    v.a.load(A, p.lda, m0, p.m, (kb + kt) * BK, p.k, t);
-    v.b.load(B, p.ldb, n0, p.n, (kb + kt) * BK, p.k, t);
+  const auto load = [&](Tile& v, int64_t kt) {   // (past the last tile the last one again)
+    const int64_t at = kb + (kt < KT ? kt : KT - 1);
+    oa.load(v.a, at, t);
+    ob.load(v.b, at, t);
   };
-  const auto store = [&](const Tile& v, int stage) {
-    v.a.store(lds + stage * STAGE, t);
-    v.b.store(lds + stage * STAGE + BM * kRowBytes, t);
+  const auto store = [&](Tile& v, int64_t kt, int stage) {
+    oa.store(v.a, lds + stage * STAGE, kb + kt, t);
+    ob.store(v.b, lds + stage * STAGE + BM * kRowBytes, kb + kt, t);
   };
   const auto tile = [&](auto utag, int64_t kt) {   // kt % 2 == u: in stage u; its successor is in in[u ^ 1]
     constexpr int u = decltype(utag)::value;
-    if (kt + 2 < KT) load(in[u], kt + 2);
+    load(in[u], kt + 2);
+    __builtin_amdgcn_sched_barrier(0);   // (the loads first)
     const char* sA = lds + u * STAGE + (wm * WM + lrow) * kRowBytes;
     const char* sB = lds + u * STAGE + (BM + wn * WN + lrow) * kRowBytes;
 #pragma unroll
@@ -232,18 +265,20 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * KG * 64, 2) void gen_kernel
 #pragma unroll
         for (int b = 0; b < MB; ++b) acc[a][b] = T::mma(bf[a], af[b], acc[a][b]);
     }
-    if (kt + 1 < KT) store(in[u ^ 1], u ^ 1);
+    store(in[u ^ 1], kt + 1, u ^ 1);   // (past the last tile for nobody)
     __syncthreads();
   };
   if (KT > 0) {   // (a product over no tokens is zero)
     load(in[0], 0);
-    if (KT > 1) load(in[1], 1);
-    store(in[0], 0);
-  }
-  __syncthreads();
-  for (int64_t kt = 0; kt < KT; kt += 2) {
-    tile(std::integral_constant<int, 0>{}, kt);
-    if (kt + 1 < KT) tile(std::integral_constant<int, 1>{}, kt + 1);
+    load(in[1], 1);
+    store(in[0], 0, 0);
+    __syncthreads();
+    int64_t kt = 0;
+    for (; kt + 1 < KT; kt += 2) {
+      tile(std::integral_constant<int, 0>{}, kt);
+      tile(std::integral_constant<int, 1>{}, kt + 1);
+    }
+    if (kt < KT) tile(std::integral_constant<int, 0>{}, kt);
   }
   if constexpr (KG == 2) {
     static_assert(WAVES * MB * NB * 4096 <= 2 * STAGE, "sums of the second group of waves");
@@ -268,7 +303,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * KG * 64, 2) void gen_kernel
         for (int e = 0; e < 4; ++e) acc[i / MB][i % MB][4 * c + e] += v[e];
       }
   }
-  char* const D = static_cast<char*>(p.D) + (int64_t)blockIdx.y * p.m * p.ldd * Tr<OUT>::es;
+  char* const out = static_cast<char*>(p.D) + (int64_t)blockIdx.y * p.m * p.ldd * Tr<OUT>::es;
 
   // lane: row m0 + wm WM + 32 b + l % 32; register r: column 8 (r / 4) + 4 (l / 32) + r % 4 of a block
 #pragma unroll
@@ -295,7 +330,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * KG * 64, 2) void gen_kernel
 #pragma unroll
           for (int e = 0; e < 4; ++e) hv[e] = gate_act<decltype(act)::value, FINE>(gv[e]) * uv[e];
         });
-        store4<OUT>(D, row * p.ldd + col, left, hv);
+        store4<OUT>(out, row * p.ldd + col, left, hv);
         if (p.Z) {
           store4<OUT>(p.Z, row * 2 * p.n + col, left, gv);
           store4<OUT>(p.Z, row * 2 * p.n + p.n + col, left, uv);
@@ -308,7 +343,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * KG * 64, 2) void gen_kernel
           float v[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = acc[a][b][4 * g + e];
-          store4<OUT>(D, row * p.ldd + col, left, v);
+          store4<OUT>(out, row * p.ldd + col, left, v);
         }
       }
     }

@@ -106,21 +106,24 @@ ge_status_t gated_layout(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool ba
 // 4, then W once per block of tokens and X, which every 16 rows read for themselves, at 6 TB/s
 // together (1 token 35 and 22 us, 32 tokens 63 and 40). The 128 x 128 tiles: 3, then W at 4.2 TB/s
 // or half a microsecond per k-tile and round of workgroups, whichever is longer (43 to 49, 79 to
-// 91, 12); the general kernel 1.4 per 128 bytes of k and round (99).
+// 91, 12); the general kernel 0.9 per 128 bytes of k and round in fp32 and 0.6 in 16 bits (333
+// tokens by 2 x 1101 x 743: 22 and 9).
 bool skinny(int64_t m, int64_t rows, int64_t k, ge_dtype_t dt, bool gated, int cus) {
   if (m <= 16) return true;
   if (m > 65535) return false;   // (its grid, by far)
   const double es = dt == GE_F32 ? 4 : 2, w = (double)rows * k * es;
   const int64_t step = m <= 32 ? 32 : 64, blocks = cdiv(m, step), groups = cdiv(gated ? rows / 2 : rows, 16);
   const double share = std::min(1.0, (double)(groups * blocks) / cus);
-  // (rows that are not whole 16-byte chunks read at less than half the rate)
-  const double rate = (int64_t)(k * es) % 16 == 0 ? 6e6 : 2.6e6;
-  const double few = 4.0 + ((double)blocks * w + (double)(groups * blocks * step) * k * es) / rate / share;
+  // (rows that are not whole 16-byte chunks: less than half the rate, and a quarter, but half of it
+  // with few workgroups too: 64 tokens by 1101 x 743, fp32 13 and bf16 13)
+  const bool chunks = (int64_t)(k * es) % 16 == 0;
+  const double rate = (chunks ? 6e6 : dt == GE_F32 ? 2.6e6 : 1.6e6) * (chunks ? share : std::max(share, 0.5));
+  const double few = 4.0 + ((double)blocks * w + (double)(groups * blocks * step) * k * es) / rate;
   double tiles;
   if (fast_shape(m, rows, k, dt, 2)) {
     tiles = 3.0 + std::max(w / 4.2e6, (double)(cdiv(cdiv(m, 128) * cdiv(rows, 128), cus) * cdiv(k, 64)) * 0.5);
   } else {
-    tiles = 3.0 + (double)(cdiv(cdiv(m, 64) * cdiv(rows, 64), 2 * cus) * cdiv((int64_t)(k * es), 128)) * 1.4;
+    tiles = 3.0 + (double)(cdiv(cdiv(m, 64) * cdiv(rows, 64), 2 * cus) * cdiv((int64_t)(k * es), 128)) * (dt == GE_F32 ? 0.9 : 0.6);
   }
   return few < tiles;
 }
