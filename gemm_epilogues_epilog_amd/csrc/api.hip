@@ -239,7 +239,7 @@ ge_status_t current_device(int* cus) {
 }
 
 ge_status_t run_product(int64_t m, int n, int k, ge_dtype_t dt, const geh::Layout& L, const void* A, const void* B,
-                        void* D, char* ws, hipStream_t s) {
+                        void* D, char* ws, bool cleared, hipStream_t s) {
   ge_plan h;
   h.m = m;
   h.n = n;
@@ -251,7 +251,7 @@ ge_status_t run_product(int64_t m, int n, int k, ge_dtype_t dt, const geh::Layou
   if (!h.gemm) return GE_ERR_NOT_SUPPORTED;
   h.ws = ws;
   h.spin_limit = kSkSpinDefault;
-  if (L.sk_wgs) {
+  if (L.sk_wgs && !cleared) {
     uint32_t* words = reinterpret_cast<uint32_t*>(ws + L.off_sk_flag);
     int nw = gek::kSkFlagWords;
     void* params[] = {&words, &nw};

@@ -158,14 +158,17 @@ hipError_t general(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, cons
   return launch(fn, dim3((unsigned)tiles(t), (unsigned)splits), 256, params, s);
 }
 
-// D (M, N) of type dt = A . B; `ws` for the k loop's split.
+bool fast_product(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, const void* A, const void* B, const void* D) {
+  return K > 0 && gegh::fast_shape(M, N, K, dt, lay) && gegh::aligned(A, 16) && gegh::aligned(B, 16) && gegh::aligned(D, 16);
+}
+
+// D (M, N) of type dt = A . B; `ws` for the k loop's split, its flags cleared already or not.
 ge_status_t product(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, const void* A, const void* B, void* D,
-                    char* ws, size_t ws_bytes, int cus, hipStream_t s) {
-  if (K > 0 && gegh::fast_shape(M, N, K, dt, lay) && gegh::aligned(A, 16) && gegh::aligned(B, 16) &&
-      gegh::aligned(D, 16)) {
+                    char* ws, size_t ws_bytes, bool cleared, int cus, hipStream_t s) {
+  if (fast_product(M, N, K, dt, lay, A, B, D)) {
     geh::Layout L;
     if (ge_status_t st = gegh::fast_layout(M, N, K, dt, lay, cus, lay ? 0 : ws_bytes, &L); st != GE_OK) return st;
-    return gei::run_product(M, (int)N, (int)K, dt, L, A, B, D, ws, s);
+    return gei::run_product(M, (int)N, (int)K, dt, L, A, B, D, ws, cleared, s);
   }
   const int splits = gegh::general_splits(M, N, K, dt, ws_bytes);
   if (splits == 1)
@@ -176,8 +179,8 @@ ge_status_t product(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, con
 
 // The tile kernels with the gated epilogues: H (and Z) of X and W, or dZ of dY, Wd and Z.
 ge_status_t gated_tiles(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool backward, int act, const void* A,
-                        const void* B, const void* bias, int vec, const void* z, void* D, void* z_out, int cus,
-                        hipStream_t s) {
+                        const void* B, const void* bias, int vec, const void* z, void* D, void* z_out, uint32_t* clear,
+                        int cus, hipStream_t s) {
   geh::Layout L;
   if (ge_status_t st = gegh::gated_layout(m, n, k, dt, backward, cus, &L); st != GE_OK) return st;
   Args a = {};
@@ -197,6 +200,7 @@ ge_status_t gated_tiles(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool bac
   a.act = act;
   a.z = z;
   a.z_out = z_out;
+  a.clear = clear;
   return get_launch_gated((int)dt, backward, L.cfg)(a, L.tiles_m * L.tiles_n, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
 }
 
@@ -238,7 +242,7 @@ ge_status_t gemm_epilog_gated_forward(int64_t m, int64_t n, int64_t k, ge_dtype_
                : GE_ERR_HIP;
   if (gegh::fast_shape(m, n, k, dt, 2) && gegh::aligned(x, 16) && gegh::aligned(w, 16) && gegh::aligned(h, 16) &&
       gegh::aligned(z, 16))
-    return gek::gated_tiles(m, n, k, dt, false, (int)act, x, w, bias, (int)vec, nullptr, h, z, cus, s);
+    return gek::gated_tiles(m, n, k, dt, false, (int)act, x, w, bias, (int)vec, nullptr, h, z, nullptr, cus, s);
   return gek::general(m, n, k, dt, 6, x, w, h, false, 1, bias, (int)vec, (int)act, z, cus, s) == hipSuccess ? GE_OK
                                                                                                       : GE_ERR_HIP;
 }
@@ -254,7 +258,7 @@ ge_status_t gemm_epilog_gated_down(int64_t m, int64_t d, int64_t n, ge_dtype_t d
                               static_cast<hipStream_t>(stream)) == hipSuccess
                ? GE_OK
                : GE_ERR_HIP;
-  return gek::product(m, d, n, dt, 2, h, w_down, y, nullptr, 0, cus, static_cast<hipStream_t>(stream));
+  return gek::product(m, d, n, dt, 2, h, w_down, y, nullptr, 0, false, cus, static_cast<hipStream_t>(stream));
 }
 
 size_t gemm_epilog_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t d, ge_dtype_t dt) {
@@ -280,9 +284,15 @@ ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t 
   if (m > 0) {
     const void* dh = dy;
     bool f32 = false;
+    uint32_t* flags = nullptr;   // of a split of dX's product
+    if (dx && gek::fast_product(m, k, 2 * n, dt, 0, dz, w, dx)) {
+      geh::Layout L;
+      if (ge_status_t st = gegh::fast_layout(m, k, 2 * n, dt, 0, cus, scratch_bytes, &L); st != GE_OK) return st;
+      if (L.sk_wgs) flags = reinterpret_cast<uint32_t*>(scratch + L.off_sk_flag);
+    }
     if (w_down && gegh::fast_shape(m, n, d, dt, 2) && gegh::aligned(dy, 16) && gegh::aligned(w_down, 16) &&
         gegh::aligned(z, 16)) {
-      if (ge_status_t st = gek::gated_tiles(m, n, d, dt, true, (int)act, dy, w_down, nullptr, 0, z, dz, nullptr, cus, s);
+      if (ge_status_t st = gek::gated_tiles(m, n, d, dt, true, (int)act, dy, w_down, nullptr, 0, z, dz, nullptr, flags, cus, s);
           st != GE_OK)
         return st;
       dh = nullptr;
@@ -300,13 +310,13 @@ ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t 
     const int64_t chunks = m * ((n + 7) / 8);
     if (dh && gek::launch(fn, dim3((unsigned)((chunks + 255) / 256)), 256, params, s) != hipSuccess) return GE_ERR_HIP;
     if (dx)
-      if (ge_status_t st = gek::product(m, k, 2 * n, dt, 0, dz, w, dx, scratch, scratch_bytes, cus, s); st != GE_OK)
+      if (ge_status_t st = gek::product(m, k, 2 * n, dt, 0, dz, w, dx, scratch, scratch_bytes, !dh, cus, s); st != GE_OK)
         return st;
   }
   if (dw)
-    if (ge_status_t st = gek::product(2 * n, k, m, dt, 1, dz, x, dw, scratch, scratch_bytes, cus, s); st != GE_OK) return st;
+    if (ge_status_t st = gek::product(2 * n, k, m, dt, 1, dz, x, dw, scratch, scratch_bytes, false, cus, s); st != GE_OK) return st;
   if (dw_down)
-    if (ge_status_t st = gek::product(d, n, m, dt, 1, dy, h, dw_down, scratch, scratch_bytes, cus, s); st != GE_OK) return st;
+    if (ge_status_t st = gek::product(d, n, m, dt, 1, dy, h, dw_down, scratch, scratch_bytes, false, cus, s); st != GE_OK) return st;
   if (dbias)
     if (ge_status_t st =
             gek::column_sums(dz, m, 2 * n, dt, dbias, vec, reinterpret_cast<float*>(scratch), s);

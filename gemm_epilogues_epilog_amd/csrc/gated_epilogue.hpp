@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "gated_math.hpp"
+#include "tiles.hpp"
 
 namespace gek {
 
@@ -119,7 +120,9 @@ __device__ __forceinline__ void gated_block(const Args& p, const f32x16 (&acc)[N
   }
 }
 
-// The whole wave tile of dH, 32 x 32 at a time; Z of the next block is on its way meanwhile.
+// The whole wave tile of dH, 32 x 32 at a time; Z of the next block is on its way meanwhile. The
+// first workgroup also clears the flags of the next product's split (every wave the same zeros):
+// a launch less (77 x 1000 x 520 f16: 38.6 -> 37.6 us).
 template <int DT, int MB, int NB>
 __device__ __forceinline__ void dgated_tile(const Args& p, const f32x16 (&acc)[NB][MB], int64_t m0, int n0, int lane,
                                             char* scratch) {
@@ -148,6 +151,8 @@ __device__ __forceinline__ void dgated_tile(const Args& p, const f32x16 (&acc)[N
   const auto swz = [](int row) { return (row ^ (row >> 3)) & 7; };   // 16-byte units of 128-byte rows
   Z z[2];
   load(0, z[0]);
+  if (p.clear && blockIdx.x == 0)
+    for (int i = lane; i < kSkFlagWords; i += 64) p.clear[i] = 0;
 #pragma unroll
   for (int i = 0; i < MB * NB; ++i) {
     const int b = i / NB, a = i % NB;

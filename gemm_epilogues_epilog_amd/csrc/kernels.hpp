@@ -84,6 +84,8 @@ struct Args {
   int32_t act;
   const void* z;
   void* z_out;
+  // DGATED: kSkFlagWords words that the launch clears for the product after it, or null.
+  uint32_t* clear;
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base) {

@@ -12,9 +12,9 @@ namespace gei {
 ge_status_t current_device(int* cus);
 
 // D (m, n) = A . B of dense 16-bit operands in the storage orders of L, by the kernels of a plan
-// with that layout. `ws`: L.ws_bytes of workspace, its flags cleared here.
+// with that layout. `ws`: L.ws_bytes of workspace, its flags cleared here unless they are already.
 ge_status_t run_product(int64_t m, int n, int k, ge_dtype_t dt, const geh::Layout& L, const void* A, const void* B,
-                        void* D, char* ws, hipStream_t s);
+                        void* D, char* ws, bool cleared, hipStream_t s);
 
 }  // namespace gei
 

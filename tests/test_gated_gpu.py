@@ -180,6 +180,46 @@ def test_backward(gpu, m, n, k, d, dtype):
         check_backward(dh, x, w, z, None, None, act, dtype, g, act + " dh")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m,n,k,d", [(40, 100, 1, 3), (70, 1, 200, 5), (3, 64, 3, 100), (200, 7, 7, 130), (150, 130, 5, 2), (300, 3, 8, 4),
+                                     (9, 4, 4, 4), (34, 8, 9, 8)])
+def test_rows_of_a_few_bytes(gpu, m, n, k, d, dtype):
+    """Rows of fewer than 16 bytes, of any operand, and just as many."""
+    x, w, b = make(m, n, k, dtype, m + n + k + d)
+    gen = torch.Generator().manual_seed(d)
+    h, z = gated.gated_forward(x, w, b, act="GELU", save=True)
+    check_forward(x, w, b, "GELU", dtype, h, z)
+    wd = (torch.randn(d, n, generator=gen) * n ** -0.5).to(T[dtype]).cuda()
+    dy = (torch.randn(m, d, generator=gen) * 0.3).to(T[dtype]).cuda()
+    close(gated.gated_down(h, wd), h.double() @ wd.double().t(), sum_error(h.double(), wd.double().t()), dtype)
+    g = gated.gated_backward(dy, x, w, z, w_down=wd, h=h, act="GELU", bias_grad="f32")
+    check_backward(dy, x, w, z, wd, h, "GELU", dtype, g)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k,d", [(40, 33, 50, 21), (150, 136, 136, 72), (300, 70, 129, 65)])
+def test_nothing_past_an_operand(gpu, m, n, k, d, dtype):
+    """Every operand between NaN, at offsets of its own: nothing beside them reaches a result, and
+    nothing beside a result is written."""
+    def inside(t, at):
+        buf = torch.full((t.numel() + 96,), float("nan"), device="cuda", dtype=t.dtype)
+        v = buf[at:at + t.numel()].view(t.shape)
+        v.copy_(t)
+        return v, buf
+    x, w, b = make(m, n, k, dtype, m + n + k + d)
+    wd = (torch.randn(d, n, device="cuda") * n ** -0.5).to(T[dtype])
+    dy = (torch.randn(m, d, device="cuda") * 0.3).to(T[dtype])
+    for at in (0, 1, 16):
+        X, W, B, WD, DY = (inside(t, at)[0] for t in (x, w, b, wd, dy))
+        H, hb = inside(torch.zeros(m, n, device="cuda", dtype=T[dtype]), at)
+        Z, zb = inside(torch.zeros(m, 2 * n, device="cuda", dtype=T[dtype]), at)
+        gated.gated_forward(X, W, B, act="SILU", out=H, z_out=Z)
+        check_forward(x, w, b, "SILU", dtype, H, Z)
+        assert all(buf[:at].isnan().all() and buf[at + v.numel():].isnan().all() for v, buf in ((H, hb), (Z, zb)))
+        check_backward(dy, x, w, Z, wd, H, "SILU", dtype,
+                       gated.gated_backward(DY, X, W, Z, w_down=WD, h=H, act="SILU", bias_grad="f32"))
+
+
 def test_gradient_against_differences(gpu):
     """Loss sum(c * y) of the whole block in fp32, moved along random directions: the central
     difference of the forward pass in 64 bits against the product of gradient and direction."""
