@@ -71,7 +71,7 @@ ge_status_t check_product(int64_t m, int64_t n, ge_dtype_t dt, ge_dtype_t out, c
 //   tiles   start 2, a round of workgroups 2 and 128 k in 3.45 us (256 x 256), 1.15 (128 x 128) or 0.75
 //           (64 x 128: 28 us for 100 tokens); groups of 64 and of 32 multiply the sums more often.
 int choose(int64_t m, int64_t n, int64_t k, int64_t group, bool gated, bool aligned, int cus) {
-  if (k < 8) return -1;   // (the tiles load eight k at a time)
+  if (m <= 16 || k < 8) return -1;   // (the tiles load eight k at a time)
   const int64_t rows = gated ? 2 * n : n;
   const double kt = (double)gew4::k_tiles(k);
   const int64_t step = m <= 16 ? 16 : m <= 32 ? 32 : 64, blocks = gew4::ceil_div(m, step);
