@@ -101,29 +101,34 @@ ge_status_t gated_layout(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool ba
   return geh::make_layout(m, cols, k, t, GE_EPILOG_NONE, lay, cus, cfg, false, gek::cfg_can_persist(cfg), L);
 }
 
-// By estimated time in microseconds, from measurements at 1 to 64 tokens by 2 x 11008 x 4096, 4096 x
-// 11008, 2 x 1376 x 1024 and, fp32, 2 x 4096 x 2048. The kernel for few tokens: start and joining
-// 4, then W once per block of tokens and X, which every 16 rows read for themselves, at 6 TB/s
-// together (1 token 35 and 22 us, 32 tokens 63 and 40). The 128 x 128 tiles: 3, then W at 4.2 TB/s
-// or half a microsecond per k-tile and round of workgroups, whichever is longer (43 to 49, 79 to
-// 91, 12); the general kernel 0.9 per 128 bytes of k and round in fp32 and 0.6 in 16 bits (333
-// tokens by 2 x 1101 x 743: 22 and 9).
+// By estimated time in microseconds, fitted to 17 to 333 tokens by 2 x 1101 x 743, 1104 x 744, 1376 x
+// 1024, 2752 x 1024, 4096 x 2048 and 11008 x 4096 and by their single halves (the kernel that is taken
+// was at most 4 us, or an eighth, behind the other at any of them).
+//   few tokens  a round of workgroups reads a block of tokens for every 16 rows (gated: 32) of W, at
+//               8.5 TB/s (gated 5.6, as a workgroup waits for more); 16-bit types faster where
+//               compute units stay idle, rows that are not whole 16-byte chunks slower. 64 tokens by 2
+//               x 4096 x 2048: bf16 23 against 18, fp32 45 against 50;
+//   tiles       128 x 128: W at 4.2 TB/s or half a microsecond per k-tile and round, whichever is
+//               longer;
+//   general     0.78 per 128 bytes of k in fp32 and 0.5 in 16 bits, 0.5 and 0.3 more for each further
+//               tile of a compute unit.
 bool skinny(int64_t m, int64_t rows, int64_t k, ge_dtype_t dt, bool gated, int cus) {
   if (m <= 16) return true;
   if (m > 65535) return false;   // (its grid, by far)
-  const double es = dt == GE_F32 ? 4 : 2, w = (double)rows * k * es;
-  const int64_t step = m <= 32 ? 32 : 64, blocks = cdiv(m, step), groups = cdiv(gated ? rows / 2 : rows, 16);
-  const double share = std::min(1.0, (double)(groups * blocks) / cus);
-  // (rows that are not whole 16-byte chunks: less than half the rate, and a quarter, but half of it
-  // with few workgroups too: 64 tokens by 1101 x 743, fp32 13 and bf16 13)
-  const bool chunks = (int64_t)(k * es) % 16 == 0;
-  const double rate = (chunks ? 6e6 : dt == GE_F32 ? 2.6e6 : 1.6e6) * (chunks ? share : std::max(share, 0.5));
-  const double few = 4.0 + ((double)blocks * w + (double)(groups * blocks * step) * k * es) / rate;
+  const bool wide = dt == GE_F32;
+  const double es = wide ? 4 : 2, w = (double)rows * k * es;
+  const int64_t step = m <= 32 ? 32 : 64, wgs = cdiv(gated ? rows / 2 : rows, 16) * cdiv(m, step);
+  const double rounds = wgs <= cus ? 1.0 : std::max(2.0, (double)wgs / cus);
+  double rate = gated ? 5.6e6 : 8.5e6;
+  if ((int64_t)(k * es) % 16) rate *= wide ? 0.7 : 0.4;
+  else if (!wide) rate /= std::min(1.0, std::max(0.4, (double)wgs / cus));
+  const double few = (wide ? 3.5 : 2.5) + rounds * (double)((gated ? 32 : 16) + step) * (double)k * es * cus / rate;
   double tiles;
   if (fast_shape(m, rows, k, dt, 2)) {
     tiles = 3.0 + std::max(w / 4.2e6, (double)(cdiv(cdiv(m, 128) * cdiv(rows, 128), cus) * cdiv(k, 64)) * 0.5);
   } else {
-    tiles = 3.0 + (double)(cdiv(cdiv(m, 64) * cdiv(rows, 64), 2 * cus) * cdiv((int64_t)(k * es), 128)) * (dt == GE_F32 ? 0.9 : 0.6);
+    const double more = (double)cdiv(cdiv(m, 64) * cdiv(rows, 64), cus) - 1.0;
+    tiles = 3.0 + (double)cdiv((int64_t)(k * es), 128) * (wide ? 0.78 + 0.5 * more : 0.5 + 0.3 * more);
   }
   return few < tiles;
 }
