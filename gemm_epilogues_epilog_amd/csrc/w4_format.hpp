@@ -28,7 +28,7 @@ constexpr int64_t k_groups(int64_t k, int64_t group) { return ceil_div(k, group)
 struct W4TileCfg {
   int bm, bn, waves;
 };
-enum W4Tiles { W4_L = 0, W4_M, W4_S, W4_COUNT };
-constexpr W4TileCfg kTiles[W4_COUNT] = {{256, 256, 8}, {128, 128, 8}, {64, 128, 8}};
+enum W4Tiles { W4_L = 0, W4_L3, W4_M, W4_S, W4_COUNT };
+constexpr W4TileCfg kTiles[W4_COUNT] = {{256, 256, 8}, {192, 256, 8}, {128, 128, 8}, {64, 128, 8}};
 
 }  // namespace gew4

@@ -68,8 +68,9 @@ ge_status_t check_product(int64_t m, int64_t n, ge_dtype_t dt, ge_dtype_t out, c
 //           X, which every row group reads for itself, at the 10 TB/s that the L2 caches gave (fewer
 //           workgroups than compute units get their share): 7, 11, 18, 28 and 60 us for 16, 32, 64, 100
 //           and 256 tokens by 4096 x 4096. X in pieces of less than 16 bytes: 2.5 times that;
-//   tiles   start 2, a round of workgroups 2 and 128 k in 3.45 us (256 x 256), 1.15 (128 x 128) or 0.75
-//           (64 x 128: 28 us for 100 tokens); groups of 64 and of 32 multiply the sums more often.
+//   tiles   start 2, a round of workgroups 2 and 128 k in 3.45 us (256 x 256), 2.9 (192 x 256), 1.15 (128
+//           x 128) or 0.75 (64 x 128: 28 us for 100 tokens); groups of 64 and of 32 multiply the sums
+//           more often.
 int choose(int64_t m, int64_t n, int64_t k, int64_t group, bool gated, bool aligned, int cus) {
   if (m <= 16 || k < 8) return -1;   // (the tiles load eight k at a time)
   const int64_t rows = gated ? 2 * n : n;
@@ -79,10 +80,10 @@ int choose(int64_t m, int64_t n, int64_t k, int64_t group, bool gated, bool alig
   const double x = (double)m * (double)rows / 16 * (double)k * 2 / 10e6, w = (double)blocks * (double)rows * (double)k * 0.5 / 5e6;
   double best = (4.0 + 1.2 * (wgs / (share * cus) - 1.0) + (x + w) / share) * (aligned ? 1.0 : 2.5);
   int cfg = -1;
-  const double per[gew4::W4_COUNT][3] = {{3.45, 4.0, 0.0}, {1.15, 1.55, 2.0}, {0.75, 0.87, 1.3}};
+  const double per[gew4::W4_COUNT][3] = {{3.45, 4.1, 0.0}, {2.9, 3.6, 0.0}, {1.15, 1.55, 2.0}, {0.75, 0.87, 1.3}};
   const int e = group == 32 ? 2 : group == 64 ? 1 : 0;
   for (int c = 0; c < gew4::W4_COUNT; ++c) {
-    if (c == gew4::W4_L && (e == 2 || !aligned)) continue;   // (not instantiated)
+    if (c <= gew4::W4_L3 && (e == 2 || !aligned)) continue;   // (not instantiated)
     const int64_t tiles = gew4::ceil_div(m, gew4::kTiles[c].bm) * gew4::ceil_div(rows, gew4::kTiles[c].bn);
     const double t = 2.0 + (double)gew4::ceil_div(tiles, cus) * (2.0 + kt * per[c][e]);
     if (t < best) {

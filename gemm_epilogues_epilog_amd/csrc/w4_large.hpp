@@ -1,13 +1,17 @@
 // Tile kernel of the products with 4-bit weights for thousands of tokens (layout: w4_format.hpp; the
 // numbers (q - z) p and the units of the sums: w4_tile.hpp).
 //
-// A 256 x 256 tile of D, k in tiles of 64. X goes straight into LDS; W's codes go through registers,
+// A 256 x 256 or 192 x 256 tile of D, k in tiles of 64. X goes straight into LDS; W's codes go through registers,
 // each once per workgroup, and lie in LDS as 16-bit numbers in the same k-major order. The two
 // operands then meet in v_mfma_f32_32x32x16 as in the 16-bit kernels (gemm_dtl.hpp). A code is
 // converted once per 256 tokens and a sum multiplied as often as in the smaller tiles, so this is
-// the kernel where there is work for every compute unit: 3000 x 4096 x 4096 bf16 with groups of 128
-// (of 64) takes 115 (132) us here and 135 (160) in tiles of 128 x 128; 600 x 4096 x 4096 99 and 41. X's rows
-// are whole 16-byte chunks, and groups hold at least 64 (of 32 the factors do not fit the registers).
+// the kernel where there is work for every compute unit. bf16 with groups of 128, tiles of 256, of 192
+// and of 128 x 128: 3000 x 4096 x 4096 112, 107 and 136 us (groups of 64: 135, 121 and 159), 4096
+// tokens 131, 186 and 187, 600 tokens 98, 86 and 44. X's rows are whole 16-byte chunks, and groups
+// hold at least 64 (of 32 the factors do not fit the registers).
+//
+// The matrix unit is busy a third of the time (192 of 256 units with 256 x 256): the conversions
+// of eight codes and the factors stand among the products, and two waves to a SIMD hide part of it.
 //
 // At the end of k-tile t every wave waits until its copies of X's tile t + 1 have landed and its
 // reads of tile t and its writes of W's tile t + 1 are done; one barrier publishes tile t + 1 and
@@ -22,8 +26,9 @@
 
 namespace gek {
 
+template <int BM_>
 struct W4Large {
-  static constexpr int BM = 256, BN = 256, WM = 128, WN = 64;
+  static constexpr int BM = BM_, BN = 256, WM = BM / 2, WN = 64;
   static constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN, NW = WAVES_M * WAVES_N, NT = NW * 64;
   static constexpr int MB = WM / 32, NB = WN / 32;
   static constexpr int X_BYTES = BM * 128, W_BYTES = BN * 128, OFF_W = 2 * X_BYTES;   // (two stages of each)
@@ -34,6 +39,7 @@ struct W4Large {
   static constexpr int OFF_C = OFF_R + 2 * BN * 4;
   static constexpr int EPI = 8192;                    // epilogue bytes per wave (in the stages)
   static constexpr int LDS = OFF_C + NW * CODES;
+  static_assert(X_BYTES % (1024 * NW) == 0 && WM % 32 == 0, "shares of a wave");
   static_assert(NW * EPI <= OFF_R && LDS <= 160 * 1024, "LDS");
 };
 
@@ -64,10 +70,10 @@ __device__ __forceinline__ void copy_to_lds_b32(const i32x4& srd, uint32_t voff,
 // Epilogue: 32 x 32 blocks of sums through fp32 scratch (gated: one of the gate and one of the up
 // projection), so that a lane gets eight neighbouring columns of a token and memory sees whole
 // pieces of rows at any alignment.
-template <int DT, bool GATED>
-__device__ __forceinline__ void w4_large_epilogue(const W4Args& p, const f32x16 (&acc)[W4Large::NB][W4Large::MB], int64_t m0, int n0,
+template <int DT, bool GATED, class C>
+__device__ __forceinline__ void w4_large_epilogue(const W4Args& p, const f32x16 (&acc)[C::NB][C::MB], int64_t m0, int n0,
                                                  int lane, char* scratch) {
-  constexpr int NH = GATED ? W4Large::NB / 2 : W4Large::NB;
+  constexpr int NH = GATED ? C::NB / 2 : C::NB;
   const int lrow = lane & 31, lhi = lane >> 5, r16 = lane >> 2, c = lane & 3;
   const auto swz = [](int row) { return (row ^ (row >> 3)) & 7; };   // 16-byte units of 128-byte rows
   const auto put = [&](const f32x16& v, char* to) {
@@ -95,7 +101,7 @@ __device__ __forceinline__ void w4_large_epilogue(const W4Args& p, const f32x16 
       bu[e] = GATED && p.bias && e < left ? load_vec(p.bias, p.vec, p.n + col + e) : 0.0f;
     }
 #pragma unroll
-    for (int b = 0; b < W4Large::MB; ++b) {
+    for (int b = 0; b < C::MB; ++b) {
       put(acc[a][b], scratch);
       if constexpr (GATED) put(acc[a + NH][b], scratch + 4096);
       __builtin_amdgcn_wave_barrier();
@@ -139,10 +145,10 @@ __device__ __forceinline__ void w4_large_epilogue(const W4Args& p, const f32x16 
 }
 
 // E: groups of a row in a pair of k-tiles: 2 (of 64), 1 (of 128 and more).
-template <int DT, bool GATED, int E>
+template <int DT, bool GATED, int BM, int E>
 __global__ __launch_bounds__(512, 2) void w4_large_kernel(W4Args p, W4Launch L) {
-  using C = W4Large;
-  constexpr int BM = C::BM, BN = C::BN, WM = C::WM, WN = C::WN, MB = C::MB, NB = C::NB, RG = C::RG, XI = C::XI;
+  using C = W4Large<BM>;
+  constexpr int BN = C::BN, WM = C::WM, WN = C::WN, MB = C::MB, NB = C::NB, RG = C::RG, XI = C::XI;
   constexpr int NCODE = RG + 2, NMMA = MB * NB;
   static_assert(E == 1 || E == 2, "groups");
   __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
@@ -370,7 +376,7 @@ __global__ __launch_bounds__(512, 2) void w4_large_kernel(W4Args p, W4Launch L) 
     if (q == 0) reinterpret_cast<float*>(smem + C::OFF_R)[(w * RG + r) * 16 + li] = f[r];
   __syncthreads();
   rescale(0);
-  w4_large_epilogue<DT, GATED>(p, acc, m0 + wm * WM, n0 + wn * (GATED ? WN / 2 : WN), lane, smem + w * C::EPI);
+  w4_large_epilogue<DT, GATED, C>(p, acc, m0 + wm * WM, n0 + wn * (GATED ? WN / 2 : WN), lane, smem + w * C::EPI);
 }
 
 }  // namespace gek

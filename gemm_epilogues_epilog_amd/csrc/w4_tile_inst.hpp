@@ -12,10 +12,10 @@ const void* w4_tile_fn(int e) {
          : e == 2 ? reinterpret_cast<const void*>(&w4_tile_kernel<DT, GATED, BM, 2>)
                   : reinterpret_cast<const void*>(&w4_tile_kernel<DT, GATED, BM, 1>);
 }
-template <int DT, bool GATED>
+template <int DT, bool GATED, int BM>
 const void* w4_large_fn(int e) {
-  return e == 2 ? reinterpret_cast<const void*>(&w4_large_kernel<DT, GATED, 2>)
-                : reinterpret_cast<const void*>(&w4_large_kernel<DT, GATED, 1>);
+  return e == 2 ? reinterpret_cast<const void*>(&w4_large_kernel<DT, GATED, BM, 2>)
+                : reinterpret_cast<const void*>(&w4_large_kernel<DT, GATED, BM, 1>);
 }
 
 // Tile `cfg` (gew4::W4Tiles) of one type.
@@ -23,7 +23,8 @@ template <int DT>
 const void* w4_tile_pick(int cfg, bool gated, int64_t group) {
   const int e = group == 32 ? 4 : group == 64 ? 2 : 1;
   switch (cfg) {
-    case gew4::W4_L: return gated ? w4_large_fn<DT, true>(e) : w4_large_fn<DT, false>(e);
+    case gew4::W4_L: return gated ? w4_large_fn<DT, true, 256>(e) : w4_large_fn<DT, false, 256>(e);
+    case gew4::W4_L3: return gated ? w4_large_fn<DT, true, 192>(e) : w4_large_fn<DT, false, 192>(e);
     case gew4::W4_M: return gated ? w4_tile_fn<DT, true, 128>(e) : w4_tile_fn<DT, false, 128>(e);
     default: return gated ? w4_tile_fn<DT, true, 64>(e) : w4_tile_fn<DT, false, 64>(e);
   }

@@ -143,7 +143,7 @@ void check_w4() {
                 if (!m || (chunks && k % 8)) continue;
                 const int c = gew4h::choose(m, n, k, group, gated, chunks, cus);
                 check(c >= -1 && c < gew4::W4_COUNT, "kernel", m, n, k, c);
-                check(c != gew4::W4_L || (chunks && group >= 64), "the large tile's operands", m, n, k, group);
+                check((c != gew4::W4_L && c != gew4::W4_L3) || (chunks && group >= 64), "the large tiles' operands", m, n, k, group);
                 check(c < 0 || k >= 8, "rows of eight", m, n, k, c);
                 check(m > 16 || c < 0, "few tokens", n, k, group, c);
               }

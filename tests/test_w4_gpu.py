@@ -207,10 +207,11 @@ def test_gated(gpu, m, n, k, group, dtype):
     check_gated(*a, dtype, [("SILU", True), ("GELU", False), ("RELU", True)])
 
 
-# 256 x 256, 128 x 128 and 64 x 128 tiles: more than one of each, ragged rows, columns and k, an odd
+# 256 x 256, 192 x 256, 128 x 128 and 64 x 128 tiles: more than one of each, ragged rows, columns and k, an odd
 # number of k-tiles, one k-tile, groups longer than k
 TILES = [(1030, 8208, 392, 64), (1030, 8208, 520, 128), (2100, 4100, 64, 64), (1000, 4130, 456, 32), (1290, 8300, 131, 128),
-         (900, 5000, 130, 32), (700, 1500, 1100, 256), (130, 260, 2000, 64), (66, 1000, 24, 1024), (257, 4099, 333, 64)]
+         (900, 5000, 130, 32), (700, 1500, 1100, 256), (130, 260, 2000, 64), (66, 1000, 24, 1024), (257, 4099, 333, 64),
+         (2900, 4104, 264, 128), (2900, 4104, 264, 64), (2900, 4104, 64, 64), (1340, 8200, 200, 64), (300, 20000, 136, 64)]
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
