@@ -41,7 +41,8 @@ __device__ __forceinline__ void store8(void* row, int64_t pos, int64_t len, cons
   }
 }
 
-// dZ from dH and Z, eight columns a thread. Bound by memory: reads dH and Z, writes dZ.
+// dZ from dH and Z, eight columns a thread, where the product's kernel does not do it (fp32, unaligned
+// rows, or dH given). Bound by memory: reads dH and Z, writes dZ.
 template <int DT, int DH>
 __global__ __launch_bounds__(256) void dz_kernel(const void* dh, const void* z, void* dz, int64_t m, int64_t n, int act) {
   constexpr int64_t es = Tr<DT>::es;
@@ -69,8 +70,9 @@ __global__ __launch_bounds__(256) void dz_kernel(const void* dh, const void* z, 
   store8<DT>(o + n * es, pos, n, du);
 }
 
-// partial[part][col], or with one part out[col] of type vec: sums of the columns of a dense (m, cols) matrix over the part's rows, in a
-// fixed order: four rows side by side, each in ascending order, then those four in order.
+// partial[part][col], or with one part out[col] of type vec: sums of the columns of a dense (m, cols)
+// matrix over the part's rows, in a fixed order: four rows side by side, each in ascending order, then
+// those four in order. Bound by memory, with few rows by its start (77 x 2000: 4.5 us).
 template <int DT>
 __global__ __launch_bounds__(256) void colsum_kernel(const void* x, int64_t m, int64_t cols, float* partial, void* out,
                                                      int vec) {

@@ -5,6 +5,13 @@
 // fp32 sum is scaled once, so that no product sees a rounded weight. A code byte is e4m3's
 // 2^-9 times its value (eight subnormals, then eight values of the same spacing), so one
 // conversion with scale 2^9 turns two codes into two exact 16-bit numbers.
+//
+// Few tokens: a workgroup takes 16 rows of W (gated: 16 of each half) and up to 64 tokens; its waves
+// share the k-tiles and add their sums through LDS in wave order. Bound by W's codes from memory, and
+// by the start: 1 x 4096 x 11008 f16 7.6 us (3.1 TB/s; a kernel's start, the first reads and the joining
+// are about 4), 1 x 2 x 11008 x 4096 bf16 11.4 (4.2 TB/s). Every byte comes once (23.9 and 47.4 MB by the
+// counters). From 17 tokens on X, which every 16 rows read for themselves, bounds it: 32 and 64
+// tokens by 4096 x 4096 take 11 and 18 us.
 #pragma once
 
 #include <type_traits>

@@ -10,8 +10,8 @@
 // tokens 131, 186 and 187, 600 tokens 98, 86 and 44. X's rows are whole 16-byte chunks, and groups
 // hold at least 64 (of 32 the factors do not fit the registers).
 //
-// The matrix unit is busy a third of the time (192 of 256 units with 256 x 256): the conversions
-// of eight codes and the factors stand among the products, and two waves to a SIMD hide part of it.
+// The matrix unit is busy 37% of the cycles (192 x 256 at 3000 x 4096 x 4096, groups of 64): the
+// conversions and the factors stand among the products, and two waves to a SIMD hide part of them.
 //
 // At the end of k-tile t every wave waits until its copies of X's tile t + 1 have landed and its
 // reads of tile t and its writes of W's tile t + 1 are done; one barrier publishes tile t + 1 and
