@@ -592,6 +592,8 @@ ge_status_t gemm_epilog_w4_dequantize(int64_t rows, int64_t k, int64_t group, in
  *   bias : n values of type vec (dt or fp32); ignored (may be NULL) for NONE.
  * x, D and bias are aligned to their elements; X with k a multiple of 8 and 16-byte aligned runs
  * faster.
+ * An infinity or a NaN in a token of X makes all of that token's results infinite or NaN (NaN also
+ * where the sum over (q - z) s would be infinite; after RELU_BIAS 0 then), and no other token's.
  */
 ge_status_t gemm_epilog_w4_matmul(int64_t m, int64_t n, int64_t k, int64_t group, ge_dtype_t dt, ge_dtype_t out,
                                   ge_epilog_t ep, const void* x, const void* codes, const void* scales,

@@ -309,6 +309,17 @@ def test_rows_stay_apart(gpu, m):
     assert torch.equal(d, aligned) and (out[:3] == 7).all() and (out[3 + m * 50:] == 7).all()
 
 
+@pytest.mark.parametrize("m,n", [(1, 50), (17, 70), (40, 50), (200, 500), (700, 1500), (2100, 4104)])
+def test_infinities_in_a_token(gpu, m, n):
+    x, W, b, full, mags = make(m, n, 264, 64, "bf16", 4)
+    x[m // 2, 7], x[m // 2, 200] = float("inf"), -float("inf")
+    D = w4.w4_matmul(x, W, out_dtype="f32")
+    assert not torch.isfinite(D[m // 2]).any()
+    keep = [i for i in range(m) if i != m // 2]
+    X = x[keep].double()
+    close(D[keep], X @ full.t(), (8 * math.sqrt(264) + 8) * U * (X.abs() @ mags.t()), "f32")
+
+
 def test_no_rows(gpu):
     x, W, b, *_ = make(1, 20, 40, 32, "f16", 1)
     assert w4.w4_matmul(x[:0], W).shape == (0, 20)
