@@ -7,10 +7,11 @@
 // elements' alignment. At the end of a row the load is moved back to the row's last 16 bytes
 // and its value shifted, so that nothing past a row is read and nothing branches per element;
 // rows of fewer than 16 bytes are read one element at a time.
-// fp32 runs v_mfma_f32_32x32x2 and is bound by it in large products (154 TFLOP/s in the library's):
+// fp32 runs v_mfma_f32_32x32x2 and is bound by it in large products (plain 8192^3 products by rocBLAS: 154 TFLOP/s):
 // 2048 x 2 x 4096 x 2048 538 us, 128 TFLOP/s. 333 x 2 x 1101 x 743 takes 26 us, 0.8 per k-tile of
 // 32, of which the products are 0.43: one wave a SIMD waits for LDS, for the stores of the next tile
-// and for the barrier. Four k-tiles on their way and four groups of waves changed nothing.
+// and for the barrier. Four k-tiles on their way, four groups of waves, and the next tile stored before
+// the products changed nothing.
 #pragma once
 
 #include <type_traits>
