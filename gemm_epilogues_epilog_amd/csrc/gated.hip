@@ -147,8 +147,7 @@ hipError_t general(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, cons
   a.act = act;
   // the large tile where it gives every compute unit one
   const auto tiles = [&](int t) { return (M + t - 1) / t * ((N + (lay == 6 ? t / 2 : t) - 1) / (lay == 6 ? t / 2 : t)); };
-  const int64_t row_a = lay & 1 ? M : K, row_b = lay & 2 ? K : N;
-  const bool narrow = (row_a < row_b ? row_a : row_b) * (dt == GE_F32 ? 4 : 2) < 16;
+  const bool narrow = gegh::general_narrow(M, N, K, dt, lay);
   const bool large = !narrow && gegh::general_large(M, lay == 6 ? 2 * N : N, cus);
   const int t = large ? 128 : 64;
   a.tiles_m = (int)((M + t - 1) / t);
@@ -238,12 +237,13 @@ ge_status_t gemm_epilog_gated_forward(int64_t m, int64_t n, int64_t k, ge_dtype_
   int cus = 0;
   if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (gegh::skinny(m, 2 * n, k, dt, true, cus))
+  const bool on16 = gegh::aligned(x, 16) && gegh::aligned(w, 16) && gegh::aligned(h, 16) && gegh::aligned(z, 16);
+  const gegh::Kernel kernel = gegh::forward_kernel(m, n, k, dt, true, on16, cus);
+  if (kernel == gegh::Kernel::kFew)
     return gek::launch_skinny(m, n, k, (int)dt, true, (int)act, x, w, bias, (int)vec, h, z, cus, s) == hipSuccess
                ? GE_OK
                : GE_ERR_HIP;
-  if (gegh::fast_shape(m, n, k, dt, 2) && gegh::aligned(x, 16) && gegh::aligned(w, 16) && gegh::aligned(h, 16) &&
-      gegh::aligned(z, 16))
+  if (kernel == gegh::Kernel::kTiles)
     return gek::gated_tiles(m, n, k, dt, false, (int)act, x, w, bias, (int)vec, nullptr, h, z, nullptr, cus, s);
   return gek::general(m, n, k, dt, 6, x, w, h, false, 1, bias, (int)vec, (int)act, z, cus, s) == hipSuccess ? GE_OK
                                                                                                       : GE_ERR_HIP;
@@ -255,7 +255,7 @@ ge_status_t gemm_epilog_gated_down(int64_t m, int64_t d, int64_t n, ge_dtype_t d
   if (m == 0) return GE_OK;
   int cus = 0;
   if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
-  if (gegh::skinny(m, d, n, dt, false, cus))
+  if (gegh::forward_kernel(m, d, n, dt, false, false, cus) == gegh::Kernel::kFew)
     return gek::launch_skinny(m, d, n, (int)dt, false, 0, h, w_down, nullptr, 0, y, nullptr, cus,
                               static_cast<hipStream_t>(stream)) == hipSuccess
                ? GE_OK
@@ -292,8 +292,8 @@ ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t 
       if (ge_status_t st = gegh::fast_layout(m, k, 2 * n, dt, 0, cus, scratch_bytes, &L); st != GE_OK) return st;
       if (L.sk_wgs) flags = reinterpret_cast<uint32_t*>(scratch + L.off_sk_flag);
     }
-    if (w_down && gegh::fast_shape(m, n, d, dt, 2) && gegh::aligned(dy, 16) && gegh::aligned(w_down, 16) &&
-        gegh::aligned(z, 16)) {
+    const bool on16 = gegh::aligned(dy, 16) && gegh::aligned(w_down, 16) && gegh::aligned(z, 16);
+    if (w_down && gegh::gradient_kernel(m, n, d, dt, on16) == gegh::Kernel::kTiles) {
       if (ge_status_t st = gek::gated_tiles(m, n, d, dt, true, (int)act, dy, w_down, nullptr, 0, z, dz, nullptr, flags, cus, s);
           st != GE_OK)
         return st;

@@ -133,6 +133,20 @@ bool skinny(int64_t m, int64_t rows, int64_t k, ge_dtype_t dt, bool gated, int c
   return few < tiles;
 }
 
+Kernel forward_kernel(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool gated, bool on16, int cus) {
+  if (skinny(m, gated ? 2 * n : n, k, dt, gated, cus)) return Kernel::kFew;
+  return fast_shape(m, n, k, dt, 2) && on16 ? Kernel::kTiles : Kernel::kGeneral;
+}
+
+Kernel gradient_kernel(int64_t m, int64_t n, int64_t d, ge_dtype_t dt, bool on16) {
+  return fast_shape(m, n, d, dt, 0) && on16 ? Kernel::kTiles : Kernel::kGeneral;
+}
+
+bool general_narrow(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay) {
+  const int64_t row_a = lay & 1 ? M : K, row_b = lay & 2 ? K : N;
+  return std::min(row_a, row_b) * (int64_t)geh::elem_size(dt) < 16;
+}
+
 int64_t colsum_parts(int64_t m, int64_t cols) {
   const int64_t across = cdiv(cols, 512);
   if (m <= 128) return 1;   // (one kernel, 20 to 32 rows after each other in each of its four rows)

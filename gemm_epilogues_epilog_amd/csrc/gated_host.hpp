@@ -47,6 +47,14 @@ ge_status_t gated_layout(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool ba
 // tokens.
 bool skinny(int64_t m, int64_t rows, int64_t k, ge_dtype_t dt, bool gated, int cus);
 
+// The kernel of X (m, k) . W^T with n columns (gated: of each half), where the pointers are on 16
+// bytes or not; and of dY (m, d) . Wd with the activations' gradient.
+enum class Kernel { kFew, kTiles, kGeneral };
+Kernel forward_kernel(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool gated, bool on16, int cus);
+Kernel gradient_kernel(int64_t m, int64_t n, int64_t d, ge_dtype_t dt, bool on16);
+// The general kernel's form for rows of fewer than 16 bytes.
+bool general_narrow(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay);
+
 // Column sums of (m, 2 n) values: row ranges summed side by side.
 int64_t colsum_parts(int64_t m, int64_t cols);
 

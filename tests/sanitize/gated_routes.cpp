@@ -1,0 +1,68 @@
+// Names the kernels that the host rules of the gated block and of 4-bit weights choose on 256 compute
+// units, for 16-byte aligned operands: host code only, built by tests/test_gated_routes.py with g++.
+// Reads lines of
+//   forward m n k dt | down m d n dt | gradient m n d dt | product M N K dt lay |
+//   w4 m n k group gated chunks
+// (dt 0 f32, 1 f16, 2 bf16) and prints a name for each.
+#include <cstdio>
+#include <cstring>
+
+#include "gated_host.hpp"
+#include "tiles.hpp"
+#include "w4_host.hpp"
+
+namespace {
+
+constexpr int kCus = 256;
+
+void tiles(const geh::Layout& L) {
+  std::printf("%s%s%s\n", gek::kTiles[L.cfg].name, L.persist_grid ? " persistent" : "", L.sk_wgs ? " split" : "");
+}
+
+// The general kernel; lay 6: gated, of both halves.
+void general(long M, long N, long K, ge_dtype_t dt, int lay, size_t ws) {
+  if (gegh::general_narrow(M, N, K, dt, lay)) std::printf("general narrow");
+  else std::printf(gegh::general_large(M, lay == 6 ? 2 * N : N, kCus) ? "general large" : "general small");
+  const int parts = lay == 6 ? 1 : gegh::general_splits(M, N, K, dt, ws);
+  if (parts > 1) std::printf(" %d parts", parts);
+  std::printf("\n");
+}
+
+}  // namespace
+
+int main() {
+  char op[16];
+  while (std::scanf("%15s", op) == 1) {
+    geh::Layout L;
+    long a, b, c, d, e, f;
+    if (!std::strcmp(op, "w4")) {
+      if (std::scanf("%ld %ld %ld %ld %ld %ld", &a, &b, &c, &d, &e, &f) != 6) return 1;
+      const int cfg = gew4h::choose(a, b, c, d, e != 0, f != 0, kCus);
+      if (cfg < 0) std::printf("few\n");
+      else std::printf("%d x %d\n", gew4::kTiles[cfg].bm, gew4::kTiles[cfg].bn);
+      continue;
+    }
+    if (std::scanf("%ld %ld %ld %ld", &a, &b, &c, &d) != 4) return 1;
+    const ge_dtype_t dt = (ge_dtype_t)d;
+    const bool gated = !std::strcmp(op, "forward");
+    if (gated || !std::strcmp(op, "down")) {
+      const gegh::Kernel kernel = gegh::forward_kernel(a, b, c, dt, gated, true, kCus);
+      if (kernel == gegh::Kernel::kFew) std::printf("few\n");
+      else if (kernel == gegh::Kernel::kGeneral) general(a, b, c, dt, gated ? 6 : 2, 0);
+      else if ((gated ? gegh::gated_layout(a, b, c, dt, false, kCus, &L) : gegh::fast_layout(a, b, c, dt, 2, kCus, 0, &L)) == GE_OK) tiles(L);
+      else return 1;
+    } else if (!std::strcmp(op, "gradient")) {
+      if (gegh::gradient_kernel(a, b, c, dt, true) == gegh::Kernel::kGeneral) general(a, b, c, dt, 0, 0);
+      else if (gegh::gated_layout(a, b, c, dt, true, kCus, &L) == GE_OK) tiles(L);
+      else return 1;
+    } else if (!std::strcmp(op, "product")) {
+      if (std::scanf("%ld", &e) != 1) return 1;
+      if (!gegh::fast_shape(a, b, c, dt, (int)e)) general(a, b, c, dt, (int)e, ~(size_t)0);
+      else if (gegh::fast_layout(a, b, c, dt, (int)e, kCus, e ? 0 : ~(size_t)0, &L) == GE_OK) tiles(L);
+      else return 1;
+    } else {
+      return 1;
+    }
+  }
+  return 0;
+}
