@@ -19,8 +19,9 @@
 // (q - z) p, exact in 16 bits. The sums are held in units of f: where a group of a row begins they
 // are multiplied by the last group's f over the new one's (one fp32 multiplication per sum and
 // group, no second set of sums), and by the last f at the end. p takes the whole exponent of s
-// where (q - z) p stays a normal number, so f lies in [1, 2) but for scales out there, and the
-// quotients stay far from fp32's limits.
+// where (q - z) p stays a normal number, from 2^-14 to 2^11 in fp16 and 2^-126 to 2^124 in bf16, so f
+// lies in [1, 2) but for scales out there: below 32 and 16, and not below 2^-10 and 2^-7 (subnormal
+// scales). So the sums in units of f stay finite wherever the row's own stay below 2^120 (fp16: always).
 #pragma once
 
 #include "gemm_dtl.hpp"
@@ -33,7 +34,7 @@ template <int DT>
 __device__ __forceinline__ void w4_split(uint16_t bits, float& p, float& f) {
   const float s = Tr<DT>::widen(bits);
   const uint32_t e = __float_as_uint(s) & 0x7f800000u;
-  constexpr uint32_t lo = (uint32_t)(127 - (DT == BF16 ? 100 : 14)) << 23, hi = (uint32_t)(127 + (DT == BF16 ? 100 : 11)) << 23;
+  constexpr uint32_t lo = (uint32_t)(127 - (DT == BF16 ? 126 : 14)) << 23, hi = (uint32_t)(127 + (DT == BF16 ? 124 : 11)) << 23;
   const uint32_t c = min(max(e, lo), hi);
   p = __uint_as_float(c);
   f = s * __uint_as_float((254u << 23) - c);
