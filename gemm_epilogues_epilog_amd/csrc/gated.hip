@@ -220,6 +220,30 @@ ge_status_t column_sums(const void* x, int64_t m, int64_t cols, ge_dtype_t dt, v
   return launch_bgrad_reduce(partial, parts, cols, out, (int)vec, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
 }
 
+ge_status_t status(hipError_t e) { return e == hipSuccess ? GE_OK : GE_ERR_HIP; }
+const void* at(const void* p, int64_t bytes) { return p ? static_cast<const char*>(p) + bytes : nullptr; }
+void* at(void* p, int64_t bytes) { return p ? static_cast<char*>(p) + bytes : nullptr; }
+
+// The rows of one launch.
+ge_status_t forward_rows(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, ge_gate_t act, const void* x, const void* w,
+                         const void* bias, ge_dtype_t vec, void* h, void* z, int cus, hipStream_t s) {
+  const bool on16 = gegh::aligned(x, 16) && gegh::aligned(w, 16) && gegh::aligned(h, 16) && gegh::aligned(z, 16);
+  switch (gegh::forward_kernel(m, n, k, dt, true, on16, cus)) {
+    case gegh::Kernel::kFew:
+      return status(launch_skinny(m, n, k, (int)dt, true, (int)act, x, w, bias, (int)vec, h, z, cus, s));
+    case gegh::Kernel::kTiles:
+      return gated_tiles(m, n, k, dt, false, (int)act, x, w, bias, (int)vec, nullptr, h, z, nullptr, cus, s);
+    default:
+      return status(general(m, n, k, dt, 6, x, w, h, false, 1, bias, (int)vec, (int)act, z, cus, s));
+  }
+}
+ge_status_t down_rows(int64_t m, int64_t d, int64_t n, ge_dtype_t dt, const void* h, const void* w_down, void* y, int cus,
+                      hipStream_t s) {
+  if (gegh::forward_kernel(m, d, n, dt, false, false, cus) == gegh::Kernel::kFew)
+    return status(launch_skinny(m, d, n, (int)dt, false, 0, h, w_down, nullptr, 0, y, nullptr, cus, s));
+  return product(m, d, n, dt, 2, h, w_down, y, nullptr, 0, false, cus, s);
+}
+
 template <int DT>
 const void* dz_of(bool f32_dh) {
   return f32_dh ? reinterpret_cast<const void*>(&dz_kernel<DT, F32>) : reinterpret_cast<const void*>(&dz_kernel<DT, DT>);
@@ -236,17 +260,14 @@ ge_status_t gemm_epilog_gated_forward(int64_t m, int64_t n, int64_t k, ge_dtype_
   if (m == 0) return GE_OK;
   int cus = 0;
   if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool on16 = gegh::aligned(x, 16) && gegh::aligned(w, 16) && gegh::aligned(h, 16) && gegh::aligned(z, 16);
-  const gegh::Kernel kernel = gegh::forward_kernel(m, n, k, dt, true, on16, cus);
-  if (kernel == gegh::Kernel::kFew)
-    return gek::launch_skinny(m, n, k, (int)dt, true, (int)act, x, w, bias, (int)vec, h, z, cus, s) == hipSuccess
-               ? GE_OK
-               : GE_ERR_HIP;
-  if (kernel == gegh::Kernel::kTiles)
-    return gek::gated_tiles(m, n, k, dt, false, (int)act, x, w, bias, (int)vec, nullptr, h, z, nullptr, cus, s);
-  return gek::general(m, n, k, dt, 6, x, w, h, false, 1, bias, (int)vec, (int)act, z, cus, s) == hipSuccess ? GE_OK
-                                                                                                      : GE_ERR_HIP;
+  const int64_t most = gegh::launch_rows(n, true), row = (int64_t)geh::elem_size(dt);
+  for (int64_t r = 0; r < m; r += most)
+    if (ge_status_t st = gek::forward_rows(std::min(most, m - r), n, k, dt, act, gek::at(x, r * k * row), w, bias, vec,
+                                           gek::at(h, r * n * row), gek::at(z, r * 2 * n * row), cus,
+                                           static_cast<hipStream_t>(stream));
+        st != GE_OK)
+      return st;
+  return GE_OK;
 }
 
 ge_status_t gemm_epilog_gated_down(int64_t m, int64_t d, int64_t n, ge_dtype_t dt, const void* h, const void* w_down,
@@ -255,12 +276,13 @@ ge_status_t gemm_epilog_gated_down(int64_t m, int64_t d, int64_t n, ge_dtype_t d
   if (m == 0) return GE_OK;
   int cus = 0;
   if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
-  if (gegh::forward_kernel(m, d, n, dt, false, false, cus) == gegh::Kernel::kFew)
-    return gek::launch_skinny(m, d, n, (int)dt, false, 0, h, w_down, nullptr, 0, y, nullptr, cus,
-                              static_cast<hipStream_t>(stream)) == hipSuccess
-               ? GE_OK
-               : GE_ERR_HIP;
-  return gek::product(m, d, n, dt, 2, h, w_down, y, nullptr, 0, false, cus, static_cast<hipStream_t>(stream));
+  const int64_t most = gegh::launch_rows(d, false), row = (int64_t)geh::elem_size(dt);
+  for (int64_t r = 0; r < m; r += most)
+    if (ge_status_t st = gek::down_rows(std::min(most, m - r), d, n, dt, gek::at(h, r * n * row), w_down,
+                                        gek::at(y, r * d * row), cus, static_cast<hipStream_t>(stream));
+        st != GE_OK)
+      return st;
+  return GE_OK;
 }
 
 size_t gemm_epilog_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t d, ge_dtype_t dt) {

@@ -147,6 +147,9 @@ bool general_narrow(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay) {
   return std::min(row_a, row_b) * (int64_t)geh::elem_size(dt) < 16;
 }
 
+// (whole tiles of any of them: 256 rows)
+int64_t launch_rows(int64_t n, bool gated) { return geh::rows_per_launch(256, 4 * cdiv(n, gated ? 32 : 64), 256); }
+
 int64_t colsum_parts(int64_t m, int64_t cols) {
   const int64_t across = cdiv(cols, 512);
   if (m <= 128) return 1;   // (one kernel, 20 to 32 rows after each other in each of its four rows)

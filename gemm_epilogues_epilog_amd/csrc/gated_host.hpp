@@ -55,6 +55,10 @@ Kernel gradient_kernel(int64_t m, int64_t n, int64_t d, ge_dtype_t dt, bool on16
 // The general kernel's form for rows of fewer than 16 bytes.
 bool general_narrow(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay);
 
+// Rows that one launch of any of these kernels takes, for n columns (gated: of each half): their
+// workgroups have at least 16 values of the product for each lane.
+int64_t launch_rows(int64_t n, bool gated);
+
 // Column sums of (m, 2 n) values: row ranges summed side by side.
 int64_t colsum_parts(int64_t m, int64_t cols);
 

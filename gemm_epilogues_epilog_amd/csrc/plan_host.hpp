@@ -70,6 +70,12 @@ std::string describe(ge_dtypes_t dt, ge_epilog_t ep, const Layout& L);
 ge_status_t check_execute_args(ge_epilog_t ep, ge_dtypes_t dt, const void* A, const void* B, const void* bias,
                                const void* D, const void* aux, const void* bgrad);
 
+// Rows of a product that one launch takes: so many, in whole tiles of `step` rows, that `across`
+// workgroups of `lanes` lanes for each of them stay below the 2^32 lanes of a launch.
+constexpr int64_t rows_per_launch(int64_t step, int64_t across, int64_t lanes) {
+  return ((int64_t(1) << 32) - 1) / lanes / across * step;
+}
+
 // An environment switch set to "0" (tuning experiments).
 bool env_off(const char* name);
 

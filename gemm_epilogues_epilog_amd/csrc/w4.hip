@@ -55,8 +55,8 @@ __device__ __forceinline__ void w4_quotients(const float (&v)[8], float s, float
 // 4.5 TB/s.
 template <int SRC, int NG>
 __global__ __launch_bounds__(256) void w4_quantize_kernel(const void* src, int64_t ld, W4Weight o, int dt, int symmetric,
-                                                          int64_t units) {
-  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+                                                          int64_t first, int64_t units) {
+  const int64_t unit = first + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (unit >= units) return;
   const int lane = threadIdx.x & 63, li = lane & 15, q = lane >> 4;
   const int64_t per = NG == 0 ? o.groups : o.kt;       // units of a row group
@@ -179,8 +179,8 @@ const void* quantize_of(int64_t group) {
 // rows' scales beside it. Once per weight of a checkpoint:
 // 2 x 11008 x 4096 in 35 us.
 __global__ __launch_bounds__(256) void w4_pack_kernel(const uint8_t* src, const uint16_t* scales, const uint8_t* zeros,
-                                                      W4Weight o, int64_t units) {
-  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+                                                      W4Weight o, int64_t first, int64_t units) {
+  const int64_t unit = first + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (unit >= units) return;
   const int lane = threadIdx.x & 63, li = lane & 15, q = lane >> 4;
   const int64_t rg = unit / o.kt, t = unit - rg * o.kt;
@@ -223,8 +223,9 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(const uint8_t* src, const 
 // (q - z) s, rounded to DT. A wave per tile, eight values at a time. Bound by memory: 11008 x 4096
 // bf16 28 us, 4.0 TB/s.
 template <int DT>
-__global__ __launch_bounds__(256) void w4_dequantize_kernel(W4Weight o, int sdt, void* dst, int64_t ld, int64_t units) {
-  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+__global__ __launch_bounds__(256) void w4_dequantize_kernel(W4Weight o, int sdt, void* dst, int64_t ld, int64_t first,
+                                                            int64_t units) {
+  const int64_t unit = first + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (unit >= units) return;
   const int lane = threadIdx.x & 63, li = lane & 15, q = lane >> 4;
   const int64_t rg = unit / o.kt, t = unit - rg * o.kt;
@@ -311,12 +312,22 @@ ge_status_t skinny(W4Args& a, bool vec, int cus, void* stream) {
 ge_status_t tiled(W4Args& a, int cfg, ge_dtype_t dt, bool gated, void* stream) {
   const gew4::W4TileCfg& T = gew4::kTiles[cfg];
   W4Launch L;
-  L.tiles_m = (int32_t)gew4::ceil_div(a.m, T.bm);
   L.tiles_n = (int32_t)gew4::ceil_div(gated ? 2 * (int64_t)a.n : a.n, T.bn);
   L.group_m = 8;
   const void* fn = dt == GE_F16 ? w4_tile_f16(cfg, gated, a.group) : w4_tile_bf16(cfg, gated, a.group);
-  void* params[] = {&a, &L};
-  return run(fn, dim3((unsigned)((int64_t)L.tiles_m * L.tiles_n)), T.waves * 64, 0, params, stream);
+  const int64_t step = geh::rows_per_launch(T.bm, L.tiles_n, T.waves * 64), all = a.m;
+  const char* x = static_cast<const char*>(a.x);
+  char* d = static_cast<char*>(a.D);
+  for (int64_t at = 0; at < all; at += step) {
+    a.m = std::min(step, all - at);
+    a.x = x + at * a.k * 2;
+    a.D = d + at * a.n * (a.out == F32 ? 4 : 2);
+    L.tiles_m = (int32_t)gew4::ceil_div(a.m, T.bm);
+    void* params[] = {&a, &L};
+    if (ge_status_t st = run(fn, dim3((unsigned)((int64_t)L.tiles_m * L.tiles_n)), T.waves * 64, 0, params, stream); st != GE_OK)
+      return st;
+  }
+  return GE_OK;
 }
 
 ge_status_t multiply(int64_t m, int64_t n, int64_t k, int64_t group, ge_dtype_t dt, ge_dtype_t out, bool gated, int ep,
@@ -351,7 +362,16 @@ ge_status_t multiply(int64_t m, int64_t n, int64_t k, int64_t group, ge_dtype_t 
   return gated ? skinny<BF16, true>(a, chunks, cus, stream) : skinny<BF16, false>(a, chunks, cus, stream);
 }
 
-dim3 waves(int64_t units) { return dim3((unsigned)((units + 3) / 4)); }
+// A kernel with a wave for each unit, four to a workgroup: units from `first` on, in launches of fewer
+// than 2^32 lanes.
+ge_status_t run_units(const void* fn, int64_t& first, int64_t units, void** params, void* stream) {
+  const int64_t most = geh::rows_per_launch(4, 1, 256);
+  for (first = 0; first < units; first += most)
+    if (ge_status_t st = run(fn, dim3((unsigned)gew4::ceil_div(std::min(most, units - first), 4)), 256, 0, params, stream);
+        st != GE_OK)
+      return st;
+  return GE_OK;
+}
 
 }  // namespace
 }  // namespace gek
@@ -371,13 +391,13 @@ ge_status_t gemm_epilog_w4_quantize(int64_t rows, int64_t k, ge_dtype_t src_dt, 
   int cus = 0;
   if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
   gek::W4Weight w = gek::weight(rows, k, group, halves, codes, scales, zeros);
-  int64_t units = w.rgs * halves * (group > gew4::kTileK ? w.groups : w.kt);
+  int64_t first = 0, units = w.rgs * halves * (group > gew4::kTileK ? w.groups : w.kt);
   int d = (int)dt, sym = symmetric != 0;
-  void* params[] = {&src, &ld, &w, &d, &sym, &units};
+  void* params[] = {&src, &ld, &w, &d, &sym, &first, &units};
   const void* fn = src_dt == GE_F32   ? gek::quantize_of<gek::F32>(group)
                    : src_dt == GE_F16 ? gek::quantize_of<gek::F16>(group)
                                       : gek::quantize_of<gek::BF16>(group);
-  return gek::run(fn, gek::waves(units), 256, 0, params, stream);
+  return gek::run_units(fn, first, units, params, stream);
 }
 
 ge_status_t gemm_epilog_w4_pack(int64_t rows, int64_t k, int64_t group, int halves, const void* src_codes,
@@ -389,9 +409,9 @@ ge_status_t gemm_epilog_w4_pack(int64_t rows, int64_t k, int64_t group, int halv
   int cus = 0;
   if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
   gek::W4Weight w = gek::weight(rows, k, group, halves, codes, scales, zeros);
-  int64_t units = w.rgs * halves * w.kt;
-  void* params[] = {&src_codes, &src_scales, &src_zeros, &w, &units};
-  return gek::run(reinterpret_cast<const void*>(&gek::w4_pack_kernel), gek::waves(units), 256, 0, params, stream);
+  int64_t first = 0, units = w.rgs * halves * w.kt;
+  void* params[] = {&src_codes, &src_scales, &src_zeros, &w, &first, &units};
+  return gek::run_units(reinterpret_cast<const void*>(&gek::w4_pack_kernel), first, units, params, stream);
 }
 
 ge_status_t gemm_epilog_w4_dequantize(int64_t rows, int64_t k, int64_t group, int halves, ge_dtype_t dt,
@@ -402,13 +422,13 @@ ge_status_t gemm_epilog_w4_dequantize(int64_t rows, int64_t k, int64_t group, in
   int cus = 0;
   if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
   gek::W4Weight w = gek::weight(rows, k, group, halves, codes, scales, zeros);
-  int64_t units = w.rgs * halves * w.kt;
+  int64_t first = 0, units = w.rgs * halves * w.kt;
   int d = (int)dt;
-  void* params[] = {&w, &d, &dst, &ld, &units};
+  void* params[] = {&w, &d, &dst, &ld, &first, &units};
   const void* fn = dst_dt == GE_F32   ? reinterpret_cast<const void*>(&gek::w4_dequantize_kernel<gek::F32>)
                    : dst_dt == GE_F16 ? reinterpret_cast<const void*>(&gek::w4_dequantize_kernel<gek::F16>)
                                       : reinterpret_cast<const void*>(&gek::w4_dequantize_kernel<gek::BF16>);
-  return gek::run(fn, gek::waves(units), 256, 0, params, stream);
+  return gek::run_units(fn, first, units, params, stream);
 }
 
 ge_status_t gemm_epilog_w4_matmul(int64_t m, int64_t n, int64_t k, int64_t group, ge_dtype_t dt, ge_dtype_t out,

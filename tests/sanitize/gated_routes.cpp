@@ -3,7 +3,9 @@
 // Reads lines of
 //   forward m n k dt | down m d n dt | gradient m n d dt | product M N K dt lay |
 //   w4 m n k group gated chunks
-// (dt 0 f32, 1 f16, 2 bf16) and prints a name for each.
+// (dt 0 f32, 1 f16, 2 bf16) and prints a name for each, and of
+//   rows n gated | w4rows n gated tile
+// and prints how many rows one launch takes.
 #include <cstdio>
 #include <cstring>
 
@@ -40,6 +42,17 @@ int main() {
       const int cfg = gew4h::choose(a, b, c, d, e != 0, f != 0, kCus);
       if (cfg < 0) std::printf("few\n");
       else std::printf("%d x %d\n", gew4::kTiles[cfg].bm, gew4::kTiles[cfg].bn);
+      continue;
+    }
+    if (!std::strcmp(op, "rows")) {
+      if (std::scanf("%ld %ld", &a, &b) != 2) return 1;
+      std::printf("%ld\n", (long)gegh::launch_rows(a, b != 0));
+      continue;
+    }
+    if (!std::strcmp(op, "w4rows")) {
+      if (std::scanf("%ld %ld %ld", &a, &b, &c) != 3) return 1;
+      const gew4::W4TileCfg& T = gew4::kTiles[c];
+      std::printf("%ld\n", (long)geh::rows_per_launch(T.bm, gew4::ceil_div(b ? 2 * a : a, T.bn), T.waves * 64));
       continue;
     }
     if (std::scanf("%ld %ld %ld %ld", &a, &b, &c, &d) != 4) return 1;

@@ -53,3 +53,18 @@ def test_backward(routes):
 def test_w4(routes):
     got = routes(*(line("w4", m, n, k, group, gated, k % 8 == 0) for m, n, k, group, gated in S.W4))
     assert got == list(S.W4.values())
+
+
+def test_lanes_of_a_launch(routes):
+    """A launch has fewer than 2^32 lanes, whichever kernel takes its rows."""
+    cdiv = lambda a, b: -(-a // b)   # noqa: E731
+    for n in (1, 7, 8, 32, 33, 64, 65, 100, 2752, 11008, 1 << 20):
+        for gated in (0, 1):
+            rows = int(routes(line("rows", n, gated))[0])
+            assert rows >= 256 and rows % 256 == 0
+            # tiles and lanes of the general kernel and of the tile kernels (gated: half their columns)
+            for bm, bn, lanes in ((64, 64, 256), (128, 128, 256), (128, 128, 512), (128, 256, 512), (192, 256, 512), (256, 256, 512)):
+                assert cdiv(rows, bm) * cdiv(n, bn // (1 + gated)) * lanes < 1 << 32, (n, gated, bm, bn)
+            for tile, (bm, bn) in enumerate(((256, 256), (192, 256), (128, 128), (64, 128))):
+                rows = int(routes(line("w4rows", n, gated, tile))[0])
+                assert rows >= bm and rows % bm == 0 and rows // bm * cdiv(n * (1 + gated), bn) * 512 < 1 << 32
