@@ -48,7 +48,7 @@ EXPORTS = ("gemm_epilog_plan", "gemm_epilog_plan_ex", "gemm_epilog_plan_info", "
            "gemm_epilog_mx_execute", "gemm_epilog_mx_free",
            "gemm_epilog_rms_norm", "gemm_epilog_rms_norm_workspace_bytes", "gemm_epilog_rms_norm_backward",
            "gemm_epilog_gated_forward", "gemm_epilog_gated_down", "gemm_epilog_gated_workspace_bytes",
-           "gemm_epilog_gated_backward",
+           "gemm_epilog_gated_backward", "gemm_epilog_gated_lost_waits",
            "gemm_epilog_w4_code_bytes", "gemm_epilog_w4_scale_count", "gemm_epilog_w4_quantize", "gemm_epilog_w4_pack",
            "gemm_epilog_w4_dequantize", "gemm_epilog_w4_matmul", "gemm_epilog_w4_gated")
 MXFP4, MXFP8 = 0, 1
@@ -143,6 +143,7 @@ def load() -> ctypes.CDLL:
             ("gated_down", [i64, i64, i64, c_int, vp, vp, vp, vp], c_int),
             ("gated_workspace_bytes", [i64, i64, i64, i64, c_int], size),
             ("gated_backward", [i64, i64, i64, i64, c_int, c_int, *[vp] * 10, c_int, vp, size, vp], c_int),
+            ("gated_lost_waits", [vp, ctypes.POINTER(ctypes.c_uint32)], c_int),
             ("w4_code_bytes", [i64, i64, c_int], size),
             ("w4_scale_count", [i64, i64, i64, c_int], size),
             ("w4_quantize", [i64, i64, c_int, vp, i64, i64, c_int, c_int, c_int, vp, vp, vp, vp], c_int),

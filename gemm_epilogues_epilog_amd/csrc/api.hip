@@ -39,6 +39,7 @@ struct ge_plan {
   void* ws;                // device workspace
   uint32_t epoch;          // execute counter, 1 .. 2^31 - 1
   uint32_t spin_limit;     // polls of a split-tail owner's bounded wait
+  uint32_t* lost;          // count of its waits that ran out; null: in the workspace
   std::string desc;
 };
 
@@ -47,6 +48,13 @@ namespace {
 // Default polls of a split-tail owner's wait for a partial (about a second);
 // GE_SK_SPIN=n overrides it (failure-path tests force a wait to run out).
 constexpr uint32_t kSkSpinDefault = 1u << 20;
+uint32_t spin_limit() {
+  if (const char* e = std::getenv("GE_SK_SPIN")) {
+    const long v = std::atol(e);
+    if (v >= 0 && v <= (long)kSkSpinDefault) return (uint32_t)v;
+  }
+  return kSkSpinDefault;
+}
 
 // Zero `bytes` of device memory and wait for it, on a stream of its own (default
 // priority) so that other streams are not synchronised.
@@ -111,11 +119,8 @@ ge_status_t build_plan(int64_t m, int64_t n, int64_t k, ge_dtypes_t dt, ge_epilo
   h->allow_persist = allow_persist;
   h->L = L;
   h->gemm = fn;
-  h->spin_limit = kSkSpinDefault;
-  if (const char* e = std::getenv("GE_SK_SPIN")) {
-    const long v = std::atol(e);
-    if (v >= 0 && v <= (long)kSkSpinDefault) h->spin_limit = (uint32_t)v;
-  }
+  h->spin_limit = spin_limit();
+  h->lost = nullptr;
   if (L.ws_bytes) {
     if (hipMalloc(&h->ws, L.ws_bytes) != hipSuccess) {
       delete h;
@@ -164,6 +169,7 @@ ge_status_t enqueue(const ge_plan& h, char* ws, uint32_t epoch, const void* A, c
   a.sk_wgs = L.sk_wgs;
   a.sk_partial = L.sk_wgs ? reinterpret_cast<float*>(ws + L.off_sk_partial) : nullptr;
   a.sk_flag = L.sk_wgs ? reinterpret_cast<uint32_t*>(ws + L.off_sk_flag) : nullptr;
+  a.sk_lost = h.lost ? h.lost : L.sk_wgs ? a.sk_flag + gek::kSkLostWord : nullptr;
   a.sk_spin_limit = h.spin_limit;
   a.persist_grid = L.persist_grid;
   a.epoch = epoch;
@@ -206,6 +212,34 @@ struct ScratchState {
   uint32_t epoch[kMaxDevices] = {};  // execute counter per device
 };
 ScratchState g_scratch;
+
+// Waits of products without a plan that ran out, counted on each device (addressed as `scratch` is)
+// and never cleared; what was reported of it is kept here.
+static __device__ uint32_t lost_count;
+struct LostState {
+  std::mutex mu;
+  uint32_t* ptr[kMaxDevices] = {};
+  uint32_t reported[kMaxDevices] = {};
+};
+LostState g_lost;
+
+// The current device's count; g_lost.mu is held.
+ge_status_t lost_word_locked(int* dev, uint32_t** word) {
+  if (hipGetDevice(dev) != hipSuccess) return GE_ERR_HIP;
+  if (*dev < 0 || *dev >= kMaxDevices) return GE_ERR_NOT_SUPPORTED;
+  if (!g_lost.ptr[*dev]) {
+    void* p = nullptr;
+    if (hipGetSymbolAddress(&p, HIP_SYMBOL(lost_count)) != hipSuccess || !p) return GE_ERR_HIP;
+    g_lost.ptr[*dev] = static_cast<uint32_t*>(p);
+  }
+  *word = g_lost.ptr[*dev];
+  return GE_OK;
+}
+ge_status_t lost_word(uint32_t** word) {
+  int dev = 0;
+  std::lock_guard<std::mutex> lock(g_lost.mu);
+  return lost_word_locked(&dev, word);
+}
 
 }  // namespace
 
@@ -250,7 +284,10 @@ ge_status_t run_product(int64_t m, int n, int k, ge_dtype_t dt, const geh::Layou
   h.gemm = lookup(dt, GE_EPILOG_NONE, L.cfg, L.lay);
   if (!h.gemm) return GE_ERR_NOT_SUPPORTED;
   h.ws = ws;
-  h.spin_limit = kSkSpinDefault;
+  h.spin_limit = spin_limit();
+  h.lost = nullptr;
+  if (L.sk_wgs)
+    if (ge_status_t st = lost_word(&h.lost); st != GE_OK) return st;
   if (L.sk_wgs && !cleared) {
     uint32_t* words = reinterpret_cast<uint32_t*>(ws + L.off_sk_flag);
     int nw = gek::kSkFlagWords;
@@ -468,11 +505,8 @@ ge_status_t gemm_epilog_execute_noalloc(int64_t m, int64_t n, int64_t k, ge_dtyp
   h.gemm = lookup(dt.ab, geh::gemm_epilog_of(ep), cfg, lay);
   if (!h.gemm) return GE_ERR_NOT_SUPPORTED;
   h.ws = ws;
-  h.spin_limit = kSkSpinDefault;
-  if (const char* e = std::getenv("GE_SK_SPIN")) {
-    const long v = std::atol(e);
-    if (v >= 0 && v <= (long)kSkSpinDefault) h.spin_limit = (uint32_t)v;
-  }
+  h.spin_limit = spin_limit();
+  h.lost = nullptr;
   return enqueue(h, ws, epoch, A, B, bias, D, aux, bgrad, s);
 }
 
@@ -487,6 +521,23 @@ ge_status_t gemm_epilog_lost_waits(ge_handle_t h, void* stream, uint32_t* count)
       hipMemsetAsync(word, 0, sizeof(v), s) != hipSuccess || hipStreamSynchronize(s) != hipSuccess)
     return GE_ERR_HIP;
   *count = v;
+  return GE_OK;
+}
+
+ge_status_t gemm_epilog_gated_lost_waits(void* stream, uint32_t* count) {
+  if (!count) return GE_ERR_NULL_POINTER;
+  *count = 0;
+  int cus = 0, dev = 0;
+  if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_lost.mu);
+  uint32_t* word = nullptr;
+  if (ge_status_t st = lost_word_locked(&dev, &word); st != GE_OK) return st;
+  uint32_t v = 0;
+  if (hipMemcpyAsync(&v, word, sizeof(v), hipMemcpyDeviceToHost, s) != hipSuccess || hipStreamSynchronize(s) != hipSuccess)
+    return GE_ERR_HIP;
+  *count = v - g_lost.reported[dev];
+  g_lost.reported[dev] = v;
   return GE_OK;
 }
 

@@ -1234,7 +1234,7 @@ constexpr int kDeviceScope = 16;   // cache-policy bit sc1 of a buffer instructi
 // the partial swaps 0 -> epoch once its stores have completed. The owner waits (a
 // bounded spin, p.sk_spin_limit polls, about a second by default) for the epoch, adds
 // the partial and swaps epoch -> 0. If the wait runs out, the owner swaps 0 -> kSkAbort
-// (unless the epoch arrived meanwhile), counts the loss in p.sk_flag[kSkLostWord], gives
+// (unless the epoch arrived meanwhile), counts the loss in p.sk_lost, gives
 // the tile's D NaN; the publisher that finds kSkAbort resets the flag to 0 instead of
 // publishing. So every flag is 0 again when the kernel ends, lost wait or not, and a
 // later execute with the same epoch (a replay of a captured graph) never finds a stale
@@ -1293,7 +1293,7 @@ __device__ __forceinline__ uint32_t sk_wait_flags(uint32_t* flags, int np, uint3
 // before it waits and finishes after its wait, so the last to finish finds both
 // complete and nothing touches them after it: the counters are 0 when the kernel ends,
 // lost wait or not, and a replayed graph starts from clean counters. A wait that runs
-// out is counted in the flag region's last word and gives NaN for the run's part.
+// out is counted in p.sk_lost and gives NaN for the run's part.
 template <int DT, int EP, int BM, int BN, int WM, int WN, int BK, int STAGES, bool ILV, int CW>
 __device__ __forceinline__ void sk_reduce_scatter(const Args& p, char* smem, int q, int S, uint32_t& lost_any) {
   using C = DtlCfg<BM, BN, WM, WN, BK, STAGES>;
@@ -1364,7 +1364,7 @@ __device__ __forceinline__ void sk_reduce_scatter(const Args& p, char* smem, int
       if (!all) __builtin_amdgcn_s_sleep(2);
     }
     if (!all) all = __hip_atomic_load(cnt, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)S;
-    if (!all) __hip_atomic_fetch_add(p.sk_flag + kSkLostWord, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (!all) __hip_atomic_fetch_add(p.sk_lost, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     lost_any = all ? 0u : 1u;
   }
   wait_lgkmcnt<0>();
@@ -1509,7 +1509,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 1) void gemm_sk_kernel(
     if (w == 0) {
       const uint32_t lost = sk_wait_flags(p.sk_flag + r + 1, run.last - r, p.epoch, p.sk_spin_limit, lane);
       if (lane == 0) {
-        if (lost) __hip_atomic_fetch_add(p.sk_flag + kSkLostWord, lost, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (lost) __hip_atomic_fetch_add(p.sk_lost, lost, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         lost_any = lost;
       }
     }

@@ -8,6 +8,7 @@ g = gated_backward(dy, x, w, z, w_down=w_down, h=h)        # g.dx, g.dw, g.dw_do
 Tokens along the rows; w (2 n, k) holds the gate's rows, then the up projection's. f32, f16
 and bf16, any sizes; argument marshalling only.
 """
+import ctypes
 from typing import NamedTuple, Optional
 
 import torch
@@ -107,7 +108,7 @@ def gated_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch.
                    stream=None) -> GatedGrads:
     """From dy (m, d), the gradient of y = h w_down^T; without w_down, dy (m, n) is the gradient
     of h. dw_down comes back where w_down and h are given, dbias where bias_grad names its type
-    (x's or "f32")."""
+    (x's or "f32"). A tile of dx is NaN where a wait ran out (gated_lost_waits)."""
     m, k = _rows2(x, "x")
     dev, t = x.device, x.dtype
     a = _gate(act)
@@ -139,3 +140,15 @@ def gated_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch.
                                         ptr(dwd), ptr(db), DTYPES[bias_grad or "f32"], ws.data_ptr(), size,
                                         _stream(stream, dev)), "gemm_epilog_gated_backward")
     return GatedGrads(dx, dw, dwd, db)
+
+
+def gated_lost_waits(stream=None) -> int:
+    """Synchronise the stream and return how many waits of gated_backward ran out on the current
+    device since the last call (their tiles of dx hold NaN)."""
+    if stream is None:
+        stream = torch.cuda.current_stream().cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    n = ctypes.c_uint32(0)
+    _check(load().gemm_epilog_gated_lost_waits(stream, ctypes.byref(n)), "gemm_epilog_gated_lost_waits")
+    return int(n.value)

@@ -533,12 +533,21 @@ size_t gemm_epilog_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_
  *   workspace : device, 256-byte aligned, workspace_bytes >= gemm_epilog_gated_workspace_bytes
  *            (else GE_ERR_SCRATCH), used until the work is done.
  * dX may share its k loop between workgroups that wait for each other's sums, bounded, as a split
- * plan does (see gemm_epilog_lost_waits): a wait that runs out gives that tile NaN.
+ * plan does (see gemm_epilog_lost_waits): a wait that runs out gives that tile NaN and is counted
+ * (gemm_epilog_gated_lost_waits).
  */
 ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t d, ge_dtype_t dt, ge_gate_t act,
                                        const void* dy, const void* x, const void* w, const void* z, const void* h,
                                        const void* w_down, void* dx, void* dw, void* dw_down, void* dbias,
                                        ge_dtype_t vec, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gemm_epilog_gated_lost_waits - how many waits of gemm_epilog_gated_backward ran out on the current
+ * device, in calls of the whole process, captured and replayed ones too, since the last call of this
+ * function there (normally 0). Synchronises `stream` first (not while it is being captured), so the
+ * calls enqueued on it are counted; those of other streams as far as they have come.
+ */
+ge_status_t gemm_epilog_gated_lost_waits(void* stream, uint32_t* count);
 
 /* ---- 4-bit weights with group scales ----------------------------------------------------
  * W (rows, k) = (q - z) s: codes q of 0 .. 15, and for each `group` consecutive k values of a row
