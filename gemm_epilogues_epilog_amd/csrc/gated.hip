@@ -13,19 +13,27 @@
 #include "gated_host.hpp"
 #include "gated_tiles.hpp"
 #include "product.hpp"
+#include "tiles.hpp"
 
 namespace gek {
 namespace {
 
-// Eight values of a row of len from pos on (zeros past its end), widened.
-template <int DT>
+// Eight values of a row of len from pos on (zeros past its end), widened. FLAT (rows of at least
+// eight): without a branch, so that several are on their way at once.
+template <int DT, bool FLAT = false>
 __device__ __forceinline__ void load8(const void* row, int64_t pos, int64_t len, float (&v)[8]) {
   constexpr int ES = Tr<DT>::es, E = 16 / ES;
   const char* p = static_cast<const char*>(row);
   i32x4 raw[8 / E];
 #pragma unroll
-  for (int j = 0; j < 8 / E; ++j)
-    raw[j] = pos + 8 <= len ? load16(p + (pos + j * E) * ES) : load_end<ES>(p, pos + j * E, len);
+  for (int j = 0; j < 8 / E; ++j) {
+    if constexpr (FLAT) {
+      const int64_t to = pos + j * E, a = to < len - E ? to : len - E;
+      raw[j] = shift_down<ES>(load16(p + a * ES), (int)(to - a < E ? to - a : E));
+    } else {
+      raw[j] = pos + 8 <= len ? load16(p + (pos + j * E) * ES) : load_end<ES>(p, pos + j * E, len);
+    }
+  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     if constexpr (DT == F32) v[e] = __int_as_float(raw[e / 4][e % 4]);
@@ -70,24 +78,85 @@ __global__ __launch_bounds__(256) void dz_kernel(const void* dh, const void* z, 
   store8<DT>(o + n * es, pos, n, du);
 }
 
-// partial[part][col], or with one part out[col] of type vec: sums of the columns of a dense (m, cols)
-// matrix over the part's rows, in a fixed order: four rows side by side, each in ascending order, then
-// those four in order. Bound by memory, with few rows by its start (77 x 2000: 4.5 us).
-template <int DT>
-__global__ __launch_bounds__(256) void colsum_kernel(const void* x, int64_t m, int64_t cols, float* partial, void* out,
+// The four rows' sums of a workgroup, V values for each of 64 lanes, in order.
+template <int V>
+__device__ __forceinline__ float four_rows(const float (&sums)[4][64][V + 1], int c, int e) {
+  return ((sums[0][c][e] + sums[1][c][e]) + sums[2][c][e]) + sums[3][c][e];
+}
+
+// partial[part][2 n], or with one part out[2 n] of type vec: sums of the columns of dZ over the part's rows,
+// from dH and Z as dz_kernel has them, before their rounding, in a fixed order: four rows side by side,
+// each in ascending order, then those four in order. Bound by memory.
+template <int DT, int DH>
+__global__ __launch_bounds__(256) void dz_sums_kernel(const void* dh, const void* z, int64_t m, int64_t n, int act,
+                                                      float* partial, void* out, int vec) {
+  constexpr int64_t es = Tr<DT>::es;
+  constexpr int U = 4;
+  __shared__ float sums[4][64][17];
+  const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int64_t pos = ((int64_t)blockIdx.x * 64 + c) * 8;
+  const int64_t r0 = m * blockIdx.y / gridDim.y, r1 = m * (blockIdx.y + 1) / gridDim.y;
+  float sg[8] = {}, su[8] = {};
+  if (pos < n) {
+    const auto add = [&](auto a, auto flat) {
+      constexpr bool FLAT = decltype(flat)::value;
+      for (int64_t r = r0 + q; r < r1; r += 4 * U) {
+        float d[U][8], g[U][8], u[U][8];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int64_t at = r + 4 * i < r1 ? r + 4 * i : r;
+          load8<DH, FLAT>(static_cast<const char*>(dh) + at * n * Tr<DH>::es, pos, n, d[i]);
+          load8<DT, FLAT>(static_cast<const char*>(z) + at * 2 * n * es, pos, n, g[i]);
+          load8<DT, FLAT>(static_cast<const char*>(z) + (at * 2 + 1) * n * es, pos, n, u[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float v, s;
+            gate_slope<decltype(a)::value, DT == F32>(g[i][e], v, s);
+            sg[e] += r + 4 * i < r1 ? d[i][e] * u[i][e] * s : 0.0f;
+            su[e] += r + 4 * i < r1 ? d[i][e] * v : 0.0f;
+          }
+      }
+    };
+    with_gate(act, [&](auto a) {
+      if (n >= 8) add(a, std::true_type{});
+      else add(a, std::false_type{});
+    });
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    sums[q][c][e] = sg[e];
+    sums[q][c][8 + e] = su[e];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 1024; i += 256) {
+    const int64_t col = (int64_t)blockIdx.x * 512 + i % 512;
+    if (col < n) {
+      const float v = four_rows<16>(sums, i % 512 / 8, i / 512 * 8 + i % 8);
+      const int64_t to = i / 512 * n + col;
+      if (gridDim.y == 1) store_vec(out, vec, to, v);
+      else partial[(int64_t)blockIdx.y * 2 * n + to] = v;
+    }
+  }
+}
+
+// The same of a dense (m, cols) matrix in fp32, cols a multiple of 8; with few rows bound by its start
+// (4 us).
+__global__ __launch_bounds__(256) void colsum_kernel(const float* x, int64_t m, int64_t cols, float* partial, void* out,
                                                      int vec) {
   constexpr int U = 4;
   __shared__ float sums[4][64][9];
   const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
   const int64_t pos = ((int64_t)blockIdx.x * 64 + c) * 8;
   const int64_t r0 = m * blockIdx.y / gridDim.y, r1 = m * (blockIdx.y + 1) / gridDim.y;
-  const char* p = static_cast<const char*>(x);
   float s[8] = {};
   if (pos < cols) {
     for (int64_t r = r0 + q; r < r1; r += 4 * U) {
       float v[U][8];
 #pragma unroll
-      for (int i = 0; i < U; ++i) load8<DT>(p + (r + 4 * i < r1 ? r + 4 * i : r) * cols * Tr<DT>::es, pos, cols, v[i]);
+      for (int i = 0; i < U; ++i) __builtin_memcpy(v[i], x + (r + 4 * i < r1 ? r + 4 * i : r) * cols + pos, 32);
 #pragma unroll
       for (int i = 0; i < U; ++i)
 #pragma unroll
@@ -100,7 +169,7 @@ __global__ __launch_bounds__(256) void colsum_kernel(const void* x, int64_t m, i
   for (int i = threadIdx.x; i < 512; i += 256) {
     const int64_t col = (int64_t)blockIdx.x * 512 + i;
     if (col < cols) {
-      const float v = ((sums[0][i / 8][i % 8] + sums[1][i / 8][i % 8]) + sums[2][i / 8][i % 8]) + sums[3][i / 8][i % 8];
+      const float v = four_rows<8>(sums, i / 8, i % 8);
       if (gridDim.y == 1) store_vec(out, vec, col, v);
       else partial[(int64_t)blockIdx.y * cols + col] = v;
     }
@@ -181,7 +250,7 @@ ge_status_t product(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay, con
 // The tile kernels with the gated epilogues: H (and Z) of X and W, or dZ of dY, Wd and Z.
 ge_status_t gated_tiles(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool backward, int act, const void* A,
                         const void* B, const void* bias, int vec, const void* z, void* D, void* z_out, uint32_t* clear,
-                        int cus, hipStream_t s) {
+                        float* sums, int64_t* sum_rows, int cus, hipStream_t s) {
   geh::Layout L;
   if (ge_status_t st = gegh::gated_layout(m, n, k, dt, backward, cus, &L); st != GE_OK) return st;
   Args a = {};
@@ -202,22 +271,39 @@ ge_status_t gated_tiles(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool bac
   a.z = z;
   a.z_out = z_out;
   a.clear = clear;
+  a.sums = sums;
+  if (sums) *sum_rows = (int64_t)L.tiles_m * (kTiles[L.cfg].bm / kTiles[L.cfg].wm);
   return get_launch_gated((int)dt, backward, L.cfg)(a, L.tiles_m * L.tiles_n, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
 }
 
-ge_status_t column_sums(const void* x, int64_t m, int64_t cols, ge_dtype_t dt, void* out, ge_dtype_t vec, float* partial,
-                        hipStream_t s) {
-  int parts = m ? (int)gegh::colsum_parts(m, cols) : 0;
+// out[cols] of type vec from `rows` rows of sums; what lies behind them is scratch.
+ge_status_t add_sums(float* sums, int64_t rows, int64_t cols, void* out, ge_dtype_t vec, hipStream_t s) {
+  const int parts = rows ? (int)gegh::colsum_parts(rows, cols) : 0;
+  float* partial = sums + rows * cols;
+  int v = (int)vec;
   if (parts) {
-    const void* fn = dt == GE_F32   ? reinterpret_cast<const void*>(&colsum_kernel<F32>)
-                     : dt == GE_F16 ? reinterpret_cast<const void*>(&colsum_kernel<F16>)
-                                    : reinterpret_cast<const void*>(&colsum_kernel<BF16>);
-    int v = (int)vec;
-    void* params[] = {&x, &m, &cols, &partial, &out, &v};
-    if (launch(fn, dim3((unsigned)((cols + 511) / 512), parts), 256, params, s) != hipSuccess) return GE_ERR_HIP;
+    void* params[] = {&sums, &rows, &cols, &partial, &out, &v};
+    if (launch(reinterpret_cast<const void*>(&colsum_kernel), dim3((unsigned)((cols + 511) / 512), parts), 256, params, s) != hipSuccess)
+      return GE_ERR_HIP;
     if (parts == 1) return GE_OK;
   }
-  return launch_bgrad_reduce(partial, parts, cols, out, (int)vec, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
+  return launch_bgrad_reduce(partial, parts, cols, out, v, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
+}
+
+template <int DT>
+const void* dz_sums_of(bool f32_dh) {
+  return f32_dh ? reinterpret_cast<const void*>(&dz_sums_kernel<DT, F32>) : reinterpret_cast<const void*>(&dz_sums_kernel<DT, DT>);
+}
+// out[2 n] of type vec: column sums of dZ from dH and Z, by way of `partial`.
+ge_status_t dz_sums(const void* dh, bool f32_dh, const void* z, int64_t m, int64_t n, ge_dtype_t dt, int act, void* out,
+                    ge_dtype_t vec, float* partial, hipStream_t s) {
+  const int parts = (int)gegh::dz_parts(m, n);
+  const void* fn = dt == GE_F32 ? dz_sums_of<F32>(f32_dh) : dt == GE_F16 ? dz_sums_of<F16>(f32_dh) : dz_sums_of<BF16>(f32_dh);
+  int v = (int)vec;
+  void* params[] = {&dh, &z, &m, &n, &act, &partial, &out, &v};
+  if (launch(fn, dim3((unsigned)((n + 511) / 512), parts), 256, params, s) != hipSuccess) return GE_ERR_HIP;
+  if (parts == 1) return GE_OK;
+  return launch_bgrad_reduce(partial, parts, 2 * n, out, v, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
 }
 
 ge_status_t status(hipError_t e) { return e == hipSuccess ? GE_OK : GE_ERR_HIP; }
@@ -232,7 +318,7 @@ ge_status_t forward_rows(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, ge_gate
     case gegh::Kernel::kFew:
       return status(launch_skinny(m, n, k, (int)dt, true, (int)act, x, w, bias, (int)vec, h, z, cus, s));
     case gegh::Kernel::kTiles:
-      return gated_tiles(m, n, k, dt, false, (int)act, x, w, bias, (int)vec, nullptr, h, z, nullptr, cus, s);
+      return gated_tiles(m, n, k, dt, false, (int)act, x, w, bias, (int)vec, nullptr, h, z, nullptr, nullptr, nullptr, cus, s);
     default:
       return status(general(m, n, k, dt, 6, x, w, h, false, 1, bias, (int)vec, (int)act, z, cus, s));
   }
@@ -314,11 +400,16 @@ ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t 
       if (ge_status_t st = gegh::fast_layout(m, k, 2 * n, dt, 0, cus, scratch_bytes, &L); st != GE_OK) return st;
       if (L.sk_wgs) flags = reinterpret_cast<uint32_t*>(scratch + L.off_sk_flag);
     }
+    float* sums = reinterpret_cast<float*>(scratch + geh::kSkFlagRegion);   // (beside the flags)
     const bool on16 = gegh::aligned(dy, 16) && gegh::aligned(w_down, 16) && gegh::aligned(z, 16);
     if (w_down && gegh::gradient_kernel(m, n, d, dt, on16) == gegh::Kernel::kTiles) {
-      if (ge_status_t st = gek::gated_tiles(m, n, d, dt, true, (int)act, dy, w_down, nullptr, 0, z, dz, nullptr, flags, cus, s);
+      int64_t sum_rows = 0;
+      if (ge_status_t st = gek::gated_tiles(m, n, d, dt, true, (int)act, dy, w_down, nullptr, 0, z, dz, nullptr, flags,
+                                            dbias ? sums : nullptr, &sum_rows, cus, s);
           st != GE_OK)
         return st;
+      if (dbias)
+        if (ge_status_t st = gek::add_sums(sums, sum_rows, 2 * n, dbias, vec, s); st != GE_OK) return st;
       dh = nullptr;
     } else if (w_down) {
       dh = ws + at.dh;
@@ -333,6 +424,8 @@ ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t 
     void* params[] = {&dh, &z, &dz, &m, &n, &a};
     const int64_t chunks = m * ((n + 7) / 8);
     if (dh && gek::launch(fn, dim3((unsigned)((chunks + 255) / 256)), 256, params, s) != hipSuccess) return GE_ERR_HIP;
+    if (dh && dbias)
+      if (ge_status_t st = gek::dz_sums(dh, f32, z, m, n, dt, a, dbias, vec, sums, s); st != GE_OK) return st;
     if (dx)
       if (ge_status_t st = gek::product(m, k, 2 * n, dt, 0, dz, w, dx, scratch, scratch_bytes, !dh, cus, s); st != GE_OK)
         return st;
@@ -341,11 +434,8 @@ ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t 
     if (ge_status_t st = gek::product(2 * n, k, m, dt, 1, dz, x, dw, scratch, scratch_bytes, false, cus, s); st != GE_OK) return st;
   if (dw_down)
     if (ge_status_t st = gek::product(d, n, m, dt, 1, dy, h, dw_down, scratch, scratch_bytes, false, cus, s); st != GE_OK) return st;
-  if (dbias)
-    if (ge_status_t st =
-            gek::column_sums(dz, m, 2 * n, dt, dbias, vec, reinterpret_cast<float*>(scratch), s);
-        st != GE_OK)
-      return st;
+  if (dbias && m == 0)
+    if (ge_status_t st = gek::add_sums(nullptr, 0, 2 * n, dbias, vec, s); st != GE_OK) return st;
   return GE_OK;
 }
 

@@ -2,10 +2,16 @@
 //   GATED   the wave's WN tile columns are WN / 2 of the gate and the same WN / 2 of the up
 //           projection (blocks a and a + NB / 2 hold the same columns): H = act(G) * U, and Z =
 //           [G | U] if wanted;
-//   DGATED  the accumulators are dH: with G and U read from Z, dZ = [dH U a'(G) | dH a(G)].
+//   DGATED  the accumulators are dH: with G and U read from Z, dZ = [dH U a'(G) | dH a(G)], and the
+//           sums of its columns, for the bias, before its rounding.
 // Lane l holds row l % 32 of a block, register r column 8 (r / 4) + 4 (l / 32) + r % 4 (kernels.hpp).
 // 32 rows at a time go through 32 WN bytes (GATED) or 4 KB (DGATED) of scratch, so that memory
 // sees 16 bytes a lane and whole pieces of rows.
+//
+// dZ leaves rounded to the operands' type, as the matrix instruction takes it in dX and dW: half a step
+// of each term, independently, which adds as much to those gradients as their own rounding (root mean
+// square error against 64 bits: bf16 2.35e-3 instead of 1.66e-3, fp16 2.95e-4 instead of 2.09e-4). Two
+// 16-bit parts would keep fp32 and double two products of three.
 //
 // The product bounds both: 4096 x 2 x 11008 x 4096 bf16 592 us, 1250 TFLOP/s (the plain product with a
 // bias and ReLU at 4096 x 11008 x 4096: 1230), its matrix unit busy 76% of the cycles; dZ at 2048 x
@@ -153,6 +159,7 @@ __device__ __forceinline__ void dgated_tile(const Args& p, const f32x16 (&acc)[N
     }
   };
   const auto swz = [](int row) { return (row ^ (row >> 3)) & 7; };   // 16-byte units of 128-byte rows
+  float sum[NB] = {};   // of the column r16 of dG's eight, then of dU's, of this lane's chunk c
   Z z[2];
   load(0, z[0]);
   if (p.clear && blockIdx.x == 0)
@@ -169,16 +176,16 @@ __device__ __forceinline__ void dgated_tile(const Args& p, const f32x16 (&acc)[N
     }
     char* at = static_cast<char*>(p.D) + ((m0 + 32 * b) * ld + n0 + 32 * a) * 2;
     const __amdgpu_buffer_rsrc_t rg = rsrc(at), ru = rsrc(at + (int64_t)N * 2);
-    f32x4 d[2][2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        d[h][q] = *reinterpret_cast<const f32x4*>(scratch + (16 * h + r16) * 128 + (((2 * c + q) ^ swz(16 * h + r16)) << 4));
     const Z& zi = z[i & 1];
+    float t[16] = {};   // dG and dU of this lane's two rows
     with_gate(p.act, [&](auto act) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        const bool in = m0 + 32 * b + 16 * h + r16 < p.m;   // (a row past the last one is NaN where Wd is)
+        f32x4 d[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          d[q] = *reinterpret_cast<const f32x4*>(scratch + (16 * h + r16) * 128 + (((2 * c + q) ^ swz(16 * h + r16)) << 4));
         i32x4 og, ou;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -187,11 +194,13 @@ __device__ __forceinline__ void dgated_tile(const Args& p, const f32x16 (&acc)[N
           for (int e = 0; e < 2; ++e) {
             const float gv = T::widen((uint16_t)((uint32_t)zi.g[h][w] >> (16 * e)));
             const float uv = T::widen((uint16_t)((uint32_t)zi.u[h][w] >> (16 * e)));
-            const float dh = d[h][w / 2][2 * (w % 2) + e];
+            const float dh = d[w / 2][2 * (w % 2) + e];
             float v, s;
             gate_slope<decltype(act)::value, false>(gv, v, s);
             dg[e] = dh * uv * s;
             du[e] = dh * v;
+            t[2 * w + e] += in ? dg[e] : 0.0f;
+            t[8 + 2 * w + e] += in ? du[e] : 0.0f;
           }
           og[w] = (int)T::pack2(dg[0], dg[1]);
           ou[w] = (int)T::pack2(du[0], du[1]);
@@ -200,6 +209,22 @@ __device__ __forceinline__ void dgated_tile(const Args& p, const f32x16 (&acc)[N
         __builtin_amdgcn_raw_buffer_store_b128(ou, ru, offset(b, a, h), 0, 0);
       }
     });
+    if (p.sums) {
+      // the 16 lanes of the same columns: each step a lane hands half of its values to the lane that
+      // keeps those, and takes its own, until it has one of all rows
+#pragma unroll
+      for (int h = 8; h > 0; h >>= 1) {
+        const bool up = (r16 & h) != 0;
+#pragma unroll
+        for (int j = 0; j < h; ++j) {
+          const float give = up ? t[j] : t[j + h];
+          t[j] = (up ? t[j + h] : t[j]) + __shfl_xor(give, 4 * h);
+        }
+      }
+      sum[a] += t[0];
+      if (b == MB - 1 && n0 + 32 * a + 8 * c < N)
+        p.sums[m0 / (32 * MB) * ld + (r16 & 8 ? N : 0) + n0 + 32 * a + 8 * c + (r16 & 7)] = sum[a];
+    }
   }
 }
 

@@ -156,12 +156,22 @@ int64_t colsum_parts(int64_t m, int64_t cols) {
   return std::max<int64_t>(1, std::min(cdiv(m, 32), cdiv(1024, across)));
 }
 
+int64_t dz_parts(int64_t m, int64_t n) {
+  if (m <= 32) return 1;   // (no second kernel)
+  return std::max<int64_t>(1, std::min(cdiv(m, 16), cdiv(1024, cdiv(n, 512))));
+}
+
+// (the tiles: one for 32 rows at least, in whole tiles of 128)
+int64_t dz_sum_rows(int64_t m, int64_t n) { return std::max(cdiv(m, 128) * 4, dz_parts(m, n)); }
+
 BackwardSpace backward_space(int64_t m, int64_t n, int64_t k, int64_t d, ge_dtype_t dt) {
   BackwardSpace s = {0, 0, 0};
   if (m < 1 || m > kMaxBackwardTokens || !dim_ok(n) || !dim_ok(k) || !dim_ok(d) || !dtype_ok(dt)) return s;
   s.dh = align256((size_t)m * 2 * n * geh::elem_size(dt));
   s.scratch = s.dh + align256((size_t)m * n * 4);
-  size_t most = (size_t)colsum_parts(m, 2 * n) * 2 * n * 4;
+  // sums of dZ, and of those (where they are too many for one kernel)
+  const int64_t sums = dz_sum_rows(m, n);
+  size_t most = geh::kSkFlagRegion + (size_t)(sums + colsum_parts(sums, 2 * n)) * 2 * n * 4;
   geh::Layout L;
   if (fast_shape(m, k, 2 * n, dt, 0) && fast_layout(m, k, 2 * n, dt, 0, kCompute, ~(size_t)0, &L) == GE_OK)
     most = std::max(most, L.ws_bytes);

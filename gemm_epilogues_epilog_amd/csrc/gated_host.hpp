@@ -59,11 +59,16 @@ bool general_narrow(int64_t M, int64_t N, int64_t K, ge_dtype_t dt, int lay);
 // workgroups have at least 16 values of the product for each lane.
 int64_t launch_rows(int64_t n, bool gated);
 
-// Column sums of (m, 2 n) values: row ranges summed side by side.
+// Column sums: ranges of rows summed side by side.
 int64_t colsum_parts(int64_t m, int64_t cols);
+// Rows of the sums of dZ's columns: from dH and Z, one for 16 rows or more; from any kernel of dZ at most.
+int64_t dz_parts(int64_t m, int64_t n);
+int64_t dz_sum_rows(int64_t m, int64_t n);
 
-// The backward's workspace: dZ (m, 2 n), then dH in fp32 (only where the product and the
-// activations' gradient are separate kernels), then what one product or the column sums need.
+// The backward's workspace: dZ (m, 2 n), then dH in fp32 (written where the product and the
+// activations' gradient are separate kernels, held for any: whether the tiles take them also depends
+// on the pointers' alignment), then the flags of dX's split, beside them the column sums of dZ until
+// they are added up, and after that what one product needs.
 struct BackwardSpace {
   size_t dh, scratch, total;   // offsets; dZ is at 0
 };

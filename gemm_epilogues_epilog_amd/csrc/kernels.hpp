@@ -84,6 +84,9 @@ struct Args {
   int32_t act;
   const void* z;
   void* z_out;
+  // DGATED: receives the sums of dZ's columns over the rows of each wave, (tiles_m BM / WM, 2 n) in fp32,
+  // or null.
+  float* sums;
   // DGATED: kSkFlagWords words that the launch clears for the product after it, or null.
   uint32_t* clear;
 };

@@ -521,8 +521,10 @@ size_t gemm_epilog_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_
 
 /*
  * gemm_epilog_gated_backward - the block's gradients.
- *   dH = dY . Wd;  dG = dH U a'(G), dU = dH a(G), dZ = [dG | dU], rounded to dt;
+ *   dH = dY . Wd;  dG = dH U a'(G), dU = dH a(G), dZ = [dG | dU];
  *   dX = dZ . W, dW = dZ^T . X, dWd = dY^T . H, dbias = column sums of dZ (in a fixed order).
+ * dH and dZ are fp32. As the operand of dX and dW, dZ is rounded to dt (in fp16 a value beyond 65504
+ * becomes infinite there); dbias sums it as it is.
  *   m      : 0 .. 2^24 (above: GE_ERR_NOT_SUPPORTED); with m = 0 the gradients of the weights
  *            and of the bias are zero.
  *   dy     : (m, d), and w_down (d, n); with w_down NULL dy is dH itself, (m, n) with d = n.

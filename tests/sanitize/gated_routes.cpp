@@ -5,7 +5,10 @@
 //   w4 m n k group gated chunks
 // (dt 0 f32, 1 f16, 2 bf16) and prints a name for each, and of
 //   rows n gated | w4rows n gated tile
-// and prints how many rows one launch takes.
+// and prints how many rows one launch takes, and of
+//   sums m n k d dt
+// and prints the rows of column sums that the kernels of dZ leave, and what the workspace has for them
+// and for the sums of those, in rows.
 #include <cstdio>
 #include <cstring>
 
@@ -47,6 +50,20 @@ int main() {
     if (!std::strcmp(op, "rows")) {
       if (std::scanf("%ld %ld", &a, &b) != 2) return 1;
       std::printf("%ld\n", (long)gegh::launch_rows(a, b != 0));
+      continue;
+    }
+    if (!std::strcmp(op, "sums")) {
+      if (std::scanf("%ld %ld %ld %ld %ld", &a, &b, &c, &d, &e) != 5) return 1;
+      const gegh::BackwardSpace s = gegh::backward_space(a, b, c, d, (ge_dtype_t)e);
+      long most = (long)gegh::dz_parts(a, b), used = most;
+      for (int cus : {64, 256, 304})
+        if (gegh::gradient_kernel(a, b, d, (ge_dtype_t)e, true) == gegh::Kernel::kTiles) {
+          if (gegh::gated_layout(a, b, d, (ge_dtype_t)e, true, cus, &L) != GE_OK) return 1;
+          const long rows = (long)L.tiles_m * (gek::kTiles[L.cfg].bm / gek::kTiles[L.cfg].wm), parts = (long)gegh::colsum_parts(rows, 2 * b);
+          if (rows > most) most = rows;
+          if (rows + (parts > 1 ? parts : 0) > used) used = rows + (parts > 1 ? parts : 0);
+        }
+      std::printf("%ld %ld %ld\n", most, used, (long)((s.total - s.scratch - geh::kSkFlagRegion) / (2 * b * 4)));
       continue;
     }
     if (!std::strcmp(op, "w4rows")) {

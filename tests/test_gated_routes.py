@@ -68,3 +68,12 @@ def test_lanes_of_a_launch(routes):
             for tile, (bm, bn) in enumerate(((256, 256), (192, 256), (128, 128), (64, 128))):
                 rows = int(routes(line("w4rows", n, gated, tile))[0])
                 assert rows >= bm and rows % bm == 0 and rows // bm * cdiv(n * (1 + gated), bn) * 512 < 1 << 32
+
+
+def test_room_for_the_column_sums(routes):
+    for m in (1, 7, 32, 33, 77, 128, 129, 2048, 2049, 16384, 100000, 1 << 24):
+        for n in (1, 7, 8, 264, 1101, 4096, 11008, 1 << 20):
+            for d in (8, 33, 4096):
+                for t in (S.F32, S.F16, S.BF16):
+                    most, used, room = map(int, routes(line("sums", m, n, 8, d, t))[0].split())
+                    assert 1 <= most <= used <= room, (m, n, d, t)
