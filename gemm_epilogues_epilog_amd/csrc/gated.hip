@@ -391,7 +391,7 @@ ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t 
   char* scratch = ws + at.scratch;
   const size_t scratch_bytes = workspace_bytes - at.scratch;   // (m = 0: nothing, and nothing is needed)
 
-  if (m > 0) {
+  if (m > 0 && (dx || dw || dbias)) {   // (dw_down needs neither dZ nor Z)
     const void* dh = dy;
     bool f32 = false;
     uint32_t* flags = nullptr;   // of a split of dX's product

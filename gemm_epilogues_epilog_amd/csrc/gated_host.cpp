@@ -49,7 +49,7 @@ ge_status_t check_backward(int64_t m, int64_t n, int64_t k, int64_t d, ge_dtype_
   if (vec != dt && vec != GE_F32) return GE_ERR_NOT_SUPPORTED;
   if (m > kMaxBackwardTokens || !grid_ok(std::max(m, 2 * n), std::max({n, k, d}))) return GE_ERR_NOT_SUPPORTED;
   if (!b.w_down && d != n) return GE_ERR_INVALID_VALUE;   // dy is then the gradient of H itself
-  if (m && (!b.dy || !b.z)) return GE_ERR_NULL_POINTER;
+  if (m && (!b.dy || (!b.z && (b.dx || b.dw || b.dbias)))) return GE_ERR_NULL_POINTER;
   if (b.dx && m && !b.w) return GE_ERR_NULL_POINTER;
   if (b.dw && m && !b.x) return GE_ERR_NULL_POINTER;
   if (b.dw_down && m && !b.h) return GE_ERR_NULL_POINTER;

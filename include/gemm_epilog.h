@@ -528,7 +528,7 @@ size_t gemm_epilog_gated_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_
  *   m      : 0 .. 2^24 (above: GE_ERR_NOT_SUPPORTED); with m = 0 the gradients of the weights
  *            and of the bias are zero.
  *   dy     : (m, d), and w_down (d, n); with w_down NULL dy is dH itself, (m, n) with d = n.
- *   z      : Z (m, 2 n) as the forward pass left it.
+ *   z      : Z (m, 2 n) as the forward pass left it; needed for dx, dw and dbias.
  *   x, w, h: X (m, k), W (2 n, k), H (m, n): needed for dw, dx and dw_down.
  *   dx (m, k), dw (2 n, k), dw_down (d, n), dbias (2 n values of type vec): each may be NULL if
  *            not wanted. None may overlap an input.

@@ -79,3 +79,25 @@ def test_infinite_weights_and_the_tiles_last_rows(gpu, m):
     bad = torch.zeros(2 * n, dtype=torch.bool, device="cuda")
     bad[5] = bad[n + 5] = True
     assert (db[bad] == float("inf")).all() and torch.isfinite(db[~bad]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_down_gradient_alone(gpu, dtype):
+    """Through the C interface, where the others' operands may be left out: the same gradient, with Z and
+    the rest of the operands missing and the part of the workspace that holds dZ untouched."""
+    m, n, k, d = 100, 264, 40, 72
+    x, w, _ = G.make(m, n, k, dtype, 1, bias=False)
+    h, z = gated.gated_forward(x, w, save=True)
+    wd, dy = torch.randn(d, n, device="cuda").to(G.T[dtype]), torch.randn(m, d, device="cuda").to(G.T[dtype])
+    want = gated.gated_backward(dy, x, w, z, w_down=wd, h=h)
+    L, t = gpu.load(), gpu.DTYPES[dtype]
+    size = L.gemm_epilog_gated_workspace_bytes(m, n, k, d, t)
+    ws, out = torch.full((size,), 7, dtype=torch.uint8, device="cuda"), torch.empty_like(want.dw_down)
+    assert L.gemm_epilog_gated_backward(m, n, k, d, t, 0, dy.data_ptr(), None, None, None, h.data_ptr(), wd.data_ptr(), None, None,
+                                        out.data_ptr(), None, 0, ws.data_ptr(), size,
+                                        torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(out, want.dw_down)
+    assert (ws[:m * 2 * n * (4 if dtype == "f32" else 2)] == 7).all()
+    # without Z the others are refused
+    assert L.gemm_epilog_gated_backward(m, n, k, d, t, 0, dy.data_ptr(), x.data_ptr(), w.data_ptr(), None, h.data_ptr(), wd.data_ptr(),
+                                        want.dx.data_ptr(), None, None, None, 0, ws.data_ptr(), size, None) == 3
