@@ -5,7 +5,6 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cstring>
 #include <type_traits>
 
@@ -182,12 +181,13 @@ const void* gen_of(bool large, bool narrow) {
          : large ? reinterpret_cast<const void*>(&gen_kernel<DT, OUT, LAY, 128, 128, 64, 1, false>)
                  : reinterpret_cast<const void*>(&gen_kernel<DT, OUT, LAY, 64, 64, 32, 2, false>);
 }
+// (fp32 results of 16-bit operands: dH, and the sums of a shared k loop, which dX, dW and dWd have)
 template <int DT>
 const void* gen_kernel_of(int lay, bool f32_out, bool large, bool narrow) {
   switch (lay) {
     case 0: return f32_out ? gen_of<DT, F32, 0>(large, narrow) : gen_of<DT, DT, 0>(large, narrow);
     case 1: return f32_out ? gen_of<DT, F32, 1>(large, narrow) : gen_of<DT, DT, 1>(large, narrow);
-    case 2: return f32_out ? gen_of<DT, F32, 2>(large, narrow) : gen_of<DT, DT, 2>(large, narrow);
+    case 2: return gen_of<DT, DT, 2>(large, narrow);
     default: return gen_of<DT, DT, 6>(large, narrow);
   }
 }

@@ -1,9 +1,12 @@
 // Few tokens: X (m, k) by W^T, W (n, k) or a gated (2 n, k), bound by reading W once.
 //
-// A workgroup takes NB = FB (gated: 2 FB) groups of 16 rows of W and 16 MT tokens. Its waves take
+// A workgroup takes 16 rows of W (gated: of each half) and 16 MT tokens. Its waves take
 // steps of 256 bytes of k in turn, stream W from memory straight into the registers that feed the
 // 16 x 16 matrix instruction (lane l: row l % 16, the 16 bytes l / 16 of each 64), with the next
-// step on its way during a step's products, and add their sums through LDS in wave order.
+// step on its way during a step's products, and add their sums through LDS in wave order. (Gated,
+// from 17 tokens on, two steps do not fit the registers: 4 to 28 of them go to scratch memory as they
+// arrive, and with them the wave waits for those loads before the products; fp32 rows that are not whole
+// 16-byte chunks from 33 tokens on 185.)
 // W's rows at any alignment: 16-byte loads, the row's last ones moved back and shifted.
 //
 // One token by 2 x 11008 x 4096 bf16: 33 us in the kernel, 5.5 TB/s of W (every byte once: 183 MB by the

@@ -272,9 +272,9 @@ ge_status_t run(const void* fn, dim3 grid, int threads, size_t lds, void** param
 
 template <int DT, bool GATED, int MT, bool VEC, bool FEW>
 const void* skinny_of(int64_t group) {
-  return group == 32   ? reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, MT, 4, VEC, FEW>)
-         : group == 64 ? reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, MT, 2, VEC, FEW>)
-                       : reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, 1, MT, 1, VEC, FEW>);
+  return group == 32   ? reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, MT, 4, VEC, FEW>)
+         : group == 64 ? reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, MT, 2, VEC, FEW>)
+                       : reinterpret_cast<const void*>(&w4_skinny_kernel<DT, GATED, MT, 1, VEC, FEW>);
 }
 template <int DT, bool GATED, int MT>
 const void* skinny_of(int64_t group, bool vec) {

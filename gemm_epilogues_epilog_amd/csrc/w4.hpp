@@ -104,37 +104,35 @@ struct W4Step {
 };
 
 // Skinny kernel: a few tokens; bound by reading W once, and beside that by the number of memory
-// instructions. A workgroup takes NB row groups (gated: the gate's and the up projection's) and 16
+// instructions. A workgroup takes a row group (gated: the gate's and the up projection's, NB) and 16
 // MT tokens; its waves take the steps of 128 k in turn and add their sums through LDS in wave
-// order. NG: groups to a step. VEC: X's rows are whole, aligned 16-byte chunks. FEW: up to four
+// order. The next step is on its way during a step's products; with 33 tokens and more in a gated weight
+// 40 to 256 of its registers do not fit and wait in scratch memory. NG: groups to a step. VEC: X's rows are whole, aligned 16-byte chunks. FEW: up to four
 // tokens.
 // Scales and zeros are loaded for 16 groups at a time, a group to each of the 16 lanes of a row
 // (which need the same four scales, those of the rows 4 (l / 16) .. + 3 of the products), and
 // handed to all of them as their turn comes. Of up to four tokens a lane loads a chunk of its own,
 // and passes it on likewise: three memory instructions to a gated step of 2 KB instead of ten (one
 // token by 2 x 11008 x 4096 from memory: 14.7 -> 13.2 us; 4096 x 11008 8.1).
-template <int DT, bool GATED, int FB, int MT, int NG, bool VEC, bool FEW>
+template <int DT, bool GATED, int MT, int NG, bool VEC, bool FEW>
 __global__ __launch_bounds__(MT == 1 ? 1024 : 512, MT == 4 ? 2 : MT == 2 ? 3 : 4) void w4_skinny_kernel(W4Args p) {
-  constexpr int NB = GATED ? 2 * FB : FB, XR = FEW ? 1 : 4 * MT, SPAN = 16 / NG;   // SPAN: steps of a load of scales
+  constexpr int NB = GATED ? 2 : 1, XR = FEW ? 1 : 4 * MT, SPAN = 16 / NG;   // SPAN: steps of a load of scales
   static_assert(!FEW || (MT == 1 && VEC), "few tokens");
   using Step = W4Step<NB, XR>;
   extern __shared__ __attribute__((aligned(16))) f32x4 red[];   // [wave][NB MT][64]
   const int nw = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, li = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rg0 = blockIdx.x * FB;
+  const int rg = blockIdx.x;
   const int64_t t0 = (int64_t)blockIdx.y * (16 * MT);
 
-  // (row groups past the last one have an empty range: zeros, and no reads)
   __amdgpu_buffer_rsrc_t rc[NB], rs[NB], rz[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    const int in = rg0 + b % FB;
-    const bool on = in < p.rgs;
-    const int64_t rg = (on ? in : 0) + (b < FB ? 0 : (int64_t)p.rgs);
-    rc[b] = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p.codes) + rg * p.kt * kTileBytes, 0, on ? p.kt * kTileBytes : 0, kBufDword3);
-    rs[b] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.scales) + rg * p.groups * kRows, 0, on ? p.groups * kRows * 2 : 0, kBufDword3);
-    rz[b] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.zeros) + rg * p.groups * kRows, 0, on ? p.groups * kRows : 0, kBufDword3);
+    const int64_t in = rg + (b ? (int64_t)p.rgs : 0);
+    rc[b] = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p.codes) + in * p.kt * kTileBytes, 0, p.kt * kTileBytes, kBufDword3);
+    rs[b] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.scales) + in * p.groups * kRows, 0, p.groups * kRows * 2, kBufDword3);
+    rz[b] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.zeros) + in * p.groups * kRows, 0, p.groups * kRows, kBufDword3);
   }
   const char* xb = static_cast<const char*>(p.x) + t0 * p.k * 2;
   const __amdgpu_buffer_rsrc_t rx = rsrc(xb);
@@ -278,8 +276,8 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512, MT == 4 ? 2 : MT == 2 ? 3 : 4
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) red[((w * NB + b) * MT + mt) * 64 + lane] = acc[b][mt];
   __syncthreads();
-  for (int i = threadIdx.x; i < FB * MT * 64; i += blockDim.x) {
-    const int l = i & 63, mt = i / 64 % MT, b = i / 64 / MT;
+  for (int i = threadIdx.x; i < MT * 64; i += blockDim.x) {
+    const int l = i & 63, mt = i / 64;
     const auto total = [&](int blk) {
       f32x4 v = red[(blk * MT + mt) * 64 + l];
       for (int o = 1; o < nw; ++o) {
@@ -290,9 +288,9 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512, MT == 4 ? 2 : MT == 2 ? 3 : 4
       return v;
     };
     const int64_t token = t0 + mt * 16 + (l & 15);
-    const int col = (rg0 + b) * kRows + (l >> 4) * 4, left = p.n - col;
+    const int col = rg * kRows + (l >> 4) * 4, left = p.n - col;
     if (token >= p.m || left <= 0) continue;
-    f32x4 v = total(b);
+    f32x4 v = total(0);
     float y[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -300,7 +298,7 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512, MT == 4 ? 2 : MT == 2 ? 3 : 4
       y[r] = v[r];
     }
     if constexpr (GATED) {
-      f32x4 u = total(FB + b);
+      f32x4 u = total(1);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (p.bias && r < left) u[r] += load_vec(p.bias, p.vec, (int64_t)p.n + col + r);

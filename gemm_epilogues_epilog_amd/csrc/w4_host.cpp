@@ -55,7 +55,7 @@ ge_status_t check_product(int64_t m, int64_t n, ge_dtype_t dt, ge_dtype_t out, c
                           ge_dtype_t vec, const void* D) {
   if (m < 0 || m > 0x7fffffff || !known(dt) || !known(out) || !known(vec)) return GE_ERR_INVALID_VALUE;
   if (!half_type(dt) || (out != dt && out != GE_F32) || (vec != dt && vec != GE_F32)) return GE_ERR_NOT_SUPPORTED;
-  // every launch has at most 2^31 - 1 workgroups of 64 x 16 values
+  // at most 2^31 - 1 blocks of 16 x 16 values
   if (gew4::ceil_div(m, 16) * gew4::ceil_div(n, 16) > 0x7fffffff) return GE_ERR_NOT_SUPPORTED;
   if (m && (!x || !D)) return GE_ERR_NULL_POINTER;
   if (!aligned(x, 2) || !aligned(D, esize(out)) || !aligned(bias, esize(vec))) return GE_ERR_MISALIGNED;
@@ -75,7 +75,7 @@ int choose(int64_t m, int64_t n, int64_t k, int64_t group, bool gated, bool alig
   if (m <= 16 || k < 8) return -1;   // (the tiles load eight k at a time)
   const int64_t rows = gated ? 2 * n : n;
   const double kt = (double)gew4::k_tiles(k);
-  const int64_t step = m <= 16 ? 16 : m <= 32 ? 32 : 64, blocks = gew4::ceil_div(m, step);
+  const int64_t step = m <= 32 ? 32 : 64, blocks = gew4::ceil_div(m, step);
   const double wgs = (double)gew4::ceil_div(n, 16) * (double)blocks, share = wgs < cus ? wgs / cus : 1.0;
   const double x = (double)m * (double)rows / 16 * (double)k * 2 / 10e6, w = (double)blocks * (double)rows * (double)k * 0.5 / 5e6;
   double best = (4.0 + 1.2 * (wgs / (share * cus) - 1.0) + (x + w) / share) * (aligned ? 1.0 : 2.5);
