@@ -93,11 +93,11 @@ ge_status_t gated_layout(int64_t m, int64_t n, int64_t k, ge_dtype_t dt, bool ba
   const ge_dtypes_t t = {dt, dt, dt};
   const int64_t cols = backward ? n : 2 * n;
   // (forward: the configurations for transposed operands; backward: those and the 192 and 128 x 256
-  // tiles; the others' places are taken by the nearest)
+  // tiles; the others' places are taken by the nearest, also where GE_TILE names a register-staged one)
   const int lay = backward ? 0 : 2;
   int cfg = geh::choose_cfg(m, cols, k, dt, cus, lay);
   if (cfg == gek::CFG_LH) cfg = gek::CFG_L;
-  if (cfg == gek::CFG_LM4) cfg = gek::CFG_LM;
+  if (cfg == gek::CFG_LM4 || !gek::cfg_is_dtl(cfg)) cfg = gek::CFG_LM;
   return geh::make_layout(m, cols, k, t, GE_EPILOG_NONE, lay, cus, cfg, false, gek::cfg_can_persist(cfg), L);
 }
 

@@ -77,3 +77,16 @@ def test_room_for_the_column_sums(routes):
                 for t in (S.F32, S.F16, S.BF16):
                     most, used, room = map(int, routes(line("sums", m, n, 8, d, t))[0].split())
                     assert 1 <= most <= used <= room, (m, n, d, t)
+
+
+@pytest.mark.parametrize("tile", ["S", "M", "L", "LH", "LM", "LM4", "LMD", "L3", "LW"])
+def test_a_forced_tile(routes, monkeypatch, tile):
+    """GE_TILE, for experiments with plans, also names tiles that the gated products do not have: the rules
+    then choose one that they do have, as its grid is made for it."""
+    monkeypatch.setenv("GE_TILE", tile)
+    kernels = {"L", "L3", "LW", "LM", "LMD"}
+    for m, n, k in ((77, 1000, 520), (512, 4096, 2048), (2048, 2048, 256), (4096, 11008, 4096)):
+        forward, gradient = (r.split()[0] for r in routes(line("forward", m, n, k, S.BF16), line("gradient", m, n, k, S.BF16)))
+        assert gradient in kernels and forward in kernels - {"L3", "LW"} | {"few"}
+        if tile in kernels:
+            assert gradient == tile
