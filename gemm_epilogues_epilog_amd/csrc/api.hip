@@ -216,29 +216,22 @@ ScratchState g_scratch;
 // Waits of products without a plan that ran out, counted on each device (addressed as `scratch` is)
 // and never cleared; what was reported of it is kept here.
 static __device__ uint32_t lost_count;
-struct LostState {
-  std::mutex mu;
-  uint32_t* ptr[kMaxDevices] = {};
-  uint32_t reported[kMaxDevices] = {};
-};
-LostState g_lost;
+std::atomic<uint32_t*> g_lost[kMaxDevices] = {};
+std::mutex g_reported_mu;
+uint32_t g_reported[kMaxDevices] = {};
 
-// The current device's count; g_lost.mu is held.
-ge_status_t lost_word_locked(int* dev, uint32_t** word) {
+// The current device's index and its count.
+ge_status_t lost_word(int* dev, uint32_t** word) {
   if (hipGetDevice(dev) != hipSuccess) return GE_ERR_HIP;
   if (*dev < 0 || *dev >= kMaxDevices) return GE_ERR_NOT_SUPPORTED;
-  if (!g_lost.ptr[*dev]) {
+  *word = g_lost[*dev].load(std::memory_order_relaxed);
+  if (!*word) {
     void* p = nullptr;
     if (hipGetSymbolAddress(&p, HIP_SYMBOL(lost_count)) != hipSuccess || !p) return GE_ERR_HIP;
-    g_lost.ptr[*dev] = static_cast<uint32_t*>(p);
+    *word = static_cast<uint32_t*>(p);
+    g_lost[*dev].store(*word, std::memory_order_relaxed);
   }
-  *word = g_lost.ptr[*dev];
   return GE_OK;
-}
-ge_status_t lost_word(uint32_t** word) {
-  int dev = 0;
-  std::lock_guard<std::mutex> lock(g_lost.mu);
-  return lost_word_locked(&dev, word);
 }
 
 }  // namespace
@@ -286,8 +279,10 @@ ge_status_t run_product(int64_t m, int n, int k, ge_dtype_t dt, const geh::Layou
   h.ws = ws;
   h.spin_limit = spin_limit();
   h.lost = nullptr;
-  if (L.sk_wgs)
-    if (ge_status_t st = lost_word(&h.lost); st != GE_OK) return st;
+  if (L.sk_wgs) {
+    int dev = 0;
+    if (ge_status_t st = lost_word(&dev, &h.lost); st != GE_OK) return st;
+  }
   if (L.sk_wgs && !cleared) {
     uint32_t* words = reinterpret_cast<uint32_t*>(ws + L.off_sk_flag);
     int nw = gek::kSkFlagWords;
@@ -529,15 +524,17 @@ ge_status_t gemm_epilog_gated_lost_waits(void* stream, uint32_t* count) {
   *count = 0;
   int cus = 0, dev = 0;
   if (ge_status_t st = gei::current_device(&cus); st != GE_OK) return st;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  std::lock_guard<std::mutex> lock(g_lost.mu);
   uint32_t* word = nullptr;
-  if (ge_status_t st = lost_word_locked(&dev, &word); st != GE_OK) return st;
+  if (ge_status_t st = lost_word(&dev, &word); st != GE_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
   uint32_t v = 0;
   if (hipMemcpyAsync(&v, word, sizeof(v), hipMemcpyDeviceToHost, s) != hipSuccess || hipStreamSynchronize(s) != hipSuccess)
     return GE_ERR_HIP;
-  *count = v - g_lost.reported[dev];
-  g_lost.reported[dev] = v;
+  std::lock_guard<std::mutex> lock(g_reported_mu);   // (not over the wait: another thread may have reported more)
+  if ((int32_t)(v - g_reported[dev]) > 0) {
+    *count = v - g_reported[dev];
+    g_reported[dev] = v;
+  }
   return GE_OK;
 }
 
