@@ -10,8 +10,10 @@
 // tokens 131, 186 and 187, 600 tokens 98, 86 and 44. X's rows are whole 16-byte chunks, and groups
 // hold at least 64 (of 32 the factors do not fit the registers).
 //
-// The matrix unit is busy 37% of the cycles (192 x 256 at 3000 x 4096 x 4096, groups of 64): the
-// conversions and the factors stand among the products, and two waves to a SIMD hide part of them.
+// The matrix unit is busy 37% of the cycles (192 x 256 at 3000 x 4096 x 4096, groups of 64): of the 4200 that
+// a k-tile takes on a SIMD, 1540 are its two waves' products and about 1800 their vector instructions
+// (conversions, and factors on the sums). All waves go through the same phases between two barriers,
+// which leaves the rest to waiting.
 //
 // At the end of k-tile t every wave waits until its copies of X's tile t + 1 have landed and its
 // reads of tile t and its writes of W's tile t + 1 are done; one barrier publishes tile t + 1 and

@@ -573,9 +573,10 @@ size_t gemm_epilog_w4_scale_count(int64_t rows, int64_t k, int64_t group, int ha
 /*
  * gemm_epilog_w4_quantize - a (rows, k) weight of type src_dt, row stride ld (elements), to codes,
  * scales of type dt (fp16 or bf16) and zeros. With lo and hi the smallest and the largest of a
- * group's values and zero: s = (hi - lo) / 15 rounded to dt, z = -lo / s and q = x / s + z, each
- * quotient rounded to nearest even, held to 0 .. 15. symmetric: s = max(-lo, hi) / 7 and z = 8. A
- * group with s = 0 stands for zeros; one that holds an infinity or a NaN gets s = NaN.
+ * group's values and zero: s = (hi - lo) / 15 rounded to dt (by way of 64 and 32 bits), z = -lo / s
+ * and q = x / s + z, each quotient rounded to nearest even, held to 0 .. 15. symmetric: s = max(-lo,
+ * hi) / 7 and z = 8. A group with s = 0 stands for zeros; one that holds an infinity or a NaN gets s =
+ * NaN, and one whose s is beyond dt's range, infinite then, stands for NaN as well.
  */
 ge_status_t gemm_epilog_w4_quantize(int64_t rows, int64_t k, ge_dtype_t src_dt, const void* src, int64_t ld,
                                     int64_t group, int halves, int symmetric, ge_dtype_t dt, void* codes, void* scales,

@@ -77,3 +77,13 @@ def test_scales_at_the_ends(gpu, m, group, dtype, i):
     mags = ((q.double() + z.double().repeat_interleave(group, 1)) * s.double().abs().repeat_interleave(group, 1)).cuda()
     X = x.double().cuda()
     Q.close(got, X @ full.t(), (8 * math.sqrt(k) + 8) * Q.U * (X.abs() @ mags.t()) + 2 * k * 2.0 ** -150, "f32", (lo, hi))
+
+
+def test_scales_beyond_the_type(gpu):
+    x = torch.ones(20, 256)
+    x[3, :128], x[5, 128:], x[7, 128] = 1e6, -2e6, 9.9e5
+    for symmetric in (False, True):
+        v = w4.w4_dequantize(w4.w4_quantize(x.cuda(), 128, symmetric=symmetric, dtype="f16"), "f32").cpu()
+        bad = torch.zeros(20, 2, dtype=torch.bool)
+        bad[3, 0] = bad[5, 1] = bad[7, 1] = True
+        assert torch.equal(v.view(20, 2, 128).isnan().all(-1), bad) and torch.isfinite(v.view(20, 2, 128)[~bad]).all()
