@@ -33,10 +33,15 @@ def _dense(t, name: str, shape, dtype, device) -> int:
     return t.data_ptr()
 
 
-def _out(t, name: str, shape, dtype, device, stream):
+def _out(t, name: str, shape, dtype, device, stream, *others):
+    """A new result, or the caller's, which has to lie apart from the operands."""
     if t is None:
         return _empty(shape, dtype, device, stream)
-    _dense(t, name, shape, dtype, device)
+    at = _dense(t, name, shape, dtype, device)
+    for o in others:
+        if o is not None and at < o.data_ptr() + o.numel() * o.element_size() and \
+                o.data_ptr() < at + t.numel() * t.element_size():
+            raise ValueError(f"{name} must not overlap an operand or another result")
     return t
 
 
@@ -80,8 +85,8 @@ def gated_forward(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor]
     a = _gate(act)
     n = _halves(w, k, t, dev)
     bp, vec = _bias(bias, 2 * n, t, dev)
-    h = _out(out, "out", (m, n), t, dev, stream)
-    z = _out(z_out, "z_out", (m, 2 * n), t, dev, stream) if save or z_out is not None else None
+    h = _out(out, "out", (m, n), t, dev, stream, x, w, bias)
+    z = _out(z_out, "z_out", (m, 2 * n), t, dev, stream, x, w, bias, h) if save or z_out is not None else None
     _check(load().gemm_epilog_gated_forward(m, n, k, DTYPES[_NAME[t]], a, x.data_ptr(), w.data_ptr(), bp, vec,
                                             h.data_ptr(), None if z is None else z.data_ptr(), _stream(stream, dev)),
            "gemm_epilog_gated_forward")
@@ -96,7 +101,7 @@ def gated_down(h: torch.Tensor, w_down: torch.Tensor, out: Optional[torch.Tensor
         raise ValueError(f"w_down must be a (d, {n}) tensor")
     d = w_down.shape[0]
     _dense(w_down, "w_down", (d, n), t, dev)
-    y = _out(out, "out", (m, d), t, dev, stream)
+    y = _out(out, "out", (m, d), t, dev, stream, h, w_down)
     _check(load().gemm_epilog_gated_down(m, d, n, DTYPES[_NAME[t]], h.data_ptr(), w_down.data_ptr(), y.data_ptr(),
                                          _stream(stream, dev)), "gemm_epilog_gated_down")
     return y

@@ -163,7 +163,7 @@ def w4_dequantize(q: W4Tensor, dtype: Optional[str] = None, out: Optional[torch.
     t = q.dtype if dtype is None else _TORCH.get(dtype)
     if t is None:
         raise ValueError(f"unknown type {dtype!r}")
-    v = _out(out, "out", (q.rows, q.k), t, q.device, stream)
+    v = _out(out, "out", (q.rows, q.k), t, q.device, stream, q._buf)
     _check(load().gemm_epilog_w4_dequantize(q.rows, q.k, q.group, 2 if q.gated else 1, DTYPES[_NAME[q.dtype]], *q.ptrs,
                                             DTYPES[_NAME[t]], v.data_ptr(), q.k, _stream(stream, q.device)),
            "gemm_epilog_w4_dequantize")
@@ -193,7 +193,7 @@ def w4_matmul(x: torch.Tensor, W: W4Tensor, bias: Optional[torch.Tensor] = None,
         raise ValueError(f"out_dtype must be {name!r} or 'f32'")
     bp, vec = _bias(bias, n, x.dtype, dev)
     o = out_dtype or name
-    D = _out(out, "out", (m, n), _TORCH[o], dev, stream)
+    D = _out(out, "out", (m, n), _TORCH[o], dev, stream, x, W._buf, bias)
     _check(load().gemm_epilog_w4_matmul(m, n, k, W.group, DTYPES[name], DTYPES[o], EPILOG[epilog], x.data_ptr(),
                                         *W.ptrs, bp, vec, D.data_ptr(), _stream(stream, dev)), "gemm_epilog_w4_matmul")
     return D
@@ -205,7 +205,7 @@ def w4_gated(x: torch.Tensor, W: W4Tensor, bias: Optional[torch.Tensor] = None, 
     m, k = _operands(x, W, True)
     a, n, dev = _gate(act), W.rows // 2, x.device
     bp, vec = _bias(bias, 2 * n, x.dtype, dev)
-    h = _out(out, "out", (m, n), x.dtype, dev, stream)
+    h = _out(out, "out", (m, n), x.dtype, dev, stream, x, W._buf, bias)
     _check(load().gemm_epilog_w4_gated(m, n, k, W.group, DTYPES[_NAME[x.dtype]], a, x.data_ptr(), *W.ptrs, bp, vec,
                                        h.data_ptr(), _stream(stream, dev)), "gemm_epilog_w4_gated")
     return h

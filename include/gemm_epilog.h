@@ -490,9 +490,9 @@ ge_status_t gemm_epilog_rms_norm_backward(int64_t rows, int64_t d, ge_dtype_t dt
  * values, H (m, n), Wd (d, n), Y (m, d). Every matrix is dense row-major, of one type dt (fp32,
  * fp16 or bf16), aligned to its elements; sums are fp32. 16-bit matrices with 16-byte aligned
  * rows (n, k, d multiples of 8) run on the direct-to-LDS kernels, any others on a slower one.
- * No plan: a call chooses its kernels by its sizes. Work is enqueued on `stream`, kernel
- * launches only (a call may be captured into a HIP graph), on the current device, whose
- * pointers they are.
+ * Results must not overlap operands or each other. No plan: a call chooses its kernels by its
+ * sizes. Work is enqueued on `stream`, kernel launches only (a call may be captured into a HIP
+ * graph), on the current device, whose pointers they are.
  */
 typedef enum {
   GE_GATE_SILU = 0, /* g / (1 + e^-g) */
@@ -603,7 +603,7 @@ ge_status_t gemm_epilog_w4_dequantize(int64_t rows, int64_t k, int64_t group, in
  *   ep   : NONE, BIAS, RELU_BIAS or GELU_BIAS (other epilogues: GE_ERR_NOT_SUPPORTED).
  *   bias : n values of type vec (dt or fp32); ignored (may be NULL) for NONE.
  * x, D and bias are aligned to their elements; X with k a multiple of 8 and 16-byte aligned runs
- * faster.
+ * faster. D must not overlap an operand.
  * An infinity or a NaN in a token of X makes all of that token's results infinite or NaN (NaN also
  * where the sum over (q - z) s would be infinite; after RELU_BIAS 0 then), and no other token's.
  */
