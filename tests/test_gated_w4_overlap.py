@@ -25,7 +25,7 @@ def test_overlapping_results(current):   # noqa: F811
     buf = OnDevice.make((4096,), torch.float16, "cuda:0")
     x, w = View.of(buf, 0, 4, 16), View.of(buf, 256, 32, 16)
     h, wd = View.of(buf, 1024, 4, 16), View.of(buf, 2048, 16, 16)
-    z, apart = View.of(buf, 3072, 4, 32), View.of(buf, 3500, 4, 16)
+    z, apart = View.of(buf, 3200, 4, 32), View.of(buf, 3600, 4, 16)
     W, G = weight(16, 16, False, "cuda:0"), weight(32, 16, True, "cuda:0")
     W._buf = View.of(buf, 1536, 256)
     G._buf = View.of(buf, 1536, 256)
