@@ -83,12 +83,13 @@ __device__ __forceinline__ float four_rows(const float (&sums)[4][64][V + 1], in
   return ((sums[0][c][e] + sums[1][c][e]) + sums[2][c][e]) + sums[3][c][e];
 }
 
-// partial[part][2 n], or with one part out[2 n] of type vec: sums of the columns of dZ over the part's rows,
-// from dH and Z as dz_kernel has them, before their rounding, in a fixed order: four rows side by side,
-// each in ascending order, then those four in order. Bound by memory.
+// dz_kernel with partial[part][2 n], or with one part out[2 n] of type vec: sums of dZ's columns over the
+// part's rows, before its rounding, in a fixed order: four rows side by side, each in ascending order, then
+// those four in order. Bound by memory: 2048 x 11008 bf16 40 us, 5.6 TB/s (dz_kernel, which has more
+// workgroups, 34).
 template <int DT, int DH>
-__global__ __launch_bounds__(256) void dz_sums_kernel(const void* dh, const void* z, int64_t m, int64_t n, int act,
-                                                      float* partial, void* out, int vec) {
+__global__ __launch_bounds__(256) void dz_sums_kernel(const void* dh, const void* z, void* dz, int64_t m, int64_t n,
+                                                      int act, float* partial, void* out, int vec) {
   constexpr int64_t es = Tr<DT>::es;
   constexpr int U = 4;
   __shared__ float sums[4][64][17];
@@ -109,14 +110,24 @@ __global__ __launch_bounds__(256) void dz_sums_kernel(const void* dh, const void
           load8<DT, FLAT>(static_cast<const char*>(z) + (at * 2 + 1) * n * es, pos, n, u[i]);
         }
 #pragma unroll
-        for (int i = 0; i < U; ++i)
+        for (int i = 0; i < U; ++i) {
+          const bool in = r + 4 * i < r1;
+          float dg[8], du[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             float v, s;
             gate_slope<decltype(a)::value, DT == F32>(g[i][e], v, s);
-            sg[e] += r + 4 * i < r1 ? d[i][e] * u[i][e] * s : 0.0f;
-            su[e] += r + 4 * i < r1 ? d[i][e] * v : 0.0f;
+            dg[e] = d[i][e] * u[i][e] * s;
+            du[e] = d[i][e] * v;
+            sg[e] += in ? dg[e] : 0.0f;
+            su[e] += in ? du[e] : 0.0f;
           }
+          if (in) {
+            char* o = static_cast<char*>(dz) + (r + 4 * i) * 2 * n * es;
+            store8<DT>(o, pos, n, dg);
+            store8<DT>(o + n * es, pos, n, du);
+          }
+        }
       }
     };
     with_gate(act, [&](auto a) {
@@ -294,13 +305,13 @@ template <int DT>
 const void* dz_sums_of(bool f32_dh) {
   return f32_dh ? reinterpret_cast<const void*>(&dz_sums_kernel<DT, F32>) : reinterpret_cast<const void*>(&dz_sums_kernel<DT, DT>);
 }
-// out[2 n] of type vec: column sums of dZ from dH and Z, by way of `partial`.
-ge_status_t dz_sums(const void* dh, bool f32_dh, const void* z, int64_t m, int64_t n, ge_dtype_t dt, int act, void* out,
+// dZ from dH and Z, and out[2 n] of type vec: its column sums, by way of `partial`.
+ge_status_t dz_sums(const void* dh, bool f32_dh, const void* z, void* dz, int64_t m, int64_t n, ge_dtype_t dt, int act, void* out,
                     ge_dtype_t vec, float* partial, hipStream_t s) {
   const int parts = (int)gegh::dz_parts(m, n);
   const void* fn = dt == GE_F32 ? dz_sums_of<F32>(f32_dh) : dt == GE_F16 ? dz_sums_of<F16>(f32_dh) : dz_sums_of<BF16>(f32_dh);
   int v = (int)vec;
-  void* params[] = {&dh, &z, &m, &n, &act, &partial, &out, &v};
+  void* params[] = {&dh, &z, &dz, &m, &n, &act, &partial, &out, &v};
   if (launch(fn, dim3((unsigned)((n + 511) / 512), parts), 256, params, s) != hipSuccess) return GE_ERR_HIP;
   if (parts == 1) return GE_OK;
   return launch_bgrad_reduce(partial, parts, 2 * n, out, v, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
@@ -417,15 +428,17 @@ ge_status_t gemm_epilog_gated_backward(int64_t m, int64_t n, int64_t k, int64_t 
       if (gek::general(m, n, d, dt, 0, dy, w_down, ws + at.dh, true, 1, nullptr, 0, 0, nullptr, cus, s) != hipSuccess)
         return GE_ERR_HIP;
     }
-    const void* fn = dt == GE_F32   ? gek::dz_of<gek::F32>(f32)
-                     : dt == GE_F16 ? gek::dz_of<gek::F16>(f32)
-                                    : gek::dz_of<gek::BF16>(f32);
-    int a = (int)act;
-    void* params[] = {&dh, &z, &dz, &m, &n, &a};
-    const int64_t chunks = m * ((n + 7) / 8);
-    if (dh && gek::launch(fn, dim3((unsigned)((chunks + 255) / 256)), 256, params, s) != hipSuccess) return GE_ERR_HIP;
-    if (dh && dbias)
-      if (ge_status_t st = gek::dz_sums(dh, f32, z, m, n, dt, a, dbias, vec, sums, s); st != GE_OK) return st;
+    if (dh && dbias) {
+      if (ge_status_t st = gek::dz_sums(dh, f32, z, dz, m, n, dt, (int)act, dbias, vec, sums, s); st != GE_OK) return st;
+    } else if (dh) {
+      const void* fn = dt == GE_F32   ? gek::dz_of<gek::F32>(f32)
+                       : dt == GE_F16 ? gek::dz_of<gek::F16>(f32)
+                                      : gek::dz_of<gek::BF16>(f32);
+      int a = (int)act;
+      void* params[] = {&dh, &z, &dz, &m, &n, &a};
+      const int64_t chunks = m * ((n + 7) / 8);
+      if (gek::launch(fn, dim3((unsigned)((chunks + 255) / 256)), 256, params, s) != hipSuccess) return GE_ERR_HIP;
+    }
     if (dx)
       if (ge_status_t st = gek::product(m, k, 2 * n, dt, 0, dz, w, dx, scratch, scratch_bytes, !dh, cus, s); st != GE_OK)
         return st;

@@ -106,8 +106,9 @@ struct W4Step {
 // Skinny kernel: a few tokens; bound by reading W once, and beside that by the number of memory
 // instructions. A workgroup takes a row group (gated: the gate's and the up projection's, NB) and 16
 // MT tokens; its waves take the steps of 128 k in turn and add their sums through LDS in wave
-// order. The next step is on its way during a step's products; with 33 tokens and more in a gated weight
-// 40 to 256 of its registers do not fit and wait in scratch memory. NG: groups to a step. VEC: X's rows are whole, aligned 16-byte chunks. FEW: up to four
+// order. The next step is on its way during a step's products; with 33 tokens and more some of its
+// registers do not fit and wait in scratch memory: 40 to 256 in a gated weight, up to 14 in another (204 with
+// groups of 32 and 64 and unaligned bf16 X). NG: groups to a step. VEC: X's rows are whole, aligned 16-byte chunks. FEW: up to four
 // tokens.
 // Scales and zeros are loaded for 16 groups at a time, a group to each of the 16 lanes of a row
 // (which need the same four scales, those of the rows 4 (l / 16) .. + 3 of the products), and
